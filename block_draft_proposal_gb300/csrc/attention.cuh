@@ -1,0 +1,222 @@
+// Attention over the paged cache and over packed prompts: what the CUDA-core
+// kernel (attention_simt.cu), the tcgen05 kernel (attention_tc.cu), the
+// join of split rows and the entry points (attention.cu) share.
+//
+// Rows.  The T tokens of a request and the G = q_heads / kv_heads query heads
+// of one key/value head are packed into T * G rows, row r = token r / G, head
+// r % G of the group, so that a pass over the keys serves them all; rows go in
+// blocks of `row_block`.  An item is one (request, key/value head, row block).
+//
+// Split of the cache (paged mode).  Requests are ragged and few rows may face
+// many keys, so the keys are split by work, not by item: the items' key tiles
+// (kKeyTile keys each, at least one per item) are numbered through, request by
+// request, head by head, row block by row block, and CTA c of C (at most W)
+// takes the tiles [c W / C, (c + 1) W / C) of all W.  A CTA that holds all of an item
+// writes its rows; an item that spans CTAs leaves unnormalised partial rows in
+// the workspace, joined by combine_kernel in CTA order.
+#pragma once
+
+#include "kernels.h"
+
+namespace dflash2 {
+namespace attn {
+
+constexpr int kKeyTile = 128;
+constexpr int kMaxBatch = 65536;
+constexpr int kMaxGroup = 128;
+
+struct Params {
+    const void *q;
+    int64_t q_stride;              // elements from token to token
+    const void *k, *v;             // packed rows (prompt) or cache arrays (paged)
+    int64_t k_stride, v_stride;    // prompt: elements from token to token
+    const uint8_t *k_exp, *v_exp;  // E4M3 cache
+    const int32_t *page_table;     // paged: [batch, max_pages]
+    int32_t max_pages;
+    int32_t page_size;
+    int64_t num_pages;
+    const int32_t *cu_q;
+    const int32_t *kv_lens;        // paged
+    const int64_t *tree_mask;      // paged: [total_q, mask_words] or NULL (chain)
+    int32_t mask_words;
+    int32_t batch, total_q, q_heads, kv_heads, group, head_dim;
+    float scale_log2;              // scale * log2(e)
+    void *out;
+    float *lse;
+    float *part;                   // paged: partial rows, kPartSlots(C) slots
+    int32_t part_rows;             // rows of a slot
+    int32_t row_block;
+    int32_t n_cta;                 // CTAs the work is split over
+    int32_t *err;
+};
+
+// Partial slot s of the workspace: part_rows rows of head_dim fp32 sums, then
+// part_rows maxima (log2 domain), then part_rows sums.  CTA c owns slots 2c
+// (an item it did not start) and 2c + 1 (an item it started and did not end).
+__host__ __device__ inline int64_t part_slot_floats(int32_t part_rows, int32_t head_dim) {
+    return (int64_t)part_rows * (head_dim + 2);
+}
+
+struct Request {
+    int32_t t0, t;    // first packed token, tokens
+    int32_t len, ctx; // keys, keys before the first token; len < 0: sees nothing
+};
+
+// cu_q and kv_lens of request b, clamped to what the arrays hold.  `bad` is
+// raised for values that had to be.
+template <bool kPaged>
+__device__ __forceinline__ Request load_request(const Params &p, int32_t b, bool *bad) {
+    Request r;
+    const int32_t a = __ldg(p.cu_q + b), e = __ldg(p.cu_q + b + 1);
+    const int32_t lo = min(max(a, 0), p.total_q), hi = min(max(e, lo), p.total_q);
+    *bad = a != lo || e != hi;
+    r.t0 = lo;
+    r.t = hi - lo;
+    if (kPaged) {
+        r.len = __ldg(p.kv_lens + b);
+        r.ctx = r.len - r.t;
+        if (r.len < r.t || (int64_t)r.len > (int64_t)p.max_pages * p.page_size) {
+            *bad = true;
+            r.len = 0;
+            r.ctx = 0;
+        }
+        if (p.tree_mask && r.t > 64 * (int64_t)p.mask_words) *bad = true;
+    } else {
+        r.len = r.t;
+        r.ctx = 0;
+    }
+    return r;
+}
+
+__device__ __forceinline__ int32_t row_blocks(const Params &p, const Request &r) {
+    return (int32_t)(((int64_t)r.t * p.group + p.row_block - 1) / p.row_block);
+}
+__device__ __forceinline__ int32_t key_tiles(const Request &r) {
+    return max(1, (r.len + kKeyTile - 1) / kKeyTile);
+}
+// Units (key tiles of items) of request b; 0 when it has no rows.
+__device__ __forceinline__ int64_t request_units(const Params &p, const Request &r) {
+    return (int64_t)p.kv_heads * row_blocks(p, r) * key_tiles(r);
+}
+
+// First unit of CTA c's range, and the CTA that holds unit u, where n_cta is
+// at most the units (split_ctas), so that no range between two is empty.
+__device__ __forceinline__ int64_t split_ctas(const Params &p, int64_t units) {
+    return units < p.n_cta ? units : p.n_cta;
+}
+__device__ __forceinline__ int64_t range_start(int64_t c, int64_t units, int64_t n_cta) {
+    return c * units / n_cta;
+}
+__device__ __forceinline__ int32_t cta_of(int64_t u, int64_t units, int64_t n_cta) {
+    return (int32_t)(((u + 1) * n_cta - 1) / units);
+}
+
+// Sum of a 64-bit value over the block; every thread gets it.
+__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t *red) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    int64_t s = 0;
+    for (int w = 0; w < (int)blockDim.x / 32; ++w) s += red[w];
+    return s;
+}
+
+// Where CTA blockIdx.x begins: all units, its range [u, end), and the request
+// that holds u with the units before that request.  Every thread of the block
+// calls it; block sums and one scan per blockDim requests.
+struct Start {
+    int64_t u, end, before;
+    int32_t b;
+};
+struct StartScratch {
+    int64_t red[32];
+    int64_t before;
+    int32_t b;
+};
+__device__ __forceinline__ Start find_start(const Params &p, StartScratch *s, bool *any_bad) {
+    bool bad;
+    int64_t mine = 0, n = 0;
+    for (int b = threadIdx.x; b < p.batch; b += blockDim.x) {
+        n = request_units(p, load_request<true>(p, b, &bad));
+        *any_bad |= bad;
+        mine += n;
+    }
+    const int64_t units = block_sum(mine, s->red);
+    Start o;
+    const int64_t n_cta = split_ctas(p, units);
+    o.u = o.end = o.before = 0;
+    o.b = 0;
+    if (blockIdx.x >= n_cta) return o;
+    o.u = range_start(blockIdx.x, units, n_cta);
+    o.end = range_start((int64_t)blockIdx.x + 1, units, n_cta);
+    int64_t passed = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += blockDim.x) {
+        const int b = b0 + threadIdx.x;
+        if (p.batch > (int)blockDim.x)
+            n = b < p.batch ? request_units(p, load_request<true>(p, b, &bad)) : 0;
+        else if (b >= p.batch)
+            n = 0;
+        int64_t incl = n;
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+            const int64_t up = __shfl_up_sync(0xFFFFFFFFu, incl, k);
+            if ((threadIdx.x & 31) >= (unsigned)k) incl += up;
+        }
+        __syncthreads();
+        if ((threadIdx.x & 31) == 31) s->red[threadIdx.x >> 5] = incl;
+        __syncthreads();
+        int64_t total = 0, warps_before = 0;
+        for (int w = 0; w < (int)blockDim.x / 32; ++w) {
+            if (w == (int)threadIdx.x / 32) warps_before = total;
+            total += s->red[w];
+        }
+        const int64_t pre = passed + warps_before + incl - n;
+        if (n > 0 && o.u >= pre && o.u < pre + n) {
+            s->before = pre;
+            s->b = b;
+        }
+        passed += total;
+        if (o.u < passed) break;
+    }
+    __syncthreads();
+    o.before = s->before;
+    o.b = s->b;
+    return o;
+}
+
+// Is key position l of a paged request seen by token i (absolute index row)?
+__device__ __forceinline__ bool sees(const Params &p, const Request &r, int32_t i, int32_t l) {
+    if (l >= r.len) return false;
+    const int32_t j = l - r.ctx;
+    if (j < 0) return true;
+    if (!p.tree_mask) return j <= i;
+    if (j >= 64 * p.mask_words) return false;
+    return (__ldg(p.tree_mask + (int64_t)(r.t0 + i) * p.mask_words + (j >> 6)) >> (j & 63)) & 1;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float pow2_byte(uint8_t b) { return ldexpf(1.0f, (int)b - 127); }
+
+// Element loads as fp32.
+__device__ __forceinline__ float as_f32(float v) { return v; }
+__device__ __forceinline__ float as_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float as_f32(uint8_t c) {
+    const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)c, __NV_E4M3);
+    return __half2float(__half(h));
+}
+__device__ __forceinline__ void put(float *p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+dflash2_status launch_simt(const DeviceInfo &di, Params p, bool paged, int32_t dtype,
+                           int32_t kv_format, cudaStream_t st);
+dflash2_status launch_combine(const DeviceInfo &di, const Params &p, int32_t dtype, cudaStream_t st);
+
+}  // namespace attn
+}  // namespace dflash2

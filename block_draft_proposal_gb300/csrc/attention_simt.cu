@@ -1,0 +1,469 @@
+// Attention on CUDA cores: fp32 inputs, and every head_dim, page size and
+// alignment the tensor-core kernel does not take.
+//
+// One pass over the keys in tiles of 64 with the running maximum m and sum l
+// of the softmax (log2 domain): S = scale log2(e) Q K^T, m' = max(m, max S),
+// P = 2^(S - m'), O = O 2^(m - m') + P V, l = l 2^(m - m') + sum P.  256
+// threads as 16 x 16: thread (ty, tx) has kRows / 16 rows and the keys tx + 16 j
+// of S, and the same rows with four of every 64 values of O, so a row's
+// statistics are 16-lane shuffles and every shared-memory read is a broadcast or
+// 16 bytes per lane without conflicts (K rows are padded by four floats).
+//
+// Bound by fp32 FMAs once rows fill the tile (kRows = 64) and by HBM for few
+// rows (kRows = 16: 32 FMA cycles per key against 45 cycles of HBM time for an
+// fp32 key and value of head_dim 128).
+#include "attention.cuh"
+
+namespace dflash2 {
+namespace attn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kKeys = 64;
+
+__host__ __device__ constexpr int simt_smem_floats(int rows, int dmax) {
+    return rows * dmax + kKeys * (dmax + 4) + kKeys * dmax + rows * kKeys;
+}
+
+// Rows of a tile into shared memory as fp32, `width` of kDMax columns live and
+// the rest zero.  row_ptr(r) gives the row's elements or NULL for a zero row;
+// row_mul(r) scales it.
+template <typename T, int kDMax, typename PtrF, typename MulF>
+__device__ __forceinline__ void stage_rows(float *dst, int pitch, int n, int width, bool vec,
+                                           PtrF row_ptr, MulF row_mul) {
+    constexpr int kChunks = kDMax / 4;
+    for (int i = threadIdx.x; i < n * kChunks; i += kThreads) {
+        const int r = i / kChunks, c = (i % kChunks) * 4;
+        const T *src = row_ptr(r);
+        float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (src && c < width) {
+            if (vec) {  // width % 4 == 0 and four elements aligned
+                if constexpr (sizeof(T) == 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(src + c);
+                    x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+                } else {
+                    T e[4];
+                    if constexpr (sizeof(T) == 2)
+                        *reinterpret_cast<uint2 *>(e) = *reinterpret_cast<const uint2 *>(src + c);
+                    else
+                        *reinterpret_cast<uint32_t *>(e) =
+                            *reinterpret_cast<const uint32_t *>(src + c);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) x[k] = as_f32(e[k]);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (c + k < width) x[k] = as_f32(src[c + k]);
+            }
+            const float mul = row_mul(r);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] *= mul;
+        }
+        *reinterpret_cast<float4 *>(dst + r * pitch + c) = make_float4(x[0], x[1], x[2], x[3]);
+    }
+}
+
+// The keys [k0, k1) of one item, added up in registers and written as final
+// rows (slot < 0) or as partial rows of workspace slot `slot`.
+template <typename T, typename C, bool kPaged, int kRows, int kDMax>
+__device__ void run_piece(const Params &p, const Request &rq, int32_t b, int32_t h, int32_t rb,
+                          int32_t k0, int32_t k1, int64_t slot, float *smem, bool vec_q, bool vec_k,
+                          bool *bad_page) {
+    constexpr int kPer = kRows / 16;   // rows per thread
+    constexpr int kQuads = kDMax / 64; // groups of four output values per thread
+    constexpr bool kE4M3 = sizeof(C) == 1;
+    float *sq = smem;
+    float *sk = sq + kRows * kDMax;
+    float *sv = sk + kKeys * (kDMax + 4);
+    float *sp = sv + kKeys * kDMax;
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    const int32_t row0 = rb * kRows;
+    const int32_t n_rows = (int32_t)min((int64_t)kRows, (int64_t)rq.t * p.group - row0);
+    const int d = p.head_dim;
+
+    __syncthreads();  // the previous piece's reads of the shared tiles are over
+    stage_rows<T, kDMax>(
+        sq, kDMax, kRows, d, vec_q,
+        [&](int r) -> const T * {
+            if (r >= n_rows) return nullptr;
+            const int32_t g = row0 + r;
+            return (const T *)p.q + (int64_t)(rq.t0 + g / p.group) * p.q_stride +
+                   (int64_t)(h * p.group + g % p.group) * d;
+        },
+        [&](int) { return p.scale_log2; });
+
+    float o[kPer][kQuads][4];
+    float m[kPer], l[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.0f;
+#pragma unroll
+        for (int q = 0; q < kQuads; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][q][e] = 0.0f;
+    }
+
+    for (int32_t kt = k0; kt < k1; kt += kKeys) {
+        const int nk = min(kKeys, k1 - kt);
+        // cache row of key r of the tile, or -1
+        auto cache_row = [&](int r) -> int64_t {
+            const int32_t l_ = kt + r;
+            if (r >= nk || l_ >= rq.len) return -1;
+            const int32_t pg = __ldg(p.page_table + (int64_t)b * p.max_pages + l_ / p.page_size);
+            if (pg < 0 || pg >= p.num_pages) {
+                *bad_page = true;
+                return -1;
+            }
+            return ((int64_t)pg * p.kv_heads + h) * p.page_size + l_ % p.page_size;
+        };
+        auto key_ptr = [&](int r, const void *base, int64_t stride) -> const C * {
+            if constexpr (kPaged) {
+                const int64_t at = cache_row(r);
+                return at < 0 ? nullptr : (const C *)base + at * d;
+            } else {
+                if (r >= nk || kt + r >= rq.len) return nullptr;
+                return (const C *)base + (int64_t)(rq.t0 + kt + r) * stride + (int64_t)h * d;
+            }
+        };
+        __syncthreads();  // the previous tile's products are over
+        stage_rows<C, kDMax>(
+            sk, kDMax + 4, kKeys, d, vec_k, [&](int r) { return key_ptr(r, p.k, p.k_stride); },
+            [&](int r) { return kE4M3 ? pow2_byte(__ldg(p.k_exp + cache_row(r))) : 1.0f; });
+        stage_rows<C, kDMax>(
+            sv, kDMax, kKeys, d, vec_k, [&](int r) { return key_ptr(r, p.v, p.v_stride); },
+            [&](int r) { return kE4M3 ? pow2_byte(__ldg(p.v_exp + cache_row(r))) : 1.0f; });
+        __syncthreads();
+
+        float s[kPer][4];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] = 0.0f;
+#pragma unroll 4
+        for (int c = 0; c < kDMax; c += 4) {
+            float4 kq[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                kq[j] = *reinterpret_cast<const float4 *>(sk + (tx + 16 * j) * (kDMax + 4) + c);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const float4 qq = *reinterpret_cast<const float4 *>(sq + (ty * kPer + i) * kDMax + c);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s[i][j] = fmaf(qq.x, kq[j].x, s[i][j]);
+                    s[i][j] = fmaf(qq.y, kq[j].y, s[i][j]);
+                    s[i][j] = fmaf(qq.z, kq[j].z, s[i][j]);
+                    s[i][j] = fmaf(qq.w, kq[j].w, s[i][j]);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int32_t r = row0 + ty * kPer + i;
+            const int32_t tok = r / p.group;
+            float top = -INFINITY;
+            bool seen[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int32_t pos = kt + tx + 16 * j;
+                seen[j] = ty * kPer + i < n_rows && tx + 16 * j < nk &&
+                          (kPaged ? sees(p, rq, tok, pos) : pos <= tok);
+                if (!seen[j]) s[i][j] = -INFINITY;
+                top = fmaxf(top, s[i][j]);
+            }
+#pragma unroll
+            for (int x = 8; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+            const float mn = fmaxf(m[i], top);
+            // no finite key yet: a base of 0 keeps -inf - base at -inf
+            const float base = mn == -INFINITY ? 0.0f : mn;
+            const float fix = ex2(m[i] - base);
+            float sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float w = seen[j] ? ex2(s[i][j] - base) : 0.0f;
+                sp[(ty * kPer + i) * kKeys + tx + 16 * j] = w;
+                sum += w;
+            }
+#pragma unroll
+            for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
+            l[i] = l[i] * fix + sum;
+            m[i] = mn;
+#pragma unroll
+            for (int q = 0; q < kQuads; ++q)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][q][e] *= fix;
+        }
+        __syncwarp();  // a row's 16 threads are in one warp: its weights are written
+        for (int key = 0; key < nk; ++key) {
+            float4 vq[kQuads];
+#pragma unroll
+            for (int q = 0; q < kQuads; ++q)
+                vq[q] = *reinterpret_cast<const float4 *>(sv + key * kDMax + 64 * q + 4 * tx);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const float w = sp[(ty * kPer + i) * kKeys + key];
+                if (w != 0.0f) {  // what a row does not see never reaches it, NaN included
+#pragma unroll
+                    for (int q = 0; q < kQuads; ++q) {
+                        o[i][q][0] = fmaf(w, vq[q].x, o[i][q][0]);
+                        o[i][q][1] = fmaf(w, vq[q].y, o[i][q][1]);
+                        o[i][q][2] = fmaf(w, vq[q].z, o[i][q][2]);
+                        o[i][q][3] = fmaf(w, vq[q].w, o[i][q][3]);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    }
+
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int r = ty * kPer + i;
+        if (r >= n_rows) continue;
+        if (slot >= 0) {
+            float *base = p.part + slot * part_slot_floats(p.part_rows, d);
+#pragma unroll
+            for (int q = 0; q < kQuads; ++q)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int c = 64 * q + 4 * tx + e;
+                    if (c < d) base[(int64_t)r * d + c] = o[i][q][e];
+                }
+            if (tx == 0) {
+                base[(int64_t)p.part_rows * d + r] = m[i];
+                base[(int64_t)p.part_rows * (d + 1) + r] = l[i];
+            }
+        } else {
+            const int32_t g = row0 + r;
+            const int64_t row = (int64_t)(rq.t0 + g / p.group) * p.q_heads + h * p.group + g % p.group;
+            const float inv = l[i] == 0.0f ? 0.0f : 1.0f / l[i];
+#pragma unroll
+            for (int q = 0; q < kQuads; ++q)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int c = 64 * q + 4 * tx + e;
+                    if (c < d) put((T *)p.out + row * d + c, o[i][q][e] * inv);
+                }
+            if (tx == 0 && p.lse)
+                p.lse[row] = l[i] == 0.0f ? -INFINITY : (m[i] + log2f(l[i])) * 0.6931471805599453f;
+        }
+    }
+}
+
+template <typename T, typename C, bool kPaged, int kRows, int kDMax>
+__global__ void __launch_bounds__(kThreads) simt_kernel(const Params p, bool vec_q, bool vec_k) {
+    extern __shared__ __align__(16) float smem[];
+    __shared__ StartScratch scratch;
+    grid_dep_wait();
+    grid_dep_launch();
+    bool bad = false, any_bad = false;
+    if constexpr (kPaged) {
+        const Start s = find_start(p, &scratch, &any_bad);
+        int64_t u = s.u, before = s.before;  // units before request b
+        const int64_t end = s.end;
+        for (int b = s.b; b < p.batch && u < end; ++b) {
+            const Request r = load_request<true>(p, b, &bad);
+            const int64_t n = request_units(p, r);
+            while (u < end && u < before + n) {
+                const int32_t tiles = key_tiles(r);
+                const int64_t item = (u - before) / tiles;
+                const int32_t t0 = (int32_t)((u - before) % tiles);
+                const int32_t t1 = (int32_t)min((int64_t)tiles, t0 + (end - u));
+                const int32_t nrb = row_blocks(p, r);
+                const bool whole = t0 == 0 && t1 == tiles;
+                run_piece<T, C, true, kRows, kDMax>(
+                    p, r, b, (int32_t)(item / nrb), (int32_t)(item % nrb), t0 * kKeyTile,
+                    min(t1 * kKeyTile, r.len), whole ? -1 : 2 * (int64_t)blockIdx.x + (t0 == 0),
+                    smem, vec_q, vec_k, &any_bad);
+                u += t1 - t0;
+            }
+            before += n;
+        }
+    } else {
+        // CTA (x, h): row block number `want` of all requests, the last blocks
+        // (which see the most keys) first
+        const int32_t h = blockIdx.y;
+        int64_t want = (int64_t)gridDim.x - 1 - blockIdx.x;
+        for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
+            const int b = b0 + threadIdx.x;
+            Request r{};
+            int64_t n = 0;
+            if (b < p.batch) {
+                r = load_request<false>(p, b, &bad);
+                any_bad |= bad;
+                n = row_blocks(p, r);
+            }
+            const int64_t total = block_sum(n, scratch.red);
+            if (want >= total) {
+                want -= total;
+                continue;
+            }
+            // walk this chunk: few requests hold most of the blocks
+            for (int i = b0; i < min(p.batch, b0 + kThreads); ++i) {
+                r = load_request<false>(p, i, &bad);
+                n = row_blocks(p, r);
+                if (want < n) {
+                    const int64_t last = min((int64_t)r.t * p.group, (want + 1) * kRows) - 1;
+                    run_piece<T, C, false, kRows, kDMax>(p, r, i, h, (int32_t)want, 0,
+                                                         (int32_t)(last / p.group) + 1, -1, smem,
+                                                         vec_q, vec_k, &any_bad);
+                    break;
+                }
+                want -= n;
+            }
+            break;
+        }
+    }
+    if (any_bad && p.err) atomicOr(p.err, DFLASH2_DEVERR_ID_RANGE);
+}
+
+// Joins the partial rows of items that span CTAs: one warp per (token, query
+// head), partials in CTA order, each lane four of 128 values.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) combine_kernel(const Params p) {
+    __shared__ int64_t red[kThreads / 32];
+    const int32_t tok = blockIdx.x;
+    // before the grid dependency only what was complete before the attention
+    // kernel started is read: cu_q and kv_lens (it releases this grid after its
+    // own wait)
+    bool bad;
+    int64_t all = 0, mine = 0;
+    __shared__ int32_t which;
+    if (threadIdx.x == 0) which = -1;
+    __syncthreads();
+    for (int b = threadIdx.x; b < p.batch; b += kThreads) {
+        const Request r = load_request<true>(p, b, &bad);
+        if (tok >= r.t0 && tok < r.t0 + r.t) which = b;
+    }
+    __syncthreads();
+    const int32_t mb = which;
+    for (int b = threadIdx.x; b < p.batch; b += kThreads) {
+        const Request r = load_request<true>(p, b, &bad);
+        const int64_t n = request_units(p, r);
+        all += n;
+        if (b < mb) mine += n;
+    }
+    const int64_t units = block_sum(all, red);
+    const int64_t before = block_sum(mine, red);
+    grid_dep_wait();
+    if (mb < 0) return;
+    const Request r = load_request<true>(p, mb, &bad);
+    const int32_t tiles = key_tiles(r), nrb = row_blocks(p, r);
+    const int lane = threadIdx.x & 31;
+    const int d = p.head_dim;
+    const int64_t slot_floats = part_slot_floats(p.part_rows, d);
+    for (int g = blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5); g < p.q_heads;
+         g += gridDim.y * (kThreads / 32)) {
+        const int32_t h = g / p.group;
+        const int64_t row = (int64_t)(tok - r.t0) * p.group + g % p.group;
+        const int32_t rb = (int32_t)(row / p.row_block), rr = (int32_t)(row % p.row_block);
+        const int64_t u0 = before + ((int64_t)h * nrb + rb) * tiles;
+        const int64_t n_cta = split_ctas(p, units);
+        const int32_t c0 = cta_of(u0, units, n_cta), c1 = cta_of(u0 + tiles - 1, units, n_cta);
+        if (c0 == c1) continue;  // the attention kernel wrote this row
+        auto part = [&](int32_t c) { return p.part + (2 * (int64_t)c + (c == c0)) * slot_floats; };
+        float m = -INFINITY;
+        for (int32_t c = c0 + lane; c <= c1; c += 32)
+            m = fmaxf(m, part(c)[(int64_t)p.part_rows * d + rr]);
+        m = warp_max(m);
+        const float base = m == -INFINITY ? 0.0f : m;
+        float l = 0.0f;
+        float o[8] = {};
+        for (int32_t c = c0; c <= c1; ++c) {
+            const float *s = part(c);
+            const float w = ex2(s[(int64_t)p.part_rows * d + rr] - base);
+            l = fmaf(w, s[(int64_t)p.part_rows * (d + 1) + rr], l);
+            if (w == 0.0f) continue;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (lane + 32 * j < d) o[j] = fmaf(w, s[(int64_t)rr * d + lane + 32 * j], o[j]);
+        }
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const int64_t at = (int64_t)tok * p.q_heads + g;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (lane + 32 * j < d) put((T *)p.out + at * d + lane + 32 * j, o[j] * inv);
+        if (lane == 0 && p.lse)
+            p.lse[at] = l == 0.0f ? -INFINITY : (base + log2f(l)) * 0.6931471805599453f;
+    }
+}
+
+template <typename T, typename C, bool kPaged, int kRows, int kDMax>
+dflash2_status launch_one(Params p, bool vec_q, bool vec_k, cudaStream_t st) {
+    constexpr int kSmem = simt_smem_floats(kRows, kDMax) * 4;
+    auto fn = simt_kernel<T, C, kPaged, kRows, kDMax>;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) {
+        cudaGetLastError();
+        return DFLASH2_ERR_CUDA;
+    }
+    p.row_block = kRows;
+    dim3 grid((unsigned)p.n_cta);
+    if (!kPaged)  // every row block of every request, and at most one short one each
+        grid = dim3((unsigned)(((int64_t)p.total_q * p.group + kRows - 1) / kRows + p.batch),
+                    (unsigned)p.kv_heads);
+    launch_k(fn, grid, dim3(kThreads), kSmem, st, p, vec_q, vec_k);
+    return launch_status();
+}
+
+template <typename T, typename C, bool kPaged>
+dflash2_status launch_typed(const Params &p, bool vec_q, bool vec_k, cudaStream_t st) {
+    // few rows per (request, head) on average: the 16-row tile
+    const bool few = (int64_t)p.total_q * p.group <= 16ll * p.batch;
+    if (p.head_dim <= 64)
+        return few ? launch_one<T, C, kPaged, 16, 64>(p, vec_q, vec_k, st)
+                   : launch_one<T, C, kPaged, 64, 64>(p, vec_q, vec_k, st);
+    if (p.head_dim <= 128)
+        return few ? launch_one<T, C, kPaged, 16, 128>(p, vec_q, vec_k, st)
+                   : launch_one<T, C, kPaged, 64, 128>(p, vec_q, vec_k, st);
+    return few ? launch_one<T, C, kPaged, 16, 256>(p, vec_q, vec_k, st)
+               : launch_one<T, C, kPaged, 64, 256>(p, vec_q, vec_k, st);
+}
+
+bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+}  // namespace
+
+dflash2_status launch_simt(const DeviceInfo &di, Params p, bool paged, int32_t dtype,
+                           int32_t kv_format, cudaStream_t st) {
+    const int el = dtype == DFLASH2_F32 ? 4 : 2;
+    const int kel = kv_format == DFLASH2_KV_E4M3 ? 1 : el;
+    const bool four = p.head_dim % 4 == 0;
+    const bool vec_q = four && aligned_to(p.q, 4 * el) && p.q_stride % 4 == 0;
+    const bool vec_k = four && aligned_to(p.k, 4 * kel) && aligned_to(p.v, 4 * kel) &&
+                       (paged || (p.k_stride % 4 == 0 && p.v_stride % 4 == 0));
+    p.n_cta = di.sm_count;
+    dflash2_status s;
+    if (dtype == DFLASH2_F32) {
+        if (!paged)
+            s = launch_typed<float, float, false>(p, vec_q, vec_k, st);
+        else if (kv_format == DFLASH2_KV_E4M3)
+            s = launch_typed<float, uint8_t, true>(p, vec_q, vec_k, st);
+        else
+            s = launch_typed<float, float, true>(p, vec_q, vec_k, st);
+    } else {
+        if (!paged)
+            s = launch_typed<__nv_bfloat16, __nv_bfloat16, false>(p, vec_q, vec_k, st);
+        else if (kv_format == DFLASH2_KV_E4M3)
+            s = launch_typed<__nv_bfloat16, uint8_t, true>(p, vec_q, vec_k, st);
+        else
+            s = launch_typed<__nv_bfloat16, __nv_bfloat16, true>(p, vec_q, vec_k, st);
+    }
+    if (s != DFLASH2_OK || !paged) return s;
+    p.row_block = (int64_t)p.total_q * p.group <= 16ll * p.batch ? 16 : 64;
+    return launch_combine(di, p, dtype, st);
+}
+
+dflash2_status launch_combine(const DeviceInfo &, const Params &p, int32_t dtype, cudaStream_t st) {
+    const int warps = kThreads / 32;
+    const dim3 grid((unsigned)p.total_q, (unsigned)((p.q_heads + warps - 1) / warps));
+    if (dtype == DFLASH2_F32)
+        launch_k(combine_kernel<float>, grid, dim3(kThreads), 0, st, p);
+    else
+        launch_k(combine_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, st, p);
+    return launch_status();
+}
+
+}  // namespace attn
+}  // namespace dflash2

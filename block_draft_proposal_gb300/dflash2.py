@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import numpy as np
 import torch
@@ -25,6 +26,7 @@ _lib = None
 
 OK = 0
 F32, BF16 = 0, 1
+KV_NATIVE, KV_E4M3 = 0, 1
 DEVERR_ID_RANGE = 0x1
 DEVERR_TIMEOUT = 0x2
 DEVERR_SHORT = 0x4
@@ -43,6 +45,9 @@ EXPORTS = (
     "dflash2_unary_topk_fp8_workspace_size", "dflash2_unary_topk_fp8",
     "dflash2_quantize_rows_nvfp4", "dflash2_unary_topk_nvfp4_workspace_size",
     "dflash2_unary_topk_nvfp4", "dflash2_nvfp4_scale_tiles_size", "dflash2_nvfp4_tile_scales",
+    "dflash2_kv_cache_write", "dflash2_kv_cache_read", "dflash2_tree_attention_workspace_size",
+    "dflash2_tree_attention", "dflash2_prompt_attention_workspace_size",
+    "dflash2_prompt_attention",
 )
 NOALLOC_SCRATCH_BYTES = 4 << 20
 
@@ -126,6 +131,23 @@ def library():
         lib.dflash2_nvfp4_tile_scales.restype = i32
         lib.dflash2_topk_merge.argtypes = [P, P, P, i32, i64, i32, i32, P, P, P, P]
         lib.dflash2_topk_merge.restype = i32
+        lib.dflash2_kv_cache_write.argtypes = [P, P, i64, i64, P, i64, i32, i32, i32, i64, i32,
+                                               i32, P, P, P, P, P, P]
+        lib.dflash2_kv_cache_write.restype = i32
+        lib.dflash2_kv_cache_read.argtypes = [P, P, P, P, P, i64, i32, i32, i32, i64, i32, i32, P,
+                                              P, P, P]
+        lib.dflash2_kv_cache_read.restype = i32
+        lib.dflash2_tree_attention_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+        lib.dflash2_tree_attention_workspace_size.restype = sz
+        lib.dflash2_tree_attention.argtypes = [P, i64, P, P, P, P, P, i32, i64, i32, P, P, P, i32,
+                                               i32, i32, i32, i32, i32, f32, i32, i32, P, P, P, sz,
+                                               P, P]
+        lib.dflash2_tree_attention.restype = i32
+        lib.dflash2_prompt_attention_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+        lib.dflash2_prompt_attention_workspace_size.restype = sz
+        lib.dflash2_prompt_attention.argtypes = [P, P, P, i64, i64, i64, P, i32, i32, i32, i32,
+                                                 i32, f32, i32, P, P, P, sz, P, P]
+        lib.dflash2_prompt_attention.restype = i32
         lib.dflash2_unary_topk_launches.argtypes = [i64, i64, i32, f32, i32]
         lib.dflash2_unary_topk_launches.restype = i32
         if lib.dflash2_abi_version() != ABI_VERSION:
@@ -678,6 +700,201 @@ def philox_uniforms(seed: int, n: int, out=None, offset: int = 0, counter=None, 
         int(seed) & (2**64 - 1), int(offset) & (2**64 - 1), _ptr(counter), int(n), _ptr(out),
         _stream(stream)))
     return out
+
+
+# ---- paged key/value cache and attention ----------------------------------------------
+
+class KVCache(NamedTuple):
+    """One layer's paged cache: keys and values [pages, kv_heads, page_size,
+    head_dim], in float32 or bfloat16, or as uint8 E4M3 codes with one exponent
+    byte per row in k_exp and v_exp [pages, kv_heads, page_size].  A slot is
+    page * page_size + offset.  The tensors are the caller's."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_exp: torch.Tensor | None = None
+    v_exp: torch.Tensor | None = None
+
+    @property
+    def e4m3(self) -> bool:
+        return self.k.dtype == torch.uint8
+
+
+def new_kv_cache(pages: int, page_size: int, kv_heads: int, head_dim: int,
+                 dtype=torch.bfloat16, e4m3: bool = False, device="cuda") -> KVCache:
+    """An empty cache: rows in `dtype`, or E4M3 codes and exponents.  What is
+    not written yet holds zeros."""
+    shape = (pages, kv_heads, page_size, head_dim)
+    held = torch.uint8 if e4m3 else dtype
+    k, v = (torch.zeros(shape, dtype=held, device=device) for _ in range(2))
+    if not e4m3:
+        return KVCache(k, v)
+    return KVCache(k, v, *(torch.full(shape[:3], 127, dtype=torch.uint8, device=device)
+                           for _ in range(2)))
+
+
+def _need_rows(t: torch.Tensor, name: str, dtype, shape) -> int:
+    """A [tokens, heads, head_dim] tensor whose tokens may be strided (a slice
+    of a packed projection) with contiguous heads; returns the token stride."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    n, heads, d = t.shape
+    st = t.stride()
+    if (st[2] != 1 and d > 1) or (st[1] != d and heads > 1):
+        raise ValueError(f"{name} must have contiguous heads")
+    if n > 1 and st[0] < heads * d:
+        raise ValueError(f"{name} must not repeat tokens")
+    return st[0] if n > 1 else heads * d
+
+
+def _need_cache(c: KVCache, dtype):
+    pages, heads, ps, d = c.k.shape
+    if c.e4m3:
+        if c.k_exp is None or c.v_exp is None:
+            raise ValueError("an E4M3 cache needs k_exp and v_exp")
+        _need(c.k, "cache.k", torch.uint8)
+        _need(c.v, "cache.v", torch.uint8, c.k.shape)
+        _need(c.k_exp, "cache.k_exp", torch.uint8, (pages, heads, ps))
+        _need(c.v_exp, "cache.v_exp", torch.uint8, (pages, heads, ps))
+        return pages, heads, ps, d, KV_E4M3
+    _need(c.k, "cache.k", dtype)
+    _need(c.v, "cache.v", dtype, c.k.shape)
+    return pages, heads, ps, d, KV_NATIVE
+
+
+def kv_cache_write(cache: KVCache, k, v, slots, err=None, stream=None):
+    """dflash2_kv_cache_write: keys and values [n, kv_heads, head_dim] into
+    their slots (int64 [n], negative skips); an E4M3 cache is quantised on the
+    way.  k and v may be slices of a packed projection."""
+    pages, heads, ps, d, fmt = _need_cache(cache, k.dtype)
+    n = k.shape[0]
+    ks = _need_rows(k, "k", k.dtype, (n, heads, d))
+    vs = _need_rows(v, "v", k.dtype, (n, heads, d))
+    _need(slots, "slots", torch.int64, (n,))
+    if err is None:
+        err = torch.zeros(1, dtype=torch.int32, device=k.device)
+    _check("dflash2_kv_cache_write", library().dflash2_kv_cache_write(
+        _ptr(k), _ptr(v), ks, vs, _ptr(slots), n, heads, d, ps, pages, _dtype_code(k), fmt,
+        _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_exp), _ptr(cache.v_exp), _ptr(err),
+        _stream(stream)))
+    return err
+
+
+def kv_cache_read(cache: KVCache, slots, dtype=torch.bfloat16, k_out=None, v_out=None, err=None,
+                  stream=None):
+    """dflash2_kv_cache_read: the rows at `slots` (int64 [n], negative gives
+    zeros) as keys and values [n, kv_heads, head_dim] in `dtype`."""
+    pages, heads, ps, d, fmt = _need_cache(cache, dtype)
+    _need(slots, "slots", torch.int64)
+    n = slots.numel()
+    if k_out is None:
+        k_out = torch.empty((n, heads, d), dtype=dtype, device=slots.device)
+    if v_out is None:
+        v_out = torch.empty((n, heads, d), dtype=dtype, device=slots.device)
+    _need(k_out, "k_out", dtype, (n, heads, d))
+    _need(v_out, "v_out", dtype, (n, heads, d))
+    if err is None:
+        err = torch.zeros(1, dtype=torch.int32, device=slots.device)
+    _check("dflash2_kv_cache_read", library().dflash2_kv_cache_read(
+        _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_exp), _ptr(cache.v_exp), _ptr(slots), n, heads,
+        d, ps, pages, _dtype_code(k_out), fmt, _ptr(k_out), _ptr(v_out), _ptr(err),
+        _stream(stream)))
+    return k_out, v_out, err
+
+
+def tree_attention_workspace_size(total_q: int, batch: int, q_heads: int, kv_heads: int,
+                                  head_dim: int) -> int:
+    return int(library().dflash2_tree_attention_workspace_size(total_q, batch, q_heads, kv_heads,
+                                                               head_dim))
+
+
+def tree_attention(q, cache: KVCache, page_table, cu_q, kv_lens, scale: float, tree_mask=None,
+                   out=None, lse=None, with_lse: bool = False, workspace=None, err=None,
+                   stream=None):
+    """dflash2_tree_attention: drafted tokens' queries q [total_q, q_heads,
+    head_dim] (tokens may be strided) over the paged cache, which already
+    holds their keys and values as each request's last cu_q[b + 1] - cu_q[b]
+    of kv_lens[b] positions (page_table int32 [batch, max_pages]).  tree_mask
+    int64 [total_q, words]: bit j of a row, it sees node j; None, a chain.
+    Returns (out, lse or None, err)."""
+    total, heads, d = q.shape
+    pages, kv_heads, ps, kd, fmt = _need_cache(cache, q.dtype)
+    if kd != d:
+        raise ValueError(f"q has head_dim {d}, the cache {kd}")
+    batch, max_pages = page_table.shape
+    qs = _need_rows(q, "q", q.dtype, (total, heads, d))
+    _need(page_table, "page_table", torch.int32)
+    _need(cu_q, "cu_q", torch.int32, (batch + 1,))
+    _need(kv_lens, "kv_lens", torch.int32, (batch,))
+    words = 0
+    if tree_mask is not None:
+        words = tree_mask.shape[-1]
+        _need(tree_mask, "tree_mask", torch.int64, (total, words))
+    dev = q.device
+    if out is None:
+        out = torch.empty((total, heads, d), dtype=q.dtype, device=dev)
+    _need(out, "out", q.dtype, (total, heads, d))
+    if lse is None and with_lse:
+        lse = torch.empty((total, heads), dtype=torch.float32, device=dev)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (total, heads))
+    if workspace is None:
+        workspace = torch.empty(max(1, tree_attention_workspace_size(total, batch, heads, kv_heads,
+                                                                     d)),
+                                dtype=torch.uint8, device=dev)
+    if err is None:
+        err = torch.zeros(1, dtype=torch.int32, device=dev)
+    _check("dflash2_tree_attention", library().dflash2_tree_attention(
+        _ptr(q), qs, _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_exp), _ptr(cache.v_exp),
+        _ptr(page_table), max_pages, pages, ps, _ptr(cu_q), _ptr(kv_lens), _ptr(tree_mask), words,
+        batch, total, heads, kv_heads, d, float(scale), _dtype_code(q), fmt, _ptr(out), _ptr(lse),
+        _ptr(workspace), workspace.numel(), _ptr(err), _stream(stream)))
+    return out, lse, err
+
+
+def prompt_attention_workspace_size(total_q: int, batch: int, q_heads: int, kv_heads: int,
+                                    head_dim: int) -> int:
+    return int(library().dflash2_prompt_attention_workspace_size(total_q, batch, q_heads, kv_heads,
+                                                                 head_dim))
+
+
+def prompt_attention(q, k, v, cu_q, scale: float, out=None, lse=None, with_lse: bool = False,
+                     workspace=None, err=None, stream=None):
+    """dflash2_prompt_attention: causal attention of packed prompts, q
+    [total_q, q_heads, head_dim], k and v [total_q, kv_heads, head_dim] (slices
+    of one packed projection are read in place), request b the tokens cu_q[b]
+    .. cu_q[b + 1] - 1.  Returns (out, lse or None, err)."""
+    total, heads, d = q.shape
+    kv_heads = k.shape[1]
+    qs = _need_rows(q, "q", q.dtype, (total, heads, d))
+    ks = _need_rows(k, "k", q.dtype, (total, kv_heads, d))
+    vs = _need_rows(v, "v", q.dtype, (total, kv_heads, d))
+    _need(cu_q, "cu_q", torch.int32)
+    batch = cu_q.numel() - 1
+    if batch < 0:
+        raise ValueError("cu_q must have batch + 1 entries")
+    dev = q.device
+    if out is None:
+        out = torch.empty((total, heads, d), dtype=q.dtype, device=dev)
+    _need(out, "out", q.dtype, (total, heads, d))
+    if lse is None and with_lse:
+        lse = torch.empty((total, heads), dtype=torch.float32, device=dev)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (total, heads))
+    if workspace is None:
+        workspace = torch.empty(max(1, prompt_attention_workspace_size(total, batch, heads,
+                                                                       kv_heads, d)),
+                                dtype=torch.uint8, device=dev)
+    if err is None:
+        err = torch.zeros(1, dtype=torch.int32, device=dev)
+    _check("dflash2_prompt_attention", library().dflash2_prompt_attention(
+        _ptr(q), _ptr(k), _ptr(v), qs, ks, vs, _ptr(cu_q), batch, total, heads, kv_heads, d,
+        float(scale), _dtype_code(q), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(),
+        _ptr(err), _stream(stream)))
+    return out, lse, err
 
 
 # ---- host <-> device helpers (plumbing) ----------------------------------------------

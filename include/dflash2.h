@@ -559,6 +559,160 @@ dflash2_status dflash2_d2t_remap(const int64_t *draft_ids, const int64_t *d2t, i
                                  int64_t draft_vocab, int64_t target_vocab,
                                  int64_t *target_ids, int32_t *err_word, void *stream);
 
+/*
+ * Paged key/value cache and attention of one layer, beside the proposal: the
+ * target model's side of a verified block (and any attention layer of the
+ * draft).  The pages leave attention to the serving engine; the definitions
+ * here are the standard ones.
+ *
+ * A cache is a pair of arrays [num_pages, kv_heads, page_size, head_dim], keys
+ * and values, and a slot is page * page_size + offset.  kv_format:
+ *   DFLASH2_KV_NATIVE  rows in `dtype`; k_exp and v_exp are not read (NULL).
+ *   DFLASH2_KV_E4M3    uint8 E4M3 codes c, and k_exp / v_exp uint8
+ *                      [num_pages, kv_heads, page_size], one exponent byte per
+ *                      row of head_dim values: a row stands for c * 2^(byte - 127).
+ * The scale is a power of two, so a code keeps E4M3's four significant bits
+ * whatever the row's magnitude and a row is exact in bf16 once read.
+ */
+typedef enum { DFLASH2_KV_NATIVE = 0, DFLASH2_KV_E4M3 = 1 } dflash2_kv_format;
+
+/*
+ * Writes keys and values of n_tokens tokens into their slots.
+ *   native:  cache row = input row.
+ *   E4M3:    e = the smallest integer in [-48, 48] with amax <= 448 * 2^e
+ *            (amax over the row's values that are not NaN), byte = e + 127,
+ *            c = E4M3(x * 2^-e), to nearest even, saturating at 448 (infinities
+ *            too); NaN becomes the NaN code.
+ *
+ * k, v      device, rows [kv_heads, head_dim] of token i at k + i * k_row_stride
+ *           elements (v likewise), so slices of one projection are read in place.
+ * slots     device int64 [n_tokens]; a negative slot skips the token.  Two
+ *           tokens with one slot leave it with either token's row.
+ * k_cache, v_cache, k_exp, v_exp  as above, written.
+ * Errors:   head_dim outside [1, 256], kv_heads < 1, page_size < 1, num_pages
+ *           < 0, n_tokens < 0, n_tokens * kv_heads >= 2^30, a row stride below
+ *           kv_heads * head_dim, a null pointer -> INVALID_ARG; kv_format or
+ *           dtype unknown -> UNSUPPORTED_DTYPE; a pointer not aligned to its
+ *           element -> MISALIGNED.  n_tokens == 0 queues nothing.
+ * Device:   a slot at or above num_pages * page_size is skipped and sets
+ *           DFLASH2_DEVERR_ID_RANGE.
+ * The fast path wants head_dim 64, 128 or 256 and every row 16-byte aligned
+ * (8-byte for E4M3 codes); other layouts take a scalar path.
+ */
+dflash2_status dflash2_kv_cache_write(const void *k, const void *v, int64_t k_row_stride,
+                                      int64_t v_row_stride, const int64_t *slots,
+                                      int64_t n_tokens, int32_t kv_heads, int32_t head_dim,
+                                      int32_t page_size, int64_t num_pages, int32_t dtype,
+                                      int32_t kv_format, void *k_cache, void *v_cache,
+                                      uint8_t *k_exp, uint8_t *v_exp, int32_t *err_word,
+                                      void *stream);
+
+/*
+ * Reads the rows at `slots` back: k_out, v_out device [n_tokens, kv_heads,
+ * head_dim] in dtype (E4M3: c * 2^(byte - 127), exact in bf16 and fp32).  Read
+ * and written again, E4M3 rows keep their values, so accepted tokens of a tree
+ * are moved by a read and a write.  Arguments, errors and fast path as for
+ * dflash2_kv_cache_write.
+ * Device:   a negative slot gives zero rows; one at or above num_pages *
+ *           page_size gives zero rows and sets DFLASH2_DEVERR_ID_RANGE.
+ */
+dflash2_status dflash2_kv_cache_read(const void *k_cache, const void *v_cache,
+                                     const uint8_t *k_exp, const uint8_t *v_exp,
+                                     const int64_t *slots, int64_t n_tokens, int32_t kv_heads,
+                                     int32_t head_dim, int32_t page_size, int64_t num_pages,
+                                     int32_t dtype, int32_t kv_format, void *k_out, void *v_out,
+                                     int32_t *err_word, void *stream);
+
+/*
+ * Attention of drafted tokens over the paged cache: the verification pass of
+ * a chain, a block or a tree, and with one token per request plain decoding.
+ * Request b has T = cu_q[b + 1] - cu_q[b] drafted tokens, whose keys and
+ * values are the last T of its kv_lens[b] cached positions; position l is at
+ * offset l % page_size of page page_table[b, l / page_size].  With ctx =
+ * kv_lens[b] - T, token i of the request and query head a (key/value head
+ * a / (q_heads / kv_heads)):
+ *
+ *   out[i, a] = sum_l p_l v_l,   p = softmax over the seen l of scale * <q[i, a], k_l>
+ *   seen: every l < ctx, and l = ctx + j where
+ *         tree_mask == NULL: j <= i;  else bit j % 64 of tree_mask[row i, j / 64].
+ *   lse[i, a] = log(sum of exp(scale * <q, k_l>)) over the seen l.
+ *
+ * A row that sees no key gives zeros and lse -inf.  What a row does not see
+ * (masked nodes, the rest of a page, other pages) does not reach it, whatever
+ * it holds, NaN included; a seen key of weight zero adds nothing.
+ *
+ * q          device, rows [q_heads, head_dim] of token i at q + i * q_row_stride
+ *            elements; tokens of all requests packed in order.
+ * cu_q       device int32 [batch + 1], cu_q[0] = 0, rising to total_q.
+ * kv_lens    device int32 [batch].
+ * page_table device int32 [batch, max_pages].
+ * tree_mask  device int64 [total_q, mask_words] or NULL.  Nodes from 64 *
+ *            mask_words on are not seen.
+ * out        device [total_q, q_heads, head_dim] dtype; lse device float
+ *            [total_q, q_heads] or NULL.
+ * workspace  device, 16-byte aligned, ws_bytes >=
+ *            dflash2_tree_attention_workspace_size(...): partial sums of the
+ *            rows whose keys are split over CTAs.  Contents need no clearing.
+ * Arithmetic: products, softmax statistics and sums in fp32 (exponentials by
+ *   PTX ex2.approx.ftz.f32).  bf16 with head_dim 64 or 128, page_size a power
+ *   of two >= 16 and 16-byte aligned rows: tcgen05 MMAs with the weights p
+ *   rounded to bf16 (native cache) or fp16 (E4M3 cache, whose codes are exact in fp16 and
+ *   whose queries are scaled by a power of two per row) before p * v; otherwise
+ *   fp32 on CUDA cores.  Reduction orders are fixed, so results are
+ *   deterministic.
+ * Errors:    q_heads not a multiple of kv_heads, q_heads / kv_heads > 128,
+ *            head_dim outside [1, 256], a size < 1 (batch, total_q: < 0),
+ *            num_pages * kv_heads >= 2^31, max_pages * page_size >= 2^31,
+ *            batch > 65536, total_q * q_heads >= 2^31, scale not finite, a
+ *            null pointer -> INVALID_ARG; unknown dtype or kv_format ->
+ *            UNSUPPORTED_DTYPE; a pointer not aligned to its element ->
+ *            MISALIGNED.  total_q == 0 or batch == 0 queues nothing.
+ * Device:    DFLASH2_DEVERR_ID_RANGE, with a defined result, for a cu_q that
+ *            falls or leaves [0, total_q] (clamped), kv_lens outside
+ *            [T, max_pages * page_size] (the request's rows see nothing), a
+ *            page outside [0, num_pages) (its rows are zero), and T above 64 *
+ *            mask_words.
+ */
+size_t dflash2_tree_attention_workspace_size(int32_t total_q, int32_t batch, int32_t q_heads,
+                                             int32_t kv_heads, int32_t head_dim);
+dflash2_status dflash2_tree_attention(const void *q, int64_t q_row_stride, const void *k_cache,
+                                      const void *v_cache, const uint8_t *k_exp,
+                                      const uint8_t *v_exp, const int32_t *page_table,
+                                      int32_t max_pages, int64_t num_pages, int32_t page_size,
+                                      const int32_t *cu_q, const int32_t *kv_lens,
+                                      const int64_t *tree_mask, int32_t mask_words,
+                                      int32_t batch, int32_t total_q, int32_t q_heads,
+                                      int32_t kv_heads, int32_t head_dim, float scale,
+                                      int32_t dtype, int32_t kv_format, void *out, float *lse,
+                                      void *workspace, size_t ws_bytes, int32_t *err_word,
+                                      void *stream);
+
+/*
+ * Causal attention of whole prompts, packed: request b is the tokens cu_q[b]
+ * .. cu_q[b + 1] - 1 of q, k and v, and token i of it sees its tokens 0 .. i.
+ * Formula, masking rule, out, lse, cu_q and arithmetic as for
+ * dflash2_tree_attention; k and v rows [kv_heads, head_dim] of token i at
+ * k + i * k_row_stride elements (v likewise), so slices of one packed
+ * projection are read in place.
+ *
+ * workspace  device, 16-byte aligned, ws_bytes >=
+ *            dflash2_prompt_attention_workspace_size(...).  Contents need no clearing.
+ * Errors:    as for dflash2_tree_attention; a row stride below heads *
+ *            head_dim -> INVALID_ARG.  The tcgen05 path wants bf16, head_dim
+ *            64 or 128 and 16-byte aligned rows.
+ * Device:    a cu_q that falls or leaves [0, total_q] is clamped and sets
+ *            DFLASH2_DEVERR_ID_RANGE; rows of tokens in no request are not written.
+ */
+size_t dflash2_prompt_attention_workspace_size(int32_t total_q, int32_t batch, int32_t q_heads,
+                                               int32_t kv_heads, int32_t head_dim);
+dflash2_status dflash2_prompt_attention(const void *q, const void *k, const void *v,
+                                        int64_t q_row_stride, int64_t k_row_stride,
+                                        int64_t v_row_stride, const int32_t *cu_q, int32_t batch,
+                                        int32_t total_q, int32_t q_heads, int32_t kv_heads,
+                                        int32_t head_dim, float scale, int32_t dtype, void *out,
+                                        float *lse, void *workspace, size_t ws_bytes,
+                                        int32_t *err_word, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
