@@ -24,7 +24,7 @@ dflash2_status check_shape(int32_t batch, int32_t total_q, int32_t q_heads, int3
     if (batch < 0 || batch > attn::kMaxBatch || total_q < 0 || kv_heads < 1 || kv_heads > 65535 ||
         q_heads < 1 || q_heads % kv_heads != 0 || q_heads / kv_heads > attn::kMaxGroup ||
         head_dim < 1 || head_dim > 256 || (int64_t)total_q * q_heads >= (1ll << 31) ||
-        !isfinite(scale))
+        !isfinite(scale * 1.4426950408889634f))
         return DFLASH2_ERR_INVALID_ARG;
     return DFLASH2_OK;
 }
@@ -81,7 +81,9 @@ extern "C" dflash2_status dflash2_tree_attention(
     p.kv_heads = kv_heads, p.group = q_heads / kv_heads, p.head_dim = head_dim;
     p.scale_log2 = scale * 1.4426950408889634f, p.out = out, p.lse = lse;
     p.part = static_cast<float *>(workspace), p.part_rows = slot_rows(total_q, p.group), p.err = err_word;
-    return attn::launch_simt(di, p, true, dtype, kv_format, static_cast<cudaStream_t>(stream));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (attn::tc_takes(p, true, dtype, kv_format)) return attn::launch_tc(di, p, true, kv_format, s);
+    return attn::launch_simt(di, p, true, dtype, kv_format, s);
 }
 
 extern "C" size_t dflash2_prompt_attention_workspace_size(int32_t total_q, int32_t batch,
@@ -119,6 +121,8 @@ extern "C" dflash2_status dflash2_prompt_attention(
     p.v_stride = v_row_stride, p.cu_q = cu_q, p.batch = batch, p.total_q = total_q;
     p.q_heads = q_heads, p.kv_heads = kv_heads, p.group = q_heads / kv_heads, p.head_dim = head_dim;
     p.scale_log2 = scale * 1.4426950408889634f, p.out = out, p.lse = lse, p.err = err_word;
-    return attn::launch_simt(di, p, false, dtype, DFLASH2_KV_NATIVE,
-                             static_cast<cudaStream_t>(stream));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (attn::tc_takes(p, false, dtype, DFLASH2_KV_NATIVE))
+        return attn::launch_tc(di, p, false, DFLASH2_KV_NATIVE, s);
+    return attn::launch_simt(di, p, false, dtype, DFLASH2_KV_NATIVE, s);
 }

@@ -77,6 +77,13 @@ dflash2_status encode_tmap_bytes_2d(CUtensorMap *map, const void *base, uint64_t
 dflash2_status encode_tmap_2d(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols,
                               uint32_t box_rows, uint32_t elem_bytes);
 
+// A 3-D tensor map (uint8 elements, elem_bytes = 1, or bf16, 2) of a {box}
+// whose inner extent is one swizzle row (64 or 128 bytes), zero fill out of
+// bounds; strides are the bytes of dimensions 1 and 2.
+dflash2_status encode_tmap_3d(CUtensorMap *map, const void *base, const uint64_t (&dims)[3],
+                              const uint64_t (&strides)[2], const uint32_t (&box)[3],
+                              uint32_t elem_bytes);
+
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 inline dflash2_status launch_status() {

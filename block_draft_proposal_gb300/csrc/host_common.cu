@@ -85,6 +85,25 @@ dflash2_status encode_tmap_2d(CUtensorMap *map, const void *base, uint64_t rows,
     return r == CUDA_SUCCESS ? DFLASH2_OK : DFLASH2_ERR_CUDA;
 }
 
+dflash2_status encode_tmap_3d(CUtensorMap *map, const void *base, const uint64_t (&dims)[3],
+                              const uint64_t (&strides)[2], const uint32_t (&box)[3],
+                              uint32_t elem_bytes) {
+    const dflash2_status st = resolve_encode();
+    if (st != DFLASH2_OK) return st;
+    cuuint64_t d[3] = {dims[0], dims[1], dims[2]};
+    cuuint64_t s[2] = {strides[0], strides[1]};
+    cuuint32_t b[3] = {box[0], box[1], box[2]};
+    cuuint32_t estr[3] = {1, 1, 1};
+    const CUtensorMapDataType type =
+        elem_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    CUresult r = g_encode(map, type, 3, const_cast<void *>(base), d, s, b, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          box[0] * elem_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                    : CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? DFLASH2_OK : DFLASH2_ERR_CUDA;
+}
+
 // Plain (unswizzled) byte rows: box of box_cols bytes (<= 256, a multiple
 // of 16) x box_rows rows.
 dflash2_status encode_tmap_bytes_2d(CUtensorMap *map, const void *base, uint64_t rows,
