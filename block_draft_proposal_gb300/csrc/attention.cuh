@@ -5,7 +5,7 @@
 // Rows.  The T tokens of a request and the G = q_heads / kv_heads query heads
 // of one key/value head are packed into T * G rows, row r = token r / G, head
 // r % G of the group, so that a pass over the keys serves them all; rows go in
-// blocks of `row_block`.  An item is one (request, key/value head, row block).
+// blocks of 2^row_shift.  An item is one (request, key/value head, row block).
 //
 // Split of the cache (paged mode).  Requests are ragged and few rows may face
 // many keys, so the keys are split by work, not by item: the items' key tiles
@@ -45,7 +45,7 @@ struct Params {
     float *lse;
     float *part;                   // paged: partial rows, kPartSlots(C) slots
     int32_t part_rows;             // rows of a slot
-    int32_t row_block;
+    int32_t row_shift;             // log2 of the rows of a block
     int32_t n_cta;                 // CTAs the work is split over
     int32_t *err;
 };
@@ -89,7 +89,8 @@ __device__ __forceinline__ Request load_request(const Params &p, int32_t b, bool
 }
 
 __device__ __forceinline__ int32_t row_blocks(const Params &p, const Request &r) {
-    return (int32_t)(((int64_t)r.t * p.group + p.row_block - 1) / p.row_block);
+    const uint32_t rows = (uint32_t)r.t * (uint32_t)p.group;  // below 2^31
+    return (int32_t)((rows + (1u << p.row_shift) - 1u) >> p.row_shift);
 }
 __device__ __forceinline__ int32_t key_tiles(const Request &r) {
     return max(1, (r.len + kKeyTile - 1) / kKeyTile);
@@ -118,8 +119,9 @@ __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t *red) {
     __syncthreads();
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
-    int64_t s = 0;
-    for (int w = 0; w < (int)blockDim.x / 32; ++w) s += red[w];
+    int64_t s = (threadIdx.x & 31) < blockDim.x / 32 ? red[threadIdx.x & 31] : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
     return s;
 }
 

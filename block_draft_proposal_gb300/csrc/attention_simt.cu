@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const Params p) {
          g += gridDim.y * (kThreads / 32)) {
         const int32_t h = g / p.group;
         const int64_t row = (int64_t)(tok - r.t0) * p.group + g % p.group;
-        const int32_t rb = (int32_t)(row / p.row_block), rr = (int32_t)(row % p.row_block);
+        const int32_t rb = (int32_t)(row >> p.row_shift), rr = (int32_t)(row & ((1 << p.row_shift) - 1));
         const int64_t u0 = before + ((int64_t)h * nrb + rb) * tiles;
         const int64_t n_cta = split_ctas(p, units);
         const int32_t c0 = cta_of(u0, units, n_cta), c1 = cta_of(u0 + tiles - 1, units, n_cta);
@@ -398,7 +398,7 @@ dflash2_status launch_one(Params p, bool vec_q, bool vec_k, cudaStream_t st) {
         cudaGetLastError();
         return DFLASH2_ERR_CUDA;
     }
-    p.row_block = kRows;
+    p.row_shift = kRows == 16 ? 4 : 6;
     dim3 grid((unsigned)p.n_cta);
     if (!kPaged)  // every row block of every request, and at most one short one each
         grid = dim3((unsigned)(((int64_t)p.total_q * p.group + kRows - 1) / kRows + p.batch),
@@ -451,7 +451,7 @@ dflash2_status launch_simt(const DeviceInfo &di, Params p, bool paged, int32_t d
             s = launch_typed<__nv_bfloat16, __nv_bfloat16, true>(p, vec_q, vec_k, st);
     }
     if (s != DFLASH2_OK || !paged) return s;
-    p.row_block = (int64_t)p.total_q * p.group <= 16ll * p.batch ? 16 : 64;
+    p.row_shift = (int64_t)p.total_q * p.group <= 16ll * p.batch ? 4 : 6;
     return launch_combine(di, p, dtype, st);
 }
 

@@ -23,21 +23,24 @@
 //               tiles in turn; their sums are joined at the end.
 //
 // Roles: warps 0-3 and 4-7 softmax of slots 0 and 1 (and the loads of Q and the
-// epilogue); warp 8 issues the MMAs; warp 9 the TMA loads (one box per
-// page and 64 columns); warps 10-11 guard the values (below); E4M3 adds warps
+// epilogue); warps 8 and 10 issue the MMAs of slots 0 and 1; warp 9 the TMA loads
+// (one box per page and 64 columns); warp 11 guards the values (below); E4M3 adds warps
 // 12-15, which widen codes to fp16 (exact) into the operand ring.
 //
 // What a row does not see must not reach it, but a product 0 * NaN would.  In the
-// key tiles that hold masked positions the guard warps zero the rows past the
+// key tiles that hold masked positions the guard warp zeroes the rows past the
 // end and every value that is not finite, and note that they found one; the
 // epilogue then adds such values to the rows that do see them.
 //
-// E4M3.  S = q' k' with q' = q 2^-a in fp16 (a per row, so that |q'| < 2^8: exact
-// for values within 2^-22 of the row's largest) and k' the codes, which fp16
-// holds; z = S 2^ke 2^a scale log2(e).  A value row's scale goes into its weight:
-// P = 2^(z - base) 2^ve 2^-x, where the row's integer x follows the largest
-// 2^(z - base) 2^ve as lazily as base follows z, so that weights fit fp16
-// whatever the scales are.  Both factors are powers of two: the sum of the weights
+// E4M3.  Codes are widened to fp16, which holds them; a row's scale goes in as far
+// as fp16 is exact: a key or value row becomes code * 2^d, d = 7 for the tile's
+// largest scale.  q' = q 2^-a in fp16 (a per row, so that |q'| < 2^8: exact for
+// values within 2^-22 of the row's largest); z = S 2^(tile) 2^a scale log2(e).  The
+// value operand's exponent goes into the weights: P = 2^(z - base) 2^(tile - x),
+// where the row's integer x follows the largest 2^(z - base) 2^(value scale) as
+// lazily as base follows z, so that weights fit fp16 whatever the scales are (a
+// tile whose value scales span more than fp16 holds exactly has them applied to
+// its weights key by key).  All of these are powers of two: the sum of the weights
 // does not depend on the values.
 #include <type_traits>
 
@@ -48,18 +51,28 @@ namespace attn {
 namespace {
 
 constexpr int kTile = 128;       // keys per tile, rows per slot
-constexpr int kRowBlock = 256;
+constexpr int kRowShift = 8, kRowBlock = 1 << kRowShift;
 constexpr float kLazy = 8.0f;    // log2 growth of the maximum that forces a rescale
-constexpr int kTopE4M3 = 6;      // fp16 weights: the largest starts in [2^6, 2^7) ...
-constexpr int kCapE4M3 = 14;     // ... and x moves once one reaches 2^14 or more
+constexpr int kTopE4M3 = 6;      // fp16 weights: the largest starts below 2^7 ...
+constexpr int kCapE4M3 = 14;     // ... and x moves before one reaches 2^15
 constexpr int kNoShift = -1000;  // no weight yet
 
 // Barriers and small state, behind the operand rings in dynamic shared memory.
+struct TileScale {
+    float key;      // E4M3: what a key tile's scores are multiplied by
+    int32_t value;  // binary exponent of its value operand
+    int32_t wide;   // bare value codes: scales per key
+};
+struct Piece;
+constexpr int kPieces = 4;
+constexpr int kPieceBytes = 64;
 struct Shared {
+    alignas(16) uint8_t piece[kPieces][kPieceBytes];
+    uint64_t piece_full[kPieces], piece_empty[kPieces];
     uint64_t full[8], empty[8];  // operand ring (E4M3: filled by the widening warps)
-    uint64_t guard_go, guard_done;  // a value tile handed to the guard warps and back
-    uint64_t s_full[2], p_full[2], o_full[2];
-    uint64_t q_full, drain;
+    uint64_t guard_go[8], guard_done[8];  // value tiles handed to the guard warp and back, in order
+    uint64_t s_full[2], p_full[2][2], o_full[2];  // weights come in halves of 64 keys
+    uint64_t q_full, drain[2];
     uint32_t tmem;
     int abort_flag;
     int poison;                  // number of the last piece with a value not finite
@@ -68,10 +81,11 @@ struct Shared {
 struct SharedE4M3 : Shared {
     uint64_t raw_full[6], raw_empty[6];      // code ring
     uint64_t sc_full[4];                     // scales of a key tile
+    TileScale scale[4];
+    int reduce[2][4][3];
     float qmul[2][kRowBlock];                // 2^a scale log2(e) of a row, by piece parity
+    int8_t vexp[4][kTile];                   // value exponents of 4 tiles
     alignas(16) uint8_t exps[6][2][kTile];   // exponent bytes as copied, by the keys' code-ring slot
-    alignas(16) float kmul[4][kTile];        // 2^ke of a key, 4 tiles
-    alignas(16) float vmul[4][kTile];        // 2^ve
 };
 
 template <int kD, bool kE4M3> struct Cfg {
@@ -122,16 +136,28 @@ __host__ __device__ constexpr uint32_t idesc16(bool f16, int n, bool b_mn) {
     return (1u << 4) | ((f16 ? 0u : 1u) << 7) | ((f16 ? 0u : 1u) << 10) | ((b_mn ? 1u : 0u) << 16) |
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
-// B operand [keys x kD], kD contiguous, 128-byte swizzle: column blocks of 64
-// are 128 keys x 128 bytes apart, groups of 8 keys 1024 bytes.
-__device__ __forceinline__ uint64_t mn_desc(uint32_t smem_addr) {
-    uint64_t d = 0;
-    d |= (uint64_t)((smem_addr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)((kTile * 128) >> 4) << 16;  // leading offset: next 64 columns
-    d |= (uint64_t)(1024 >> 4) << 32;           // stride offset: next 8 keys
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
+// Shared-memory matrix descriptors with 128-byte swizzle: the low word holds the
+// start address (and the leading offset), the high word is a constant.
+//   K-major (Q, K): 8-row groups 1024 bytes apart.
+//   MN-major (V [keys x kD], kD contiguous): column blocks of 64 are 128 keys x
+//   128 bytes apart (leading offset), groups of 8 keys 1024 bytes.
+constexpr uint32_t kKMajorHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kKMajorLo = 1u << 16;  // leading offset, unused with a swizzle
+constexpr uint32_t kMnMajorHi = kKMajorHi;
+constexpr uint32_t kMnMajorLo = (uint32_t)((kTile * 128) >> 4) << 16;
+__device__ __forceinline__ uint32_t desc_lo(uint32_t smem_addr) { return (smem_addr & 0x3FFFFu) >> 4; }
+__device__ __forceinline__ uint64_t desc64(uint32_t lo, uint32_t hi) {
+    return ((uint64_t)hi << 32) | lo;
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok));
+    return ok != 0;
 }
 
 // 32 TMEM columns of this warp's lanes; the registers are valid after
@@ -177,8 +203,63 @@ template <int kN> __device__ __forceinline__ void regs_give() {
 template <int kN> __device__ __forceinline__ void regs_take() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kN));
 }
+// mbar_wait (common.cuh) with the SM's clock for the limit: short inline code (the
+// kernel waits in some thirty places, and its roles share the instruction
+// cache), and no read of the slow global timer on the way into a wait.
+constexpr long long kWaitLimitCycles = 2000000000ll;  // about a second
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
+                                         int32_t *err) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity)) {
+        if (*abort_flag) return false;
+        if (clock64() - t0 > kWaitLimitCycles) {
+            *abort_flag = 1;
+            if (err) atomicOr(err, DFLASH2_DEVERR_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+
+// 2^e for integers e, clamped to normal numbers.
+__device__ __forceinline__ float pow2_int(int e) {
+    return __uint_as_float((uint32_t)(min(max(e, -126), 127) + 127) << 23);
+}
+
 template <int kId, int kCount> __device__ __forceinline__ void named_sync() {
     asm volatile("bar.sync %0, %1;" ::"n"(kId), "n"(kCount) : "memory");
+}
+
+// Two fp32 at a time (one issue slot).
+__device__ __forceinline__ uint64_t f2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2(uint32_t lo, uint32_t hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ __forceinline__ void unf2(uint64_t v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 template <bool kF16> __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
@@ -192,22 +273,21 @@ template <bool kF16> __device__ __forceinline__ uint32_t pack16(float lo, float 
 }
 
 // ---- pieces --------------------------------------------------------------------
-// The key tiles [t0, t1) of one item.
-struct Piece {
+// The key tiles [t0, t1) of one item, as the producer warp hands it to the other
+// roles through a ring in shared memory.
+struct alignas(16) Piece {
     Request rq;
     int32_t b, h;
-    int32_t row0, n_rows;  // first row of the block, live rows
-    int32_t t0, t1;        // key tiles
-    int32_t t1a;           // shared: the end of slot 0's tiles (prompt rows see fewer)
-    int32_t guard_from;    // first tile with positions some row does not see
-    bool shared;
-    int64_t slot;          // workspace slot, or -1: the whole item
+    int32_t row0, n_rows;   // first row of the block, live rows (0: no more pieces)
+    int32_t t0, t1;         // key tiles
+    int32_t t1a;            // shared: the end of slot 0's tiles (prompt rows see fewer)
+    int32_t guard_from;     // first tile with positions some row does not see
+    int32_t slot;           // workspace slot, or -1: the whole item
+    int32_t tok0, rem0;     // row0 / group, row0 % group
+    int32_t pad;
+    __device__ __forceinline__ bool shared() const { return n_rows > kTile; }
 };
-
-__device__ __forceinline__ void finish_piece(const Params &p, Piece *pc, int32_t first_masked) {
-    pc->shared = pc->n_rows > kTile;
-    pc->guard_from = first_masked / kTile;  // tile [128 g, 128 g + 128) reaches past first_masked - 1
-}
+static_assert(sizeof(Piece) <= kPieceBytes, "piece");
 
 // Paged: walks CTA blockIdx.x's range of units.
 struct Walk {
@@ -223,8 +303,9 @@ struct Walk {
             n = request_units(p, rq);
         }
     }
-    __device__ __forceinline__ bool next(const Params &p, Piece *pc) {
-        if (u >= end) return false;
+    __device__ __forceinline__ void next(const Params &p, Piece *pc) {
+        pc->n_rows = 0;
+        if (u >= end) return;
         while (u >= before + n) {
             bool bad;
             before += n;
@@ -232,20 +313,105 @@ struct Walk {
             rq = load_request<true>(p, b, &bad);
             n = request_units(p, rq);
         }
-        const int32_t tiles = key_tiles(rq), nrb = row_blocks(p, rq);
-        const int64_t item = (u - before) / tiles;
-        pc->t0 = (int32_t)((u - before) % tiles);
+        const uint32_t tiles = key_tiles(rq), nrb = row_blocks(p, rq);
+        uint32_t item;
+        if (n < (1ll << 31)) {
+            const uint32_t off = (uint32_t)(u - before);
+            item = off / tiles;
+            pc->t0 = (int32_t)(off - item * tiles);
+        } else {
+            const int64_t off = u - before;
+            item = (uint32_t)(off / tiles);  // kv_heads * row blocks: below 2^31
+            pc->t0 = (int32_t)(off - (int64_t)item * tiles);
+        }
         pc->t1 = (int32_t)min((int64_t)tiles, pc->t0 + (end - u));
         pc->t1a = pc->t1;
         pc->rq = rq;
         pc->b = b;
         pc->h = (int32_t)(item / nrb);
-        pc->row0 = (int32_t)(item % nrb) * kRowBlock;
+        pc->row0 = (int32_t)(item - (uint32_t)pc->h * nrb) * kRowBlock;
         pc->n_rows = min(kRowBlock, rq.t * p.group - pc->row0);
-        pc->slot = pc->t0 == 0 && pc->t1 == tiles ? -1 : 2 * (int64_t)blockIdx.x + (pc->t0 == 0);
-        finish_piece(p, pc, rq.ctx);
+        pc->slot = pc->t0 == 0 && pc->t1 == (int32_t)tiles ? -1 : 2 * (int32_t)blockIdx.x + (pc->t0 == 0);
+        pc->guard_from = rq.ctx / kTile;
         u += pc->t1 - pc->t0;
-        return true;
+    }
+};
+
+// Prompts: row blocks with the most keys first.  Level j holds block j of every
+// request that has one; the items are numbered level by level from the highest
+// down, request by request, head by head, and CTA c takes number c of the first
+// n_cta items, number n_cta - 1 - c of the next, and so on in turns, which evens the
+// CTAs' key tiles out.  A warp walks; lane i looks at request 32 k + i.
+struct Levels {
+    int32_t round, level, above, total;  // row blocks in levels > `level`; blocks in all
+    __device__ __forceinline__ int32_t blocks_of(const Params &p, int32_t b, Request *r) const {
+        bool bad;
+        *r = load_request<false>(p, b, &bad);
+        return row_blocks(p, *r);
+    }
+    __device__ __forceinline__ int32_t in_level(const Params &p, int lane) const {
+        int32_t n = 0;
+        Request r;
+        for (int b0 = 0; b0 < p.batch; b0 += 32)
+            n += __popc(__ballot_sync(0xFFFFFFFFu,
+                                      b0 + lane < p.batch && blocks_of(p, b0 + lane, &r) > level));
+        return n;
+    }
+    __device__ __forceinline__ void begin(const Params &p, int lane, bool *bad) {
+        int32_t most = 0, sum = 0;
+        for (int b = lane; b < p.batch; b += 32) {
+            bool bd;
+            const Request r = load_request<false>(p, b, &bd);
+            *bad |= bd;
+            const int32_t n = row_blocks(p, r);
+            most = max(most, n);
+            sum += n;
+        }
+        most = __reduce_max_sync(0xFFFFFFFFu, most);
+        total = __reduce_add_sync(0xFFFFFFFFu, sum);
+        level = most - 1;
+        above = 0;
+        round = 0;
+    }
+    __device__ __forceinline__ void next(const Params &p, int lane, Piece *pc) {
+        pc->n_rows = 0;
+        const int32_t n_cta = (int32_t)gridDim.x;
+        const int32_t c = (round & 1) ? n_cta - 1 - (int32_t)blockIdx.x : (int32_t)blockIdx.x;
+        const int64_t item = (int64_t)round * n_cta + c;
+        ++round;
+        if (item >= (int64_t)total * p.kv_heads) return;
+        const int32_t q = (int32_t)(item / p.kv_heads);
+        int32_t here = in_level(p, lane);
+        while (q >= above + here) {
+            above += here;
+            --level;
+            here = in_level(p, lane);
+        }
+        int32_t k = q - above;  // the k-th request of the level
+        for (int b0 = 0; b0 < p.batch; b0 += 32) {
+            Request r{};
+            const bool has = b0 + lane < p.batch && blocks_of(p, b0 + lane, &r) > level;
+            const uint32_t m = __ballot_sync(0xFFFFFFFFu, has);
+            if (k >= __popc(m)) {
+                k -= __popc(m);
+                continue;
+            }
+            const int src = __fns(m, 0, k + 1);
+            pc->rq.t0 = __shfl_sync(0xFFFFFFFFu, r.t0, src);
+            pc->rq.t = __shfl_sync(0xFFFFFFFFu, r.t, src);
+            pc->b = b0 + src;
+            break;
+        }
+        pc->rq.len = pc->rq.t;
+        pc->rq.ctx = 0;
+        pc->h = (int32_t)(item - (int64_t)q * p.kv_heads);
+        pc->row0 = level * kRowBlock;
+        pc->n_rows = min(kRowBlock, pc->rq.t * p.group - pc->row0);
+        pc->t0 = 0;
+        pc->t1 = ((pc->row0 + pc->n_rows - 1) / p.group) / kTile + 1;
+        pc->t1a = ((pc->row0 + min(pc->n_rows, kTile) - 1) / p.group) / kTile + 1;
+        pc->guard_from = (pc->row0 / p.group) / kTile;
+        pc->slot = -1;
     }
 };
 
@@ -284,7 +450,7 @@ __device__ __forceinline__ void seen_bits(const Params &p, const Request &rq, in
 
 // Values of the keys [l0, l1) that token i of the request sees and that are not
 // finite, added to columns [col, col + cols) of a row as it was written (a
-// partial row of fp32 sums, or the output row): what the guard warps took out.
+// partial row of fp32 sums, or the output row): what the guard warp took out.
 // Rare, so one thread per row.
 template <int kD, bool kE4M3, bool kPaged>
 __device__ __noinline__ void add_poison(const Params &p, Request rq, int32_t b, int32_t h, int32_t i,
@@ -333,27 +499,34 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&sh.full[i], kE4M3 ? 128 : 1);
-            mbar_init(&sh.empty[i], 1);
+            mbar_init(&sh.full[i], kE4M3 ? 4 : 1);
+            mbar_init(&sh.empty[i], 2);
         }
         if constexpr (kE4M3) {
             for (int i = 0; i < kRaw; ++i) {
                 mbar_init(&sh.raw_full[i], 1);
-                mbar_init(&sh.raw_empty[i], 128);
+                mbar_init(&sh.raw_empty[i], 4);
             }
-            for (int i = 0; i < 4; ++i) mbar_init(&sh.sc_full[i], 128);
+            for (int i = 0; i < 4; ++i) mbar_init(&sh.sc_full[i], 1);
         }
-        mbar_init(&sh.guard_go, 1);
-        mbar_init(&sh.guard_done, 64);
+        for (int i = 0; i < 8; ++i) {
+            mbar_init(&sh.guard_go[i], 1);
+            mbar_init(&sh.guard_done[i], 1);
+        }
+        for (int i = 0; i < kPieces; ++i) {
+            mbar_init(&sh.piece_full[i], 1);
+            mbar_init(&sh.piece_empty[i], kE4M3 ? 14 : 11);  // issuers, softmax warps, widening or guard
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.p_full[i], 128);
+            mbar_init(&sh.p_full[i][0], 4);
+            mbar_init(&sh.p_full[i][1], 4);
             mbar_init(&sh.o_full[i], 1);
+            mbar_init(&sh.drain[i], 1);
         }
-        mbar_init(&sh.q_full, 256);
-        mbar_init(&sh.drain, 1);
+        mbar_init(&sh.q_full, 8);
         sh.abort_flag = 0;
-        sh.poison = 0;
+        sh.poison = -1;
         fence_mbar_init();
     }
     if (warp == 8) {
@@ -367,377 +540,393 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
     grid_dep_wait();
     grid_dep_launch();
 
-    // ---- what this CTA does ----
     bool bad = false;
     Start start{};
-    Piece only{};
-    bool have = false;
     if constexpr (kPaged) {
         start = find_start(p, &sh.start, &bad);
-    } else {
-        // CTA (x, h): row block number `want` of all requests, the last ones first
-        int64_t want = (int64_t)gridDim.x - 1 - blockIdx.x;
-        for (int b0 = 0; b0 < p.batch; b0 += blockDim.x) {
-            const int b = b0 + threadIdx.x;
-            Request r{};
-            bool bd = false;
-            if (b < p.batch) r = load_request<false>(p, b, &bd);
-            bad |= bd;
-            const int64_t n = b < p.batch ? row_blocks(p, r) : 0;
-            const int64_t total = block_sum(n, sh.start.red);
-            if (want >= total) {
-                want -= total;
-                continue;
-            }
-            for (int i = b0; i < min(p.batch, b0 + (int)blockDim.x); ++i) {
-                r = load_request<false>(p, i, &bd);
-                const int32_t nb = row_blocks(p, r);
-                if (want < nb) {
-                    only.rq = r;
-                    only.b = i;
-                    only.h = blockIdx.y;
-                    only.row0 = (int32_t)want * kRowBlock;
-                    only.n_rows = (int32_t)min((int64_t)kRowBlock, (int64_t)r.t * p.group - only.row0);
-                    const int32_t last = (only.row0 + only.n_rows - 1) / p.group;
-                    const int32_t last0 = (only.row0 + min(only.n_rows, kTile) - 1) / p.group;
-                    only.t0 = 0;
-                    only.t1 = last / kTile + 1;
-                    only.t1a = last0 / kTile + 1;
-                    only.slot = -1;
-                    finish_piece(p, &only, only.row0 / p.group);
-                    have = true;
-                    break;
-                }
-                want -= nb;
-            }
-            break;
-        }
+        if (bad && p.err && blockIdx.x == 0) atomicOr(p.err, DFLASH2_DEVERR_ID_RANGE);
     }
-    if (bad && p.err && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(p.err, DFLASH2_DEVERR_ID_RANGE);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sh.tmem;
+    // the CTA holds all 512 TMEM columns: S of slot s at 128 s, O at 256 + kD s
     volatile int *abort_flag = &sh.abort_flag;
-
-    Walk walk{};
-    if constexpr (kPaged) walk.begin(p, start);
-    auto next_piece = [&](Piece *pc) -> bool {
-        if constexpr (kPaged) return walk.next(p, pc);
-        if (!have) return false;
-        *pc = only;
-        have = false;
-        return true;
+    // Piece number i of the ring, for every role but the producer's; all lanes of a
+    // warp (`whole`) or one thread.  Returns false at the end or on an abort.
+    auto take_piece = [&](uint32_t i, Piece *pc, bool whole) {
+        if (!bar_wait(&sh.piece_full[i % kPieces], (i / kPieces) & 1u, abort_flag, p.err)) return false;
+        *pc = *reinterpret_cast<const Piece *>(sh.piece[i % kPieces]);
+        if (whole) __syncwarp();
+        if (!whole || lane == 0) mbar_arrive(&sh.piece_empty[i % kPieces]);
+        return pc->n_rows > 0;
     };
-    Piece pc{};
+
     if (warp >= 8 && warp < 12) {
         regs_give<C::kRegsFew>();
         if (warp == 9) {
-        // ---- TMA producer ----
-        uint32_t pos = 0;  // operand tiles issued
-        bool ok = true;
-        const int32_t rows_box = kPaged ? min(p.page_size, kTile) : kTile;
-        const int32_t n_box = kTile / rows_box;
-        const int32_t per_page = kPaged ? max(1, p.page_size / kTile) : 1;  // tiles per page
-        bool bad_page = false;
-        auto full_bar = [&](uint32_t s) -> uint64_t * {
-            if constexpr (kE4M3)
-                return &sh.raw_full[s];
-            else
-                return &sh.full[s];
-        };
-        auto load = [&](int32_t tile, bool values) {
+            // ---- producer: the pieces, and the TMA copies by one thread ----
             constexpr uint32_t kSlots = kE4M3 ? kRaw : kStages;
-            const uint32_t s = pos % kSlots, ph = (pos / kSlots) & 1u;
-            uint64_t *fullb = full_bar(s), *emptyb;
-            if constexpr (kE4M3)
-                emptyb = &sh.raw_empty[s];
-            else
-                emptyb = &sh.empty[s];
-            int32_t z = -1, y = 0, pg = 0;
-            const int32_t l = tile * kTile + lane * rows_box;
-            if constexpr (kPaged) {
-                if (lane < n_box && l < pc.rq.len) {
-                    pg = __ldg(p.page_table + (int64_t)pc.b * p.max_pages + l / p.page_size);
-                    if (pg < 0 || pg >= p.num_pages) {
-                        bad_page = true;
-                        pg = 0;
-                    } else {
-                        z = pg * p.kv_heads + pc.h;
-                    }
-                }
-                y = per_page > 1 ? (tile % per_page) * kTile : 0;
-            }
-            if (!mbar_wait(emptyb, ph ^ 1u, abort_flag, p.err)) return false;
-            constexpr uint32_t kBytes = kE4M3 ? C::kRawBytes : C::kTileBytes;
-            const bool with_exps = kE4M3 && !values;
-            if (lane == 0) mbar_arrive_expect_tx(fullb, kBytes + (with_exps ? 2 * kTile : 0));
-            __syncwarp();
-            const CUtensorMap *map = values ? &vmap : &kmap;
-            const int box = lane % n_box, half = lane / n_box;
-            const int32_t zz = __shfl_sync(0xFFFFFFFFu, z, box);
-            if constexpr (kE4M3) {
-                if (lane < n_box) {
-                    tma_load_3d(sm_raw + s * C::kRawBytes + lane * rows_box * kD, map, fullb, 0, y, z);
-                    if (with_exps) {  // of page 0 where there is no page: any scale serves zero rows
-                        const int64_t at = ((int64_t)pg * p.kv_heads + pc.h) * p.page_size + y;
-                        bulk_load(smem_u32(&sh.exps[s][0][lane * rows_box]), p.k_exp + at, rows_box, fullb);
-                        bulk_load(smem_u32(&sh.exps[s][1][lane * rows_box]), p.v_exp + at, rows_box, fullb);
-                    }
-                }
-            } else if (lane < n_box * C::kHalves) {
-                const uint32_t dst = sm_ring + s * C::kTileBytes + half * (kTile * 128) + box * rows_box * 128;
-                if constexpr (kPaged)
-                    tma_load_3d(dst, map, fullb, 64 * half, y, zz);
+            constexpr int kMaxBox = kPaged ? kTile / 16 : 1;
+            uint32_t pos = 0, n_piece = 0;  // operand tiles issued
+            bool ok = true, bad_page = false;
+            const int32_t rows_box = kPaged ? min(p.page_size, kTile) : kTile;
+            const int32_t n_box = kTile / rows_box;
+            const int32_t shift = kPaged ? 31 - __clz(p.page_size) : 0;
+            Piece pc{};
+            auto full_bar = [&](uint32_t s) -> uint64_t * {
+                if constexpr (kE4M3)
+                    return &sh.raw_full[s];
                 else
-                    tma_load_3d(dst, map, fullb, 64 * half, pc.h, pc.rq.t0 + tile * kTile);
+                    return &sh.full[s];
+            };
+            auto empty_bar = [&](uint32_t s) -> uint64_t * {
+                if constexpr (kE4M3)
+                    return &sh.raw_empty[s];
+                else
+                    return &sh.empty[s];
+            };
+            // pages of a key tile's boxes (-1: past the end, a box of zeros)
+            struct Pages {
+                int32_t id[kMaxBox];
+            };
+            auto pages_of = [&](int32_t tile) {
+                Pages g;
+#pragma unroll
+                for (int i = 0; i < kMaxBox; ++i) {
+                    const int32_t l = tile * kTile + i * rows_box;
+                    g.id[i] = -1;
+                    if (kPaged && i < n_box && tile < pc.t1 && l < pc.rq.len)
+                        g.id[i] = __ldg(p.page_table + (int64_t)pc.b * p.max_pages + (l >> shift));
+                }
+                return g;
+            };
+            auto load = [&](int32_t tile, const Pages &g, bool values) {
+                const uint32_t s = pos % kSlots, ph = (pos / kSlots) & 1u;
+                uint64_t *fullb = full_bar(s);
+                if (!bar_wait(empty_bar(s), ph ^ 1u, abort_flag, p.err)) return false;
+                constexpr uint32_t kBytes = kE4M3 ? C::kRawBytes : C::kTileBytes;
+                const bool with_exps = kE4M3 && !values;
+                mbar_arrive_expect_tx(fullb, kBytes + (with_exps ? 2 * kTile : 0));
+                const CUtensorMap *map = values ? &vmap : &kmap;
+                if constexpr (!kPaged) {
+#pragma unroll
+                    for (int half = 0; half < C::kHalves; ++half)
+                        tma_load_3d(sm_ring + s * C::kTileBytes + half * (kTile * 128), map, fullb, 64 * half,
+                                    pc.h, pc.rq.t0 + tile * kTile);
+                } else {
+                    const int32_t y = (tile * kTile) & (p.page_size - 1) & ~(kTile - 1);
+#pragma unroll
+                    for (int i = 0; i < kMaxBox; ++i) {
+                        if (i >= n_box) break;
+                        const bool live = tile * kTile + i * rows_box < pc.rq.len;
+                        const bool good = (uint32_t)g.id[i] < (uint32_t)p.num_pages;
+                        if (live && !good) bad_page = true;
+                        const int32_t z = good ? g.id[i] * p.kv_heads + pc.h : -1;
+                        if constexpr (kE4M3) {
+                            tma_load_3d(sm_raw + s * C::kRawBytes + i * rows_box * kD, map, fullb, 0, y, z);
+                            if (with_exps) {  // page 0's where there is none: any scale serves zero rows
+                                const int64_t at =
+                                    ((int64_t)(good ? g.id[i] : 0) * p.kv_heads + pc.h) * p.page_size + y;
+                                bulk_load(smem_u32(&sh.exps[s][0][i * rows_box]), p.k_exp + at, rows_box, fullb);
+                                bulk_load(smem_u32(&sh.exps[s][1][i * rows_box]), p.v_exp + at, rows_box, fullb);
+                            }
+                        } else {
+                            const uint32_t dst = sm_ring + s * C::kTileBytes + i * rows_box * 128;
+#pragma unroll
+                            for (int half = 0; half < C::kHalves; ++half)
+                                tma_load_3d(dst + half * (kTile * 128), map, fullb, 64 * half, y, z);
+                        }
+                    }
+                }
+                ++pos;
+                return true;
+            };
+            Walk walk{};
+            Levels levels{};
+            if constexpr (kPaged)
+                walk.begin(p, start);
+            else
+                levels.begin(p, lane, &bad);
+            for (;;) {
+                if constexpr (kPaged)
+                    walk.next(p, &pc);
+                else
+                    levels.next(p, lane, &pc);
+                pc.tok0 = pc.row0 / p.group;
+                pc.rem0 = pc.row0 - pc.tok0 * p.group;
+                if (elect_one()) {
+                    ok = bar_wait(&sh.piece_empty[n_piece % kPieces], ((n_piece / kPieces) & 1u) ^ 1u,
+                                  abort_flag, p.err);
+                    if (ok) {
+                        *reinterpret_cast<Piece *>(sh.piece[n_piece % kPieces]) = pc;
+                        mbar_arrive(&sh.piece_full[n_piece % kPieces]);
+                    }
+                    if (ok && pc.n_rows > 0) {
+                        // shared K0 V0 K1 V1 ..., alternate K0 K1 V0 K2 V1 ... V(n-2) V(n-1);
+                        // page numbers are fetched a tile ahead of their copies
+                        const int32_t n = pc.t1 - pc.t0, lead = pc.shared() ? 0 : 1;
+                        Pages key = pages_of(pc.t0), value = key, value_next = key;
+                        int32_t jk = 0, jv = 0;
+#pragma unroll 1
+                        for (int32_t i = 0; ok && i < 2 * n; ++i) {
+                            const bool values = jk == n || jk - jv > lead;
+                            Pages g;
+#pragma unroll
+                            for (int k = 0; k < kMaxBox; ++k) g.id[k] = values ? value.id[k] : key.id[k];
+                            ok = load(pc.t0 + (values ? jv : jk), g, values);
+                            if (values) {
+                                value = value_next;
+                                ++jv;
+                            } else {
+                                if (jk == jv) value = key;
+                                value_next = key;
+                                key = pages_of(pc.t0 + ++jk);
+                            }
+                        }
+                    }
+                }
+                ++n_piece;
+                if (__any_sync(0xFFFFFFFFu, !ok) || pc.n_rows == 0) break;
             }
-            __syncwarp();
-            ++pos;
-            return true;
-        };
-        while (ok && next_piece(&pc)) {
-            if (pc.shared) {
-                for (int32_t t = pc.t0; ok && t < pc.t1; ++t) ok = load(t, false) && load(t, true);
-            } else {
-                ok = load(pc.t0, false);
-                for (int32_t t = pc.t0; ok && t < pc.t1; ++t)
-                    ok = (t + 1 >= pc.t1 || load(t + 1, false)) && load(t, true);
+            if ((bad_page || (!kPaged && bad && blockIdx.x == 0)) && p.err)
+                atomicOr(p.err, DFLASH2_DEVERR_ID_RANGE);
+            if (!ok) {  // wait for the copies in flight before the shared memory goes
+                for (uint32_t n = pos > kSlots ? pos - kSlots : 0; n < pos; ++n) {
+                    const uint64_t t0 = global_timer_ns();
+                    while (!mbar_try_wait(full_bar(n % kSlots), (n / kSlots) & 1u))
+                        if (global_timer_ns() - t0 > kWaitLimitNs) break;
+                }
             }
-        }
-        if (bad_page && p.err) atomicOr(p.err, DFLASH2_DEVERR_ID_RANGE);
-        if (!ok) {  // wait for the copies in flight before the shared memory goes
-            constexpr uint32_t kSlots = kE4M3 ? kRaw : kStages;
-            for (uint32_t n = pos > kSlots ? pos - kSlots : 0; n < pos; ++n) {
-                uint64_t *fullb = full_bar(n % kSlots);
+        } else if (warp == 8 || warp == 10) {
+            // ---- MMA issuer of slot s: one thread ----
+            // Each slot has its own issuer: an MMA costs the issuing thread about as
+            // long as the tensor core takes for it.  Both walk every operand of the
+            // ring in order and hand it back (an operand is free when both have).
+            if (elect_one()) {
+                const int s = warp == 8 ? 0 : 1;
+                constexpr uint32_t kIdS = idesc16(kE4M3, kTile, false);
+                constexpr uint32_t kIdO = idesc16(kE4M3, kD, true);
+                const uint32_t dS = s * kTile, dO = 256 + s * kD;
+                uint32_t pos = 0, n_piece = 0, n_guard = 0, n_p = 0;
+                bool ok = true;
+                Piece pc{};
+                auto wait_ring = [&](uint32_t n) {
+                    return bar_wait(&sh.full[n % kStages], (n / kStages) & 1u, abort_flag, p.err);
+                };
+                // scores of key operand n (mine), or the other slot's operand handed back
+                auto keys = [&](uint32_t n, bool mine, bool q1) {
+                    if (!wait_ring(n)) return false;
+                    if (!mine) {
+                        mbar_arrive(&sh.empty[n % kStages]);
+                        return true;
+                    }
+                    const uint32_t kd = desc_lo(sm_ring + (n % kStages) * C::kTileBytes) | kKMajorLo;
+                    const uint32_t qd = desc_lo(sm_q + (q1 ? C::kTileBytes : 0)) | kKMajorLo;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < kD / 16; ++k) {
+                        const uint32_t off = (k >> 2) * ((kTile * 128) >> 4) + (k & 3) * 2;
+                        tc_mma_bf16(dS, desc64(qd + off, kKMajorHi), desc64(kd + off, kKMajorHi), kIdS, k > 0);
+                    }
+                    tc_commit(&sh.s_full[s]);
+                    tc_commit(&sh.empty[n % kStages]);
+                    return true;
+                };
+                // sums over value operand n, of key tile t; issuer 0 hands guarded ones to
+                // the guard warp
+                auto values = [&](int32_t t, uint32_t n, bool mine, bool acc, bool last) {
+                    if (!wait_ring(n)) return false;
+                    if (!kE4M3 && t >= pc.guard_from) {
+                        if (s == 0) mbar_arrive(&sh.guard_go[n_guard & 7u]);
+                        if (mine &&
+                            !bar_wait(&sh.guard_done[n_guard & 7u], (n_guard >> 3) & 1u, abort_flag, p.err))
+                            return false;
+                        ++n_guard;
+                    }
+                    if (!mine) {
+                        mbar_arrive(&sh.empty[n % kStages]);
+                        return true;
+                    }
+                    const uint32_t vd = desc_lo(sm_ring + (n % kStages) * C::kTileBytes) | kMnMajorLo;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (!bar_wait(&sh.p_full[s][h], n_p & 1u, abort_flag, p.err)) return false;
+                        tc_fence_after();
+#pragma unroll
+                        for (int k = 4 * h; k < 4 * h + 4; ++k)
+                            tc_mma_ts(dO, dS + 8 * k, desc64(vd + k * (2048 >> 4), kMnMajorHi), kIdO,
+                                      acc || k > 0);
+                    }
+                    ++n_p;
+                    tc_commit(&sh.empty[n % kStages]);
+                    if (last) tc_commit(&sh.o_full[s]);
+                    return true;
+                };
+                while (ok && take_piece(n_piece, &pc, false)) {
+                    ok = bar_wait(&sh.q_full, n_piece & 1u, abort_flag, p.err);
+                    ++n_piece;
+                    const int32_t n = pc.t1 - pc.t0;
+                    // shared: K0 V0 K1 V1 ..., every tile mine (slot 0 of a prompt ends earlier)
+                    // alternate: K0 K1 V0 K2 V1 ... V(n-2) V(n-1), tile j mine if j % 2 == s
+                    const bool both = pc.shared();
+                    const int32_t n_mine = both && s == 0 ? pc.t1a - pc.t0 : n;
+                    for (int32_t j = both ? 0 : -1; ok && j < n; ++j) {
+                        // key j (shared) or j + 1 (alternate), then value j
+                        const int32_t jk = both ? j : j + 1;
+                        if (jk < n) {
+                            const uint32_t nk = pos + (both ? 2 * jk : jk == 0 ? 0 : 2 * jk - 1);
+                            // shared: S(j) follows V(j - 1), which the loop order gives
+                            ok = keys(nk, both ? jk < n_mine : (jk & 1) == s, both && s == 1);
+                        }
+                        if (ok && j >= 0) {
+                            const uint32_t nv = pos + (both ? 2 * j + 1 : j + 1 < n ? 2 * j + 2 : 2 * n - 1);
+                            const bool mine = both ? j < n_mine : (j & 1) == s;
+                            ok = values(pc.t0 + j, nv, mine, both ? j > 0 : j >= 2,
+                                        both ? j + 1 == n_mine : j + 2 >= n);
+                        }
+                    }
+                    pos += 2 * n;
+                }
+                // nothing of this slot's is in flight when the accumulators are freed
+                tc_commit(&sh.drain[s]);
                 const uint64_t t0 = global_timer_ns();
-                while (!mbar_try_wait(fullb, (n / kSlots) & 1u))
+                while (!mbar_try_wait(&sh.drain[s], 0))
                     if (global_timer_ns() - t0 > kWaitLimitNs) break;
             }
-        }
-    } else if (warp == 8) {
-        // ---- MMA issuer: lane 0 issues, the warp waits together ----
-        constexpr uint32_t kIdS = idesc16(kE4M3, kTile, false);
-        constexpr uint32_t kIdO = idesc16(kE4M3, kD, true);
-        uint32_t pos = 0, n_piece = 0, n_guard = 0;
-        uint32_t n_p[2] = {0, 0};
-        const uint64_t qd[2] = {sw128_desc(sm_q), sw128_desc(sm_q + C::kTileBytes)};
-        bool ok = true;
-        auto wait_ring = [&](uint32_t n) {
-            if (!mbar_wait(&sh.full[n % kStages], (n / kStages) & 1u, abort_flag, p.err)) return false;
-            tc_fence_after();
-            return true;
-        };
-        auto release = [&](uint32_t n) {
-            if (lane == 0) tc_commit(&sh.empty[n % kStages]);
-        };
-        auto mma_s = [&](int s, int q, uint32_t n) {
-            if (lane == 0) {
-                const uint64_t kd = sw128_desc(sm_ring + (n % kStages) * C::kTileBytes);
-#pragma unroll
-                for (int k = 0; k < kD / 16; ++k) {
-                    const uint32_t off = (k >> 2) * ((kTile * 128) >> 4) + (k & 3) * 2;
-                    tc_mma_bf16(tmem + s * kTile, qd[q] + off, kd + off, kIdS, k > 0);
-                }
-                tc_commit(&sh.s_full[s]);
-            }
-            __syncwarp();
-        };
-        auto mma_o = [&](int s, uint32_t n, bool acc) {
-            if (!mbar_wait(&sh.p_full[s], n_p[s] & 1u, abort_flag, p.err)) return false;
-            ++n_p[s];
-            tc_fence_after();
-            if (lane == 0) {
-                const uint64_t vd = mn_desc(sm_ring + (n % kStages) * C::kTileBytes);
-#pragma unroll
-                for (int k = 0; k < kTile / 16; ++k)
-                    tc_mma_ts(tmem + 256 + s * kD, tmem + s * kTile + 8 * k, vd + k * (2048 >> 4), kIdO,
-                              acc || k > 0);
-            }
-            __syncwarp();
-            return true;
-        };
-        auto wait_v = [&](int32_t t, uint32_t n) {
-            if (!wait_ring(n)) return false;
-            if (!kE4M3 && t >= pc.guard_from) {
-                if (lane == 0) mbar_arrive(&sh.guard_go);
-                __syncwarp();
-                if (!mbar_wait(&sh.guard_done, n_guard & 1u, abort_flag, p.err)) return false;
-                ++n_guard;
-            }
-            return true;
-        };
-        while (ok && next_piece(&pc)) {
-            ok = mbar_wait(&sh.q_full, n_piece & 1u, abort_flag, p.err);
-            ++n_piece;
-            tc_fence_after();
-            if (!ok) break;
-            if (pc.shared) {
-                ok = wait_ring(pos);
-                if (!ok) break;
-                mma_s(0, 0, pos);
-                mma_s(1, 1, pos);
-                release(pos);
-                for (int32_t t = pc.t0; ok && t < pc.t1; ++t) {
-                    const uint32_t nv = pos + 1, nk = pos + 2;
-                    const bool more = t + 1 < pc.t1;
-                    ok = wait_v(t, nv);
-                    if (!ok) break;
-                    if (t < pc.t1a) {
-                        ok = mma_o(0, nv, t > pc.t0);
-                        if (!ok) break;
-                    }
-                    if (more) {
-                        ok = wait_ring(nk);
-                        if (!ok) break;
-                    }
-                    if (t + 1 < pc.t1a)
-                        mma_s(0, 0, nk);
-                    else if (t + 1 == pc.t1a && lane == 0)
-                        tc_commit(&sh.o_full[0]);
-                    ok = mma_o(1, nv, t > pc.t0);
-                    if (!ok) break;
-                    release(nv);
-                    if (more) {
-                        mma_s(1, 1, nk);
-                        release(nk);
-                    } else if (lane == 0) {
-                        tc_commit(&sh.o_full[1]);
-                    }
-                    pos += 2;
-                }
-            } else {
-                // tiles in turn; operand order K0 K1 V0 K2 V1 ...
-                const int32_t n = pc.t1 - pc.t0;
-                for (int32_t j = 0; ok && j < min(n, 2); ++j) {
-                    ok = wait_ring(pos + j);
-                    if (!ok) break;
-                    mma_s(j, 0, pos + j);
-                    release(pos + j);
-                }
-                for (int32_t j = 0; ok && j < n; ++j) {
-                    // V(j) is operand 2 j + 2 of the piece, or the last one
-                    const uint32_t nv = pos + (j + 1 < n ? 2 * j + 2 : 2 * n - 1);
-                    const uint32_t nk = pos + 2 * j + 3;
-                    ok = wait_v(pc.t0 + j, nv) && mma_o(j & 1, nv, j >= 2);
-                    if (!ok) break;
-                    release(nv);
-                    if (j + 2 < n) {
-                        ok = wait_ring(nk);
-                        if (!ok) break;
-                        mma_s(j & 1, 0, nk);
-                        release(nk);
-                    } else if (lane == 0) {
-                        tc_commit(&sh.o_full[j & 1]);
-                    }
-                }
-                pos += 2 * n;
-            }
-        }
-        // nothing of this CTA's is in flight when the accumulators are freed
-        if (lane == 0) tc_commit(&sh.drain);
-        __syncwarp();
-        const uint64_t t0 = global_timer_ns();
-        while (!mbar_try_wait(&sh.drain, 0))
-            if (global_timer_ns() - t0 > kWaitLimitNs) break;
-    } else if (warp == 10 || warp == 11) {
-        // ---- guard: values of tiles with masked positions ----
-        if constexpr (!kE4M3) {
+        } else if constexpr (!kE4M3) {
+            // ---- guard: values of tiles with masked positions ----
             uint32_t pos = 0, n_piece = 0, n_guard = 0;
             bool ok = true;
-            const int tid = threadIdx.x - 320;
-            while (ok && next_piece(&pc)) {
-                ++n_piece;
+            Piece pc{};
+            while (ok && take_piece(n_piece, &pc, true)) {
                 const int32_t n = pc.t1 - pc.t0;
                 for (int32_t j = max(0, pc.guard_from - pc.t0); ok && j < n; ++j) {
-                    const uint32_t nv = pos + (pc.shared ? 2 * j + 1 : j + 1 < n ? 2 * j + 2 : 2 * n - 1);
-                    ok = mbar_wait(&sh.guard_go, n_guard & 1u, abort_flag, p.err);
+                    const uint32_t nv = pos + (pc.shared() ? 2 * j + 1 : j + 1 < n ? 2 * j + 2 : 2 * n - 1);
+                    ok = bar_wait(&sh.guard_go[n_guard & 7u], (n_guard >> 3) & 1u, abort_flag, p.err);
                     if (!ok) break;
-                    ++n_guard;
                     const uint32_t base = sm_ring + (nv % kStages) * C::kTileBytes;
                     const int32_t live = pc.rq.len - (pc.t0 + j) * kTile;  // rows of the tile that are keys
                     bool found = false;
-                    for (int i = tid; i < C::kTileBytes / 16; i += 64) {
+#pragma unroll 4
+                    for (int i = lane; i < C::kTileBytes / 16; i += 32) {
                         const uint32_t addr = base + i * 16;
                         uint32_t w[4];
                         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                                      : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                                      : "r"(addr));
-                        bool change = false;
-                        if (((i >> 3) & (kTile - 1)) >= live) {
-                            change = true;
-                            w[0] = w[1] = w[2] = w[3] = 0u;
-                        } else {
+                        const bool dead = ((i >> 3) & (kTile - 1)) >= live;
+                        // a 16-bit exponent of all ones: adding 1 to it carries into the sign's place
+                        uint32_t odd = 0;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) odd |= ((w[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+                        if (dead || odd) {
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
-                                if ((w[k] & 0x7F80u) == 0x7F80u) w[k] &= 0xFFFF0000u, change = found = true;
-                                if ((w[k] & 0x7F800000u) == 0x7F800000u) w[k] &= 0xFFFFu, change = found = true;
+                                if (dead || (w[k] & 0x7F80u) == 0x7F80u) w[k] &= 0xFFFF0000u;
+                                if (dead || (w[k] & 0x7F800000u) == 0x7F800000u) w[k] &= 0xFFFFu;
                             }
-                        }
-                        if (change)
+                            found |= !dead;
                             asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]),
                                          "r"(w[1]), "r"(w[2]), "r"(w[3])
                                          : "memory");
+                        }
                     }
                     if (found) *(volatile int *)&sh.poison = (int)n_piece;
                     fence_proxy_async_smem();
-                    mbar_arrive(&sh.guard_done);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.guard_done[n_guard & 7u]);
+                    ++n_guard;
                 }
                 pos += 2 * n;
+                ++n_piece;
             }
         }
-    }
     } else if (warp >= 12) {
-        // ---- E4M3: codes to fp16, rows past the end to zero, scales to fp32 ----
+        // ---- E4M3: codes to fp16, relative to the tile's largest scale ----
+        // A key or value row becomes code * 2^d with d = 7 for the tile's largest scale,
+        // exact for d >= -15.  A tile whose value scales span more than 22 binades
+        // ("wide") keeps bare codes, and the softmax applies the scales key by key.
         regs_give<C::kRegsFew>();
         if constexpr (kE4M3) {
             uint32_t pos = 0, n_piece = 0, tiles_done = 0;
             bool ok = true;
             const int row = threadIdx.x - 384;
-            auto widen = [&](int32_t tile, bool values, uint32_t key_no) {
+            Piece pc{};
+            uint32_t mul_k = 0, mul_v0 = 0, mul_v1 = 0;  // half2 factors of this row: key, values of two tiles
+            auto widen = [&](int32_t tile, uint32_t tile_no, bool values) {
                 const uint32_t rs = pos % kRaw, s = pos % kStages;
-                if (!mbar_wait(&sh.raw_full[rs], (pos / kRaw) & 1u, abort_flag, p.err)) return false;
-                if (!mbar_wait(&sh.empty[s], ((pos / kStages) & 1u) ^ 1u, abort_flag, p.err)) return false;
-                const uint32_t src = sm_raw + rs * C::kRawBytes + row * kD;
-                const uint32_t dst = sm_ring + s * C::kTileBytes + row * 128;
                 const bool live = tile * kTile + row < pc.rq.len;
-                const bool guarded = values && tile >= pc.guard_from;
+                if (!bar_wait(&sh.raw_full[rs], (pos / kRaw) & 1u, abort_flag, p.err)) return false;
                 if (!values) {
                     // written exponents lie in [-48, 48]; what was never written is masked
                     const int ke = min(max((int)sh.exps[rs][0][row] - 127, -48), 48);
                     const int ve = min(max((int)sh.exps[rs][1][row] - 127, -48), 48);
-                    const uint32_t ss = key_no & 3u;
-                    sh.kmul[ss][row] = __uint_as_float((uint32_t)(ke + 127) << 23);
-                    sh.vmul[ss][row] = __uint_as_float((uint32_t)(ve + 127) << 23);
-                    mbar_arrive(&sh.sc_full[ss]);
+                    const int kt = __reduce_max_sync(0xFFFFFFFFu, live ? ke : -64);
+                    const int vt = __reduce_max_sync(0xFFFFFFFFu, live ? ve : -64);
+                    const int vb = __reduce_min_sync(0xFFFFFFFFu, live ? ve : 64);
+                    int *red = sh.reduce[tile_no & 1u][warp - 12];
+                    if (lane == 0) red[0] = kt, red[1] = vt, red[2] = vb;
+                    sh.vexp[tile_no & 3u][row] = (int8_t)ve;
+                    named_sync<2, 128>();
+                    int k_top = -64, v_top = -64, v_low = 64;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        k_top = max(k_top, sh.reduce[tile_no & 1u][w][0]);
+                        v_top = max(v_top, sh.reduce[tile_no & 1u][w][1]);
+                        v_low = min(v_low, sh.reduce[tile_no & 1u][w][2]);
+                    }
+                    const bool wide = v_top - v_low > 22 && v_top > -64;
+                    if (row == 0) {
+                        sh.scale[tile_no & 3u].key = __uint_as_float((uint32_t)(k_top - 7 + 127) << 23);
+                        sh.scale[tile_no & 3u].value = v_top - 7;
+                        sh.scale[tile_no & 3u].wide = wide;
+                        mbar_arrive(&sh.sc_full[tile_no & 3u]);
+                    }
+                    auto factor = [](int d) {
+                        const __half2 h = __half2half2(__float2half_rn(pow2_int(max(d, -24))));
+                        return *reinterpret_cast<const uint32_t *>(&h);
+                    };
+                    mul_k = factor(live ? ke - k_top + 7 : 0);
+                    (tile_no & 1u ? mul_v1 : mul_v0) = factor(wide || !live ? 0 : ve - v_top + 7);
                 }
-                bool found = false;
+                const uint32_t mul = !values ? mul_k : tile_no & 1u ? mul_v1 : mul_v0;
+                const uint32_t src = sm_raw + rs * C::kRawBytes + row * kD;
+                const uint32_t dst = sm_ring + s * C::kTileBytes + row * 128;
+                const bool guarded = values && tile >= pc.guard_from;
+                uint32_t w[kD / 16][4];  // 16 codes a chunk; the copy's swizzle spreads the rows over the banks
 #pragma unroll
                 for (int c = 0; c < kD / 16; ++c) {
-                    // 16 codes; the copy's swizzle spreads the rows' chunks over the banks
-                    const uint32_t a =
-                        src + ((kD == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3)) << 4);
-                    uint32_t w[4];
+                    const uint32_t a = src + ((kD == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3)) << 4);
                     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                 : "=r"(w[c][0]), "=r"(w[c][1]), "=r"(w[c][2]), "=r"(w[c][3])
                                  : "r"(a));
-                    if (values && !live) w[0] = w[1] = w[2] = w[3] = 0u;
-                    if (guarded && live) {
+                }
+                if (values && (guarded || !live)) {
+                    bool found = false;
+#pragma unroll
+                    for (int c = 0; c < kD / 16; ++c)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const uint32_t nan = __vcmpeq4(w[k] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-                            if (nan) found = true, w[k] &= ~nan;
+                            if (!live) w[c][k] = 0u;
+                            const uint32_t nan = __vcmpeq4(w[c][k] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                            if (nan) found = true, w[c][k] &= ~nan;
                         }
-                    }
+                    if (found) *(volatile int *)&sh.poison = (int)n_piece;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.raw_empty[rs]);
+                if (!bar_wait(&sh.empty[s], ((pos / kStages) & 1u) ^ 1u, abort_flag, p.err)) return false;
+                const __half2 m2 = *reinterpret_cast<const __half2 *>(&mul);
+#pragma unroll
+                for (int c = 0; c < kD / 16; ++c) {
                     uint32_t o[8];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2(
-                            (__nv_fp8x2_storage_t)(w[k] & 0xFFFFu), __NV_E4M3);
-                        const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2(
-                            (__nv_fp8x2_storage_t)(w[k] >> 16), __NV_E4M3);
-                        o[2 * k] = (uint32_t)lo.x | ((uint32_t)lo.y << 16);
-                        o[2 * k + 1] = (uint32_t)hi.x | ((uint32_t)hi.y << 16);
+                    for (int k = 0; k < 8; ++k) {
+                        const __half2 h = __hmul2(
+                            __half2(__nv_cvt_fp8x2_to_halfraw2(
+                                (__nv_fp8x2_storage_t)(w[c][k >> 1] >> (16 * (k & 1))), __NV_E4M3)),
+                            m2);
+                        o[k] = *reinterpret_cast<const uint32_t *>(&h);
                     }
                     const uint32_t d0 = dst + (c >> 2) * (kTile * 128);
 #pragma unroll
@@ -747,26 +936,23 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                                      "r"(o[4 * k]), "r"(o[4 * k + 1]), "r"(o[4 * k + 2]), "r"(o[4 * k + 3])
                                      : "memory");
                 }
-                if (found) *(volatile int *)&sh.poison = (int)n_piece;
-                mbar_arrive(&sh.raw_empty[rs]);
                 fence_proxy_async_smem();
-                mbar_arrive(&sh.full[s]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.full[s]);
                 ++pos;
                 return true;
             };
-            while (ok && next_piece(&pc)) {
-                ++n_piece;
-                const int32_t n = pc.t1 - pc.t0;
-                if (pc.shared) {
-                    for (int32_t j = 0; ok && j < n; ++j)
-                        ok = widen(pc.t0 + j, false, tiles_done + j) && widen(pc.t0 + j, true, 0);
-                } else {
-                    ok = widen(pc.t0, false, tiles_done);
-                    for (int32_t j = 0; ok && j < n; ++j)
-                        ok = (j + 1 >= n || widen(pc.t0 + j + 1, false, tiles_done + j + 1)) &&
-                             widen(pc.t0 + j, true, 0);
+            while (ok && take_piece(n_piece, &pc, true)) {
+                // operands in the ring's order: shared K0 V0 K1 V1 ..., alternate K0 K1 V0 K2 V1 ...
+                const int32_t n = pc.t1 - pc.t0, lead = pc.shared() ? 0 : 1;
+                int32_t jk = 0, jv = 0;
+                for (int32_t i = 0; ok && i < 2 * n; ++i) {
+                    const bool values = jk == n || jk - jv > lead;
+                    const int32_t j = values ? jv++ : jk++;
+                    ok = widen(pc.t0 + j, tiles_done + j, values);
                 }
                 tiles_done += n;
+                ++n_piece;
             }
         }
     } else {
@@ -776,215 +962,282 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
         const int wq = warp & 3;
         const int my = wq * 32 + lane;  // row within the slot
         const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
-        const uint32_t tS = tmem + s * kTile + lane_base;
+        const uint32_t tS = s * kTile + lane_base;
+        const uint32_t tO = 256 + s * kD + lane_base;
         uint32_t n_piece = 0, n_s = 0, tiles_done = 0;
         uint32_t n_o[2] = {0, 0};
         bool ok = true;
-        // a negative scale negates Q; with scale 0 Q counts as zeros (masked scores are
-        // -inf and must not meet a factor 0)
-        const uint32_t flip = p.scale_log2 < 0.0f ? 0x80008000u : 0u;
-        const uint32_t keep = p.scale_log2 == 0.0f ? 0u : 0xFFFFFFFFu;
-        const float mul = p.scale_log2 == 0.0f ? 1.0f : fmaxf(fabsf(p.scale_log2), 1.1754944e-38f);
-        while (ok && next_piece(&pc)) {
-            ++n_piece;
-            // queries: kD / 8 lanes hold a row, 8 values each
+        const float mul = p.scale_log2;                                      // > 0
+        const uint32_t magic = (65536u + p.group - 1) / (uint32_t)p.group;   // x / group for x < 512
+        Piece pc{};
+        while (ok && take_piece(n_piece, &pc, true)) {
+            const bool both = pc.shared();
+            // queries: kD / 8 lanes hold a row, 8 values each; eight rows in flight per thread
             {
-                constexpr int kLanes = kD / 8;
+                constexpr int kLanes = kD / 8, kStep = 256 / kLanes;
+                [[maybe_unused]] const uint32_t row_lanes = ((1u << kLanes) - 1u) << (lane & ~(kLanes - 1));
                 const int l8 = threadIdx.x % kLanes;
-                for (int r = threadIdx.x / kLanes; r < pc.n_rows; r += 256 / kLanes) {
-                    const int32_t g = pc.row0 + r;
-                    const __nv_bfloat16 *src = (const __nv_bfloat16 *)p.q +
-                                               (int64_t)(pc.rq.t0 + g / p.group) * p.q_stride +
-                                               (int64_t)(pc.h * p.group + g % p.group) * kD + l8 * 8;
-                    uint4 v = __ldg(reinterpret_cast<const uint4 *>(src));
-                    uint32_t w[4] = {(v.x ^ flip) & keep, (v.y ^ flip) & keep, (v.z ^ flip) & keep,
-                                     (v.w ^ flip) & keep};
-                    if constexpr (kE4M3) {
-                        float f[8], amax = 0.0f;
+                const __nv_bfloat16 *q0 = (const __nv_bfloat16 *)p.q + (int64_t)(pc.rq.t0 + pc.tok0) * p.q_stride +
+                                          (int64_t)pc.h * p.group * kD + l8 * 8;
+#pragma unroll 1
+                for (int rb = threadIdx.x / kLanes; rb < pc.n_rows; rb += 8 * kStep) {
+                    uint4 v[8];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            f[2 * k] = __uint_as_float(w[k] << 16);
-                            f[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-                            amax = fmaxf(amax, fmaxf(fabsf(f[2 * k]), fabsf(f[2 * k + 1])));
-                        }
-                        const uint32_t group_mask =
-                            (kLanes == 32 ? 0xFFFFFFFFu : ((1u << kLanes) - 1u)) << (lane & ~(kLanes - 1));
-#pragma unroll
-                        for (int o = kLanes / 2; o > 0; o >>= 1)
-                            amax = fmaxf(amax, __shfl_xor_sync(group_mask, amax, o));
-                        // 2^-a: the largest magnitude's binade becomes 2^7
-                        const int a = min(max((int)(__float_as_uint(amax) >> 23) - 127 - 7, -110), 110);
-                        const float down = __uint_as_float((uint32_t)(127 - a) << 23);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) w[k] = pack16<true>(f[2 * k] * down, f[2 * k + 1] * down);
-                        if (l8 == 0)
-                            sh.qmul[n_piece & 1u][r] =
-                                fmaxf(__uint_as_float((uint32_t)(127 + a) << 23) * mul, 1.1754944e-38f);
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = rb + i * kStep;
+                        const uint32_t x = pc.rem0 + r, dt = (x * magic) >> 16;
+                        v[i] = make_uint4(0u, 0u, 0u, 0u);
+                        if (r < pc.n_rows)
+                            v[i] = __ldg(reinterpret_cast<const uint4 *>(
+                                q0 + (int64_t)dt * p.q_stride + (int)(x - dt * p.group) * kD));
                     }
-                    const int c = l8 & 7, half = l8 >> 3;
-                    const uint32_t dst = sm_q + (r >> 7) * C::kTileBytes + half * (kTile * 128) +
-                                         (r & 127) * 128 + ((c ^ (r & 7)) << 4);
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[0]), "r"(w[1]),
-                                 "r"(w[2]), "r"(w[3])
-                                 : "memory");
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = rb + i * kStep;
+                        uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                        if constexpr (kE4M3) {
+                            float f[8], amax = 0.0f;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                f[2 * k] = __uint_as_float(w[k] << 16);
+                                f[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+                                amax = fmaxf(amax, fmaxf(fabsf(f[2 * k]), fabsf(f[2 * k + 1])));
+                            }
+#pragma unroll
+                            for (int o = kLanes / 2; o > 0; o >>= 1)
+                                amax = fmaxf(amax, __shfl_xor_sync(row_lanes, amax, o));
+                            // 2^-a: the largest magnitude's binade becomes 2^7
+                            const int a = min(max((int)(__float_as_uint(amax) >> 23) - 127 - 7, -110), 110);
+                            const float down = __uint_as_float((uint32_t)(127 - a) << 23);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                w[k] = pack16<true>(f[2 * k] * down, f[2 * k + 1] * down);
+                            if (l8 == 0 && r < pc.n_rows)
+                                sh.qmul[n_piece & 1u][r] =
+                                    fmaxf(__uint_as_float((uint32_t)(127 + a) << 23) * mul, 1.1754944e-38f);
+                        }
+                        const int c = l8 & 7, half = l8 >> 3;
+                        const uint32_t dst = sm_q + (r >> 7) * C::kTileBytes + half * (kTile * 128) +
+                                             (r & 127) * 128 + ((c ^ (r & 7)) << 4);
+                        if (r < pc.n_rows)
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[0]),
+                                         "r"(w[1]), "r"(w[2]), "r"(w[3])
+                                         : "memory");
+                    }
                 }
                 fence_proxy_async_smem();
-                mbar_arrive(&sh.q_full);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.q_full);
                 if constexpr (kE4M3) named_sync<1, 256>();  // the rows' scales
             }
-            const int32_t r_blk = (pc.shared ? s * kTile : 0) + my;  // row within the block
-            const int32_t r_req = pc.row0 + r_blk;
-            const int32_t tok = r_req / p.group;
+            const int32_t r_blk = (both ? s * kTile : 0) + my;  // row within the block
+            const uint32_t r_off = pc.rem0 + r_blk, r_tok = (r_off * magic) >> 16;
+            const int32_t tok = pc.tok0 + (int32_t)r_tok;
             const bool live_row = r_blk < pc.n_rows;
-            const bool live_warp = (pc.shared ? s * kTile : 0) + wq * 32 < pc.n_rows;
-            float qm = mul;
-            if constexpr (kE4M3) qm = live_row ? sh.qmul[n_piece & 1u][r_blk] : 0.0f;
-            const int32_t first_tok = (pc.row0 + (pc.shared ? s * kTile : 0)) / p.group;
+            const bool live_warp = (both ? s * kTile : 0) + wq * 32 < pc.n_rows;
+            float qm0 = mul;
+            if constexpr (kE4M3) qm0 = live_row ? sh.qmul[n_piece & 1u][r_blk] : 1.0f;
             // positions below this one are seen by every row of the slot
-            const int32_t all_seen = kPaged ? pc.rq.ctx : first_tok + 1;
-            const int32_t t_end = pc.shared && s == 0 ? pc.t1a : pc.t1;
-            const int32_t step = pc.shared ? 1 : 2;
+            const int32_t all_seen =
+                kPaged ? pc.rq.ctx : pc.tok0 + (int32_t)(((pc.rem0 + (both ? s * kTile : 0)) * magic) >> 16) + 1;
+            const int32_t t_end = both && s == 0 ? pc.t1a : pc.t1;
             float base = -INFINITY, sum = 0.0f;
-            int shift = kNoShift;  // E4M3: x
-            const uint32_t tO = tmem + 256 + s * kD + lane_base;
+            int x_shift = kNoShift;  // E4M3: x
             bool first = true;
-            for (int32_t t = pc.t0 + (pc.shared ? 0 : s); t < t_end; t += step) {
-                const uint32_t sc = (tiles_done + (uint32_t)(t - pc.t0));
+            for (int32_t t = pc.t0 + (both ? 0 : s); t < t_end; t += both ? 1 : 2) {
+                float qm = qm0;
+                int v_exp = 0;
+                bool wide = false;
+                [[maybe_unused]] const uint32_t tile_no = tiles_done + (uint32_t)(t - pc.t0);
                 if constexpr (kE4M3) {
-                    ok = mbar_wait(&sh.sc_full[sc & 3u], (sc >> 2) & 1u, abort_flag, p.err);
+                    ok = bar_wait(&sh.sc_full[tile_no & 3u], (tile_no >> 2) & 1u, abort_flag, p.err);
                     if (!ok) break;
+                    const TileScale ts = sh.scale[tile_no & 3u];
+                    qm *= ts.key;
+                    v_exp = ts.value;
+                    wide = ts.wide;
                 }
-                ok = mbar_wait(&sh.s_full[s], n_s & 1u, abort_flag, p.err);
+                ok = bar_wait(&sh.s_full[s], n_s & 1u, abort_flag, p.err);
                 if (!ok) break;
                 ++n_s;
                 tc_fence_after();
-                if (live_warp) {
-                    uint32_t x[4][32];
+                if (!live_warp) {
+                    if (lane == 0) {
+                        mbar_arrive(&sh.p_full[s][0]);
+                        mbar_arrive(&sh.p_full[s][1]);
+                    }
+                    continue;
+                }
+                uint32_t x[4][32];
+                const bool masked = (t + 1) * kTile > all_seen;
+                auto scores = [&]() {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, x[c]);
+                    uint32_t w[4] = {0u, 0u, 0u, 0u};
+                    if (masked && live_row) seen_bits<kPaged>(p, pc.rq, tok, t, w);
                     tmem_ld_wait();
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tmem_tie(x[c]);
-                    if constexpr (kE4M3) {
-                        const float *km = sh.kmul[sc & 3u];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-#pragma unroll
-                            for (int k = 0; k < 32; k += 4) {
-                                const float4 f = *reinterpret_cast<const float4 *>(km + 32 * c + k);
-                                x[c][k] = __float_as_uint(__uint_as_float(x[c][k]) * f.x);
-                                x[c][k + 1] = __float_as_uint(__uint_as_float(x[c][k + 1]) * f.y);
-                                x[c][k + 2] = __float_as_uint(__uint_as_float(x[c][k + 2]) * f.z);
-                                x[c][k + 3] = __float_as_uint(__uint_as_float(x[c][k + 3]) * f.w);
-                            }
-                    }
-                    if ((t + 1) * kTile > all_seen) {
-                        uint32_t w[4] = {0, 0, 0, 0};
-                        if (live_row) seen_bits<kPaged>(p, pc.rq, tok, t, w);
+                    if (masked) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
                                 if (!((w[c] >> k) & 1u)) x[c][k] = 0xFF800000u;  // -inf
                     }
-                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                };
+                uint64_t part[4];
+                const uint64_t qm2 = f2(qm, qm);
+                uint32_t pk[32];
+                // weights of keys 64 h ..: 2^(z - base); E4M3 keeps them in x
+                auto weights = [&](int h, float safe) {
+                    const uint64_t off2 = f2(-safe, -safe);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                    for (int k = 0; k < 32; ++k) {
+                        const int c = 2 * h + (k >> 4), e = (2 * k) & 31;
+                        float a, b;
+                        unf2(fma2(f2(x[c][e], x[c][e + 1]), qm2, off2), a, b);
+                        a = ex2(a);
+                        b = ex2(b);
+                        part[k & 3] = add2(part[k & 3], f2(a, b));
+                        if constexpr (kE4M3)
+                            x[c][e] = __float_as_uint(a), x[c][e + 1] = __float_as_uint(b);
+                        else
+                            pk[k] = pack16<false>(a, b);
+                    }
+                };
+                auto row_top = [&]() {
+                    float top[8];
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) top[k & 3] = fmaxf(top[k & 3], __uint_as_float(x[c][k]));
-                    const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * qm;
+                    for (int k = 0; k < 8; ++k)
+                        top[k] = fmaxf(__uint_as_float(x[0][2 * k]), __uint_as_float(x[0][2 * k + 1]));
+#pragma unroll
+                    for (int k = 16; k < 128; k += 2)
+                        top[(k >> 1) & 7] =
+                            fmaxf(fmaxf(top[(k >> 1) & 7], __uint_as_float(x[k >> 5][k & 31])),
+                                  __uint_as_float(x[k >> 5][(k & 31) + 1]));
+                    return fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])),
+                                 fmaxf(fmaxf(top[4], top[5]), fmaxf(top[6], top[7]))) * qm;
+                };
+                // O and x or base move together: O 2^x 2^base stays
+                auto rescale = [&](float fix) {
+                    if (first) return;
+#pragma unroll 1
+                    for (int c = 0; c < kD; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + c, o);
+                        tmem_ld_wait();
+                        tmem_tie(o);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fix);
+                        tmem_st32(tO + c, o);
+                    }
+                };
+                auto hand_over = [&](int h) {
+                    tmem_st32(tS + 32 * h, pk);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.p_full[s][h]);
+                };
+                if constexpr (!kE4M3) {
+                    // the first half against the base so far, beside the maximum; again,
+                    // from the scores in TMEM, where the maximum moved the base (the first
+                    // tiles, mostly)
+#pragma unroll 1
+                    for (bool again = false;;) {
+                        scores();
+                        const float mx = row_top();
+                        part[0] = part[1] = part[2] = part[3] = 0ull;
+                        weights(0, base == -INFINITY ? 0.0f : base);
+                        if (again) break;
+                        const bool grow = mx > base + kLazy;
+                        if (!__any_sync(0xFFFFFFFFu, grow)) break;
+                        // grow: base was -inf (fix = 0, nothing summed yet) or finite
+                        const float fix = grow ? ex2(base - mx) : 1.0f;
+                        if (grow) base = mx;
+                        sum *= fix;
+                        rescale(fix);
+                        again = true;
+                    }
+                    hand_over(0);
+                    weights(1, base == -INFINITY ? 0.0f : base);
+                    hand_over(1);
+                } else {
+                    scores();
+                    const float mx = row_top();
                     const bool grow = mx > base + kLazy;
                     const float nb = grow ? mx : base;
                     const float safe = nb == -INFINITY ? 0.0f : nb;
-                    // grow: base was -inf (fix = 0, nothing summed yet) or finite
+                    const float gain = grow ? fminf(nb - base, 1024.0f) : 0.0f;  // 1024: base was -inf
                     float fix = grow ? ex2(base - nb) : 1.0f;
-                    bool move = grow;
                     base = nb;
                     sum *= fix;
-                    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    float down = 1.0f;  // 2^-x
-                    if constexpr (kE4M3) {
-                        const float *vm = sh.vmul[sc & 3u];
-                        float hi[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    part[0] = part[1] = part[2] = part[3] = 0ull;
+                    weights(0, safe);
+                    weights(1, safe);
+                    // binade of the largest weight with its value's scale
+                    int level = v_exp + (int)floorf(fmaxf(mx - safe, -4096.0f));
+                    bool some = mx > -INFINITY;
+                    if (wide) {
+                        float hi = 0.0f;
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
 #pragma unroll
-                            for (int k = 0; k < 32; k += 4) {
-                                const float4 f = *reinterpret_cast<const float4 *>(vm + 32 * c + k);
-                                const float v4[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const float w = ex2(fmaf(__uint_as_float(x[c][k + e]), qm, -safe));
-                                    part[e] += w;
-                                    const float u = w * v4[e];
-                                    hi[e] = fmaxf(hi[e], u);
-                                    x[c][k + e] = __float_as_uint(u);
-                                }
+                            for (int k = 0; k < 32; ++k) {
+                                const float u =
+                                    __uint_as_float(x[c][k]) *
+                                    __uint_as_float((uint32_t)(127 + sh.vexp[tile_no & 3u][32 * c + k]) << 23);
+                                hi = fmaxf(hi, u);
+                                x[c][k] = __float_as_uint(u);
                             }
-                        const float h = fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3]));
-                        const int e = (int)(__float_as_uint(h) >> 23) - 127;
-                        const bool had = shift != kNoShift;
-                        if (h > 0.0f && e - shift >= kCapE4M3) {
-                            const int ns = max(e - kTopE4M3, -100);
-                            fix = had ? fix * ex2((float)(shift - ns)) : 0.0f;
-                            shift = ns;
-                            move = true;
-                        }
-                        down = shift == kNoShift ? 1.0f : __uint_as_float((uint32_t)(127 - shift) << 23);
+                        level = (int)(__float_as_uint(hi) >> 23) - 127;
+                        some = hi > 0.0f;
+                        v_exp = 0;
                     }
-                    if (!first && __any_sync(0xFFFFFFFFu, move)) {
-#pragma unroll
-                        for (int c = 0; c < kD / 32; ++c) {
-                            uint32_t o[32];
-                            tmem_ld32(tO + 32 * c, o);
-                            tmem_ld_wait();
-                            tmem_tie(o);
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fix);
-                            tmem_st32(tO + 32 * c, o);
-                        }
+                    const bool had = x_shift != kNoShift;
+                    if (some && (grow || level - x_shift >= kCapE4M3)) {
+                        const int nx = max(had ? x_shift - (int)gain : -100, level - kTopE4M3);
+                        if (had) fix *= pow2_int(x_shift - nx);
+                        x_shift = nx;
                     }
+                    if (__any_sync(0xFFFFFFFFu, fix != 1.0f)) rescale(had ? fix : 0.0f);
+                    const float down = had || some ? pow2_int(v_exp - x_shift) : 1.0f;
+                    const uint64_t down2 = f2(down, down);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        uint32_t pk[32];
 #pragma unroll
                         for (int k = 0; k < 32; ++k) {
                             const int c = 2 * h + (k >> 4), e = (2 * k) & 31;
-                            if constexpr (kE4M3) {
-                                pk[k] = pack16<true>(__uint_as_float(x[c][e]) * down,
-                                                     __uint_as_float(x[c][e + 1]) * down);
-                            } else {
-                                const float a = ex2(fmaf(__uint_as_float(x[c][e]), qm, -safe));
-                                const float b = ex2(fmaf(__uint_as_float(x[c][e + 1]), qm, -safe));
-                                part[k & 1] += a;
-                                part[2 + (k & 1)] += b;
-                                pk[k] = pack16<false>(a, b);
-                            }
+                            float a, b;
+                            unf2(mul2(f2(x[c][e], x[c][e + 1]), down2), a, b);
+                            pk[k] = pack16<true>(a, b);
                         }
-                        tmem_st32(tS + 32 * h, pk);
+                        hand_over(h);
                     }
-                    sum += (part[0] + part[1]) + (part[2] + part[3]);
-                    tmem_st_wait();
-                    first = false;
                 }
-                tc_fence_before();
-                mbar_arrive(&sh.p_full[s]);
+                {
+                    float a, b;
+                    unf2(add2(add2(part[0], part[1]), add2(part[2], part[3])), a, b);
+                    sum += a + b;
+                }
+                first = false;
             }
             if (!ok) break;
             // ---- epilogue ----
             const int32_t n = pc.t1 - pc.t0;
-            const bool used0 = true, used1 = pc.shared || n > 1;
+            const bool used1 = both || n > 1;
             tiles_done += n;
-            const float up = !kE4M3 || shift == kNoShift ? 1.0f : __uint_as_float((uint32_t)(127 + shift) << 23);
+            const float up = !kE4M3 || x_shift == kNoShift ? 1.0f : pow2_int(x_shift);
             float f0, f1 = 0.0f;
             int col0 = 0, cols = kD;
-            if (pc.shared) {
-                ok = mbar_wait(&sh.o_full[s], n_o[s] & 1u, abort_flag, p.err);
+            if (both) {
+                ok = bar_wait(&sh.o_full[s], n_o[s] & 1u, abort_flag, p.err);
                 if (!ok) break;
                 f0 = up;
             } else {
-                ok = mbar_wait(&sh.o_full[0], n_o[0] & 1u, abort_flag, p.err) &&
-                     (!used1 || mbar_wait(&sh.o_full[1], n_o[1] & 1u, abort_flag, p.err));
+                ok = bar_wait(&sh.o_full[0], n_o[0] & 1u, abort_flag, p.err) &&
+                     (!used1 || bar_wait(&sh.o_full[1], n_o[1] & 1u, abort_flag, p.err));
                 if (!ok) break;
                 float *mine = stat + 3 * kTile * s + my;
                 mine[0] = base;
@@ -1006,35 +1259,37 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                 cols = kD / 2;
                 col0 = s * cols;
             }
-            n_o[0] += used0;
+            n_o[0] += 1;
             n_o[1] += used1;
             tc_fence_after();
             if (live_warp) {
                 const bool poisoned = *(volatile int *)&sh.poison == (int)n_piece;
                 const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                const int64_t row = (int64_t)(pc.rq.t0 + tok) * p.q_heads + pc.h * p.group + r_req % p.group;
+                const int64_t row =
+                    (int64_t)(pc.rq.t0 + tok) * p.q_heads + pc.h * p.group + (int)(r_off - r_tok * p.group);
                 float *part = pc.slot >= 0 ? p.part + pc.slot * part_slot_floats(p.part_rows, kD) : nullptr;
                 float *part_row = part ? part + (int64_t)r_blk * kD : nullptr;
                 __nv_bfloat16 *out_row = (__nv_bfloat16 *)p.out + row * kD;
-                const bool both = !pc.shared && used1;
-                const uint32_t t0 = tmem + 256 + lane_base + (pc.shared && s == 1 ? kD : 0);
+                const uint32_t t0 = 256 + lane_base + (both && s == 1 ? kD : 0);
+                const float g0 = part ? f0 : f0 * inv, g1 = part ? f1 : f1 * inv;
 #pragma unroll 1
                 for (int c0 = col0; c0 < col0 + cols; c0 += 32) {
                     uint32_t a[32];
                     tmem_ld32(t0 + c0, a);
-                    tmem_ld_wait();
-                    tmem_tie(a);
-                    if (both) {
+                    if (!both && used1) {
                         uint32_t b[32];
                         tmem_ld32(t0 + kD + c0, b);
                         tmem_ld_wait();
+                        tmem_tie(a);
                         tmem_tie(b);
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
-                            a[k] = __float_as_uint(__uint_as_float(a[k]) * f0 + __uint_as_float(b[k]) * f1);
+                            a[k] = __float_as_uint(__uint_as_float(a[k]) * g0 + __uint_as_float(b[k]) * g1);
                     } else {
+                        tmem_ld_wait();
+                        tmem_tie(a);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) a[k] = __float_as_uint(__uint_as_float(a[k]) * f0);
+                        for (int k = 0; k < 32; ++k) a[k] = __float_as_uint(__uint_as_float(a[k]) * g0);
                     }
                     if (!live_row) continue;
                     if (part) {
@@ -1046,18 +1301,17 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                         uint4 *dst = reinterpret_cast<uint4 *>(out_row + c0);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            uint32_t w[4];
+                            uint32_t o[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                w[e] = pack16<false>(__uint_as_float(a[8 * k + 2 * e]) * inv,
-                                                     __uint_as_float(a[8 * k + 2 * e + 1]) * inv);
-                            dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                                o[e] = pack16<false>(__uint_as_float(a[8 * k + 2 * e]),
+                                                     __uint_as_float(a[8 * k + 2 * e + 1]));
+                            dst[k] = make_uint4(o[0], o[1], o[2], o[3]);
                         }
                     }
                 }
                 if (poisoned && live_row)
-                    add_poison<kD, kE4M3, kPaged>(p, pc.rq, pc.b, pc.h, tok,
-                                                  max(pc.t0, pc.guard_from) * kTile,
+                    add_poison<kD, kE4M3, kPaged>(p, pc.rq, pc.b, pc.h, tok, max(pc.t0, pc.guard_from) * kTile,
                                                   min(pc.t1 * kTile, pc.rq.len), col0, cols, part_row, out_row);
                 if (live_row && col0 == 0) {
                     if (part) {
@@ -1070,6 +1324,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
             }
             // the sums are read: the next piece's q_full arrivals say so to the MMAs
             tc_fence_before();
+            ++n_piece;
         }
     }
     __syncwarp();
@@ -1077,7 +1332,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
     __syncthreads();
     if (warp == 8) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(0, 512);
     }
 }
 
@@ -1109,13 +1364,11 @@ dflash2_status launch_one(const DeviceInfo &di, Params p, cudaStream_t st) {
         }
         if (s != DFLASH2_OK) return s;
     }
-    p.row_block = kRowBlock;
-    p.n_cta = di.sm_count;
-    dim3 grid((unsigned)p.n_cta);
-    if (!kPaged)
-        grid = dim3((unsigned)(((int64_t)p.total_q * p.group + kRowBlock - 1) / kRowBlock + p.batch),
-                    (unsigned)p.kv_heads);
-    launch_k(fn, grid, dim3(C::kThreads), C::kSmem, st, p, maps[0], maps[1]);
+    p.row_shift = kRowShift;
+    // prompts: every row block of every request, at most one short one each
+    const int64_t items = ((((int64_t)p.total_q * p.group) >> kRowShift) + p.batch) * p.kv_heads;
+    p.n_cta = kPaged || items > di.sm_count ? di.sm_count : (int32_t)items;
+    launch_k(fn, dim3((unsigned)p.n_cta), dim3(C::kThreads), C::kSmem, st, p, maps[0], maps[1]);
     const dflash2_status s = launch_status();
     if (s != DFLASH2_OK || !kPaged) return s;
     return launch_combine(di, p, DFLASH2_BF16, st);
@@ -1129,6 +1382,7 @@ bool rows16(const void *p, int64_t stride, int el) {
 
 bool tc_takes(const Params &p, bool paged, int32_t dtype, int32_t kv_format) {
     if (dtype != DFLASH2_BF16 || (p.head_dim != 64 && p.head_dim != 128)) return false;
+    if (!(p.scale_log2 >= 1.1754944e-38f)) return false;  // masked scores are -inf times the scale
     if (!rows16(p.q, p.q_stride, 2) || !aligned16(p.out) || !aligned16(p.k) || !aligned16(p.v))
         return false;
     if (!paged) return rows16(p.k, p.k_stride, 2) && rows16(p.v, p.v_stride, 2);
