@@ -50,11 +50,16 @@ struct Params {
     int32_t *err;
 };
 
-// Partial slot s of the workspace: part_rows rows of head_dim fp32 sums, then
-// part_rows maxima (log2 domain), then part_rows sums.  CTA c owns slots 2c
+// Partial slot s of the workspace: fp32 sums [ceil(head_dim / 4)][part_rows][4] (a
+// warp writes and reads neighbouring rows), then part_rows maxima (log2 domain),
+// then part_rows sums.  CTA c owns slots 2c
 // (an item it did not start) and 2c + 1 (an item it started and did not end).
 __host__ __device__ inline int64_t part_slot_floats(int32_t part_rows, int32_t head_dim) {
-    return (int64_t)part_rows * (head_dim + 2);
+    return (int64_t)part_rows * ((head_dim + 3) / 4 * 4 + 2);
+}
+// Offset of a slot's maxima; the sums of weights follow.
+__host__ __device__ inline int64_t part_stats(int32_t part_rows, int32_t head_dim) {
+    return (int64_t)part_rows * ((head_dim + 3) / 4 * 4);
 }
 
 struct Request {

@@ -226,14 +226,12 @@ __device__ void run_piece(const Params &p, const Request &rq, int32_t b, int32_t
             float *base = p.part + slot * part_slot_floats(p.part_rows, d);
 #pragma unroll
             for (int q = 0; q < kQuads; ++q)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int c = 64 * q + 4 * tx + e;
-                    if (c < d) base[(int64_t)r * d + c] = o[i][q][e];
-                }
+                if (64 * q + 4 * tx < d)  // past head_dim the sums are zeros
+                    reinterpret_cast<float4 *>(base)[(int64_t)(16 * q + tx) * p.part_rows + r] =
+                        make_float4(o[i][q][0], o[i][q][1], o[i][q][2], o[i][q][3]);
             if (tx == 0) {
-                base[(int64_t)p.part_rows * d + r] = m[i];
-                base[(int64_t)p.part_rows * (d + 1) + r] = l[i];
+                base[part_stats(p.part_rows, d) + r] = m[i];
+                base[part_stats(p.part_rows, d) + p.part_rows + r] = l[i];
             }
         } else {
             const int32_t g = row0 + r;
@@ -319,73 +317,79 @@ __global__ void __launch_bounds__(kThreads) simt_kernel(const Params p, bool vec
     if (any_bad && p.err) atomicOr(p.err, DFLASH2_DEVERR_ID_RANGE);
 }
 
-// Joins the partial rows of items that span CTAs: one warp per (token, query
-// head), partials in CTA order, each lane four of 128 values.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) combine_kernel(const Params p) {
-    __shared__ int64_t red[kThreads / 32];
-    const int32_t tok = blockIdx.x;
+// Joins the partial rows of items that span CTAs, in CTA order.  A CTA takes the
+// group's rows of one token and key/value head; a warp takes eight rows (neighbours
+// in a slot) at a time, four lanes a row, so that lane (row, c) holds every fourth
+// group of four values and a load reads 128 contiguous bytes of four such groups.
+template <typename T, int kQuads>  // groups of four values per lane
+__global__ void __launch_bounds__(128) combine_kernel(const Params p) {
+    __shared__ int64_t red[32];
+    __shared__ int32_t which;
+    const int32_t tok = blockIdx.x, h = blockIdx.y;
     // before the grid dependency only what was complete before the attention
     // kernel started is read: cu_q and kv_lens (it releases this grid after its
     // own wait)
     bool bad;
     int64_t all = 0, mine = 0;
-    __shared__ int32_t which;
     if (threadIdx.x == 0) which = -1;
     __syncthreads();
-    for (int b = threadIdx.x; b < p.batch; b += kThreads) {
-        const Request r = load_request<true>(p, b, &bad);
-        if (tok >= r.t0 && tok < r.t0 + r.t) which = b;
-    }
-    __syncthreads();
-    const int32_t mb = which;
-    for (int b = threadIdx.x; b < p.batch; b += kThreads) {
+    for (int b = threadIdx.x; b < p.batch; b += 128) {
         const Request r = load_request<true>(p, b, &bad);
         const int64_t n = request_units(p, r);
         all += n;
-        if (b < mb) mine += n;
+        if (r.t0 + r.t <= tok) mine += n;  // requests before the token's
+        if (tok >= r.t0 && tok < r.t0 + r.t) which = b;
     }
     const int64_t units = block_sum(all, red);
     const int64_t before = block_sum(mine, red);
     grid_dep_wait();
-    if (mb < 0) return;
-    const Request r = load_request<true>(p, mb, &bad);
+    if (which < 0) return;
+    const Request r = load_request<true>(p, which, &bad);
     const int32_t tiles = key_tiles(r), nrb = row_blocks(p, r);
     const int lane = threadIdx.x & 31;
     const int d = p.head_dim;
-    const int64_t slot_floats = part_slot_floats(p.part_rows, d);
-    for (int g = blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5); g < p.q_heads;
-         g += gridDim.y * (kThreads / 32)) {
-        const int32_t h = g / p.group;
-        const int64_t row = (int64_t)(tok - r.t0) * p.group + g % p.group;
+    const int64_t slot_floats = part_slot_floats(p.part_rows, d), stats = part_stats(p.part_rows, d);
+    const int64_t n_cta = split_ctas(p, units);
+    for (int g0 = (threadIdx.x >> 5) * 8; g0 < p.group; g0 += 32) {
+        const int g = g0 + (lane >> 2), c = lane & 3;
+        if (g >= p.group) continue;
+        const int64_t row = (int64_t)(tok - r.t0) * p.group + g;
         const int32_t rb = (int32_t)(row >> p.row_shift), rr = (int32_t)(row & ((1 << p.row_shift) - 1));
         const int64_t u0 = before + ((int64_t)h * nrb + rb) * tiles;
-        const int64_t n_cta = split_ctas(p, units);
         const int32_t c0 = cta_of(u0, units, n_cta), c1 = cta_of(u0 + tiles - 1, units, n_cta);
         if (c0 == c1) continue;  // the attention kernel wrote this row
-        auto part = [&](int32_t c) { return p.part + (2 * (int64_t)c + (c == c0)) * slot_floats; };
+        auto part = [&](int32_t k) { return p.part + (2 * (int64_t)k + (k == c0)) * slot_floats; };
         float m = -INFINITY;
-        for (int32_t c = c0 + lane; c <= c1; c += 32)
-            m = fmaxf(m, part(c)[(int64_t)p.part_rows * d + rr]);
-        m = warp_max(m);
+        for (int32_t k = c0; k <= c1; ++k) m = fmaxf(m, part(k)[stats + rr]);
         const float base = m == -INFINITY ? 0.0f : m;
         float l = 0.0f;
-        float o[8] = {};
-        for (int32_t c = c0; c <= c1; ++c) {
-            const float *s = part(c);
-            const float w = ex2(s[(int64_t)p.part_rows * d + rr] - base);
-            l = fmaf(w, s[(int64_t)p.part_rows * (d + 1) + rr], l);
+        float4 o[kQuads];
+#pragma unroll
+        for (int q = 0; q < kQuads; ++q) o[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int32_t k = c0; k <= c1; ++k) {
+            const float *s = part(k);
+            const float w = ex2(s[stats + rr] - base);
+            l = fmaf(w, s[stats + p.part_rows + rr], l);
             if (w == 0.0f) continue;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (lane + 32 * j < d) o[j] = fmaf(w, s[(int64_t)rr * d + lane + 32 * j], o[j]);
+            for (int q = 0; q < kQuads; ++q) {
+                if (4 * (4 * q + c) >= d) break;
+                const float4 v = reinterpret_cast<const float4 *>(s)[(int64_t)(4 * q + c) * p.part_rows + rr];
+                o[q].x = fmaf(w, v.x, o[q].x), o[q].y = fmaf(w, v.y, o[q].y);
+                o[q].z = fmaf(w, v.z, o[q].z), o[q].w = fmaf(w, v.w, o[q].w);
+            }
         }
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        const int64_t at = (int64_t)tok * p.q_heads + g;
+        const int64_t at = (int64_t)tok * p.q_heads + h * p.group + g;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (lane + 32 * j < d) put((T *)p.out + at * d + lane + 32 * j, o[j] * inv);
-        if (lane == 0 && p.lse)
+        for (int q = 0; q < kQuads; ++q) {
+            const int col = 4 * (4 * q + c);
+            const float v[4] = {o[q].x, o[q].y, o[q].z, o[q].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (col + e < d) put((T *)p.out + at * d + col + e, v[e] * inv);
+        }
+        if (c == 0 && p.lse)
             p.lse[at] = l == 0.0f ? -INFINITY : (base + log2f(l)) * 0.6931471805599453f;
     }
 }
@@ -455,13 +459,20 @@ dflash2_status launch_simt(const DeviceInfo &di, Params p, bool paged, int32_t d
     return launch_combine(di, p, dtype, st);
 }
 
-dflash2_status launch_combine(const DeviceInfo &, const Params &p, int32_t dtype, cudaStream_t st) {
-    const int warps = kThreads / 32;
-    const dim3 grid((unsigned)p.total_q, (unsigned)((p.q_heads + warps - 1) / warps));
-    if (dtype == DFLASH2_F32)
-        launch_k(combine_kernel<float>, grid, dim3(kThreads), 0, st, p);
+template <typename T> void combine_typed(const Params &p, cudaStream_t st) {
+    const dim3 grid((unsigned)p.total_q, (unsigned)p.kv_heads);
+    if (p.head_dim <= 64)
+        launch_k(combine_kernel<T, 4>, grid, dim3(128), 0, st, p);
+    else if (p.head_dim <= 128)
+        launch_k(combine_kernel<T, 8>, grid, dim3(128), 0, st, p);
     else
-        launch_k(combine_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, st, p);
+        launch_k(combine_kernel<T, 16>, grid, dim3(128), 0, st, p);
+}
+dflash2_status launch_combine(const DeviceInfo &, const Params &p, int32_t dtype, cudaStream_t st) {
+    if (dtype == DFLASH2_F32)
+        combine_typed<float>(p, st);
+    else
+        combine_typed<__nv_bfloat16>(p, st);
     return launch_status();
 }
 

@@ -449,8 +449,8 @@ __device__ __forceinline__ void seen_bits(const Params &p, const Request &rq, in
 }
 
 // Values of the keys [l0, l1) that token i of the request sees and that are not
-// finite, added to columns [col, col + cols) of a row as it was written (a
-// partial row of fp32 sums, or the output row): what the guard warp took out.
+// finite, added to columns [col, col + cols) of a row as it was written (`part`:
+// the row's first four sums of a partial slot, or `out`: the output row): what the guard warp took out.
 // Rare, so one thread per row.
 template <int kD, bool kE4M3, bool kPaged>
 __device__ __noinline__ void add_poison(const Params &p, Request rq, int32_t b, int32_t h, int32_t i,
@@ -471,7 +471,7 @@ __device__ __noinline__ void add_poison(const Params &p, Request rq, int32_t b, 
                                   : as_f32(((const __nv_bfloat16 *)p.v)[at + c]);
             if (fabsf(v) <= 3.4e38f) continue;
             if (part)
-                part[c] += v;
+                part[(int64_t)(c >> 2) * 4 * p.part_rows + (c & 3)] += v;
             else
                 out[c] = __float2bfloat16_rn(__bfloat162float(out[c]) + v);
         }
@@ -654,6 +654,14 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                     levels.next(p, lane, &pc);
                 pc.tok0 = pc.row0 / p.group;
                 pc.rem0 = pc.row0 - pc.tok0 * p.group;
+                for (int r = lane; r < pc.n_rows; r += 32) {  // the queries, on their way to L2
+                    const int x = pc.rem0 + r, dt = x / p.group;
+                    const __nv_bfloat16 *q = (const __nv_bfloat16 *)p.q +
+                                             (int64_t)(pc.rq.t0 + pc.tok0 + dt) * p.q_stride +
+                                             (int64_t)(pc.h * p.group + x - dt * p.group) * kD;
+#pragma unroll
+                    for (int c = 0; c < kD; c += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + c));
+                }
                 if (elect_one()) {
                     ok = bar_wait(&sh.piece_empty[n_piece % kPieces], ((n_piece / kPieces) & 1u) ^ 1u,
                                   abort_flag, p.err);
@@ -804,31 +812,39 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                     const uint32_t nv = pos + (pc.shared() ? 2 * j + 1 : j + 1 < n ? 2 * j + 2 : 2 * n - 1);
                     ok = bar_wait(&sh.guard_go[n_guard & 7u], (n_guard >> 3) & 1u, abort_flag, p.err);
                     if (!ok) break;
-                    const uint32_t base = sm_ring + (nv % kStages) * C::kTileBytes;
-                    const int32_t live = pc.rq.len - (pc.t0 + j) * kTile;  // rows of the tile that are keys
+                    // rows [low, live) of the tile may be masked for some row; from live on
+                    // they are no keys.  A 128-byte row of a column block is 8 chunks.
+                    const int32_t first = (pc.t0 + j) * kTile;
+                    const int32_t live = min(max(pc.rq.len - first, 0), kTile);
+                    const int32_t low = min(max((kPaged ? pc.rq.ctx : pc.tok0) - first, 0), live);
                     bool found = false;
-#pragma unroll 4
-                    for (int i = lane; i < C::kTileBytes / 16; i += 32) {
-                        const uint32_t addr = base + i * 16;
-                        uint32_t w[4];
-                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                                     : "r"(addr));
-                        const bool dead = ((i >> 3) & (kTile - 1)) >= live;
-                        // a 16-bit exponent of all ones: adding 1 to it carries into the sign's place
-                        uint32_t odd = 0;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) odd |= ((w[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
-                        if (dead || odd) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                if (dead || (w[k] & 0x7F80u) == 0x7F80u) w[k] &= 0xFFFF0000u;
-                                if (dead || (w[k] & 0x7F800000u) == 0x7F800000u) w[k] &= 0xFFFFu;
-                            }
-                            found |= !dead;
-                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]),
-                                         "r"(w[1]), "r"(w[2]), "r"(w[3])
+#pragma unroll 1
+                    for (int half = 0; half < C::kHalves; ++half) {
+                        const uint32_t base = sm_ring + (nv % kStages) * C::kTileBytes + half * (kTile * 128);
+#pragma unroll 1
+                        for (int i = live * 8 + lane; i < kTile * 8; i += 32)
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(base + i * 16), "r"(0)
                                          : "memory");
+#pragma unroll 4
+                        for (int i = low * 8 + lane; i < live * 8; i += 32) {
+                            uint32_t w[4], odd = 0;
+                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                         : "r"(base + i * 16));
+                            // a 16-bit exponent of all ones: adding 1 to it carries into the sign's place
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) odd |= ((w[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+                            found |= odd != 0;
+                        }
+                        if (__any_sync(0xFFFFFFFFu, found)) {
+#pragma unroll 1
+                            for (int i = low * 32 + lane; i < live * 32; i += 32) {
+                                uint32_t w;
+                                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(base + i * 4));
+                                if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+                                if ((w & 0x7F800000u) == 0x7F800000u) w &= 0xFFFFu;
+                                asm volatile("st.shared.u32 [%0], %1;" ::"r"(base + i * 4), "r"(w) : "memory");
+                            }
                         }
                     }
                     if (found) *(volatile int *)&sh.poison = (int)n_piece;
@@ -1268,7 +1284,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                 const int64_t row =
                     (int64_t)(pc.rq.t0 + tok) * p.q_heads + pc.h * p.group + (int)(r_off - r_tok * p.group);
                 float *part = pc.slot >= 0 ? p.part + pc.slot * part_slot_floats(p.part_rows, kD) : nullptr;
-                float *part_row = part ? part + (int64_t)r_blk * kD : nullptr;
+                float4 *part_col = reinterpret_cast<float4 *>(part) + r_blk;  // [kD / 4][part_rows] of four
                 __nv_bfloat16 *out_row = (__nv_bfloat16 *)p.out + row * kD;
                 const uint32_t t0 = 256 + lane_base + (both && s == 1 ? kD : 0);
                 const float g0 = part ? f0 : f0 * inv, g1 = part ? f1 : f1 * inv;
@@ -1293,10 +1309,11 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                     }
                     if (!live_row) continue;
                     if (part) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(part_row + c0);
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
-                            dst[k] = make_uint4(a[4 * k], a[4 * k + 1], a[4 * k + 2], a[4 * k + 3]);
+                            part_col[(c0 / 4 + k) * p.part_rows] =
+                                make_float4(__uint_as_float(a[4 * k]), __uint_as_float(a[4 * k + 1]),
+                                            __uint_as_float(a[4 * k + 2]), __uint_as_float(a[4 * k + 3]));
                     } else {
                         uint4 *dst = reinterpret_cast<uint4 *>(out_row + c0);
 #pragma unroll
@@ -1312,11 +1329,11 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                 }
                 if (poisoned && live_row)
                     add_poison<kD, kE4M3, kPaged>(p, pc.rq, pc.b, pc.h, tok, max(pc.t0, pc.guard_from) * kTile,
-                                                  min(pc.t1 * kTile, pc.rq.len), col0, cols, part_row, out_row);
+                                                  min(pc.t1 * kTile, pc.rq.len), col0, cols, part ? part + 4 * r_blk : nullptr, out_row);
                 if (live_row && col0 == 0) {
                     if (part) {
-                        part[(int64_t)p.part_rows * kD + r_blk] = base;
-                        part[(int64_t)p.part_rows * (kD + 1) + r_blk] = sum;
+                        part[part_stats(p.part_rows, kD) + r_blk] = base;
+                        part[part_stats(p.part_rows, kD) + p.part_rows + r_blk] = sum;
                     } else if (p.lse) {
                         p.lse[row] = sum == 0.0f ? -INFINITY : (base + log2f(sum)) * 0.6931471805599453f;
                     }
