@@ -20,28 +20,32 @@
 //   shared:     a row block of up to 256 rows; slot s holds rows 128 s ..; both
 //               take every key tile, so a key is loaded once for 256 rows.
 //   alternate:  up to 128 rows; both slots hold the same rows and take the key
-//               tiles in turn; their sums are joined at the end.
+//               tiles in turn; their sums are joined at the end.  With 64 or 32
+//               rows or fewer the accumulator holds 2 or 4 copies of them, and each
+//               copy's warps take the weights of their share of a tile's keys (zero
+//               elsewhere), so that four warps work however few the rows are.
 //
 // Roles: warps 0-3 and 4-7 softmax of slots 0 and 1 (and the loads of Q and the
 // epilogue); warps 8 and 10 issue the MMAs of slots 0 and 1; warp 9 the TMA loads
 // (one box per page and 64 columns); warp 11 guards the values (below); E4M3 adds warps
-// 12-15, which widen codes to fp16 (exact) into the operand ring.
+// 12-15, which widen value codes to fp16 into the operand ring.
 //
 // What a row does not see must not reach it, but a product 0 * NaN would.  In the
 // key tiles that hold masked positions the guard warp zeroes the rows past the
 // end and every value that is not finite, and note that they found one; the
 // epilogue then adds such values to the rows that do see them.
 //
-// E4M3.  Codes are widened to fp16, which holds them; a row's scale goes in as far
-// as fp16 is exact: a key or value row becomes code * 2^d, d = 7 for the tile's
-// largest scale.  q' = q 2^-a in fp16 (a per row, so that |q'| < 2^8: exact for
-// values within 2^-22 of the row's largest); z = S 2^(tile) 2^a scale log2(e).  The
-// value operand's exponent goes into the weights: P = 2^(z - base) 2^(tile - x),
-// where the row's integer x follows the largest 2^(z - base) 2^(value scale) as
-// lazily as base follows z, so that weights fit fp16 whatever the scales are (a
-// tile whose value scales span more than fp16 holds exactly has them applied to
-// its weights key by key).  All of these are powers of two: the sum of the weights
-// does not depend on the values.
+// E4M3.  S = q' k' on the codes themselves, with q' = q 2^-a as two codes, the nearest
+// one and that of the rest (a per row, so that |q'| < 2^8): together they hold the
+// eight bits of a bf16 value down to 2^-10 of the row's largest, and 2^-18 of that
+// below.  z = S 2^(key scale) 2^a scale log2(e).  Value codes are widened to fp16,
+// a row's scale going in as far as fp16 is exact: code * 2^d, d = 7 for the tile's
+// largest scale.  The tile's exponent goes into the weights: P = 2^(z - base)
+// 2^(tile - x), where the row's integer x follows the largest 2^(z - base) 2^(value
+// scale) as lazily as base follows z, so that weights fit fp16 whatever the scales
+// are (a tile whose value scales span more than fp16 holds exactly has them applied
+// to its weights key by key).  All of these are powers of two: the sum of the
+// weights does not depend on the values.
 #include <type_traits>
 
 #include "attention.cuh"
@@ -58,9 +62,8 @@ constexpr int kCapE4M3 = 14;     // ... and x moves before one reaches 2^15
 constexpr int kNoShift = -1000;  // no weight yet
 
 // Barriers and small state, behind the operand rings in dynamic shared memory.
-struct TileScale {
-    float key;      // E4M3: what a key tile's scores are multiplied by
-    int32_t value;  // binary exponent of its value operand
+struct TileScale {  // E4M3
+    int32_t value;  // binary exponent of a tile's value operand
     int32_t wide;   // bare value codes: scales per key
 };
 struct Piece;
@@ -79,13 +82,16 @@ struct Shared {
     StartScratch start;
 };
 struct SharedE4M3 : Shared {
-    uint64_t raw_full[6], raw_empty[6];      // code ring
-    uint64_t sc_full[4];                     // scales of a key tile
+    uint64_t kraw_full[4], kraw_empty[4];    // key codes, as the MMAs read them
+    uint64_t vraw_full[4], vraw_empty[4];    // value codes, to be widened
+    uint64_t ex_full[4], ex_empty[4];        // exponent bytes of a tile
+    uint64_t sc_full[4];                     // scales of a tile, from the widening warps
     TileScale scale[4];
-    int reduce[2][4][3];
+    int reduce[2][4][2];
     float qmul[2][kRowBlock];                // 2^a scale log2(e) of a row, by piece parity
     int8_t vexp[4][kTile];                   // value exponents of 4 tiles
-    alignas(16) uint8_t exps[6][2][kTile];   // exponent bytes as copied, by the keys' code-ring slot
+    alignas(16) float kmul[4][kTile];        // 2^ke of the keys of 4 tiles
+    alignas(16) uint8_t exps[4][2][kTile];   // exponent bytes as copied
 };
 
 template <int kD, bool kE4M3> struct Cfg {
@@ -93,13 +99,18 @@ template <int kD, bool kE4M3> struct Cfg {
     static constexpr int kHalves = kD / 64;            // 128-byte column blocks of a 16-bit tile
     static constexpr int kTileBytes = kTile * kD * 2;  // a 16-bit operand tile
     static constexpr int kRawBytes = kTile * kD;       // E4M3 codes of a tile
-    static constexpr int kStages = kE4M3 ? 3 : (kD == 128 ? 5 : 8);
-    static constexpr int kRaw = kE4M3 ? (kD == 128 ? 3 : 6) : 0;
+    // operand ring: keys and values in turn, or (E4M3) widened values alone
+    static constexpr int kStages = kE4M3 ? (kD == 128 ? 2 : 4) : (kD == 128 ? 5 : 8);
+    static constexpr int kKRaw = kE4M3 ? (kD == 128 ? 3 : 4) : 0, kVRaw = kE4M3 ? (kD == 128 ? 2 : 4) : 0;
+    static constexpr int kRaw = kKRaw + kVRaw;
     static constexpr int kThreads = kE4M3 ? 512 : 384;
     // registers: softmax warps take what the others give back
     static constexpr int kRegsMany = kE4M3 ? 192 : 216, kRegsFew = kE4M3 ? 64 : 72;
+    // alternate: (base, sum, 2^x) of 2 x 128 accumulator rows and 128 reciprocal sums; head_dim
+    // 128 has room for them in the second query tile, which that mode leaves unused
+    static constexpr int kStatBytes = kD == 128 ? 0 : 7 * kTile * 4;
     static constexpr int kSmem =
-        2 * kTileBytes + kStages * kTileBytes + kRaw * kRawBytes + (int)sizeof(Sh) + 1024;
+        2 * kTileBytes + kStages * kTileBytes + kRaw * kRawBytes + (int)sizeof(Sh) + kStatBytes + 1024;
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -130,6 +141,16 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b_des
         "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// D (+)= A * B, E4M3 codes from shared memory (K = 32 a step).
+__device__ __forceinline__ void tc_mma_f8(uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
 // kind::f16 instruction descriptor: bf16 or fp16 operands, fp32 accumulator,
 // M = 128; b_mn: B is MN-major.
 __host__ __device__ constexpr uint32_t idesc16(bool f16, int n, bool b_mn) {
@@ -144,6 +165,10 @@ __host__ __device__ constexpr uint32_t idesc16(bool f16, int n, bool b_mn) {
 constexpr uint32_t kKMajorHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 constexpr uint32_t kKMajorLo = 1u << 16;  // leading offset, unused with a swizzle
 constexpr uint32_t kMnMajorHi = kKMajorHi;
+// K-major codes: rows of 128 bytes as above, or of 64 bytes with the 64-byte swizzle
+// (8-row groups 512 bytes apart).
+template <int kD>
+constexpr uint32_t kCodesHi = kD == 128 ? kKMajorHi : (512u >> 4) | (1u << 14) | (4u << 29);
 constexpr uint32_t kMnMajorLo = (uint32_t)((kTile * 128) >> 4) << 16;
 __device__ __forceinline__ uint32_t desc_lo(uint32_t smem_addr) { return (smem_addr & 0x3FFFFu) >> 4; }
 __device__ __forceinline__ uint64_t desc64(uint32_t lo, uint32_t hi) {
@@ -432,20 +457,14 @@ __device__ __forceinline__ uint32_t below(int32_t first, int32_t end) {
     return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
 }
 
-// The positions of key tile `tile` that token i of the request sees.
+// The positions first .. first + 31 that token i of the request sees.
 template <bool kPaged>
-__device__ __forceinline__ void seen_bits(const Params &p, const Request &rq, int32_t i,
-                                          int32_t tile, uint32_t (&w)[4]) {
+__device__ __forceinline__ uint32_t seen_bits(const Params &p, const Request &rq, int32_t i, int32_t first) {
     const bool tree = kPaged && p.tree_mask;
-    const int32_t end = min(rq.len, tree ? rq.len : rq.ctx + i + 1);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int32_t first = tile * kTile + 32 * k;
-        w[k] = below(first, end);
-        if (tree && w[k])
-            w[k] &= tree_bits(p.tree_mask + (int64_t)(rq.t0 + i) * p.mask_words, p.mask_words,
-                              first - rq.ctx);
-    }
+    uint32_t w = below(first, min(rq.len, tree ? rq.len : rq.ctx + i + 1));
+    if (tree && w)
+        w &= tree_bits(p.tree_mask + (int64_t)(rq.t0 + i) * p.mask_words, p.mask_words, first - rq.ctx);
+    return w;
 }
 
 // Values of the keys [l0, l1) that token i of the request sees and that are not
@@ -485,16 +504,16 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
               const __grid_constant__ CUtensorMap vmap) {
     using C = Cfg<kD, kE4M3>;
     constexpr int kStages = C::kStages;
-    constexpr int kRaw = kE4M3 ? C::kRaw : 1;
     extern __shared__ uint8_t dyn[];
     const uint32_t pad = (0u - smem_u32(dyn)) & 1023u;
     const uint32_t sm_q = smem_u32(dyn) + pad;
     const uint32_t sm_ring = sm_q + 2 * C::kTileBytes;
-    const uint32_t sm_raw = sm_ring + kStages * C::kTileBytes;
-    auto &sh = *reinterpret_cast<typename C::Sh *>(
-        dyn + pad + (2 + kStages) * C::kTileBytes + C::kRaw * C::kRawBytes);
-    // alternate: each slot's (base, sum, 2^x) per row, in the second query tile, which that mode leaves unused
-    float *stat = reinterpret_cast<float *>(dyn + pad + C::kTileBytes);
+    const uint32_t sm_kraw = sm_ring + kStages * C::kTileBytes;
+    const uint32_t sm_vraw = sm_kraw + C::kKRaw * C::kRawBytes;
+    uint8_t *tail = dyn + pad + (2 + kStages) * C::kTileBytes + C::kRaw * C::kRawBytes;
+    auto &sh = *reinterpret_cast<typename C::Sh *>(tail);
+    float *stat = reinterpret_cast<float *>(C::kStatBytes ? tail + sizeof(typename C::Sh)
+                                                          : dyn + pad + C::kTileBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -503,11 +522,15 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
             mbar_init(&sh.empty[i], 2);
         }
         if constexpr (kE4M3) {
-            for (int i = 0; i < kRaw; ++i) {
-                mbar_init(&sh.raw_full[i], 1);
-                mbar_init(&sh.raw_empty[i], 4);
+            for (int i = 0; i < 4; ++i) {
+                mbar_init(&sh.kraw_full[i], 1);
+                mbar_init(&sh.kraw_empty[i], 2);
+                mbar_init(&sh.vraw_full[i], 1);
+                mbar_init(&sh.vraw_empty[i], 4);
+                mbar_init(&sh.ex_full[i], 1);
+                mbar_init(&sh.ex_empty[i], 2);
+                mbar_init(&sh.sc_full[i], 1);
             }
-            for (int i = 0; i < 4; ++i) mbar_init(&sh.sc_full[i], 1);
         }
         for (int i = 0; i < 8; ++i) {
             mbar_init(&sh.guard_go[i], 1);
@@ -565,26 +588,14 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
         regs_give<C::kRegsFew>();
         if (warp == 9) {
             // ---- producer: the pieces, and the TMA copies by one thread ----
-            constexpr uint32_t kSlots = kE4M3 ? kRaw : kStages;
             constexpr int kMaxBox = kPaged ? kTile / 16 : 1;
             uint32_t pos = 0, n_piece = 0;  // operand tiles issued
+            uint32_t n_key = 0, n_value = 0;
             bool ok = true, bad_page = false;
             const int32_t rows_box = kPaged ? min(p.page_size, kTile) : kTile;
             const int32_t n_box = kTile / rows_box;
             const int32_t shift = kPaged ? 31 - __clz(p.page_size) : 0;
             Piece pc{};
-            auto full_bar = [&](uint32_t s) -> uint64_t * {
-                if constexpr (kE4M3)
-                    return &sh.raw_full[s];
-                else
-                    return &sh.full[s];
-            };
-            auto empty_bar = [&](uint32_t s) -> uint64_t * {
-                if constexpr (kE4M3)
-                    return &sh.raw_empty[s];
-                else
-                    return &sh.empty[s];
-            };
             // pages of a key tile's boxes (-1: past the end, a box of zeros)
             struct Pages {
                 int32_t id[kMaxBox];
@@ -601,18 +612,34 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                 return g;
             };
             auto load = [&](int32_t tile, const Pages &g, bool values) {
-                const uint32_t s = pos % kSlots, ph = (pos / kSlots) & 1u;
-                uint64_t *fullb = full_bar(s);
-                if (!bar_wait(empty_bar(s), ph ^ 1u, abort_flag, p.err)) return false;
-                constexpr uint32_t kBytes = kE4M3 ? C::kRawBytes : C::kTileBytes;
-                const bool with_exps = kE4M3 && !values;
-                mbar_arrive_expect_tx(fullb, kBytes + (with_exps ? 2 * kTile : 0));
+                uint64_t *fullb;
+                uint32_t dst;
+                [[maybe_unused]] const uint32_t ex = n_key & 3u;
+                if constexpr (kE4M3) {
+                    const uint32_t n = values ? n_value : n_key, slots = values ? C::kVRaw : C::kKRaw;
+                    const uint32_t s = n % slots, ph = ((n / slots) & 1u) ^ 1u;
+                    fullb = values ? &sh.vraw_full[s] : &sh.kraw_full[s];
+                    dst = (values ? sm_vraw : sm_kraw) + s * C::kRawBytes;
+                    if (!bar_wait(values ? &sh.vraw_empty[s] : &sh.kraw_empty[s], ph, abort_flag, p.err))
+                        return false;
+                    if (!values) {
+                        if (!bar_wait(&sh.ex_empty[ex], ((n_key >> 2) & 1u) ^ 1u, abort_flag, p.err)) return false;
+                        mbar_arrive_expect_tx(&sh.ex_full[ex], 2 * kTile);
+                    }
+                    mbar_arrive_expect_tx(fullb, C::kRawBytes);
+                } else {
+                    const uint32_t s = pos % kStages;
+                    fullb = &sh.full[s];
+                    dst = sm_ring + s * C::kTileBytes;
+                    if (!bar_wait(&sh.empty[s], ((pos / kStages) & 1u) ^ 1u, abort_flag, p.err)) return false;
+                    mbar_arrive_expect_tx(fullb, C::kTileBytes);
+                }
                 const CUtensorMap *map = values ? &vmap : &kmap;
                 if constexpr (!kPaged) {
 #pragma unroll
                     for (int half = 0; half < C::kHalves; ++half)
-                        tma_load_3d(sm_ring + s * C::kTileBytes + half * (kTile * 128), map, fullb, 64 * half,
-                                    pc.h, pc.rq.t0 + tile * kTile);
+                        tma_load_3d(dst + half * (kTile * 128), map, fullb, 64 * half, pc.h,
+                                    pc.rq.t0 + tile * kTile);
                 } else {
                     const int32_t y = (tile * kTile) & (p.page_size - 1) & ~(kTile - 1);
 #pragma unroll
@@ -623,21 +650,25 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                         if (live && !good) bad_page = true;
                         const int32_t z = good ? g.id[i] * p.kv_heads + pc.h : -1;
                         if constexpr (kE4M3) {
-                            tma_load_3d(sm_raw + s * C::kRawBytes + i * rows_box * kD, map, fullb, 0, y, z);
-                            if (with_exps) {  // page 0's where there is none: any scale serves zero rows
+                            tma_load_3d(dst + i * rows_box * kD, map, fullb, 0, y, z);
+                            if (!values) {  // page 0's where there is none: any scale serves zero rows
                                 const int64_t at =
                                     ((int64_t)(good ? g.id[i] : 0) * p.kv_heads + pc.h) * p.page_size + y;
-                                bulk_load(smem_u32(&sh.exps[s][0][i * rows_box]), p.k_exp + at, rows_box, fullb);
-                                bulk_load(smem_u32(&sh.exps[s][1][i * rows_box]), p.v_exp + at, rows_box, fullb);
+                                bulk_load(smem_u32(&sh.exps[ex][0][i * rows_box]), p.k_exp + at, rows_box,
+                                          &sh.ex_full[ex]);
+                                bulk_load(smem_u32(&sh.exps[ex][1][i * rows_box]), p.v_exp + at, rows_box,
+                                          &sh.ex_full[ex]);
                             }
                         } else {
-                            const uint32_t dst = sm_ring + s * C::kTileBytes + i * rows_box * 128;
 #pragma unroll
                             for (int half = 0; half < C::kHalves; ++half)
-                                tma_load_3d(dst + half * (kTile * 128), map, fullb, 64 * half, y, z);
+                                tma_load_3d(dst + half * (kTile * 128) + i * rows_box * 128, map, fullb, 64 * half,
+                                            y, z);
                         }
                     }
                 }
+                n_key += !values;
+                n_value += values;
                 ++pos;
                 return true;
             };
@@ -699,10 +730,19 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
             if ((bad_page || (!kPaged && bad && blockIdx.x == 0)) && p.err)
                 atomicOr(p.err, DFLASH2_DEVERR_ID_RANGE);
             if (!ok) {  // wait for the copies in flight before the shared memory goes
-                for (uint32_t n = pos > kSlots ? pos - kSlots : 0; n < pos; ++n) {
-                    const uint64_t t0 = global_timer_ns();
-                    while (!mbar_try_wait(full_bar(n % kSlots), (n / kSlots) & 1u))
-                        if (global_timer_ns() - t0 > kWaitLimitNs) break;
+                auto drain = [&](uint64_t *bars, uint32_t issued, uint32_t slots) {
+                    for (uint32_t n = issued > slots ? issued - slots : 0; n < issued; ++n) {
+                        const uint64_t t0 = global_timer_ns();
+                        while (!mbar_try_wait(bars + n % slots, (n / slots) & 1u))
+                            if (global_timer_ns() - t0 > kWaitLimitNs) break;
+                    }
+                };
+                if constexpr (kE4M3) {
+                    drain(sh.kraw_full, n_key, C::kKRaw);
+                    drain(sh.vraw_full, n_value, C::kVRaw);
+                    drain(sh.ex_full, n_key, 4);
+                } else {
+                    drain(sh.full, pos, kStages);
                 }
             }
         } else if (warp == 8 || warp == 10) {
@@ -712,38 +752,53 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
             // ring in order and hand it back (an operand is free when both have).
             if (elect_one()) {
                 const int s = warp == 8 ? 0 : 1;
-                constexpr uint32_t kIdS = idesc16(kE4M3, kTile, false);
+                constexpr uint32_t kIdS = kE4M3 ? idesc_e4m3(kTile, kTile) : idesc16(false, kTile, false);
                 constexpr uint32_t kIdO = idesc16(kE4M3, kD, true);
                 const uint32_t dS = s * kTile, dO = 256 + s * kD;
-                uint32_t pos = 0, n_piece = 0, n_guard = 0, n_p = 0;
+                uint32_t pos = 0, tiles_done = 0, n_piece = 0, n_guard = 0, n_p = 0;
                 bool ok = true;
                 Piece pc{};
-                auto wait_ring = [&](uint32_t n) {
-                    return bar_wait(&sh.full[n % kStages], (n / kStages) & 1u, abort_flag, p.err);
+                // an operand's place: bf16, operand n of the ring; E4M3, by key tile
+                struct Place {
+                    uint64_t *full, *empty;
+                    uint32_t phase, addr;
                 };
-                // scores of key operand n (mine), or the other slot's operand handed back
-                auto keys = [&](uint32_t n, bool mine, bool q1) {
-                    if (!wait_ring(n)) return false;
+                auto ring = [&](uint32_t n) {
+                    const uint32_t i = n % kStages;
+                    return Place{&sh.full[i], &sh.empty[i], (n / kStages) & 1u, sm_ring + i * C::kTileBytes};
+                };
+                // scores of a key operand (mine), or the other slot's operand handed back
+                auto keys = [&](const Place &o, bool mine, bool q1) {
+                    if (!bar_wait(o.full, o.phase, abort_flag, p.err)) return false;
                     if (!mine) {
-                        mbar_arrive(&sh.empty[n % kStages]);
+                        mbar_arrive(o.empty);
                         return true;
                     }
-                    const uint32_t kd = desc_lo(sm_ring + (n % kStages) * C::kTileBytes) | kKMajorLo;
+                    const uint32_t kd = desc_lo(o.addr) | kKMajorLo;
                     const uint32_t qd = desc_lo(sm_q + (q1 ? C::kTileBytes : 0)) | kKMajorLo;
                     tc_fence_after();
+                    if constexpr (kE4M3) {  // both parts of Q, one after the other
 #pragma unroll
-                    for (int k = 0; k < kD / 16; ++k) {
-                        const uint32_t off = (k >> 2) * ((kTile * 128) >> 4) + (k & 3) * 2;
-                        tc_mma_bf16(dS, desc64(qd + off, kKMajorHi), desc64(kd + off, kKMajorHi), kIdS, k > 0);
+                        for (int k = 0; k < 2 * (kD / 32); ++k) {
+                            const uint32_t off = (k % (kD / 32)) * 2;
+                            tc_mma_f8(dS, desc64(qd + (k >= kD / 32 ? C::kRawBytes >> 4 : 0) + off, kCodesHi<kD>),
+                                      desc64(kd + off, kCodesHi<kD>), kIdS, k > 0);
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < kD / 16; ++k) {
+                            const uint32_t off = (k >> 2) * ((kTile * 128) >> 4) + (k & 3) * 2;
+                            tc_mma_bf16(dS, desc64(qd + off, kKMajorHi), desc64(kd + off, kKMajorHi), kIdS, k > 0);
+                        }
                     }
                     tc_commit(&sh.s_full[s]);
-                    tc_commit(&sh.empty[n % kStages]);
+                    tc_commit(o.empty);
                     return true;
                 };
-                // sums over value operand n, of key tile t; issuer 0 hands guarded ones to
+                // sums over the value operand of key tile t; issuer 0 hands guarded ones to
                 // the guard warp
-                auto values = [&](int32_t t, uint32_t n, bool mine, bool acc, bool last) {
-                    if (!wait_ring(n)) return false;
+                auto values = [&](int32_t t, const Place &o, bool mine, bool acc, bool last) {
+                    if (!bar_wait(o.full, o.phase, abort_flag, p.err)) return false;
                     if (!kE4M3 && t >= pc.guard_from) {
                         if (s == 0) mbar_arrive(&sh.guard_go[n_guard & 7u]);
                         if (mine &&
@@ -751,11 +806,13 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                             return false;
                         ++n_guard;
                     }
+                    [[maybe_unused]] const uint32_t ex = (tiles_done + (uint32_t)(t - pc.t0)) & 3u;
                     if (!mine) {
-                        mbar_arrive(&sh.empty[n % kStages]);
+                        mbar_arrive(o.empty);
+                        if constexpr (kE4M3) mbar_arrive(&sh.ex_empty[ex]);
                         return true;
                     }
-                    const uint32_t vd = desc_lo(sm_ring + (n % kStages) * C::kTileBytes) | kMnMajorLo;
+                    const uint32_t vd = desc_lo(o.addr) | kMnMajorLo;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         if (!bar_wait(&sh.p_full[s][h], n_p & 1u, abort_flag, p.err)) return false;
@@ -766,7 +823,8 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                                       acc || k > 0);
                     }
                     ++n_p;
-                    tc_commit(&sh.empty[n % kStages]);
+                    tc_commit(o.empty);
+                    if constexpr (kE4M3) tc_commit(&sh.ex_empty[ex]);
                     if (last) tc_commit(&sh.o_full[s]);
                     return true;
                 };
@@ -782,17 +840,25 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                         // key j (shared) or j + 1 (alternate), then value j
                         const int32_t jk = both ? j : j + 1;
                         if (jk < n) {
-                            const uint32_t nk = pos + (both ? 2 * jk : jk == 0 ? 0 : 2 * jk - 1);
-                            // shared: S(j) follows V(j - 1), which the loop order gives
-                            ok = keys(nk, both ? jk < n_mine : (jk & 1) == s, both && s == 1);
+                            Place o;
+                            if constexpr (kE4M3) {
+                                const uint32_t kt = tiles_done + jk, i = kt % C::kKRaw;
+                                o = Place{&sh.kraw_full[i], &sh.kraw_empty[i], (kt / C::kKRaw) & 1u,
+                                          sm_kraw + i * C::kRawBytes};
+                            } else {
+                                o = ring(pos + (both ? 2 * jk : jk == 0 ? 0 : 2 * jk - 1));
+                            }
+                            ok = keys(o, both ? jk < n_mine : (jk & 1) == s, both && s == 1);
                         }
                         if (ok && j >= 0) {
-                            const uint32_t nv = pos + (both ? 2 * j + 1 : j + 1 < n ? 2 * j + 2 : 2 * n - 1);
+                            const Place o = ring(kE4M3 ? tiles_done + j
+                                                       : pos + (both ? 2 * j + 1 : j + 1 < n ? 2 * j + 2 : 2 * n - 1));
                             const bool mine = both ? j < n_mine : (j & 1) == s;
-                            ok = values(pc.t0 + j, nv, mine, both ? j > 0 : j >= 2,
+                            ok = values(pc.t0 + j, o, mine, both ? j > 0 : j >= 2,
                                         both ? j + 1 == n_mine : j + 2 >= n);
                         }
                     }
+                    tiles_done += n;
                     pos += 2 * n;
                 }
                 // nothing of this slot's is in flight when the accumulators are freed
@@ -858,57 +924,55 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
             }
         }
     } else if (warp >= 12) {
-        // ---- E4M3: codes to fp16, relative to the tile's largest scale ----
-        // A key or value row becomes code * 2^d with d = 7 for the tile's largest scale,
-        // exact for d >= -15.  A tile whose value scales span more than 22 binades
-        // ("wide") keeps bare codes, and the softmax applies the scales key by key.
+        // ---- E4M3: value codes to fp16, relative to the tile's largest scale ----
+        // A value row becomes code * 2^d with d = 7 for the tile's largest scale, exact for
+        // d >= -15.  A tile whose value scales span more than 22 binades ("wide") keeps bare
+        // codes, and the softmax applies the scales key by key.
         regs_give<C::kRegsFew>();
         if constexpr (kE4M3) {
-            uint32_t pos = 0, n_piece = 0, tiles_done = 0;
+            uint32_t n_piece = 0, tiles_done = 0;
             bool ok = true;
             const int row = threadIdx.x - 384;
             Piece pc{};
-            uint32_t mul_k = 0, mul_v0 = 0, mul_v1 = 0;  // half2 factors of this row: key, values of two tiles
-            auto widen = [&](int32_t tile, uint32_t tile_no, bool values) {
-                const uint32_t rs = pos % kRaw, s = pos % kStages;
+            uint32_t mul0 = 0, mul1 = 0;  // half2 factors of this row in an even and an odd tile
+            // the scales of key tile number `no`
+            auto scales = [&](int32_t tile, uint32_t no) {
+                const uint32_t i = no & 3u;
                 const bool live = tile * kTile + row < pc.rq.len;
-                if (!bar_wait(&sh.raw_full[rs], (pos / kRaw) & 1u, abort_flag, p.err)) return false;
-                if (!values) {
-                    // written exponents lie in [-48, 48]; what was never written is masked
-                    const int ke = min(max((int)sh.exps[rs][0][row] - 127, -48), 48);
-                    const int ve = min(max((int)sh.exps[rs][1][row] - 127, -48), 48);
-                    const int kt = __reduce_max_sync(0xFFFFFFFFu, live ? ke : -64);
-                    const int vt = __reduce_max_sync(0xFFFFFFFFu, live ? ve : -64);
-                    const int vb = __reduce_min_sync(0xFFFFFFFFu, live ? ve : 64);
-                    int *red = sh.reduce[tile_no & 1u][warp - 12];
-                    if (lane == 0) red[0] = kt, red[1] = vt, red[2] = vb;
-                    sh.vexp[tile_no & 3u][row] = (int8_t)ve;
-                    named_sync<2, 128>();
-                    int k_top = -64, v_top = -64, v_low = 64;
+                if (!bar_wait(&sh.ex_full[i], (no >> 2) & 1u, abort_flag, p.err)) return false;
+                // written exponents lie in [-48, 48]; what was never written is masked
+                const int ke = min(max((int)sh.exps[i][0][row] - 127, -48), 48);
+                const int ve = min(max((int)sh.exps[i][1][row] - 127, -48), 48);
+                const int vt = __reduce_max_sync(0xFFFFFFFFu, live ? ve : -64);
+                const int vb = __reduce_min_sync(0xFFFFFFFFu, live ? ve : 64);
+                int *red = sh.reduce[no & 1u][warp - 12];
+                if (lane == 0) red[0] = vt, red[1] = vb;
+                sh.kmul[i][row] = pow2_int(ke);
+                sh.vexp[i][row] = (int8_t)ve;
+                named_sync<2, 128>();
+                int v_top = -64, v_low = 64;
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        k_top = max(k_top, sh.reduce[tile_no & 1u][w][0]);
-                        v_top = max(v_top, sh.reduce[tile_no & 1u][w][1]);
-                        v_low = min(v_low, sh.reduce[tile_no & 1u][w][2]);
-                    }
-                    const bool wide = v_top - v_low > 22 && v_top > -64;
-                    if (row == 0) {
-                        sh.scale[tile_no & 3u].key = __uint_as_float((uint32_t)(k_top - 7 + 127) << 23);
-                        sh.scale[tile_no & 3u].value = v_top - 7;
-                        sh.scale[tile_no & 3u].wide = wide;
-                        mbar_arrive(&sh.sc_full[tile_no & 3u]);
-                    }
-                    auto factor = [](int d) {
-                        const __half2 h = __half2half2(__float2half_rn(pow2_int(max(d, -24))));
-                        return *reinterpret_cast<const uint32_t *>(&h);
-                    };
-                    mul_k = factor(live ? ke - k_top + 7 : 0);
-                    (tile_no & 1u ? mul_v1 : mul_v0) = factor(wide || !live ? 0 : ve - v_top + 7);
+                for (int w = 0; w < 4; ++w) {
+                    v_top = max(v_top, sh.reduce[no & 1u][w][0]);
+                    v_low = min(v_low, sh.reduce[no & 1u][w][1]);
                 }
-                const uint32_t mul = !values ? mul_k : tile_no & 1u ? mul_v1 : mul_v0;
-                const uint32_t src = sm_raw + rs * C::kRawBytes + row * kD;
+                const bool wide = v_top - v_low > 22 && v_top > -64;
+                if (row == 0) {
+                    sh.scale[i].value = v_top - 7;
+                    sh.scale[i].wide = wide;
+                    mbar_arrive(&sh.sc_full[i]);
+                }
+                const __half2 h = __half2half2(__float2half_rn(pow2_int(wide || !live ? 0 : max(ve - v_top + 7, -24))));
+                (no & 1u ? mul1 : mul0) = *reinterpret_cast<const uint32_t *>(&h);
+                return true;
+            };
+            auto widen = [&](int32_t tile, uint32_t no) {
+                const uint32_t rs = no % C::kVRaw, s = no % kStages;
+                const bool live = tile * kTile + row < pc.rq.len;
+                const uint32_t mul = no & 1u ? mul1 : mul0;
+                const uint32_t src = sm_vraw + rs * C::kRawBytes + row * kD;
                 const uint32_t dst = sm_ring + s * C::kTileBytes + row * 128;
-                const bool guarded = values && tile >= pc.guard_from;
+                if (!bar_wait(&sh.vraw_full[rs], (no / C::kVRaw) & 1u, abort_flag, p.err)) return false;
                 uint32_t w[kD / 16][4];  // 16 codes a chunk; the copy's swizzle spreads the rows over the banks
 #pragma unroll
                 for (int c = 0; c < kD / 16; ++c) {
@@ -917,7 +981,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                                  : "=r"(w[c][0]), "=r"(w[c][1]), "=r"(w[c][2]), "=r"(w[c][3])
                                  : "r"(a));
                 }
-                if (values && (guarded || !live)) {
+                if (tile >= pc.guard_from || !live) {
                     bool found = false;
 #pragma unroll
                     for (int c = 0; c < kD / 16; ++c)
@@ -930,8 +994,8 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                     if (found) *(volatile int *)&sh.poison = (int)n_piece;
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.raw_empty[rs]);
-                if (!bar_wait(&sh.empty[s], ((pos / kStages) & 1u) ^ 1u, abort_flag, p.err)) return false;
+                if (lane == 0) mbar_arrive(&sh.vraw_empty[rs]);
+                if (!bar_wait(&sh.empty[s], ((no / kStages) & 1u) ^ 1u, abort_flag, p.err)) return false;
                 const __half2 m2 = *reinterpret_cast<const __half2 *>(&mul);
 #pragma unroll
                 for (int c = 0; c < kD / 16; ++c) {
@@ -955,17 +1019,15 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.full[s]);
-                ++pos;
                 return true;
             };
             while (ok && take_piece(n_piece, &pc, true)) {
-                // operands in the ring's order: shared K0 V0 K1 V1 ..., alternate K0 K1 V0 K2 V1 ...
+                // in the copies' order: alternate scales a tile ahead of its values
                 const int32_t n = pc.t1 - pc.t0, lead = pc.shared() ? 0 : 1;
-                int32_t jk = 0, jv = 0;
-                for (int32_t i = 0; ok && i < 2 * n; ++i) {
-                    const bool values = jk == n || jk - jv > lead;
-                    const int32_t j = values ? jv++ : jk++;
-                    ok = widen(pc.t0 + j, tiles_done + j, values);
+                int32_t jk = 0;
+                for (int32_t j = 0; ok && j < n; ++j) {
+                    for (; ok && jk < n && jk <= j + lead; ++jk) ok = scales(pc.t0 + jk, tiles_done + jk);
+                    ok = ok && widen(pc.t0 + j, tiles_done + j);
                 }
                 tiles_done += n;
                 ++n_piece;
@@ -976,7 +1038,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
         regs_take<C::kRegsMany>();
         const int s = warp >> 2;
         const int wq = warp & 3;
-        const int my = wq * 32 + lane;  // row within the slot
+        const int my = wq * 32 + lane;  // accumulator row
         const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
         const uint32_t tS = s * kTile + lane_base;
         const uint32_t tO = 256 + s * kD + lane_base;
@@ -988,6 +1050,9 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
         Piece pc{};
         while (ok && take_piece(n_piece, &pc, true)) {
             const bool both = pc.shared();
+            // few rows: `copies` copies of them in the accumulator's rows, one per 128 /
+            // copies, each with its share of the tile's keys (log2 of the copies)
+            const int split = !kPaged || pc.n_rows > 64 ? 0 : pc.n_rows > 32 ? 1 : 2;
             // queries: kD / 8 lanes hold a row, 8 values each; eight rows in flight per thread
             {
                 constexpr int kLanes = kD / 8, kStep = 256 / kLanes;
@@ -1010,7 +1075,8 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int r = rb + i * kStep;
-                        uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                        if (r >= pc.n_rows) break;
+                        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
                         if constexpr (kE4M3) {
                             float f[8], amax = 0.0f;
 #pragma unroll
@@ -1024,21 +1090,45 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                                 amax = fmaxf(amax, __shfl_xor_sync(row_lanes, amax, o));
                             // 2^-a: the largest magnitude's binade becomes 2^7
                             const int a = min(max((int)(__float_as_uint(amax) >> 23) - 127 - 7, -110), 110);
-                            const float down = __uint_as_float((uint32_t)(127 - a) << 23);
+                            // an infinite value makes the row NaN: codes hold no infinity
+                            const float down =
+                                amax <= 3.4e38f ? __uint_as_float((uint32_t)(127 - a) << 23) : __int_as_float(0x7FC00000);
+                            uint32_t hi[2], lo[2];
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                w[k] = pack16<true>(f[2 * k] * down, f[2 * k + 1] * down);
-                            if (l8 == 0 && r < pc.n_rows)
+                            for (int k = 0; k < 4; ++k) {
+                                const float2 y = make_float2(f[2 * k] * down, f[2 * k + 1] * down);
+                                const uint32_t ch = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+                                const float2 back = __half22float2(
+                                    __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)ch, __NV_E4M3)));
+                                const uint32_t cl = __nv_cvt_float2_to_fp8x2(
+                                    make_float2(y.x - back.x, y.y - back.y), __NV_SATFINITE, __NV_E4M3);
+                                hi[k >> 1] = (k & 1) ? hi[k >> 1] | (ch << 16) : ch;
+                                lo[k >> 1] = (k & 1) ? lo[k >> 1] | (cl << 16) : cl;
+                            }
+                            if (l8 == 0)
                                 sh.qmul[n_piece & 1u][r] =
                                     fmaxf(__uint_as_float((uint32_t)(127 + a) << 23) * mul, 1.1754944e-38f);
+                            for (int k = 0; k < (1 << split); ++k) {
+                                const int row = (r & 127) + (k << (7 - split));
+                                const int c = kD == 128 ? (l8 >> 1) ^ (row & 7) : (l8 >> 1) ^ ((row >> 1) & 3);
+                                const uint32_t dst =
+                                    sm_q + (r >> 7) * C::kTileBytes + row * kD + (c << 4) + ((l8 & 1) << 3);
+                                asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(dst), "r"(hi[0]), "r"(hi[1])
+                                             : "memory");
+                                asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(dst + C::kRawBytes), "r"(lo[0]),
+                                             "r"(lo[1])
+                                             : "memory");
+                            }
+                        } else {
+                            for (int k = 0; k < (1 << split); ++k) {
+                                const int row = (r & 127) + (k << (7 - split));
+                                const uint32_t dst = sm_q + (r >> 7) * C::kTileBytes + (l8 >> 3) * (kTile * 128) +
+                                                     row * 128 + (((l8 & 7) ^ (row & 7)) << 4);
+                                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[0]),
+                                             "r"(w[1]), "r"(w[2]), "r"(w[3])
+                                             : "memory");
+                            }
                         }
-                        const int c = l8 & 7, half = l8 >> 3;
-                        const uint32_t dst = sm_q + (r >> 7) * C::kTileBytes + half * (kTile * 128) +
-                                             (r & 127) * 128 + ((c ^ (r & 7)) << 4);
-                        if (r < pc.n_rows)
-                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[0]),
-                                         "r"(w[1]), "r"(w[2]), "r"(w[3])
-                                         : "memory");
                     }
                 }
                 fence_proxy_async_smem();
@@ -1046,13 +1136,14 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                 if (lane == 0) mbar_arrive(&sh.q_full);
                 if constexpr (kE4M3) named_sync<1, 256>();  // the rows' scales
             }
-            const int32_t r_blk = (both ? s * kTile : 0) + my;  // row within the block
+            const int copy = my >> (7 - split);
+            const int r_blk = (both ? s * kTile : 0) + my - (copy << (7 - split));  // row within the block
             const uint32_t r_off = pc.rem0 + r_blk, r_tok = (r_off * magic) >> 16;
             const int32_t tok = pc.tok0 + (int32_t)r_tok;
             const bool live_row = r_blk < pc.n_rows;
-            const bool live_warp = (both ? s * kTile : 0) + wq * 32 < pc.n_rows;
-            float qm0 = mul;
-            if constexpr (kE4M3) qm0 = live_row ? sh.qmul[n_piece & 1u][r_blk] : 1.0f;
+            const bool live_warp = (r_blk & ~31) < pc.n_rows;
+            float qm = mul;
+            if constexpr (kE4M3) qm = live_row ? sh.qmul[n_piece & 1u][r_blk] : 1.0f;
             // positions below this one are seen by every row of the slot
             const int32_t all_seen =
                 kPaged ? pc.rq.ctx : pc.tok0 + (int32_t)(((pc.rem0 + (both ? s * kTile : 0)) * magic) >> 16) + 1;
@@ -1060,43 +1151,52 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
             float base = -INFINITY, sum = 0.0f;
             int x_shift = kNoShift;  // E4M3: x
             bool first = true;
-            for (int32_t t = pc.t0 + (both ? 0 : s); t < t_end; t += both ? 1 : 2) {
-                float qm = qm0;
-                int v_exp = 0;
-                bool wide = false;
-                [[maybe_unused]] const uint32_t tile_no = tiles_done + (uint32_t)(t - pc.t0);
-                if constexpr (kE4M3) {
-                    ok = bar_wait(&sh.sc_full[tile_no & 3u], (tile_no >> 2) & 1u, abort_flag, p.err);
-                    if (!ok) break;
-                    const TileScale ts = sh.scale[tile_no & 3u];
-                    qm *= ts.key;
-                    v_exp = ts.value;
-                    wide = ts.wide;
+            // O and x or base move together: O 2^x 2^base stays
+            auto rescale = [&](float fix) {
+                if (first) return;
+#pragma unroll 1
+                for (int c = 0; c < kD; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + c, o);
+                    tmem_ld_wait();
+                    tmem_tie(o);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fix);
+                    tmem_st32(tO + c, o);
                 }
-                ok = bar_wait(&sh.s_full[s], n_s & 1u, abort_flag, p.err);
-                if (!ok) break;
-                ++n_s;
-                tc_fence_after();
-                if (!live_warp) {
-                    if (lane == 0) {
-                        mbar_arrive(&sh.p_full[s][0]);
-                        mbar_arrive(&sh.p_full[s][1]);
-                    }
-                    continue;
-                }
-                uint32_t x[4][32];
+            };
+            // One key tile: this warp's kC chunks of 32 keys, from chunk c0 on.
+            auto tile = [&](auto chunks, const int c0, const int32_t t, const uint32_t i4) {
+                constexpr int kC = decltype(chunks)::value;
+                uint32_t x[kC][32];
                 const bool masked = (t + 1) * kTile > all_seen;
                 auto scores = [&]() {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, x[c]);
-                    uint32_t w[4] = {0u, 0u, 0u, 0u};
-                    if (masked && live_row) seen_bits<kPaged>(p, pc.rq, tok, t, w);
+                    for (int c = 0; c < kC; ++c) tmem_ld32(tS + 32 * (c0 + c), x[c]);
+                    uint32_t w[kC];
+#pragma unroll
+                    for (int c = 0; c < kC; ++c)
+                        w[c] = masked && live_row ? seen_bits<kPaged>(p, pc.rq, tok, t * kTile + 32 * (c0 + c)) : 0u;
                     tmem_ld_wait();
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_tie(x[c]);
+                    for (int c = 0; c < kC; ++c) tmem_tie(x[c]);
+                    if constexpr (kE4M3) {
+#pragma unroll
+                        for (int c = 0; c < kC; ++c)
+#pragma unroll
+                            for (int k = 0; k < 32; k += 4) {
+                                const ulonglong2 f =
+                                    *reinterpret_cast<const ulonglong2 *>(&sh.kmul[i4][32 * (c0 + c) + k]);
+                                float a, b;
+                                unf2(mul2(f2(x[c][k], x[c][k + 1]), f.x), a, b);
+                                x[c][k] = __float_as_uint(a), x[c][k + 1] = __float_as_uint(b);
+                                unf2(mul2(f2(x[c][k + 2], x[c][k + 3]), f.y), a, b);
+                                x[c][k + 2] = __float_as_uint(a), x[c][k + 3] = __float_as_uint(b);
+                            }
+                    }
                     if (masked) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
+                        for (int c = 0; c < kC; ++c)
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
                                 if (!((w[c] >> k) & 1u)) x[c][k] = 0xFF800000u;  // -inf
@@ -1105,21 +1205,24 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                 uint64_t part[4];
                 const uint64_t qm2 = f2(qm, qm);
                 uint32_t pk[32];
-                // weights of keys 64 h ..: 2^(z - base); E4M3 keeps them in x
-                auto weights = [&](int h, float safe) {
+                // weights of the chunks [from, to): 2^(z - base); E4M3 keeps them in x
+                auto weights = [&](int from, int to, float safe) {
                     const uint64_t off2 = f2(-safe, -safe);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const int c = 2 * h + (k >> 4), e = (2 * k) & 31;
-                        float a, b;
-                        unf2(fma2(f2(x[c][e], x[c][e + 1]), qm2, off2), a, b);
-                        a = ex2(a);
-                        b = ex2(b);
-                        part[k & 3] = add2(part[k & 3], f2(a, b));
-                        if constexpr (kE4M3)
-                            x[c][e] = __float_as_uint(a), x[c][e + 1] = __float_as_uint(b);
-                        else
-                            pk[k] = pack16<false>(a, b);
+                    for (int c = 0; c < kC; ++c) {
+                        if (c < from || c >= to) continue;
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) {
+                            float a, b;
+                            unf2(fma2(f2(x[c][k], x[c][k + 1]), qm2, off2), a, b);
+                            a = ex2(a);
+                            b = ex2(b);
+                            part[(k >> 1) & 3] = add2(part[(k >> 1) & 3], f2(a, b));
+                            if constexpr (kE4M3)
+                                x[c][k] = __float_as_uint(a), x[c][k + 1] = __float_as_uint(b);
+                            else
+                                pk[16 * (c & 1) + (k >> 1)] = pack16<false>(a, b);
+                        }
                     }
                 };
                 auto row_top = [&]() {
@@ -1128,44 +1231,47 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                     for (int k = 0; k < 8; ++k)
                         top[k] = fmaxf(__uint_as_float(x[0][2 * k]), __uint_as_float(x[0][2 * k + 1]));
 #pragma unroll
-                    for (int k = 16; k < 128; k += 2)
+                    for (int k = 16; k < 32 * kC; k += 2)
                         top[(k >> 1) & 7] =
                             fmaxf(fmaxf(top[(k >> 1) & 7], __uint_as_float(x[k >> 5][k & 31])),
                                   __uint_as_float(x[k >> 5][(k & 31) + 1]));
                     return fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])),
                                  fmaxf(fmaxf(top[4], top[5]), fmaxf(top[6], top[7]))) * qm;
                 };
-                // O and x or base move together: O 2^x 2^base stays
-                auto rescale = [&](float fix) {
-                    if (first) return;
-#pragma unroll 1
-                    for (int c = 0; c < kD; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(tO + c, o);
-                        tmem_ld_wait();
-                        tmem_tie(o);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fix);
-                        tmem_st32(tO + c, o);
-                    }
-                };
                 auto hand_over = [&](int h) {
-                    tmem_st32(tS + 32 * h, pk);
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sh.p_full[s][h]);
                 };
+                // few rows: this copy's weights, zeros at the other copies' keys
+                auto store_split = [&]() {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t v[32];
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            if constexpr (kC == 2)
+                                v[k] = c0 == 2 * h ? pk[k] : 0u;
+                            else
+                                v[k] = c0 == 2 * h + (k >> 4) ? pk[k & 15] : 0u;
+                        }
+                        tmem_st32(tS + 32 * h, v);
+                    }
+                    hand_over(0);
+                    if (lane == 0) mbar_arrive(&sh.p_full[s][1]);
+                };
                 if constexpr (!kE4M3) {
-                    // the first half against the base so far, beside the maximum; again,
+                    // the first weights against the base so far, beside the maximum; again,
                     // from the scores in TMEM, where the maximum moved the base (the first
                     // tiles, mostly)
+                    constexpr int kFirst = kC == 4 ? 2 : kC;
 #pragma unroll 1
                     for (bool again = false;;) {
                         scores();
                         const float mx = row_top();
                         part[0] = part[1] = part[2] = part[3] = 0ull;
-                        weights(0, base == -INFINITY ? 0.0f : base);
+                        weights(0, kFirst, base == -INFINITY ? 0.0f : base);
                         if (again) break;
                         const bool grow = mx > base + kLazy;
                         if (!__any_sync(0xFFFFFFFFu, grow)) break;
@@ -1176,9 +1282,15 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                         rescale(fix);
                         again = true;
                     }
-                    hand_over(0);
-                    weights(1, base == -INFINITY ? 0.0f : base);
-                    hand_over(1);
+                    if constexpr (kC == 4) {
+                        tmem_st32(tS, pk);
+                        hand_over(0);
+                        weights(2, 4, base == -INFINITY ? 0.0f : base);
+                        tmem_st32(tS + 32, pk);
+                        hand_over(1);
+                    } else {
+                        store_split();
+                    }
                 } else {
                     scores();
                     const float mx = row_top();
@@ -1190,20 +1302,20 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                     base = nb;
                     sum *= fix;
                     part[0] = part[1] = part[2] = part[3] = 0ull;
-                    weights(0, safe);
-                    weights(1, safe);
+                    weights(0, kC, safe);
                     // binade of the largest weight with its value's scale
+                    const TileScale ts = sh.scale[i4];
+                    int v_exp = ts.value;
                     int level = v_exp + (int)floorf(fmaxf(mx - safe, -4096.0f));
                     bool some = mx > -INFINITY;
-                    if (wide) {
+                    if (ts.wide) {
                         float hi = 0.0f;
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
+                        for (int c = 0; c < kC; ++c)
 #pragma unroll
                             for (int k = 0; k < 32; ++k) {
-                                const float u =
-                                    __uint_as_float(x[c][k]) *
-                                    __uint_as_float((uint32_t)(127 + sh.vexp[tile_no & 3u][32 * c + k]) << 23);
+                                const float u = __uint_as_float(x[c][k]) *
+                                                __uint_as_float((uint32_t)(127 + sh.vexp[i4][32 * (c0 + c) + k]) << 23);
                                 hi = fmaxf(hi, u);
                                 x[c][k] = __float_as_uint(u);
                             }
@@ -1220,24 +1332,62 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                     if (__any_sync(0xFFFFFFFFu, fix != 1.0f)) rescale(had ? fix : 0.0f);
                     const float down = had || some ? pow2_int(v_exp - x_shift) : 1.0f;
                     const uint64_t down2 = f2(down, down);
+                    auto pack = [&](int from) {  // two chunks (kC == 1: one)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
+                        for (int c = 0; c < kC; ++c) {
+                            if (c < from || c >= from + 2) continue;
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            const int c = 2 * h + (k >> 4), e = (2 * k) & 31;
-                            float a, b;
-                            unf2(mul2(f2(x[c][e], x[c][e + 1]), down2), a, b);
-                            pk[k] = pack16<true>(a, b);
+                            for (int k = 0; k < 32; k += 2) {
+                                float a, b;
+                                unf2(mul2(f2(x[c][k], x[c][k + 1]), down2), a, b);
+                                pk[16 * (c & 1) + (k >> 1)] = pack16<true>(a, b);
+                            }
                         }
-                        hand_over(h);
+                    };
+                    pack(0);
+                    if constexpr (kC == 4) {
+                        tmem_st32(tS, pk);
+                        hand_over(0);
+                        pack(2);
+                        tmem_st32(tS + 32, pk);
+                        hand_over(1);
+                    } else {
+                        store_split();
                     }
                 }
-                {
-                    float a, b;
-                    unf2(add2(add2(part[0], part[1]), add2(part[2], part[3])), a, b);
-                    sum += a + b;
-                }
+                float a, b;
+                unf2(add2(add2(part[0], part[1]), add2(part[2], part[3])), a, b);
+                sum += a + b;
                 first = false;
+            };
+            for (int32_t t = pc.t0 + (both ? 0 : s); t < t_end; t += both ? 1 : 2) {
+                const uint32_t tile_no = tiles_done + (uint32_t)(t - pc.t0);
+                if constexpr (kE4M3) {
+                    ok = bar_wait(&sh.sc_full[tile_no & 3u], (tile_no >> 2) & 1u, abort_flag, p.err);
+                    if (!ok) break;
+                }
+                ok = bar_wait(&sh.s_full[s], n_s & 1u, abort_flag, p.err);
+                if (!ok) break;
+                ++n_s;
+                tc_fence_after();
+                if (!live_warp) {
+                    if (lane == 0) {
+                        mbar_arrive(&sh.p_full[s][0]);
+                        mbar_arrive(&sh.p_full[s][1]);
+                    }
+                    continue;
+                }
+                if constexpr (kPaged) {
+                    if (split == 2) {
+                        tile(std::integral_constant<int, 1>{}, copy, t, tile_no & 3u);
+                        continue;
+                    }
+                    if (split == 1) {
+                        tile(std::integral_constant<int, 2>{}, 2 * copy, t, tile_no & 3u);
+                        continue;
+                    }
+                }
+                tile(std::integral_constant<int, 4>{}, 0, t, tile_no & 3u);
             }
             if (!ok) break;
             // ---- epilogue ----
@@ -1245,98 +1395,129 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
             const bool used1 = both || n > 1;
             tiles_done += n;
             const float up = !kE4M3 || x_shift == kNoShift ? 1.0f : pow2_int(x_shift);
-            float f0, f1 = 0.0f;
-            int col0 = 0, cols = kD;
+            const int64_t row =
+                (int64_t)(pc.rq.t0 + tok) * p.q_heads + pc.h * p.group + (int)(r_off - r_tok * p.group);
+            float *part = pc.slot >= 0 ? p.part + pc.slot * part_slot_floats(p.part_rows, kD) : nullptr;
+            bool owner = live_row;  // this thread writes the row's statistics
             if (both) {
+                // each slot's rows are its own: a thread writes its row
                 ok = bar_wait(&sh.o_full[s], n_o[s] & 1u, abort_flag, p.err);
                 if (!ok) break;
-                f0 = up;
+                tc_fence_after();
+                if (live_warp) {
+                    const float g = part ? up : sum == 0.0f ? 0.0f : up / sum;
+                    float4 *part_col = reinterpret_cast<float4 *>(part) + r_blk;  // [kD / 4][part_rows] of four
+                    __nv_bfloat16 *out_row = (__nv_bfloat16 *)p.out + row * kD;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < kD; c0 += 32) {
+                        uint32_t a[32];
+                        tmem_ld32(tO + c0, a);
+                        tmem_ld_wait();
+                        tmem_tie(a);
+                        if (!live_row) continue;
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) a[k] = __float_as_uint(__uint_as_float(a[k]) * g);
+                        if (part) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                part_col[(c0 / 4 + k) * p.part_rows] =
+                                    make_float4(__uint_as_float(a[4 * k]), __uint_as_float(a[4 * k + 1]),
+                                                __uint_as_float(a[4 * k + 2]), __uint_as_float(a[4 * k + 3]));
+                        } else {
+                            uint4 *dst = reinterpret_cast<uint4 *>(out_row + c0);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                uint32_t o[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    o[e] = pack16<false>(__uint_as_float(a[8 * k + 2 * e]),
+                                                         __uint_as_float(a[8 * k + 2 * e + 1]));
+                                dst[k] = make_uint4(o[0], o[1], o[2], o[3]);
+                            }
+                        }
+                    }
+                }
             } else {
+                // a row's sums lie in up to two slots and four copies: joined through shared
+                // memory, 32 columns at a time (the query tiles are free by now)
                 ok = bar_wait(&sh.o_full[0], n_o[0] & 1u, abort_flag, p.err) &&
                      (!used1 || bar_wait(&sh.o_full[1], n_o[1] & 1u, abort_flag, p.err));
                 if (!ok) break;
+                tc_fence_after();
                 float *mine = stat + 3 * kTile * s + my;
                 mine[0] = base;
                 mine[kTile] = sum;
                 mine[2 * kTile] = up;
                 named_sync<1, 256>();
-                const float *st0 = stat + my, *st1 = stat + 3 * kTile + my;
-                const float b0 = st0[0], b1 = used1 ? st1[0] : -INFINITY;
-                const float l0 = st0[kTile], l1 = used1 ? st1[kTile] : 0.0f;
-                const float u0 = st0[2 * kTile], u1 = used1 ? st1[2 * kTile] : 0.0f;
-                named_sync<1, 256>();  // both have read: the next piece's queries may come
-                base = fmaxf(b0, b1);
-                const float safe = base == -INFINITY ? 0.0f : base;
-                f0 = ex2(b0 - safe);
-                f1 = ex2(b1 - safe);
-                sum = l0 * f0 + l1 * f1;
-                f0 *= u0;
-                f1 *= u1;
-                cols = kD / 2;
-                col0 = s * cols;
+                const int rows = kTile >> split, row_in = my & (rows - 1);
+                const int sources = (used1 ? 2 : 1) << split;  // source i: slot i >> split, copy i & ...
+                float top = -INFINITY;
+                for (int i = 0; i < sources; ++i)
+                    top = fmaxf(top, stat[3 * kTile * (i >> split) + (i & ((1 << split) - 1)) * rows + row_in]);
+                const float safe = top == -INFINITY ? 0.0f : top;
+                const float g = ex2(base - safe) * up;
+                float all = 0.0f;
+                for (int i = 0; i < sources; ++i) {
+                    const float *st = stat + 3 * kTile * (i >> split) + (i & ((1 << split) - 1)) * rows + row_in;
+                    all = fmaf(st[kTile], ex2(st[0] - safe), all);
+                }
+                base = top;
+                sum = all;
+                owner = live_row && s == 0 && copy == 0;
+                float *inv = stat + 6 * kTile;
+                if (s == 0 && copy == 0) inv[row_in] = part ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+                float4 *red = reinterpret_cast<float4 *>(dyn + pad);  // [source][row][8 of four], swizzled
+#pragma unroll 1
+                for (int c0 = 0; c0 < kD; c0 += 32) {
+                    if (live_warp && (s == 0 || used1)) {
+                        uint32_t a[32];
+                        tmem_ld32(tO + c0, a);
+                        tmem_ld_wait();
+                        tmem_tie(a);
+                        float4 *dst = red + ((((s << split) + copy) * rows) + row_in) * 8;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            dst[k ^ (row_in & 7)] =
+                                make_float4(__uint_as_float(a[4 * k]) * g, __uint_as_float(a[4 * k + 1]) * g,
+                                            __uint_as_float(a[4 * k + 2]) * g, __uint_as_float(a[4 * k + 3]) * g);
+                    }
+                    named_sync<1, 256>();
+                    const int tid = threadIdx.x;
+                    for (int i = tid; i < rows * 8; i += 256) {
+                        // partial rows: rows fastest; output rows: columns fastest
+                        const int r = part ? i & (rows - 1) : i >> 3, k = part ? i >> (7 - split) : i & 7;
+                        if (r >= pc.n_rows) continue;
+                        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        for (int src = 0; src < sources; ++src) {
+                            const float4 v = red[(src * rows + r) * 8 + (k ^ (r & 7))];
+                            o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+                        }
+                        if (part) {
+                            reinterpret_cast<float4 *>(part)[(c0 / 4 + k) * p.part_rows + r] = o;
+                        } else {
+                            const uint32_t ro = pc.rem0 + r, rt = (ro * magic) >> 16;
+                            const int64_t to = ((int64_t)(pc.rq.t0 + pc.tok0 + (int)rt) * p.q_heads +
+                                                pc.h * p.group + (int)(ro - rt * p.group)) * kD + c0 + 4 * k;
+                            const float f = inv[r];
+                            *reinterpret_cast<uint2 *>((__nv_bfloat16 *)p.out + to) =
+                                make_uint2(pack16<false>(o.x * f, o.y * f), pack16<false>(o.z * f, o.w * f));
+                        }
+                    }
+                    named_sync<1, 256>();
+                }
             }
             n_o[0] += 1;
             n_o[1] += used1;
-            tc_fence_after();
-            if (live_warp) {
-                const bool poisoned = *(volatile int *)&sh.poison == (int)n_piece;
-                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                const int64_t row =
-                    (int64_t)(pc.rq.t0 + tok) * p.q_heads + pc.h * p.group + (int)(r_off - r_tok * p.group);
-                float *part = pc.slot >= 0 ? p.part + pc.slot * part_slot_floats(p.part_rows, kD) : nullptr;
-                float4 *part_col = reinterpret_cast<float4 *>(part) + r_blk;  // [kD / 4][part_rows] of four
-                __nv_bfloat16 *out_row = (__nv_bfloat16 *)p.out + row * kD;
-                const uint32_t t0 = 256 + lane_base + (both && s == 1 ? kD : 0);
-                const float g0 = part ? f0 : f0 * inv, g1 = part ? f1 : f1 * inv;
-#pragma unroll 1
-                for (int c0 = col0; c0 < col0 + cols; c0 += 32) {
-                    uint32_t a[32];
-                    tmem_ld32(t0 + c0, a);
-                    if (!both && used1) {
-                        uint32_t b[32];
-                        tmem_ld32(t0 + kD + c0, b);
-                        tmem_ld_wait();
-                        tmem_tie(a);
-                        tmem_tie(b);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            a[k] = __float_as_uint(__uint_as_float(a[k]) * g0 + __uint_as_float(b[k]) * g1);
-                    } else {
-                        tmem_ld_wait();
-                        tmem_tie(a);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) a[k] = __float_as_uint(__uint_as_float(a[k]) * g0);
-                    }
-                    if (!live_row) continue;
-                    if (part) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            part_col[(c0 / 4 + k) * p.part_rows] =
-                                make_float4(__uint_as_float(a[4 * k]), __uint_as_float(a[4 * k + 1]),
-                                            __uint_as_float(a[4 * k + 2]), __uint_as_float(a[4 * k + 3]));
-                    } else {
-                        uint4 *dst = reinterpret_cast<uint4 *>(out_row + c0);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            uint32_t o[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                o[e] = pack16<false>(__uint_as_float(a[8 * k + 2 * e]),
-                                                     __uint_as_float(a[8 * k + 2 * e + 1]));
-                            dst[k] = make_uint4(o[0], o[1], o[2], o[3]);
-                        }
-                    }
-                }
-                if (poisoned && live_row)
+            if (owner) {
+                if (*(volatile int *)&sh.poison == (int)n_piece)
                     add_poison<kD, kE4M3, kPaged>(p, pc.rq, pc.b, pc.h, tok, max(pc.t0, pc.guard_from) * kTile,
-                                                  min(pc.t1 * kTile, pc.rq.len), col0, cols, part ? part + 4 * r_blk : nullptr, out_row);
-                if (live_row && col0 == 0) {
-                    if (part) {
-                        part[part_stats(p.part_rows, kD) + r_blk] = base;
-                        part[part_stats(p.part_rows, kD) + p.part_rows + r_blk] = sum;
-                    } else if (p.lse) {
-                        p.lse[row] = sum == 0.0f ? -INFINITY : (base + log2f(sum)) * 0.6931471805599453f;
-                    }
+                                                  min(pc.t1 * kTile, pc.rq.len), 0, kD, part ? part + 4 * r_blk : nullptr,
+                                                  (__nv_bfloat16 *)p.out + row * kD);
+                if (part) {
+                    part[part_stats(p.part_rows, kD) + r_blk] = base;
+                    part[part_stats(p.part_rows, kD) + p.part_rows + r_blk] = sum;
+                } else if (p.lse) {
+                    p.lse[row] = sum == 0.0f ? -INFINITY : (base + log2f(sum)) * 0.6931471805599453f;
                 }
             }
             // the sums are read: the next piece's q_full arrivals say so to the MMAs
