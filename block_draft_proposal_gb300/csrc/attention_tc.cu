@@ -71,6 +71,7 @@ constexpr int kPieces = 4;
 constexpr int kPieceBytes = 64;
 struct Shared {
     alignas(16) uint8_t piece[kPieces][kPieceBytes];
+    int32_t pages[2][kTile / 16 * 8 + 1];  // page numbers of eight key tiles, twice
     uint64_t piece_full[kPieces], piece_empty[kPieces];
     uint64_t full[8], empty[8];  // operand ring (E4M3: filled by the widening warps)
     uint64_t guard_go[8], guard_done[8];  // value tiles handed to the guard warp and back, in order
@@ -588,30 +589,41 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
         regs_give<C::kRegsFew>();
         if (warp == 9) {
             // ---- producer: the pieces, and the TMA copies by one thread ----
-            constexpr int kMaxBox = kPaged ? kTile / 16 : 1;
             uint32_t pos = 0, n_piece = 0;  // operand tiles issued
             uint32_t n_key = 0, n_value = 0;
             bool ok = true, bad_page = false;
             const int32_t rows_box = kPaged ? min(p.page_size, kTile) : kTile;
-            const int32_t n_box = kTile / rows_box;
-            const int32_t shift = kPaged ? 31 - __clz(p.page_size) : 0;
+            const int32_t page_shift = kPaged ? 31 - __clz(p.page_size) : 0;
+            const int32_t box_shift = kPaged ? 7 - min(page_shift, 7) : 0;  // log2 of the boxes of a tile
             Piece pc{};
-            // pages of a key tile's boxes (-1: past the end, a box of zeros)
-            struct Pages {
-                int32_t id[kMaxBox];
-            };
-            auto pages_of = [&](int32_t tile) {
-                Pages g;
+            // Page numbers come eight key tiles at a time: the lanes load the next eight's
+            // while one thread issues the copies of these.  -1: no page (past the end, or
+            // out of range), a box of zeros.
+            int32_t ids[2] = {-1, -1};
+            auto fetch_pages = [&](int32_t tile) {
 #pragma unroll
-                for (int i = 0; i < kMaxBox; ++i) {
-                    const int32_t l = tile * kTile + i * rows_box;
-                    g.id[i] = -1;
-                    if (kPaged && i < n_box && tile < pc.t1 && l < pc.rq.len)
-                        g.id[i] = __ldg(p.page_table + (int64_t)pc.b * p.max_pages + (l >> shift));
+                for (int k = 0; k < 2; ++k) {
+                    const int32_t e = lane + 32 * k, at = tile + (e >> box_shift);
+                    const int32_t l = at * kTile + (e & ((1 << box_shift) - 1)) * rows_box;
+                    ids[k] = -1;
+                    if (e < (8 << box_shift) && at < pc.t1 && l < pc.rq.len) {
+                        ids[k] = __ldg(p.page_table + (int64_t)pc.b * p.max_pages + (l >> page_shift));
+                    }
                 }
-                return g;
             };
-            auto load = [&](int32_t tile, const Pages &g, bool values) {
+            auto keep_pages = [&](int32_t tile, uint32_t buffer) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int32_t e = lane + 32 * k, at = tile + (e >> box_shift);
+                    const int32_t l = at * kTile + (e & ((1 << box_shift) - 1)) * rows_box;
+                    const bool good = (uint64_t)(int64_t)ids[k] < (uint64_t)p.num_pages;
+                    if (e < (8 << box_shift) && at < pc.t1 && l < pc.rq.len && !good) bad_page = true;
+                    if (e < (8 << box_shift)) sh.pages[buffer][e] = good ? ids[k] : -1;
+                }
+                __syncwarp();
+            };
+            auto load = [&](int32_t j, bool values) {  // key tile t0 + j
+                const int32_t tile = pc.t0 + j;
                 uint64_t *fullb;
                 uint32_t dst;
                 [[maybe_unused]] const uint32_t ex = n_key & 3u;
@@ -642,18 +654,16 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                                     pc.rq.t0 + tile * kTile);
                 } else {
                     const int32_t y = (tile * kTile) & (p.page_size - 1) & ~(kTile - 1);
-#pragma unroll
-                    for (int i = 0; i < kMaxBox; ++i) {
-                        if (i >= n_box) break;
-                        const bool live = tile * kTile + i * rows_box < pc.rq.len;
-                        const bool good = (uint32_t)g.id[i] < (uint32_t)p.num_pages;
-                        if (live && !good) bad_page = true;
-                        const int32_t z = good ? g.id[i] * p.kv_heads + pc.h : -1;
+                    const int32_t *page = sh.pages[(j >> 3) & 1] + ((j & 7) << box_shift);
+                    int32_t id = page[0];
+#pragma unroll 1
+                    for (int i = 0; i < (1 << box_shift); ++i) {
+                        const int32_t z = id >= 0 ? id * p.kv_heads + pc.h : -1;
+                        const int32_t next = page[i + 1];  // past the last: unused
                         if constexpr (kE4M3) {
                             tma_load_3d(dst + i * rows_box * kD, map, fullb, 0, y, z);
                             if (!values) {  // page 0's where there is none: any scale serves zero rows
-                                const int64_t at =
-                                    ((int64_t)(good ? g.id[i] : 0) * p.kv_heads + pc.h) * p.page_size + y;
+                                const int64_t at = (int64_t)max(z, pc.h) * p.page_size + y;
                                 bulk_load(smem_u32(&sh.exps[ex][0][i * rows_box]), p.k_exp + at, rows_box,
                                           &sh.ex_full[ex]);
                                 bulk_load(smem_u32(&sh.exps[ex][1][i * rows_box]), p.v_exp + at, rows_box,
@@ -665,6 +675,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                                 tma_load_3d(dst + half * (kTile * 128) + i * rows_box * 128, map, fullb, 64 * half,
                                             y, z);
                         }
+                        id = next;
                     }
                 }
                 n_key += !values;
@@ -693,6 +704,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
 #pragma unroll
                     for (int c = 0; c < kD; c += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + c));
                 }
+                if (kPaged && pc.n_rows > 0) fetch_pages(pc.t0);
                 if (elect_one()) {
                     ok = bar_wait(&sh.piece_empty[n_piece % kPieces], ((n_piece / kPieces) & 1u) ^ 1u,
                                   abort_flag, p.err);
@@ -700,29 +712,27 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                         *reinterpret_cast<Piece *>(sh.piece[n_piece % kPieces]) = pc;
                         mbar_arrive(&sh.piece_full[n_piece % kPieces]);
                     }
-                    if (ok && pc.n_rows > 0) {
-                        // shared K0 V0 K1 V1 ..., alternate K0 K1 V0 K2 V1 ... V(n-2) V(n-1);
-                        // page numbers are fetched a tile ahead of their copies
-                        const int32_t n = pc.t1 - pc.t0, lead = pc.shared() ? 0 : 1;
-                        Pages key = pages_of(pc.t0), value = key, value_next = key;
-                        int32_t jk = 0, jv = 0;
-#pragma unroll 1
-                        for (int32_t i = 0; ok && i < 2 * n; ++i) {
+                }
+                // shared K0 V0 K1 V1 ..., alternate K0 K1 V0 K2 V1 ... V(n-2) V(n-1)
+                const int32_t n = pc.n_rows > 0 ? pc.t1 - pc.t0 : 0, lead = pc.shared() ? 0 : 1;
+                int32_t jk = 0, jv = 0;
+                for (int32_t c = 0; c < n; c += 8) {
+                    if constexpr (kPaged) {
+                        keep_pages(pc.t0 + c, (c >> 3) & 1);
+                        fetch_pages(pc.t0 + c + 8);
+                    }
+                    if (elect_one()) {
+                        // the keys of these eight tiles and the values that follow them
+                        while (ok && (jk < min(n, c + 8) || (c + 8 >= n && jv < n))) {
                             const bool values = jk == n || jk - jv > lead;
-                            Pages g;
-#pragma unroll
-                            for (int k = 0; k < kMaxBox; ++k) g.id[k] = values ? value.id[k] : key.id[k];
-                            ok = load(pc.t0 + (values ? jv : jk), g, values);
-                            if (values) {
-                                value = value_next;
+                            ok = load(values ? jv : jk, values);
+                            if (values)
                                 ++jv;
-                            } else {
-                                if (jk == jv) value = key;
-                                value_next = key;
-                                key = pages_of(pc.t0 + ++jk);
-                            }
+                            else
+                                ++jk;
                         }
                     }
+                    __syncwarp();
                 }
                 ++n_piece;
                 if (__any_sync(0xFFFFFFFFu, !ok) || pc.n_rows == 0) break;
