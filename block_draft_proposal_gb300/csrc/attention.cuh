@@ -8,12 +8,13 @@
 // blocks of 2^row_shift.  An item is one (request, key/value head, row block).
 //
 // Split of the cache (paged mode).  Requests are ragged and few rows may face
-// many keys, so the keys are split by work, not by item: the items' key tiles
-// (kKeyTile keys each, at least one per item) are numbered through, request by
-// request, head by head, row block by row block, and CTA c of C (at most W)
-// takes the tiles [c W / C, (c + 1) W / C) of all W.  A CTA that holds all of an item
-// writes its rows; an item that spans CTAs leaves unnormalised partial rows in
-// the workspace, joined by combine_kernel in CTA order.
+// many keys, so the keys are split by work, not by item: an item is worth its key
+// tiles (kKeyTile keys each, at least one) and item_units more for its start and
+// end; these units are numbered through, request by request, head by head, row
+// block by row block, an item's extra ones first, and CTA c of C (at most W) takes
+// the units [c W / C, (c + 1) W / C) of all W.  A CTA that holds all tiles of an
+// item writes its rows; an item whose tiles span CTAs leaves unnormalised partial
+// rows in the workspace, joined by combine_kernel in CTA order.
 #pragma once
 
 #include "kernels.h"
@@ -46,6 +47,7 @@ struct Params {
     float *part;                   // paged: partial rows, kPartSlots(C) slots
     int32_t part_rows;             // rows of a slot
     int32_t row_shift;             // log2 of the rows of a block
+    int32_t item_units;            // units of an item beside its key tiles
     int32_t n_cta;                 // CTAs the work is split over
     int32_t *err;
 };
@@ -100,9 +102,9 @@ __device__ __forceinline__ int32_t row_blocks(const Params &p, const Request &r)
 __device__ __forceinline__ int32_t key_tiles(const Request &r) {
     return max(1, (r.len + kKeyTile - 1) / kKeyTile);
 }
-// Units (key tiles of items) of request b; 0 when it has no rows.
+// Units of request b; 0 when it has no rows.
 __device__ __forceinline__ int64_t request_units(const Params &p, const Request &r) {
-    return (int64_t)p.kv_heads * row_blocks(p, r) * key_tiles(r);
+    return (int64_t)p.kv_heads * row_blocks(p, r) * (key_tiles(r) + p.item_units);
 }
 
 // First unit of CTA c's range, and the CTA that holds unit u, where n_cta is

@@ -265,17 +265,19 @@ __global__ void __launch_bounds__(kThreads) simt_kernel(const Params p, bool vec
             const Request r = load_request<true>(p, b, &bad);
             const int64_t n = request_units(p, r);
             while (u < end && u < before + n) {
-                const int32_t tiles = key_tiles(r);
-                const int64_t item = (u - before) / tiles;
-                const int32_t t0 = (int32_t)((u - before) % tiles);
-                const int32_t t1 = (int32_t)min((int64_t)tiles, t0 + (end - u));
+                const int32_t tiles = key_tiles(r), worth = tiles + p.item_units;
+                const int64_t item = (u - before) / worth;
+                const int32_t o0 = (int32_t)((u - before) % worth);
+                const int32_t o1 = (int32_t)min((int64_t)worth, o0 + (end - u));
+                const int32_t t0 = max(o0 - p.item_units, 0), t1 = o1 - p.item_units;
                 const int32_t nrb = row_blocks(p, r);
                 const bool whole = t0 == 0 && t1 == tiles;
-                run_piece<T, C, true, kRows, kDMax>(
-                    p, r, b, (int32_t)(item / nrb), (int32_t)(item % nrb), t0 * kKeyTile,
-                    min(t1 * kKeyTile, r.len), whole ? -1 : 2 * (int64_t)blockIdx.x + (t0 == 0),
-                    smem, vec_q, vec_k, &any_bad);
-                u += t1 - t0;
+                if (t1 > t0)
+                    run_piece<T, C, true, kRows, kDMax>(
+                        p, r, b, (int32_t)(item / nrb), (int32_t)(item % nrb), t0 * kKeyTile,
+                        min(t1 * kKeyTile, r.len), whole ? -1 : 2 * (int64_t)blockIdx.x + (t0 == 0),
+                        smem, vec_q, vec_k, &any_bad);
+                u += o1 - o0;
             }
             before += n;
         }
@@ -355,7 +357,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const Params p) {
         if (g >= p.group) continue;
         const int64_t row = (int64_t)(tok - r.t0) * p.group + g;
         const int32_t rb = (int32_t)(row >> p.row_shift), rr = (int32_t)(row & ((1 << p.row_shift) - 1));
-        const int64_t u0 = before + ((int64_t)h * nrb + rb) * tiles;
+        const int64_t u0 = before + ((int64_t)h * nrb + rb) * (tiles + p.item_units) + p.item_units;
         const int32_t c0 = cta_of(u0, units, n_cta), c1 = cta_of(u0 + tiles - 1, units, n_cta);
         if (c0 == c1) continue;  // the attention kernel wrote this row
         auto part = [&](int32_t k) { return p.part + (2 * (int64_t)k + (k == c0)) * slot_floats; };
@@ -438,6 +440,7 @@ dflash2_status launch_simt(const DeviceInfo &di, Params p, bool paged, int32_t d
     const bool vec_k = four && aligned_to(p.k, 4 * kel) && aligned_to(p.v, 4 * kel) &&
                        (paged || (p.k_stride % 4 == 0 && p.v_stride % 4 == 0));
     p.n_cta = di.sm_count;
+    p.item_units = 1;
     dflash2_status s;
     if (dtype == DFLASH2_F32) {
         if (!paged)

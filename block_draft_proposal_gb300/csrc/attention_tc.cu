@@ -56,6 +56,7 @@ namespace {
 
 constexpr int kTile = 128;       // keys per tile, rows per slot
 constexpr int kRowShift = 8, kRowBlock = 1 << kRowShift;
+constexpr int kItemUnits = 4;    // an item's start and end cost about as much as four key tiles
 constexpr float kLazy = 8.0f;    // log2 growth of the maximum that forces a rescale
 constexpr int kTopE4M3 = 6;      // fp16 weights: the largest starts below 2^7 ...
 constexpr int kCapE4M3 = 14;     // ... and x moves before one reaches 2^15
@@ -71,7 +72,7 @@ constexpr int kPieces = 4;
 constexpr int kPieceBytes = 64;
 struct Shared {
     alignas(16) uint8_t piece[kPieces][kPieceBytes];
-    int32_t pages[2][kTile / 16 * 8 + 1];  // page numbers of eight key tiles, twice
+    int32_t pages[2][2][kTile / 16 * 8 + 1];  // page numbers of eight key tiles, twice, by producer
     uint64_t piece_full[kPieces], piece_empty[kPieces];
     uint64_t full[8], empty[8];  // operand ring (E4M3: filled by the widening warps)
     uint64_t guard_go[8], guard_done[8];  // value tiles handed to the guard warp and back, in order
@@ -331,35 +332,41 @@ struct Walk {
     }
     __device__ __forceinline__ void next(const Params &p, Piece *pc) {
         pc->n_rows = 0;
-        if (u >= end) return;
-        while (u >= before + n) {
-            bool bad;
-            before += n;
-            ++b;
-            rq = load_request<true>(p, b, &bad);
-            n = request_units(p, rq);
+        while (u < end) {
+            while (u >= before + n) {
+                bool bad;
+                before += n;
+                ++b;
+                rq = load_request<true>(p, b, &bad);
+                n = request_units(p, rq);
+            }
+            const uint32_t worth = key_tiles(rq) + p.item_units, nrb = row_blocks(p, rq);
+            uint32_t item;
+            int32_t o0;
+            if (n < (1ll << 31)) {
+                const uint32_t off = (uint32_t)(u - before);
+                item = off / worth;
+                o0 = (int32_t)(off - item * worth);
+            } else {
+                const int64_t off = u - before;
+                item = (uint32_t)(off / worth);  // kv_heads * row blocks: below 2^31
+                o0 = (int32_t)(off - (int64_t)item * worth);
+            }
+            const int32_t o1 = (int32_t)min((int64_t)worth, o0 + (end - u));
+            u += o1 - o0;
+            pc->t0 = max(o0 - p.item_units, 0);
+            pc->t1 = o1 - p.item_units;
+            if (pc->t1 <= pc->t0) continue;  // the range ends within the item's extra units
+            pc->t1a = pc->t1;
+            pc->rq = rq;
+            pc->b = b;
+            pc->h = (int32_t)(item / nrb);
+            pc->row0 = (int32_t)(item - (uint32_t)pc->h * nrb) * kRowBlock;
+            pc->n_rows = min(kRowBlock, rq.t * p.group - pc->row0);
+            pc->slot = pc->t0 == 0 && o1 == (int32_t)worth ? -1 : 2 * (int32_t)blockIdx.x + (pc->t0 == 0);
+            pc->guard_from = rq.ctx / kTile;
+            return;
         }
-        const uint32_t tiles = key_tiles(rq), nrb = row_blocks(p, rq);
-        uint32_t item;
-        if (n < (1ll << 31)) {
-            const uint32_t off = (uint32_t)(u - before);
-            item = off / tiles;
-            pc->t0 = (int32_t)(off - item * tiles);
-        } else {
-            const int64_t off = u - before;
-            item = (uint32_t)(off / tiles);  // kv_heads * row blocks: below 2^31
-            pc->t0 = (int32_t)(off - (int64_t)item * tiles);
-        }
-        pc->t1 = (int32_t)min((int64_t)tiles, pc->t0 + (end - u));
-        pc->t1a = pc->t1;
-        pc->rq = rq;
-        pc->b = b;
-        pc->h = (int32_t)(item / nrb);
-        pc->row0 = (int32_t)(item - (uint32_t)pc->h * nrb) * kRowBlock;
-        pc->n_rows = min(kRowBlock, rq.t * p.group - pc->row0);
-        pc->slot = pc->t0 == 0 && pc->t1 == (int32_t)tiles ? -1 : 2 * (int32_t)blockIdx.x + (pc->t0 == 0);
-        pc->guard_from = rq.ctx / kTile;
-        u += pc->t1 - pc->t0;
     }
 };
 
@@ -528,7 +535,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                 mbar_init(&sh.kraw_empty[i], 2);
                 mbar_init(&sh.vraw_full[i], 1);
                 mbar_init(&sh.vraw_empty[i], 4);
-                mbar_init(&sh.ex_full[i], 1);
+                mbar_init(&sh.ex_full[i], 2);
                 mbar_init(&sh.ex_empty[i], 2);
                 mbar_init(&sh.sc_full[i], 1);
             }
@@ -539,7 +546,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
         }
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(&sh.piece_full[i], 1);
-            mbar_init(&sh.piece_empty[i], kE4M3 ? 14 : 11);  // issuers, softmax warps, widening or guard
+            mbar_init(&sh.piece_empty[i], kE4M3 ? 15 : 11);  // all but the producer
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_full[i], 1);
@@ -587,8 +594,10 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
 
     if (warp >= 8 && warp < 12) {
         regs_give<C::kRegsFew>();
-        if (warp == 9) {
-            // ---- producer: the pieces, and the TMA copies by one thread ----
+        if (warp == 9 || (kE4M3 && warp == 11)) {
+            // ---- producer: the pieces, and the TMA copies by one thread.  E4M3: warp 9 the
+            // keys, warp 11 the values, each with its exponent bytes ----
+            const bool of_keys = !kE4M3 || warp == 9;
             uint32_t pos = 0, n_piece = 0;  // operand tiles issued
             uint32_t n_key = 0, n_value = 0;
             bool ok = true, bad_page = false;
@@ -618,7 +627,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                     const int32_t l = at * kTile + (e & ((1 << box_shift) - 1)) * rows_box;
                     const bool good = (uint64_t)(int64_t)ids[k] < (uint64_t)p.num_pages;
                     if (e < (8 << box_shift) && at < pc.t1 && l < pc.rq.len && !good) bad_page = true;
-                    if (e < (8 << box_shift)) sh.pages[buffer][e] = good ? ids[k] : -1;
+                    if (e < (8 << box_shift)) sh.pages[warp >> 1 & 1][buffer][e] = good ? ids[k] : -1;
                 }
                 __syncwarp();
             };
@@ -626,7 +635,6 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                 const int32_t tile = pc.t0 + j;
                 uint64_t *fullb;
                 uint32_t dst;
-                [[maybe_unused]] const uint32_t ex = n_key & 3u;
                 if constexpr (kE4M3) {
                     const uint32_t n = values ? n_value : n_key, slots = values ? C::kVRaw : C::kKRaw;
                     const uint32_t s = n % slots, ph = ((n / slots) & 1u) ^ 1u;
@@ -634,10 +642,6 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                     dst = (values ? sm_vraw : sm_kraw) + s * C::kRawBytes;
                     if (!bar_wait(values ? &sh.vraw_empty[s] : &sh.kraw_empty[s], ph, abort_flag, p.err))
                         return false;
-                    if (!values) {
-                        if (!bar_wait(&sh.ex_empty[ex], ((n_key >> 2) & 1u) ^ 1u, abort_flag, p.err)) return false;
-                        mbar_arrive_expect_tx(&sh.ex_full[ex], 2 * kTile);
-                    }
                     mbar_arrive_expect_tx(fullb, C::kRawBytes);
                 } else {
                     const uint32_t s = pos % kStages;
@@ -654,7 +658,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                                     pc.rq.t0 + tile * kTile);
                 } else {
                     const int32_t y = (tile * kTile) & (p.page_size - 1) & ~(kTile - 1);
-                    const int32_t *page = sh.pages[(j >> 3) & 1] + ((j & 7) << box_shift);
+                    const int32_t *page = sh.pages[warp >> 1 & 1][(j >> 3) & 1] + ((j & 7) << box_shift);
                     int32_t id = page[0];
 #pragma unroll 1
                     for (int i = 0; i < (1 << box_shift); ++i) {
@@ -662,13 +666,6 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                         const int32_t next = page[i + 1];  // past the last: unused
                         if constexpr (kE4M3) {
                             tma_load_3d(dst + i * rows_box * kD, map, fullb, 0, y, z);
-                            if (!values) {  // page 0's where there is none: any scale serves zero rows
-                                const int64_t at = (int64_t)max(z, pc.h) * p.page_size + y;
-                                bulk_load(smem_u32(&sh.exps[ex][0][i * rows_box]), p.k_exp + at, rows_box,
-                                          &sh.ex_full[ex]);
-                                bulk_load(smem_u32(&sh.exps[ex][1][i * rows_box]), p.v_exp + at, rows_box,
-                                          &sh.ex_full[ex]);
-                            }
                         } else {
 #pragma unroll
                             for (int half = 0; half < C::kHalves; ++half)
@@ -683,34 +680,61 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                 ++pos;
                 return true;
             };
+            // E4M3: exponent bytes of key tile t0 + j, this warp's half of them
+            uint32_t n_ex = 0;
+            [[maybe_unused]] auto load_exps = [&](int32_t j) {
+                if constexpr (kE4M3) {
+                    const uint32_t i = n_ex & 3u;
+                    if (!bar_wait(&sh.ex_empty[i], ((n_ex >> 2) & 1u) ^ 1u, abort_flag, p.err)) return false;
+                    mbar_arrive_expect_tx(&sh.ex_full[i], kTile);
+                    const int32_t y = ((pc.t0 + j) * kTile) & (p.page_size - 1) & ~(kTile - 1);
+                    const int32_t *page = sh.pages[warp >> 1 & 1][(j >> 3) & 1] + ((j & 7) << box_shift);
+                    const uint8_t *src = of_keys ? p.k_exp : p.v_exp;
+                    const uint32_t dst = smem_u32(sh.exps[i][of_keys ? 0 : 1]);
+#pragma unroll 1
+                    for (int b = 0; b < (1 << box_shift); ++b) {
+                        // page 0's where there is none: any scale serves zero rows
+                        const int32_t z = max(page[b], 0) * p.kv_heads + pc.h;
+                        bulk_load(dst + b * rows_box, src + (int64_t)z * p.page_size + y, rows_box, &sh.ex_full[i]);
+                    }
+                    ++n_ex;
+                }
+                return true;
+            };
             Walk walk{};
             Levels levels{};
-            if constexpr (kPaged)
-                walk.begin(p, start);
-            else
+            if constexpr (!kPaged)
                 levels.begin(p, lane, &bad);
+            else if (of_keys)
+                walk.begin(p, start);
             for (;;) {
-                if constexpr (kPaged)
-                    walk.next(p, &pc);
-                else
-                    levels.next(p, lane, &pc);
-                pc.tok0 = pc.row0 / p.group;
-                pc.rem0 = pc.row0 - pc.tok0 * p.group;
-                for (int r = lane; r < pc.n_rows; r += 32) {  // the queries, on their way to L2
-                    const int x = pc.rem0 + r, dt = x / p.group;
-                    const __nv_bfloat16 *q = (const __nv_bfloat16 *)p.q +
-                                             (int64_t)(pc.rq.t0 + pc.tok0 + dt) * p.q_stride +
-                                             (int64_t)(pc.h * p.group + x - dt * p.group) * kD;
+                if (!of_keys) {
+                    const bool more = take_piece(n_piece, &pc, true);
+                    if (!more) pc.n_rows = 0;
+                    if (kPaged && more) fetch_pages(pc.t0);
+                } else {
+                    if constexpr (kPaged)
+                        walk.next(p, &pc);
+                    else
+                        levels.next(p, lane, &pc);
+                    pc.tok0 = pc.row0 / p.group;
+                    pc.rem0 = pc.row0 - pc.tok0 * p.group;
+                    for (int r = lane; r < pc.n_rows; r += 32) {  // the queries, on their way to L2
+                        const int x = pc.rem0 + r, dt = x / p.group;
+                        const __nv_bfloat16 *q = (const __nv_bfloat16 *)p.q +
+                                                 (int64_t)(pc.rq.t0 + pc.tok0 + dt) * p.q_stride +
+                                                 (int64_t)(pc.h * p.group + x - dt * p.group) * kD;
 #pragma unroll
-                    for (int c = 0; c < kD; c += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + c));
-                }
-                if (kPaged && pc.n_rows > 0) fetch_pages(pc.t0);
-                if (elect_one()) {
-                    ok = bar_wait(&sh.piece_empty[n_piece % kPieces], ((n_piece / kPieces) & 1u) ^ 1u,
-                                  abort_flag, p.err);
-                    if (ok) {
-                        *reinterpret_cast<Piece *>(sh.piece[n_piece % kPieces]) = pc;
-                        mbar_arrive(&sh.piece_full[n_piece % kPieces]);
+                        for (int c = 0; c < kD; c += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + c));
+                    }
+                    if (kPaged && pc.n_rows > 0) fetch_pages(pc.t0);
+                    if (elect_one()) {
+                        ok = bar_wait(&sh.piece_empty[n_piece % kPieces], ((n_piece / kPieces) & 1u) ^ 1u,
+                                      abort_flag, p.err);
+                        if (ok) {
+                            *reinterpret_cast<Piece *>(sh.piece[n_piece % kPieces]) = pc;
+                            mbar_arrive(&sh.piece_full[n_piece % kPieces]);
+                        }
                     }
                 }
                 // shared K0 V0 K1 V1 ..., alternate K0 K1 V0 K2 V1 ... V(n-2) V(n-1)
@@ -722,14 +746,18 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                         fetch_pages(pc.t0 + c + 8);
                     }
                     if (elect_one()) {
-                        // the keys of these eight tiles and the values that follow them
-                        while (ok && (jk < min(n, c + 8) || (c + 8 >= n && jv < n))) {
-                            const bool values = jk == n || jk - jv > lead;
-                            ok = load(values ? jv : jk, values);
-                            if (values)
-                                ++jv;
-                            else
-                                ++jk;
+                        if constexpr (kE4M3) {
+                            for (; ok && jk < min(n, c + 8); ++jk) ok = load_exps(jk) && load(jk, !of_keys);
+                        } else {
+                            // the keys of these eight tiles and the values that follow them
+                            while (ok && (jk < min(n, c + 8) || (c + 8 >= n && jv < n))) {
+                                const bool values = jk == n || jk - jv > lead;
+                                ok = load(values ? jv : jk, values);
+                                if (values)
+                                    ++jv;
+                                else
+                                    ++jk;
+                            }
                         }
                     }
                     __syncwarp();
@@ -750,7 +778,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                 if constexpr (kE4M3) {
                     drain(sh.kraw_full, n_key, C::kKRaw);
                     drain(sh.vraw_full, n_value, C::kVRaw);
-                    drain(sh.ex_full, n_key, 4);
+                    drain(sh.ex_full, n_ex, 4);
                 } else {
                     drain(sh.full, pos, kStages);
                 }
@@ -1573,6 +1601,7 @@ dflash2_status launch_one(const DeviceInfo &di, Params p, cudaStream_t st) {
         if (s != DFLASH2_OK) return s;
     }
     p.row_shift = kRowShift;
+    p.item_units = kItemUnits;
     // prompts: every row block of every request, at most one short one each
     const int64_t items = ((((int64_t)p.total_q * p.group) >> kRowShift) + p.batch) * p.kv_heads;
     p.n_cta = kPaged || items > di.sm_count ? di.sm_count : (int32_t)items;
