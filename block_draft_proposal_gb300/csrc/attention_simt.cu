@@ -320,11 +320,13 @@ __global__ void __launch_bounds__(kThreads) simt_kernel(const Params p, bool vec
 }
 
 // Joins the partial rows of items that span CTAs, in CTA order.  A CTA takes the
-// group's rows of one token and key/value head; a warp takes eight rows (neighbours
-// in a slot) at a time, four lanes a row, so that lane (row, c) holds every fourth
-// group of four values and a load reads 128 contiguous bytes of four such groups.
-template <typename T, int kQuads>  // groups of four values per lane
-__global__ void __launch_bounds__(128) combine_kernel(const Params p) {
+// group's rows of one token and key/value head, a thread four values of a row
+// (neighbouring threads neighbouring rows, which neighbour in a slot).  Where the
+// partials lie follows from cu_q and kv_lens alone and is worked out before the
+// attention kernel ends; what is left then is one read of them, four at a time.
+constexpr int kJoinThreads = 128;
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads) combine_kernel(const Params p) {
     __shared__ int64_t red[32];
     __shared__ int32_t which;
     const int32_t tok = blockIdx.x, h = blockIdx.y;
@@ -335,7 +337,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const Params p) {
     int64_t all = 0, mine = 0;
     if (threadIdx.x == 0) which = -1;
     __syncthreads();
-    for (int b = threadIdx.x; b < p.batch; b += 128) {
+    for (int b = threadIdx.x; b < p.batch; b += kJoinThreads) {
         const Request r = load_request<true>(p, b, &bad);
         const int64_t n = request_units(p, r);
         all += n;
@@ -344,55 +346,71 @@ __global__ void __launch_bounds__(128) combine_kernel(const Params p) {
     }
     const int64_t units = block_sum(all, red);
     const int64_t before = block_sum(mine, red);
+    Request r{};
+    int32_t tiles = 0, c0 = 0, c1 = 0, rr = 0;
+    const int d = p.head_dim, quads = (d + 3) / 4;
+    const int64_t n_cta = split_ctas(p, units);
+    // the CTAs that hold the row's item, and the row in its block
+    auto place = [&](int32_t g) {
+        const int32_t row = (tok - r.t0) * p.group + g, rb = row >> p.row_shift;
+        rr = row & ((1 << p.row_shift) - 1);
+        const int64_t u0 = before + ((int64_t)h * row_blocks(p, r) + rb) * (tiles + p.item_units) + p.item_units;
+        c0 = cta_of(u0, units, n_cta);
+        c1 = cta_of(u0 + tiles - 1, units, n_cta);
+    };
+    if (which >= 0) {
+        r = load_request<true>(p, which, &bad);
+        tiles = key_tiles(r);
+        place(threadIdx.x % p.group);
+    }
+    const int64_t slot_floats = part_slot_floats(p.part_rows, d), stats = part_stats(p.part_rows, d);
     grid_dep_wait();
     if (which < 0) return;
-    const Request r = load_request<true>(p, which, &bad);
-    const int32_t tiles = key_tiles(r), nrb = row_blocks(p, r);
-    const int lane = threadIdx.x & 31;
-    const int d = p.head_dim;
-    const int64_t slot_floats = part_slot_floats(p.part_rows, d), stats = part_stats(p.part_rows, d);
-    const int64_t n_cta = split_ctas(p, units);
-    for (int g0 = (threadIdx.x >> 5) * 8; g0 < p.group; g0 += 32) {
-        const int g = g0 + (lane >> 2), c = lane & 3;
-        if (g >= p.group) continue;
-        const int64_t row = (int64_t)(tok - r.t0) * p.group + g;
-        const int32_t rb = (int32_t)(row >> p.row_shift), rr = (int32_t)(row & ((1 << p.row_shift) - 1));
-        const int64_t u0 = before + ((int64_t)h * nrb + rb) * (tiles + p.item_units) + p.item_units;
-        const int32_t c0 = cta_of(u0, units, n_cta), c1 = cta_of(u0 + tiles - 1, units, n_cta);
+    for (int i = threadIdx.x; i < p.group * quads; i += kJoinThreads) {
+        const int32_t g = i % p.group, c = i / p.group;
+        if (i >= kJoinThreads) place(g);
         if (c0 == c1) continue;  // the attention kernel wrote this row
-        auto part = [&](int32_t k) { return p.part + (2 * (int64_t)k + (k == c0)) * slot_floats; };
-        float m = -INFINITY;
-        for (int32_t k = c0; k <= c1; ++k) m = fmaxf(m, part(k)[stats + rr]);
-        const float base = m == -INFINITY ? 0.0f : m;
-        float l = 0.0f;
-        float4 o[kQuads];
+        const float *first = p.part + (2 * (int64_t)c0 + 1) * slot_floats;  // the item's start
+        const float *rest = p.part + 2 * (int64_t)(c0 + 1) * slot_floats;
+        float m = -INFINITY, l = 0.0f;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int32_t k = c0; k <= c1; k += 4) {
+            float mk[4], lk[4];
+            float4 v[4];
 #pragma unroll
-        for (int q = 0; q < kQuads; ++q) o[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int32_t k = c0; k <= c1; ++k) {
-            const float *s = part(k);
-            const float w = ex2(s[stats + rr] - base);
-            l = fmaf(w, s[stats + p.part_rows + rr], l);
-            if (w == 0.0f) continue;
-#pragma unroll
-            for (int q = 0; q < kQuads; ++q) {
-                if (4 * (4 * q + c) >= d) break;
-                const float4 v = reinterpret_cast<const float4 *>(s)[(int64_t)(4 * q + c) * p.part_rows + rr];
-                o[q].x = fmaf(w, v.x, o[q].x), o[q].y = fmaf(w, v.y, o[q].y);
-                o[q].z = fmaf(w, v.z, o[q].z), o[q].w = fmaf(w, v.w, o[q].w);
+            for (int e = 0; e < 4; ++e) {
+                const float *s = k + e == c0 ? first : rest + (int64_t)(k + e - c0 - 1) * 2 * slot_floats;
+                mk[e] = -INFINITY, lk[e] = 0.0f, v[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (k + e <= c1) {
+                    mk[e] = __ldcg(s + stats + rr);
+                    lk[e] = __ldcg(s + stats + p.part_rows + rr);
+                    v[e] = __ldcg(reinterpret_cast<const float4 *>(s) + (int64_t)c * p.part_rows + rr);
+                }
             }
+            const float top = fmaxf(m, fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])));
+            const float base = top == -INFINITY ? 0.0f : top;
+            const float fix = ex2(m - base);
+            l *= fix, o.x *= fix, o.y *= fix, o.z *= fix, o.w *= fix;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float w = ex2(mk[e] - base);
+                l = fmaf(w, lk[e], l);
+                if (w != 0.0f) {
+                    o.x = fmaf(w, v[e].x, o.x), o.y = fmaf(w, v[e].y, o.y);
+                    o.z = fmaf(w, v[e].z, o.z), o.w = fmaf(w, v[e].w, o.w);
+                }
+            }
+            m = top;
         }
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const int64_t at = (int64_t)tok * p.q_heads + h * p.group + g;
+        T *dst = (T *)p.out + at * d + 4 * c;
+        const float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
 #pragma unroll
-        for (int q = 0; q < kQuads; ++q) {
-            const int col = 4 * (4 * q + c);
-            const float v[4] = {o[q].x, o[q].y, o[q].z, o[q].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (col + e < d) put((T *)p.out + at * d + col + e, v[e] * inv);
-        }
+        for (int e = 0; e < 4; ++e)
+            if (4 * c + e < d) put(dst + e, v[e]);
         if (c == 0 && p.lse)
-            p.lse[at] = l == 0.0f ? -INFINITY : (base + log2f(l)) * 0.6931471805599453f;
+            p.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     }
 }
 
@@ -462,20 +480,12 @@ dflash2_status launch_simt(const DeviceInfo &di, Params p, bool paged, int32_t d
     return launch_combine(di, p, dtype, st);
 }
 
-template <typename T> void combine_typed(const Params &p, cudaStream_t st) {
-    const dim3 grid((unsigned)p.total_q, (unsigned)p.kv_heads);
-    if (p.head_dim <= 64)
-        launch_k(combine_kernel<T, 4>, grid, dim3(128), 0, st, p);
-    else if (p.head_dim <= 128)
-        launch_k(combine_kernel<T, 8>, grid, dim3(128), 0, st, p);
-    else
-        launch_k(combine_kernel<T, 16>, grid, dim3(128), 0, st, p);
-}
 dflash2_status launch_combine(const DeviceInfo &, const Params &p, int32_t dtype, cudaStream_t st) {
+    const dim3 grid((unsigned)p.total_q, (unsigned)p.kv_heads);
     if (dtype == DFLASH2_F32)
-        combine_typed<float>(p, st);
+        launch_k(combine_kernel<float>, grid, dim3(kJoinThreads), 0, st, p);
     else
-        combine_typed<__nv_bfloat16>(p, st);
+        launch_k(combine_kernel<__nv_bfloat16>, grid, dim3(kJoinThreads), 0, st, p);
     return launch_status();
 }
 
