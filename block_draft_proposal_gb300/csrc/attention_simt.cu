@@ -415,13 +415,12 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const Params p) {
 }
 
 template <typename T, typename C, bool kPaged, int kRows, int kDMax>
-dflash2_status launch_one(Params p, bool vec_q, bool vec_k, cudaStream_t st) {
+dflash2_status launch_one(Params p, int device, bool vec_q, bool vec_k, cudaStream_t st) {
     constexpr int kSmem = simt_smem_floats(kRows, kDMax) * 4;
     auto fn = simt_kernel<T, C, kPaged, kRows, kDMax>;
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) {
-        cudaGetLastError();
-        return DFLASH2_ERR_CUDA;
-    }
+    static std::atomic<uint64_t> done{0};
+    const dflash2_status allowed = allow_smem(fn, kSmem, device, done);
+    if (allowed != DFLASH2_OK) return allowed;
     p.row_shift = kRows == 16 ? 4 : 6;
     dim3 grid((unsigned)p.n_cta);
     if (!kPaged)  // every row block of every request, and at most one short one each
@@ -432,17 +431,17 @@ dflash2_status launch_one(Params p, bool vec_q, bool vec_k, cudaStream_t st) {
 }
 
 template <typename T, typename C, bool kPaged>
-dflash2_status launch_typed(const Params &p, bool vec_q, bool vec_k, cudaStream_t st) {
+dflash2_status launch_typed(const Params &p, int device, bool vec_q, bool vec_k, cudaStream_t st) {
     // few rows per (request, head) on average: the 16-row tile
     const bool few = (int64_t)p.total_q * p.group <= 16ll * p.batch;
     if (p.head_dim <= 64)
-        return few ? launch_one<T, C, kPaged, 16, 64>(p, vec_q, vec_k, st)
-                   : launch_one<T, C, kPaged, 64, 64>(p, vec_q, vec_k, st);
+        return few ? launch_one<T, C, kPaged, 16, 64>(p, device, vec_q, vec_k, st)
+                   : launch_one<T, C, kPaged, 64, 64>(p, device, vec_q, vec_k, st);
     if (p.head_dim <= 128)
-        return few ? launch_one<T, C, kPaged, 16, 128>(p, vec_q, vec_k, st)
-                   : launch_one<T, C, kPaged, 64, 128>(p, vec_q, vec_k, st);
-    return few ? launch_one<T, C, kPaged, 16, 256>(p, vec_q, vec_k, st)
-               : launch_one<T, C, kPaged, 64, 256>(p, vec_q, vec_k, st);
+        return few ? launch_one<T, C, kPaged, 16, 128>(p, device, vec_q, vec_k, st)
+                   : launch_one<T, C, kPaged, 64, 128>(p, device, vec_q, vec_k, st);
+    return few ? launch_one<T, C, kPaged, 16, 256>(p, device, vec_q, vec_k, st)
+               : launch_one<T, C, kPaged, 64, 256>(p, device, vec_q, vec_k, st);
 }
 
 bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -462,18 +461,18 @@ dflash2_status launch_simt(const DeviceInfo &di, Params p, bool paged, int32_t d
     dflash2_status s;
     if (dtype == DFLASH2_F32) {
         if (!paged)
-            s = launch_typed<float, float, false>(p, vec_q, vec_k, st);
+            s = launch_typed<float, float, false>(p, di.device, vec_q, vec_k, st);
         else if (kv_format == DFLASH2_KV_E4M3)
-            s = launch_typed<float, uint8_t, true>(p, vec_q, vec_k, st);
+            s = launch_typed<float, uint8_t, true>(p, di.device, vec_q, vec_k, st);
         else
-            s = launch_typed<float, float, true>(p, vec_q, vec_k, st);
+            s = launch_typed<float, float, true>(p, di.device, vec_q, vec_k, st);
     } else {
         if (!paged)
-            s = launch_typed<__nv_bfloat16, __nv_bfloat16, false>(p, vec_q, vec_k, st);
+            s = launch_typed<__nv_bfloat16, __nv_bfloat16, false>(p, di.device, vec_q, vec_k, st);
         else if (kv_format == DFLASH2_KV_E4M3)
-            s = launch_typed<__nv_bfloat16, uint8_t, true>(p, vec_q, vec_k, st);
+            s = launch_typed<__nv_bfloat16, uint8_t, true>(p, di.device, vec_q, vec_k, st);
         else
-            s = launch_typed<__nv_bfloat16, __nv_bfloat16, true>(p, vec_q, vec_k, st);
+            s = launch_typed<__nv_bfloat16, __nv_bfloat16, true>(p, di.device, vec_q, vec_k, st);
     }
     if (s != DFLASH2_OK || !paged) return s;
     p.row_shift = (int64_t)p.total_q * p.group <= 16ll * p.batch ? 4 : 6;

@@ -1576,10 +1576,9 @@ template <int kD, bool kE4M3, bool kPaged>
 dflash2_status launch_one(const DeviceInfo &di, Params p, cudaStream_t st) {
     using C = Cfg<kD, kE4M3>;
     auto fn = tc_kernel<kD, kE4M3, kPaged>;
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) {
-        cudaGetLastError();
-        return DFLASH2_ERR_CUDA;
-    }
+    static std::atomic<uint64_t> done{0};
+    const dflash2_status allowed = allow_smem(fn, C::kSmem, di.device, done);
+    if (allowed != DFLASH2_OK) return allowed;
     CUtensorMap maps[2];
     for (int i = 0; i < 2; ++i) {
         const void *base = i ? p.v : p.k;

@@ -13,6 +13,8 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <atomic>
+
 #include "../../include/dflash2.h"
 
 namespace dflash2 {
@@ -83,6 +85,20 @@ dflash2_status encode_tmap_2d(CUtensorMap *map, const void *base, uint64_t rows,
 dflash2_status encode_tmap_3d(CUtensorMap *map, const void *base, const uint64_t (&dims)[3],
                               const uint64_t (&strides)[2], const uint32_t (&box)[3],
                               uint32_t elem_bytes);
+
+// Lets `kernel` use `bytes` of dynamic shared memory on the current device, once
+// per kernel and device (`done`: one bit per device, one word per kernel).
+template <typename Kernel>
+inline dflash2_status allow_smem(Kernel *kernel, int bytes, int device, std::atomic<uint64_t> &done) {
+    const uint64_t bit = 1ull << (device & 63);
+    if (done.load(std::memory_order_relaxed) & bit) return DFLASH2_OK;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+        cudaGetLastError();
+        return DFLASH2_ERR_CUDA;
+    }
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return DFLASH2_OK;
+}
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 

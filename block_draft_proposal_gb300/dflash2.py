@@ -62,6 +62,8 @@ class Dflash2Error(RuntimeError):
 def library():
     """Load libdflash2.so once and declare the C signatures."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -174,8 +176,9 @@ def _ptr(t):
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:  # torch.cuda.current_stream() without building a Stream object
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    return ctypes.c_void_p(stream.cuda_stream)
 
 
 def _need(t: torch.Tensor, name: str, dtype=None, shape=None):
@@ -185,7 +188,7 @@ def _need(t: torch.Tensor, name: str, dtype=None, shape=None):
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -739,9 +742,9 @@ def _need_rows(t: torch.Tensor, name: str, dtype, shape) -> int:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    n, heads, d = t.shape
+    n, heads, d = shape
     st = t.stride()
     if (st[2] != 1 and d > 1) or (st[1] != d and heads > 1):
         raise ValueError(f"{name} must have contiguous heads")
@@ -792,10 +795,12 @@ def kv_cache_read(cache: KVCache, slots, dtype=torch.bfloat16, k_out=None, v_out
     n = slots.numel()
     if k_out is None:
         k_out = torch.empty((n, heads, d), dtype=dtype, device=slots.device)
+    else:
+        _need(k_out, "k_out", dtype, (n, heads, d))
     if v_out is None:
-        v_out = torch.empty((n, heads, d), dtype=dtype, device=slots.device)
-    _need(k_out, "k_out", dtype, (n, heads, d))
-    _need(v_out, "v_out", dtype, (n, heads, d))
+        v_out = torch.empty_like(k_out)
+    else:
+        _need(v_out, "v_out", dtype, (n, heads, d))
     if err is None:
         err = torch.zeros(1, dtype=torch.int32, device=slots.device)
     _check("dflash2_kv_cache_read", library().dflash2_kv_cache_read(
@@ -836,11 +841,12 @@ def tree_attention(q, cache: KVCache, page_table, cu_q, kv_lens, scale: float, t
     dev = q.device
     if out is None:
         out = torch.empty((total, heads, d), dtype=q.dtype, device=dev)
-    _need(out, "out", q.dtype, (total, heads, d))
-    if lse is None and with_lse:
-        lse = torch.empty((total, heads), dtype=torch.float32, device=dev)
+    else:
+        _need(out, "out", q.dtype, (total, heads, d))
     if lse is not None:
         _need(lse, "lse", torch.float32, (total, heads))
+    elif with_lse:
+        lse = torch.empty((total, heads), dtype=torch.float32, device=dev)
     if workspace is None:
         workspace = torch.empty(max(1, tree_attention_workspace_size(total, batch, heads, kv_heads,
                                                                      d)),
@@ -879,11 +885,12 @@ def prompt_attention(q, k, v, cu_q, scale: float, out=None, lse=None, with_lse: 
     dev = q.device
     if out is None:
         out = torch.empty((total, heads, d), dtype=q.dtype, device=dev)
-    _need(out, "out", q.dtype, (total, heads, d))
-    if lse is None and with_lse:
-        lse = torch.empty((total, heads), dtype=torch.float32, device=dev)
+    else:
+        _need(out, "out", q.dtype, (total, heads, d))
     if lse is not None:
         _need(lse, "lse", torch.float32, (total, heads))
+    elif with_lse:
+        lse = torch.empty((total, heads), dtype=torch.float32, device=dev)
     if workspace is None:
         workspace = torch.empty(max(1, prompt_attention_workspace_size(total, batch, heads,
                                                                        kv_heads, d)),
