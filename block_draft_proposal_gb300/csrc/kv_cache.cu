@@ -1,15 +1,15 @@
 // Paged key/value cache: write (with E4M3 quantisation) and read back.
 //
-// A row is one (token, keys or values, head): head_dim values.  Rows are
-// numbered (token * 2 + which) * kv_heads + head, so neighbouring rows are
-// neighbours in the packed tensor and the cache's 64 .. 512 byte rows are the
-// scattered side.  Both operators move each byte once and compute next to
-// nothing; HBM bounds them once the rows fill the GPU, a launch below that.
+// Both operators move each byte once and compute next to nothing; HBM bounds them
+// once the rows fill the GPU, a launch below that.
 //
-// Fast path (head_dim 64, 128 or 256): kLanes = head_dim / 8 lanes hold a row,
-// 8 values each, and every lane group takes kUnroll rows at once so that a
-// thread has that many 16-byte loads in flight.  The row's largest magnitude is a
-// shuffle over those lanes.
+// Fast path (head_dim 64, 128 or 256): a warp takes the keys or the values of one
+// token, so the slot is read and split into page and offset once for all heads;
+// kLanes = head_dim / 8 lanes hold a row, 8 values each, and a thread has four
+// rows' loads in flight.  The row's largest magnitude is a shuffle over its lanes.
+// (A warp per two rows of any token, with its divisions for every row, was bound by
+// instructions: 51 us for 20011 tokens x 8 heads written as E4M3, 165 us for 100003
+// tokens read.)
 #include "kernels.h"
 
 namespace dflash2 {
@@ -23,7 +23,7 @@ struct KvArgs {
     void *ko, *vo;      // packed rows (read: output)
     int64_t k_stride, v_stride;
     const int64_t *slots;
-    int32_t n_rows;  // 2 * n_tokens * kv_heads
+    int32_t n_tokens, n_rows;  // n_rows = 2 * n_tokens * kv_heads
     int32_t kv_heads, head_dim, page_size;
     int64_t n_slots;
     void *kc, *vc;
@@ -46,14 +46,15 @@ template <typename T> __device__ __forceinline__ void store_raw8(T *p, const Raw
 #pragma unroll
     for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4 *>(p)[i] = r.w[i];
 }
-__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
-    const float4 b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+__device__ __forceinline__ void as_floats(const Raw8<float> &r, float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        x[4 * i] = __uint_as_float(r.w[i].x), x[4 * i + 1] = __uint_as_float(r.w[i].y);
+        x[4 * i + 2] = __uint_as_float(r.w[i].z), x[4 * i + 3] = __uint_as_float(r.w[i].w);
+    }
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8]) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p));
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+__device__ __forceinline__ void as_floats(const Raw8<__nv_bfloat16> &r, float (&x)[8]) {
+    const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         x[2 * i] = __uint_as_float(w[i] << 16);
@@ -101,140 +102,146 @@ struct Row {
     int head;
     bool values;
 };
-// `first` is the one lane of the row that reports a bad slot.
+// Row of head 0 of a token in the cache arrays, or -1; the rows of the next heads
+// follow at page_size.  `first` is the one lane that reports a bad slot.
+__device__ __forceinline__ int64_t find_token(const KvArgs &a, int64_t token, bool first) {
+    const int64_t slot = __ldg(a.slots + token);
+    if (slot >= a.n_slots) {
+        if (first && a.err) atomicOr(a.err, DFLASH2_DEVERR_ID_RANGE);
+        return -1;
+    }
+    if (slot < 0) return -1;
+    int64_t page, off;
+    if (a.n_slots <= 0xFFFFFFFFll) {  // 32-bit division when the slots allow it
+        page = (uint32_t)slot / (uint32_t)a.page_size;
+        off = (uint32_t)slot - (uint32_t)page * (uint32_t)a.page_size;
+    } else {
+        page = slot / a.page_size;
+        off = slot - page * a.page_size;
+    }
+    return page * a.kv_heads * a.page_size + off;
+}
 __device__ __forceinline__ Row find_row(const KvArgs &a, int32_t r, bool first) {
     Row o;
     const uint32_t th = (uint32_t)r / (uint32_t)a.kv_heads;
     o.head = r - (int32_t)(th * (uint32_t)a.kv_heads);
     o.values = th & 1u;
     o.token = th >> 1;
-    const int64_t slot = __ldg(a.slots + o.token);
-    o.at = -1;
-    if (slot >= a.n_slots) {
-        if (first && a.err) atomicOr(a.err, DFLASH2_DEVERR_ID_RANGE);
-    } else if (slot >= 0) {
-        int64_t page, off;
-        if (a.n_slots <= 0xFFFFFFFFll) {  // 32-bit division when the slots allow it
-            page = (uint32_t)slot / (uint32_t)a.page_size;
-            off = (uint32_t)slot - (uint32_t)page * (uint32_t)a.page_size;
-        } else {
-            page = slot / a.page_size;
-            off = slot - page * a.page_size;
-        }
-        o.at = (page * a.kv_heads + o.head) * a.page_size + off;
-    }
+    const int64_t at = find_token(a, o.token, first);
+    o.at = at < 0 ? -1 : at + (int64_t)o.head * a.page_size;
     return o;
 }
 
-template <typename T, bool kE4M3, int kLanes, int kUnroll>
+constexpr int kUnroll = 4;
+
+template <typename T, bool kE4M3, int kLanes>
 __global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvArgs a) {
-    constexpr int kDim = kLanes * 8;
+    constexpr int kDim = kLanes * 8, kRows = 32 / kLanes;  // rows a warp holds at once
     grid_dep_wait();
-    const int lane = threadIdx.x % kLanes;
-    const int32_t groups = kThreads / kLanes;
-    const int64_t r0 = (int64_t)blockIdx.x * groups * kUnroll + threadIdx.x / kLanes;
-    Row row[kUnroll];
-    float x[kUnroll][8];
-    Raw8<T> raw[kUnroll];
+    const int lane = threadIdx.x % kLanes, sub = (threadIdx.x & 31) / kLanes;
+    const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const int64_t token = w >> 1;
+    if (token >= a.n_tokens) return;
+    const bool values = w & 1;
+    const int64_t at = find_token(a, token, (threadIdx.x & 31) == 0 && !values);
+    if (at < 0) return;
+    const T *src = (values ? (const T *)a.v + token * a.v_stride : (const T *)a.k + token * a.k_stride) + lane * 8;
+    void *cache = values ? a.vc : a.kc;
+    uint8_t *exps = values ? a.ve : a.ke;
+    for (int h0 = sub; h0 - sub < a.kv_heads; h0 += kRows * kUnroll) {
+        Raw8<T> raw[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-        const int64_t r = r0 + u * groups;
-        row[u].at = -1;
-        if (r >= a.n_rows) continue;
-        row[u] = find_row(a, (int32_t)r, lane == 0);
-        if (row[u].at < 0) continue;
-        const T *src = row[u].values ? (const T *)a.v + row[u].token * a.v_stride
-                                     : (const T *)a.k + row[u].token * a.k_stride;
-        src += (int64_t)row[u].head * kDim + lane * 8;
-        if constexpr (kE4M3)
-            load8(src, x[u]);
-        else
-            raw[u] = load_raw8(src);
-    }
+        for (int u = 0; u < kUnroll; ++u) {
+            raw[u] = Raw8<T>{};
+            if (h0 + u * kRows < a.kv_heads) raw[u] = load_raw8(src + (int64_t)(h0 + u * kRows) * kDim);
+        }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-        if constexpr (!kE4M3) {
-            if (row[u].at >= 0)
-                store_raw8((T *)(row[u].values ? a.vc : a.kc) + row[u].at * kDim + lane * 8, raw[u]);
-        } else {
-            float amax = 0.0f;
-            if (row[u].at >= 0) {
+        for (int u = 0; u < kUnroll; ++u) {
+            const int h = h0 + u * kRows;
+            const int64_t row = at + (int64_t)h * a.page_size;
+            if constexpr (!kE4M3) {
+                if (h < a.kv_heads) store_raw8((T *)cache + row * kDim + lane * 8, raw[u]);
+            } else {
+                float x[8], amax = 0.0f;
+                as_floats(raw[u], x);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[u][i]));
-            }
+                for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
 #pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1)
-                amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-            if (row[u].at >= 0) {
+                for (int o = kLanes / 2; o > 0; o >>= 1)
+                    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
                 const int e = row_exponent(amax);
                 const float s = pow2i(-e);
-                uint32_t w[2];
+                uint32_t c[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float *y = x[u] + 4 * i;
+                    const float *y = x + 4 * i;
                     const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0] * s, y[1] * s),
                                                                  __NV_SATFINITE, __NV_E4M3);
                     const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2] * s, y[3] * s),
                                                                  __NV_SATFINITE, __NV_E4M3);
-                    w[i] = lo | (hi << 16);
+                    c[i] = lo | (hi << 16);
                 }
-                uint8_t *dst = (uint8_t *)(row[u].values ? a.vc : a.kc) + row[u].at * kDim + lane * 8;
-                *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
-                if (lane == 0) (row[u].values ? a.ve : a.ke)[row[u].at] = (uint8_t)(e + 127);
+                if (h < a.kv_heads) {
+                    *reinterpret_cast<uint2 *>((uint8_t *)cache + row * kDim + lane * 8) = make_uint2(c[0], c[1]);
+                    if (lane == 0) exps[row] = (uint8_t)(e + 127);
+                }
             }
         }
     }
 }
 
-template <typename T, bool kE4M3, int kLanes, int kUnroll>
+template <typename T, bool kE4M3, int kLanes>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvArgs a) {
-    constexpr int kDim = kLanes * 8;
+    constexpr int kDim = kLanes * 8, kRows = 32 / kLanes;
     grid_dep_wait();
-    const int lane = threadIdx.x % kLanes;
-    const int32_t groups = kThreads / kLanes;
-    const int64_t r0 = (int64_t)blockIdx.x * groups * kUnroll + threadIdx.x / kLanes;
-    Row row[kUnroll];
-    Raw8<T> raw[kUnroll];
-    uint2 c[kUnroll];
-    int e[kUnroll];
+    const int lane = threadIdx.x % kLanes, sub = (threadIdx.x & 31) / kLanes;
+    const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const int64_t token = w >> 1;
+    if (token >= a.n_tokens) return;
+    const bool values = w & 1;
+    const int64_t at = find_token(a, token, (threadIdx.x & 31) == 0 && !values);
+    const void *cache = values ? a.vc : a.kc;
+    const uint8_t *exps = values ? a.ve : a.ke;
+    T *dst = (T *)(values ? a.vo : a.ko) + token * a.kv_heads * kDim + lane * 8;
+    for (int h0 = sub; h0 < a.kv_heads; h0 += kRows * kUnroll) {
+        Raw8<T> raw[kUnroll];
+        uint2 c[kUnroll];
+        int e[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-        const int64_t r = r0 + u * groups;
-        raw[u] = Raw8<T>{};
-        c[u] = make_uint2(0u, 0u);
-        e[u] = 0;
-        row[u].token = -1;
-        if (r >= a.n_rows) continue;
-        row[u] = find_row(a, (int32_t)r, lane == 0);
-        if (row[u].at < 0) continue;
-        const void *src = row[u].values ? a.vc : a.kc;
-        if constexpr (kE4M3) {
-            c[u] = __ldg(reinterpret_cast<const uint2 *>((const uint8_t *)src + row[u].at * kDim) + lane);
-            e[u] = (int)__ldg((row[u].values ? a.ve : a.ke) + row[u].at) - 127;
-        } else {
-            raw[u] = load_raw8((const T *)src + row[u].at * kDim + lane * 8);
-        }
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-        if (row[u].token < 0) continue;
-        T *dst = (row[u].values ? (T *)a.vo : (T *)a.ko) +
-                 (row[u].token * a.kv_heads + row[u].head) * kDim + lane * 8;
-        if constexpr (kE4M3) {
-            float x[8];
-            const float s = ldexpf(1.0f, e[u]);
-            const uint32_t w[2] = {c[u].x, c[u].y};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-                    (__nv_fp8x2_storage_t)(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
-                const float2 f = __half22float2(__half2(h));
-                x[2 * i] = f.x * s;
-                x[2 * i + 1] = f.y * s;
+        for (int u = 0; u < kUnroll; ++u) {
+            const int h = h0 + u * kRows;
+            const int64_t row = at + (int64_t)h * a.page_size;
+            raw[u] = Raw8<T>{};
+            c[u] = make_uint2(0u, 0u);
+            e[u] = 0;
+            if (at < 0 || h >= a.kv_heads) continue;
+            if constexpr (kE4M3) {
+                c[u] = __ldg(reinterpret_cast<const uint2 *>((const uint8_t *)cache + row * kDim) + lane);
+                e[u] = (int)__ldg(exps + row) - 127;
+            } else {
+                raw[u] = load_raw8((const T *)cache + row * kDim + lane * 8);
             }
-            store8(dst, x);
-        } else {
-            store_raw8(dst, raw[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int h = h0 + u * kRows;
+            if (h >= a.kv_heads) continue;
+            if constexpr (kE4M3) {
+                float x[8];
+                const float s = ldexpf(1.0f, e[u]);
+                const uint32_t b[2] = {c[u].x, c[u].y};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const __half2_raw y = __nv_cvt_fp8x2_to_halfraw2(
+                        (__nv_fp8x2_storage_t)(b[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
+                    const float2 f = __half22float2(__half2(y));
+                    x[2 * i] = f.x * s;
+                    x[2 * i + 1] = f.y * s;
+                }
+                store8(dst + (int64_t)h * kDim, x);
+            } else {
+                store_raw8(dst + (int64_t)h * kDim, raw[u]);
+            }
         }
     }
 }
@@ -290,22 +297,13 @@ __global__ void __launch_bounds__(kThreads) kv_read_scalar(const KvArgs a) {
     }
 }
 
-// Rows per lane group: four once the rows fill every SM several times over
-// (measured at 100003 tokens x 8 heads), one below that, where more CTAs in
-// flight answer sooner (measured at 512 tokens x 8 heads).
-constexpr int kManyRows = 152 * 8 * (kThreads / 16) * 4;
-
 template <typename T, bool kE4M3, bool kWrite, int kLanes>
 dflash2_status launch_lanes(const KvArgs &a, cudaStream_t st) {
-    const int groups = kThreads / kLanes;
-    const int per = a.n_rows >= kManyRows ? 4 : 1;
-    const unsigned grid = (unsigned)(((int64_t)a.n_rows + groups * per - 1) / (groups * per));
-    void (*fn)(const KvArgs);
+    const unsigned grid = (unsigned)((2ll * a.n_tokens + kThreads / 32 - 1) / (kThreads / 32));
     if constexpr (kWrite)
-        fn = per == 4 ? kv_write_kernel<T, kE4M3, kLanes, 4> : kv_write_kernel<T, kE4M3, kLanes, 1>;
+        launch_k(kv_write_kernel<T, kE4M3, kLanes>, dim3(grid), dim3(kThreads), 0, st, a);
     else
-        fn = per == 4 ? kv_read_kernel<T, kE4M3, kLanes, 4> : kv_read_kernel<T, kE4M3, kLanes, 1>;
-    launch_k(fn, dim3(grid), dim3(kThreads), 0, st, a);
+        launch_k(kv_read_kernel<T, kE4M3, kLanes>, dim3(grid), dim3(kThreads), 0, st, a);
     return launch_status();
 }
 
@@ -336,6 +334,7 @@ dflash2_status check_kv(KvArgs *a, const int64_t *slots, int64_t n_tokens, int32
         n_tokens >= (1ll << 30) / kv_heads + ((1ll << 30) % kv_heads ? 1 : 0))
         return DFLASH2_ERR_INVALID_ARG;
     a->slots = slots;
+    a->n_tokens = (int32_t)n_tokens;
     a->n_rows = (int32_t)(2 * n_tokens * kv_heads);
     a->kv_heads = kv_heads;
     a->head_dim = head_dim;
