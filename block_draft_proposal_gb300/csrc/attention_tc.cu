@@ -77,6 +77,7 @@ struct Shared {
     uint64_t full[8], empty[8];  // operand ring (E4M3: filled by the widening warps)
     uint64_t guard_go[8], guard_done[8];  // value tiles handed to the guard warp and back, in order
     uint64_t s_full[2], p_full[2][2], o_full[2];  // weights come in halves of 64 keys
+    uint64_t turn[2];            // shared: whose weights' and next scores' MMAs come next
     uint64_t q_full, drain[2];
     uint32_t tmem;
     int abort_flag;
@@ -554,6 +555,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
             mbar_init(&sh.p_full[i][1], 4);
             mbar_init(&sh.o_full[i], 1);
             mbar_init(&sh.drain[i], 1);
+            mbar_init(&sh.turn[i], 1);
         }
         mbar_init(&sh.q_full, 8);
         sh.abort_flag = 0;
@@ -793,7 +795,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                 constexpr uint32_t kIdS = kE4M3 ? idesc_e4m3(kTile, kTile) : idesc16(false, kTile, false);
                 constexpr uint32_t kIdO = idesc16(kE4M3, kD, true);
                 const uint32_t dS = s * kTile, dO = 256 + s * kD;
-                uint32_t pos = 0, tiles_done = 0, n_piece = 0, n_guard = 0, n_p = 0;
+                uint32_t pos = 0, tiles_done = 0, n_piece = 0, n_guard = 0, n_p = 0, n_turn = 0;
                 bool ok = true;
                 Piece pc{};
                 // an operand's place: bf16, operand n of the ring; E4M3, by key tile
@@ -874,27 +876,40 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                     // alternate: K0 K1 V0 K2 V1 ... V(n-2) V(n-1), tile j mine if j % 2 == s
                     const bool both = pc.shared();
                     const int32_t n_mine = both && s == 0 ? pc.t1a - pc.t0 : n;
-                    for (int32_t j = both ? 0 : -1; ok && j < n; ++j) {
-                        // key j (shared) or j + 1 (alternate), then value j
-                        const int32_t jk = both ? j : j + 1;
-                        if (jk < n) {
-                            Place o;
-                            if constexpr (kE4M3) {
-                                const uint32_t kt = tiles_done + jk, i = kt % C::kKRaw;
-                                o = Place{&sh.kraw_full[i], &sh.kraw_empty[i], (kt / C::kKRaw) & 1u,
-                                          sm_kraw + i * C::kRawBytes};
-                            } else {
-                                o = ring(pos + (both ? 2 * jk : jk == 0 ? 0 : 2 * jk - 1));
-                            }
-                            ok = keys(o, both ? jk < n_mine : (jk & 1) == s, both && s == 1);
+                    auto key = [&](int32_t j) {
+                        Place o;
+                        if constexpr (kE4M3) {
+                            const uint32_t kt = tiles_done + j, i = kt % C::kKRaw;
+                            o = Place{&sh.kraw_full[i], &sh.kraw_empty[i], (kt / C::kKRaw) & 1u,
+                                      sm_kraw + i * C::kRawBytes};
+                        } else {
+                            o = ring(pos + (both ? 2 * j : j == 0 ? 0 : 2 * j - 1));
                         }
-                        if (ok && j >= 0) {
-                            const Place o = ring(kE4M3 ? tiles_done + j
-                                                       : pos + (both ? 2 * j + 1 : j + 1 < n ? 2 * j + 2 : 2 * n - 1));
-                            const bool mine = both ? j < n_mine : (j & 1) == s;
-                            ok = values(pc.t0 + j, o, mine, both ? j > 0 : j >= 2,
-                                        both ? j + 1 == n_mine : j + 2 >= n);
+                        return keys(o, both ? j < n_mine : (j & 1) == s, both && s == 1);
+                    };
+                    // the next scores follow the sums that free their place: key j + 1 after
+                    // value j of both slots, or key j + 2 after value j of its own
+                    if (ok) ok = key(0);
+                    if (ok && !both && n > 1) ok = key(1);
+#pragma unroll 1
+                    for (int32_t j = 0; ok && j < n; ++j) {
+                        // shared: the slots' MMAs take turns, a tile's sums and the next scores
+                        // together, so that one slot's softmax runs beside the other's MMAs
+                        // (issued as they come, both slots fall into step and neither does:
+                        // 3400 cycles per tile and pair of slots against 2500)
+                        if (both) {
+                            ok = bar_wait(&sh.turn[s], (n_turn & 1u) ^ (s == 0 ? 1u : 0u), abort_flag, p.err);
+                            if (!ok) break;
+                            ++n_turn;
                         }
+                        const Place o = ring(kE4M3 ? tiles_done + j
+                                                   : pos + (both ? 2 * j + 1 : j + 1 < n ? 2 * j + 2 : 2 * n - 1));
+                        const bool mine = both ? j < n_mine : (j & 1) == s;
+                        ok = values(pc.t0 + j, o, mine, both ? j > 0 : j >= 2,
+                                    both ? j + 1 == n_mine : j + 2 >= n);
+                        const int32_t next = both ? j + 1 : j + 2;
+                        if (ok && next < n) ok = key(next);
+                        if (both) mbar_arrive(&sh.turn[s ^ 1]);
                     }
                     tiles_done += n;
                     pos += 2 * n;
