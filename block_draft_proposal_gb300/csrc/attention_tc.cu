@@ -92,8 +92,8 @@ struct SharedE4M3 : Shared {
     TileScale scale[4];
     int reduce[2][4][2];
     float qmul[2][kRowBlock];                // 2^a scale log2(e) of a row, by piece parity
-    int8_t vexp[4][kTile];                   // value exponents of 4 tiles
     alignas(16) float kmul[4][kTile];        // 2^ke of the keys of 4 tiles
+    alignas(16) float vmul[4][kTile];        // 2^ve
     alignas(16) uint8_t exps[4][2][kTile];   // exponent bytes as copied
 };
 
@@ -221,6 +221,15 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::DF_OUT32(
             DF_USE, r),
         "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
         : "memory");
 }
 
@@ -1001,7 +1010,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                 int *red = sh.reduce[no & 1u][warp - 12];
                 if (lane == 0) red[0] = vt, red[1] = vb;
                 sh.kmul[i][row] = pow2_int(ke);
-                sh.vexp[i][row] = (int8_t)ve;
+                sh.vmul[i][row] = pow2_int(ve);
                 named_sync<2, 128>();
                 int v_top = -64, v_low = 64;
 #pragma unroll
@@ -1026,49 +1035,57 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                 const uint32_t src = sm_vraw + rs * C::kRawBytes + row * kD;
                 const uint32_t dst = sm_ring + s * C::kTileBytes + row * 128;
                 if (!bar_wait(&sh.vraw_full[rs], (no / C::kVRaw) & 1u, abort_flag, p.err)) return false;
-                uint32_t w[kD / 16][4];  // 16 codes a chunk; the copy's swizzle spreads the rows over the banks
+                if (!bar_wait(&sh.empty[s], ((no / kStages) & 1u) ^ 1u, abort_flag, p.err)) return false;
+                const bool fix = tile >= pc.guard_from || !live;
+                const __half2 m2 = *reinterpret_cast<const __half2 *>(&mul);
+                bool found = false;
+                // 16 codes a chunk, two at a time; the copy's swizzle spreads the rows over the banks
+#pragma unroll 1
+                for (int c0 = 0; c0 < kD / 16; c0 += 2) {
+                    uint32_t w[2][4];
 #pragma unroll
-                for (int c = 0; c < kD / 16; ++c) {
-                    const uint32_t a = src + ((kD == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3)) << 4);
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(w[c][0]), "=r"(w[c][1]), "=r"(w[c][2]), "=r"(w[c][3])
-                                 : "r"(a));
-                }
-                if (tile >= pc.guard_from || !live) {
-                    bool found = false;
+                    for (int e = 0; e < 2; ++e) {
+                        const int c = c0 + e;
+                        const uint32_t a = src + ((kD == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3)) << 4);
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(w[e][0]), "=r"(w[e][1]), "=r"(w[e][2]), "=r"(w[e][3])
+                                     : "r"(a));
+                    }
+                    if (fix) {
 #pragma unroll
-                    for (int c = 0; c < kD / 16; ++c)
+                        for (int e = 0; e < 2; ++e)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            if (!live) w[c][k] = 0u;
-                            const uint32_t nan = __vcmpeq4(w[c][k] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-                            if (nan) found = true, w[c][k] &= ~nan;
+                            for (int k = 0; k < 4; ++k) {
+                                if (!live) w[e][k] = 0u;
+                                const uint32_t nan = __vcmpeq4(w[e][k] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                                found |= nan != 0;
+                                w[e][k] &= ~nan;
+                            }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int c = c0 + e;
+                        uint32_t o[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const __half2 h = __hmul2(
+                                __half2(__nv_cvt_fp8x2_to_halfraw2(
+                                    (__nv_fp8x2_storage_t)(w[e][k >> 1] >> (16 * (k & 1))), __NV_E4M3)),
+                                m2);
+                            o[k] = *reinterpret_cast<const uint32_t *>(&h);
                         }
-                    if (found) *(volatile int *)&sh.poison = (int)n_piece;
+                        const uint32_t d0 = dst + (c >> 2) * (kTile * 128);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                             d0 + (((2 * (c & 3) + k) ^ (row & 7)) << 4)),
+                                         "r"(o[4 * k]), "r"(o[4 * k + 1]), "r"(o[4 * k + 2]), "r"(o[4 * k + 3])
+                                         : "memory");
+                    }
                 }
+                if (found) *(volatile int *)&sh.poison = (int)n_piece;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.vraw_empty[rs]);
-                if (!bar_wait(&sh.empty[s], ((no / kStages) & 1u) ^ 1u, abort_flag, p.err)) return false;
-                const __half2 m2 = *reinterpret_cast<const __half2 *>(&mul);
-#pragma unroll
-                for (int c = 0; c < kD / 16; ++c) {
-                    uint32_t o[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const __half2 h = __hmul2(
-                            __half2(__nv_cvt_fp8x2_to_halfraw2(
-                                (__nv_fp8x2_storage_t)(w[c][k >> 1] >> (16 * (k & 1))), __NV_E4M3)),
-                            m2);
-                        o[k] = *reinterpret_cast<const uint32_t *>(&h);
-                    }
-                    const uint32_t d0 = dst + (c >> 2) * (kTile * 128);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                         d0 + (((2 * (c & 3) + k) ^ (row & 7)) << 4)),
-                                     "r"(o[4 * k]), "r"(o[4 * k + 1]), "r"(o[4 * k + 2]), "r"(o[4 * k + 3])
-                                     : "memory");
-                }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.full[s]);
@@ -1218,8 +1235,14 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                     tmem_st32(tO + c, o);
                 }
             };
+            auto hand_over = [&](int h) {
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.p_full[s][h]);
+            };
             // One key tile: this warp's kC chunks of 32 keys, from chunk c0 on.
-            auto tile = [&](auto chunks, const int c0, const int32_t t, const uint32_t i4) {
+            [[maybe_unused]] auto tile = [&](auto chunks, const int c0, const int32_t t) {
                 constexpr int kC = decltype(chunks)::value;
                 uint32_t x[kC][32];
                 const bool masked = (t + 1) * kTile > all_seen;
@@ -1233,20 +1256,6 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                     tmem_ld_wait();
 #pragma unroll
                     for (int c = 0; c < kC; ++c) tmem_tie(x[c]);
-                    if constexpr (kE4M3) {
-#pragma unroll
-                        for (int c = 0; c < kC; ++c)
-#pragma unroll
-                            for (int k = 0; k < 32; k += 4) {
-                                const ulonglong2 f =
-                                    *reinterpret_cast<const ulonglong2 *>(&sh.kmul[i4][32 * (c0 + c) + k]);
-                                float a, b;
-                                unf2(mul2(f2(x[c][k], x[c][k + 1]), f.x), a, b);
-                                x[c][k] = __float_as_uint(a), x[c][k + 1] = __float_as_uint(b);
-                                unf2(mul2(f2(x[c][k + 2], x[c][k + 3]), f.y), a, b);
-                                x[c][k + 2] = __float_as_uint(a), x[c][k + 3] = __float_as_uint(b);
-                            }
-                    }
                     if (masked) {
 #pragma unroll
                         for (int c = 0; c < kC; ++c)
@@ -1258,7 +1267,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                 uint64_t part[4];
                 const uint64_t qm2 = f2(qm, qm);
                 uint32_t pk[32];
-                // weights of the chunks [from, to): 2^(z - base); E4M3 keeps them in x
+                // weights of the chunks [from, to): 2^(z - base)
                 auto weights = [&](int from, int to, float safe) {
                     const uint64_t off2 = f2(-safe, -safe);
 #pragma unroll
@@ -1271,10 +1280,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                             a = ex2(a);
                             b = ex2(b);
                             part[(k >> 1) & 3] = add2(part[(k >> 1) & 3], f2(a, b));
-                            if constexpr (kE4M3)
-                                x[c][k] = __float_as_uint(a), x[c][k + 1] = __float_as_uint(b);
-                            else
-                                pk[16 * (c & 1) + (k >> 1)] = pack16<false>(a, b);
+                            pk[16 * (c & 1) + (k >> 1)] = pack16<false>(a, b);
                         }
                     }
                 };
@@ -1290,12 +1296,6 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                                   __uint_as_float(x[k >> 5][(k & 31) + 1]));
                     return fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])),
                                  fmaxf(fmaxf(top[4], top[5]), fmaxf(top[6], top[7]))) * qm;
-                };
-                auto hand_over = [&](int h) {
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.p_full[s][h]);
                 };
                 // few rows: this copy's weights, zeros at the other copies' keys
                 auto store_split = [&]() {
@@ -1314,39 +1314,83 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                     hand_over(0);
                     if (lane == 0) mbar_arrive(&sh.p_full[s][1]);
                 };
-                if constexpr (!kE4M3) {
-                    // the first weights against the base so far, beside the maximum; again,
-                    // from the scores in TMEM, where the maximum moved the base (the first
-                    // tiles, mostly)
-                    constexpr int kFirst = kC == 4 ? 2 : kC;
+                // the first weights against the base so far, beside the maximum; again, from
+                // the scores in TMEM, where the maximum moved the base (the first tiles,
+                // mostly)
+                constexpr int kFirst = kC == 4 ? 2 : kC;
 #pragma unroll 1
-                    for (bool again = false;;) {
-                        scores();
-                        const float mx = row_top();
-                        part[0] = part[1] = part[2] = part[3] = 0ull;
-                        weights(0, kFirst, base == -INFINITY ? 0.0f : base);
-                        if (again) break;
-                        const bool grow = mx > base + kLazy;
-                        if (!__any_sync(0xFFFFFFFFu, grow)) break;
-                        // grow: base was -inf (fix = 0, nothing summed yet) or finite
-                        const float fix = grow ? ex2(base - mx) : 1.0f;
-                        if (grow) base = mx;
-                        sum *= fix;
-                        rescale(fix);
-                        again = true;
-                    }
-                    if constexpr (kC == 4) {
-                        tmem_st32(tS, pk);
-                        hand_over(0);
-                        weights(2, 4, base == -INFINITY ? 0.0f : base);
-                        tmem_st32(tS + 32, pk);
-                        hand_over(1);
-                    } else {
-                        store_split();
-                    }
-                } else {
+                for (bool again = false;;) {
                     scores();
                     const float mx = row_top();
+                    part[0] = part[1] = part[2] = part[3] = 0ull;
+                    weights(0, kFirst, base == -INFINITY ? 0.0f : base);
+                    if (again) break;
+                    const bool grow = mx > base + kLazy;
+                    if (!__any_sync(0xFFFFFFFFu, grow)) break;
+                    // grow: base was -inf (fix = 0, nothing summed yet) or finite
+                    const float fix = grow ? ex2(base - mx) : 1.0f;
+                    if (grow) base = mx;
+                    sum *= fix;
+                    rescale(fix);
+                    again = true;
+                }
+                if constexpr (kC == 4) {
+                    tmem_st32(tS, pk);
+                    hand_over(0);
+                    weights(2, 4, base == -INFINITY ? 0.0f : base);
+                    tmem_st32(tS + 32, pk);
+                    hand_over(1);
+                } else {
+                    store_split();
+                }
+                float a, b;
+                unf2(add2(add2(part[0], part[1]), add2(part[2], part[3])), a, b);
+                sum += a + b;
+                first = false;
+            };
+            // The same with E4M3 scales, chunk by chunk from TMEM, once for the maximum and
+            // once for the weights: one short body for every number of chunks, since these
+            // warps share the instruction cache with the widening ones (unrolled as above,
+            // every second issue slot waited for an instruction).
+            [[maybe_unused]] auto tile_e4m3 = [&](const int c0, const int c1, const int32_t t, const uint32_t i4) {
+                if constexpr (kE4M3) {
+                    const bool masked = (t + 1) * kTile > all_seen;
+                    uint32_t x[32];
+                    // chunk c's scores times 2^ke, -inf where not seen
+                    auto scores = [&](int c) {
+                        tmem_ld32(tS + 32 * c, x);
+                        const uint32_t w =
+                            masked && live_row ? seen_bits<kPaged>(p, pc.rq, tok, t * kTile + 32 * c) : 0u;
+                        tmem_ld_wait();
+                        tmem_tie(x);
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4) {
+                            const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(&sh.kmul[i4][32 * c + k]);
+                            float a, b;
+                            unf2(mul2(f2(x[k], x[k + 1]), f.x), a, b);
+                            x[k] = __float_as_uint(a), x[k + 1] = __float_as_uint(b);
+                            unf2(mul2(f2(x[k + 2], x[k + 3]), f.y), a, b);
+                            x[k + 2] = __float_as_uint(a), x[k + 3] = __float_as_uint(b);
+                        }
+                        if (masked) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (!((w >> k) & 1u)) x[k] = 0xFF800000u;  // -inf
+                        }
+                    };
+                    const bool once = c1 - c0 == 1;  // the scores stay in registers
+                    float mx = -INFINITY;
+#pragma unroll 1
+                    for (int c = c0; c < c1; ++c) {
+                        scores(c);
+                        float top[4] = {mx, mx, mx, mx};
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2)
+                            top[(k >> 1) & 3] = fmaxf(fmaxf(top[(k >> 1) & 3], __uint_as_float(x[k])),
+                                                      __uint_as_float(x[k + 1]));
+                        mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                    }
+                    mx *= qm;
                     const bool grow = mx > base + kLazy;
                     const float nb = grow ? mx : base;
                     const float safe = nb == -INFINITY ? 0.0f : nb;
@@ -1354,24 +1398,20 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                     float fix = grow ? ex2(base - nb) : 1.0f;
                     base = nb;
                     sum *= fix;
-                    part[0] = part[1] = part[2] = part[3] = 0ull;
-                    weights(0, kC, safe);
                     // binade of the largest weight with its value's scale
                     const TileScale ts = sh.scale[i4];
                     int v_exp = ts.value;
                     int level = v_exp + (int)floorf(fmaxf(mx - safe, -4096.0f));
                     bool some = mx > -INFINITY;
-                    if (ts.wide) {
+                    if (ts.wide) {  // the scales differ too much: look at each weight
                         float hi = 0.0f;
+#pragma unroll 1
+                        for (int c = c0; c < c1; ++c) {
+                            if (!once) scores(c);
 #pragma unroll
-                        for (int c = 0; c < kC; ++c)
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) {
-                                const float u = __uint_as_float(x[c][k]) *
-                                                __uint_as_float((uint32_t)(127 + sh.vexp[i4][32 * (c0 + c) + k]) << 23);
-                                hi = fmaxf(hi, u);
-                                x[c][k] = __float_as_uint(u);
-                            }
+                            for (int k = 0; k < 32; ++k)
+                                hi = fmaxf(hi, ex2(fmaf(__uint_as_float(x[k]), qm, -safe)) * sh.vmul[i4][32 * c + k]);
+                        }
                         level = (int)(__float_as_uint(hi) >> 23) - 127;
                         some = hi > 0.0f;
                         v_exp = 0;
@@ -1384,37 +1424,42 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                     }
                     if (__any_sync(0xFFFFFFFFu, fix != 1.0f)) rescale(had ? fix : 0.0f);
                     const float down = had || some ? pow2_int(v_exp - x_shift) : 1.0f;
-                    const uint64_t down2 = f2(down, down);
-                    auto pack = [&](int from) {  // two chunks (kC == 1: one)
+                    const uint64_t down2 = f2(down, down), qm2 = f2(qm, qm), off2 = f2(-safe, -safe);
+                    uint64_t part[2] = {0ull, 0ull};
+#pragma unroll 1
+                    for (int c = c0; c < c1; ++c) {
+                        if (!once) scores(c);
+                        uint32_t pk[16];
 #pragma unroll
-                        for (int c = 0; c < kC; ++c) {
-                            if (c < from || c >= from + 2) continue;
-#pragma unroll
-                            for (int k = 0; k < 32; k += 2) {
-                                float a, b;
-                                unf2(mul2(f2(x[c][k], x[c][k + 1]), down2), a, b);
-                                pk[16 * (c & 1) + (k >> 1)] = pack16<true>(a, b);
-                            }
+                        for (int k = 0; k < 32; k += 2) {
+                            float a, b;
+                            unf2(fma2(f2(x[k], x[k + 1]), qm2, off2), a, b);
+                            const uint64_t w2 = f2(ex2(a), ex2(b));
+                            part[(k >> 1) & 1] = add2(part[(k >> 1) & 1], w2);
+                            uint64_t u2 = mul2(w2, down2);
+                            if (ts.wide)
+                                u2 = mul2(u2, *reinterpret_cast<const uint64_t *>(&sh.vmul[i4][32 * c + k]));
+                            unf2(u2, a, b);
+                            pk[k >> 1] = pack16<true>(a, b);
                         }
-                    };
-                    pack(0);
-                    if constexpr (kC == 4) {
-                        tmem_st32(tS, pk);
-                        hand_over(0);
-                        pack(2);
-                        tmem_st32(tS + 32, pk);
-                        hand_over(1);
-                    } else {
-                        store_split();
+                        tmem_st16(tS + 16 * c, pk);  // over scores of chunk c / 2: done, or in registers
+                        if (c == 1 && c1 == 4) hand_over(0);
                     }
+                    // few rows: zeros at the other copies' keys
+                    const uint32_t zero[16] = {};
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c)
+                        if (c < c0 || c >= c1) tmem_st16(tS + 16 * c, zero);
+                    hand_over(1);
+                    if (c1 - c0 < 4 && lane == 0) mbar_arrive(&sh.p_full[s][0]);
+                    float a, b;
+                    unf2(add2(part[0], part[1]), a, b);
+                    sum += a + b;
+                    first = false;
                 }
-                float a, b;
-                unf2(add2(add2(part[0], part[1]), add2(part[2], part[3])), a, b);
-                sum += a + b;
-                first = false;
             };
             for (int32_t t = pc.t0 + (both ? 0 : s); t < t_end; t += both ? 1 : 2) {
-                const uint32_t tile_no = tiles_done + (uint32_t)(t - pc.t0);
+                [[maybe_unused]] const uint32_t tile_no = tiles_done + (uint32_t)(t - pc.t0);
                 if constexpr (kE4M3) {
                     ok = bar_wait(&sh.sc_full[tile_no & 3u], (tile_no >> 2) & 1u, abort_flag, p.err);
                     if (!ok) break;
@@ -1430,17 +1475,16 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                     }
                     continue;
                 }
-                if constexpr (kPaged) {
-                    if (split == 2) {
-                        tile(std::integral_constant<int, 1>{}, copy, t, tile_no & 3u);
-                        continue;
-                    }
-                    if (split == 1) {
-                        tile(std::integral_constant<int, 2>{}, 2 * copy, t, tile_no & 3u);
-                        continue;
-                    }
+                if constexpr (kE4M3) {
+                    const int chunks = 4 >> split;
+                    tile_e4m3(copy * chunks, (copy + 1) * chunks, t, tile_no & 3u);
+                } else if (!kPaged || split == 0) {
+                    tile(std::integral_constant<int, 4>{}, 0, t);
+                } else if (split == 1) {
+                    tile(std::integral_constant<int, 2>{}, 2 * copy, t);
+                } else {
+                    tile(std::integral_constant<int, 1>{}, copy, t);
                 }
-                tile(std::integral_constant<int, 4>{}, 0, t, tile_no & 3u);
             }
             if (!ok) break;
             // ---- epilogue ----
