@@ -36,7 +36,8 @@ extern "C" size_t dflash2_tree_attention_workspace_size(int32_t total_q, int32_t
                                                         int32_t head_dim) {
     if (check_shape(batch, total_q, q_heads, kv_heads, head_dim, 1.0f, DFLASH2_BF16) != DFLASH2_OK)
         return 0;
-    return (size_t)(2 * kWorkspaceCtas *
+    return sizeof(attn::Join) * kWorkspaceCtas +
+           (size_t)(2 * kWorkspaceCtas *
                     attn::part_slot_floats(slot_rows(total_q, q_heads / kv_heads), head_dim)) * 4;
 }
 
@@ -80,7 +81,8 @@ extern "C" dflash2_status dflash2_tree_attention(
     p.mask_words = mask_words, p.batch = batch, p.total_q = total_q, p.q_heads = q_heads;
     p.kv_heads = kv_heads, p.group = q_heads / kv_heads, p.head_dim = head_dim;
     p.scale_log2 = scale * 1.4426950408889634f, p.out = out, p.lse = lse;
-    p.part = static_cast<float *>(workspace), p.part_rows = slot_rows(total_q, p.group), p.err = err_word;
+    p.join = static_cast<attn::Join *>(workspace);
+    p.part = reinterpret_cast<float *>(p.join + kWorkspaceCtas), p.part_rows = slot_rows(total_q, p.group), p.err = err_word;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (attn::tc_takes(p, true, dtype, kv_format)) return attn::launch_tc(di, p, true, kv_format, s);
     return attn::launch_simt(di, p, true, dtype, kv_format, s);

@@ -44,7 +44,8 @@ struct Params {
     float scale_log2;              // scale * log2(e)
     void *out;
     float *lse;
-    float *part;                   // paged: partial rows, kPartSlots(C) slots
+    struct Join *join;             // paged: one per CTA, then
+    float *part;                   // the partial rows' slots
     int32_t part_rows;             // rows of a slot
     int32_t row_shift;             // log2 of the rows of a block
     int32_t item_units;            // units of an item beside its key tiles
@@ -63,6 +64,17 @@ __host__ __device__ inline int64_t part_slot_floats(int32_t part_rows, int32_t h
 __host__ __device__ inline int64_t part_stats(int32_t part_rows, int32_t head_dim) {
     return (int64_t)part_rows * ((head_dim + 3) / 4 * 4);
 }
+
+// The item that CTA c starts and does not end, for combine_kernel; every CTA
+// writes its own.
+struct alignas(16) Join {
+    int32_t rows;  // live rows, or 0: there is none
+    int32_t last;  // the CTA that ends it
+    int32_t row0;  // its first row
+    int32_t t0;    // the request's first packed token
+    int32_t h;     // key/value head
+    int32_t pad[3];
+};
 
 struct Request {
     int32_t t0, t;    // first packed token, tokens
@@ -132,11 +144,11 @@ __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t *red) {
     return s;
 }
 
-// Where CTA blockIdx.x begins: all units, its range [u, end), and the request
+// Where CTA `cta` of the split begins: all units, its range [u, end), and the request
 // that holds u with the units before that request.  Every thread of the block
 // calls it; block sums and one scan per blockDim requests.
 struct Start {
-    int64_t u, end, before;
+    int64_t u, end, before, units;
     int32_t b;
 };
 struct StartScratch {
@@ -144,7 +156,7 @@ struct StartScratch {
     int64_t before;
     int32_t b;
 };
-__device__ __forceinline__ Start find_start(const Params &p, StartScratch *s, bool *any_bad) {
+__device__ __forceinline__ Start find_start(const Params &p, int64_t cta, StartScratch *s, bool *any_bad) {
     bool bad;
     int64_t mine = 0, n = 0;
     for (int b = threadIdx.x; b < p.batch; b += blockDim.x) {
@@ -157,9 +169,10 @@ __device__ __forceinline__ Start find_start(const Params &p, StartScratch *s, bo
     const int64_t n_cta = split_ctas(p, units);
     o.u = o.end = o.before = 0;
     o.b = 0;
-    if (blockIdx.x >= n_cta) return o;
-    o.u = range_start(blockIdx.x, units, n_cta);
-    o.end = range_start((int64_t)blockIdx.x + 1, units, n_cta);
+    o.units = units;
+    if (cta >= n_cta) return o;
+    o.u = range_start(cta, units, n_cta);
+    o.end = range_start(cta + 1, units, n_cta);
     int64_t passed = 0;
     for (int b0 = 0; b0 < p.batch; b0 += blockDim.x) {
         const int b = b0 + threadIdx.x;

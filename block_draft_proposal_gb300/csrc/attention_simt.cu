@@ -258,9 +258,10 @@ __global__ void __launch_bounds__(kThreads) simt_kernel(const Params p, bool vec
     grid_dep_launch();
     bool bad = false, any_bad = false;
     if constexpr (kPaged) {
-        const Start s = find_start(p, &scratch, &any_bad);
+        const Start s = find_start(p, blockIdx.x, &scratch, &any_bad);
         int64_t u = s.u, before = s.before;  // units before request b
         const int64_t end = s.end;
+        Join join{};
         for (int b = s.b; b < p.batch && u < end; ++b) {
             const Request r = load_request<true>(p, b, &bad);
             const int64_t n = request_units(p, r);
@@ -277,10 +278,17 @@ __global__ void __launch_bounds__(kThreads) simt_kernel(const Params p, bool vec
                         p, r, b, (int32_t)(item / nrb), (int32_t)(item % nrb), t0 * kKeyTile,
                         min(t1 * kKeyTile, r.len), whole ? -1 : 2 * (int64_t)blockIdx.x + (t0 == 0),
                         smem, vec_q, vec_k, &any_bad);
+                if (t0 == 0 && t1 > 0 && !whole) {
+                    const int32_t row0 = (int32_t)(item % nrb) * kRows;
+                    join.rows = min(kRows, r.t * p.group - row0);
+                    join.last = cta_of(u - o0 + worth - 1, s.units, split_ctas(p, s.units));
+                    join.row0 = row0, join.t0 = r.t0, join.h = (int32_t)(item / nrb);
+                }
                 u += o1 - o0;
             }
             before += n;
         }
+        if (threadIdx.x == 0) p.join[blockIdx.x] = join;
     } else {
         // CTA (x, h): row block number `want` of all requests, the last blocks
         // (which see the most keys) first
@@ -319,59 +327,25 @@ __global__ void __launch_bounds__(kThreads) simt_kernel(const Params p, bool vec
     if (any_bad && p.err) atomicOr(p.err, DFLASH2_DEVERR_ID_RANGE);
 }
 
-// Joins the partial rows of items that span CTAs, in CTA order.  A CTA takes the
-// group's rows of one token and key/value head, a thread four values of a row
-// (neighbouring threads neighbouring rows, which neighbour in a slot).  Where the
-// partials lie follows from cu_q and kv_lens alone and is worked out before the
-// attention kernel ends; what is left then is one read of them, four at a time.
-constexpr int kJoinThreads = 128;
+// Joins the partial rows of items whose tiles span CTAs, in CTA order.  CTA (x, y)
+// takes rows 8 y .. of the item that attention CTA x starts and does not end, a
+// thread four values of a row (neighbouring threads neighbouring rows, which
+// neighbour in a slot): one read of the partials, four at a time.
+constexpr int kJoinRows = 8;
 template <typename T>
-__global__ void __launch_bounds__(kJoinThreads) combine_kernel(const Params p) {
-    __shared__ int64_t red[32];
-    __shared__ int32_t which;
-    const int32_t tok = blockIdx.x, h = blockIdx.y;
-    // before the grid dependency only what was complete before the attention
-    // kernel started is read: cu_q and kv_lens (it releases this grid after its
-    // own wait)
-    bool bad;
-    int64_t all = 0, mine = 0;
-    if (threadIdx.x == 0) which = -1;
-    __syncthreads();
-    for (int b = threadIdx.x; b < p.batch; b += kJoinThreads) {
-        const Request r = load_request<true>(p, b, &bad);
-        const int64_t n = request_units(p, r);
-        all += n;
-        if (r.t0 + r.t <= tok) mine += n;  // requests before the token's
-        if (tok >= r.t0 && tok < r.t0 + r.t) which = b;
-    }
-    const int64_t units = block_sum(all, red);
-    const int64_t before = block_sum(mine, red);
-    Request r{};
-    int32_t tiles = 0, c0 = 0, c1 = 0, rr = 0;
-    const int d = p.head_dim, quads = (d + 3) / 4;
-    const int64_t n_cta = split_ctas(p, units);
-    // the CTAs that hold the row's item, and the row in its block
-    auto place = [&](int32_t g) {
-        const int32_t row = (tok - r.t0) * p.group + g, rb = row >> p.row_shift;
-        rr = row & ((1 << p.row_shift) - 1);
-        const int64_t u0 = before + ((int64_t)h * row_blocks(p, r) + rb) * (tiles + p.item_units) + p.item_units;
-        c0 = cta_of(u0, units, n_cta);
-        c1 = cta_of(u0 + tiles - 1, units, n_cta);
-    };
-    if (which >= 0) {
-        r = load_request<true>(p, which, &bad);
-        tiles = key_tiles(r);
-        place(threadIdx.x % p.group);
-    }
-    const int64_t slot_floats = part_slot_floats(p.part_rows, d), stats = part_stats(p.part_rows, d);
+__global__ void __launch_bounds__(kThreads) combine_kernel(const Params p) {
     grid_dep_wait();
-    if (which < 0) return;
-    for (int i = threadIdx.x; i < p.group * quads; i += kJoinThreads) {
-        const int32_t g = i % p.group, c = i / p.group;
-        if (i >= kJoinThreads) place(g);
-        if (c0 == c1) continue;  // the attention kernel wrote this row
-        const float *first = p.part + (2 * (int64_t)c0 + 1) * slot_floats;  // the item's start
-        const float *rest = p.part + 2 * (int64_t)(c0 + 1) * slot_floats;
+    const int32_t rr = blockIdx.y * kJoinRows + (threadIdx.x & (kJoinRows - 1));
+    const int4 j = __ldcg(reinterpret_cast<const int4 *>(p.join + blockIdx.x));  // rows, last, row0, t0
+    const int32_t h = __ldcg(&p.join[blockIdx.x].h);
+    if (rr >= j.x) return;
+    const int32_t c0 = blockIdx.x, c1 = j.y, row = j.z + rr;
+    const int d = p.head_dim, quads = (d + 3) / 4;
+    const int64_t slot_floats = part_slot_floats(p.part_rows, d), stats = part_stats(p.part_rows, d);
+    const float *first = p.part + (2 * (int64_t)c0 + 1) * slot_floats;  // the item's start
+    const float *rest = p.part + 2 * (int64_t)(c0 + 1) * slot_floats;
+    const int64_t at = (int64_t)(j.w + row / p.group) * p.q_heads + h * p.group + row % p.group;
+    for (int c = threadIdx.x / kJoinRows; c < quads; c += kThreads / kJoinRows) {
         float m = -INFINITY, l = 0.0f;
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         for (int32_t k = c0; k <= c1; k += 4) {
@@ -379,12 +353,12 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const Params p) {
             float4 v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float *s = k + e == c0 ? first : rest + (int64_t)(k + e - c0 - 1) * 2 * slot_floats;
+                const float *part = k + e == c0 ? first : rest + (int64_t)(k + e - c0 - 1) * 2 * slot_floats;
                 mk[e] = -INFINITY, lk[e] = 0.0f, v[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 if (k + e <= c1) {
-                    mk[e] = __ldcg(s + stats + rr);
-                    lk[e] = __ldcg(s + stats + p.part_rows + rr);
-                    v[e] = __ldcg(reinterpret_cast<const float4 *>(s) + (int64_t)c * p.part_rows + rr);
+                    mk[e] = __ldcg(part + stats + rr);
+                    lk[e] = __ldcg(part + stats + p.part_rows + rr);
+                    v[e] = __ldcg(reinterpret_cast<const float4 *>(part) + (int64_t)c * p.part_rows + rr);
                 }
             }
             const float top = fmaxf(m, fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])));
@@ -403,7 +377,6 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const Params p) {
             m = top;
         }
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        const int64_t at = (int64_t)tok * p.q_heads + h * p.group + g;
         T *dst = (T *)p.out + at * d + 4 * c;
         const float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
 #pragma unroll
@@ -480,11 +453,14 @@ dflash2_status launch_simt(const DeviceInfo &di, Params p, bool paged, int32_t d
 }
 
 dflash2_status launch_combine(const DeviceInfo &, const Params &p, int32_t dtype, cudaStream_t st) {
-    const dim3 grid((unsigned)p.total_q, (unsigned)p.kv_heads);
+    if (p.n_cta < 2) return DFLASH2_OK;
+    // no row block is longer than its size or than all rows
+    const int64_t all = (int64_t)p.total_q * p.group, most = all < (1 << p.row_shift) ? all : 1 << p.row_shift;
+    const dim3 grid((unsigned)(p.n_cta - 1), (unsigned)((most + kJoinRows - 1) / kJoinRows));
     if (dtype == DFLASH2_F32)
-        launch_k(combine_kernel<float>, grid, dim3(kJoinThreads), 0, st, p);
+        launch_k(combine_kernel<float>, grid, dim3(kThreads), 0, st, p);
     else
-        launch_k(combine_kernel<__nv_bfloat16>, grid, dim3(kJoinThreads), 0, st, p);
+        launch_k(combine_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, st, p);
     return launch_status();
 }
 

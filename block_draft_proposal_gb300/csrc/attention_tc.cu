@@ -38,14 +38,11 @@
 // E4M3.  S = q' k' on the codes themselves, with q' = q 2^-a as two codes, the nearest
 // one and that of the rest (a per row, so that |q'| < 2^8): together they hold the
 // eight bits of a bf16 value down to 2^-10 of the row's largest, and 2^-18 of that
-// below.  z = S 2^(key scale) 2^a scale log2(e).  Value codes are widened to fp16,
-// a row's scale going in as far as fp16 is exact: code * 2^d, d = 7 for the tile's
-// largest scale.  The tile's exponent goes into the weights: P = 2^(z - base)
-// 2^(tile - x), where the row's integer x follows the largest 2^(z - base) 2^(value
-// scale) as lazily as base follows z, so that weights fit fp16 whatever the scales
-// are (a tile whose value scales span more than fp16 holds exactly has them applied
-// to its weights key by key).  All of these are powers of two: the sum of the
-// weights does not depend on the values.
+// below.  z = S 2^(key scale) 2^a scale log2(e).  Value codes are widened to fp16, which
+// holds them, and a value row's scale goes into its weight: P = 2^(z - base)
+// 2^(value scale) 2^-x, where the row's integer x follows the largest of them as
+// lazily as base follows z, so that weights fit fp16 whatever the scales are.  All of
+// these are powers of two: the sum of the weights does not depend on the values.
 #include <type_traits>
 
 #include "attention.cuh"
@@ -58,14 +55,14 @@ constexpr int kTile = 128;       // keys per tile, rows per slot
 constexpr int kRowShift = 8, kRowBlock = 1 << kRowShift;
 constexpr int kItemUnits = 4;    // an item's start and end cost about as much as four key tiles
 constexpr float kLazy = 8.0f;    // log2 growth of the maximum that forces a rescale
-constexpr int kTopE4M3 = 6;      // fp16 weights: the largest starts below 2^7 ...
+constexpr int kTopE4M3 = 6;      // fp16 weights: the largest (or its bound) starts below 2^7 ...
 constexpr int kCapE4M3 = 14;     // ... and x moves before one reaches 2^15
 constexpr int kNoShift = -1000;  // no weight yet
 
 // Barriers and small state, behind the operand rings in dynamic shared memory.
 struct TileScale {  // E4M3
-    int32_t value;  // binary exponent of a tile's value operand
-    int32_t wide;   // bare value codes: scales per key
+    int32_t top;   // largest binary exponent of a tile's value scales
+    int32_t wide;  // they span more than 22 binades
 };
 struct Piece;
 constexpr int kPieces = 4;
@@ -328,12 +325,14 @@ static_assert(sizeof(Piece) <= kPieceBytes, "piece");
 
 // Paged: walks CTA blockIdx.x's range of units.
 struct Walk {
-    int64_t u, end, before, n;
+    int64_t u, end, before, n, units;
     int32_t b;
     Request rq;
+    Join join;  // the item that the range starts and does not end
     __device__ __forceinline__ void begin(const Params &p, const Start &s) {
         bool bad;
-        u = s.u, end = s.end, before = s.before, b = s.b;
+        join = Join{};
+        u = s.u, end = s.end, before = s.before, b = s.b, units = s.units;
         n = 0;
         if (u < end) {
             rq = load_request<true>(p, b, &bad);
@@ -375,6 +374,10 @@ struct Walk {
             pc->n_rows = min(kRowBlock, rq.t * p.group - pc->row0);
             pc->slot = pc->t0 == 0 && o1 == (int32_t)worth ? -1 : 2 * (int32_t)blockIdx.x + (pc->t0 == 0);
             pc->guard_from = rq.ctx / kTile;
+            if (pc->slot >= 0 && pc->t0 == 0) {
+                join.rows = pc->n_rows, join.row0 = pc->row0, join.t0 = rq.t0, join.h = pc->h;
+                join.last = cta_of(u - o1 + worth - 1, units, split_ctas(p, units));
+            }
             return;
         }
     }
@@ -585,7 +588,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
     bool bad = false;
     Start start{};
     if constexpr (kPaged) {
-        start = find_start(p, &sh.start, &bad);
+        start = find_start(p, blockIdx.x, &sh.start, &bad);
         if (bad && p.err && blockIdx.x == 0) atomicOr(p.err, DFLASH2_DEVERR_ID_RANGE);
     }
     tc_fence_before();
@@ -776,6 +779,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                 ++n_piece;
                 if (__any_sync(0xFFFFFFFFu, !ok) || pc.n_rows == 0) break;
             }
+            if (kPaged && of_keys && lane == 0) p.join[blockIdx.x] = walk.join;
             if ((bad_page || (!kPaged && bad && blockIdx.x == 0)) && p.err)
                 atomicOr(p.err, DFLASH2_DEVERR_ID_RANGE);
             if (!ok) {  // wait for the copies in flight before the shared memory goes
@@ -986,17 +990,13 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
             }
         }
     } else if (warp >= 12) {
-        // ---- E4M3: value codes to fp16, relative to the tile's largest scale ----
-        // A value row becomes code * 2^d with d = 7 for the tile's largest scale, exact for
-        // d >= -15.  A tile whose value scales span more than 22 binades ("wide") keeps bare
-        // codes, and the softmax applies the scales key by key.
+        // ---- E4M3: value codes to fp16 (exact), and the scales of both to fp32 ----
         regs_give<C::kRegsFew>();
         if constexpr (kE4M3) {
             uint32_t n_piece = 0, tiles_done = 0;
             bool ok = true;
             const int row = threadIdx.x - 384;
             Piece pc{};
-            uint32_t mul0 = 0, mul1 = 0;  // half2 factors of this row in an even and an odd tile
             // the scales of key tile number `no`
             auto scales = [&](int32_t tile, uint32_t no) {
                 const uint32_t i = no & 3u;
@@ -1018,26 +1018,21 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                     v_top = max(v_top, sh.reduce[no & 1u][w][0]);
                     v_low = min(v_low, sh.reduce[no & 1u][w][1]);
                 }
-                const bool wide = v_top - v_low > 22 && v_top > -64;
                 if (row == 0) {
-                    sh.scale[i].value = v_top - 7;
-                    sh.scale[i].wide = wide;
+                    sh.scale[i].top = v_top;
+                    sh.scale[i].wide = v_top - v_low > 22;  // no live row: -64 and 64
                     mbar_arrive(&sh.sc_full[i]);
                 }
-                const __half2 h = __half2half2(__float2half_rn(pow2_int(wide || !live ? 0 : max(ve - v_top + 7, -24))));
-                (no & 1u ? mul1 : mul0) = *reinterpret_cast<const uint32_t *>(&h);
                 return true;
             };
             auto widen = [&](int32_t tile, uint32_t no) {
                 const uint32_t rs = no % C::kVRaw, s = no % kStages;
                 const bool live = tile * kTile + row < pc.rq.len;
-                const uint32_t mul = no & 1u ? mul1 : mul0;
                 const uint32_t src = sm_vraw + rs * C::kRawBytes + row * kD;
                 const uint32_t dst = sm_ring + s * C::kTileBytes + row * 128;
                 if (!bar_wait(&sh.vraw_full[rs], (no / C::kVRaw) & 1u, abort_flag, p.err)) return false;
                 if (!bar_wait(&sh.empty[s], ((no / kStages) & 1u) ^ 1u, abort_flag, p.err)) return false;
                 const bool fix = tile >= pc.guard_from || !live;
-                const __half2 m2 = *reinterpret_cast<const __half2 *>(&mul);
                 bool found = false;
                 // 16 codes a chunk, two at a time; the copy's swizzle spreads the rows over the banks
 #pragma unroll 1
@@ -1068,10 +1063,8 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                         uint32_t o[8];
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
-                            const __half2 h = __hmul2(
-                                __half2(__nv_cvt_fp8x2_to_halfraw2(
-                                    (__nv_fp8x2_storage_t)(w[e][k >> 1] >> (16 * (k & 1))), __NV_E4M3)),
-                                m2);
+                            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+                                (__nv_fp8x2_storage_t)(w[e][k >> 1] >> (16 * (k & 1))), __NV_E4M3);
                             o[k] = *reinterpret_cast<const uint32_t *>(&h);
                         }
                         const uint32_t d0 = dst + (c >> 2) * (kTile * 128);
@@ -1398,10 +1391,10 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                     float fix = grow ? ex2(base - nb) : 1.0f;
                     base = nb;
                     sum *= fix;
-                    // binade of the largest weight with its value's scale
+                    // binade of the largest weight with its value's scale: at most the largest
+                    // weight's and the largest scale's
                     const TileScale ts = sh.scale[i4];
-                    int v_exp = ts.value;
-                    int level = v_exp + (int)floorf(fmaxf(mx - safe, -4096.0f));
+                    int level = ts.top + (int)floorf(fmaxf(mx - safe, -4096.0f));
                     bool some = mx > -INFINITY;
                     if (ts.wide) {  // the scales differ too much: look at each weight
                         float hi = 0.0f;
@@ -1414,7 +1407,6 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                         }
                         level = (int)(__float_as_uint(hi) >> 23) - 127;
                         some = hi > 0.0f;
-                        v_exp = 0;
                     }
                     const bool had = x_shift != kNoShift;
                     if (some && (grow || level - x_shift >= kCapE4M3)) {
@@ -1423,7 +1415,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                         x_shift = nx;
                     }
                     if (__any_sync(0xFFFFFFFFu, fix != 1.0f)) rescale(had ? fix : 0.0f);
-                    const float down = had || some ? pow2_int(v_exp - x_shift) : 1.0f;
+                    const float down = had || some ? pow2_int(-x_shift) : 1.0f;
                     const uint64_t down2 = f2(down, down), qm2 = f2(qm, qm), off2 = f2(-safe, -safe);
                     uint64_t part[2] = {0ull, 0ull};
 #pragma unroll 1
@@ -1436,10 +1428,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                             unf2(fma2(f2(x[k], x[k + 1]), qm2, off2), a, b);
                             const uint64_t w2 = f2(ex2(a), ex2(b));
                             part[(k >> 1) & 1] = add2(part[(k >> 1) & 1], w2);
-                            uint64_t u2 = mul2(w2, down2);
-                            if (ts.wide)
-                                u2 = mul2(u2, *reinterpret_cast<const uint64_t *>(&sh.vmul[i4][32 * c + k]));
-                            unf2(u2, a, b);
+                            unf2(mul2(mul2(w2, down2), *reinterpret_cast<const uint64_t *>(&sh.vmul[i4][32 * c + k])), a, b);
                             pk[k >> 1] = pack16<true>(a, b);
                         }
                         tmem_st16(tS + 16 * c, pk);  // over scores of chunk c / 2: done, or in registers
