@@ -1318,7 +1318,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                     part[0] = part[1] = part[2] = part[3] = 0ull;
                     weights(0, kFirst, base == -INFINITY ? 0.0f : base);
                     if (again) break;
-                    const bool grow = mx > base + kLazy;
+                    const bool grow = live_row && mx > base + kLazy;
                     if (!__any_sync(0xFFFFFFFFu, grow)) break;
                     // grow: base was -inf (fix = 0, nothing summed yet) or finite
                     const float fix = grow ? ex2(base - mx) : 1.0f;
@@ -1384,7 +1384,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                         mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                     }
                     mx *= qm;
-                    const bool grow = mx > base + kLazy;
+                    const bool grow = live_row && mx > base + kLazy;
                     const float nb = grow ? mx : base;
                     const float safe = nb == -INFINITY ? 0.0f : nb;
                     const float gain = grow ? fminf(nb - base, 1024.0f) : 0.0f;  // 1024: base was -inf
@@ -1409,7 +1409,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                         some = hi > 0.0f;
                     }
                     const bool had = x_shift != kNoShift;
-                    if (some && (grow || level - x_shift >= kCapE4M3)) {
+                    if (live_row && some && (grow || level - x_shift >= kCapE4M3)) {
                         const int nx = max(had ? x_shift - (int)gain : -100, level - kTopE4M3);
                         if (had) fix *= pow2_int(x_shift - nx);
                         x_shift = nx;
