@@ -84,7 +84,7 @@ extern "C" dflash2_status dflash2_tree_attention(
     p.join = static_cast<attn::Join *>(workspace);
     p.part = reinterpret_cast<float *>(p.join + kWorkspaceCtas), p.part_rows = slot_rows(total_q, p.group), p.err = err_word;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (attn::tc_takes(p, true, dtype, kv_format)) return attn::launch_tc(di, p, true, kv_format, s);
+    if (attn::tc_takes(p, true, dtype)) return attn::launch_tc(di, p, true, kv_format, s);
     return attn::launch_simt(di, p, true, dtype, kv_format, s);
 }
 
@@ -124,7 +124,7 @@ extern "C" dflash2_status dflash2_prompt_attention(
     p.q_heads = q_heads, p.kv_heads = kv_heads, p.group = q_heads / kv_heads, p.head_dim = head_dim;
     p.scale_log2 = scale * 1.4426950408889634f, p.out = out, p.lse = lse, p.err = err_word;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (attn::tc_takes(p, false, dtype, DFLASH2_KV_NATIVE))
+    if (attn::tc_takes(p, false, dtype))
         return attn::launch_tc(di, p, false, DFLASH2_KV_NATIVE, s);
     return attn::launch_simt(di, p, false, dtype, DFLASH2_KV_NATIVE, s);
 }

@@ -239,7 +239,7 @@ __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bf
 dflash2_status launch_simt(const DeviceInfo &di, Params p, bool paged, int32_t dtype,
                            int32_t kv_format, cudaStream_t st);
 // attention_tc.cu: whether the tcgen05 kernel takes the call, and the call.
-bool tc_takes(const Params &p, bool paged, int32_t dtype, int32_t kv_format);
+bool tc_takes(const Params &p, bool paged, int32_t dtype);
 dflash2_status launch_tc(const DeviceInfo &di, const Params &p, bool paged, int32_t kv_format,
                          cudaStream_t st);
 dflash2_status launch_combine(const DeviceInfo &di, const Params &p, int32_t dtype, cudaStream_t st);

@@ -28,7 +28,7 @@
 // Roles: warps 0-3 and 4-7 softmax of slots 0 and 1 (and the loads of Q and the
 // epilogue); warps 8 and 10 issue the MMAs of slots 0 and 1; warp 9 the TMA loads
 // (one box per page and 64 columns); warp 11 guards the values (below); E4M3 adds warps
-// 12-15, which widen value codes to fp16 into the operand ring.
+// 12-19, which widen value codes to fp16 into the operand ring.
 //
 // What a row does not see must not reach it, but a product 0 * NaN would.  In the
 // key tiles that hold masked positions the guard warp zeroes the rows past the
@@ -81,21 +81,18 @@ struct Shared {
     int poison;                  // number of the last piece with a value not finite
     StartScratch start;
 };
-struct SharedE4M3 : Shared {
+template <int kTiles> struct SharedE4M3 : Shared {
     uint64_t kraw_full[4], kraw_empty[4];    // key codes, as the MMAs read them
     uint64_t vraw_full[4], vraw_empty[4];    // value codes, to be widened
-    uint64_t ex_full[4], ex_empty[4];        // exponent bytes of a tile
-    uint64_t sc_full[4];                     // scales of a tile, from the widening warps
-    TileScale scale[4];
-    int reduce[2][4][2];
+    uint64_t sc_full[kTiles];                // scales of a tile, from the widening warps
+    TileScale scale[kTiles];
+    int reduce[2][2][4][2];                  // by widening warpgroup and its tile's parity
     float qmul[2][kRowBlock];                // 2^a scale log2(e) of a row, by piece parity
-    alignas(16) float kmul[4][kTile];        // 2^ke of the keys of 4 tiles
-    alignas(16) float vmul[4][kTile];        // 2^ve
-    alignas(16) uint8_t exps[4][2][kTile];   // exponent bytes as copied
+    alignas(16) float kmul[kTiles][kTile];   // 2^ke of the tiles' keys
+    alignas(16) float vmul[kTiles][kTile];   // 2^ve
 };
 
 template <int kD, bool kE4M3> struct Cfg {
-    using Sh = std::conditional_t<kE4M3, SharedE4M3, Shared>;
     static constexpr int kHalves = kD / 64;            // 128-byte column blocks of a 16-bit tile
     static constexpr int kTileBytes = kTile * kD * 2;  // a 16-bit operand tile
     static constexpr int kRawBytes = kTile * kD;       // E4M3 codes of a tile
@@ -103,9 +100,13 @@ template <int kD, bool kE4M3> struct Cfg {
     static constexpr int kStages = kE4M3 ? (kD == 128 ? 2 : 4) : (kD == 128 ? 5 : 8);
     static constexpr int kKRaw = kE4M3 ? (kD == 128 ? 3 : 4) : 0, kVRaw = kE4M3 ? (kD == 128 ? 2 : 4) : 0;
     static constexpr int kRaw = kKRaw + kVRaw;
-    static constexpr int kThreads = kE4M3 ? 512 : 384;
-    // registers: softmax warps take what the others give back
-    static constexpr int kRegsMany = kE4M3 ? 192 : 216, kRegsFew = kE4M3 ? 64 : 72;
+    // a tile's scales are written after the same warps' value operand of two tiles before,
+    // which waited for the one kStages before that: kStages + 2 tiles at least
+    static constexpr int kScales = kStages <= 2 ? 4 : 8;
+    using Sh = std::conditional_t<kE4M3, SharedE4M3<kScales>, Shared>;
+    static constexpr int kThreads = kE4M3 ? 640 : 384;
+    // registers: softmax warps take what the others give back (E4M3: 96 each at launch)
+    static constexpr int kRegsMany = kE4M3 ? 144 : 216, kRegsFew = kE4M3 ? 64 : 72;
     // alternate: (base, sum, 2^x) of 2 x 128 accumulator rows and 128 reciprocal sums; head_dim
     // 128 has room for them in the second query tile, which that mode leaves unused
     static constexpr int kStatBytes = kD == 128 ? 0 : 7 * kTile * 4;
@@ -121,14 +122,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
-        : "memory");
-}
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
-                                          uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-            dst),
-        "l"(src), "r"(bytes), "r"(smem_u32(bar))
         : "memory");
 }
 // D (+)= A[tmem] * B[smem], 16-bit inputs.
@@ -548,10 +541,8 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                 mbar_init(&sh.kraw_empty[i], 2);
                 mbar_init(&sh.vraw_full[i], 1);
                 mbar_init(&sh.vraw_empty[i], 4);
-                mbar_init(&sh.ex_full[i], 2);
-                mbar_init(&sh.ex_empty[i], 2);
-                mbar_init(&sh.sc_full[i], 1);
             }
+            for (int i = 0; i < C::kScales; ++i) mbar_init(&sh.sc_full[i], 1);
         }
         for (int i = 0; i < 8; ++i) {
             mbar_init(&sh.guard_go[i], 1);
@@ -559,7 +550,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
         }
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(&sh.piece_full[i], 1);
-            mbar_init(&sh.piece_empty[i], kE4M3 ? 15 : 11);  // all but the producer
+            mbar_init(&sh.piece_empty[i], kE4M3 ? 19 : 11);  // all but the producer
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_full[i], 1);
@@ -610,7 +601,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
         regs_give<C::kRegsFew>();
         if (warp == 9 || (kE4M3 && warp == 11)) {
             // ---- producer: the pieces, and the TMA copies by one thread.  E4M3: warp 9 the
-            // keys, warp 11 the values, each with its exponent bytes ----
+            // keys, warp 11 the values ----
             const bool of_keys = !kE4M3 || warp == 9;
             uint32_t pos = 0, n_piece = 0;  // operand tiles issued
             uint32_t n_key = 0, n_value = 0;
@@ -694,27 +685,6 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                 ++pos;
                 return true;
             };
-            // E4M3: exponent bytes of key tile t0 + j, this warp's half of them
-            uint32_t n_ex = 0;
-            [[maybe_unused]] auto load_exps = [&](int32_t j) {
-                if constexpr (kE4M3) {
-                    const uint32_t i = n_ex & 3u;
-                    if (!bar_wait(&sh.ex_empty[i], ((n_ex >> 2) & 1u) ^ 1u, abort_flag, p.err)) return false;
-                    mbar_arrive_expect_tx(&sh.ex_full[i], kTile);
-                    const int32_t y = ((pc.t0 + j) * kTile) & (p.page_size - 1) & ~(kTile - 1);
-                    const int32_t *page = sh.pages[warp >> 1 & 1][(j >> 3) & 1] + ((j & 7) << box_shift);
-                    const uint8_t *src = of_keys ? p.k_exp : p.v_exp;
-                    const uint32_t dst = smem_u32(sh.exps[i][of_keys ? 0 : 1]);
-#pragma unroll 1
-                    for (int b = 0; b < (1 << box_shift); ++b) {
-                        // page 0's where there is none: any scale serves zero rows
-                        const int32_t z = max(page[b], 0) * p.kv_heads + pc.h;
-                        bulk_load(dst + b * rows_box, src + (int64_t)z * p.page_size + y, rows_box, &sh.ex_full[i]);
-                    }
-                    ++n_ex;
-                }
-                return true;
-            };
             Walk walk{};
             Levels levels{};
             if constexpr (!kPaged)
@@ -761,7 +731,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                     }
                     if (elect_one()) {
                         if constexpr (kE4M3) {
-                            for (; ok && jk < min(n, c + 8); ++jk) ok = load_exps(jk) && load(jk, !of_keys);
+                            for (; ok && jk < min(n, c + 8); ++jk) ok = load(jk, !of_keys);
                         } else {
                             // the keys of these eight tiles and the values that follow them
                             while (ok && (jk < min(n, c + 8) || (c + 8 >= n && jv < n))) {
@@ -793,7 +763,6 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                 if constexpr (kE4M3) {
                     drain(sh.kraw_full, n_key, C::kKRaw);
                     drain(sh.vraw_full, n_value, C::kVRaw);
-                    drain(sh.ex_full, n_ex, 4);
                 } else {
                     drain(sh.full, pos, kStages);
                 }
@@ -859,10 +828,8 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                             return false;
                         ++n_guard;
                     }
-                    [[maybe_unused]] const uint32_t ex = (tiles_done + (uint32_t)(t - pc.t0)) & 3u;
                     if (!mine) {
                         mbar_arrive(o.empty);
-                        if constexpr (kE4M3) mbar_arrive(&sh.ex_empty[ex]);
                         return true;
                     }
                     const uint32_t vd = desc_lo(o.addr) | kMnMajorLo;
@@ -877,7 +844,6 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                     }
                     ++n_p;
                     tc_commit(o.empty);
-                    if constexpr (kE4M3) tc_commit(&sh.ex_empty[ex]);
                     if (last) tc_commit(&sh.o_full[s]);
                     return true;
                 };
@@ -990,40 +956,60 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
             }
         }
     } else if (warp >= 12) {
-        // ---- E4M3: value codes to fp16 (exact), and the scales of both to fp32 ----
+        // ---- E4M3: value codes to fp16 (exact), and the scales of both to fp32; warps 12-15
+        // the even key tiles, warps 16-19 the odd ones ----
         regs_give<C::kRegsFew>();
         if constexpr (kE4M3) {
             uint32_t n_piece = 0, tiles_done = 0;
             bool ok = true;
-            const int row = threadIdx.x - 384;
+            const int group = warp >= 16, row = (threadIdx.x - 384) & 127;
             Piece pc{};
+            // Exponent bytes: this row's key of the group's next tile, and its page of the one
+            // after that, so that neither load is waited for.
+            const int32_t page_shift = 31 - __clz(p.page_size);
+            int32_t page = -1;
+            int ke = 0, ve = 0;
+            auto fetch_page = [&](int32_t tile) {
+                const int32_t l = tile * kTile + row;
+                page = -1;
+                if (tile < pc.t1 && l < pc.rq.len)
+                    page = __ldg(p.page_table + (int64_t)pc.b * p.max_pages + (l >> page_shift));
+            };
+            auto fetch_exps = [&](int32_t tile) {  // of `page`
+                ke = ve = 127;
+                if ((uint64_t)(int64_t)page < (uint64_t)p.num_pages) {
+                    const int32_t off = (tile * kTile + row) & (p.page_size - 1);
+                    const int64_t at = ((int64_t)page * p.kv_heads + pc.h) * p.page_size + off;
+                    ke = __ldg(p.k_exp + at);
+                    ve = __ldg(p.v_exp + at);
+                }
+            };
             // the scales of key tile number `no`
             auto scales = [&](int32_t tile, uint32_t no) {
-                const uint32_t i = no & 3u;
+                const uint32_t i = no % C::kScales;
                 const bool live = tile * kTile + row < pc.rq.len;
-                if (!bar_wait(&sh.ex_full[i], (no >> 2) & 1u, abort_flag, p.err)) return false;
                 // written exponents lie in [-48, 48]; what was never written is masked
-                const int ke = min(max((int)sh.exps[i][0][row] - 127, -48), 48);
-                const int ve = min(max((int)sh.exps[i][1][row] - 127, -48), 48);
-                const int vt = __reduce_max_sync(0xFFFFFFFFu, live ? ve : -64);
-                const int vb = __reduce_min_sync(0xFFFFFFFFu, live ? ve : 64);
-                int *red = sh.reduce[no & 1u][warp - 12];
-                if (lane == 0) red[0] = vt, red[1] = vb;
-                sh.kmul[i][row] = pow2_int(ke);
-                sh.vmul[i][row] = pow2_int(ve);
-                named_sync<2, 128>();
+                const int k_exp = min(max(ke - 127, -48), 48), v_exp = min(max(ve - 127, -48), 48);
+                fetch_exps(tile + 2);
+                fetch_page(tile + 4);
+                const int vt = __reduce_max_sync(0xFFFFFFFFu, live ? v_exp : -64);
+                const int vb = __reduce_min_sync(0xFFFFFFFFu, live ? v_exp : 64);
+                int(*red)[2] = sh.reduce[group][(no >> 1) & 1u];
+                if (lane == 0) red[warp & 3][0] = vt, red[warp & 3][1] = vb;
+                sh.kmul[i][row] = pow2_int(k_exp);
+                sh.vmul[i][row] = pow2_int(v_exp);
+                asm volatile("bar.sync %0, 128;" ::"r"(2 + group) : "memory");
                 int v_top = -64, v_low = 64;
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
-                    v_top = max(v_top, sh.reduce[no & 1u][w][0]);
-                    v_low = min(v_low, sh.reduce[no & 1u][w][1]);
+                    v_top = max(v_top, red[w][0]);
+                    v_low = min(v_low, red[w][1]);
                 }
                 if (row == 0) {
                     sh.scale[i].top = v_top;
                     sh.scale[i].wide = v_top - v_low > 22;  // no live row: -64 and 64
                     mbar_arrive(&sh.sc_full[i]);
                 }
-                return true;
             };
             auto widen = [&](int32_t tile, uint32_t no) {
                 const uint32_t rs = no % C::kVRaw, s = no % kStages;
@@ -1085,12 +1071,15 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                 return true;
             };
             while (ok && take_piece(n_piece, &pc, true)) {
-                // in the copies' order: alternate scales a tile ahead of its values
-                const int32_t n = pc.t1 - pc.t0, lead = pc.shared() ? 0 : 1;
-                int32_t jk = 0;
-                for (int32_t j = 0; ok && j < n; ++j) {
-                    for (; ok && jk < n && jk <= j + lead; ++jk) ok = scales(pc.t0 + jk, tiles_done + jk);
-                    ok = ok && widen(pc.t0 + j, tiles_done + j);
+                const int32_t n = pc.t1 - pc.t0;
+                const int32_t from = (tiles_done & 1u) == (uint32_t)group ? 0 : 1;
+                fetch_page(pc.t0 + from);
+                fetch_exps(pc.t0 + from);
+                fetch_page(pc.t0 + from + 2);
+#pragma unroll 1
+                for (int32_t j = from; ok && j < n; j += 2) {
+                    scales(pc.t0 + j, tiles_done + j);
+                    ok = widen(pc.t0 + j, tiles_done + j);
                 }
                 tiles_done += n;
                 ++n_piece;
@@ -1450,7 +1439,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
             for (int32_t t = pc.t0 + (both ? 0 : s); t < t_end; t += both ? 1 : 2) {
                 [[maybe_unused]] const uint32_t tile_no = tiles_done + (uint32_t)(t - pc.t0);
                 if constexpr (kE4M3) {
-                    ok = bar_wait(&sh.sc_full[tile_no & 3u], (tile_no >> 2) & 1u, abort_flag, p.err);
+                    ok = bar_wait(&sh.sc_full[tile_no % C::kScales], (tile_no / C::kScales) & 1u, abort_flag, p.err);
                     if (!ok) break;
                 }
                 ok = bar_wait(&sh.s_full[s], n_s & 1u, abort_flag, p.err);
@@ -1466,7 +1455,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                 }
                 if constexpr (kE4M3) {
                     const int chunks = 4 >> split;
-                    tile_e4m3(copy * chunks, (copy + 1) * chunks, t, tile_no & 3u);
+                    tile_e4m3(copy * chunks, (copy + 1) * chunks, t, tile_no % C::kScales);
                 } else if (!kPaged || split == 0) {
                     tile(std::integral_constant<int, 4>{}, 0, t);
                 } else if (split == 1) {
@@ -1536,46 +1525,65 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                 mine[2 * kTile] = up;
                 named_sync<1, 256>();
                 const int rows = kTile >> split, row_in = my & (rows - 1);
-                const int sources = (used1 ? 2 : 1) << split;  // source i: slot i >> split, copy i & ...
+                // source i: slot i >> split, copy i & (copies - 1)
+                const int sources = (used1 ? 2 : 1) << split;
+                float sb[8], sl[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float *st = stat + 3 * kTile * (i >> split) + (i & ((1 << split) - 1)) * rows + row_in;
+                    sb[i] = i < sources ? st[0] : -INFINITY;
+                    sl[i] = i < sources ? st[kTile] : 0.0f;
+                }
                 float top = -INFINITY;
-                for (int i = 0; i < sources; ++i)
-                    top = fmaxf(top, stat[3 * kTile * (i >> split) + (i & ((1 << split) - 1)) * rows + row_in]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) top = fmaxf(top, sb[i]);
                 const float safe = top == -INFINITY ? 0.0f : top;
                 const float g = ex2(base - safe) * up;
                 float all = 0.0f;
-                for (int i = 0; i < sources; ++i) {
-                    const float *st = stat + 3 * kTile * (i >> split) + (i & ((1 << split) - 1)) * rows + row_in;
-                    all = fmaf(st[kTile], ex2(st[0] - safe), all);
-                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) all = fmaf(sl[i], ex2(sb[i] - safe), all);
                 base = top;
                 sum = all;
                 owner = live_row && s == 0 && copy == 0;
                 float *inv = stat + 6 * kTile;
                 if (s == 0 && copy == 0) inv[row_in] = part ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
-                float4 *red = reinterpret_cast<float4 *>(dyn + pad);  // [source][row][8 of four], swizzled
+                // [source][row][groups of four, swizzled]: rows up to a power of two, and as many
+                // columns at a time as 32 KB hold
+                const int row_shift = max(0, 32 - __clz(pc.n_rows - 1)), rows_in = 1 << row_shift;
+                const int per = (2 << split) * rows_in;  // rows of all sources: 2 .. 256
+                const int k_shift = kD == 128 && per <= 64 ? 5 : per <= 128 ? 4 : 3, quads = 1 << k_shift;
+                float4 *red = reinterpret_cast<float4 *>(dyn + pad);
 #pragma unroll 1
-                for (int c0 = 0; c0 < kD; c0 += 32) {
+                for (int c0 = 0; c0 < kD; c0 += 4 * quads) {
                     if (live_warp && (s == 0 || used1)) {
-                        uint32_t a[32];
-                        tmem_ld32(tO + c0, a);
-                        tmem_ld_wait();
-                        tmem_tie(a);
-                        float4 *dst = red + ((((s << split) + copy) * rows) + row_in) * 8;
+                        float4 *dst = red + (((((s << split) + copy) << row_shift) + row_in) << k_shift);
+#pragma unroll 1
+                        for (int q = 0; q < quads; q += 8) {
+                            uint32_t a[32];
+                            tmem_ld32(tO + c0 + 4 * q, a);
+                            tmem_ld_wait();
+                            tmem_tie(a);
+                            if (live_row) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            dst[k ^ (row_in & 7)] =
-                                make_float4(__uint_as_float(a[4 * k]) * g, __uint_as_float(a[4 * k + 1]) * g,
-                                            __uint_as_float(a[4 * k + 2]) * g, __uint_as_float(a[4 * k + 3]) * g);
+                                for (int k = 0; k < 8; ++k)
+                                    dst[(q + k) ^ (row_in & 7)] =
+                                        make_float4(__uint_as_float(a[4 * k]) * g, __uint_as_float(a[4 * k + 1]) * g,
+                                                    __uint_as_float(a[4 * k + 2]) * g, __uint_as_float(a[4 * k + 3]) * g);
+                            }
+                        }
                     }
                     named_sync<1, 256>();
-                    const int tid = threadIdx.x;
-                    for (int i = tid; i < rows * 8; i += 256) {
+#pragma unroll 1
+                    for (int i = threadIdx.x; i < rows_in << k_shift; i += 256) {
                         // partial rows: rows fastest; output rows: columns fastest
-                        const int r = part ? i & (rows - 1) : i >> 3, k = part ? i >> (7 - split) : i & 7;
+                        const int r = part ? i & (rows_in - 1) : i >> k_shift;
+                        const int k = part ? i >> row_shift : i & (quads - 1);
                         if (r >= pc.n_rows) continue;
                         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        for (int src = 0; src < sources; ++src) {
-                            const float4 v = red[(src * rows + r) * 8 + (k ^ (r & 7))];
+#pragma unroll
+                        for (int src = 0; src < 8; ++src) {
+                            if (src >= sources) break;
+                            const float4 v = red[(((src << row_shift) + r) << k_shift) + (k ^ (r & 7))];
                             o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
                         }
                         if (part) {
@@ -1664,14 +1672,13 @@ bool rows16(const void *p, int64_t stride, int el) {
 
 }  // namespace
 
-bool tc_takes(const Params &p, bool paged, int32_t dtype, int32_t kv_format) {
+bool tc_takes(const Params &p, bool paged, int32_t dtype) {
     if (dtype != DFLASH2_BF16 || (p.head_dim != 64 && p.head_dim != 128)) return false;
     if (!(p.scale_log2 >= 1.1754944e-38f)) return false;  // masked scores are -inf times the scale
     if (!rows16(p.q, p.q_stride, 2) || !aligned16(p.out) || !aligned16(p.k) || !aligned16(p.v))
         return false;
     if (!paged) return rows16(p.k, p.k_stride, 2) && rows16(p.v, p.v_stride, 2);
-    return p.page_size >= 16 && (p.page_size & (p.page_size - 1)) == 0 &&
-           (kv_format == DFLASH2_KV_NATIVE || (aligned16(p.k_exp) && aligned16(p.v_exp)));
+    return p.page_size >= 16 && (p.page_size & (p.page_size - 1)) == 0;
 }
 
 dflash2_status launch_tc(const DeviceInfo &di, const Params &p, bool paged, int32_t kv_format,
