@@ -242,6 +242,8 @@ dflash2_status launch_simt(const DeviceInfo &di, Params p, bool paged, int32_t d
 bool tc_takes(const Params &p, bool paged, int32_t dtype);
 dflash2_status launch_tc(const DeviceInfo &di, const Params &p, bool paged, int32_t kv_format,
                          cudaStream_t st);
+// attention_few.cu: the same call over an E4M3 cache, where few rows share the keys.
+dflash2_status launch_few(const DeviceInfo &di, const Params &p, cudaStream_t st);
 dflash2_status launch_combine(const DeviceInfo &di, const Params &p, int32_t dtype, cudaStream_t st);
 
 }  // namespace attn

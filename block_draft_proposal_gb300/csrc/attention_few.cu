@@ -1,0 +1,798 @@
+// Attention over an E4M3 cache on the 5th-generation tensor cores, for requests of
+// few query rows (a row: one token's query head).  head_dim 64 or 128.
+//
+// One pass over the keys in tiles of 128, transposed, so that an MMA's 128 rows are
+// keys and then channels, and its columns only as many as there are query rows:
+//
+//   S^T = K Q^T        tcgen05.mma kind::f8f6f4 on the codes as they are held
+//   P^T = 2^(z - base) one thread per key: its two scales are the thread's own, and
+//                      the exponentials of a key's rows need no shuffles
+//   O^T += V^T P^T     the same kind, V's codes read as the MN-major A operand
+//
+// Both products run at the rate of 8-bit operands and no code is widened: the
+// operands that carry more than four bits are split into E4M3 parts instead, where
+// they are small.  Q is two parts (the nearest code and that of the rest, under a
+// power of two per row): the eight bits of a bf16 value down to 2^-10 of the row's
+// largest, and 2^-18 of that below.  P is three, the rest scaled by 2^4 each time, in
+// columns of their own that the end adds up: twelve bits, and 2^-18 absolute below
+// that, where the largest P so far lies between 2^5 and 2^8.
+//
+// z = S 2^(key scale) 2^a scale log2(e), and a weight carries its value's scale:
+// P = 2^(z - base) 2^(value scale) 2^-x with an integer x per row.  base and x are
+// lazy: a tile is computed against the ones so far, and only where some z exceeds
+// its base by 8 or some P reaches 2^8 (the first tile, and few after it) the
+// warpgroup finds the maxima, moves them and rescales its sums.  base follows z alone, so
+// that the sum of the weights does not depend on the values.
+//
+// Two slots of accumulators, each with a softmax warpgroup, take the key tiles in
+// turns; the end adds them.  Warps 0-3 and 4-7: slots 0 and 1; warps 8 and 10 issue their
+// MMAs; warp 9 loads the keys, warp 11 the values (one TMA box per page).
+#include <type_traits>
+
+#include "attention_tc.cuh"
+
+namespace dflash2 {
+namespace attn {
+namespace {
+
+constexpr int kRowShift = 6, kRows = 1 << kRowShift;  // rows of a block
+constexpr int kItemUnits = 3;   // an item's start and end cost about as much as three key tiles
+constexpr int kParts = 3;       // of a weight
+constexpr float kLazy = 8.0f;   // log2 growth of a maximum that moves its base
+constexpr float kCap = 8.0f;    // log2 of the largest P
+constexpr int kTop = 4;         // binade of the largest P where x moves
+constexpr float kNever = 3.0e38f;
+
+struct Shared {
+    alignas(16) uint8_t piece[kPieces][kPieceBytes];
+    alignas(16) float qm[kRows];       // 2^a scale log2(e) of a row
+    alignas(16) float off[2][kRows];   // by slot: -base (0: no base yet)
+    alignas(16) float lx[2][kRows];    // -x; kNever: any seen key moves it, -kNever: no row
+    alignas(16) float xm[2][kRows];    // 2^-x
+    alignas(16) float fix_sum[2][kRows], fix_o[2][kRows];
+    float top[2][4][2][kRows];         // a warp's largest z, and z + value scale
+    float sums[2][4][kRows], tile_sum[2][4][kRows];
+    alignas(16) float zero[16];
+    int32_t pages[2][2][kTile / 16 * 8 + 1];  // page numbers of eight key tiles, twice, by producer
+    uint64_t piece_full[kPieces], piece_empty[kPieces];
+    uint64_t raw_full[2][8], raw_empty[2][8];  // codes of keys, values
+    uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], q_full, drain[2];
+    uint32_t tmem;
+    int abort_flag;
+    int stop[2];  // no more pieces, by piece parity
+    int poison;  // number of the last piece with a value not finite
+    StartScratch start;
+};
+
+template <int kD> struct Few {
+    static constexpr int kRawBytes = kTile * kD;           // codes of a tile
+    static constexpr int kStages = kD == 128 ? 4 : 8;      // tiles of keys, and of values
+    static constexpr int kQBytes = 2 * kRows * kD;         // both parts
+    static constexpr int kPBytes = 2 * kTile * 128;        // [column blocks of 128][key][column]
+    static constexpr int kThreads = 384;
+    static constexpr int kRegsMany = 216, kRegsFew = 72;   // 168 each at launch
+    static constexpr int kSmem = kQBytes + 2 * kPBytes + 2 * kStages * kRawBytes + (int)sizeof(Shared) + 1024;
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ float warp_max(float v) {
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+// Does any thread of warpgroup s say so?  (a barrier of its 128 threads)
+__device__ __forceinline__ bool group_any(int s, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.aligned.pred q, %2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v), "r"(2 + s)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void group_sync(int s) {
+    asm volatile("bar.sync %0, 128;" ::"r"(2 + s) : "memory");
+}
+
+template <int kD>
+__global__ void __launch_bounds__(Few<kD>::kThreads, 1)
+    few_kernel(const Params p, const __grid_constant__ CUtensorMap kmap,
+               const __grid_constant__ CUtensorMap vmap) {
+    using C = Few<kD>;
+    constexpr int kStages = C::kStages;
+    extern __shared__ uint8_t dyn[];
+    const uint32_t pad = (0u - smem_u32(dyn)) & 1023u;
+    const uint32_t sm_q = smem_u32(dyn) + pad;
+    const uint32_t sm_p = sm_q + C::kQBytes;
+    const uint32_t sm_raw[2] = {sm_p + 2 * C::kPBytes, sm_p + 2 * C::kPBytes + kStages * C::kRawBytes};
+    Shared &sh = *reinterpret_cast<Shared *>(dyn + pad + C::kQBytes + 2 * C::kPBytes + 2 * kStages * C::kRawBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < 2; ++k)
+            for (int i = 0; i < kStages; ++i) {
+                mbar_init(&sh.raw_full[k][i], 1);
+                mbar_init(&sh.raw_empty[k][i], 1);
+            }
+        for (int i = 0; i < kPieces; ++i) {
+            mbar_init(&sh.piece_full[i], 1);
+            mbar_init(&sh.piece_empty[i], 11);  // all but the producer
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.s_free[i], 4);
+            mbar_init(&sh.p_full[i], 4);
+            mbar_init(&sh.pv_done[i], 1);
+            mbar_init(&sh.drain[i], 1);
+        }
+        mbar_init(&sh.q_full, 8);
+        for (int i = 0; i < 16; ++i) sh.zero[i] = 0.0f;
+        sh.abort_flag = 0;
+        sh.stop[0] = sh.stop[1] = 0;
+        sh.poison = -1;
+        fence_mbar_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(&sh.tmem, 512);
+        tmem_relinquish();
+    }
+    if (warp == 9 && lane == 0) {
+        prefetch_tmap(&kmap);
+        prefetch_tmap(&vmap);
+    }
+    grid_dep_wait();
+    grid_dep_launch();
+
+    bool bad = false;
+    const Start start = find_start(p, blockIdx.x, &sh.start, &bad);
+    if (bad && p.err && blockIdx.x == 0) atomicOr(p.err, DFLASH2_DEVERR_ID_RANGE);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // the CTA holds all 512 TMEM columns: S^T of slot s at 64 s, O^T at 128 + 192 s
+    volatile int *abort_flag = &sh.abort_flag;
+    // Piece number i of the ring, for every role but the producer's; all lanes of a
+    // warp (`whole`) or one thread.  Returns false at the end or on an abort.
+    auto take_piece = [&](uint32_t i, Piece *pc, bool whole) {
+        if (!bar_wait(&sh.piece_full[i % kPieces], (i / kPieces) & 1u, abort_flag, p.err)) return false;
+        *pc = *reinterpret_cast<const Piece *>(sh.piece[i % kPieces]);
+        if (whole) __syncwarp();
+        if (!whole || lane == 0) mbar_arrive(&sh.piece_empty[i % kPieces]);
+        return pc->n_rows > 0;
+    };
+
+    if (warp >= 8) {
+        regs_give<C::kRegsFew>();
+        if (warp == 9 || warp == 11) {
+            // ---- producers: warp 9 the pieces and the keys, warp 11 the values ----
+            const int of = warp == 9 ? 0 : 1;
+            uint32_t issued = 0, n_piece = 0;
+            bool ok = true, bad_page = false;
+            const int32_t rows_box = min(p.page_size, kTile);
+            const int32_t page_shift = 31 - __clz(p.page_size);
+            const int32_t box_shift = 7 - min(page_shift, 7);  // log2 of the boxes of a tile
+            Piece pc{};
+            // Page numbers come eight key tiles at a time: the lanes load the next eight's
+            // while one thread issues the copies of these.  -1: no page (past the end, or
+            // out of range), a box of zeros.
+            int32_t ids[2] = {-1, -1};
+            auto line_of = [&](int32_t tile, int k) {  // first key of box lane + 32 k, or -1
+                const int32_t e = lane + 32 * k, at = tile + (e >> box_shift);
+                const int32_t l = at * kTile + (e & ((1 << box_shift) - 1)) * rows_box;
+                return e < (8 << box_shift) && at < pc.t1 && l < pc.rq.len ? l : -1;
+            };
+            auto fetch_pages = [&](int32_t tile) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int32_t l = line_of(tile, k);
+                    ids[k] = l >= 0 ? __ldg(p.page_table + (int64_t)pc.b * p.max_pages + (l >> page_shift)) : -1;
+                }
+            };
+            auto keep_pages = [&](int32_t tile, uint32_t buffer) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int32_t e = lane + 32 * k;
+                    const bool good = (uint64_t)(int64_t)ids[k] < (uint64_t)p.num_pages;
+                    if (!good && line_of(tile, k) >= 0) bad_page = true;
+                    if (e < (8 << box_shift)) sh.pages[of][buffer][e] = good ? ids[k] : -1;
+                }
+                __syncwarp();
+            };
+            auto load = [&](int32_t j) {  // key tile t0 + j
+                const int32_t tile = pc.t0 + j;
+                const uint32_t s = issued % kStages;
+                uint64_t *fullb = &sh.raw_full[of][s];
+                if (!bar_wait(&sh.raw_empty[of][s], ((issued / kStages) & 1u) ^ 1u, abort_flag, p.err)) return false;
+                mbar_arrive_expect_tx(fullb, C::kRawBytes);
+                const uint32_t dst = sm_raw[of] + s * C::kRawBytes;
+                const int32_t y = (tile * kTile) & (p.page_size - 1) & ~(kTile - 1);
+                const int32_t *page = sh.pages[of][(j >> 3) & 1] + ((j & 7) << box_shift);
+                int32_t id = page[0];
+#pragma unroll 1
+                for (int i = 0; i < (1 << box_shift); ++i) {
+                    const int32_t z = id >= 0 ? id * p.kv_heads + pc.h : -1;
+                    const int32_t next = page[i + 1];  // past the last: unused
+                    tma_load_3d(dst + i * rows_box * kD, of ? &vmap : &kmap, fullb, 0, y, z);
+                    id = next;
+                }
+                ++issued;
+                return true;
+            };
+            Walk walk{};
+            if (of == 0) walk.begin(p, start);
+            for (;;) {
+                if (of == 1) {
+                    if (!take_piece(n_piece, &pc, true)) pc.n_rows = 0;
+                } else {
+                    walk.next(p, &pc);
+                    pc.tok0 = pc.row0 / p.group;
+                    pc.rem0 = pc.row0 - pc.tok0 * p.group;
+                    for (int r = lane; r < pc.n_rows; r += 32) {  // the queries, on their way to L2
+                        const int x = pc.rem0 + r, dt = x / p.group;
+                        const __nv_bfloat16 *q = (const __nv_bfloat16 *)p.q +
+                                                 (int64_t)(pc.rq.t0 + pc.tok0 + dt) * p.q_stride +
+                                                 (int64_t)(pc.h * p.group + x - dt * p.group) * kD;
+#pragma unroll
+                        for (int c = 0; c < kD; c += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + c));
+                    }
+                    if (elect_one()) {
+                        ok = bar_wait(&sh.piece_empty[n_piece % kPieces], ((n_piece / kPieces) & 1u) ^ 1u,
+                                      abort_flag, p.err);
+                        if (ok) {
+                            *reinterpret_cast<Piece *>(sh.piece[n_piece % kPieces]) = pc;
+                            mbar_arrive(&sh.piece_full[n_piece % kPieces]);
+                        }
+                    }
+                }
+                const int32_t n = pc.n_rows > 0 ? pc.t1 - pc.t0 : 0;
+                if (n > 0) fetch_pages(pc.t0);
+                for (int32_t c = 0; c < n; c += 8) {
+                    keep_pages(pc.t0 + c, (c >> 3) & 1);
+                    fetch_pages(pc.t0 + c + 8);
+                    if (elect_one())
+                        for (int32_t j = c; ok && j < min(n, c + 8); ++j) ok = load(j);
+                    __syncwarp();
+                }
+                ++n_piece;
+                if (__any_sync(0xFFFFFFFFu, !ok) || pc.n_rows == 0) break;
+            }
+            if (of == 0 && lane == 0) p.join[blockIdx.x] = walk.join;
+            if (bad_page && p.err) atomicOr(p.err, DFLASH2_DEVERR_ID_RANGE);
+            if (!ok) {  // wait for the copies in flight before the shared memory goes
+                for (uint32_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i) {
+                    const uint64_t t0 = global_timer_ns();
+                    while (!mbar_try_wait(&sh.raw_full[of][i % kStages], (i / kStages) & 1u))
+                        if (global_timer_ns() - t0 > kWaitLimitNs) break;
+                }
+            }
+        } else if (elect_one()) {
+            // ---- MMA issuer of slot s: one thread ----
+            const int s = warp == 8 ? 0 : 1;
+            const uint32_t dS = s * kRows, dO = 128 + s * (kParts * kRows);
+            uint32_t tiles_done = 0, n_piece = 0, n_s = 0, n_p = 0;
+            bool ok = true;
+            Piece pc{};
+            // descriptors' high words: K-major rows of kD bytes; V [keys][kD] as MN-major with
+            // 8-key groups one swizzle atom apart (head_dim 64: M is 128 all the same, and
+            // the second 64 repeat the first, a leading offset of zero)
+            constexpr uint32_t kVHi = kCodesHi<kD>;
+            while (ok && take_piece(n_piece, &pc, false)) {
+                ok = bar_wait(&sh.q_full, n_piece & 1u, abort_flag, p.err);
+                ++n_piece;
+                const int32_t n = pc.t1 - pc.t0, cols = (pc.n_rows + 15) & ~15;
+                const uint32_t id_s = idesc_e4m3(128, cols);
+                const uint32_t id_o = idesc_e4m3(128, kParts * cols) | (1u << 15) | (1u << 16);  // both MN-major
+                auto scores = [&](int32_t j) {
+                    const uint32_t kt = tiles_done + j, i = kt % kStages;
+                    if (!bar_wait(&sh.raw_full[0][i], (kt / kStages) & 1u, abort_flag, p.err) ||
+                        !bar_wait(&sh.s_free[s], (n_s & 1u) ^ 1u, abort_flag, p.err))
+                        return false;
+                    ++n_s;
+                    tc_fence_after();
+                    const uint32_t kd = desc_lo(sm_raw[0] + i * C::kRawBytes) | kKMajorLo;
+                    const uint32_t qd = desc_lo(sm_q) | kKMajorLo;
+#pragma unroll
+                    for (int k = 0; k < 2 * (kD / 32); ++k) {  // both parts of Q, one after the other
+                        const uint32_t at = (k % (kD / 32)) * 2, part = k >= kD / 32 ? (kRows * kD) >> 4 : 0;
+                        tc_mma_f8(dS, desc64(kd + at, kCodesHi<kD>), desc64(qd + part + at, kCodesHi<kD>), id_s,
+                                  k > 0);
+                    }
+                    tc_commit(&sh.s_full[s]);
+                    tc_commit(&sh.raw_empty[0][i]);
+                    return true;
+                };
+                if (ok && s < n) ok = scores(s);
+#pragma unroll 1
+                for (int32_t j = s; ok && j < n; j += 2) {
+                    if (j + 2 < n) ok = scores(j + 2);
+                    const uint32_t kt = tiles_done + j, i = kt % kStages;
+                    ok = ok && bar_wait(&sh.raw_full[1][i], (kt / kStages) & 1u, abort_flag, p.err) &&
+                         bar_wait(&sh.p_full[s], n_p & 1u, abort_flag, p.err);
+                    if (!ok) break;
+                    ++n_p;
+                    tc_fence_after();
+                    const uint32_t vd = desc_lo(sm_raw[1] + i * C::kRawBytes);
+                    const uint32_t pd = desc_lo(sm_p + s * C::kPBytes) | kMnMajorLo;
+#pragma unroll
+                    for (int k = 0; k < kTile / 32; ++k)
+                        tc_mma_f8(dO, desc64(vd + k * (32 * kD >> 4), kVHi), desc64(pd + k * (32 * 128 >> 4), kMnMajorHi),
+                                  id_o, j > s || k > 0);
+                    tc_commit(&sh.raw_empty[1][i]);
+                    tc_commit(&sh.pv_done[s]);
+                }
+                tiles_done += n;
+            }
+            // nothing of this slot's is in flight when the accumulators are freed
+            tc_commit(&sh.drain[s]);
+            const uint64_t t0 = global_timer_ns();
+            while (!mbar_try_wait(&sh.drain[s], 0))
+                if (global_timer_ns() - t0 > kWaitLimitNs) break;
+        }
+    } else {
+        // ---- softmax of slot s, with the loads of Q and the epilogue ----
+        regs_take<C::kRegsMany>();
+        const int s = warp >> 2, wq = warp & 3;
+        const int my = wq * 32 + lane;  // key of a tile, channel of the sums
+        const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
+        const uint32_t tS = s * kRows + lane_base;
+        const uint32_t tO = 128 + s * (kParts * kRows) + lane_base;
+        const uint32_t my_p = sm_p + s * C::kPBytes + my * 128;
+        const uint32_t magic = (65536u + p.group - 1) / (uint32_t)p.group;  // x / group for x < 512
+        const int32_t page_shift = 31 - __clz(p.page_size);
+        uint32_t n_piece = 0, n_s = 0, tiles_done = 0;
+        uint32_t n_pv[2] = {0, 0};  // sums complete, by slot
+        Piece pc{};
+        int32_t page = -1;
+        int ke = 127, ve = 127;
+        // Exponent bytes: this thread's key of the slot's next tile, and its page of the one
+        // after that, so that neither load is waited for.
+        auto fetch_page = [&](int32_t tile) {
+            const int32_t l = tile * kTile + my;
+            page = -1;
+            if (tile < pc.t1 && l < pc.rq.len)
+                page = __ldg(p.page_table + (int64_t)pc.b * p.max_pages + (l >> page_shift));
+        };
+        auto fetch_exps = [&](int32_t tile) {  // of `page`
+            ke = ve = 127;
+            if ((uint64_t)(int64_t)page < (uint64_t)p.num_pages) {
+                const int32_t at = (tile * kTile + my) & (p.page_size - 1);
+                const int64_t i = ((int64_t)page * p.kv_heads + pc.h) * p.page_size + at;
+                ke = __ldg(p.k_exp + i);
+                ve = __ldg(p.v_exp + i);
+            }
+        };
+        // (no wait's failure leaves the loop: the barriers below want all warps)
+        for (;;) {
+            if (!take_piece(n_piece, &pc, true)) sh.stop[n_piece & 1u] = 1;
+            named_sync<1, 256>();
+            if (*(volatile int *)&sh.stop[n_piece & 1u]) break;
+            fetch_page(pc.t0 + s);
+            // queries: kD / 8 lanes hold a row, 8 values each
+            {
+                constexpr int kLanes = kD / 8, kStep = 256 / kLanes, kEach = kRows / kStep;
+                const uint32_t row_lanes = ((1u << kLanes) - 1u) << (lane & ~(kLanes - 1));
+                const int l8 = threadIdx.x % kLanes;
+                const __nv_bfloat16 *q0 = (const __nv_bfloat16 *)p.q + (int64_t)(pc.rq.t0 + pc.tok0) * p.q_stride +
+                                          (int64_t)pc.h * p.group * kD + l8 * 8;
+                uint4 v[kEach];
+#pragma unroll
+                for (int i = 0; i < kEach; ++i) {
+                    const int r = threadIdx.x / kLanes + i * kStep;
+                    const uint32_t x = pc.rem0 + r, dt = (x * magic) >> 16;
+                    v[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (r < pc.n_rows)
+                        v[i] = __ldg(reinterpret_cast<const uint4 *>(q0 + (int64_t)dt * p.q_stride +
+                                                                     (int)(x - dt * p.group) * kD));
+                }
+                fetch_exps(pc.t0 + s);
+                fetch_page(pc.t0 + s + 2);
+                if (threadIdx.x < 2 * kRows) {
+                    const int c = threadIdx.x & (kRows - 1), of = threadIdx.x / kRows;
+                    sh.off[of][c] = 0.0f;
+                    sh.lx[of][c] = c < pc.n_rows ? kNever : -kNever;
+                    sh.xm[of][c] = c < pc.n_rows ? 1.0f : 0.0f;
+                }
+#pragma unroll
+                for (int i = 0; i < kEach; ++i) {
+                    const int r = threadIdx.x / kLanes + i * kStep;
+                    if (r >= pc.n_rows) {
+                        if (l8 == 0) sh.qm[r] = 0.0f;
+                        continue;
+                    }
+                    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                    float f[8], amax = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        f[2 * k] = __uint_as_float(w[k] << 16);
+                        f[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+                        amax = fmaxf(amax, fmaxf(fabsf(f[2 * k]), fabsf(f[2 * k + 1])));
+                    }
+#pragma unroll
+                    for (int o = kLanes / 2; o > 0; o >>= 1)
+                        amax = fmaxf(amax, __shfl_xor_sync(row_lanes, amax, o));
+                    // 2^-a: the largest magnitude's binade becomes 2^7
+                    const int a = min(max((int)(__float_as_uint(amax) >> 23) - 127 - 7, -110), 110);
+                    // an infinite value makes the row NaN: codes hold no infinity
+                    const float down =
+                        amax <= 3.4e38f ? __uint_as_float((uint32_t)(127 - a) << 23) : __int_as_float(0x7FC00000);
+                    uint32_t hi[2], lo[2];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 y = make_float2(f[2 * k] * down, f[2 * k + 1] * down);
+                        const uint32_t ch = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+                        const float2 back = __half22float2(
+                            __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)ch, __NV_E4M3)));
+                        const uint32_t cl = __nv_cvt_float2_to_fp8x2(make_float2(y.x - back.x, y.y - back.y),
+                                                                     __NV_SATFINITE, __NV_E4M3);
+                        hi[k >> 1] = (k & 1) ? hi[k >> 1] | (ch << 16) : ch;
+                        lo[k >> 1] = (k & 1) ? lo[k >> 1] | (cl << 16) : cl;
+                    }
+                    if (l8 == 0)
+                        sh.qm[r] = fmaxf(__uint_as_float((uint32_t)(127 + a) << 23) * p.scale_log2, 1.1754944e-38f);
+                    const int c = kD == 128 ? (l8 >> 1) ^ (r & 7) : (l8 >> 1) ^ ((r >> 1) & 3);
+                    const uint32_t dst = sm_q + r * kD + (c << 4) + ((l8 & 1) << 3);
+                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(dst), "r"(hi[0]), "r"(hi[1]) : "memory");
+                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(dst + kRows * kD), "r"(lo[0]), "r"(lo[1])
+                                 : "memory");
+                }
+                fence_proxy_async_smem();
+                // all threads: the rows' factors are there, and the last piece's sums are read
+                named_sync<1, 256>();
+                if (lane == 0) mbar_arrive(&sh.q_full);
+            }
+            const int n_chunk = (pc.n_rows + 15) >> 4;  // of 16 rows
+            float sum[2] = {0.0f, 0.0f};  // this warp's keys, rows 2 lane and the next
+            // row `my`: its base (-inf: none yet), largest z + value scale at the last move, x
+            float row_base = -INFINITY, row_top = -INFINITY, row_x = 0.0f;
+
+            for (int32_t t = pc.t0 + s; t < pc.t1; t += 2) {
+                const bool first = t == pc.t0 + s;
+                const int32_t l = t * kTile + my;
+                // written exponents lie in [-48, 48]; what was never written is masked
+                const float km = pow2_int(min(max(ke - 127, -48), 48));
+                const int v_exp = min(max(ve - 127, -48), 48);
+                const float vm = pow2_int(v_exp), vf = (float)v_exp;
+                fetch_exps(t + 2);
+                fetch_page(t + 4);
+                const bool masked = (t + 1) * kTile > pc.rq.ctx;
+                // the rows that see this key: bit r; all of a token's rows do, or none
+                uint64_t seen = ~0ull;
+                if (masked) {
+                    seen = 0;
+                    const int n_tok = (pc.rem0 + pc.n_rows + p.group - 1) / p.group;
+#pragma unroll 4
+                    for (int i = 0; i < n_tok; ++i) {
+                        const int r0 = max(i * p.group - pc.rem0, 0), r1 = min((i + 1) * p.group - pc.rem0, pc.n_rows);
+                        const uint64_t rows = (r1 >= 64 ? ~0ull : (1ull << r1) - 1ull) & ~((1ull << r0) - 1ull);
+                        if (sees(p, pc.rq, pc.tok0 + i, l)) seen |= rows;
+                    }
+                }
+                bar_wait(&sh.s_full[s], n_s & 1u, abort_flag, p.err);
+                ++n_s;
+                tc_fence_after();
+                const uint64_t km2 = f2(km, km), vm2 = f2(vm, vm);
+                uint32_t x[16];
+                // z of the 16 rows from c on, against the slot's bases (`off`) or none (zeros)
+                auto scores = [&](int c, const float *off) {
+                    tmem_ld16(tS + c, x);
+                    tmem_ld_wait();
+                    tmem_tie16(x);
+#pragma unroll
+                    for (int k = 0; k < 16; k += 4) {
+                        const ulonglong2 q4 = *reinterpret_cast<const ulonglong2 *>(&sh.qm[c + k]);
+                        const ulonglong2 o4 = *reinterpret_cast<const ulonglong2 *>(off + k);
+                        float a, b;
+                        unf2(fma2(mul2(f2(x[k], x[k + 1]), km2), q4.x, o4.x), a, b);
+                        x[k] = __float_as_uint(a), x[k + 1] = __float_as_uint(b);
+                        unf2(fma2(mul2(f2(x[k + 2], x[k + 3]), km2), q4.y, o4.y), a, b);
+                        x[k + 2] = __float_as_uint(a), x[k + 3] = __float_as_uint(b);
+                    }
+                    if (masked) {
+                        const uint32_t w = (uint32_t)(seen >> c);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            if (!((w >> k) & 1u)) x[k] = 0xFF800000u;  // -inf
+                    }
+                };
+                // weights against the bases and x so far; again where those had to move
+#pragma unroll 1
+                for (bool move = first;; move = true) {
+                    if (move) {
+#pragma unroll 1
+                        for (int c = 0; c < pc.n_rows; c += 16) {
+                            scores(c, sh.zero);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const float z = __uint_as_float(x[k]);
+                                const float top = warp_max(z), top_v = warp_max(z + vf);
+                                if (lane == 0) {
+                                    sh.top[s][wq][0][c + k] = top;
+                                    sh.top[s][wq][1][c + k] = top_v;
+                                }
+                            }
+                        }
+                        group_sync(s);
+                        if (my < pc.n_rows) {
+                            float top = -INFINITY, fix = 1.0f, fix_o = 1.0f;
+#pragma unroll
+                            for (int w = 0; w < 4; ++w) {
+                                top = fmaxf(top, sh.top[s][w][0][my]);
+                                row_top = fmaxf(row_top, sh.top[s][w][1][my]);
+                            }
+                            const bool had = row_base > -INFINITY;
+                            if (top > row_base + kLazy) {
+                                if (had) fix = ex2(row_base - top);
+                                fix_o = fix;
+                                row_base = top;
+                            }
+                            if (row_base > -INFINITY) {
+                                const float nx = floorf(fminf(fmaxf(row_top - row_base, -100.0f), 100.0f)) - kTop;
+                                if (had) fix_o *= ex2(row_x - nx);
+                                row_x = nx;
+                                sh.off[s][my] = -row_base;
+                                sh.lx[s][my] = -nx;
+                                sh.xm[s][my] = pow2_int(-(int)nx);
+                            }
+                            sh.fix_sum[s][my] = fix;
+                            sh.fix_o[s][my] = fix_o;
+                        }
+                        group_sync(s);
+                        if (!first) {  // the sums so far, all of them there
+                            if (2 * lane < pc.n_rows) sum[0] *= sh.fix_sum[s][2 * lane];
+                            if (2 * lane + 1 < pc.n_rows) sum[1] *= sh.fix_sum[s][2 * lane + 1];
+#pragma unroll 1
+                            for (int i = 0; i < kParts * n_chunk; ++i) {
+                                uint32_t o[16];
+                                tmem_ld16(tO + 16 * i, o);
+                                tmem_ld_wait();
+                                tmem_tie16(o);
+                                const float *f = sh.fix_o[s] + i / kParts * 16;
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f[k]);
+                                tmem_st16(tO + 16 * i, o);
+                            }
+                            tmem_st_wait();
+                        }
+                    } else {  // the last weights are read
+                        bar_wait(&sh.pv_done[s], (n_pv[s] - 1u) & 1u, abort_flag, p.err);
+                        tc_fence_after();
+                    }
+                    float most = -INFINITY, most_p = -INFINITY;
+                    uint32_t dst = my_p, swz = my & 7;  // block of 16 columns: (block ^ key) % 8
+#pragma unroll 1
+                    for (int c = 0; c < pc.n_rows; c += 16) {
+                        scores(c, &sh.off[s][c]);
+                        uint32_t pk[kParts][4];
+                        float w[16];
+#pragma unroll
+                        for (int k = 0; k < 16; k += 4) {
+                            const ulonglong2 l4 = *reinterpret_cast<const ulonglong2 *>(&sh.lx[s][c + k]);
+                            const ulonglong2 x4 = *reinterpret_cast<const ulonglong2 *>(&sh.xm[s][c + k]);
+                            uint32_t half[kParts][2];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const float za = __uint_as_float(x[k + 2 * e]), zb = __uint_as_float(x[k + 2 * e + 1]);
+                                float a, b;
+                                most = fmaxf(fmaxf(most, za), zb);
+                                unf2(add2(f2(za, zb), e ? l4.y : l4.x), a, b);
+                                most_p = fmaxf(fmaxf(most_p, a), b);
+                                w[k + 2 * e] = ex2(za), w[k + 2 * e + 1] = ex2(zb);
+                                uint64_t rest = mul2(mul2(f2(w[k + 2 * e], w[k + 2 * e + 1]), vm2), e ? x4.y : x4.x);
+                                const uint64_t up = f2(16.0f, 16.0f), neg = f2(-16.0f, -16.0f);
+#pragma unroll
+                                for (int part = 0; part < kParts; ++part) {
+                                    unf2(rest, a, b);
+                                    half[part][e] = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+                                    if (part + 1 == kParts) break;
+                                    const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
+                                        (__nv_fp8x2_storage_t)half[part][e], __NV_E4M3)));
+                                    rest = fma2(f2(back.x, back.y), neg, mul2(rest, up));  // exact
+                                }
+                            }
+#pragma unroll
+                            for (int part = 0; part < kParts; ++part)
+                                pk[part][k / 4] = half[part][0] | (half[part][1] << 16);
+                        }
+#pragma unroll
+                        for (int part = 0; part < kParts; ++part) {
+                            const int at = kParts * (c >> 4) + part;
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                             dst + (at >> 3) * (kTile * 128) + (((at & 7) ^ swz) << 4)),
+                                         "r"(pk[part][0]), "r"(pk[part][1]), "r"(pk[part][2]), "r"(pk[part][3])
+                                         : "memory");
+                        }
+                        // the warp's sums of the rows: half of them go to either half of the lanes
+#pragma unroll
+                        for (int o = 16; o > 1; o >>= 1) {
+                            const bool up = lane & o;
+#pragma unroll
+                            for (int k = 0; k < o / 2; ++k) {
+                                const float keep = up ? w[k + o / 2] : w[k], give = up ? w[k] : w[k + o / 2];
+                                w[k] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+                            }
+                        }
+                        w[0] += __shfl_xor_sync(0xFFFFFFFFu, w[0], 1);
+                        if (!(lane & 1)) sh.tile_sum[s][wq][c + (lane >> 1)] = w[0];
+                    }
+                    if (move || !group_any(s, most > kLazy || most_p + vf > kCap)) break;
+                }
+                // the scores are read: the next tile's may come
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.s_free[s]);
+                ++n_pv[s];
+                sum[0] += sh.tile_sum[s][wq][2 * lane];  // (of rows that are not there: unused)
+                sum[1] += sh.tile_sum[s][wq][2 * lane + 1];
+                // What a row does not see must not reach it, but a product 0 * NaN would: the
+                // values past the end, and NaN codes where some row may be masked, become
+                // zero; the epilogue adds the NaN to the rows that do see it.
+                if (t >= pc.guard_from) {
+                    const uint32_t kt = tiles_done + (uint32_t)(t - pc.t0), i = kt % kStages;
+                    bar_wait(&sh.raw_full[1][i], (kt / kStages) & 1u, abort_flag, p.err);
+                    const uint32_t src = sm_raw[1] + i * C::kRawBytes + my * kD;
+                    const bool live = l < pc.rq.len;
+                    bool found = false;
+#pragma unroll 2
+                    for (int c = 0; c < kD / 16; ++c) {
+                        const uint32_t a = src + ((kD == 128 ? c ^ (my & 7) : c ^ ((my >> 1) & 3)) << 4);
+                        uint32_t w[4];
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                     : "r"(a));
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (!live) w[k] = 0u;
+                            const uint32_t nan = __vcmpeq4(w[k] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                            found |= nan != 0;
+                            w[k] &= ~nan;
+                        }
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(w[0]), "r"(w[1]),
+                                     "r"(w[2]), "r"(w[3])
+                                     : "memory");
+                    }
+                    if (found) *(volatile int *)&sh.poison = (int)n_piece;
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.p_full[s]);
+            }
+            // ---- epilogue ----
+            const int32_t n = pc.t1 - pc.t0;
+            tiles_done += n;
+            const bool used1 = n > 1;
+            n_pv[s ^ 1] += (uint32_t)((n + s) >> 1);  // slot 0 has (n + 1) / 2 tiles, slot 1 n / 2
+            sh.sums[s][wq][2 * lane] = sum[0];
+            sh.sums[s][wq][2 * lane + 1] = sum[1];
+            if (my < pc.n_rows) sh.top[s][0][0][my] = row_base, sh.top[s][0][1][my] = row_x;
+            if (s == 0 || used1) {
+                bar_wait(&sh.pv_done[s], (n_pv[s] - 1u) & 1u, abort_flag, p.err);
+            }
+            named_sync<1, 256>();
+            // both slots' last sums are complete: these waits return at once
+            if (s == 0 ? used1 : true) {
+                bar_wait(&sh.pv_done[s ^ 1], (n_pv[s ^ 1] - 1u) & 1u, abort_flag, p.err);
+            }
+            tc_fence_after();
+            float *part = pc.slot >= 0 ? p.part + pc.slot * part_slot_floats(p.part_rows, kD) : nullptr;
+            auto out_row = [&](int r) {
+                const uint32_t x = pc.rem0 + r, dt = (x * magic) >> 16;
+                return (int64_t)(pc.rq.t0 + pc.tok0 + (int)dt) * p.q_heads + pc.h * p.group + (int)(x - dt * p.group);
+            };
+            if ((int)threadIdx.x < pc.n_rows) {  // a row's statistics, and its factors for the two sums
+                const int r = threadIdx.x;
+                float b[2], l[2], top = -INFINITY, all = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const bool used = i == 0 || used1;
+                    b[i] = used ? sh.top[i][0][0][r] : -INFINITY;
+                    l[i] = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) l[i] += used ? sh.sums[i][w][r] : 0.0f;
+                    top = fmaxf(top, b[i]);
+                }
+                const float safe = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) all = fmaf(l[i], ex2(b[i] - safe), all);
+                const float inv = part ? 1.0f : all == 0.0f ? 0.0f : 1.0f / all;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    sh.fix_o[i][r] = ex2(b[i] - safe) * pow2_int((int)sh.top[i][0][1][r]) * inv;
+                if (part) {
+                    part[part_stats(p.part_rows, kD) + r] = top;
+                    part[part_stats(p.part_rows, kD) + p.part_rows + r] = all;
+                } else if (p.lse) {
+                    p.lse[out_row(r)] = all == 0.0f ? -INFINITY : (top + log2f(all)) * 0.6931471805599453f;
+                }
+            }
+            named_sync<1, 256>();
+            // eight rows at a time, by the warpgroups in turns; this thread has channel `my`
+            const uint32_t tO0 = 128 + lane_base;
+#pragma unroll 1
+            for (int r0 = 8 * s; r0 < pc.n_rows; r0 += 16) {
+                float o[8] = {};
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (i == 1 && !used1) break;
+                    uint32_t a[kParts][8];
+#pragma unroll
+                    for (int q = 0; q < kParts; ++q)
+                        tmem_ld8(tO0 + i * (kParts * kRows) + (r0 >> 4) * (16 * kParts) + 16 * q + (r0 & 15), a[q]);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int q = 0; q < kParts; ++q) tmem_tie8(a[q]);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        o[k] = fmaf(fmaf(fmaf(__uint_as_float(a[2][k]), 0.0625f, __uint_as_float(a[1][k])), 0.0625f,
+                                         __uint_as_float(a[0][k])),
+                                    sh.fix_o[i][r0 + k], o[k]);
+                }
+                if (kD == 64 && my >= kD) continue;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if (r0 + k >= pc.n_rows) break;
+                    if (part)
+                        part[((int64_t)(my >> 2) * p.part_rows + r0 + k) * 4 + (my & 3)] = o[k];
+                    else
+                        ((__nv_bfloat16 *)p.out)[out_row(r0 + k) * kD + my] = __float2bfloat16_rn(o[k]);
+                }
+            }
+            if (*(volatile int *)&sh.poison == (int)n_piece) {
+                __threadfence_block();
+                named_sync<1, 256>();
+                if ((int)threadIdx.x < pc.n_rows) {
+                    const int r = threadIdx.x;
+                    add_poison<kD, true, true>(p, pc.rq, pc.b, pc.h, pc.tok0 + (int)(((pc.rem0 + r) * magic) >> 16),
+                                               max(pc.t0, pc.guard_from) * kTile, min(pc.t1 * kTile, pc.rq.len), 0, kD,
+                                               part ? part + 4 * r : nullptr,
+                                               (__nv_bfloat16 *)p.out + out_row(r) * kD);
+                }
+            }
+            // the sums are read: the next piece's first barrier says so
+            tc_fence_before();
+            ++n_piece;
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_dealloc(0, 512);
+    }
+}
+
+template <int kD> dflash2_status launch_one(const DeviceInfo &di, Params p, cudaStream_t st) {
+    using C = Few<kD>;
+    auto fn = few_kernel<kD>;
+    static std::atomic<uint64_t> done{0};
+    const dflash2_status allowed = allow_smem(fn, C::kSmem, di.device, done);
+    if (allowed != DFLASH2_OK) return allowed;
+    CUtensorMap maps[2];
+    for (int i = 0; i < 2; ++i) {
+        const uint64_t dims[3] = {(uint64_t)kD, (uint64_t)p.page_size, (uint64_t)p.num_pages * p.kv_heads};
+        const uint64_t strides[2] = {kD, (uint64_t)kD * p.page_size};
+        const uint32_t box[3] = {(uint32_t)kD, (uint32_t)(p.page_size < kTile ? p.page_size : kTile), 1u};
+        const dflash2_status s = encode_tmap_3d(&maps[i], i ? p.v : p.k, dims, strides, box, 1);
+        if (s != DFLASH2_OK) return s;
+    }
+    p.row_shift = kRowShift;
+    p.item_units = kItemUnits;
+    p.n_cta = di.sm_count;
+    launch_k(fn, dim3((unsigned)p.n_cta), dim3(C::kThreads), C::kSmem, st, p, maps[0], maps[1]);
+    const dflash2_status s = launch_status();
+    if (s != DFLASH2_OK) return s;
+    return launch_combine(di, p, DFLASH2_BF16, st);
+}
+
+}  // namespace
+
+dflash2_status launch_few(const DeviceInfo &di, const Params &p, cudaStream_t st) {
+    return p.head_dim == 64 ? launch_one<64>(di, p, st) : launch_one<128>(di, p, st);
+}
+
+}  // namespace attn
+}  // namespace dflash2
