@@ -36,23 +36,21 @@ namespace attn {
 namespace {
 
 constexpr int kRowShift = 6, kRows = 1 << kRowShift;  // rows of a block
-constexpr int kItemUnits = 3;   // an item's start and end cost about as much as three key tiles
+// Units of a key tile with up to 16, 32, 48 and 64 rows, and of an item's start and end.
+constexpr int kTileUnits[4] = {10, 13, 16, 20}, kItemUnits = 40;
 constexpr int kParts = 3;       // of a weight
 constexpr float kLazy = 8.0f;   // log2 growth of a maximum that moves its base
-constexpr float kCap = 8.0f;    // log2 of the largest P
-constexpr int kTop = 4;         // binade of the largest P where x moves
-constexpr float kNever = 3.0e38f;
+constexpr float kCap = 256.0f;  // the largest P
+constexpr int kTop = 3;         // binade of the largest P where x moves
 
 struct Shared {
     alignas(16) uint8_t piece[kPieces][kPieceBytes];
     alignas(16) float qm[kRows];       // 2^a scale log2(e) of a row
     alignas(16) float off[2][kRows];   // by slot: -base (0: no base yet)
-    alignas(16) float lx[2][kRows];    // -x; kNever: any seen key moves it, -kNever: no row
     alignas(16) float xm[2][kRows];    // 2^-x
     alignas(16) float fix_sum[2][kRows], fix_o[2][kRows];
     float top[2][4][2][kRows];         // a warp's largest z, and z + value scale
-    float sums[2][4][kRows], tile_sum[2][4][kRows];
-    alignas(16) float zero[16];
+    float sums[2][4][kRows];           // of a tile's weights by warp, then of all
     int32_t pages[2][2][kTile / 16 * 8 + 1];  // page numbers of eight key tiles, twice, by producer
     uint64_t piece_full[kPieces], piece_empty[kPieces];
     uint64_t raw_full[2][8], raw_empty[2][8];  // codes of keys, values
@@ -129,7 +127,6 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
             mbar_init(&sh.drain[i], 1);
         }
         mbar_init(&sh.q_full, 8);
-        for (int i = 0; i < 16; ++i) sh.zero[i] = 0.0f;
         sh.abort_flag = 0;
         sh.stop[0] = sh.stop[1] = 0;
         sh.poison = -1;
@@ -392,7 +389,6 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                 if (threadIdx.x < 2 * kRows) {
                     const int c = threadIdx.x & (kRows - 1), of = threadIdx.x / kRows;
                     sh.off[of][c] = 0.0f;
-                    sh.lx[of][c] = c < pc.n_rows ? kNever : -kNever;
                     sh.xm[of][c] = c < pc.n_rows ? 1.0f : 0.0f;
                 }
 #pragma unroll
@@ -444,7 +440,8 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                 if (lane == 0) mbar_arrive(&sh.q_full);
             }
             const int n_chunk = (pc.n_rows + 15) >> 4;  // of 16 rows
-            float sum[2] = {0.0f, 0.0f};  // this warp's keys, rows 2 lane and the next
+            float sum[2] = {0.0f, 0.0f};  // this warp's keys: rows 2 lane and the next
+            bool late = false;            // some row may have no base after the slot's first tile
             // row `my`: its base (-inf: none yet), largest z + value scale at the last move, x
             float row_base = -INFINITY, row_top = -INFINITY, row_x = 0.0f;
 
@@ -458,16 +455,25 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                 fetch_exps(t + 2);
                 fetch_page(t + 4);
                 const bool masked = (t + 1) * kTile > pc.rq.ctx;
+                if (first) late = masked;
                 // the rows that see this key: bit r; all of a token's rows do, or none
                 uint64_t seen = ~0ull;
                 if (masked) {
                     seen = 0;
                     const int n_tok = (pc.rem0 + pc.n_rows + p.group - 1) / p.group;
-#pragma unroll 4
-                    for (int i = 0; i < n_tok; ++i) {
-                        const int r0 = max(i * p.group - pc.rem0, 0), r1 = min((i + 1) * p.group - pc.rem0, pc.n_rows);
-                        const uint64_t rows = (r1 >= 64 ? ~0ull : (1ull << r1) - 1ull) & ~((1ull << r0) - 1ull);
-                        if (sees(p, pc.rq, pc.tok0 + i, l)) seen |= rows;
+#pragma unroll 1
+                    for (int i0 = 0; i0 < n_tok; i0 += 32) {  // a lane loads a token's bits of this warp's keys
+                        uint32_t bits = 0;
+                        if (i0 + lane < n_tok)
+                            bits = seen_bits<true>(p, pc.rq, pc.tok0 + i0 + lane, t * kTile + wq * 32);
+                        const int n_here = min(n_tok - i0, 32);
+#pragma unroll 1
+                        for (int i = 0; i < n_here; ++i) {
+                            const uint32_t w = __shfl_sync(0xFFFFFFFFu, bits, i);
+                            const int at = (i0 + i) * p.group - pc.rem0;  // the token's first row
+                            const uint64_t rows = p.group >= 64 ? ~0ull : (1ull << p.group) - 1ull;
+                            if ((w >> lane) & 1u) seen |= at >= 0 ? rows << at : rows >> -at;
+                        }
                     }
                 }
                 bar_wait(&sh.s_full[s], n_s & 1u, abort_flag, p.err);
@@ -475,15 +481,15 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                 tc_fence_after();
                 const uint64_t km2 = f2(km, km), vm2 = f2(vm, vm);
                 uint32_t x[16];
-                // z of the 16 rows from c on, against the slot's bases (`off`) or none (zeros)
-                auto scores = [&](int c, const float *off) {
+                // z of the 16 rows from c on, against the slot's bases
+                auto scores = [&](int c) {
                     tmem_ld16(tS + c, x);
                     tmem_ld_wait();
                     tmem_tie16(x);
 #pragma unroll
                     for (int k = 0; k < 16; k += 4) {
                         const ulonglong2 q4 = *reinterpret_cast<const ulonglong2 *>(&sh.qm[c + k]);
-                        const ulonglong2 o4 = *reinterpret_cast<const ulonglong2 *>(off + k);
+                        const ulonglong2 o4 = *reinterpret_cast<const ulonglong2 *>(&sh.off[s][c + k]);
                         float a, b;
                         unf2(fma2(mul2(f2(x[k], x[k + 1]), km2), q4.x, o4.x), a, b);
                         x[k] = __float_as_uint(a), x[k + 1] = __float_as_uint(b);
@@ -497,16 +503,25 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                             if (!((w >> k) & 1u)) x[k] = 0xFF800000u;  // -inf
                     }
                 };
-                // weights against the bases and x so far; again where those had to move
+                // Weights against the bases and x so far; again where those had to move.  They
+                // move first in a slot's first tile, and in masked ones where a row may see
+                // its first key.
 #pragma unroll 1
-                for (bool move = first;; move = true) {
+                for (bool move = first || (masked && late), again = false;; move = again = true) {
                     if (move) {
+                        // four rows at a time: this code is rarely in the instruction cache
 #pragma unroll 1
-                        for (int c = 0; c < pc.n_rows; c += 16) {
-                            scores(c, sh.zero);
+                        for (int c = 0; c < pc.n_rows; c += 4) {
+                            uint32_t y[4];
+                            tmem_ld4(tS + c, y);
+                            tmem_ld_wait();
+                            tmem_tie4(y);
+                            const float4 q4 = *reinterpret_cast<const float4 *>(&sh.qm[c]);
+                            const float q[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                const float z = __uint_as_float(x[k]);
+                            for (int k = 0; k < 4; ++k) {
+                                float z = fmaf(__uint_as_float(y[k]) * km, q[k], 0.0f);
+                                if (!((seen >> (c + k)) & 1u)) z = -INFINITY;
                                 const float top = warp_max(z), top_v = warp_max(z + vf);
                                 if (lane == 0) {
                                     sh.top[s][wq][0][c + k] = top;
@@ -533,25 +548,34 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                                 if (had) fix_o *= ex2(row_x - nx);
                                 row_x = nx;
                                 sh.off[s][my] = -row_base;
-                                sh.lx[s][my] = -nx;
                                 sh.xm[s][my] = pow2_int(-(int)nx);
                             }
                             sh.fix_sum[s][my] = fix;
                             sh.fix_o[s][my] = fix_o;
                         }
                         group_sync(s);
-                        if (!first) {  // the sums so far, all of them there
+                        if (!first) {
                             if (2 * lane < pc.n_rows) sum[0] *= sh.fix_sum[s][2 * lane];
                             if (2 * lane + 1 < pc.n_rows) sum[1] *= sh.fix_sum[s][2 * lane + 1];
+                            if (!again) {  // the products so far, all of them there
+                                bar_wait(&sh.pv_done[s], (n_pv[s] - 1u) & 1u, abort_flag, p.err);
+                                tc_fence_after();
+                            }
 #pragma unroll 1
                             for (int i = 0; i < kParts * n_chunk; ++i) {
                                 uint32_t o[16];
                                 tmem_ld16(tO + 16 * i, o);
                                 tmem_ld_wait();
                                 tmem_tie16(o);
-                                const float *f = sh.fix_o[s] + i / kParts * 16;
+                                const float4 *f4 = reinterpret_cast<const float4 *>(sh.fix_o[s] + i / kParts * 16);
 #pragma unroll
-                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f[k]);
+                                for (int k = 0; k < 4; ++k) {
+                                    const float4 f = f4[k];
+                                    o[4 * k] = __float_as_uint(__uint_as_float(o[4 * k]) * f.x);
+                                    o[4 * k + 1] = __float_as_uint(__uint_as_float(o[4 * k + 1]) * f.y);
+                                    o[4 * k + 2] = __float_as_uint(__uint_as_float(o[4 * k + 2]) * f.z);
+                                    o[4 * k + 3] = __float_as_uint(__uint_as_float(o[4 * k + 3]) * f.w);
+                                }
                                 tmem_st16(tO + 16 * i, o);
                             }
                             tmem_st_wait();
@@ -560,16 +584,16 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                         bar_wait(&sh.pv_done[s], (n_pv[s] - 1u) & 1u, abort_flag, p.err);
                         tc_fence_after();
                     }
-                    float most = -INFINITY, most_p = -INFINITY;
-                    uint32_t dst = my_p, swz = my & 7;  // block of 16 columns: (block ^ key) % 8
+                    float most = -INFINITY;
+                    __half2 most_p = __float2half2_rn(0.0f);
+                    const __half2 up = __float2half2_rn(16.0f);
 #pragma unroll 1
                     for (int c = 0; c < pc.n_rows; c += 16) {
-                        scores(c, &sh.off[s][c]);
+                        scores(c);
                         uint32_t pk[kParts][4];
-                        float w[16];
+                        uint64_t w2[8];
 #pragma unroll
                         for (int k = 0; k < 16; k += 4) {
-                            const ulonglong2 l4 = *reinterpret_cast<const ulonglong2 *>(&sh.lx[s][c + k]);
                             const ulonglong2 x4 = *reinterpret_cast<const ulonglong2 *>(&sh.xm[s][c + k]);
                             uint32_t half[kParts][2];
 #pragma unroll
@@ -577,19 +601,19 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                                 const float za = __uint_as_float(x[k + 2 * e]), zb = __uint_as_float(x[k + 2 * e + 1]);
                                 float a, b;
                                 most = fmaxf(fmaxf(most, za), zb);
-                                unf2(add2(f2(za, zb), e ? l4.y : l4.x), a, b);
-                                most_p = fmaxf(fmaxf(most_p, a), b);
-                                w[k + 2 * e] = ex2(za), w[k + 2 * e + 1] = ex2(zb);
-                                uint64_t rest = mul2(mul2(f2(w[k + 2 * e], w[k + 2 * e + 1]), vm2), e ? x4.y : x4.x);
-                                const uint64_t up = f2(16.0f, 16.0f), neg = f2(-16.0f, -16.0f);
+                                w2[k / 2 + e] = f2(ex2(za), ex2(zb));
+                                unf2(mul2(mul2(w2[k / 2 + e], vm2), e ? x4.y : x4.x), a, b);
+                                // fp16's eleven bits, as three parts of four: no part's
+                                // rest is rounded (P below 2^-17 apart)
+                                __half2 rest = __floats2half2_rn(a, b);
+                                most_p = __hmax2(most_p, rest);
 #pragma unroll
                                 for (int part = 0; part < kParts; ++part) {
-                                    unf2(rest, a, b);
-                                    half[part][e] = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+                                    half[part][e] = __nv_cvt_halfraw2_to_fp8x2(rest, __NV_SATFINITE, __NV_E4M3);
                                     if (part + 1 == kParts) break;
-                                    const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
-                                        (__nv_fp8x2_storage_t)half[part][e], __NV_E4M3)));
-                                    rest = fma2(f2(back.x, back.y), neg, mul2(rest, up));  // exact
+                                    const __half2 back(__nv_cvt_fp8x2_to_halfraw2(
+                                        (__nv_fp8x2_storage_t)half[part][e], __NV_E4M3));
+                                    rest = __hmul2(__hsub2(rest, back), up);
                                 }
                             }
 #pragma unroll
@@ -598,34 +622,39 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                         }
 #pragma unroll
                         for (int part = 0; part < kParts; ++part) {
-                            const int at = kParts * (c >> 4) + part;
+                            const int at = kParts * (c >> 4) + part;  // block of 16 columns
                             asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                             dst + (at >> 3) * (kTile * 128) + (((at & 7) ^ swz) << 4)),
+                                             my_p + (at >> 3) * (kTile * 128) + (((at & 7) ^ (my & 7)) << 4)),
                                          "r"(pk[part][0]), "r"(pk[part][1]), "r"(pk[part][2]), "r"(pk[part][3])
                                          : "memory");
                         }
                         // the warp's sums of the rows: half of them go to either half of the lanes
+                        float w[16];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) unf2(w2[k], w[2 * k], w[2 * k + 1]);
 #pragma unroll
                         for (int o = 16; o > 1; o >>= 1) {
-                            const bool up = lane & o;
+                            const bool upper = lane & o;
 #pragma unroll
                             for (int k = 0; k < o / 2; ++k) {
-                                const float keep = up ? w[k + o / 2] : w[k], give = up ? w[k] : w[k + o / 2];
+                                const float keep = upper ? w[k + o / 2] : w[k], give = upper ? w[k] : w[k + o / 2];
                                 w[k] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
                             }
                         }
                         w[0] += __shfl_xor_sync(0xFFFFFFFFu, w[0], 1);
-                        if (!(lane & 1)) sh.tile_sum[s][wq][c + (lane >> 1)] = w[0];
+                        if (!(lane & 1)) sh.sums[s][wq][c + (lane >> 1)] = w[0];
                     }
-                    if (move || !group_any(s, most > kLazy || most_p + vf > kCap)) break;
+                    if (again ||
+                        !group_any(s, most > kLazy || fmaxf(__low2float(most_p), __high2float(most_p)) > kCap))
+                        break;
                 }
                 // the scores are read: the next tile's may come
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.s_free[s]);
                 ++n_pv[s];
-                sum[0] += sh.tile_sum[s][wq][2 * lane];  // (of rows that are not there: unused)
-                sum[1] += sh.tile_sum[s][wq][2 * lane + 1];
+                sum[0] += sh.sums[s][wq][2 * lane];  // (of rows that are not there: unused)
+                sum[1] += sh.sums[s][wq][2 * lane + 1];
                 // What a row does not see must not reach it, but a product 0 * NaN would: the
                 // values past the end, and NaN codes where some row may be masked, become
                 // zero; the epilogue adds the NaN to the rows that do see it.
@@ -665,6 +694,7 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
             tiles_done += n;
             const bool used1 = n > 1;
             n_pv[s ^ 1] += (uint32_t)((n + s) >> 1);  // slot 0 has (n + 1) / 2 tiles, slot 1 n / 2
+            __syncwarp();
             sh.sums[s][wq][2 * lane] = sum[0];
             sh.sums[s][wq][2 * lane + 1] = sum[1];
             if (my < pc.n_rows) sh.top[s][0][0][my] = row_base, sh.top[s][0][1][my] = row_x;
@@ -781,6 +811,11 @@ template <int kD> dflash2_status launch_one(const DeviceInfo &di, Params p, cuda
     }
     p.row_shift = kRowShift;
     p.item_units = kItemUnits;
+    const int64_t rows = (int64_t)p.total_q * p.group;
+    for (int i = 0; i < 4; ++i) {
+        p.tile_units[i] = kTileUnits[i];
+        if (i == 0 || rows > kRows / 4 * i) p.most_units = kTileUnits[i];
+    }
     p.n_cta = di.sm_count;
     launch_k(fn, dim3((unsigned)p.n_cta), dim3(C::kThreads), C::kSmem, st, p, maps[0], maps[1]);
     const dflash2_status s = launch_status();

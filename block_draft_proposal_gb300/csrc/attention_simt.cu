@@ -431,6 +431,8 @@ dflash2_status launch_simt(const DeviceInfo &di, Params p, bool paged, int32_t d
                        (paged || (p.k_stride % 4 == 0 && p.v_stride % 4 == 0));
     p.n_cta = di.sm_count;
     p.item_units = 1;
+    for (int i = 0; i < 4; ++i) p.tile_units[i] = 1;
+    p.most_units = 1;
     dflash2_status s;
     if (dtype == DFLASH2_F32) {
         if (!paged)

@@ -191,33 +191,6 @@ struct Levels {
     }
 };
 
-// Bits j0 .. j0 + 31 of a node's mask words (bit k: it sees node j0 + k); nodes
-// before 0 are context and seen.
-__device__ __forceinline__ uint32_t tree_bits(const int64_t *words, int32_t n_words, int32_t j0) {
-    if (j0 <= -32) return 0xFFFFFFFFu;
-    if (j0 < 0) return (uint32_t)((uint64_t)__ldg(words) << -j0) | ((1u << -j0) - 1u);
-    const int32_t w = j0 >> 6, s = j0 & 63;
-    if (w >= n_words) return 0u;
-    uint64_t x = (uint64_t)__ldg(words + w) >> s;
-    if (s > 32 && w + 1 < n_words) x |= (uint64_t)__ldg(words + w + 1) << (64 - s);
-    return (uint32_t)x;
-}
-// Bits of the positions first .. first + 31 that lie below `end`.
-__device__ __forceinline__ uint32_t below(int32_t first, int32_t end) {
-    const int32_t n = end - first;
-    return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
-}
-
-// The positions first .. first + 31 that token i of the request sees.
-template <bool kPaged>
-__device__ __forceinline__ uint32_t seen_bits(const Params &p, const Request &rq, int32_t i, int32_t first) {
-    const bool tree = kPaged && p.tree_mask;
-    uint32_t w = below(first, min(rq.len, tree ? rq.len : rq.ctx + i + 1));
-    if (tree && w)
-        w &= tree_bits(p.tree_mask + (int64_t)(rq.t0 + i) * p.mask_words, p.mask_words, first - rq.ctx);
-    return w;
-}
-
 // ---- the kernel ------------------------------------------------------------------
 template <int kD, bool kE4M3, bool kPaged>
 __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
@@ -1365,6 +1338,8 @@ dflash2_status launch_one(const DeviceInfo &di, Params p, cudaStream_t st) {
     }
     p.row_shift = kRowShift;
     p.item_units = kItemUnits;
+    for (int i = 0; i < 4; ++i) p.tile_units[i] = 1;
+    p.most_units = 1;
     // prompts: every row block of every request, at most one short one each
     const int64_t items = ((((int64_t)p.total_q * p.group) >> kRowShift) + p.batch) * p.kv_heads;
     p.n_cta = kPaged || items > di.sm_count ? di.sm_count : (int32_t)items;

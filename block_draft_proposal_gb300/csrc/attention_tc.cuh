@@ -137,6 +137,14 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t *r) {
         : DF_OUT8(DF_SET, r)
         : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&r)[4]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_tie4(uint32_t (&r)[4]) {
+    asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]));
+}
 __device__ __forceinline__ void tmem_tie8(uint32_t *r) { asm volatile("" : DF_OUT8(DF_TIE, r)); }
 
 // Register split of a warpgroup, inside its branch (ptxas allots a branch what it sees there).
@@ -259,7 +267,8 @@ struct Walk {
                 rq = load_request<true>(p, b, &bad);
                 n = request_units(p, rq);
             }
-            const uint32_t worth = key_tiles(rq) + p.item_units, nrb = row_blocks(p, rq);
+            const int32_t tile = tile_units(p, rq), tiles = key_tiles(rq);
+            const uint32_t worth = tiles * tile + p.item_units, nrb = row_blocks(p, rq);
             uint32_t item;
             int32_t o0;
             if (n < (1ll << 31)) {
@@ -273,25 +282,52 @@ struct Walk {
             }
             const int32_t o1 = (int32_t)min((int64_t)worth, o0 + (end - u));
             u += o1 - o0;
-            pc->t0 = max(o0 - p.item_units, 0);
-            pc->t1 = o1 - p.item_units;
-            if (pc->t1 <= pc->t0) continue;  // the range ends within the item's extra units
+            pc->t0 = (max(o0 - p.item_units, 0) + tile - 1) / tile;
+            pc->t1 = (max(o1 - p.item_units, 0) + tile - 1) / tile;
+            if (pc->t1 <= pc->t0) continue;  // no tile's first unit lies in the range
             pc->t1a = pc->t1;
             pc->rq = rq;
             pc->b = b;
             pc->h = (int32_t)(item / nrb);
             pc->row0 = (int32_t)(item - (uint32_t)pc->h * nrb) << p.row_shift;
             pc->n_rows = min(1 << p.row_shift, rq.t * p.group - pc->row0);
-            pc->slot = pc->t0 == 0 && o1 == (int32_t)worth ? -1 : 2 * (int32_t)blockIdx.x + (pc->t0 == 0);
+            pc->slot = pc->t0 == 0 && pc->t1 == tiles ? -1 : 2 * (int32_t)blockIdx.x + (pc->t0 == 0);
             pc->guard_from = rq.ctx / kTile;
             if (pc->slot >= 0 && pc->t0 == 0) {
                 join.rows = pc->n_rows, join.row0 = pc->row0, join.t0 = rq.t0, join.h = pc->h;
-                join.last = cta_of(u - o1 + worth - 1, units, split_ctas(p, units));
+                join.last = cta_of(u - o1 + p.item_units + (tiles - 1) * tile, units, split_ctas(p, units));
             }
             return;
         }
     }
 };
+
+// Bits j0 .. j0 + 31 of a node's mask words (bit k: it sees node j0 + k); nodes
+// before 0 are context and seen.
+__device__ __forceinline__ uint32_t tree_bits(const int64_t *words, int32_t n_words, int32_t j0) {
+    if (j0 <= -32) return 0xFFFFFFFFu;
+    if (j0 < 0) return (uint32_t)((uint64_t)__ldg(words) << -j0) | ((1u << -j0) - 1u);
+    const int32_t w = j0 >> 6, s = j0 & 63;
+    if (w >= n_words) return 0u;
+    uint64_t x = (uint64_t)__ldg(words + w) >> s;
+    if (s > 32 && w + 1 < n_words) x |= (uint64_t)__ldg(words + w + 1) << (64 - s);
+    return (uint32_t)x;
+}
+// Bits of the positions first .. first + 31 that lie below `end`.
+__device__ __forceinline__ uint32_t below(int32_t first, int32_t end) {
+    const int32_t n = end - first;
+    return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
+}
+
+// The positions first .. first + 31 that token i of the request sees.
+template <bool kPaged>
+__device__ __forceinline__ uint32_t seen_bits(const Params &p, const Request &rq, int32_t i, int32_t first) {
+    const bool tree = kPaged && p.tree_mask;
+    uint32_t w = below(first, min(rq.len, tree ? rq.len : rq.ctx + i + 1));
+    if (tree && w)
+        w &= tree_bits(p.tree_mask + (int64_t)(rq.t0 + i) * p.mask_words, p.mask_words, first - rq.ctx);
+    return w;
+}
 
 // Values of the keys [l0, l1) that token i of the request sees and that are not
 // finite, added to columns [col, col + cols) of a row as it was written (`part`:
