@@ -48,8 +48,8 @@ struct Params {
     float *part;                   // the partial rows' slots
     int32_t part_rows;             // rows of a slot
     int32_t row_shift;             // log2 of the rows of a block
-    int32_t item_units;            // units of an item beside its key tiles
     int32_t tile_units[4];         // units of a key tile, by quarters of a full row block
+    int32_t item_units[4];         // units of an item beside its key tiles
     int32_t most_units;            // the largest of those that a request may have
     int32_t n_cta;                 // CTAs the work is split over
     int32_t *err;
@@ -116,15 +116,16 @@ __device__ __forceinline__ int32_t row_blocks(const Params &p, const Request &r)
 __device__ __forceinline__ int32_t key_tiles(const Request &r) {
     return max(1, (r.len + kKeyTile - 1) / kKeyTile);
 }
-// Units of a key tile: those of the request's first row block.
-__device__ __forceinline__ int32_t tile_units(const Params &p, const Request &r) {
+// Which of tile_units and item_units holds: that of the request's first row block.
+__device__ __forceinline__ int32_t units_class(const Params &p, const Request &r) {
     const uint32_t rows = min((uint32_t)r.t * (uint32_t)p.group, 1u << p.row_shift);
-    return p.tile_units[(max(rows, 1u) - 1u) >> (p.row_shift - 2)];
+    return (max(rows, 1u) - 1u) >> (p.row_shift - 2);
 }
 // Units of one item (a head and row block) of the request, and of all of them; 0 when it
 // has no rows.
 __device__ __forceinline__ int64_t units_of_item(const Params &p, const Request &r) {
-    return (int64_t)key_tiles(r) * tile_units(p, r) + p.item_units;
+    const int32_t c = units_class(p, r);
+    return (int64_t)key_tiles(r) * p.tile_units[c] + p.item_units[c];
 }
 __device__ __forceinline__ int64_t request_units(const Params &p, const Request &r) {
     return (int64_t)p.kv_heads * row_blocks(p, r) * units_of_item(p, r);
@@ -134,7 +135,8 @@ __device__ __forceinline__ int64_t request_units(const Params &p, const Request 
 // CTA's that holds its first unit; split_ctas leaves every range as many units as any
 // tile has, so that no CTA between two others of an item has no tile.
 __device__ __forceinline__ int64_t split_ctas(const Params &p, int64_t units) {
-    return units < p.n_cta * (int64_t)p.most_units ? (units + p.most_units - 1) / p.most_units : p.n_cta;
+    if (units >= p.n_cta * (int64_t)p.most_units) return p.n_cta;
+    return units < p.most_units ? min(units, (int64_t)1) : units / p.most_units;
 }
 __device__ __forceinline__ int64_t range_start(int64_t c, int64_t units, int64_t n_cta) {
     return c * units / n_cta;

@@ -37,7 +37,7 @@ namespace {
 
 constexpr int kRowShift = 6, kRows = 1 << kRowShift;  // rows of a block
 // Units of a key tile with up to 16, 32, 48 and 64 rows, and of an item's start and end.
-constexpr int kTileUnits[4] = {10, 13, 16, 20}, kItemUnits = 40;
+constexpr int kTileUnits[4] = {10, 13, 17, 21}, kItemUnits[4] = {55, 75, 95, 115};
 constexpr int kParts = 3;       // of a weight
 constexpr float kLazy = 8.0f;   // log2 growth of a maximum that moves its base
 constexpr float kCap = 256.0f;  // the largest P
@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
             const int32_t rows_box = min(p.page_size, kTile);
             const int32_t page_shift = 31 - __clz(p.page_size);
             const int32_t box_shift = 7 - min(page_shift, 7);  // log2 of the boxes of a tile
+            const uint8_t *exps = of ? p.v_exp : p.k_exp;
             Piece pc{};
             // Page numbers come eight key tiles at a time: the lanes load the next eight's
             // while one thread issues the copies of these.  -1: no page (past the end, or
@@ -195,6 +196,10 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                     const bool good = (uint64_t)(int64_t)ids[k] < (uint64_t)p.num_pages;
                     if (!good && line_of(tile, k) >= 0) bad_page = true;
                     if (e < (8 << box_shift)) sh.pages[of][buffer][e] = good ? ids[k] : -1;
+                    // the box's exponents, on their way to L2
+                    if (good)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                            exps + ((int64_t)ids[k] * p.kv_heads + pc.h) * p.page_size + (line_of(tile, k) & (p.page_size - 1))));
                 }
                 __syncwarp();
             };
@@ -282,6 +287,7 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                 const int32_t n = pc.t1 - pc.t0, cols = (pc.n_rows + 15) & ~15;
                 const uint32_t id_s = idesc_e4m3(128, cols);
                 const uint32_t id_o = idesc_e4m3(128, kParts * cols) | (1u << 15) | (1u << 16);  // both MN-major
+                const bool two_p = pc.n_rows <= kRows / 2;
                 auto scores = [&](int32_t j) {
                     const uint32_t kt = tiles_done + j, i = kt % kStages;
                     if (!bar_wait(&sh.raw_full[0][i], (kt / kStages) & 1u, abort_flag, p.err) ||
@@ -312,7 +318,7 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                     ++n_p;
                     tc_fence_after();
                     const uint32_t vd = desc_lo(sm_raw[1] + i * C::kRawBytes);
-                    const uint32_t pd = desc_lo(sm_p + s * C::kPBytes) | kMnMajorLo;
+                    const uint32_t pd = desc_lo(sm_p + s * C::kPBytes + (two_p ? ((j >> 1) & 1) * (kTile * 128) : 0)) | kMnMajorLo;
 #pragma unroll
                     for (int k = 0; k < kTile / 32; ++k)
                         tc_mma_f8(dO, desc64(vd + k * (32 * kD >> 4), kVHi), desc64(pd + k * (32 * 128 >> 4), kMnMajorHi),
@@ -336,7 +342,6 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
         const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
         const uint32_t tS = s * kRows + lane_base;
         const uint32_t tO = 128 + s * (kParts * kRows) + lane_base;
-        const uint32_t my_p = sm_p + s * C::kPBytes + my * 128;
         const uint32_t magic = (65536u + p.group - 1) / (uint32_t)p.group;  // x / group for x < 512
         const int32_t page_shift = 31 - __clz(p.page_size);
         uint32_t n_piece = 0, n_s = 0, tiles_done = 0;
@@ -440,6 +445,8 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                 if (lane == 0) mbar_arrive(&sh.q_full);
             }
             const int n_chunk = (pc.n_rows + 15) >> 4;  // of 16 rows
+            // up to 32 rows' weights are one block of columns: two of them in turns
+            const bool two_p = pc.n_rows <= kRows / 2;
             float sum[2] = {0.0f, 0.0f};  // this warp's keys: rows 2 lane and the next
             bool late = false;            // some row may have no base after the slot's first tile
             // row `my`: its base (-inf: none yet), largest z + value scale at the last move, x
@@ -480,6 +487,9 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                 ++n_s;
                 tc_fence_after();
                 const uint64_t km2 = f2(km, km), vm2 = f2(vm, vm);
+                const uint32_t my_p = sm_p + s * C::kPBytes + my * 128 +
+                                      (two_p ? (((t - pc.t0) >> 1) & 1) * (kTile * 128) : 0);
+                bool pv_waited = first;
                 uint32_t x[16];
                 // z of the 16 rows from c on, against the slot's bases
                 auto scores = [&](int c) {
@@ -557,10 +567,11 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                         if (!first) {
                             if (2 * lane < pc.n_rows) sum[0] *= sh.fix_sum[s][2 * lane];
                             if (2 * lane + 1 < pc.n_rows) sum[1] *= sh.fix_sum[s][2 * lane + 1];
-                            if (!again) {  // the products so far, all of them there
+                            if (!pv_waited) {  // the products so far, all of them there
                                 bar_wait(&sh.pv_done[s], (n_pv[s] - 1u) & 1u, abort_flag, p.err);
-                                tc_fence_after();
+                                pv_waited = true;
                             }
+                            tc_fence_after();
 #pragma unroll 1
                             for (int i = 0; i < kParts * n_chunk; ++i) {
                                 uint32_t o[16];
@@ -580,9 +591,9 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                             }
                             tmem_st_wait();
                         }
-                    } else {  // the last weights are read
+                    } else if (!two_p) {  // the last weights are read
                         bar_wait(&sh.pv_done[s], (n_pv[s] - 1u) & 1u, abort_flag, p.err);
-                        tc_fence_after();
+                        pv_waited = true;
                     }
                     float most = -INFINITY;
                     __half2 most_p = __float2half2_rn(0.0f);
@@ -652,6 +663,8 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.s_free[s]);
+                // the products of the slot's last tile, whose weights' place the next one takes
+                if (!pv_waited) bar_wait(&sh.pv_done[s], (n_pv[s] - 1u) & 1u, abort_flag, p.err);
                 ++n_pv[s];
                 sum[0] += sh.sums[s][wq][2 * lane];  // (of rows that are not there: unused)
                 sum[1] += sh.sums[s][wq][2 * lane + 1];
@@ -810,10 +823,10 @@ template <int kD> dflash2_status launch_one(const DeviceInfo &di, Params p, cuda
         if (s != DFLASH2_OK) return s;
     }
     p.row_shift = kRowShift;
-    p.item_units = kItemUnits;
     const int64_t rows = (int64_t)p.total_q * p.group;
     for (int i = 0; i < 4; ++i) {
         p.tile_units[i] = kTileUnits[i];
+        p.item_units[i] = kItemUnits[i];
         if (i == 0 || rows > kRows / 4 * i) p.most_units = kTileUnits[i];
     }
     p.n_cta = di.sm_count;

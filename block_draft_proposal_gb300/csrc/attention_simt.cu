@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kKeys = 64;
+constexpr int kItemUnits = 1;  // units of an item's start and end, beside its key tiles
 
 __host__ __device__ constexpr int simt_smem_floats(int rows, int dmax) {
     return rows * dmax + kKeys * (dmax + 4) + kKeys * dmax + rows * kKeys;
@@ -266,11 +267,11 @@ __global__ void __launch_bounds__(kThreads) simt_kernel(const Params p, bool vec
             const Request r = load_request<true>(p, b, &bad);
             const int64_t n = request_units(p, r);
             while (u < end && u < before + n) {
-                const int32_t tiles = key_tiles(r), worth = tiles + p.item_units;
+                const int32_t tiles = key_tiles(r), worth = tiles + kItemUnits;
                 const int64_t item = (u - before) / worth;
                 const int32_t o0 = (int32_t)((u - before) % worth);
                 const int32_t o1 = (int32_t)min((int64_t)worth, o0 + (end - u));
-                const int32_t t0 = max(o0 - p.item_units, 0), t1 = o1 - p.item_units;
+                const int32_t t0 = max(o0 - kItemUnits, 0), t1 = o1 - kItemUnits;
                 const int32_t nrb = row_blocks(p, r);
                 const bool whole = t0 == 0 && t1 == tiles;
                 if (t1 > t0)
@@ -430,8 +431,7 @@ dflash2_status launch_simt(const DeviceInfo &di, Params p, bool paged, int32_t d
     const bool vec_k = four && aligned_to(p.k, 4 * kel) && aligned_to(p.v, 4 * kel) &&
                        (paged || (p.k_stride % 4 == 0 && p.v_stride % 4 == 0));
     p.n_cta = di.sm_count;
-    p.item_units = 1;
-    for (int i = 0; i < 4; ++i) p.tile_units[i] = 1;
+    for (int i = 0; i < 4; ++i) p.tile_units[i] = 1, p.item_units[i] = kItemUnits;
     p.most_units = 1;
     dflash2_status s;
     if (dtype == DFLASH2_F32) {

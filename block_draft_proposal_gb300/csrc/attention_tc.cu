@@ -1337,8 +1337,7 @@ dflash2_status launch_one(const DeviceInfo &di, Params p, cudaStream_t st) {
         if (s != DFLASH2_OK) return s;
     }
     p.row_shift = kRowShift;
-    p.item_units = kItemUnits;
-    for (int i = 0; i < 4; ++i) p.tile_units[i] = 1;
+    for (int i = 0; i < 4; ++i) p.tile_units[i] = 1, p.item_units[i] = kItemUnits;
     p.most_units = 1;
     // prompts: every row block of every request, at most one short one each
     const int64_t items = ((((int64_t)p.total_q * p.group) >> kRowShift) + p.batch) * p.kv_heads;

@@ -267,8 +267,9 @@ struct Walk {
                 rq = load_request<true>(p, b, &bad);
                 n = request_units(p, rq);
             }
-            const int32_t tile = tile_units(p, rq), tiles = key_tiles(rq);
-            const uint32_t worth = tiles * tile + p.item_units, nrb = row_blocks(p, rq);
+            const int32_t c = units_class(p, rq), tile = p.tile_units[c], start = p.item_units[c];
+            const int32_t tiles = key_tiles(rq);
+            const uint32_t worth = tiles * tile + start, nrb = row_blocks(p, rq);
             uint32_t item;
             int32_t o0;
             if (n < (1ll << 31)) {
@@ -282,8 +283,8 @@ struct Walk {
             }
             const int32_t o1 = (int32_t)min((int64_t)worth, o0 + (end - u));
             u += o1 - o0;
-            pc->t0 = (max(o0 - p.item_units, 0) + tile - 1) / tile;
-            pc->t1 = (max(o1 - p.item_units, 0) + tile - 1) / tile;
+            pc->t0 = (max(o0 - start, 0) + tile - 1) / tile;
+            pc->t1 = (max(o1 - start, 0) + tile - 1) / tile;
             if (pc->t1 <= pc->t0) continue;  // no tile's first unit lies in the range
             pc->t1a = pc->t1;
             pc->rq = rq;
@@ -295,7 +296,7 @@ struct Walk {
             pc->guard_from = rq.ctx / kTile;
             if (pc->slot >= 0 && pc->t0 == 0) {
                 join.rows = pc->n_rows, join.row0 = pc->row0, join.t0 = rq.t0, join.h = pc->h;
-                join.last = cta_of(u - o1 + p.item_units + (tiles - 1) * tile, units, split_ctas(p, units));
+                join.last = cta_of(u - o1 + start + (tiles - 1) * tile, units, split_ctas(p, units));
             }
             return;
         }
