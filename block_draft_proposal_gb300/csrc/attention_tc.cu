@@ -69,7 +69,7 @@ struct Shared {
     int32_t pages[2][2][kTile / 16 * 8 + 1];  // page numbers of eight key tiles, twice, by producer
     uint64_t piece_full[kPieces], piece_empty[kPieces];
     uint64_t full[8], empty[8];  // operand ring (E4M3: filled by the widening warps)
-    uint64_t guard_go[8], guard_done[8];  // value tiles handed to the guard warp and back, in order
+    uint64_t guard_go[8], guard_done[8];  // value tiles on their way, for the guard warp, and back, in order
     uint64_t s_full[2], p_full[2][2], o_full[2];  // weights come in halves of 64 keys
     uint64_t turn[2];            // shared: whose weights' and next scores' MMAs come next
     uint64_t q_full, drain[2];
@@ -286,6 +286,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
             const bool of_keys = !kE4M3 || warp == 9;
             uint32_t pos = 0, n_piece = 0;  // operand tiles issued
             uint32_t n_key = 0, n_value = 0;
+            [[maybe_unused]] uint32_t n_guard = 0;
             bool ok = true, bad_page = false;
             const int32_t rows_box = kPaged ? min(p.page_size, kTile) : kTile;
             const int32_t page_shift = kPaged ? 31 - __clz(p.page_size) : 0;
@@ -361,6 +362,8 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                         id = next;
                     }
                 }
+                // the guard may wait for the copy now: the operand's barrier is in its phase
+                if (!kE4M3 && values && tile >= pc.guard_from) mbar_arrive(&sh.guard_go[n_guard++ & 7u]);
                 n_key += !values;
                 n_value += values;
                 ++pos;
@@ -498,12 +501,10 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                     tc_commit(o.empty);
                     return true;
                 };
-                // sums over the value operand of key tile t; issuer 0 hands guarded ones to
-                // the guard warp
+                // sums over the value operand of key tile t, once the guard is done with it
                 auto values = [&](int32_t t, const Place &o, bool mine, bool acc, bool last) {
                     if (!bar_wait(o.full, o.phase, abort_flag, p.err)) return false;
                     if (!kE4M3 && t >= pc.guard_from) {
-                        if (s == 0) mbar_arrive(&sh.guard_go[n_guard & 7u]);
                         if (mine &&
                             !bar_wait(&sh.guard_done[n_guard & 7u], (n_guard >> 3) & 1u, abort_flag, p.err))
                             return false;
@@ -589,7 +590,8 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                 const int32_t n = pc.t1 - pc.t0;
                 for (int32_t j = max(0, pc.guard_from - pc.t0); ok && j < n; ++j) {
                     const uint32_t nv = pos + (pc.shared() ? 2 * j + 1 : j + 1 < n ? 2 * j + 2 : 2 * n - 1);
-                    ok = bar_wait(&sh.guard_go[n_guard & 7u], (n_guard >> 3) & 1u, abort_flag, p.err);
+                    ok = bar_wait(&sh.guard_go[n_guard & 7u], (n_guard >> 3) & 1u, abort_flag, p.err) &&
+                         bar_wait(&sh.full[nv % kStages], (nv / kStages) & 1u, abort_flag, p.err);
                     if (!ok) break;
                     // rows [low, live) of the tile may be masked for some row; from live on
                     // they are no keys.  A 128-byte row of a column block is 8 chunks.
@@ -791,31 +793,45 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
             // few rows: `copies` copies of them in the accumulator's rows, one per 128 /
             // copies, each with its share of the tile's keys (log2 of the copies)
             const int split = !kPaged || pc.n_rows > 64 ? 0 : pc.n_rows > 32 ? 1 : 2;
-            // queries: kD / 8 lanes hold a row, 8 values each; eight rows in flight per thread
+            // queries: kD / 8 lanes hold a row, 8 values each.  bf16: copied as they are, all rows
+            // at once; E4M3: eight rows in flight per thread
             {
                 constexpr int kLanes = kD / 8, kStep = 256 / kLanes;
-                [[maybe_unused]] const uint32_t row_lanes = ((1u << kLanes) - 1u) << (lane & ~(kLanes - 1));
                 const int l8 = threadIdx.x % kLanes;
                 const __nv_bfloat16 *q0 = (const __nv_bfloat16 *)p.q + (int64_t)(pc.rq.t0 + pc.tok0) * p.q_stride +
                                           (int64_t)pc.h * p.group * kD + l8 * 8;
-#pragma unroll 1
-                for (int rb = threadIdx.x / kLanes; rb < pc.n_rows; rb += 8 * kStep) {
-                    uint4 v[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int r = rb + i * kStep;
+                if constexpr (!kE4M3) {
+#pragma unroll 4
+                    for (int r = threadIdx.x / kLanes; r < pc.n_rows; r += kStep) {
                         const uint32_t x = pc.rem0 + r, dt = (x * magic) >> 16;
-                        v[i] = make_uint4(0u, 0u, 0u, 0u);
-                        if (r < pc.n_rows)
-                            v[i] = __ldg(reinterpret_cast<const uint4 *>(
-                                q0 + (int64_t)dt * p.q_stride + (int)(x - dt * p.group) * kD));
+                        const __nv_bfloat16 *src = q0 + (int64_t)dt * p.q_stride + (int)(x - dt * p.group) * kD;
+                        for (int k = 0; k < (1 << split); ++k) {
+                            const int row = (r & 127) + (k << (7 - split));
+                            const uint32_t dst = sm_q + (r >> 7) * C::kTileBytes + (l8 >> 3) * (kTile * 128) +
+                                                 row * 128 + (((l8 & 7) ^ (row & 7)) << 4);
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+                        }
                     }
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                } else {
+                    const uint32_t row_lanes = ((1u << kLanes) - 1u) << (lane & ~(kLanes - 1));
+#pragma unroll 1
+                    for (int rb = threadIdx.x / kLanes; rb < pc.n_rows; rb += 8 * kStep) {
+                        uint4 v[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int r = rb + i * kStep;
-                        if (r >= pc.n_rows) break;
-                        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                        if constexpr (kE4M3) {
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = rb + i * kStep;
+                            const uint32_t x = pc.rem0 + r, dt = (x * magic) >> 16;
+                            v[i] = make_uint4(0u, 0u, 0u, 0u);
+                            if (r < pc.n_rows)
+                                v[i] = __ldg(reinterpret_cast<const uint4 *>(
+                                    q0 + (int64_t)dt * p.q_stride + (int)(x - dt * p.group) * kD));
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = rb + i * kStep;
+                            if (r >= pc.n_rows) break;
+                            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
                             float f[8], amax = 0.0f;
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
@@ -855,15 +871,6 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                                              : "memory");
                                 asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(dst + C::kRawBytes), "r"(lo[0]),
                                              "r"(lo[1])
-                                             : "memory");
-                            }
-                        } else {
-                            for (int k = 0; k < (1 << split); ++k) {
-                                const int row = (r & 127) + (k << (7 - split));
-                                const uint32_t dst = sm_q + (r >> 7) * C::kTileBytes + (l8 >> 3) * (kTile * 128) +
-                                                     row * 128 + (((l8 & 7) ^ (row & 7)) << 4);
-                                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[0]),
-                                             "r"(w[1]), "r"(w[2]), "r"(w[3])
                                              : "memory");
                             }
                         }
@@ -1164,7 +1171,10 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                 if (live_warp) {
                     const float g = part ? up : sum == 0.0f ? 0.0f : up / sum;
                     float4 *part_col = reinterpret_cast<float4 *>(part) + r_blk;  // [kD / 4][part_rows] of four
-                    __nv_bfloat16 *out_row = (__nv_bfloat16 *)p.out + row * kD;
+                    // output rows through the slot's query tile, which no product reads any more, so
+                    // that a warp writes whole rows (each thread its own: 32 lines a store)
+                    constexpr int kRow16 = kD / 8;
+                    uint4 *stage = reinterpret_cast<uint4 *>(dyn + pad + s * C::kTileBytes) + wq * 32 * kRow16;
 #pragma unroll 1
                     for (int c0 = 0; c0 < kD; c0 += 32) {
                         uint32_t a[32];
@@ -1181,7 +1191,6 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                                     make_float4(__uint_as_float(a[4 * k]), __uint_as_float(a[4 * k + 1]),
                                                 __uint_as_float(a[4 * k + 2]), __uint_as_float(a[4 * k + 3]));
                         } else {
-                            uint4 *dst = reinterpret_cast<uint4 *>(out_row + c0);
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
                                 uint32_t o[4];
@@ -1189,8 +1198,20 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                                 for (int e = 0; e < 4; ++e)
                                     o[e] = pack16<false>(__uint_as_float(a[8 * k + 2 * e]),
                                                          __uint_as_float(a[8 * k + 2 * e + 1]));
-                                dst[k] = make_uint4(o[0], o[1], o[2], o[3]);
+                                stage[lane * kRow16 + ((c0 / 8 + k) ^ (lane & 7))] = make_uint4(o[0], o[1], o[2], o[3]);
                             }
+                        }
+                    }
+                    if (!part) {
+                        __syncwarp();
+                        const int first_row = r_blk - lane, rows = min(32, pc.n_rows - first_row);
+#pragma unroll 4
+                        for (int i = lane / kRow16; i < rows; i += 32 / kRow16) {
+                            const uint32_t x = pc.rem0 + first_row + i, dt = (x * magic) >> 16;
+                            const int64_t at = (int64_t)(pc.rq.t0 + pc.tok0 + (int)dt) * p.q_heads + pc.h * p.group +
+                                               (int)(x - dt * p.group);
+                            const int c = lane % kRow16;
+                            reinterpret_cast<uint4 *>((__nv_bfloat16 *)p.out + at * kD)[c] = stage[i * kRow16 + (c ^ (i & 7))];
                         }
                     }
                 }
