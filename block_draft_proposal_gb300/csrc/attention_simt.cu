@@ -32,16 +32,21 @@ __host__ __device__ constexpr int simt_smem_floats(int rows, int dmax) {
 template <typename T, int kDMax, typename PtrF, typename MulF>
 __device__ __forceinline__ void stage_rows(float *dst, int pitch, int n, int width, bool vec,
                                            PtrF row_ptr, MulF row_mul) {
-    constexpr int kChunks = kDMax / 4;
-    for (int i = threadIdx.x; i < n * kChunks; i += kThreads) {
-        const int r = i / kChunks, c = (i % kChunks) * 4;
-        const T *src = row_ptr(r);
-        float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (src && c < width) {
+    constexpr int kChunks = kDMax / 4, kFly = 4;  // loads in flight per thread
+#pragma unroll 1
+    for (int i0 = threadIdx.x; i0 < n * kChunks; i0 += kFly * kThreads) {
+        float x[kFly][4];
+#pragma unroll
+        for (int f = 0; f < kFly; ++f) {
+            const int i = i0 + f * kThreads, r = i / kChunks, c = (i % kChunks) * 4;
+            const T *src = i < n * kChunks ? row_ptr(r) : nullptr;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[f][k] = 0.0f;
+            if (!src || c >= width) continue;
             if (vec) {  // width % 4 == 0 and four elements aligned
                 if constexpr (sizeof(T) == 4) {
-                    const float4 f = *reinterpret_cast<const float4 *>(src + c);
-                    x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+                    const float4 q = *reinterpret_cast<const float4 *>(src + c);
+                    x[f][0] = q.x, x[f][1] = q.y, x[f][2] = q.z, x[f][3] = q.w;
                 } else {
                     T e[4];
                     if constexpr (sizeof(T) == 2)
@@ -50,18 +55,24 @@ __device__ __forceinline__ void stage_rows(float *dst, int pitch, int n, int wid
                         *reinterpret_cast<uint32_t *>(e) =
                             *reinterpret_cast<const uint32_t *>(src + c);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) x[k] = as_f32(e[k]);
+                    for (int k = 0; k < 4; ++k) x[f][k] = as_f32(e[k]);
                 }
             } else {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    if (c + k < width) x[k] = as_f32(src[c + k]);
+                    if (c + k < width) x[f][k] = as_f32(src[c + k]);
             }
             const float mul = row_mul(r);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) x[k] *= mul;
+            for (int k = 0; k < 4; ++k) x[f][k] *= mul;
         }
-        *reinterpret_cast<float4 *>(dst + r * pitch + c) = make_float4(x[0], x[1], x[2], x[3]);
+#pragma unroll
+        for (int f = 0; f < kFly; ++f) {
+            const int i = i0 + f * kThreads;
+            if (i < n * kChunks)
+                *reinterpret_cast<float4 *>(dst + i / kChunks * pitch + i % kChunks * 4) =
+                    make_float4(x[f][0], x[f][1], x[f][2], x[f][3]);
+        }
     }
 }
 
@@ -197,21 +208,30 @@ __device__ void run_piece(const Params &p, const Request &rq, int32_t b, int32_t
                 for (int e = 0; e < 4; ++e) o[i][q][e] *= fix;
         }
         __syncwarp();  // a row's 16 threads are in one warp: its weights are written
-        for (int key = 0; key < nk; ++key) {
-            float4 vq[kQuads];
-#pragma unroll
-            for (int q = 0; q < kQuads; ++q)
-                vq[q] = *reinterpret_cast<const float4 *>(sv + key * kDMax + 64 * q + 4 * tx);
+        // four keys at a time (past nk: weights of zero, and rows of zeros)
+        for (int key = 0; key < nk; key += 4) {
+            float w[kPer][4];
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
-                const float w = sp[(ty * kPer + i) * kKeys + key];
-                if (w != 0.0f) {  // what a row does not see never reaches it, NaN included
+                const float4 w4 = *reinterpret_cast<const float4 *>(sp + (ty * kPer + i) * kKeys + key);
+                w[i][0] = w4.x, w[i][1] = w4.y, w[i][2] = w4.z, w[i][3] = w4.w;
+            }
 #pragma unroll
-                    for (int q = 0; q < kQuads; ++q) {
-                        o[i][q][0] = fmaf(w, vq[q].x, o[i][q][0]);
-                        o[i][q][1] = fmaf(w, vq[q].y, o[i][q][1]);
-                        o[i][q][2] = fmaf(w, vq[q].z, o[i][q][2]);
-                        o[i][q][3] = fmaf(w, vq[q].w, o[i][q][3]);
+            for (int j = 0; j < 4; ++j) {
+                float4 vq[kQuads];
+#pragma unroll
+                for (int q = 0; q < kQuads; ++q)
+                    vq[q] = *reinterpret_cast<const float4 *>(sv + (key + j) * kDMax + 64 * q + 4 * tx);
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    if (w[i][j] != 0.0f) {  // what a row does not see never reaches it, NaN included
+#pragma unroll
+                        for (int q = 0; q < kQuads; ++q) {
+                            o[i][q][0] = fmaf(w[i][j], vq[q].x, o[i][q][0]);
+                            o[i][q][1] = fmaf(w[i][j], vq[q].y, o[i][q][1]);
+                            o[i][q][2] = fmaf(w[i][j], vq[q].z, o[i][q][2]);
+                            o[i][q][3] = fmaf(w[i][j], vq[q].w, o[i][q][3]);
+                        }
                     }
                 }
             }
