@@ -13,20 +13,31 @@
 // operands that carry more than four bits are split into E4M3 parts instead, where
 // they are small.  Q is two parts (the nearest code and that of the rest, under a
 // power of two per row): the eight bits of a bf16 value down to 2^-10 of the row's
-// largest, and 2^-18 of that below.  P is three, the rest scaled by 2^4 each time, in
-// columns of their own that the end adds up: twelve bits, and 2^-18 absolute below
-// that, where the largest P so far lies between 2^5 and 2^8.
+// largest, and 2^-18 of that below.  P is three, in columns of their own that the end
+// adds up: fp16's eleven bits, each part's rest scaled by 2^5 for the next, down to
+// 2^-20 absolute, where a row's largest P lies between 2^3 and 2^8.  A higher start
+// would keep smaller weights and move x more often (2^5: 256 us in place of 196, at the
+// 60 rows below).
 //
 // z = S 2^(key scale) 2^a scale log2(e), and a weight carries its value's scale:
 // P = 2^(z - base) 2^(value scale) 2^-x with an integer x per row.  base and x are
 // lazy: a tile is computed against the ones so far, and only where some z exceeds
-// its base by 8 or some P reaches 2^8 (the first tile, and few after it) the
-// warpgroup finds the maxima, moves them and rescales its sums.  base follows z alone, so
-// that the sum of the weights does not depend on the values.
+// its base by 8 or some P exceeds 2^8 (the first tile, and few after it) the
+// warpgroup finds the maxima, moves them, rescales its sums and takes the tile
+// again.  base follows z alone, so that the sum of the weights does not depend on
+// the values.
 //
 // Two slots of accumulators, each with a softmax warpgroup, take the key tiles in
 // turns; the end adds them.  Warps 0-3 and 4-7: slots 0 and 1; warps 8 and 10 issue their
 // MMAs; warp 9 loads the keys, warp 11 the values (one TMA box per page).
+//
+// Measured (128 per head, 8 key/value heads, pages of 32): 64 requests of one token over
+// 0 to 8191 keys, 4 rows a head: 105 us, 5.2 TB/s of the cache's bytes.  Few rows are
+// bound by the loads and by an item's start and end (about five tiles' time); many by
+// the softmax warps' issue slots: 64 requests over 3000 to 4096 keys with 15, 30 and 60
+// rows take 102, 121 and 196 us.  Its code is kept short, chunk by chunk of 16 rows:
+// unrolled over 64 rows, the warps wait for instructions (309 us for 60 rows).  A second
+// warpgroup per slot gains little there (187) and costs few rows (112 for 105).
 #include <type_traits>
 
 #include "attention_tc.cuh"
@@ -39,6 +50,7 @@ constexpr int kRowShift = 6, kRows = 1 << kRowShift;  // rows of a block
 // Units of a key tile with up to 16, 32, 48 and 64 rows, and of an item's start and end.
 constexpr int kTileUnits[4] = {10, 13, 17, 21}, kItemUnits[4] = {55, 75, 95, 115};
 constexpr int kParts = 3;       // of a weight
+constexpr float kPartScale = 32.0f;  // from one part to the next: what is left of 2^8 stays below 2^8
 constexpr float kLazy = 8.0f;   // log2 growth of a maximum that moves its base
 constexpr float kCap = 256.0f;  // the largest P
 constexpr int kTop = 3;         // binade of the largest P where x moves
@@ -597,7 +609,7 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                     }
                     float most = -INFINITY;
                     __half2 most_p = __float2half2_rn(0.0f);
-                    const __half2 up = __float2half2_rn(16.0f);
+                    const __half2 up = __float2half2_rn(kPartScale);
 #pragma unroll 1
                     for (int c = 0; c < pc.n_rows; c += 16) {
                         scores(c);
@@ -614,8 +626,8 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                                 most = fmaxf(fmaxf(most, za), zb);
                                 w2[k / 2 + e] = f2(ex2(za), ex2(zb));
                                 unf2(mul2(mul2(w2[k / 2 + e], vm2), e ? x4.y : x4.x), a, b);
-                                // fp16's eleven bits, as three parts of four: no part's
-                                // rest is rounded (P below 2^-17 apart)
+                                // fp16's eleven bits, as three parts of four: what one
+                                // leaves is exact in fp16
                                 __half2 rest = __floats2half2_rn(a, b);
                                 most_p = __hmax2(most_p, rest);
 #pragma unroll
@@ -769,7 +781,7 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                     for (int q = 0; q < kParts; ++q) tmem_tie8(a[q]);
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        o[k] = fmaf(fmaf(fmaf(__uint_as_float(a[2][k]), 0.0625f, __uint_as_float(a[1][k])), 0.0625f,
+                        o[k] = fmaf(fmaf(fmaf(__uint_as_float(a[2][k]), 1.0f / kPartScale, __uint_as_float(a[1][k])), 1.0f / kPartScale,
                                          __uint_as_float(a[0][k])),
                                     sh.fix_o[i][r0 + k], o[k]);
                 }

@@ -91,7 +91,6 @@ template <int kTiles> struct SharedE4M3 : Shared {
 };
 
 template <int kD, bool kE4M3> struct Cfg {
-    static constexpr int kHalves = kD / 64;            // 128-byte column blocks of a 16-bit tile
     static constexpr int kTileBytes = kTile * kD * 2;  // a 16-bit operand tile
     static constexpr int kRawBytes = kTile * kD;       // E4M3 codes of a tile
     // operand ring: keys and values in turn, or (E4M3) widened values alone
@@ -198,6 +197,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
               const __grid_constant__ CUtensorMap vmap) {
     using C = Cfg<kD, kE4M3>;
     constexpr int kStages = C::kStages;
+    [[maybe_unused]] constexpr int kHalves = kD / 64;  // 128-byte column blocks of a 16-bit tile
     extern __shared__ uint8_t dyn[];
     const uint32_t pad = (0u - smem_u32(dyn)) & 1023u;
     const uint32_t sm_q = smem_u32(dyn) + pad;
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                 const CUtensorMap *map = values ? &vmap : &kmap;
                 if constexpr (!kPaged) {
 #pragma unroll
-                    for (int half = 0; half < C::kHalves; ++half)
+                    for (int half = 0; half < kHalves; ++half)
                         tma_load_3d(dst + half * (kTile * 128), map, fullb, 64 * half, pc.h,
                                     pc.rq.t0 + tile * kTile);
                 } else {
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                             tma_load_3d(dst + i * rows_box * kD, map, fullb, 0, y, z);
                         } else {
 #pragma unroll
-                            for (int half = 0; half < C::kHalves; ++half)
+                            for (int half = 0; half < kHalves; ++half)
                                 tma_load_3d(dst + half * (kTile * 128) + i * rows_box * 128, map, fullb, 64 * half,
                                             y, z);
                         }
@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                     const int32_t low = min(max((kPaged ? pc.rq.ctx : pc.tok0) - first, 0), live);
                     bool found = false;
 #pragma unroll 1
-                    for (int half = 0; half < C::kHalves; ++half) {
+                    for (int half = 0; half < kHalves; ++half) {
                         const uint32_t base = sm_ring + (nv % kStages) * C::kTileBytes + half * (kTile * 128);
 #pragma unroll 1
                         for (int i = live * 8 + lane; i < kTile * 8; i += 32)
@@ -1389,7 +1389,10 @@ dflash2_status launch_tc(const DeviceInfo &di, const Params &p, bool paged, int3
     if (!paged)
         return p.head_dim == 64 ? launch_one<64, false, false>(di, p, st)
                                 : launch_one<128, false, false>(di, p, st);
-    if (kv_format == DFLASH2_KV_E4M3 && (int64_t)p.total_q * p.group <= 64 * (int64_t)p.batch)
+    // Few rows a request on average: the transposed kernel.  64 requests over 0 to 8191 keys,
+    // head_dim 128, with 4, 16, 32, 48 and 64 rows take it 106, 109, 138, 182 and 221 us, and
+    // this file's 155, 159, 165, 211 and 212.
+    if (kv_format == DFLASH2_KV_E4M3 && (int64_t)p.total_q * p.group <= 48 * (int64_t)p.batch)
         return launch_few(di, p, st);
     if (kv_format == DFLASH2_KV_E4M3)
         return p.head_dim == 64 ? launch_one<64, true, true>(di, p, st)
