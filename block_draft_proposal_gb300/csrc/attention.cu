@@ -10,12 +10,14 @@ namespace {
 
 bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-constexpr int kWorkspaceCtas = 160;  // CTAs the workspace has slots for: one per SM, 152 on GB300
+// CTAs the workspace has slots for, one per SM (152 on GB300); or twice as many with
+// slots of half of the rows (attention_few.cu), 64 of them.
+constexpr int kWorkspaceCtas = 160;
 
 // Rows of a partial slot: no row block is longer than 256 rows or than all rows.
 int32_t slot_rows(int32_t total_q, int32_t group) {
     const int64_t rows = ((int64_t)total_q * group + 15) / 16 * 16;
-    return (int32_t)(rows < 64 ? 64 : rows > 256 ? 256 : rows);
+    return (int32_t)(rows < 128 ? 128 : rows > 256 ? 256 : rows);
 }
 
 dflash2_status check_shape(int32_t batch, int32_t total_q, int32_t q_heads, int32_t kv_heads,
@@ -36,7 +38,7 @@ extern "C" size_t dflash2_tree_attention_workspace_size(int32_t total_q, int32_t
                                                         int32_t head_dim) {
     if (check_shape(batch, total_q, q_heads, kv_heads, head_dim, 1.0f, DFLASH2_BF16) != DFLASH2_OK)
         return 0;
-    return sizeof(attn::Join) * kWorkspaceCtas +
+    return sizeof(attn::Join) * 2 * kWorkspaceCtas +
            (size_t)(2 * kWorkspaceCtas *
                     attn::part_slot_floats(slot_rows(total_q, q_heads / kv_heads), head_dim)) * 4;
 }
@@ -82,7 +84,7 @@ extern "C" dflash2_status dflash2_tree_attention(
     p.kv_heads = kv_heads, p.group = q_heads / kv_heads, p.head_dim = head_dim;
     p.scale_log2 = scale * 1.4426950408889634f, p.out = out, p.lse = lse;
     p.join = static_cast<attn::Join *>(workspace);
-    p.part = reinterpret_cast<float *>(p.join + kWorkspaceCtas), p.part_rows = slot_rows(total_q, p.group), p.err = err_word;
+    p.part = reinterpret_cast<float *>(p.join + 2 * kWorkspaceCtas), p.part_rows = slot_rows(total_q, p.group), p.err = err_word;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (attn::tc_takes(p, true, dtype)) return attn::launch_tc(di, p, true, kv_format, s);
     return attn::launch_simt(di, p, true, dtype, kv_format, s);

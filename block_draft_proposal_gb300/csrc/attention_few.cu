@@ -58,15 +58,15 @@ constexpr int kTop = 3;         // binade of the largest P where x moves
 struct Shared {
     alignas(16) uint8_t piece[kPieces][kPieceBytes];
     alignas(16) float qm[kRows];       // 2^a scale log2(e) of a row
-    alignas(16) float off[2][kRows];   // by slot: -base (0: no base yet)
-    alignas(16) float xm[2][kRows];    // 2^-x
-    alignas(16) float fix_sum[2][kRows], fix_o[2][kRows];
-    float top[2][4][2][kRows];         // a warp's largest z, and z + value scale
-    float sums[2][4][kRows];           // of a tile's weights by warp, then of all
+    alignas(16) float off[kRows];      // -base (0: no base yet)
+    alignas(16) float xm[kRows];       // 2^-x
+    alignas(16) float fix_sum[kRows], fix_o[kRows];
+    float top[4][2][kRows];            // a warp's largest z, and z + value scale
+    float sums[4][kRows];              // of a tile's weights by warp, then of all
     int32_t pages[2][2][kTile / 16 * 8 + 1];  // page numbers of eight key tiles, twice, by producer
     uint64_t piece_full[kPieces], piece_empty[kPieces];
-    uint64_t raw_full[2][8], raw_empty[2][8];  // codes of keys, values
-    uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], q_full, drain[2];
+    uint64_t raw_full[2][4], raw_empty[2][4];  // codes of keys, values
+    uint64_t s_full, s_free, p_full, pv_done, q_full, drain;
     uint32_t tmem;
     int abort_flag;
     int stop[2];  // no more pieces, by piece parity
@@ -76,13 +76,13 @@ struct Shared {
 
 template <int kD> struct Few {
     static constexpr int kRawBytes = kTile * kD;           // codes of a tile
-    static constexpr int kStages = kD == 128 ? 4 : 8;      // tiles of keys, and of values
+    static constexpr int kStages = kD == 128 ? 2 : 4;      // tiles of keys, and of values
     static constexpr int kQBytes = 2 * kRows * kD;         // both parts
-    static constexpr int kPBytes = 2 * kTile * 128;        // [column blocks of 128][key][column]
-    static constexpr int kThreads = 384;
-    static constexpr int kRegsMany = 216, kRegsFew = 72;   // 168 each at launch
-    static constexpr int kSmem = kQBytes + 2 * kPBytes + 2 * kStages * kRawBytes + (int)sizeof(Shared) + 1024;
-    static_assert(kSmem <= 227 * 1024, "shared memory");
+    static constexpr int kPBytes = kParts * kTile * 64;    // [column blocks of 64][key][column]
+    static constexpr int kThreads = 256;
+    static constexpr int kRegsMany = 184, kRegsFew = 72;   // 128 each at launch
+    static constexpr int kSmem = kQBytes + kPBytes + 2 * kStages * kRawBytes + (int)sizeof(Shared) + 1024;
+    static_assert(kSmem <= 113 * 1024, "shared memory of two CTAs");
 };
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -90,25 +90,23 @@ __device__ __forceinline__ float warp_max(float v) {
     asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
     return r;
 }
-// Does any thread of warpgroup s say so?  (a barrier of its 128 threads)
-__device__ __forceinline__ bool group_any(int s, bool v) {
+// Does any softmax thread say so?  (a barrier of them)
+__device__ __forceinline__ bool group_any(bool v) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.aligned.pred q, %2, 128, p;\n\t"
+        "barrier.cta.red.or.aligned.pred q, 2, 128, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)v), "r"(2 + s)
+        : "r"((uint32_t)v)
         : "memory");
     return r != 0;
 }
-__device__ __forceinline__ void group_sync(int s) {
-    asm volatile("bar.sync %0, 128;" ::"r"(2 + s) : "memory");
-}
+__device__ __forceinline__ void group_sync() { named_sync<1, 128>(); }
 
 template <int kD>
-__global__ void __launch_bounds__(Few<kD>::kThreads, 1)
+__global__ void __launch_bounds__(Few<kD>::kThreads, 2)
     few_kernel(const Params p, const __grid_constant__ CUtensorMap kmap,
                const __grid_constant__ CUtensorMap vmap) {
     using C = Few<kD>;
@@ -117,8 +115,8 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
     const uint32_t pad = (0u - smem_u32(dyn)) & 1023u;
     const uint32_t sm_q = smem_u32(dyn) + pad;
     const uint32_t sm_p = sm_q + C::kQBytes;
-    const uint32_t sm_raw[2] = {sm_p + 2 * C::kPBytes, sm_p + 2 * C::kPBytes + kStages * C::kRawBytes};
-    Shared &sh = *reinterpret_cast<Shared *>(dyn + pad + C::kQBytes + 2 * C::kPBytes + 2 * kStages * C::kRawBytes);
+    const uint32_t sm_raw[2] = {sm_p + C::kPBytes, sm_p + C::kPBytes + kStages * C::kRawBytes};
+    Shared &sh = *reinterpret_cast<Shared *>(dyn + pad + C::kQBytes + C::kPBytes + 2 * kStages * C::kRawBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -129,26 +127,24 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
             }
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(&sh.piece_full[i], 1);
-            mbar_init(&sh.piece_empty[i], 11);  // all but the producer
+            mbar_init(&sh.piece_empty[i], 6);  // all but the producer
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.s_free[i], 4);
-            mbar_init(&sh.p_full[i], 4);
-            mbar_init(&sh.pv_done[i], 1);
-            mbar_init(&sh.drain[i], 1);
-        }
-        mbar_init(&sh.q_full, 8);
+        mbar_init(&sh.s_full, 1);
+        mbar_init(&sh.s_free, 4);
+        mbar_init(&sh.p_full, 4);
+        mbar_init(&sh.pv_done, 1);
+        mbar_init(&sh.drain, 1);
+        mbar_init(&sh.q_full, 4);
         sh.abort_flag = 0;
         sh.stop[0] = sh.stop[1] = 0;
         sh.poison = -1;
         fence_mbar_init();
     }
-    if (warp == 8) {
-        tmem_alloc(&sh.tmem, 512);
+    if (warp == 4) {
+        tmem_alloc(&sh.tmem, 256);
         tmem_relinquish();
     }
-    if (warp == 9 && lane == 0) {
+    if (warp == 5 && lane == 0) {
         prefetch_tmap(&kmap);
         prefetch_tmap(&vmap);
     }
@@ -161,7 +157,8 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // the CTA holds all 512 TMEM columns: S^T of slot s at 64 s, O^T at 128 + 192 s
+    // two CTAs share the SM's TMEM, 256 columns each: S^T, then O^T
+    const uint32_t tmem = sh.tmem;
     volatile int *abort_flag = &sh.abort_flag;
     // Piece number i of the ring, for every role but the producer's; all lanes of a
     // warp (`whole`) or one thread.  Returns false at the end or on an abort.
@@ -173,11 +170,11 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
         return pc->n_rows > 0;
     };
 
-    if (warp >= 8) {
+    if (warp >= 4) {
         regs_give<C::kRegsFew>();
-        if (warp == 9 || warp == 11) {
-            // ---- producers: warp 9 the pieces and the keys, warp 11 the values ----
-            const int of = warp == 9 ? 0 : 1;
+        if (warp == 5 || warp == 6) {
+            // ---- producers: warp 5 the pieces and the keys, warp 6 the values ----
+            const int of = warp - 5;
             uint32_t issued = 0, n_piece = 0;
             bool ok = true, bad_page = false;
             const int32_t rows_box = min(p.page_size, kTile);
@@ -282,10 +279,9 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                         if (global_timer_ns() - t0 > kWaitLimitNs) break;
                 }
             }
-        } else if (elect_one()) {
-            // ---- MMA issuer of slot s: one thread ----
-            const int s = warp == 8 ? 0 : 1;
-            const uint32_t dS = s * kRows, dO = 128 + s * (kParts * kRows);
+        } else if (warp == 4 && elect_one()) {
+            // ---- MMA issuer: one thread ----
+            const uint32_t dS = tmem, dO = tmem + kRows;
             uint32_t tiles_done = 0, n_piece = 0, n_s = 0, n_p = 0;
             bool ok = true;
             Piece pc{};
@@ -299,11 +295,10 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                 const int32_t n = pc.t1 - pc.t0, cols = (pc.n_rows + 15) & ~15;
                 const uint32_t id_s = idesc_e4m3(128, cols);
                 const uint32_t id_o = idesc_e4m3(128, kParts * cols) | (1u << 15) | (1u << 16);  // both MN-major
-                const bool two_p = pc.n_rows <= kRows / 2;
                 auto scores = [&](int32_t j) {
                     const uint32_t kt = tiles_done + j, i = kt % kStages;
                     if (!bar_wait(&sh.raw_full[0][i], (kt / kStages) & 1u, abort_flag, p.err) ||
-                        !bar_wait(&sh.s_free[s], (n_s & 1u) ^ 1u, abort_flag, p.err))
+                        !bar_wait(&sh.s_free, (n_s & 1u) ^ 1u, abort_flag, p.err))
                         return false;
                     ++n_s;
                     tc_fence_after();
@@ -315,54 +310,52 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                         tc_mma_f8(dS, desc64(kd + at, kCodesHi<kD>), desc64(qd + part + at, kCodesHi<kD>), id_s,
                                   k > 0);
                     }
-                    tc_commit(&sh.s_full[s]);
+                    tc_commit(&sh.s_full);
                     tc_commit(&sh.raw_empty[0][i]);
                     return true;
                 };
-                if (ok && s < n) ok = scores(s);
+                if (ok) ok = scores(0);
 #pragma unroll 1
-                for (int32_t j = s; ok && j < n; j += 2) {
-                    if (j + 2 < n) ok = scores(j + 2);
+                for (int32_t j = 0; ok && j < n; ++j) {
+                    if (j + 1 < n) ok = scores(j + 1);
                     const uint32_t kt = tiles_done + j, i = kt % kStages;
                     ok = ok && bar_wait(&sh.raw_full[1][i], (kt / kStages) & 1u, abort_flag, p.err) &&
-                         bar_wait(&sh.p_full[s], n_p & 1u, abort_flag, p.err);
+                         bar_wait(&sh.p_full, n_p & 1u, abort_flag, p.err);
                     if (!ok) break;
                     ++n_p;
                     tc_fence_after();
                     const uint32_t vd = desc_lo(sm_raw[1] + i * C::kRawBytes);
-                    const uint32_t pd = desc_lo(sm_p + s * C::kPBytes + (two_p ? ((j >> 1) & 1) * (kTile * 128) : 0)) | kMnMajorLo;
+                    const uint32_t pd = desc_lo(sm_p) | (uint32_t)((kTile * 64) >> 4) << 16;
 #pragma unroll
                     for (int k = 0; k < kTile / 32; ++k)
-                        tc_mma_f8(dO, desc64(vd + k * (32 * kD >> 4), kVHi), desc64(pd + k * (32 * 128 >> 4), kMnMajorHi),
-                                  id_o, j > s || k > 0);
+                        tc_mma_f8(dO, desc64(vd + k * (32 * kD >> 4), kVHi), desc64(pd + k * (32 * 64 >> 4), kCodesHi<64>), id_o,
+                                  j > 0 || k > 0);
                     tc_commit(&sh.raw_empty[1][i]);
-                    tc_commit(&sh.pv_done[s]);
+                    tc_commit(&sh.pv_done);
                 }
                 tiles_done += n;
             }
-            // nothing of this slot's is in flight when the accumulators are freed
-            tc_commit(&sh.drain[s]);
+            // nothing is in flight when the accumulators are freed
+            tc_commit(&sh.drain);
             const uint64_t t0 = global_timer_ns();
-            while (!mbar_try_wait(&sh.drain[s], 0))
+            while (!mbar_try_wait(&sh.drain, 0))
                 if (global_timer_ns() - t0 > kWaitLimitNs) break;
         }
     } else {
-        // ---- softmax of slot s, with the loads of Q and the epilogue ----
+        // ---- softmax, with the loads of Q and the epilogue ----
         regs_take<C::kRegsMany>();
-        const int s = warp >> 2, wq = warp & 3;
-        const int my = wq * 32 + lane;  // key of a tile, channel of the sums
-        const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
-        const uint32_t tS = s * kRows + lane_base;
-        const uint32_t tO = 128 + s * (kParts * kRows) + lane_base;
+        const int my = threadIdx.x;  // key of a tile, channel of the sums
+        const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+        const uint32_t tS = tmem + lane_base, tO = tS + kRows;
+        const uint32_t my_p = sm_p + my * 64;
         const uint32_t magic = (65536u + p.group - 1) / (uint32_t)p.group;  // x / group for x < 512
         const int32_t page_shift = 31 - __clz(p.page_size);
-        uint32_t n_piece = 0, n_s = 0, tiles_done = 0;
-        uint32_t n_pv[2] = {0, 0};  // sums complete, by slot
+        uint32_t n_piece = 0, n_tile = 0, tiles_done = 0;
         Piece pc{};
         int32_t page = -1;
         int ke = 127, ve = 127;
-        // Exponent bytes: this thread's key of the slot's next tile, and its page of the one
-        // after that, so that neither load is waited for.
+        // Exponent bytes: this thread's key of the next tile, and its page of the one after
+        // that, so that neither load is waited for.
         auto fetch_page = [&](int32_t tile) {
             const int32_t l = tile * kTile + my;
             page = -1;
@@ -381,12 +374,12 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
         // (no wait's failure leaves the loop: the barriers below want all warps)
         for (;;) {
             if (!take_piece(n_piece, &pc, true)) sh.stop[n_piece & 1u] = 1;
-            named_sync<1, 256>();
+            group_sync();
             if (*(volatile int *)&sh.stop[n_piece & 1u]) break;
-            fetch_page(pc.t0 + s);
+            fetch_page(pc.t0);
             // queries: kD / 8 lanes hold a row, 8 values each
             {
-                constexpr int kLanes = kD / 8, kStep = 256 / kLanes, kEach = kRows / kStep;
+                constexpr int kLanes = kD / 8, kStep = 128 / kLanes, kEach = kRows / kStep;
                 const uint32_t row_lanes = ((1u << kLanes) - 1u) << (lane & ~(kLanes - 1));
                 const int l8 = threadIdx.x % kLanes;
                 const __nv_bfloat16 *q0 = (const __nv_bfloat16 *)p.q + (int64_t)(pc.rq.t0 + pc.tok0) * p.q_stride +
@@ -401,12 +394,11 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                         v[i] = __ldg(reinterpret_cast<const uint4 *>(q0 + (int64_t)dt * p.q_stride +
                                                                      (int)(x - dt * p.group) * kD));
                 }
-                fetch_exps(pc.t0 + s);
-                fetch_page(pc.t0 + s + 2);
-                if (threadIdx.x < 2 * kRows) {
-                    const int c = threadIdx.x & (kRows - 1), of = threadIdx.x / kRows;
-                    sh.off[of][c] = 0.0f;
-                    sh.xm[of][c] = c < pc.n_rows ? 1.0f : 0.0f;
+                fetch_exps(pc.t0);
+                fetch_page(pc.t0 + 1);
+                if (my < kRows) {
+                    sh.off[my] = 0.0f;
+                    sh.xm[my] = my < pc.n_rows ? 1.0f : 0.0f;
                 }
 #pragma unroll
                 for (int i = 0; i < kEach; ++i) {
@@ -453,26 +445,24 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                 }
                 fence_proxy_async_smem();
                 // all threads: the rows' factors are there, and the last piece's sums are read
-                named_sync<1, 256>();
+                group_sync();
                 if (lane == 0) mbar_arrive(&sh.q_full);
             }
             const int n_chunk = (pc.n_rows + 15) >> 4;  // of 16 rows
-            // up to 32 rows' weights are one block of columns: two of them in turns
-            const bool two_p = pc.n_rows <= kRows / 2;
             float sum[2] = {0.0f, 0.0f};  // this warp's keys: rows 2 lane and the next
-            bool late = false;            // some row may have no base after the slot's first tile
+            bool late = false;            // some row may have no base after the first tile
             // row `my`: its base (-inf: none yet), largest z + value scale at the last move, x
             float row_base = -INFINITY, row_top = -INFINITY, row_x = 0.0f;
 
-            for (int32_t t = pc.t0 + s; t < pc.t1; t += 2) {
-                const bool first = t == pc.t0 + s;
+            for (int32_t t = pc.t0; t < pc.t1; ++t, ++n_tile) {
+                const bool first = t == pc.t0;
                 const int32_t l = t * kTile + my;
                 // written exponents lie in [-48, 48]; what was never written is masked
                 const float km = pow2_int(min(max(ke - 127, -48), 48));
                 const int v_exp = min(max(ve - 127, -48), 48);
                 const float vm = pow2_int(v_exp), vf = (float)v_exp;
-                fetch_exps(t + 2);
-                fetch_page(t + 4);
+                fetch_exps(t + 1);
+                fetch_page(t + 2);
                 const bool masked = (t + 1) * kTile > pc.rq.ctx;
                 if (first) late = masked;
                 // the rows that see this key: bit r; all of a token's rows do, or none
@@ -484,7 +474,7 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                     for (int i0 = 0; i0 < n_tok; i0 += 32) {  // a lane loads a token's bits of this warp's keys
                         uint32_t bits = 0;
                         if (i0 + lane < n_tok)
-                            bits = seen_bits<true>(p, pc.rq, pc.tok0 + i0 + lane, t * kTile + wq * 32);
+                            bits = seen_bits<true>(p, pc.rq, pc.tok0 + i0 + lane, t * kTile + warp * 32);
                         const int n_here = min(n_tok - i0, 32);
 #pragma unroll 1
                         for (int i = 0; i < n_here; ++i) {
@@ -495,13 +485,9 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                         }
                     }
                 }
-                bar_wait(&sh.s_full[s], n_s & 1u, abort_flag, p.err);
-                ++n_s;
+                bar_wait(&sh.s_full, n_tile & 1u, abort_flag, p.err);
                 tc_fence_after();
                 const uint64_t km2 = f2(km, km), vm2 = f2(vm, vm);
-                const uint32_t my_p = sm_p + s * C::kPBytes + my * 128 +
-                                      (two_p ? (((t - pc.t0) >> 1) & 1) * (kTile * 128) : 0);
-                bool pv_waited = first;
                 uint32_t x[16];
                 // z of the 16 rows from c on, against the slot's bases
                 auto scores = [&](int c) {
@@ -511,7 +497,7 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
 #pragma unroll
                     for (int k = 0; k < 16; k += 4) {
                         const ulonglong2 q4 = *reinterpret_cast<const ulonglong2 *>(&sh.qm[c + k]);
-                        const ulonglong2 o4 = *reinterpret_cast<const ulonglong2 *>(&sh.off[s][c + k]);
+                        const ulonglong2 o4 = *reinterpret_cast<const ulonglong2 *>(&sh.off[c + k]);
                         float a, b;
                         unf2(fma2(mul2(f2(x[k], x[k + 1]), km2), q4.x, o4.x), a, b);
                         x[k] = __float_as_uint(a), x[k + 1] = __float_as_uint(b);
@@ -526,7 +512,7 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                     }
                 };
                 // Weights against the bases and x so far; again where those had to move.  They
-                // move first in a slot's first tile, and in masked ones where a row may see
+                // move first in an item's first tile, and in masked ones where a row may see
                 // its first key.
 #pragma unroll 1
                 for (bool move = first || (masked && late), again = false;; move = again = true) {
@@ -546,18 +532,18 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                                 if (!((seen >> (c + k)) & 1u)) z = -INFINITY;
                                 const float top = warp_max(z), top_v = warp_max(z + vf);
                                 if (lane == 0) {
-                                    sh.top[s][wq][0][c + k] = top;
-                                    sh.top[s][wq][1][c + k] = top_v;
+                                    sh.top[warp][0][c + k] = top;
+                                    sh.top[warp][1][c + k] = top_v;
                                 }
                             }
                         }
-                        group_sync(s);
+                        group_sync();
                         if (my < pc.n_rows) {
                             float top = -INFINITY, fix = 1.0f, fix_o = 1.0f;
 #pragma unroll
                             for (int w = 0; w < 4; ++w) {
-                                top = fmaxf(top, sh.top[s][w][0][my]);
-                                row_top = fmaxf(row_top, sh.top[s][w][1][my]);
+                                top = fmaxf(top, sh.top[w][0][my]);
+                                row_top = fmaxf(row_top, sh.top[w][1][my]);
                             }
                             const bool had = row_base > -INFINITY;
                             if (top > row_base + kLazy) {
@@ -569,20 +555,18 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                                 const float nx = floorf(fminf(fmaxf(row_top - row_base, -100.0f), 100.0f)) - kTop;
                                 if (had) fix_o *= ex2(row_x - nx);
                                 row_x = nx;
-                                sh.off[s][my] = -row_base;
-                                sh.xm[s][my] = pow2_int(-(int)nx);
+                                sh.off[my] = -row_base;
+                                sh.xm[my] = pow2_int(-(int)nx);
                             }
-                            sh.fix_sum[s][my] = fix;
-                            sh.fix_o[s][my] = fix_o;
+                            sh.fix_sum[my] = fix;
+                            sh.fix_o[my] = fix_o;
                         }
-                        group_sync(s);
+                        group_sync();
                         if (!first) {
-                            if (2 * lane < pc.n_rows) sum[0] *= sh.fix_sum[s][2 * lane];
-                            if (2 * lane + 1 < pc.n_rows) sum[1] *= sh.fix_sum[s][2 * lane + 1];
-                            if (!pv_waited) {  // the products so far, all of them there
-                                bar_wait(&sh.pv_done[s], (n_pv[s] - 1u) & 1u, abort_flag, p.err);
-                                pv_waited = true;
-                            }
+                            if (2 * lane < pc.n_rows) sum[0] *= sh.fix_sum[2 * lane];
+                            if (2 * lane + 1 < pc.n_rows) sum[1] *= sh.fix_sum[2 * lane + 1];
+                            // the products so far, all of them there
+                            if (!again) bar_wait(&sh.pv_done, (n_tile - 1u) & 1u, abort_flag, p.err);
                             tc_fence_after();
 #pragma unroll 1
                             for (int i = 0; i < kParts * n_chunk; ++i) {
@@ -590,7 +574,7 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                                 tmem_ld16(tO + 16 * i, o);
                                 tmem_ld_wait();
                                 tmem_tie16(o);
-                                const float4 *f4 = reinterpret_cast<const float4 *>(sh.fix_o[s] + i / kParts * 16);
+                                const float4 *f4 = reinterpret_cast<const float4 *>(sh.fix_o + i / kParts * 16);
 #pragma unroll
                                 for (int k = 0; k < 4; ++k) {
                                     const float4 f = f4[k];
@@ -603,9 +587,8 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                             }
                             tmem_st_wait();
                         }
-                    } else if (!two_p) {  // the last weights are read
-                        bar_wait(&sh.pv_done[s], (n_pv[s] - 1u) & 1u, abort_flag, p.err);
-                        pv_waited = true;
+                    } else {  // the last weights are read
+                        bar_wait(&sh.pv_done, (n_tile - 1u) & 1u, abort_flag, p.err);
                     }
                     float most = -INFINITY;
                     __half2 most_p = __float2half2_rn(0.0f);
@@ -617,7 +600,7 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                         uint64_t w2[8];
 #pragma unroll
                         for (int k = 0; k < 16; k += 4) {
-                            const ulonglong2 x4 = *reinterpret_cast<const ulonglong2 *>(&sh.xm[s][c + k]);
+                            const ulonglong2 x4 = *reinterpret_cast<const ulonglong2 *>(&sh.xm[c + k]);
                             uint32_t half[kParts][2];
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
@@ -647,7 +630,7 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                         for (int part = 0; part < kParts; ++part) {
                             const int at = kParts * (c >> 4) + part;  // block of 16 columns
                             asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                             my_p + (at >> 3) * (kTile * 128) + (((at & 7) ^ (my & 7)) << 4)),
+                                             my_p + (at >> 2) * (kTile * 64) + (((at & 3) ^ ((my >> 1) & 3)) << 4)),
                                          "r"(pk[part][0]), "r"(pk[part][1]), "r"(pk[part][2]), "r"(pk[part][3])
                                          : "memory");
                         }
@@ -665,21 +648,18 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                             }
                         }
                         w[0] += __shfl_xor_sync(0xFFFFFFFFu, w[0], 1);
-                        if (!(lane & 1)) sh.sums[s][wq][c + (lane >> 1)] = w[0];
+                        if (!(lane & 1)) sh.sums[warp][c + (lane >> 1)] = w[0];
                     }
                     if (again ||
-                        !group_any(s, most > kLazy || fmaxf(__low2float(most_p), __high2float(most_p)) > kCap))
+                        !group_any(most > kLazy || fmaxf(__low2float(most_p), __high2float(most_p)) > kCap))
                         break;
                 }
                 // the scores are read: the next tile's may come
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.s_free[s]);
-                // the products of the slot's last tile, whose weights' place the next one takes
-                if (!pv_waited) bar_wait(&sh.pv_done[s], (n_pv[s] - 1u) & 1u, abort_flag, p.err);
-                ++n_pv[s];
-                sum[0] += sh.sums[s][wq][2 * lane];  // (of rows that are not there: unused)
-                sum[1] += sh.sums[s][wq][2 * lane + 1];
+                if (lane == 0) mbar_arrive(&sh.s_free);
+                sum[0] += sh.sums[warp][2 * lane];  // (of rows that are not there: unused)
+                sum[1] += sh.sums[warp][2 * lane + 1];
                 // What a row does not see must not reach it, but a product 0 * NaN would: the
                 // values past the end, and NaN codes where some row may be masked, become
                 // zero; the epilogue adds the NaN to the rows that do see it.
@@ -712,79 +692,50 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.p_full[s]);
+                if (lane == 0) mbar_arrive(&sh.p_full);
             }
             // ---- epilogue ----
             const int32_t n = pc.t1 - pc.t0;
             tiles_done += n;
-            const bool used1 = n > 1;
-            n_pv[s ^ 1] += (uint32_t)((n + s) >> 1);  // slot 0 has (n + 1) / 2 tiles, slot 1 n / 2
             __syncwarp();
-            sh.sums[s][wq][2 * lane] = sum[0];
-            sh.sums[s][wq][2 * lane + 1] = sum[1];
-            if (my < pc.n_rows) sh.top[s][0][0][my] = row_base, sh.top[s][0][1][my] = row_x;
-            if (s == 0 || used1) {
-                bar_wait(&sh.pv_done[s], (n_pv[s] - 1u) & 1u, abort_flag, p.err);
-            }
-            named_sync<1, 256>();
-            // both slots' last sums are complete: these waits return at once
-            if (s == 0 ? used1 : true) {
-                bar_wait(&sh.pv_done[s ^ 1], (n_pv[s ^ 1] - 1u) & 1u, abort_flag, p.err);
-            }
+            sh.sums[warp][2 * lane] = sum[0];
+            sh.sums[warp][2 * lane + 1] = sum[1];
+            bar_wait(&sh.pv_done, (n_tile - 1u) & 1u, abort_flag, p.err);
+            group_sync();
             tc_fence_after();
             float *part = pc.slot >= 0 ? p.part + pc.slot * part_slot_floats(p.part_rows, kD) : nullptr;
             auto out_row = [&](int r) {
                 const uint32_t x = pc.rem0 + r, dt = (x * magic) >> 16;
                 return (int64_t)(pc.rq.t0 + pc.tok0 + (int)dt) * p.q_heads + pc.h * p.group + (int)(x - dt * p.group);
             };
-            if ((int)threadIdx.x < pc.n_rows) {  // a row's statistics, and its factors for the two sums
-                const int r = threadIdx.x;
-                float b[2], l[2], top = -INFINITY, all = 0.0f;
+            if (my < pc.n_rows) {  // a row's statistics, and the factor of its sums
+                float all = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const bool used = i == 0 || used1;
-                    b[i] = used ? sh.top[i][0][0][r] : -INFINITY;
-                    l[i] = 0.0f;
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) l[i] += used ? sh.sums[i][w][r] : 0.0f;
-                    top = fmaxf(top, b[i]);
-                }
-                const float safe = top == -INFINITY ? 0.0f : top;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) all = fmaf(l[i], ex2(b[i] - safe), all);
-                const float inv = part ? 1.0f : all == 0.0f ? 0.0f : 1.0f / all;
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    sh.fix_o[i][r] = ex2(b[i] - safe) * pow2_int((int)sh.top[i][0][1][r]) * inv;
+                for (int w = 0; w < 4; ++w) all += sh.sums[w][my];
+                sh.fix_o[my] = pow2_int((int)row_x) * (part ? 1.0f : all == 0.0f ? 0.0f : 1.0f / all);
                 if (part) {
-                    part[part_stats(p.part_rows, kD) + r] = top;
-                    part[part_stats(p.part_rows, kD) + p.part_rows + r] = all;
+                    part[part_stats(p.part_rows, kD) + my] = row_base;
+                    part[part_stats(p.part_rows, kD) + p.part_rows + my] = all;
                 } else if (p.lse) {
-                    p.lse[out_row(r)] = all == 0.0f ? -INFINITY : (top + log2f(all)) * 0.6931471805599453f;
+                    p.lse[out_row(my)] = all == 0.0f ? -INFINITY : (row_base + log2f(all)) * 0.6931471805599453f;
                 }
             }
-            named_sync<1, 256>();
-            // eight rows at a time, by the warpgroups in turns; this thread has channel `my`
-            const uint32_t tO0 = 128 + lane_base;
+            group_sync();
+            // eight rows at a time; this thread has channel `my`
 #pragma unroll 1
-            for (int r0 = 8 * s; r0 < pc.n_rows; r0 += 16) {
-                float o[8] = {};
+            for (int r0 = 0; r0 < pc.n_rows; r0 += 8) {
+                float o[8];
+                uint32_t a[kParts][8];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (i == 1 && !used1) break;
-                    uint32_t a[kParts][8];
+                for (int q = 0; q < kParts; ++q)
+                    tmem_ld8(tO + (r0 >> 4) * (16 * kParts) + 16 * q + (r0 & 15), a[q]);
+                tmem_ld_wait();
 #pragma unroll
-                    for (int q = 0; q < kParts; ++q)
-                        tmem_ld8(tO0 + i * (kParts * kRows) + (r0 >> 4) * (16 * kParts) + 16 * q + (r0 & 15), a[q]);
-                    tmem_ld_wait();
+                for (int q = 0; q < kParts; ++q) tmem_tie8(a[q]);
 #pragma unroll
-                    for (int q = 0; q < kParts; ++q) tmem_tie8(a[q]);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        o[k] = fmaf(fmaf(fmaf(__uint_as_float(a[2][k]), 1.0f / kPartScale, __uint_as_float(a[1][k])), 1.0f / kPartScale,
-                                         __uint_as_float(a[0][k])),
-                                    sh.fix_o[i][r0 + k], o[k]);
-                }
+                for (int k = 0; k < 8; ++k)
+                    o[k] = fmaf(fmaf(__uint_as_float(a[2][k]), 1.0f / kPartScale, __uint_as_float(a[1][k])),
+                                1.0f / kPartScale, __uint_as_float(a[0][k])) * sh.fix_o[r0 + k];
                 if (kD == 64 && my >= kD) continue;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
@@ -797,9 +748,9 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
             }
             if (*(volatile int *)&sh.poison == (int)n_piece) {
                 __threadfence_block();
-                named_sync<1, 256>();
-                if ((int)threadIdx.x < pc.n_rows) {
-                    const int r = threadIdx.x;
+                group_sync();
+                if (my < pc.n_rows) {
+                    const int r = my;
                     add_poison<kD, true, true>(p, pc.rq, pc.b, pc.h, pc.tok0 + (int)(((pc.rem0 + r) * magic) >> 16),
                                                max(pc.t0, pc.guard_from) * kTile, min(pc.t1 * kTile, pc.rq.len), 0, kD,
                                                part ? part + 4 * r : nullptr,
@@ -814,9 +765,9 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 1)
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == 4) {
         tc_fence_after();
-        tmem_dealloc(0, 512);
+        tmem_dealloc(tmem, 256);
     }
 }
 
@@ -841,7 +792,8 @@ template <int kD> dflash2_status launch_one(const DeviceInfo &di, Params p, cuda
         p.item_units[i] = kItemUnits[i];
         if (i == 0 || rows > kRows / 4 * i) p.most_units = kTileUnits[i];
     }
-    p.n_cta = di.sm_count;
+    p.n_cta = 2 * di.sm_count;
+    p.part_rows = kRows;
     launch_k(fn, dim3((unsigned)p.n_cta), dim3(C::kThreads), C::kSmem, st, p, maps[0], maps[1]);
     const dflash2_status s = launch_status();
     if (s != DFLASH2_OK) return s;

@@ -639,7 +639,8 @@ dflash2_status dflash2_kv_cache_read(const void *k_cache, const void *v_cache,
  *
  * A row that sees no key gives zeros and lse -inf.  What a row does not see
  * (masked nodes, the rest of a page, other pages) does not reach it, whatever
- * it holds, NaN included; a seen key of weight zero adds nothing.
+ * it holds, NaN included.  A seen value that is not finite makes the row's
+ * column so; where its key's weight underflows to zero it may be left out.
  *
  * q          device, rows [q_heads, head_dim] of token i at q + i * q_row_stride
  *            elements; tokens of all requests packed in order.
@@ -655,11 +656,15 @@ dflash2_status dflash2_kv_cache_read(const void *k_cache, const void *v_cache,
  *            rows whose keys are split over CTAs.  Contents need no clearing.
  * Arithmetic: products, softmax statistics and sums in fp32 (exponentials by
  *   PTX ex2.approx.ftz.f32).  bf16 with head_dim 64 or 128, page_size a power
- *   of two >= 16 and 16-byte aligned rows: tcgen05 MMAs with the weights p
- *   rounded to bf16 (native cache) or fp16 (E4M3 cache, whose codes are exact in fp16 and
- *   whose queries are scaled by a power of two per row) before p * v; otherwise
- *   fp32 on CUDA cores.  Reduction orders are fixed, so results are
- *   deterministic.
+ *   of two >= 16, scale > 0 (a normal float) and 16-byte aligned rows: tcgen05
+ *   MMAs.  Native cache: weights p rounded to bf16 before p * v.  E4M3 cache:
+ *   scores of the key codes with the queries as two E4M3 parts each (eight bits
+ *   down to 2^-10 of the row's largest value), weights times their value's
+ *   scale rounded to fp16's eleven bits, under a power of two per row (requests
+ *   of 48 rows q_heads / kv_heads * T or fewer on average: as three E4M3 parts
+ *   with the value codes, down to 2^-23 of the row's largest; more: with the
+ *   codes widened to fp16).  Otherwise fp32 on CUDA cores.  Reduction orders
+ *   are fixed, so results are deterministic.
  * Errors:    q_heads not a multiple of kv_heads, q_heads / kv_heads > 128,
  *            head_dim outside [1, 256], a size < 1 (batch, total_q: < 0),
  *            num_pages * kv_heads >= 2^31, max_pages * page_size >= 2^31,
@@ -699,9 +704,10 @@ dflash2_status dflash2_tree_attention(const void *q, int64_t q_row_stride, const
  *            dflash2_prompt_attention_workspace_size(...).  Contents need no clearing.
  * Errors:    as for dflash2_tree_attention; a row stride below heads *
  *            head_dim -> INVALID_ARG.  The tcgen05 path wants bf16, head_dim
- *            64 or 128 and 16-byte aligned rows.
+ *            64 or 128, scale > 0 and 16-byte aligned rows.
  * Device:    a cu_q that falls or leaves [0, total_q] is clamped and sets
- *            DFLASH2_DEVERR_ID_RANGE; rows of tokens in no request are not written.
+ *            DFLASH2_DEVERR_ID_RANGE; rows of tokens in no request are not
+ *            written, and those that clamping puts in two hold either's result.
  */
 size_t dflash2_prompt_attention_workspace_size(int32_t total_q, int32_t batch, int32_t q_heads,
                                                int32_t kv_heads, int32_t head_dim);
