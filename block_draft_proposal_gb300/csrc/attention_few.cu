@@ -16,28 +16,29 @@
 // largest, and 2^-18 of that below.  P is three, in columns of their own that the end
 // adds up: fp16's eleven bits, each part's rest scaled by 2^5 for the next, down to
 // 2^-20 absolute, where a row's largest P lies between 2^3 and 2^8.  A higher start
-// would keep smaller weights and move x more often (2^5: 256 us in place of 196, at the
+// would keep smaller weights and move x more often (2^5: 234 us in place of 181, at the
 // 60 rows below).
 //
 // z = S 2^(key scale) 2^a scale log2(e), and a weight carries its value's scale:
 // P = 2^(z - base) 2^(value scale) 2^-x with an integer x per row.  base and x are
 // lazy: a tile is computed against the ones so far, and only where some z exceeds
-// its base by 8 or some P exceeds 2^8 (the first tile, and few after it) the
-// warpgroup finds the maxima, moves them, rescales its sums and takes the tile
-// again.  base follows z alone, so that the sum of the weights does not depend on
-// the values.
+// its base by 8 or some P exceeds 2^8 (the first tile, and few after it) the CTA finds
+// the maxima, moves them, rescales its sums and takes the tile again.  base follows z
+// alone, so that the sum of the weights does not depend on the values.
 //
-// Two slots of accumulators, each with a softmax warpgroup, take the key tiles in
-// turns; the end adds them.  Warps 0-3 and 4-7: slots 0 and 1; warps 8 and 10 issue their
-// MMAs; warp 9 loads the keys, warp 11 the values (one TMA box per page).
+// Two CTAs share an SM, so that one's softmax runs beside the other's waits, an item's
+// start and end among them (one CTA per SM with two accumulators that take the key tiles
+// in turns: 105 and 189 us for the 101 and 171 below).  Warps 0-3 softmax, the loads of
+// Q and the epilogue; warp 4 issues the MMAs; warp 5 loads the keys, warp 6 the values
+// (one TMA box per page).
 //
-// Measured (128 per head, 8 key/value heads, pages of 32): 64 requests of one token over
-// 0 to 8191 keys, 4 rows a head: 105 us, 5.2 TB/s of the cache's bytes.  Few rows are
-// bound by the loads and by an item's start and end (about five tiles' time); many by
-// the softmax warps' issue slots: 64 requests over 3000 to 4096 keys with 15, 30 and 60
-// rows take 102, 121 and 196 us.  Its code is kept short, chunk by chunk of 16 rows:
-// unrolled over 64 rows, the warps wait for instructions (309 us for 60 rows).  A second
-// warpgroup per slot gains little there (187) and costs few rows (112 for 105).
+// Measured (128 per head, 8 key/value heads): 64 requests of one token over 0 to 8191
+// keys, 4 rows a head, take 101 us, 5.4 TB/s of the cache's bytes; 128 requests of trees of
+// up to 12 tokens over 13 to 4096 keys, 5 to 60 rows, 171 us.  Few rows are bound by the
+// loads and by an item's start and end (four to five tiles' time); many by the softmax
+// warps' issue slots: 64 requests over 3000 to 4096 keys with 15, 30 and 60 rows take 94,
+// 115 and 181 us.  Their code is kept short, chunk by chunk of 16 rows: unrolled over 64
+// rows, the warps wait for instructions (309 us for 60 rows).
 #include <type_traits>
 
 #include "attention_tc.cuh"
@@ -48,7 +49,7 @@ namespace {
 
 constexpr int kRowShift = 6, kRows = 1 << kRowShift;  // rows of a block
 // Units of a key tile with up to 16, 32, 48 and 64 rows, and of an item's start and end.
-constexpr int kTileUnits[4] = {10, 13, 17, 21}, kItemUnits[4] = {55, 75, 95, 115};
+constexpr int kTileUnits[4] = {10, 13, 18, 23}, kItemUnits[4] = {40, 50, 60, 70};
 constexpr int kParts = 3;       // of a weight
 constexpr float kPartScale = 32.0f;  // from one part to the next: what is left of 2^8 stays below 2^8
 constexpr float kLazy = 8.0f;   // log2 growth of a maximum that moves its base
@@ -82,7 +83,7 @@ template <int kD> struct Few {
     static constexpr int kThreads = 256;
     static constexpr int kRegsMany = 184, kRegsFew = 72;   // 128 each at launch
     static constexpr int kSmem = kQBytes + kPBytes + 2 * kStages * kRawBytes + (int)sizeof(Shared) + 1024;
-    static_assert(kSmem <= 113 * 1024, "shared memory of two CTAs");
+    static_assert(kSmem <= 113 * 1024, "half of an SM's shared memory");
 };
 
 __device__ __forceinline__ float warp_max(float v) {

@@ -27,8 +27,9 @@
 //
 // Roles: warps 0-3 and 4-7 softmax of slots 0 and 1 (and the loads of Q and the
 // epilogue); warps 8 and 10 issue the MMAs of slots 0 and 1; warp 9 the TMA loads
-// (one box per page and 64 columns); warp 11 guards the values (below); E4M3 adds warps
-// 12-19, which widen value codes to fp16 into the operand ring.
+// (one box per page and 64 columns); warp 11 guards the values (below).  E4M3: warp 9
+// loads the keys, warp 11 the values, and warps 12-19 widen value codes to fp16 into the
+// operand ring.
 //
 // What a row does not see must not reach it, but a product 0 * NaN would.  In the
 // key tiles that hold masked positions the guard warp zeroes the rows past the
@@ -43,6 +44,18 @@
 // 2^(value scale) 2^-x, where the row's integer x follows the largest of them as
 // lazily as base follows z, so that weights fit fp16 whatever the scales are.  All of
 // these are powers of two: the sum of the weights does not depend on the values.
+// (Requests of few rows go to attention_few.cu.)
+//
+// Measured, 8 key/value heads of 128.  Prompts, bound by the tensor pipe in the tiles (a
+// tile for both slots 2500 to 2700 cycles, its MMAs 2048; the softmax's issue slots next)
+// and by an item's start and end, some four tiles' time: one of 12001 tokens with 32
+// heads 725 us, 1.62 PFLOP/s; sixteen of 100 to 2048 tokens with 40 heads 266 us.  Paged,
+// bound by HBM in the tiles, by starts, ends and joins beside: four trees of 64 tokens over
+// 30011 to 60000 keys 158 us, 4.7 TB/s; 32 blocks of 16 tokens over 500 to 8000 keys
+// 108 us, 5.3 TB/s.  What paid, in that order: the slots' MMAs in turns (3400 cycles a tile
+// without), tiles in registers and the base kept from the tile before (no second pass),
+// page numbers eight tiles ahead, queries copied asynchronously, output rows written
+// whole.  More polling (test_wait) or less (a suspend hint) both cost.
 #include <type_traits>
 
 #include "attention_tc.cuh"
@@ -71,7 +84,7 @@ struct Shared {
     uint64_t full[8], empty[8];  // operand ring (E4M3: filled by the widening warps)
     uint64_t guard_go[8], guard_done[8];  // value tiles on their way, for the guard warp, and back, in order
     uint64_t s_full[2], p_full[2][2], o_full[2];  // weights come in halves of 64 keys
-    uint64_t turn[2];            // shared: whose weights' and next scores' MMAs come next
+    uint64_t turn[2];            // shared: whose sums' and next scores' MMAs come next
     uint64_t q_full, drain[2];
     uint32_t tmem;
     int abort_flag;
@@ -1390,7 +1403,7 @@ dflash2_status launch_tc(const DeviceInfo &di, const Params &p, bool paged, int3
         return p.head_dim == 64 ? launch_one<64, false, false>(di, p, st)
                                 : launch_one<128, false, false>(di, p, st);
     // Few rows a request on average: the transposed kernel.  64 requests over 0 to 8191 keys,
-    // head_dim 128, with 4, 16, 32, 48 and 64 rows take it 106, 109, 138, 182 and 221 us, and
+    // head_dim 128, with 4, 16, 32, 48 and 64 rows take it 101, 103, 128, 167 and 216 us, and
     // this file's 155, 159, 165, 211 and 212.
     if (kv_format == DFLASH2_KV_E4M3 && (int64_t)p.total_q * p.group <= 48 * (int64_t)p.batch)
         return launch_few(di, p, st);
