@@ -171,17 +171,20 @@ def _dtype_code(t: torch.Tensor) -> int:
     raise TypeError(f"unsupported dtype {t.dtype}: fp32 or bf16 only")
 
 
-def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+def _ptr(t):  # the argument types make a void * of it
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
     if stream is None:  # torch.cuda.current_stream() without building a Stream object
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
-    return ctypes.c_void_p(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _need(t: torch.Tensor, name: str, dtype=None, shape=None):
+    if (t.is_cuda and t.is_contiguous() and (dtype is None or t.dtype == dtype)
+            and (shape is None or t.shape == shape)):
+        return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
@@ -746,6 +749,8 @@ def _need_rows(t: torch.Tensor, name: str, dtype, shape) -> int:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     n, heads, d = shape
     st = t.stride()
+    if st[2] == 1 and st[1] == d and n > 1 and st[0] >= heads * d:
+        return st[0]
     if (st[2] != 1 and d > 1) or (st[1] != d and heads > 1):
         raise ValueError(f"{name} must have contiguous heads")
     if n > 1 and st[0] < heads * d:
@@ -754,17 +759,20 @@ def _need_rows(t: torch.Tensor, name: str, dtype, shape) -> int:
 
 
 def _need_cache(c: KVCache, dtype):
-    pages, heads, ps, d = c.k.shape
-    if c.e4m3:
-        if c.k_exp is None or c.v_exp is None:
+    k, v, k_exp, v_exp = c
+    shape = k.shape
+    pages, heads, ps, d = shape
+    if k.dtype == torch.uint8:
+        if k_exp is None or v_exp is None:
             raise ValueError("an E4M3 cache needs k_exp and v_exp")
-        _need(c.k, "cache.k", torch.uint8)
-        _need(c.v, "cache.v", torch.uint8, c.k.shape)
-        _need(c.k_exp, "cache.k_exp", torch.uint8, (pages, heads, ps))
-        _need(c.v_exp, "cache.v_exp", torch.uint8, (pages, heads, ps))
+        _need(k, "cache.k", torch.uint8)
+        _need(v, "cache.v", torch.uint8, shape)
+        exps = (pages, heads, ps)
+        _need(k_exp, "cache.k_exp", torch.uint8, exps)
+        _need(v_exp, "cache.v_exp", torch.uint8, exps)
         return pages, heads, ps, d, KV_E4M3
-    _need(c.k, "cache.k", dtype)
-    _need(c.v, "cache.v", dtype, c.k.shape)
+    _need(k, "cache.k", dtype)
+    _need(v, "cache.v", dtype, shape)
     return pages, heads, ps, d, KV_NATIVE
 
 
