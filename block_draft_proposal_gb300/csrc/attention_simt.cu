@@ -11,10 +11,11 @@
 //
 // Bound by fp32 FMAs once rows fill the tile (kRows = 64) and by HBM for few
 // rows (kRows = 16: 32 FMA cycles per key against 45 cycles of HBM time for an
-// fp32 key and value of head_dim 128).  Short calls wait for each tile's loads (four in
-// flight per thread): three fp32 prompts of up to 301 tokens with 8 heads of 64 take
-// 34 us, some 6 us a tile of 64 keys, and 16-row blocks on more SMs no less.  One prompt
-// of 1500 tokens with 8 heads of 128: 275 us, 17 TFLOP/s.
+// fp32 key and value of head_dim 128).  Short calls are bound by one tile after the
+// other: 64 keys of head_dim 64 take 11400 cycles, 2100 for the loads (four in flight per
+// thread), 4200 for S and 3700 for O, and blocks of 16 rows no less, since every warp
+// reads the whole tile from shared memory.  Three fp32 prompts of up to 301 tokens with 8
+// heads of 64 take 34 us; one of 1500 tokens with 8 heads of 128 275 us, 17 TFLOP/s.
 #include "attention.cuh"
 
 namespace dflash2 {
