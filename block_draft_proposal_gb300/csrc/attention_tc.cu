@@ -66,7 +66,11 @@ namespace {
 
 // A slot has kTile rows, a row block two slots.
 constexpr int kRowShift = 8, kRowBlock = 1 << kRowShift;
-constexpr int kItemUnits = 4;    // an item's start and end cost about as much as four key tiles
+// The split: units of a key tile, and an item's start and end in tiles.  A tile of more
+// than 128 rows of an E4M3 cache counts for more, since the softmax bounds it (32 requests
+// of 1 to 64 tokens over 100 to 6000 keys, 4 to 256 rows: 165 us, and 183 with 10 for all);
+// over a bf16 cache HBM bounds either (109 us, and 114 with 17).
+constexpr int kTileUnits = 10, kSharedUnits = 17, kItemTiles = 4;
 constexpr float kLazy = 8.0f;    // log2 growth of the maximum that forces a rescale
 constexpr int kTopE4M3 = 6;      // fp16 weights: the largest (or its bound) starts below 2^7 ...
 constexpr int kCapE4M3 = 14;     // ... and x moves before one reaches 2^15
@@ -1371,8 +1375,12 @@ dflash2_status launch_one(const DeviceInfo &di, Params p, cudaStream_t st) {
         if (s != DFLASH2_OK) return s;
     }
     p.row_shift = kRowShift;
-    for (int i = 0; i < 4; ++i) p.tile_units[i] = 1, p.item_units[i] = kItemUnits;
-    p.most_units = 1;
+    const bool shared = (int64_t)p.total_q * p.group > kTile;  // some row block may fill both slots
+    for (int i = 0; i < 4; ++i) {
+        p.tile_units[i] = kE4M3 && i >= 2 ? kSharedUnits : kTileUnits;
+        p.item_units[i] = kItemTiles * p.tile_units[i];
+    }
+    p.most_units = kE4M3 && shared ? kSharedUnits : kTileUnits;
     // prompts: every row block of every request, at most one short one each
     const int64_t items = ((((int64_t)p.total_q * p.group) >> kRowShift) + p.batch) * p.kv_heads;
     p.n_cta = kPaged || items > di.sm_count ? di.sm_count : (int32_t)items;
