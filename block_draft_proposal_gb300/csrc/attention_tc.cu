@@ -10,8 +10,8 @@
 //   O += P V           tcgen05.mma, P from TMEM, V [keys x head_dim] as the
 //                      MN-major B operand, as it lies in memory
 //
-// base follows the row's maximum lazily: O and the sum are rescaled only when
-// the maximum has grown by more than 2^8 (weights stay below 2^8 and the sums
+// base follows the row's maximum lazily, from 16: O and the sum are rescaled only
+// when the maximum has grown by more than 2^8 (weights stay below 2^8 and the sums
 // are fp32, so nothing is lost), which leaves the accumulators alone in most
 // tiles.
 //
@@ -49,9 +49,9 @@
 // Measured, 8 key/value heads of 128.  Prompts, bound by the tensor pipe in the tiles (a
 // tile for both slots 2500 to 2700 cycles, its MMAs 2048; the softmax's issue slots next)
 // and by an item's start and end, some four tiles' time: one of 12001 tokens with 32
-// heads 725 us, 1.62 PFLOP/s; sixteen of 100 to 2048 tokens with 40 heads 266 us.  Paged,
+// heads 720 us, 1.64 PFLOP/s; sixteen of 100 to 2048 tokens with 40 heads 257 us.  Paged,
 // bound by HBM in the tiles, by starts, ends and joins beside: four trees of 64 tokens over
-// 30011 to 60000 keys 158 us, 4.7 TB/s; 32 blocks of 16 tokens over 500 to 8000 keys
+// 30011 to 60000 keys 156 us, 4.8 TB/s; 32 blocks of 16 tokens over 500 to 8000 keys
 // 108 us, 5.3 TB/s.  What paid, in that order: the slots' MMAs in turns (3400 cycles a tile
 // without), tiles in registers and the base kept from the tile before (no second pass),
 // page numbers eight tiles ahead, queries copied asynchronously, output rows written
@@ -72,6 +72,10 @@ constexpr int kRowShift = 8, kRowBlock = 1 << kRowShift;
 // over a bf16 cache HBM bounds either (109 us, and 114 with 17).
 constexpr int kTileUnits = 10, kSharedUnits = 17, kItemTiles = 4;
 constexpr float kLazy = 8.0f;    // log2 growth of the maximum that forces a rescale
+// Rows over bf16 keys start from this base, which most never move: their maxima lie
+// between 64 below it and 8 above (from 0, rows cross 8 at one tile or another of a long
+// context: 194 us for the four trees below).
+constexpr float kFirstBase = 16.0f, kLow = 64.0f;
 constexpr int kTopE4M3 = 6;      // fp16 weights: the largest (or its bound) starts below 2^7 ...
 constexpr int kCapE4M3 = 14;     // ... and x moves before one reaches 2^15
 constexpr int kNoShift = -1000;  // no weight yet
@@ -910,7 +914,8 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
             const int32_t all_seen =
                 kPaged ? pc.rq.ctx : pc.tok0 + (int32_t)(((pc.rem0 + (both ? s * kTile : 0)) * magic) >> 16) + 1;
             const int32_t t_end = both && s == 0 ? pc.t1a : pc.t1;
-            float base = -INFINITY, sum = 0.0f;
+            // a row without a weight has no base in the end (below)
+            float base = kE4M3 ? -INFINITY : kFirstBase, sum = 0.0f;
             int x_shift = kNoShift;  // E4M3: x
             bool first = true;
             // O and x or base move together: O 2^x 2^base stays
@@ -1007,20 +1012,20 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                     if (lane == 0) mbar_arrive(&sh.p_full[s][1]);
                 };
                 // the first weights against the base so far, beside the maximum; again, from
-                // the scores in TMEM, where the maximum moved the base (the first tiles,
-                // mostly)
+                // the scores in TMEM, where the maximum moved the base
                 constexpr int kFirst = kC == 4 ? 2 : kC;
 #pragma unroll 1
                 for (bool again = false;;) {
                     scores();
                     const float mx = row_top();
                     part[0] = part[1] = part[2] = part[3] = 0ull;
-                    weights(0, kFirst, base == -INFINITY ? 0.0f : base);
+                    weights(0, kFirst, base);
                     if (again) break;
-                    const bool grow = live_row && mx > base + kLazy;
+                    const bool none = sum == 0.0f;  // no weight yet: the base may fall as well
+                    const bool grow =
+                        live_row && (mx > base + kLazy || (none && mx < base - kLow && mx > -INFINITY));
                     if (!__any_sync(0xFFFFFFFFu, grow)) break;
-                    // grow: base was -inf (fix = 0, nothing summed yet) or finite
-                    const float fix = grow ? ex2(base - mx) : 1.0f;
+                    const float fix = grow && !none ? ex2(base - mx) : 1.0f;
                     if (grow) base = mx;
                     sum *= fix;
                     rescale(fix);
@@ -1029,7 +1034,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                 if constexpr (kC == 4) {
                     tmem_st32(tS, pk);
                     hand_over(0);
-                    weights(2, 4, base == -INFINITY ? 0.0f : base);
+                    weights(2, 4, base);
                     tmem_st32(tS + 32, pk);
                     hand_over(1);
                 } else {
@@ -1176,6 +1181,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
             const int32_t n = pc.t1 - pc.t0;
             const bool used1 = both || n > 1;
             tiles_done += n;
+            if (sum == 0.0f) base = -INFINITY;
             const float up = !kE4M3 || x_shift == kNoShift ? 1.0f : pow2_int(x_shift);
             const int64_t row =
                 (int64_t)(pc.rq.t0 + tok) * p.q_heads + pc.h * p.group + (int)(r_off - r_tok * p.group);
