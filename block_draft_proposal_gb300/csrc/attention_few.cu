@@ -28,16 +28,16 @@
 //
 // Two CTAs share an SM, so that one's softmax runs beside the other's waits, an item's
 // start and end among them (one CTA per SM with two accumulators that take the key tiles
-// in turns: 105 and 189 us for the 101 and 171 below).  Warps 0-3 softmax, the loads of
+// in turns: 105 and 189 us for the 96 and 170 below).  Warps 0-3 softmax, the loads of
 // Q and the epilogue; warp 4 issues the MMAs; warp 5 loads the keys, warp 6 the values
 // (one TMA box per page).
 //
 // Measured (128 per head, 8 key/value heads): 64 requests of one token over 0 to 8191
-// keys, 4 rows a head, take 101 us, 5.4 TB/s of the cache's bytes; 128 requests of trees of
-// up to 12 tokens over 13 to 4096 keys, 5 to 60 rows, 171 us.  Few rows are bound by the
+// keys, 4 rows a head, take 96 us, 5.7 TB/s of the cache's bytes; 128 requests of trees of
+// up to 12 tokens over 13 to 4096 keys, 5 to 60 rows, 170 us.  Few rows are bound by the
 // loads and by an item's start and end (four to five tiles' time); many by the softmax
-// warps' issue slots: 64 requests over 3000 to 4096 keys with 15, 30 and 60 rows take 94,
-// 115 and 181 us.  Their code is kept short, chunk by chunk of 16 rows: unrolled over 64
+// warps' issue slots: 64 requests over 3000 to 4096 keys with 15, 30 and 60 rows take 89,
+// 113 and 189 us.  Their code is kept short, chunk by chunk of 16 rows: unrolled over 64
 // rows, the warps wait for instructions (309 us for 60 rows).
 #include <type_traits>
 
@@ -81,7 +81,8 @@ template <int kD> struct Few {
     static constexpr int kQBytes = 2 * kRows * kD;         // both parts
     static constexpr int kPBytes = kParts * kTile * 64;    // [column blocks of 64][key][column]
     static constexpr int kThreads = 256;
-    static constexpr int kRegsMany = 184, kRegsFew = 72;   // 128 each at launch
+    // registers: 128 each at launch; with 72 for the producers, they spill (101 us below for 96)
+    static constexpr int kRegsMany = 144, kRegsFew = 112;
     static constexpr int kSmem = kQBytes + kPBytes + 2 * kStages * kRawBytes + (int)sizeof(Shared) + 1024;
     static_assert(kSmem <= 113 * 1024, "half of an SM's shared memory");
 };

@@ -49,10 +49,10 @@
 // Measured, 8 key/value heads of 128.  Prompts, bound by the tensor pipe in the tiles (a
 // tile for both slots 2500 to 2700 cycles, its MMAs 2048; the softmax's issue slots next)
 // and by an item's start and end, some four tiles' time: one of 12001 tokens with 32
-// heads 720 us, 1.64 PFLOP/s; sixteen of 100 to 2048 tokens with 40 heads 257 us.  Paged,
+// heads 705 us, 1.67 PFLOP/s; sixteen of 100 to 2048 tokens with 40 heads 255 us.  Paged,
 // bound by HBM in the tiles, by starts, ends and joins beside: four trees of 64 tokens over
-// 30011 to 60000 keys 156 us, 4.8 TB/s; 32 blocks of 16 tokens over 500 to 8000 keys
-// 108 us, 5.3 TB/s.  What paid, in that order: the slots' MMAs in turns (3400 cycles a tile
+// 30011 to 60000 keys 149 us, 5.0 TB/s; 32 blocks of 16 tokens over 500 to 8000 keys
+// 107 us, 5.3 TB/s.  What paid, in that order: the slots' MMAs in turns (3400 cycles a tile
 // without), tiles in registers and the base kept from the tile before (no second pass),
 // page numbers eight tiles ahead, queries copied asynchronously, output rows written
 // whole.  More polling (test_wait) or less (a suspend hint) both cost.
@@ -123,8 +123,10 @@ template <int kD, bool kE4M3> struct Cfg {
     static constexpr int kScales = kStages <= 2 ? 4 : 8;
     using Sh = std::conditional_t<kE4M3, SharedE4M3<kScales>, Shared>;
     static constexpr int kThreads = kE4M3 ? 640 : 384;
-    // registers: softmax warps take what the others give back (E4M3: 96 each at launch)
-    static constexpr int kRegsMany = kE4M3 ? 144 : 216, kRegsFew = kE4M3 ? 64 : 72;
+    // registers: softmax warps take what the others give back (E4M3: 96 each at launch, else
+    // 168; 72 for the others spill in the producer: 256, 718 and 155 us below in place of 255, 705
+    // and 149)
+    static constexpr int kRegsMany = kE4M3 ? 144 : 208, kRegsFew = kE4M3 ? 64 : 88;
     // alternate: (base, sum, 2^x) of 2 x 128 accumulator rows and 128 reciprocal sums; head_dim
     // 128 has room for them in the second query tile, which that mode leaves unused
     static constexpr int kStatBytes = kD == 128 ? 0 : 7 * kTile * 4;
