@@ -15,9 +15,9 @@
 // power of two per row): the eight bits of a bf16 value down to 2^-10 of the row's
 // largest, and 2^-18 of that below.  P is three, in columns of their own that the end
 // adds up: fp16's eleven bits, each part's rest scaled by 2^5 for the next, down to
-// 2^-20 absolute, where a row's largest P lies between 2^3 and 2^8.  A higher start
-// would keep smaller weights and move x more often (2^5: 234 us in place of 181, at the
-// 60 rows below).
+// 2^-20 absolute, where a row's largest P starts at 2^3 and stays below 2^8.  A higher start
+// would keep smaller weights and move x more often (2^5: 210 us in place of 171, for the
+// trees below).
 //
 // z = S 2^(key scale) 2^a scale log2(e), and a weight carries its value's scale:
 // P = 2^(z - base) 2^(value scale) 2^-x with an integer x per row.  base and x are
@@ -36,9 +36,11 @@
 // keys, 4 rows a head, take 96 us, 5.7 TB/s of the cache's bytes; 128 requests of trees of
 // up to 12 tokens over 13 to 4096 keys, 5 to 60 rows, 170 us.  Few rows are bound by the
 // loads and by an item's start and end (four to five tiles' time); many by the softmax
-// warps' issue slots: 64 requests over 3000 to 4096 keys with 15, 30 and 60 rows take 89,
-// 113 and 189 us.  Their code is kept short, chunk by chunk of 16 rows: unrolled over 64
-// rows, the warps wait for instructions (309 us for 60 rows).
+// warps, whose chains of conversions two warps per scheduler do not fill (56 % of the issue
+// slots): 64 requests over 3000 to 4096 keys with 15, 30 and 60 rows take 89, 113 and 178
+// us.  Their code is kept short, chunk by chunk of 16 rows: over two chunks at once, 128
+// requests take 200 us, and unrolled over 64 rows 309, since the warps wait for
+// instructions.  Sums in place of the maxima that tell when to move: no change.
 #include <type_traits>
 
 #include "attention_tc.cuh"

@@ -1419,8 +1419,8 @@ dflash2_status launch_tc(const DeviceInfo &di, const Params &p, bool paged, int3
         return p.head_dim == 64 ? launch_one<64, false, false>(di, p, st)
                                 : launch_one<128, false, false>(di, p, st);
     // Few rows a request on average: the transposed kernel.  64 requests over 0 to 8191 keys,
-    // head_dim 128, with 4, 16, 32, 48 and 64 rows take it 101, 103, 128, 167 and 216 us, and
-    // this file's 155, 159, 165, 211 and 212.
+    // head_dim 128, with 4, 16, 32, 48 and 60 rows take it 97, 100, 127, 165 and 212 us, and
+    // this file's 155, 158, 165, 211 and 211 (head_dim 64, 48 and 60 rows: 155 and 196, 177 and 177).
     if (kv_format == DFLASH2_KV_E4M3 && (int64_t)p.total_q * p.group <= 48 * (int64_t)p.batch)
         return launch_few(di, p, st);
     if (kv_format == DFLASH2_KV_E4M3)
