@@ -10,10 +10,13 @@
 //   O += P V           tcgen05.mma, P from TMEM, V [keys x head_dim] as the
 //                      MN-major B operand, as it lies in memory
 //
-// base follows the row's maximum lazily, from 16: O and the sum are rescaled only
-// when the maximum has grown by more than 2^8 (weights stay below 2^8 and the sums
+// base follows the row's maximum lazily: O and the sum are rescaled only when
+// the maximum has grown by more than 2^8 (weights stay below 2^8 and the sums
 // are fp32, so nothing is lost), which leaves the accumulators alone in most
-// tiles.
+// tiles.  It starts at the first tile's maximum, whose weight of 1 is exact: from a
+// fixed base the first tile is not taken twice (255 us in place of 264 for the sixteen
+// prompts below), but a row of few keys then carries its only weight's rounding (0.0023
+// from 64 bits in place of 0.0020, over all rows).
 //
 // There are two slots, each with a softmax warpgroup, so that one slot's
 // exponentials run beside the other's MMAs:
@@ -49,9 +52,9 @@
 // Measured, 8 key/value heads of 128.  Prompts, bound by the tensor pipe in the tiles (a
 // tile for both slots 2500 to 2700 cycles, its MMAs 2048; the softmax's issue slots next)
 // and by an item's start and end, some four tiles' time: one of 12001 tokens with 32
-// heads 705 us, 1.67 PFLOP/s; sixteen of 100 to 2048 tokens with 40 heads 255 us.  Paged,
+// heads 715 us, 1.65 PFLOP/s; sixteen of 100 to 2048 tokens with 40 heads 264 us.  Paged,
 // bound by HBM in the tiles, by starts, ends and joins beside: four trees of 64 tokens over
-// 30011 to 60000 keys 149 us, 5.0 TB/s; 32 blocks of 16 tokens over 500 to 8000 keys
+// 30011 to 60000 keys 152 us, 4.9 TB/s; 32 blocks of 16 tokens over 500 to 8000 keys
 // 107 us, 5.3 TB/s.  What paid, in that order: the slots' MMAs in turns (3400 cycles a tile
 // without), tiles in registers and the base kept from the tile before (no second pass),
 // page numbers eight tiles ahead, queries copied asynchronously, output rows written
@@ -72,10 +75,6 @@ constexpr int kRowShift = 8, kRowBlock = 1 << kRowShift;
 // over a bf16 cache HBM bounds either (109 us, and 114 with 17).
 constexpr int kTileUnits = 10, kSharedUnits = 17, kItemTiles = 4;
 constexpr float kLazy = 8.0f;    // log2 growth of the maximum that forces a rescale
-// Rows over bf16 keys start from this base, which most never move: their maxima lie
-// between 64 below it and 8 above (from 0, rows cross 8 at one tile or another of a long
-// context: 194 us for the four trees below).
-constexpr float kFirstBase = 16.0f, kLow = 64.0f;
 constexpr int kTopE4M3 = 6;      // fp16 weights: the largest (or its bound) starts below 2^7 ...
 constexpr int kCapE4M3 = 14;     // ... and x moves before one reaches 2^15
 constexpr int kNoShift = -1000;  // no weight yet
@@ -124,8 +123,7 @@ template <int kD, bool kE4M3> struct Cfg {
     using Sh = std::conditional_t<kE4M3, SharedE4M3<kScales>, Shared>;
     static constexpr int kThreads = kE4M3 ? 640 : 384;
     // registers: softmax warps take what the others give back (E4M3: 96 each at launch, else
-    // 168; 72 for the others spill in the producer: 256, 718 and 155 us below in place of 255, 705
-    // and 149)
+    // 168; with 72 for the others, the producer spills: 159 us in place of 152 for the four trees)
     static constexpr int kRegsMany = kE4M3 ? 144 : 208, kRegsFew = kE4M3 ? 64 : 88;
     // alternate: (base, sum, 2^x) of 2 x 128 accumulator rows and 128 reciprocal sums; head_dim
     // 128 has room for them in the second query tile, which that mode leaves unused
@@ -916,8 +914,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
             const int32_t all_seen =
                 kPaged ? pc.rq.ctx : pc.tok0 + (int32_t)(((pc.rem0 + (both ? s * kTile : 0)) * magic) >> 16) + 1;
             const int32_t t_end = both && s == 0 ? pc.t1a : pc.t1;
-            // a row without a weight has no base in the end (below)
-            float base = kE4M3 ? -INFINITY : kFirstBase, sum = 0.0f;
+            float base = -INFINITY, sum = 0.0f;
             int x_shift = kNoShift;  // E4M3: x
             bool first = true;
             // O and x or base move together: O 2^x 2^base stays
@@ -1014,20 +1011,20 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                     if (lane == 0) mbar_arrive(&sh.p_full[s][1]);
                 };
                 // the first weights against the base so far, beside the maximum; again, from
-                // the scores in TMEM, where the maximum moved the base
+                // the scores in TMEM, where the maximum moved the base (the first tiles,
+                // mostly)
                 constexpr int kFirst = kC == 4 ? 2 : kC;
 #pragma unroll 1
                 for (bool again = false;;) {
                     scores();
                     const float mx = row_top();
                     part[0] = part[1] = part[2] = part[3] = 0ull;
-                    weights(0, kFirst, base);
+                    weights(0, kFirst, base == -INFINITY ? 0.0f : base);
                     if (again) break;
-                    const bool none = sum == 0.0f;  // no weight yet: the base may fall as well
-                    const bool grow =
-                        live_row && (mx > base + kLazy || (none && mx < base - kLow && mx > -INFINITY));
+                    const bool grow = live_row && mx > base + kLazy;
                     if (!__any_sync(0xFFFFFFFFu, grow)) break;
-                    const float fix = grow && !none ? ex2(base - mx) : 1.0f;
+                    // grow: base was -inf (fix = 0, nothing summed yet) or finite
+                    const float fix = grow ? ex2(base - mx) : 1.0f;
                     if (grow) base = mx;
                     sum *= fix;
                     rescale(fix);
@@ -1036,7 +1033,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                 if constexpr (kC == 4) {
                     tmem_st32(tS, pk);
                     hand_over(0);
-                    weights(2, 4, base);
+                    weights(2, 4, base == -INFINITY ? 0.0f : base);
                     tmem_st32(tS + 32, pk);
                     hand_over(1);
                 } else {
@@ -1183,7 +1180,6 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
             const int32_t n = pc.t1 - pc.t0;
             const bool used1 = both || n > 1;
             tiles_done += n;
-            if (sum == 0.0f) base = -INFINITY;
             const float up = !kE4M3 || x_shift == kNoShift ? 1.0f : pow2_int(x_shift);
             const int64_t row =
                 (int64_t)(pc.rq.t0 + tok) * p.q_heads + pc.h * p.group + (int)(r_off - r_tok * p.group);
