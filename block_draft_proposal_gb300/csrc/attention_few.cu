@@ -483,9 +483,10 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 2)
 #pragma unroll 1
                         for (int i = 0; i < n_here; ++i) {
                             const uint32_t w = __shfl_sync(0xFFFFFFFFu, bits, i);
-                            const int at = (i0 + i) * p.group - pc.rem0;  // the token's first row
-                            const uint64_t rows = p.group >= 64 ? ~0ull : (1ull << p.group) - 1ull;
-                            if ((w >> lane) & 1u) seen |= at >= 0 ? rows << at : rows >> -at;
+                            // the token's rows in the block: one at least, and they may begin before it
+                            const int at = (i0 + i) * p.group - pc.rem0;
+                            const int r0 = max(at, 0), n_rows = min(at + p.group, kRows) - r0;
+                            if ((w >> lane) & 1u) seen |= (~0ull >> (kRows - n_rows)) << r0;
                         }
                     }
                 }
