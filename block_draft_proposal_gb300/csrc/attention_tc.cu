@@ -84,6 +84,8 @@ struct TileScale {  // E4M3
     int32_t top;   // largest binary exponent of a tile's value scales
     int32_t wide;  // they span more than 22 binades
 };
+constexpr int kMarks = 2 * kPieces;
+__device__ __forceinline__ uint8_t poison_mark(uint32_t piece) { return (uint8_t)(piece / kMarks % 255 + 1); }
 struct Shared {
     alignas(16) uint8_t piece[kPieces][kPieceBytes];
     int32_t pages[2][2][kTile / 16 * 8 + 1];  // page numbers of eight key tiles, twice, by producer
@@ -96,7 +98,11 @@ struct Shared {
     uint32_t tmem;
     int abort_flag;
     int stop[3][2];              // no more pieces: softmax warps, widening warpgroups; by piece parity
-    int poison;                  // number of the last piece with a value not finite
+    // The last pieces with a value not finite: entry i % kMarks holds piece i's mark.  Who finds
+    // one may be kPieces pieces ahead of the epilogue that looks for its own (no piece is handed
+    // out before all roles have taken the one kPieces before it).  An older piece with the same
+    // mark is harmless: the epilogue looks for values and finds none.
+    uint8_t poison[kMarks];
     StartScratch start;
 };
 template <int kTiles> struct SharedE4M3 : Shared {
@@ -264,7 +270,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
         mbar_init(&sh.q_full, 8);
         sh.abort_flag = 0;
         for (int i = 0; i < 3; ++i) sh.stop[i][0] = sh.stop[i][1] = 0;
-        sh.poison = -1;
+        for (int i = 0; i < kMarks; ++i) sh.poison[i] = 0;
         fence_mbar_init();
     }
     if (warp == 8) {
@@ -649,7 +655,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                             }
                         }
                     }
-                    if (found) *(volatile int *)&sh.poison = (int)n_piece;
+                    if (found) *(volatile uint8_t *)&sh.poison[n_piece % kMarks] = poison_mark(n_piece);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sh.guard_done[n_guard & 7u]);
@@ -765,7 +771,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                                          : "memory");
                     }
                 }
-                if (found) *(volatile int *)&sh.poison = (int)n_piece;
+                if (found) *(volatile uint8_t *)&sh.poison[n_piece % kMarks] = poison_mark(n_piece);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.vraw_empty[rs]);
                 fence_proxy_async_smem();
@@ -1326,7 +1332,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
             n_o[0] += 1;
             n_o[1] += used1;
             if (owner) {
-                if (*(volatile int *)&sh.poison == (int)n_piece)
+                if (*(volatile uint8_t *)&sh.poison[n_piece % kMarks] == poison_mark(n_piece))
                     add_poison<kD, kE4M3, kPaged>(p, pc.rq, pc.b, pc.h, tok, max(pc.t0, pc.guard_from) * kTile,
                                                   min(pc.t1 * kTile, pc.rq.len), 0, kD, part ? part + 4 * r_blk : nullptr,
                                                   (__nv_bfloat16 *)p.out + row * kD);
