@@ -1240,6 +1240,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
                             const int c = lane % kRow16;
                             reinterpret_cast<uint4 *>((__nv_bfloat16 *)p.out + at * kD)[c] = stage[i * kRow16 + (c ^ (i & 7))];
                         }
+                        __syncwarp();  // other lanes wrote this thread's row, and it may add to it below
                     }
                 }
             } else {

@@ -81,3 +81,30 @@ def test_short_prompts(cuda, each, d):
         out, lse, err = dflash2.prompt_attention(*rows, cu.cuda(), d ** -0.5, with_lse=True)
         assert int(err.item()) == 0
         _check_prompt(lens, hq, hk, qkv, out, lse, d ** -0.5, BF)
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["native", "e4m3"])
+@pytest.mark.parametrize("t,hq", [(33, 4), (40, 4), (64, 4), (43, 5)])      # 132 to 256 rows
+@pytest.mark.parametrize("d", [64, 128])
+def test_row_blocks_that_fill_both_slots(cuda, d, t, hq, e4m3):
+    """A warp writes whole output rows, and each row's own thread adds the values that
+    are not finite."""
+    c = Case([t] * 40, [(i * 31) % 60 for i in range(40)], 2 * hq, 2, d, 16, e4m3=e4m3, words=1, seed=t)
+    _spoil(c, 1, (NAN,) if e4m3 else (NAN, math.inf, -math.inf))
+    _run(c)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_longer_prompts(cuda, d):
+    lens, hq, hk = [200, 333, 129, 257, 70, 65], 8, 2
+    _, qkv, cu = _prompt(lens, hq, hk, d, BF, 880)
+    at = 0
+    for b, n in enumerate(lens):
+        for i, bad in ((n // 3, NAN), (n // 2, math.inf), (n - 1, -math.inf)):
+            qkv[at + i, hq + hk:, (b + i) % d] = bad
+        at += n
+    dev = qkv.cuda()
+    out, lse, err = dflash2.prompt_attention(dev[:, :hq], dev[:, hq:hq + hk], dev[:, hq + hk:], cu.cuda(),
+                                             d ** -0.5, with_lse=True)
+    assert int(err.item()) == 0
+    _check_prompt(lens, hq, hk, qkv, out, lse, d ** -0.5, BF)
