@@ -662,9 +662,9 @@ dflash2_status dflash2_kv_cache_read(const void *k_cache, const void *v_cache,
  *   down to 2^-10 of the row's largest value), weights times their value's
  *   scale rounded to fp16's eleven bits, under a power of two per row (requests
  *   of 48 rows q_heads / kv_heads * T or fewer on average: as three E4M3 parts
- *   with the value codes, down to 2^-23 of the row's largest; more: with the
- *   codes widened to fp16).  Otherwise fp32 on CUDA cores.  Reduction orders
- *   are fixed, so results are deterministic.
+ *   with the value codes, on a grid 2^-23 of the row's largest; more: with the
+ *   codes widened to fp16, on a grid 2^-22 of it or finer).  Otherwise fp32 on
+ *   CUDA cores.  Reduction orders are fixed, so results are deterministic.
  * Errors:    q_heads not a multiple of kv_heads, q_heads / kv_heads > 128,
  *            head_dim outside [1, 256], a size < 1 (batch, total_q: < 0),
  *            num_pages * kv_heads >= 2^31, max_pages * page_size >= 2^31,
