@@ -238,7 +238,10 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-__device__ __forceinline__ float pow2_byte(uint8_t b) { return ldexpf(1.0f, (int)b - 127); }
+// 2^e of an exponent byte: a normal number.
+__device__ __forceinline__ float pow2_byte(uint8_t b) {
+    return __uint_as_float((uint32_t)(kv_exponent(b) + 127) << 23);
+}
 
 // Element loads as fp32.
 __device__ __forceinline__ float as_f32(float v) { return v; }

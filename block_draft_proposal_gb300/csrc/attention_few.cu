@@ -461,10 +461,8 @@ __global__ void __launch_bounds__(Few<kD>::kThreads, 2)
             for (int32_t t = pc.t0; t < pc.t1; ++t, ++n_tile) {
                 const bool first = t == pc.t0;
                 const int32_t l = t * kTile + my;
-                // written exponents lie in [-48, 48]; what was never written is masked
-                const float km = pow2_int(min(max(ke - 127, -48), 48));
-                const int v_exp = min(max(ve - 127, -48), 48);
-                const float vm = pow2_int(v_exp), vf = (float)v_exp;
+                const float km = pow2_byte((uint8_t)ke), vm = pow2_byte((uint8_t)ve);
+                const float vf = (float)kv_exponent((uint8_t)ve);
                 fetch_exps(t + 1);
                 fetch_page(t + 2);
                 const bool masked = (t + 1) * kTile > pc.rq.ctx;

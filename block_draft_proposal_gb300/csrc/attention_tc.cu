@@ -703,8 +703,7 @@ __global__ void __launch_bounds__(Cfg<kD, kE4M3>::kThreads, 1)
             auto scales = [&](int32_t tile, uint32_t no) {
                 const uint32_t i = no % C::kScales;
                 const bool live = tile * kTile + row < pc.rq.len;
-                // written exponents lie in [-48, 48]; what was never written is masked
-                const int k_exp = min(max(ke - 127, -48), 48), v_exp = min(max(ve - 127, -48), 48);
+                const int k_exp = kv_exponent((uint8_t)ke), v_exp = kv_exponent((uint8_t)ve);
                 fetch_exps(tile + 2);
                 fetch_page(tile + 4);
                 const int vt = __reduce_max_sync(0xFFFFFFFFu, live ? v_exp : -64);

@@ -100,6 +100,13 @@ inline dflash2_status allow_smem(Kernel *kernel, int bytes, int device, std::ato
     return DFLASH2_OK;
 }
 
+// The exponent of an E4M3 cache's row.  Writes leave bytes in [79, 175]; for any other byte every
+// reader takes the nearest of these, so that a row means the same to all of them.
+constexpr int kKvMinExp = -48, kKvMaxExp = 48;
+__device__ __forceinline__ int kv_exponent(uint8_t byte) {
+    return min(max((int)byte - 127, kKvMinExp), kKvMaxExp);
+}
+
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 inline dflash2_status launch_status() {

@@ -19,7 +19,6 @@ namespace dflash2 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMinExp = -48, kMaxExp = 48;
 
 struct KvArgs {
     const void *k, *v;  // packed rows (write: input; read: unused)
@@ -84,12 +83,12 @@ __device__ __forceinline__ void from_f32(__nv_bfloat16 *p, float v) { *p = __flo
 
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// The smallest e in [kMinExp, kMaxExp] with amax <= 448 * 2^e: 448 = 1.75 * 2^8,
+// The smallest e in [kKvMinExp, kKvMaxExp] with amax <= 448 * 2^e: 448 = 1.75 * 2^8,
 // so e is amax's binade minus 8, one more when its significand exceeds 1.75.
 __device__ __forceinline__ int row_exponent(float amax) {
     const uint32_t b = __float_as_uint(amax);
     const int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-    return min(max(e, kMinExp), kMaxExp);
+    return min(max(e, kKvMinExp), kKvMaxExp);
 }
 __device__ __forceinline__ uint8_t encode1(float x) {
     return (uint8_t)__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
@@ -219,11 +218,11 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvArgs a) {
             const int64_t row = at + (int64_t)h * a.page_size;
             raw[u] = Raw8<T>{};
             c[u] = make_uint2(0u, 0u);
-            e[u] = 0;
+            e[u] = 127;
             if (at < 0 || h >= a.kv_heads) continue;
             if constexpr (kE4M3) {
                 c[u] = __ldg(reinterpret_cast<const uint2 *>((const uint8_t *)cache + row * kDim) + lane);
-                e[u] = (int)__ldg(exps + row) - 127;
+                e[u] = __ldg(exps + row);
             } else {
                 raw[u] = load_raw8((const T *)cache + row * kDim + lane * 8);
             }
@@ -234,7 +233,7 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvArgs a) {
             if (h >= a.kv_heads) continue;
             if constexpr (kE4M3) {
                 float x[8];
-                const float s = ldexpf(1.0f, e[u]);
+                const float s = pow2i(kv_exponent((uint8_t)e[u]));
                 const uint32_t b[2] = {c[u].x, c[u].y};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -295,7 +294,7 @@ __global__ void __launch_bounds__(kThreads) kv_read_scalar(const KvArgs a) {
             float x = 0.0f;
             if (row.at >= 0)
                 x = decode1(((const uint8_t *)(row.values ? a.vc : a.kc))[row.at * d + j]) *
-                    ldexpf(1.0f, (int)(row.values ? a.ve : a.ke)[row.at] - 127);
+                    pow2i(kv_exponent((row.values ? a.ve : a.ke)[row.at]));
             from_f32(dst + j, x);
         } else {
             dst[j] = row.at >= 0 ? ((const T *)(row.values ? a.vc : a.kc))[row.at * d + j] : T(0.0f);

@@ -713,8 +713,9 @@ def philox_uniforms(seed: int, n: int, out=None, offset: int = 0, counter=None, 
 class KVCache(NamedTuple):
     """One layer's paged cache: keys and values [pages, kv_heads, page_size,
     head_dim], in float32 or bfloat16, or as uint8 E4M3 codes with one exponent
-    byte per row in k_exp and v_exp [pages, kv_heads, page_size].  A slot is
-    page * page_size + offset.  The tensors are the caller's."""
+    byte per row in k_exp and v_exp [pages, kv_heads, page_size], 79 to 175 (the
+    nearest of these is taken for others).  A slot is page * page_size + offset.
+    The tensors are the caller's."""
     k: torch.Tensor
     v: torch.Tensor
     k_exp: torch.Tensor | None = None

@@ -571,6 +571,8 @@ dflash2_status dflash2_d2t_remap(const int64_t *draft_ids, const int64_t *d2t, i
  *   DFLASH2_KV_E4M3    uint8 E4M3 codes c, and k_exp / v_exp uint8
  *                      [num_pages, kv_heads, page_size], one exponent byte per
  *                      row of head_dim values: a row stands for c * 2^(byte - 127).
+ *                      Bytes are in [79, 175], as every write leaves them; for
+ *                      any other the nearest of these is taken, by all readers.
  * The scale is a power of two, so a code keeps E4M3's four significant bits
  * whatever the row's magnitude and a row is exact in bf16 once read.
  */
