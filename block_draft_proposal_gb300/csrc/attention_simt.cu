@@ -275,8 +275,62 @@ __device__ void run_piece(const Params &p, const Request &rq, int32_t b, int32_t
     }
 }
 
+// Prompts: row block number `want` of all requests, request by request, with every key that its
+// rows may see; `*see` is set where cu_q falls in a chunk of 256 requests that is looked at on the
+// way.  The CTAs that hold the blocks from such a chunk on all find it, and are so many: the grid has
+// a CTA for every block of the requests before the chunk, and one more for each of the others.
+// False: there is no such block.
+template <typename T, int kRows, int kDMax>
+__device__ __forceinline__ bool run_block(const Params &p, int64_t want, StartScratch *scratch, int32_t *see,
+                                          float *smem, bool vec_q, bool vec_k) {
+    constexpr int kBad = 48;  // a chunk's blocks are fewer than 2^48; above that, its clamped requests
+    bool bad = false;
+    const int64_t first = want;
+    for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
+        const int b = b0 + threadIdx.x;
+        Request r{};
+        int64_t n = 0;
+        if (b < p.batch) {
+            r = load_request<false>(p, b, &bad);
+            n = row_blocks(p, r) + ((int64_t)bad << kBad);
+        }
+        int64_t total = block_sum(n, scratch->red);
+        if (total >> kBad) {
+            total &= (1ll << kBad) - 1;
+            if (threadIdx.x == 0) {
+                if (*see == 0) *see = (int32_t)(gridDim.x - (first - want));
+                if (p.err) atomicOr(p.err, DFLASH2_DEVERR_ID_RANGE);
+            }
+        }
+        if (want >= total) {
+            want -= total;
+            continue;
+        }
+        // walk this chunk: few requests hold most of the blocks
+        for (int i = b0; i < min(p.batch, b0 + kThreads); ++i) {
+            r = load_request<false>(p, i, &bad);
+            n = row_blocks(p, r);
+            if (want < n) {
+                const int64_t last = min((int64_t)r.t * p.group, (want + 1) * kRows) - 1;
+                run_piece<T, T, false, kRows, kDMax>(p, r, i, blockIdx.y, (int32_t)want, 0,
+                                                     (int32_t)(last / p.group) + 1, -1, smem, vec_q,
+                                                     vec_k, &bad);
+                break;
+            }
+            want -= n;
+        }
+        return true;
+    }
+    return false;
+}
+
+// CTAs per SM that the registers leave room for.  Prompts of head_dim 64: what shared memory holds
+// (600 fp32 prompts of up to 40 tokens 114 us, and 141 with two in place of three).
+constexpr int min_ctas(bool paged, int rows, int dmax) { return paged || dmax > 64 ? 1 : rows == 16 ? 4 : 3; }
+
 template <typename T, typename C, bool kPaged, int kRows, int kDMax>
-__global__ void __launch_bounds__(kThreads) simt_kernel(const Params p, bool vec_q, bool vec_k) {
+__global__ void __launch_bounds__(kThreads, min_ctas(kPaged, kRows, kDMax))
+    simt_kernel(const Params p, bool vec_q, bool vec_k) {
     extern __shared__ __align__(16) float smem[];
     __shared__ StartScratch scratch;
     grid_dep_wait();
@@ -315,38 +369,22 @@ __global__ void __launch_bounds__(kThreads) simt_kernel(const Params p, bool vec
         }
         if (threadIdx.x == 0) p.join[blockIdx.x] = join;
     } else {
-        // CTA (x, h): row block number `want` of all requests, the last blocks
-        // (which see the most keys) first
-        const int32_t h = blockIdx.y;
-        int64_t want = (int64_t)gridDim.x - 1 - blockIdx.x;
-        for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
-            const int b = b0 + threadIdx.x;
-            Request r{};
-            int64_t n = 0;
-            if (b < p.batch) {
-                r = load_request<false>(p, b, &bad);
-                any_bad |= bad;
-                n = row_blocks(p, r);
-            }
-            const int64_t total = block_sum(n, scratch.red);
-            if (want >= total) {
-                want -= total;
-                continue;
-            }
-            // walk this chunk: few requests hold most of the blocks
-            for (int i = b0; i < min(p.batch, b0 + kThreads); ++i) {
-                r = load_request<false>(p, i, &bad);
-                n = row_blocks(p, r);
-                if (want < n) {
-                    const int64_t last = min((int64_t)r.t * p.group, (want + 1) * kRows) - 1;
-                    run_piece<T, C, false, kRows, kDMax>(p, r, i, h, (int32_t)want, 0,
-                                                         (int32_t)(last / p.group) + 1, -1, smem,
-                                                         vec_q, vec_k, &any_bad);
-                    break;
-                }
-                want -= n;
-            }
-            break;
+        // CTA (x, h): a row block, the last blocks (which see the most keys) first.  The grid has
+        // a CTA for every one, unless cu_q falls and requests overlap: the CTAs that find this go
+        // on.  (What the loop keeps is in shared memory: run_piece has no registers to spare.)
+        __shared__ int32_t see;
+        __shared__ int64_t want;
+        if (threadIdx.x == 0) {
+            see = 0;
+            want = (int64_t)gridDim.x - 1 - blockIdx.x;
+        }
+        __syncthreads();
+#pragma unroll 1
+        while (run_block<T, kRows, kDMax>(p, want, &scratch, &see, smem, vec_q, vec_k)) {
+            __syncthreads();
+            if (see == 0) break;
+            if (threadIdx.x == 0) want += see;
+            __syncthreads();
         }
     }
     if (any_bad && p.err) atomicOr(p.err, DFLASH2_DEVERR_ID_RANGE);
