@@ -8,7 +8,9 @@ there is no fallback.  If the shared library is missing the first call
 raises: build it with ``python -c "import __graft_entry__ as g; g.build()"``.
 
 PyTorch provides device memory and streams only.  Workspaces are caller-owned
-device buffers; the helpers here allocate them with torch when not given.
+device buffers; the helpers here allocate them with torch when not given.  A call
+with ``stream`` allocates what it was not given (workspace, outputs, error word) in
+that stream; that its inputs are ready there is the caller's to see to.
 """
 from __future__ import annotations
 
@@ -195,6 +197,27 @@ def _need(t: torch.Tensor, name: str, dtype=None, shape=None):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _empty(shape, dtype, device, stream):
+    """A tensor that belongs to the stream the call runs on: when it is dropped, its memory goes
+    to later work of that stream, not to the current one's while the call still uses it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _workspace(size: int, device, stream):
+    return _empty(max(1, size), torch.uint8, device, stream)
+
+
+def _error_word(device, stream):
+    """A device error word, cleared in the call's own stream."""
+    if stream is None:
+        return torch.zeros(1, dtype=torch.int32, device=device)
+    with torch.cuda.stream(stream):
+        return torch.zeros(1, dtype=torch.int32, device=device)
+
+
 # ---- entry points -----------------------------------------------------------------
 
 def grouped_conv(x, base, delta, block_size: int, group_size: int, taps: int, out=None,
@@ -205,7 +228,7 @@ def grouped_conv(x, base, delta, block_size: int, group_size: int, taps: int, ou
     for t, nm in ((x, "x"), (base, "base"), (delta, "delta")):
         _need(t, nm, x.dtype)
     if out is None:
-        out = torch.empty_like(x)
+        out = _empty(x.shape, x.dtype, x.device, stream)
     _need(out, "out", x.dtype, x.shape)
     groups = hidden // group_size
     if delta_row_stride is None:
@@ -236,16 +259,16 @@ def unary_topk(h, lm_head, target_vocab: int, mult: float, cap: float, top_k: in
     code = _dtype_code(h)
     dev = h.device
     if cand_ids is None:
-        cand_ids = torch.empty((rows, top_k), dtype=torch.int64, device=dev)
+        cand_ids = _empty((rows, top_k), torch.int64, dev, stream)
     if cand_u is None:
-        cand_u = torch.empty((rows, top_k), dtype=torch.float32, device=dev)
+        cand_u = _empty((rows, top_k), torch.float32, dev, stream)
     _need(cand_ids, "cand_ids", torch.int64)
     _need(cand_u, "cand_u", torch.float32)
     if workspace is None:
-        workspace = torch.empty(max(1, unary_topk_workspace_size(rows, draft_vocab, top_k, code)),
-                                dtype=torch.uint8, device=dev)
+        workspace = _workspace(unary_topk_workspace_size(rows, draft_vocab, top_k,
+                                                         code), dev, stream)
     if err is None:
-        err = torch.zeros(1, dtype=torch.int32, device=dev)
+        err = _error_word(dev, stream)
     _check("dflash2_unary_topk", library().dflash2_unary_topk(
         _ptr(h), _ptr(lm_head), rows, hidden, draft_vocab, target_vocab, float(mult),
         float(cap), top_k, code, _ptr(cand_ids), _ptr(cand_u), _ptr(workspace),
@@ -258,9 +281,9 @@ def quantize_rows_e4m3(x, q=None, scale=None, stream=None):
     rows, cols = x.shape
     _need(x, "x")
     if q is None:
-        q = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
+        q = _empty((rows, cols), torch.uint8, x.device, stream)
     if scale is None:
-        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+        scale = _empty(rows, torch.float32, x.device, stream)
     _check("dflash2_quantize_rows_e4m3", library().dflash2_quantize_rows_e4m3(
         _ptr(x), rows, cols, _dtype_code(x), _ptr(q), _ptr(scale), _stream(stream)))
     return q, scale
@@ -281,15 +304,14 @@ def unary_topk_fp8(h, lm_head_q, w_scale, target_vocab: int, mult: float, cap: f
     _need(w_scale, "w_scale", torch.float32, (draft_vocab,))
     dev = h.device
     if cand_ids is None:
-        cand_ids = torch.empty((rows, top_k), dtype=torch.int64, device=dev)
+        cand_ids = _empty((rows, top_k), torch.int64, dev, stream)
     if cand_u is None:
-        cand_u = torch.empty((rows, top_k), dtype=torch.float32, device=dev)
+        cand_u = _empty((rows, top_k), torch.float32, dev, stream)
     if workspace is None:
-        workspace = torch.empty(max(1, unary_topk_fp8_workspace_size(rows, hidden, draft_vocab,
-                                                                     top_k)),
-                                dtype=torch.uint8, device=dev)
+        workspace = _workspace(unary_topk_fp8_workspace_size(rows, hidden, draft_vocab,
+                                                             top_k), dev, stream)
     if err is None:
-        err = torch.zeros(1, dtype=torch.int32, device=dev)
+        err = _error_word(dev, stream)
     _check("dflash2_unary_topk_fp8", library().dflash2_unary_topk_fp8(
         _ptr(h), _dtype_code(h), _ptr(lm_head_q), _ptr(w_scale), rows, hidden, draft_vocab,
         target_vocab, float(mult), float(cap), top_k, _ptr(cand_ids), _ptr(cand_u),
@@ -305,11 +327,11 @@ def quantize_rows_nvfp4(x, codes=None, scales=None, g=None, stream=None):
     _need(x, "x")
     dev = x.device
     if codes is None:
-        codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=dev)
+        codes = _empty((rows, cols // 2), torch.uint8, dev, stream)
     if scales is None:
-        scales = torch.empty((rows, cols // 16), dtype=torch.uint8, device=dev)
+        scales = _empty((rows, cols // 16), torch.uint8, dev, stream)
     if g is None:
-        g = torch.empty(rows, dtype=torch.float32, device=dev)
+        g = _empty(rows, torch.float32, dev, stream)
     _check("dflash2_quantize_rows_nvfp4", library().dflash2_quantize_rows_nvfp4(
         _ptr(x), rows, cols, _dtype_code(x), _ptr(codes), _ptr(scales), _ptr(g),
         _stream(stream)))
@@ -322,8 +344,8 @@ def nvfp4_tile_scales(scales, hidden: int, tiles=None, stream=None):
     rows = scales.shape[0]
     _need(scales, "scales", torch.uint8, (rows, hidden // 16))
     if tiles is None:
-        tiles = torch.empty(max(1, int(library().dflash2_nvfp4_scale_tiles_size(rows, hidden))),
-                            dtype=torch.uint8, device=scales.device)
+        tiles = _workspace(int(library().dflash2_nvfp4_scale_tiles_size(rows, hidden)),
+                           scales.device, stream)
     _check("dflash2_nvfp4_tile_scales", library().dflash2_nvfp4_tile_scales(
         _ptr(scales), rows, hidden, _ptr(tiles), _stream(stream)))
     return tiles
@@ -351,15 +373,14 @@ def unary_topk_nvfp4(h, lm_head_q, w_scale_tiles, w_global: float, target_vocab:
         raise ValueError(f"w_scale_tiles: uint8 scale tiles of {need} bytes expected")
     dev = h.device
     if cand_ids is None:
-        cand_ids = torch.empty((rows, top_k), dtype=torch.int64, device=dev)
+        cand_ids = _empty((rows, top_k), torch.int64, dev, stream)
     if cand_u is None:
-        cand_u = torch.empty((rows, top_k), dtype=torch.float32, device=dev)
+        cand_u = _empty((rows, top_k), torch.float32, dev, stream)
     if workspace is None:
-        workspace = torch.empty(max(1, unary_topk_nvfp4_workspace_size(rows, hidden, draft_vocab,
-                                                                       top_k)),
-                                dtype=torch.uint8, device=dev)
+        workspace = _workspace(unary_topk_nvfp4_workspace_size(rows, hidden, draft_vocab,
+                                                               top_k), dev, stream)
     if err is None:
-        err = torch.zeros(1, dtype=torch.int32, device=dev)
+        err = _error_word(dev, stream)
     _check("dflash2_unary_topk_nvfp4", library().dflash2_unary_topk_nvfp4(
         _ptr(h), _dtype_code(h), _ptr(lm_head_q), _ptr(w_scale_tiles), float(w_global), rows, hidden,
         draft_vocab, target_vocab, float(mult), float(cap), top_k, _ptr(cand_ids), _ptr(cand_u),
@@ -378,13 +399,13 @@ def topk_merge(ids, u, id_offsets, k_out: int, out_ids=None, out_u=None, err=Non
         raise ValueError("one id offset per shard")
     dev = ids.device
     if out_ids is None:
-        out_ids = torch.empty((rows, k_out), dtype=torch.int64, device=dev)
+        out_ids = _empty((rows, k_out), torch.int64, dev, stream)
     if out_u is None:
-        out_u = torch.empty((rows, k_out), dtype=torch.float32, device=dev)
+        out_u = _empty((rows, k_out), torch.float32, dev, stream)
     _need(out_ids, "out_ids", torch.int64, (rows, k_out))
     _need(out_u, "out_u", torch.float32, (rows, k_out))
     if err is None:
-        err = torch.zeros(1, dtype=torch.int32, device=dev)
+        err = _error_word(dev, stream)
     host_offs = (ctypes.c_int64 * shards)(*offs)
     _check("dflash2_topk_merge", library().dflash2_topk_merge(
         _ptr(ids), _ptr(u), ctypes.cast(host_offs, ctypes.c_void_p), shards, rows, k_in, k_out,
@@ -485,17 +506,16 @@ def selector_walk(h, proj, A, B, anchor_ids, cand_ids, cand_u, temperatures, gre
     if A.shape != B.shape or A.shape[1] != rank:
         raise ValueError("A and B must both be [table_rows, rank]")
     if tokens is None:
-        tokens = torch.empty((batch, slots), dtype=torch.int64, device=dev)
+        tokens = _empty((batch, slots), torch.int64, dev, stream)
     if q is None:
-        q = torch.empty((batch, slots, top_k), dtype=torch.float32, device=dev)
+        q = _empty((batch, slots, top_k), torch.float32, dev, stream)
     if path_scores is None and with_path_scores:
-        path_scores = torch.empty((batch, slots, top_k), dtype=torch.float32, device=dev)
+        path_scores = _empty((batch, slots, top_k), torch.float32, dev, stream)
     if workspace is None:
-        workspace = torch.empty(
-            max(1, selector_walk_workspace_size(batch, slots, hidden, rank, top_k, code)),
-            dtype=torch.uint8, device=dev)
+        workspace = _workspace(selector_walk_workspace_size(batch, slots, hidden, rank, top_k,
+                                                            code), dev, stream)
     if err is None:
-        err = torch.zeros(1, dtype=torch.int32, device=dev)
+        err = _error_word(dev, stream)
     _check("dflash2_selector_walk", library().dflash2_selector_walk(
         _ptr(h), _ptr(proj), _ptr(A), _ptr(B), A.shape[0], _ptr(anchor_ids), _ptr(cand_ids),
         _ptr(cand_u), _ptr(temperatures), _ptr(greedy), _ptr(uniforms), batch, slots, hidden,
@@ -544,13 +564,13 @@ def selector_walk_projected(A, B, anchor_ids, cand_ids, cand_u, temperatures, gr
     if A.shape != B.shape:
         raise ValueError("A and B must both be [table_rows, rank]")
     if tokens is None:
-        tokens = torch.empty((batch, slots), dtype=torch.int64, device=dev)
+        tokens = _empty((batch, slots), torch.int64, dev, stream)
     if q is None:
-        q = torch.empty((batch, slots, top_k), dtype=torch.float32, device=dev)
+        q = _empty((batch, slots, top_k), torch.float32, dev, stream)
     if path_scores is None and with_path_scores:
-        path_scores = torch.empty((batch, slots, top_k), dtype=torch.float32, device=dev)
+        path_scores = _empty((batch, slots, top_k), torch.float32, dev, stream)
     if err is None:
-        err = torch.zeros(1, dtype=torch.int32, device=dev)
+        err = _error_word(dev, stream)
     _check("dflash2_selector_walk_projected", library().dflash2_selector_walk_projected(
         _ptr(A), _ptr(B), A.shape[0], _ptr(anchor_ids), _ptr(cand_ids), _ptr(cand_u),
         _ptr(temperatures), _ptr(greedy), _ptr(uniforms), batch, slots, hidden, rank, top_k, code,
@@ -577,13 +597,13 @@ def selector_walk_noalloc(h, proj, A, B, anchor_ids, cand_ids, cand_u, temperatu
     _need(uniforms, "uniforms", torch.float32, (batch, slots))
     dev = h.device
     if tokens is None:
-        tokens = torch.empty((batch, slots), dtype=torch.int64, device=dev)
+        tokens = _empty((batch, slots), torch.int64, dev, stream)
     if q is None:
-        q = torch.empty((batch, slots, top_k), dtype=torch.float32, device=dev)
+        q = _empty((batch, slots, top_k), torch.float32, dev, stream)
     if path_scores is None and with_path_scores:
-        path_scores = torch.empty((batch, slots, top_k), dtype=torch.float32, device=dev)
+        path_scores = _empty((batch, slots, top_k), torch.float32, dev, stream)
     if err is None:
-        err = torch.zeros(1, dtype=torch.int32, device=dev)
+        err = _error_word(dev, stream)
     _check("dflash2_selector_walk_noalloc", library().dflash2_selector_walk_noalloc(
         _ptr(h), _ptr(proj), _ptr(A), _ptr(B), A.shape[0], _ptr(anchor_ids), _ptr(cand_ids),
         _ptr(cand_u), _ptr(temperatures), _ptr(greedy), _ptr(uniforms), batch, slots,
@@ -599,9 +619,9 @@ def d2t_remap(draft_ids, d2t, draft_vocab: int, target_vocab: int, out=None, err
     if d2t is not None:
         _need(d2t, "d2t", torch.int64, (draft_vocab,))
     if out is None:
-        out = torch.empty_like(draft_ids)
+        out = _empty(draft_ids.shape, draft_ids.dtype, draft_ids.device, stream)
     if err is None:
-        err = torch.zeros(1, dtype=torch.int32, device=draft_ids.device)
+        err = _error_word(draft_ids.device, stream)
     _check("dflash2_d2t_remap", library().dflash2_d2t_remap(
         _ptr(draft_ids), _ptr(d2t), draft_ids.numel(), draft_vocab, target_vocab, _ptr(out),
         _ptr(err), _stream(stream)))
@@ -618,12 +638,12 @@ def conv_prepare(x, w_kp, base2, block_size: int, group_size: int, taps: int, ou
     _need(w_kp, "w_kp", x.dtype, (2 * taps * groups, hidden))
     _need(base2, "base2", x.dtype, (2, taps, hidden))
     if out is None:
-        out = torch.empty_like(x)
+        out = _empty(x.shape, x.dtype, x.device, stream)
     if coef is None:
-        coef = torch.empty((n, 2, taps, groups), dtype=x.dtype, device=x.device)
+        coef = _empty((n, 2, taps, groups), x.dtype, x.device, stream)
     _need(coef, "coef", x.dtype, (n, 2, taps, groups))
     if err is None:
-        err = torch.zeros(1, dtype=torch.int32, device=x.device)
+        err = _error_word(x.device, stream)
     _check("dflash2_conv_prepare", library().dflash2_conv_prepare(
         _ptr(x), _ptr(w_kp), _ptr(base2), n, hidden, group_size, taps, block_size, code,
         _ptr(out), _ptr(coef), _ptr(err), _stream(stream)))
@@ -640,7 +660,7 @@ def conv_finish(y, coef, base2, block_size: int, group_size: int, taps: int, out
     _need(coef, "coef", y.dtype, (n, 2, taps, groups))
     _need(base2, "base2", y.dtype, (2, taps, hidden))
     if out is None:
-        out = torch.empty_like(y)
+        out = _empty(y.shape, y.dtype, y.device, stream)
     _check("dflash2_conv_finish", library().dflash2_conv_finish(
         _ptr(y), _ptr(base2), _ptr(coef), n, hidden, group_size, taps, block_size, code,
         _ptr(out), _stream(stream)))
@@ -665,14 +685,13 @@ def verify(target_logits, temperatures, greedy, draft, cand, q, uniforms, accept
     _need(uniforms, "uniforms", torch.float32, (b, s1))
     dev = target_logits.device
     if accept_len is None:
-        accept_len = torch.empty(b, dtype=torch.int64, device=dev)
+        accept_len = _empty(b, torch.int64, dev, stream)
     if out_tokens is None:
-        out_tokens = torch.empty((b, s1), dtype=torch.int64, device=dev)
+        out_tokens = _empty((b, s1), torch.int64, dev, stream)
     if workspace is None:
-        workspace = torch.empty(max(1, verify_workspace_size(b, slots, vocab)),
-                                dtype=torch.uint8, device=dev)
+        workspace = _workspace(verify_workspace_size(b, slots, vocab), dev, stream)
     if err is None:
-        err = torch.zeros(1, dtype=torch.int32, device=dev)
+        err = _error_word(dev, stream)
     _check("dflash2_verify", library().dflash2_verify(
         _ptr(target_logits), vocab, _ptr(temperatures), _ptr(greedy), _ptr(draft), _ptr(cand),
         _ptr(q), _ptr(uniforms), b, slots, k, code, _ptr(accept_len), _ptr(out_tokens),
@@ -697,7 +716,7 @@ def philox_uniforms(seed: int, n: int, out=None, offset: int = 0, counter=None, 
     if out is None:
         if device is None:
             raise ValueError("philox_uniforms needs `out`, `counter` or `device`")
-        out = torch.empty(int(n), dtype=torch.float32, device=device)
+        out = _empty(int(n), torch.float32, device, stream)
     else:
         _need(out, "out", torch.float32)
         if out.numel() < n:
@@ -787,7 +806,7 @@ def kv_cache_write(cache: KVCache, k, v, slots, err=None, stream=None):
     vs = _need_rows(v, "v", k.dtype, (n, heads, d))
     _need(slots, "slots", torch.int64, (n,))
     if err is None:
-        err = torch.zeros(1, dtype=torch.int32, device=k.device)
+        err = _error_word(k.device, stream)
     _check("dflash2_kv_cache_write", library().dflash2_kv_cache_write(
         _ptr(k), _ptr(v), ks, vs, _ptr(slots), n, heads, d, ps, pages, _dtype_code(k), fmt,
         _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_exp), _ptr(cache.v_exp), _ptr(err),
@@ -803,15 +822,15 @@ def kv_cache_read(cache: KVCache, slots, dtype=torch.bfloat16, k_out=None, v_out
     _need(slots, "slots", torch.int64)
     n = slots.numel()
     if k_out is None:
-        k_out = torch.empty((n, heads, d), dtype=dtype, device=slots.device)
+        k_out = _empty((n, heads, d), dtype, slots.device, stream)
     else:
         _need(k_out, "k_out", dtype, (n, heads, d))
     if v_out is None:
-        v_out = torch.empty_like(k_out)
+        v_out = _empty(k_out.shape, k_out.dtype, k_out.device, stream)
     else:
         _need(v_out, "v_out", dtype, (n, heads, d))
     if err is None:
-        err = torch.zeros(1, dtype=torch.int32, device=slots.device)
+        err = _error_word(slots.device, stream)
     _check("dflash2_kv_cache_read", library().dflash2_kv_cache_read(
         _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_exp), _ptr(cache.v_exp), _ptr(slots), n, heads,
         d, ps, pages, _dtype_code(k_out), fmt, _ptr(k_out), _ptr(v_out), _ptr(err),
@@ -849,19 +868,18 @@ def tree_attention(q, cache: KVCache, page_table, cu_q, kv_lens, scale: float, t
         _need(tree_mask, "tree_mask", torch.int64, (total, words))
     dev = q.device
     if out is None:
-        out = torch.empty((total, heads, d), dtype=q.dtype, device=dev)
+        out = _empty((total, heads, d), q.dtype, dev, stream)
     else:
         _need(out, "out", q.dtype, (total, heads, d))
     if lse is not None:
         _need(lse, "lse", torch.float32, (total, heads))
     elif with_lse:
-        lse = torch.empty((total, heads), dtype=torch.float32, device=dev)
+        lse = _empty((total, heads), torch.float32, dev, stream)
     if workspace is None:
-        workspace = torch.empty(max(1, tree_attention_workspace_size(total, batch, heads, kv_heads,
-                                                                     d)),
-                                dtype=torch.uint8, device=dev)
+        workspace = _workspace(tree_attention_workspace_size(total, batch, heads, kv_heads,
+                                                             d), dev, stream)
     if err is None:
-        err = torch.zeros(1, dtype=torch.int32, device=dev)
+        err = _error_word(dev, stream)
     _check("dflash2_tree_attention", library().dflash2_tree_attention(
         _ptr(q), qs, _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_exp), _ptr(cache.v_exp),
         _ptr(page_table), max_pages, pages, ps, _ptr(cu_q), _ptr(kv_lens), _ptr(tree_mask), words,
@@ -893,19 +911,18 @@ def prompt_attention(q, k, v, cu_q, scale: float, out=None, lse=None, with_lse: 
         raise ValueError("cu_q must have batch + 1 entries")
     dev = q.device
     if out is None:
-        out = torch.empty((total, heads, d), dtype=q.dtype, device=dev)
+        out = _empty((total, heads, d), q.dtype, dev, stream)
     else:
         _need(out, "out", q.dtype, (total, heads, d))
     if lse is not None:
         _need(lse, "lse", torch.float32, (total, heads))
     elif with_lse:
-        lse = torch.empty((total, heads), dtype=torch.float32, device=dev)
+        lse = _empty((total, heads), torch.float32, dev, stream)
     if workspace is None:
-        workspace = torch.empty(max(1, prompt_attention_workspace_size(total, batch, heads,
-                                                                       kv_heads, d)),
-                                dtype=torch.uint8, device=dev)
+        workspace = _workspace(prompt_attention_workspace_size(total, batch, heads, kv_heads,
+                                                               d), dev, stream)
     if err is None:
-        err = torch.zeros(1, dtype=torch.int32, device=dev)
+        err = _error_word(dev, stream)
     _check("dflash2_prompt_attention", library().dflash2_prompt_attention(
         _ptr(q), _ptr(k), _ptr(v), qs, ks, vs, _ptr(cu_q), batch, total, heads, kv_heads, d,
         float(scale), _dtype_code(q), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(),
