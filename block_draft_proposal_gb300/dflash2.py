@@ -866,6 +866,8 @@ def tree_attention(q, cache: KVCache, page_table, cu_q, kv_lens, scale: float, t
     if tree_mask is not None:
         words = tree_mask.shape[-1]
         _need(tree_mask, "tree_mask", torch.int64, (total, words))
+        if words < 1:  # an empty tensor's pointer is NULL: no mask
+            raise ValueError("tree_mask must have a word per token at least")
     dev = q.device
     if out is None:
         out = _empty((total, heads, d), q.dtype, dev, stream)
