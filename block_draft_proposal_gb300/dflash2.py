@@ -778,6 +778,15 @@ def _need_rows(t: torch.Tensor, name: str, dtype, shape) -> int:
     return st[0] if n > 1 else heads * d
 
 
+def _need_error_word(err, device, stream):
+    if err is None:
+        return _error_word(device, stream)
+    _need(err, "err", torch.int32)
+    if err.numel() < 1:
+        raise ValueError("err must hold a word")
+    return err
+
+
 def _need_cache(c: KVCache, dtype):
     k, v, k_exp, v_exp = c
     shape = k.shape
@@ -805,8 +814,7 @@ def kv_cache_write(cache: KVCache, k, v, slots, err=None, stream=None):
     ks = _need_rows(k, "k", k.dtype, (n, heads, d))
     vs = _need_rows(v, "v", k.dtype, (n, heads, d))
     _need(slots, "slots", torch.int64, (n,))
-    if err is None:
-        err = _error_word(k.device, stream)
+    err = _need_error_word(err, k.device, stream)
     _check("dflash2_kv_cache_write", library().dflash2_kv_cache_write(
         _ptr(k), _ptr(v), ks, vs, _ptr(slots), n, heads, d, ps, pages, _dtype_code(k), fmt,
         _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_exp), _ptr(cache.v_exp), _ptr(err),
@@ -829,8 +837,7 @@ def kv_cache_read(cache: KVCache, slots, dtype=torch.bfloat16, k_out=None, v_out
         v_out = _empty(k_out.shape, k_out.dtype, k_out.device, stream)
     else:
         _need(v_out, "v_out", dtype, (n, heads, d))
-    if err is None:
-        err = _error_word(slots.device, stream)
+    err = _need_error_word(err, slots.device, stream)
     _check("dflash2_kv_cache_read", library().dflash2_kv_cache_read(
         _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_exp), _ptr(cache.v_exp), _ptr(slots), n, heads,
         d, ps, pages, _dtype_code(k_out), fmt, _ptr(k_out), _ptr(v_out), _ptr(err),
@@ -880,13 +887,14 @@ def tree_attention(q, cache: KVCache, page_table, cu_q, kv_lens, scale: float, t
     if workspace is None:
         workspace = _workspace(tree_attention_workspace_size(total, batch, heads, kv_heads,
                                                              d), dev, stream)
-    if err is None:
-        err = _error_word(dev, stream)
+    else:
+        _need(workspace, "workspace")
+    err = _need_error_word(err, dev, stream)
     _check("dflash2_tree_attention", library().dflash2_tree_attention(
         _ptr(q), qs, _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_exp), _ptr(cache.v_exp),
         _ptr(page_table), max_pages, pages, ps, _ptr(cu_q), _ptr(kv_lens), _ptr(tree_mask), words,
         batch, total, heads, kv_heads, d, float(scale), _dtype_code(q), fmt, _ptr(out), _ptr(lse),
-        _ptr(workspace), workspace.numel(), _ptr(err), _stream(stream)))
+        _ptr(workspace), workspace.nbytes, _ptr(err), _stream(stream)))
     return out, lse, err
 
 
@@ -923,11 +931,12 @@ def prompt_attention(q, k, v, cu_q, scale: float, out=None, lse=None, with_lse: 
     if workspace is None:
         workspace = _workspace(prompt_attention_workspace_size(total, batch, heads, kv_heads,
                                                                d), dev, stream)
-    if err is None:
-        err = _error_word(dev, stream)
+    else:
+        _need(workspace, "workspace")
+    err = _need_error_word(err, dev, stream)
     _check("dflash2_prompt_attention", library().dflash2_prompt_attention(
         _ptr(q), _ptr(k), _ptr(v), qs, ks, vs, _ptr(cu_q), batch, total, heads, kv_heads, d,
-        float(scale), _dtype_code(q), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(),
+        float(scale), _dtype_code(q), _ptr(out), _ptr(lse), _ptr(workspace), workspace.nbytes,
         _ptr(err), _stream(stream)))
     return out, lse, err
 

@@ -37,3 +37,34 @@ def test_a_mask_without_words():
         _tree(tree_mask=_t(3, 0, dtype=torch.int64))
     with pytest.raises(ValueError):
         _tree(tree_mask=_t(3, dtype=torch.int64))
+
+
+def _write(**kw):
+    return dflash2.kv_cache_write(dflash2.new_kv_cache(4, 16, 2, 64), _t(3, 2, 64), _t(3, 2, 64),
+                                  _t(3, dtype=torch.int64), **kw)
+
+
+def _read(**kw):
+    return dflash2.kv_cache_read(dflash2.new_kv_cache(4, 16, 2, 64), _t(3, dtype=torch.int64), **kw)
+
+
+def _prompt(**kw):
+    return dflash2.prompt_attention(_t(3, 4, 64), _t(3, 2, 64), _t(3, 2, 64), _t(3, dtype=torch.int32), 0.1, **kw)
+
+
+@pytest.mark.parametrize("call", [_write, _read, _tree, _prompt])
+def test_error_words(call):
+    call(err=_t(1, dtype=torch.int32))
+    call(err=_t(4, dtype=torch.int32))
+    for bad, kind in ((_t(1, dtype=torch.int32, device="cpu"), ValueError), (_t(1, dtype=torch.int64), TypeError),
+                      (_t(0, dtype=torch.int32), ValueError)):
+        with pytest.raises(kind):
+            call(err=bad)
+
+
+@pytest.mark.parametrize("call", [_tree, _prompt])
+def test_workspaces(call):
+    call(workspace=_t(64, dtype=torch.uint8))
+    for bad in (_t(64, dtype=torch.uint8, device="cpu"), _t(128, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError):
+            call(workspace=bad)
