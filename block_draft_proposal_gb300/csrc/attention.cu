@@ -55,7 +55,7 @@ extern "C" dflash2_status dflash2_tree_attention(
     if (kv_format != DFLASH2_KV_NATIVE && kv_format != DFLASH2_KV_E4M3)
         return DFLASH2_ERR_UNSUPPORTED_DTYPE;
     if (page_size < 1 || max_pages < 1 || num_pages < 1 ||
-        (int64_t)max_pages * page_size >= (1ll << 31) || num_pages >= (1ll << 31) / kv_heads ||
+        (int64_t)max_pages * page_size > attn::kMaxKeys || num_pages >= (1ll << 31) / kv_heads ||
         q_row_stride < (int64_t)q_heads * head_dim || (tree_mask && (mask_words < 1 || mask_words > (1 << 20))))
         return DFLASH2_ERR_INVALID_ARG;
     if (total_q == 0 || batch == 0) return DFLASH2_OK;

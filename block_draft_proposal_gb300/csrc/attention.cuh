@@ -25,6 +25,9 @@ namespace attn {
 constexpr int kKeyTile = 128;
 constexpr int kMaxBatch = 65536;
 constexpr int kMaxGroup = 128;
+// Keys of a paged request.  Kernels count positions in 32 bits up to some tiles past the last key
+// (its tile's end, and page numbers fetched fifteen tiles ahead).
+constexpr int64_t kMaxKeys = (1ll << 31) - 4096;
 
 struct Params {
     const void *q;

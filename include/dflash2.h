@@ -669,7 +669,7 @@ dflash2_status dflash2_kv_cache_read(const void *k_cache, const void *v_cache,
  *   CUDA cores.  Reduction orders are fixed, so results are deterministic.
  * Errors:    q_heads not a multiple of kv_heads, q_heads / kv_heads > 128,
  *            head_dim outside [1, 256], a size < 1 (batch, total_q: < 0),
- *            num_pages * kv_heads >= 2^31, max_pages * page_size >= 2^31,
+ *            num_pages * kv_heads >= 2^31, max_pages * page_size > 2^31 - 4096,
  *            batch > 65536, total_q * q_heads >= 2^31, scale not finite, a
  *            null pointer -> INVALID_ARG; unknown dtype or kv_format ->
  *            UNSUPPORTED_DTYPE; a pointer not aligned to its element ->
