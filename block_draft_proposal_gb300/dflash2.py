@@ -781,8 +781,8 @@ def _need_rows(t: torch.Tensor, name: str, dtype, shape) -> int:
 def _need_error_word(err, device, stream):
     if err is None:
         return _error_word(device, stream)
-    _need(err, "err", torch.int32)
-    if err.numel() < 1:
+    if not (err.is_cuda and err.dtype == torch.int32 and err.numel()):
+        _need(err, "err", torch.int32)
         raise ValueError("err must hold a word")
     return err
 
