@@ -15,7 +15,7 @@
 // other: 64 keys of head_dim 64 take 11400 cycles, 2100 for the loads (four in flight per
 // thread), 4200 for S and 3700 for O, and blocks of 16 rows no less, since every warp
 // reads the whole tile from shared memory.  Three fp32 prompts of up to 301 tokens with 8
-// heads of 64 take 34 us; one of 1500 tokens with 8 heads of 128 275 us, 17 TFLOP/s.
+// heads of 64 take 34 us; one of 1500 tokens with 8 heads of 128 265 us, 17 TFLOP/s.
 #include "attention.cuh"
 
 namespace dflash2 {

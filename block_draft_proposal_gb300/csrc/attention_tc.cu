@@ -52,10 +52,11 @@
 // Measured, 8 key/value heads of 128.  Prompts, bound by the tensor pipe in the tiles (a
 // tile for both slots 2500 to 2700 cycles, its MMAs 2048; the softmax's issue slots next)
 // and by an item's start and end, some four tiles' time: one of 12001 tokens with 32
-// heads 715 us, 1.65 PFLOP/s; sixteen of 100 to 2048 tokens with 40 heads 264 us.  Paged,
-// bound by HBM in the tiles, by starts, ends and joins beside: four trees of 64 tokens over
-// 30011 to 60000 keys 152 us, 4.9 TB/s; 32 blocks of 16 tokens over 500 to 8000 keys
-// 107 us, 5.3 TB/s.  What paid, in that order: the slots' MMAs in turns (3400 cycles a tile
+// heads 715 to 780 us with the clock under the power cap, 1.52 to 1.65 PFLOP/s; sixteen of
+// 100 to 2048 tokens with 40 heads 269 us, the tensor pipe busy for 49 % of it.  Paged, starts,
+// ends and joins beside: four trees of 64 tokens over 30011 to 60000 keys 152 to 169 us, 4.4 to
+// 4.9 TB/s, bound by the tensor pipe and HBM alike (61 and 67 % busy); 32 blocks of 16 tokens
+// over 500 to 8000 keys by HBM, 107 us, 5.3 TB/s.  What paid, in that order: the slots' MMAs in turns (3400 cycles a tile
 // without), tiles in registers and the base kept from the tile before (no second pass),
 // page numbers eight tiles ahead, queries copied asynchronously, output rows written
 // whole.  More polling (test_wait) or less (a suspend hint) both cost.
@@ -80,7 +81,7 @@ constexpr int kCapE4M3 = 14;     // ... and x moves before one reaches 2^15
 // ... and the bound (the tile's largest value scale times the row's largest weight, mostly of
 // another key) is at most this many binades above what it stands for: the largest starts at 2^-2
 // or more, where fp16's grid ends 2^-22 below it.  Where scales differ more, each weight is looked
-// at (the 32 requests below, with values e^(s n) n', n and n' normal, s = 0.3, 1 and 2: 165, 179 and
+// at (the 32 requests above, with values e^(s n) n', n and n' normal, s = 0.3, 1 and 2: 165, 179 and
 // 216 us; at 22 binades in place of 8 165, 173 and 173, with the small weights lost).
 constexpr int kWideE4M3 = 8;
 constexpr int kNoShift = -1000;  // no weight yet
@@ -1429,6 +1430,9 @@ dflash2_status launch_tc(const DeviceInfo &di, const Params &p, bool paged, int3
     // Few rows a request on average: the transposed kernel.  64 requests over 0 to 8191 keys,
     // head_dim 128, with 4, 16, 32, 48 and 60 rows take it 97, 100, 127, 165 and 212 us, and
     // this file's 155, 158, 165, 211 and 211 (head_dim 64, 48 and 60 rows: 155 and 196, 177 and 177).
+    // Empty requests count, since only the device knows them: beside 48 or 56 empty ones, 16
+    // requests of 128 rows over 4000 keys take it 234 us and this file's kernel 95, 8 of 256 rows
+    // 230 and 89, 8 of 64 rows 76 and 50.
     if (kv_format == DFLASH2_KV_E4M3 && (int64_t)p.total_q * p.group <= 48 * (int64_t)p.batch)
         return launch_few(di, p, st);
     if (kv_format == DFLASH2_KV_E4M3)

@@ -9,10 +9,10 @@
 // rows' loads in flight.  The row's largest magnitude is a shuffle over its lanes.
 // (A warp per two rows of any token, with its divisions for every row, was bound by
 // instructions: 51 us for 20011 tokens x 8 heads written as E4M3, 165 us for 100003
-// tokens read.)  A write's first rows are loaded beside its slot (29 us before).
-// Measured, 8 heads of 128, bf16 rows and an E4M3 cache: 20011 tokens written in 24 us,
-// 5.1 TB/s, and read back in 18; 100003 tokens read in 95 us, 6.5 TB/s; 512 tokens
-// written to a bf16 cache in 9 us, the call.
+// tokens read.)  A write's first rows are loaded beside its slot (24 us, 29 before).
+// Measured, 8 heads of 128, bf16 rows and an E4M3 cache: 20011 tokens written and read back
+// in 40 us, 6.1 TB/s; 100003 tokens read in 92 us, 6.7 TB/s; 512 tokens written to a bf16
+// cache in 9 us, the call.
 #include "kernels.h"
 
 namespace dflash2 {

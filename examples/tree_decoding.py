@@ -121,7 +121,7 @@ class Sequences:
     def keep(self, paths):
         """paths[b]: the accepted nodes, root first.  Their rows move to the
         sequence's next positions.  All are read before any is written, and a
-        row that is read back from codes is written as the same codes."""
+        row that is read back from codes and written again keeps its values."""
         src, dst = [], []
         for b, path in enumerate(paths):
             for i, node in enumerate(path):

@@ -588,8 +588,9 @@ typedef enum { DFLASH2_KV_NATIVE = 0, DFLASH2_KV_E4M3 = 1 } dflash2_kv_format;
  *
  * k, v      device, rows [kv_heads, head_dim] of token i at k + i * k_row_stride
  *           elements (v likewise), so slices of one projection are read in place.
- * slots     device int64 [n_tokens]; a negative slot skips the token.  Two
- *           tokens with one slot leave it with either token's row.
+ * slots     device int64 [n_tokens]; a negative slot skips the token.  Where
+ *           two tokens have one slot, what it holds is undefined (parts of
+ *           either row, and another's exponent).
  * k_cache, v_cache, k_exp, v_exp  as above, written.
  * Errors:   head_dim outside [1, 256], kv_heads < 1, page_size < 1, num_pages
  *           < 0, n_tokens < 0, n_tokens * kv_heads >= 2^30, a row stride below
@@ -612,8 +613,9 @@ dflash2_status dflash2_kv_cache_write(const void *k, const void *v, int64_t k_ro
 /*
  * Reads the rows at `slots` back: k_out, v_out device [n_tokens, kv_heads,
  * head_dim] in dtype (E4M3: c * 2^(byte - 127), exact in bf16 and fp32).  Read
- * and written again, E4M3 rows keep their values, so accepted tokens of a tree
- * are moved by a read and a write.  Arguments, errors and fast path as for
+ * and written again, E4M3 rows keep their values (codes and exponent may move
+ * by a power of two: 224 * 2^0 comes back as 448 * 2^-1), so accepted tokens of
+ * a tree are moved by a read and a write.  Arguments, errors and fast path as for
  * dflash2_kv_cache_write.
  * Device:   a negative slot gives zero rows; one at or above num_pages *
  *           page_size gives zero rows and sets DFLASH2_DEVERR_ID_RANGE.
@@ -667,13 +669,19 @@ dflash2_status dflash2_kv_cache_read(const void *k_cache, const void *v_cache,
  *   with the value codes, on a grid 2^-23 of the row's largest; more: with the
  *   codes widened to fp16, on a grid 2^-22 of it or finer).  Otherwise fp32 on
  *   CUDA cores.  Reduction orders are fixed, so results are deterministic.
+ *   The average counts empty requests (the host knows no others' rows): where
+ *   most are and the rest have many rows, a batch without them is two to three
+ *   times faster over an E4M3 cache.
  * Errors:    q_heads not a multiple of kv_heads, q_heads / kv_heads > 128,
- *            head_dim outside [1, 256], a size < 1 (batch, total_q: < 0),
- *            num_pages * kv_heads >= 2^31, max_pages * page_size > 2^31 - 4096,
- *            batch > 65536, total_q * q_heads >= 2^31, scale not finite, a
- *            null pointer -> INVALID_ARG; unknown dtype or kv_format ->
- *            UNSUPPORTED_DTYPE; a pointer not aligned to its element ->
- *            MISALIGNED.  total_q == 0 or batch == 0 queues nothing.
+ *            kv_heads > 65535, head_dim outside [1, 256], a size < 1 (batch,
+ *            total_q: < 0), q_row_stride < q_heads * head_dim, mask_words >
+ *            2^20 (with a mask), num_pages * kv_heads >= 2^31, max_pages *
+ *            page_size > 2^31 - 4096, batch > 65536, total_q * q_heads >= 2^31,
+ *            scale (times log2 e) not finite, a null pointer -> INVALID_ARG;
+ *            unknown dtype or kv_format -> UNSUPPORTED_DTYPE; a pointer not
+ *            aligned to its element -> MISALIGNED; a workspace that is NULL,
+ *            too small or not aligned -> WORKSPACE.  total_q == 0 or batch ==
+ *            0 queues nothing.
  * Device:    DFLASH2_DEVERR_ID_RANGE, with a defined result, for a cu_q that
  *            falls or leaves [0, total_q] (clamped), kv_lens outside
  *            [T, max_pages * page_size] (the request's rows see nothing), a
