@@ -141,6 +141,13 @@ dflash2_status launch_quant_rows_e4m3(const void *x, int32_t dtype, int64_t rows
 dflash2_status launch_quant_rows_nvfp4(const void *x, int32_t dtype, int64_t rows, int32_t cols,
                                        uint8_t *codes, uint8_t *scales, float *g, cudaStream_t st);
 
+// E4M3 block quantisation of rows (norm.cu): q [rows, cols] codes, scale [rows,
+// ceil(cols / 128)]; `check` refuses what the launch cannot take.
+dflash2_status check_quant_blocks(const void *x, int64_t stride, int32_t dtype, int64_t rows,
+                                  int32_t cols);
+dflash2_status launch_quant_blocks_e4m3(const void *x, int64_t stride, int32_t dtype, int64_t rows,
+                                        int32_t cols, uint8_t *q, float *scale, cudaStream_t st);
+
 // CTA pairs of one fused launch (every CTA resident at once) and their
 // epilogue warps, or 0 when the device cannot hold such a launch.  Host-side,
 // cached per device.

@@ -13,7 +13,7 @@
 // Measured, 8 heads of 128, bf16 rows and an E4M3 cache: 20011 tokens written and read back
 // in 40 us, 6.1 TB/s; 100003 tokens read in 92 us, 6.7 TB/s; 512 tokens written to a bf16
 // cache in 9 us, the call.
-#include "kernels.h"
+#include "rows.cuh"
 
 namespace dflash2 {
 namespace {
@@ -32,71 +32,6 @@ struct KvArgs {
     uint8_t *ke, *ve;
     int32_t *err;
 };
-
-// 8 values as they are (a native cache copies rows bit for bit, NaN payloads
-// included), and as fp32.
-template <typename T> struct Raw8 {
-    uint4 w[sizeof(T) / 2];
-};
-template <typename T> __device__ __forceinline__ Raw8<T> load_raw8(const T *p) {
-    Raw8<T> r;
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
-    return r;
-}
-template <typename T> __device__ __forceinline__ void store_raw8(T *p, const Raw8<T> &r) {
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4 *>(p)[i] = r.w[i];
-}
-__device__ __forceinline__ void as_floats(const Raw8<float> &r, float (&x)[8]) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        x[4 * i] = __uint_as_float(r.w[i].x), x[4 * i + 1] = __uint_as_float(r.w[i].y);
-        x[4 * i + 2] = __uint_as_float(r.w[i].z), x[4 * i + 3] = __uint_as_float(r.w[i].w);
-    }
-}
-__device__ __forceinline__ void as_floats(const Raw8<__nv_bfloat16> &r, float (&x)[8]) {
-    const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-}
-__device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
-    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&b);
-    }
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ void from_f32(float *p, float v) { *p = v; }
-__device__ __forceinline__ void from_f32(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
-
-__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
-
-// The smallest e in [kKvMinExp, kKvMaxExp] with amax <= 448 * 2^e: 448 = 1.75 * 2^8,
-// so e is amax's binade minus 8, one more when its significand exceeds 1.75.
-__device__ __forceinline__ int row_exponent(float amax) {
-    const uint32_t b = __float_as_uint(amax);
-    const int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-    return min(max(e, kKvMinExp), kKvMaxExp);
-}
-__device__ __forceinline__ uint8_t encode1(float x) {
-    return (uint8_t)__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
-}
-__device__ __forceinline__ float decode1(uint8_t c) {
-    const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)c, __NV_E4M3);
-    return __half2float(__half(h));
-}
 
 struct Row {
     int64_t token;
@@ -175,19 +110,9 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvArgs a) {
                 for (int o = kLanes / 2; o > 0; o >>= 1)
                     amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
                 const int e = row_exponent(amax);
-                const float s = pow2i(-e);
-                uint32_t c[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float *y = x + 4 * i;
-                    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0] * s, y[1] * s),
-                                                                 __NV_SATFINITE, __NV_E4M3);
-                    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2] * s, y[3] * s),
-                                                                 __NV_SATFINITE, __NV_E4M3);
-                    c[i] = lo | (hi << 16);
-                }
+                const uint2 c = encode8(x, pow2i(-e));
                 if (h < a.kv_heads) {
-                    *reinterpret_cast<uint2 *>((uint8_t *)cache + row * kDim + lane * 8) = make_uint2(c[0], c[1]);
+                    *reinterpret_cast<uint2 *>((uint8_t *)cache + row * kDim + lane * 8) = c;
                     if (lane == 0) exps[row] = (uint8_t)(e + 127);
                 }
             }
@@ -324,8 +249,6 @@ dflash2_status launch_kv(const KvArgs &a, bool aligned, cudaStream_t st) {
         launch_k(kv_read_scalar<T, kE4M3>, dim3(grid), dim3(kThreads), 0, st, a);
     return launch_status();
 }
-
-bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // The checks both entry points share; fills what is common.
 dflash2_status check_kv(KvArgs *a, const int64_t *slots, int64_t n_tokens, int32_t kv_heads,

@@ -1,0 +1,364 @@
+// The norms around a sublayer (attention, MLP) with its gate and residual:
+//
+//   norm:  out = x / sqrt(mean(x^2) + eps) * (w + offset)
+//   join:  h  = post ? rms(y) * (w_post + offset) : y
+//          r' = r + branch_scale * act(gate) * h
+//          out = rms(r') * (w_next + offset)          (if asked)
+//
+// and the E4M3 block quantisation of rows, alone or of `out` as it is made.  Every value
+// is read and written once: the row stays in registers between the two sums of squares,
+// which a join needs one after the other (three sums over r and h alone would do in one
+// pass, but the next norm would lose what cancels in r + h).  r' goes into the next norm
+// as computed in fp32, not as rounded for storage.
+//
+// HBM bounds them once the rows fill the GPU, a launch below that.  A thread holds
+// kChunks x 8 values; a row takes as many threads as it needs (a warp where kChunks x 256
+// values suffice), and the loads of y, r and the gate are all in flight at once.
+#include "rows.cuh"
+
+namespace dflash2 {
+namespace {
+
+enum { kGateNone = DFLASH2_GATE_NONE, kGateChannel = DFLASH2_GATE_CHANNEL,
+       kGateToken = DFLASH2_GATE_TOKEN, kGateFull = DFLASH2_GATE_FULL };
+
+struct NormArgs {
+    const void *x;  // residual stream (norm: the input)
+    const void *y, *w_post, *gate, *w_next;
+    int64_t x_stride, y_stride, gate_stride, r_stride;
+    int32_t gate_kind, gate_act;
+    float branch, w_off, eps;
+    int64_t rows;
+    int32_t hidden;
+    void *r_out, *out;
+    float *scale;   // E4M3 blocks if not NULL
+    bool code_vec;  // rows of codes are 8-byte aligned
+};
+
+template <typename T, bool kVec> struct Held {  // 8 values of a thread
+    Raw8<T> raw;
+    __device__ __forceinline__ void load(const T *p, int n) {
+        raw = Raw8<T>{};
+        if (n > 0) raw = load_raw8_written(p);
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const { as_floats(raw, x); }
+};
+template <typename T> struct Held<T, false> {
+    float v[8];
+    __device__ __forceinline__ void load(const T *p, int n) { load8_any(p, n, v); }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = v[i];
+    }
+};
+template <typename T, bool kVec> __device__ __forceinline__ void put8(T *p, int n, const float (&x)[8]) {
+    if constexpr (kVec) {
+        if (n > 0) store8(p, x);
+    } else {
+        store8_any(p, n, x);
+    }
+}
+
+__device__ __forceinline__ float gate_value(float g, int act) {
+    if (act == DFLASH2_GATE_SIGMOID) return __fdiv_rn(1.0f, 1.0f + expf(-g));
+    return act == DFLASH2_GATE_TANH ? tanhf(g) : g;
+}
+
+// The sum over a row's threads, the same in each (fixed order).  `red` is used by one
+// call of the row alone.
+template <bool kWarpRow> __device__ __forceinline__ float row_sum(float v, float *red) {
+    v = warp_sum(v);
+    if constexpr (!kWarpRow) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        if (lane == 0) red[warp] = v;
+        __syncthreads();
+        v = warp_sum(lane < (int)(blockDim.x >> 5) ? red[lane] : 0.0f);
+    }
+    return v;
+}
+
+// kThreads: a row's threads at most; 32 stands for a warp per row, 8 rows a block.
+template <typename TX, typename T, int kChunks, bool kVec, bool kJoin, int kThreads>
+__global__ void __launch_bounds__(kThreads == 32 ? 256 : kThreads) sublayer_kernel(const NormArgs a) {
+    constexpr bool kWarpRow = kThreads == 32;
+    __shared__ float red[2][32];
+    grid_dep_wait();
+    const int t = kWarpRow ? threadIdx.x & 31 : threadIdx.x;
+    const int per = kWarpRow ? 32 : blockDim.x;
+    const int64_t row = kWarpRow ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+    if (row >= a.rows) return;  // a whole warp or block
+    const int hidden = a.hidden;
+    const float inv_n = 1.0f / (float)hidden;
+
+    Held<TX, kVec> held[kChunks];
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+        const int col = (c * per + t) * 8;
+        held[c].load((const TX *)a.x + row * a.x_stride + col, hidden - col);
+    }
+    float r[kChunks][8];
+    float sum = 0.0f;
+    if constexpr (kJoin) {
+        Held<T, kVec> y[kChunks], g[kChunks];
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            const int col = (c * per + t) * 8;
+            y[c].load((const T *)a.y + row * a.y_stride + col, hidden - col);
+            if (a.gate_kind == kGateChannel || a.gate_kind == kGateFull)
+                g[c].load((const T *)a.gate + (a.gate_kind == kGateFull ? row * a.gate_stride : 0) + col, hidden - col);
+        }
+        const float token_gate =
+            a.gate_kind == kGateToken
+                ? gate_value(to_f32(((const T *)a.gate)[row * a.gate_stride]), a.gate_act) : 1.0f;
+        float y_rms = 1.0f;
+        if (a.w_post) {
+            float s = 0.0f;
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                float v[8];
+                y[c].get(v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s += v[i] * v[i];
+            }
+            y_rms = __frsqrt_rn(row_sum<kWarpRow>(s, red[0]) * inv_n + a.eps);
+        }
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            const int col = (c * per + t) * 8;
+            float h[8], v[8];
+            y[c].get(h);
+            if (a.w_post) {
+                Held<T, kVec> w;
+                w.load((const T *)a.w_post + col, hidden - col);
+                w.get(v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) h[i] = h[i] * y_rms * (v[i] + a.w_off);
+            }
+            if (a.gate_kind == kGateChannel || a.gate_kind == kGateFull) {
+                g[c].get(v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) h[i] *= gate_value(v[i], a.gate_act);
+            } else if (a.gate_kind == kGateToken) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) h[i] *= token_gate;
+            }
+            held[c].get(r[c]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r[c][i] += a.branch * h[i];
+            put8<TX, kVec>((TX *)a.r_out + row * a.r_stride + col, hidden - col, r[c]);
+        }
+        if (!a.w_next) return;
+    } else {
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) held[c].get(r[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (kVec || !kJoin || (c * per + t) * 8 + i < hidden) sum += r[c][i] * r[c][i];
+    const float rms = __frsqrt_rn(row_sum<kWarpRow>(sum, red[1]) * inv_n + a.eps);
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+        const int col = (c * per + t) * 8;
+        Held<T, kVec> w;
+        float v[8];
+        w.load((const T *)a.w_next + col, hidden - col);
+        w.get(v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = r[c][i] * rms * (v[i] + a.w_off);
+        if (!a.scale) {
+            put8<T, kVec>((T *)a.out + row * hidden + col, hidden - col, v);
+            continue;
+        }
+        if (!kVec)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = col + i < hidden ? v[i] : 0.0f;
+        float s;
+        const uint2 codes = quantise_block(v, &s);
+        if (col >= hidden) continue;
+        store_codes((uint8_t *)a.out + row * hidden + col, hidden - col, a.code_vec, codes);
+        if (col % kQuantBlock == 0)
+            a.scale[row * ((hidden + kQuantBlock - 1) / kQuantBlock) + col / kQuantBlock] = s;
+    }
+}
+
+template <typename TX, typename T, bool kVec, bool kJoin>
+dflash2_status launch_vec(const NormArgs &a, cudaStream_t st) {
+    constexpr int kChunks = 4;
+    const int threads = ((a.hidden + 8 * kChunks - 1) / (8 * kChunks) + 31) / 32 * 32;
+    if (threads == 32)
+        launch_k(sublayer_kernel<TX, T, kChunks, kVec, kJoin, 32>, dim3((unsigned)((a.rows + 7) / 8)), dim3(256), 0,
+                 st, a);
+    else if (threads <= 256)
+        launch_k(sublayer_kernel<TX, T, kChunks, kVec, kJoin, 256>, dim3((unsigned)a.rows), dim3(threads), 0, st, a);
+    else
+        launch_k(sublayer_kernel<TX, T, kChunks, kVec, kJoin, 1024>, dim3((unsigned)a.rows), dim3(threads), 0, st, a);
+    return launch_status();
+}
+
+template <typename TX, typename T, bool kJoin>
+dflash2_status launch_norm(const NormArgs &a, bool vec, cudaStream_t st) {
+    return vec ? launch_vec<TX, T, true, kJoin>(a, st) : launch_vec<TX, T, false, kJoin>(a, st);
+}
+
+template <bool kJoin>
+dflash2_status dispatch_norm(NormArgs a, int32_t x_dtype, int32_t dtype, bool vec, cudaStream_t st) {
+    a.code_vec = a.scale && a.hidden % 8 == 0 && aligned_to(a.out, 8);
+    if (x_dtype == DFLASH2_F32)
+        return dtype == DFLASH2_F32 ? launch_norm<float, float, kJoin>(a, vec, st)
+                                    : launch_norm<float, __nv_bfloat16, kJoin>(a, vec, st);
+    return dtype == DFLASH2_F32 ? launch_norm<__nv_bfloat16, float, kJoin>(a, vec, st)
+                                : launch_norm<__nv_bfloat16, __nv_bfloat16, kJoin>(a, vec, st);
+}
+
+bool known(int32_t dtype) { return dtype == DFLASH2_F32 || dtype == DFLASH2_BF16; }
+uintptr_t size_of(int32_t dtype) { return dtype == DFLASH2_F32 ? 4 : 2; }
+constexpr int64_t kMaxStride = 1ll << 32;  // row strides: 2^31 rows of them stay in 64 bits
+
+dflash2_status check_norm(const NormArgs &a, int32_t x_dtype, int32_t dtype) {
+    if (!known(x_dtype) || !known(dtype)) return DFLASH2_ERR_UNSUPPORTED_DTYPE;
+    if (a.rows < 0 || a.rows > INT32_MAX || a.hidden < 1 || a.hidden > 32768 || !(a.eps >= 0.0f) ||
+        !(a.eps <= FLT_MAX) || !(fabsf(a.w_off) <= FLT_MAX) || a.x_stride < a.hidden || a.x_stride > kMaxStride)
+        return DFLASH2_ERR_INVALID_ARG;
+    return DFLASH2_OK;
+}
+// Rows in steps of 8 values: 16-byte aligned starts of whole steps.
+bool vec_rows(const void *p, int64_t stride, uintptr_t el) {
+    return aligned_to(p, 16) && stride * (int64_t)el % 16 == 0;
+}
+
+// ---- block quantisation of rows ----------------------------------------------
+constexpr int kQuantThreads = 256;
+
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kQuantThreads)
+    quantise_rows_kernel(const T *x, int64_t stride, int64_t rows, int32_t cols, uint8_t *q, float *scale,
+                         bool code_vec) {
+    grid_dep_wait();
+    const int nb = (cols + kQuantBlock - 1) / kQuantBlock;
+    const int64_t b = ((int64_t)blockIdx.x * kQuantThreads + threadIdx.x) / kQuantLanes;
+    const bool live = b < rows * nb;
+    const int64_t row = live ? b / nb : 0;
+    const int block = live ? (int)(b - row * nb) : 0, lane = threadIdx.x % kQuantLanes;
+    const int col = block * kQuantBlock + lane * 8, n = live ? cols - col : 0;
+    Held<T, kVec> h;
+    float v[8], s;
+    h.load(x + row * stride + col, n);
+    h.get(v);
+    const uint2 codes = quantise_block(v, &s);
+    if (n <= 0) return;
+    store_codes(q + row * cols + col, n, code_vec, codes);
+    if (lane == 0) scale[row * nb + block] = s;
+}
+
+}  // namespace
+
+dflash2_status launch_quant_blocks_e4m3(const void *x, int64_t stride, int32_t dtype, int64_t rows, int32_t cols,
+                                        uint8_t *q, float *scale, cudaStream_t st) {
+    const int64_t blocks = rows * ((cols + kQuantBlock - 1) / kQuantBlock);
+    const int64_t grid = (blocks * kQuantLanes + kQuantThreads - 1) / kQuantThreads;
+    const bool vec = cols % 8 == 0 && vec_rows(x, stride, size_of(dtype));
+    const bool code_vec = cols % 8 == 0 && aligned_to(q, 8);
+    const dim3 g((unsigned)grid), t(kQuantThreads);
+    using B = __nv_bfloat16;
+    if (dtype == DFLASH2_F32) {
+        const float *p = (const float *)x;
+        if (vec)
+            launch_k(quantise_rows_kernel<float, true>, g, t, 0, st, p, stride, rows, cols, q, scale, code_vec);
+        else
+            launch_k(quantise_rows_kernel<float, false>, g, t, 0, st, p, stride, rows, cols, q, scale, code_vec);
+    } else {
+        const B *p = (const B *)x;
+        if (vec)
+            launch_k(quantise_rows_kernel<B, true>, g, t, 0, st, p, stride, rows, cols, q, scale, code_vec);
+        else
+            launch_k(quantise_rows_kernel<B, false>, g, t, 0, st, p, stride, rows, cols, q, scale, code_vec);
+    }
+    return launch_status();
+}
+
+dflash2_status check_quant_blocks(const void *x, int64_t stride, int32_t dtype, int64_t rows, int32_t cols) {
+    if (!known(dtype)) return DFLASH2_ERR_UNSUPPORTED_DTYPE;
+    if (rows < 0 || cols < 1 || cols > 1 << 30 || stride < cols || stride > kMaxStride || rows > INT32_MAX ||
+        (int64_t)rows * ((cols + kQuantBlock - 1) / kQuantBlock) > 1ll << 34)
+        return DFLASH2_ERR_INVALID_ARG;
+    if (rows == 0) return DFLASH2_OK;
+    if (!x) return DFLASH2_ERR_INVALID_ARG;
+    return aligned_to(x, size_of(dtype)) ? DFLASH2_OK : DFLASH2_ERR_MISALIGNED;
+}
+
+}  // namespace dflash2
+
+using namespace dflash2;
+
+extern "C" dflash2_status dflash2_quantize_blocks_e4m3(const void *x, int64_t x_row_stride, int64_t rows, int32_t cols,
+                                                       int32_t dtype, uint8_t *q, float *scale, void *stream) {
+    dflash2_status st = check_quant_blocks(x, x_row_stride, dtype, rows, cols);
+    if (st != DFLASH2_OK || rows == 0) return st;
+    if (!q || !scale) return DFLASH2_ERR_INVALID_ARG;
+    if (!aligned_to(scale, 4)) return DFLASH2_ERR_MISALIGNED;
+    DeviceInfo di;
+    st = current_device(&di);
+    if (st != DFLASH2_OK) return st;
+    return launch_quant_blocks_e4m3(x, x_row_stride, dtype, rows, cols, q, scale, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" dflash2_status dflash2_sublayer_norm(const void *x, int64_t x_row_stride, int32_t x_dtype,
+                                                const void *weight, float weight_offset, float eps, int64_t rows,
+                                                int32_t hidden, int32_t dtype, void *out, float *scale, void *stream) {
+    NormArgs a{};
+    a.x = x, a.x_stride = x_row_stride, a.w_next = weight, a.w_off = weight_offset, a.eps = eps;
+    a.rows = rows, a.hidden = hidden, a.out = out, a.scale = scale;
+    dflash2_status st = check_norm(a, x_dtype, dtype);
+    if (st != DFLASH2_OK || rows == 0) return st;
+    if (!x || !weight || !out) return DFLASH2_ERR_INVALID_ARG;
+    const uintptr_t xe = size_of(x_dtype), el = size_of(dtype);
+    if (!aligned_to(x, xe) || !aligned_to(weight, el) || !aligned_to(out, scale ? 1 : el) || !aligned_to(scale, 4))
+        return DFLASH2_ERR_MISALIGNED;
+    DeviceInfo di;
+    st = current_device(&di);
+    if (st != DFLASH2_OK) return st;
+    const bool vec = hidden % 8 == 0 && vec_rows(x, x_row_stride, xe) && aligned_to(weight, 16) &&
+                     (scale || aligned_to(out, 16));
+    return dispatch_norm<false>(a, x_dtype, dtype, vec, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" dflash2_status dflash2_sublayer_join(
+    const void *residual, int64_t residual_row_stride, int32_t residual_dtype, const void *y, int64_t y_row_stride,
+    const void *post_weight, const void *gate, int32_t gate_kind, int64_t gate_row_stride, int32_t gate_act,
+    float branch_scale, const void *next_weight, float weight_offset, float eps, int64_t rows, int32_t hidden,
+    int32_t dtype, void *residual_out, int64_t residual_out_row_stride, void *out, float *scale, void *stream) {
+    NormArgs a{};
+    a.x = residual, a.x_stride = residual_row_stride, a.y = y, a.y_stride = y_row_stride;
+    a.w_post = post_weight, a.gate = gate, a.gate_kind = gate_kind, a.gate_act = gate_act;
+    a.gate_stride = gate_row_stride, a.branch = branch_scale, a.w_next = next_weight, a.w_off = weight_offset;
+    a.eps = eps, a.rows = rows, a.hidden = hidden, a.r_out = residual_out, a.r_stride = residual_out_row_stride;
+    a.out = out, a.scale = scale;
+    dflash2_status st = check_norm(a, residual_dtype, dtype);
+    if (st != DFLASH2_OK) return st;
+    if (gate_kind < kGateNone || gate_kind > kGateFull || gate_act < DFLASH2_GATE_IDENTITY ||
+        gate_act > DFLASH2_GATE_TANH || !(fabsf(branch_scale) <= FLT_MAX) || y_row_stride < hidden ||
+        y_row_stride > kMaxStride || residual_out_row_stride < hidden || residual_out_row_stride > kMaxStride ||
+        (gate_kind == kGateToken && (gate_row_stride < 1 || gate_row_stride > kMaxStride)) ||
+        (gate_kind == kGateFull && (gate_row_stride < hidden || gate_row_stride > kMaxStride)))
+        return DFLASH2_ERR_INVALID_ARG;
+    if (rows == 0) return DFLASH2_OK;
+    if (!residual || !y || !residual_out || (gate_kind != kGateNone && !gate) || (next_weight && !out) ||
+        (!next_weight && (out || scale)) || (residual_out == residual && residual_out_row_stride != residual_row_stride))
+        return DFLASH2_ERR_INVALID_ARG;
+    const uintptr_t xe = size_of(residual_dtype), el = size_of(dtype);
+    if (!aligned_to(residual, xe) || !aligned_to(residual_out, xe) || !aligned_to(y, el) ||
+        !aligned_to(post_weight, el) || !aligned_to(next_weight, el) || (gate_kind != kGateNone && !aligned_to(gate, el)) ||
+        !aligned_to(out, scale ? 1 : el) || !aligned_to(scale, 4))
+        return DFLASH2_ERR_MISALIGNED;
+    DeviceInfo di;
+    st = current_device(&di);
+    if (st != DFLASH2_OK) return st;
+    const bool gate_vec = gate_kind == kGateChannel  ? aligned_to(gate, 16)
+                          : gate_kind == kGateFull ? vec_rows(gate, gate_row_stride, el) : true;
+    const bool vec = hidden % 8 == 0 && vec_rows(residual, residual_row_stride, xe) &&
+                     vec_rows(residual_out, residual_out_row_stride, xe) && vec_rows(y, y_row_stride, el) && gate_vec &&
+                     aligned_to(post_weight, 16) && aligned_to(next_weight, 16) && (scale || aligned_to(out, 16));
+    return dispatch_norm<true>(a, residual_dtype, dtype, vec, static_cast<cudaStream_t>(stream));
+}

@@ -1,0 +1,375 @@
+// Rotary positions with several axes, of queries and keys, and the write of the rotated
+// keys and the values into the paged cache.
+//
+//   angle(i, j) = positions[axis[j], i] * f[j]       token i, pair j of rotary_dim / 2
+//   (a, b) -> magnitude * (a cos - b sin, b cos + a sin)
+//   pairs (j, j + rotary_dim / 2), or adjacent (2j, 2j + 1); the rest of a row is copied
+//
+// Frequencies are 64-bit fractions of a turn, so position * frequency modulo 2^64 is the
+// angle modulo a turn: exact for every 64-bit position, where an fp32 product has lost
+// 0.06 rad at position 10^6, and one integer multiplication.  The signed fraction goes to
+// sincospi in fp32.
+//
+// Every value moves once: HBM bounds it, a launch where tokens are few.  A lane holds the
+// same two steps of 8 values of every row, chosen so that both halves of its pairs are
+// its own (for halves: step u and u + rotary_dim / 16), so sines and cosines are read from
+// shared memory once per token and the rows need no exchange between lanes but the E4M3
+// maximum.  A warp computes a token's sines and cosines for up to kUnroll rows per lane
+// group, all of whose loads are in flight together.
+#include "rows.cuh"
+
+namespace dflash2 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxPairs = 128;
+
+struct RotaryArgs {
+    const void *q, *k, *v;
+    void *qo, *ko;
+    int64_t q_stride, k_stride, v_stride, qo_stride, ko_stride;
+    const int64_t *positions;  // [axes, n_tokens]
+    const uint64_t *freq;
+    const uint8_t *axis;
+    int32_t axes, pairs;       // pairs = rotary_dim / 2
+    int32_t adjacent;
+    float magnitude;
+    int64_t n_tokens;
+    int32_t q_rows, k_rows, v_rows;  // heads of each, 0 if absent
+    int32_t head_dim, kv_heads, page_size;
+    const int64_t *slots;      // NULL: no cache
+    int64_t n_slots;
+    void *kc, *vc;
+    uint8_t *ke, *ve;
+    int32_t parts;             // warps a token's rows are split over
+    int32_t *err;
+};
+
+// Sines and cosines of a token's pairs into the warp's table.
+__device__ __forceinline__ void token_angles(const RotaryArgs &a, int64_t token, bool report, float2 *cs) {
+    const int lane = threadIdx.x & 31;
+    for (int j = lane; j < a.pairs; j += 32) {
+        const int axis = __ldg(a.axis + j);
+        uint64_t phase = 0;
+        if (axis < a.axes)
+            phase = (uint64_t)__ldg(a.positions + axis * a.n_tokens + token) * __ldg(a.freq + j);
+        else if (report && a.err)
+            atomicOr(a.err, DFLASH2_DEVERR_ID_RANGE);
+        float s, c;
+        sincospif(__ll2float_rn((int64_t)phase) * 0x1p-63f, &s, &c);
+        cs[j] = make_float2(c * a.magnitude, s * a.magnitude);
+    }
+    __syncwarp();
+}
+
+// Head 0's row of a token in the cache arrays, or -1.
+__device__ __forceinline__ int64_t cache_row(const RotaryArgs &a, int64_t token, bool report) {
+    if (!a.slots) return -1;
+    const int64_t slot = __ldg(a.slots + token);
+    if (slot >= a.n_slots) {
+        if (report && a.err) atomicOr(a.err, DFLASH2_DEVERR_ID_RANGE);
+        return -1;
+    }
+    if (slot < 0) return -1;
+    const int64_t page = slot / a.page_size;
+    return page * a.kv_heads * a.page_size + (slot - page * a.page_size);
+}
+
+// kLanes lanes (a power of two) hold a row of up to 16 kLanes values.
+template <typename T, bool kE4M3, int kLanes, int kUnroll>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
+    constexpr int kRows = 32 / kLanes;
+    __shared__ float2 table[kWarps][kMaxPairs];
+    grid_dep_wait();
+    const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int64_t token = w / a.parts;
+    if (token >= a.n_tokens) return;
+    const int part = (int)(w - token * a.parts);
+    const int lane = threadIdx.x % kLanes, sub = (threadIdx.x & 31) / kLanes;
+    const int total = a.q_rows + a.k_rows + a.v_rows, d = a.head_dim;
+    const int first = part * kRows * kUnroll;
+
+    // this lane's two steps, and whether each is turned
+    const int steps = d / 8, turned = a.pairs / 4;
+    int s0, s1;
+    if (a.adjacent || lane >= turned / 2) {
+        s0 = 2 * lane, s1 = s0 + 1;
+    } else {
+        s0 = lane, s1 = lane + turned / 2;
+    }
+    const bool on0 = s0 < steps, on1 = s1 < steps;
+
+    Raw8<T> raw[kUnroll][2];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+        int r = first + u * kRows + sub;
+        raw[u][0] = raw[u][1] = Raw8<T>{};
+        if (r >= total) continue;
+        const T *p;
+        if (r < a.q_rows)
+            p = (const T *)a.q + token * a.q_stride + (int64_t)r * d;
+        else if ((r -= a.q_rows) < a.k_rows)
+            p = (const T *)a.k + token * a.k_stride + (int64_t)r * d;
+        else
+            p = (const T *)a.v + token * a.v_stride + (int64_t)(r - a.k_rows) * d;
+        if (on0) raw[u][0] = load_raw8_written(p + s0 * 8);
+        if (on1) raw[u][1] = load_raw8_written(p + s1 * 8);
+    }
+    const bool reports = part == 0 && (threadIdx.x & 31) == 0;
+    const int64_t at = cache_row(a, token, reports);
+    float2 *cs = table[threadIdx.x >> 5];
+    token_angles(a, token, part == 0, cs);
+    float co[8], si[8];  // halves: of the 8 pairs; adjacent: of the 4 of each step
+    const bool turn0 = s0 < turned, turn1 = s1 < turned;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int j = a.adjacent ? (i < 4 ? 4 * s0 + i : 4 * s1 + i - 4) : 8 * s0 + i;
+        const float2 x = j < a.pairs ? cs[j] : make_float2(1.0f, 0.0f);
+        co[i] = x.x, si[i] = x.y;
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+        if (first + u * kRows >= total) break;  // the whole warp
+        const int r = first + u * kRows + sub;
+        const bool values = r >= a.q_rows + a.k_rows, key = !values && r >= a.q_rows;
+        float x[8], y[8];
+        as_floats(raw[u][0], x);
+        as_floats(raw[u][1], y);
+        if (!values) {
+            if (a.adjacent) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float p = x[2 * i], o = x[2 * i + 1], p1 = y[2 * i], o1 = y[2 * i + 1];
+                    if (turn0) {
+                        x[2 * i] = p * co[i] - o * si[i];
+                        x[2 * i + 1] = o * co[i] + p * si[i];
+                    }
+                    if (turn1) {
+                        y[2 * i] = p1 * co[4 + i] - o1 * si[4 + i];
+                        y[2 * i + 1] = o1 * co[4 + i] + p1 * si[4 + i];
+                    }
+                }
+            } else if (turn0) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float p = x[i], o = y[i];
+                    x[i] = p * co[i] - o * si[i];
+                    y[i] = o * co[i] + p * si[i];
+                }
+            }
+        }
+        const bool live = r < total;
+        const int head = values ? r - a.q_rows - a.k_rows : key ? r - a.q_rows : r;
+        T *dst = nullptr;
+        if (live && !values) {
+            if (!key)
+                dst = (T *)a.qo + token * a.qo_stride + (int64_t)head * d;
+            else if (a.ko)
+                dst = (T *)a.ko + token * a.ko_stride + (int64_t)head * d;
+        }
+        if (dst) {
+            if (on0) store8(dst + s0 * 8, x);
+            if (on1) store8(dst + s1 * 8, y);
+        }
+        const bool held = live && (key || values) && at >= 0;
+        const int64_t row = at + (int64_t)head * a.page_size;
+        if constexpr (kE4M3) {
+            float amax = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(x[i]), fabsf(y[i])));
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+            if (!held) continue;
+            const int e = row_exponent(amax);
+            uint8_t *c = (uint8_t *)(values ? a.vc : a.kc) + row * d;
+            if (on0) *reinterpret_cast<uint2 *>(c + s0 * 8) = encode8(x, pow2i(-e));
+            if (on1) *reinterpret_cast<uint2 *>(c + s1 * 8) = encode8(y, pow2i(-e));
+            if (lane == 0) (values ? a.ve : a.ke)[row] = (uint8_t)(e + 127);
+        } else if (held) {
+            T *c = (T *)(values ? a.vc : a.kc) + row * d;
+            if (values) {  // a value row keeps its bits
+                if (on0) store_raw8(c + s0 * 8, raw[u][0]);
+                if (on1) store_raw8(c + s1 * 8, raw[u][1]);
+            } else {
+                if (on0) store8(c + s0 * 8, x);
+                if (on1) store8(c + s1 * 8, y);
+            }
+        }
+    }
+}
+
+// Any head_dim up to 256, rotary_dim and alignment: a warp per kScalarRows rows of a token,
+// a value per lane and step.  All of a row is read before any of it is written, so calls
+// in place are safe here too.
+constexpr int kScalarRows = 4;
+
+template <typename T, bool kE4M3>
+__global__ void __launch_bounds__(kThreads) rotary_scalar(const RotaryArgs a) {
+    __shared__ float2 table[kWarps][kMaxPairs];
+    grid_dep_wait();
+    const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int64_t token = w / a.parts;
+    if (token >= a.n_tokens) return;
+    const int part = (int)(w - token * a.parts), lane = threadIdx.x & 31;
+    const int total = a.q_rows + a.k_rows + a.v_rows, d = a.head_dim;
+    const int64_t at = cache_row(a, token, part == 0 && lane == 0);
+    float2 *cs = table[threadIdx.x >> 5];
+    token_angles(a, token, part == 0, cs);
+    for (int r = part * kScalarRows; r < min(total, (part + 1) * kScalarRows); ++r) {
+        const bool values = r >= a.q_rows + a.k_rows, key = !values && r >= a.q_rows;
+        const int head = values ? r - a.q_rows - a.k_rows : key ? r - a.q_rows : r;
+        const T *src = (values ? (const T *)a.v + token * a.v_stride
+                               : key ? (const T *)a.k + token * a.k_stride : (const T *)a.q + token * a.q_stride) +
+                       (int64_t)head * d;
+        float x[8], amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int j = lane + 32 * i;
+            x[i] = 0.0f;
+            if (j >= d) continue;
+            x[i] = to_f32(src[j]);
+            if (!values && j < 2 * a.pairs) {
+                const bool second = a.adjacent ? j & 1 : j >= a.pairs;
+                const int other = a.adjacent ? j ^ 1 : second ? j - a.pairs : j + a.pairs;
+                const float2 t = cs[a.adjacent ? j >> 1 : second ? j - a.pairs : j];
+                const float o = to_f32(src[other]);
+                x[i] = second ? x[i] * t.x + o * t.y : x[i] * t.x - o * t.y;
+            }
+            amax = fmaxf(amax, fabsf(x[i]));
+        }
+        __syncwarp();
+        T *dst = values ? nullptr : key ? (T *)a.ko + token * a.ko_stride : (T *)a.qo + token * a.qo_stride;
+        if (key && !a.ko) dst = nullptr;
+        const bool held = (key || values) && at >= 0;
+        const int64_t row = at + (int64_t)head * a.page_size;
+        int e = 0;
+        if constexpr (kE4M3) {
+            e = row_exponent(warp_max(amax));
+            if (held && lane == 0) (values ? a.ve : a.ke)[row] = (uint8_t)(e + 127);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int j = lane + 32 * i;
+            if (j >= d) continue;
+            if (dst) from_f32(dst + (int64_t)head * d + j, x[i]);
+            if (!held) continue;
+            if constexpr (kE4M3)
+                ((uint8_t *)(values ? a.vc : a.kc))[row * d + j] = encode1(x[i] * pow2i(-e));
+            else if (values)
+                ((T *)a.vc)[row * d + j] = src[j];
+            else
+                from_f32((T *)a.kc + row * d + j, x[i]);
+        }
+    }
+}
+
+template <typename T, bool kE4M3, int kLanes, int kUnroll>
+void launch_unroll(RotaryArgs a, cudaStream_t st) {
+    constexpr int rows = 32 / kLanes * kUnroll;
+    a.parts = (a.q_rows + a.k_rows + a.v_rows + rows - 1) / rows;
+    const int64_t warps = a.n_tokens * a.parts;
+    launch_k(rotary_kernel<T, kE4M3, kLanes, kUnroll>, dim3((unsigned)((warps + kWarps - 1) / kWarps)), dim3(kThreads),
+             0, st, a);
+}
+
+template <typename T, bool kE4M3>
+dflash2_status launch_rotary(RotaryArgs a, bool vec, cudaStream_t st) {
+    if (!vec) {
+        a.parts = (a.q_rows + a.k_rows + a.v_rows + kScalarRows - 1) / kScalarRows;
+        const int64_t warps = a.n_tokens * a.parts;
+        launch_k(rotary_scalar<T, kE4M3>, dim3((unsigned)((warps + kWarps - 1) / kWarps)), dim3(kThreads), 0, st, a);
+    } else if (a.head_dim <= 64) {
+        launch_unroll<T, kE4M3, 4, 4>(a, st);
+    } else if (a.head_dim <= 128) {
+        launch_unroll<T, kE4M3, 8, 4>(a, st);
+    } else {
+        launch_unroll<T, kE4M3, 16, 4>(a, st);
+    }
+    return launch_status();
+}
+
+dflash2_status run_rotary(RotaryArgs a, int32_t dtype, int32_t kv_format, int32_t rotary_dim, bool cached, void *stream) {
+    if (dtype != DFLASH2_F32 && dtype != DFLASH2_BF16) return DFLASH2_ERR_UNSUPPORTED_DTYPE;
+    if (kv_format != DFLASH2_KV_NATIVE && kv_format != DFLASH2_KV_E4M3) return DFLASH2_ERR_UNSUPPORTED_DTYPE;
+    const int64_t total = (int64_t)a.q_rows + a.k_rows + a.v_rows;
+    const int64_t qw = (int64_t)a.q_rows * a.head_dim, kw = (int64_t)a.k_rows * a.head_dim;
+    constexpr int64_t kMaxStride = 1ll << 32;
+    const auto bad = [&](int64_t stride, int64_t width) { return stride < width || stride > kMaxStride; };
+    if (a.head_dim < 1 || a.head_dim > 256 || rotary_dim < 2 || rotary_dim > a.head_dim || rotary_dim % 2 != 0 ||
+        a.axes < 1 || a.axes > 255 || a.adjacent < 0 || a.adjacent > 1 || !(fabsf(a.magnitude) <= FLT_MAX) ||
+        a.n_tokens < 0 || a.q_rows < 0 || a.k_rows < 0 || (cached && a.k_rows < 1) || total < 1 ||
+        total > (1 << 16) || a.n_tokens > INT32_MAX / total || (a.q_rows && (bad(a.q_stride, qw) || bad(a.qo_stride, qw))) ||
+        (a.k_rows && (bad(a.k_stride, kw) || (a.ko && bad(a.ko_stride, kw)))) || (cached && bad(a.v_stride, kw)))
+        return DFLASH2_ERR_INVALID_ARG;
+    const int64_t num_pages = a.n_slots;  // turned into slots below
+    if (cached && (a.page_size < 1 || num_pages < 0 || num_pages > (INT64_MAX >> 9) / a.page_size / a.kv_heads))
+        return DFLASH2_ERR_INVALID_ARG;
+    if (a.n_tokens == 0) return DFLASH2_OK;
+    const bool q8 = kv_format == DFLASH2_KV_E4M3;
+    if (!a.positions || !a.freq || !a.axis || (a.q_rows && (!a.q || !a.qo)) || (a.k_rows && !a.k) ||
+        (!cached && a.k_rows && !a.ko) ||
+        (cached && (!a.v || !a.slots || !a.kc || !a.vc || (q8 && (!a.ke || !a.ve)))) ||
+        (a.q == a.qo && a.q_rows && a.q_stride != a.qo_stride) || (a.k_rows && a.k == a.ko && a.k_stride != a.ko_stride))
+        return DFLASH2_ERR_INVALID_ARG;
+    const uintptr_t el = dtype == DFLASH2_F32 ? 4 : 2;
+    if ((a.q_rows && (!aligned_to(a.q, el) || !aligned_to(a.qo, el))) || (a.k_rows && !aligned_to(a.k, el)) ||
+        !aligned_to(a.ko, el) || !aligned_to(a.positions, 8) || !aligned_to(a.freq, 8) || !aligned_to(a.err, 4) ||
+        (cached && (!aligned_to(a.v, el) || !aligned_to(a.slots, 8) ||
+                    (!q8 && (!aligned_to(a.kc, el) || !aligned_to(a.vc, el))))))
+        return DFLASH2_ERR_MISALIGNED;
+    DeviceInfo di;
+    const dflash2_status st = current_device(&di);
+    if (st != DFLASH2_OK) return st;
+    a.n_slots = cached ? num_pages * a.page_size : 0;
+    // steps of 8 values: aligned rows, and pairs whose halves both begin at a step
+    const auto rows_vec = [&](const void *p, int64_t stride) { return aligned_to(p, 16) && stride * (int64_t)el % 16 == 0; };
+    const uintptr_t kept = q8 ? 8 : 16;
+    bool vec = a.head_dim % 8 == 0 && rotary_dim % (a.adjacent ? 8 : 16) == 0;
+    if (a.q_rows) vec = vec && rows_vec(a.q, a.q_stride) && rows_vec(a.qo, a.qo_stride);
+    if (a.k_rows) vec = vec && rows_vec(a.k, a.k_stride) && (!a.ko || rows_vec(a.ko, a.ko_stride));
+    if (cached) vec = vec && rows_vec(a.v, a.v_stride) && aligned_to(a.kc, kept) && aligned_to(a.vc, kept);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    using B = __nv_bfloat16;
+    if (cached && q8)
+        return dtype == DFLASH2_F32 ? launch_rotary<float, true>(a, vec, s) : launch_rotary<B, true>(a, vec, s);
+    return dtype == DFLASH2_F32 ? launch_rotary<float, false>(a, vec, s) : launch_rotary<B, false>(a, vec, s);
+}
+
+}  // namespace
+}  // namespace dflash2
+
+using namespace dflash2;
+
+extern "C" dflash2_status dflash2_rotary(const void *q, int64_t q_row_stride, const void *k, int64_t k_row_stride,
+                                         const int64_t *positions, int32_t axes, const uint64_t *freq,
+                                         const uint8_t *axis, int32_t rotary_dim, int32_t adjacent, float magnitude,
+                                         int64_t n_tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                         int32_t dtype, void *q_out, int64_t q_out_row_stride, void *k_out,
+                                         int64_t k_out_row_stride, int32_t *err_word, void *stream) {
+    RotaryArgs a{};
+    a.q = q, a.q_stride = q_row_stride, a.k = k, a.k_stride = k_row_stride;
+    a.positions = positions, a.axes = axes, a.freq = freq, a.axis = axis, a.pairs = rotary_dim / 2;
+    a.adjacent = adjacent, a.magnitude = magnitude, a.n_tokens = n_tokens;
+    a.q_rows = q_heads, a.k_rows = kv_heads, a.head_dim = head_dim, a.kv_heads = kv_heads;
+    a.qo = q_out, a.qo_stride = q_out_row_stride, a.ko = k_out, a.ko_stride = k_out_row_stride, a.err = err_word;
+    return run_rotary(a, dtype, DFLASH2_KV_NATIVE, rotary_dim, false, stream);
+}
+
+extern "C" dflash2_status dflash2_rotary_kv_write(
+    const void *q, int64_t q_row_stride, const void *k, int64_t k_row_stride, const void *v, int64_t v_row_stride,
+    const int64_t *positions, int32_t axes, const uint64_t *freq, const uint8_t *axis, int32_t rotary_dim,
+    int32_t adjacent, float magnitude, const int64_t *slots, int64_t n_tokens, int32_t q_heads, int32_t kv_heads,
+    int32_t head_dim, int32_t page_size, int64_t num_pages, int32_t dtype, int32_t kv_format, void *q_out,
+    int64_t q_out_row_stride, void *k_out, int64_t k_out_row_stride, void *k_cache, void *v_cache, uint8_t *k_exp,
+    uint8_t *v_exp, int32_t *err_word, void *stream) {
+    RotaryArgs a{};
+    a.q = q, a.q_stride = q_row_stride, a.k = k, a.k_stride = k_row_stride, a.v = v, a.v_stride = v_row_stride;
+    a.positions = positions, a.axes = axes, a.freq = freq, a.axis = axis, a.pairs = rotary_dim / 2;
+    a.adjacent = adjacent, a.magnitude = magnitude, a.slots = slots, a.n_tokens = n_tokens;
+    a.q_rows = q_heads, a.k_rows = kv_heads, a.v_rows = kv_heads, a.head_dim = head_dim, a.kv_heads = kv_heads;
+    a.page_size = page_size, a.n_slots = num_pages;
+    a.qo = q_out, a.qo_stride = q_out_row_stride, a.ko = k_out, a.ko_stride = k_out_row_stride;
+    a.kc = k_cache, a.vc = v_cache, a.ke = k_exp, a.ve = v_exp, a.err = err_word;
+    return run_rotary(a, dtype, kv_format, rotary_dim, true, stream);
+}

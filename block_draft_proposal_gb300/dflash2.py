@@ -15,6 +15,7 @@ that stream; that its inputs are ready there is the caller's to see to.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 from typing import NamedTuple
@@ -29,6 +30,8 @@ _lib = None
 OK = 0
 F32, BF16 = 0, 1
 KV_NATIVE, KV_E4M3 = 0, 1
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
+GATE_ACTS = {"none": 0, "sigmoid": 1, "tanh": 2}
 DEVERR_ID_RANGE = 0x1
 DEVERR_TIMEOUT = 0x2
 DEVERR_SHORT = 0x4
@@ -49,7 +52,9 @@ EXPORTS = (
     "dflash2_unary_topk_nvfp4", "dflash2_nvfp4_scale_tiles_size", "dflash2_nvfp4_tile_scales",
     "dflash2_kv_cache_write", "dflash2_kv_cache_read", "dflash2_tree_attention_workspace_size",
     "dflash2_tree_attention", "dflash2_prompt_attention_workspace_size",
-    "dflash2_prompt_attention",
+    "dflash2_prompt_attention", "dflash2_quantize_blocks_e4m3",
+    "dflash2_linear_fp8_blocks_workspace_size", "dflash2_linear_fp8_blocks",
+    "dflash2_sublayer_norm", "dflash2_sublayer_join", "dflash2_rotary", "dflash2_rotary_kv_write",
 )
 NOALLOC_SCRATCH_BYTES = 4 << 20
 
@@ -152,6 +157,25 @@ def library():
         lib.dflash2_prompt_attention.argtypes = [P, P, P, i64, i64, i64, P, i32, i32, i32, i32,
                                                  i32, f32, i32, P, P, P, sz, P, P]
         lib.dflash2_prompt_attention.restype = i32
+        lib.dflash2_quantize_blocks_e4m3.argtypes = [P, i64, i64, i32, i32, P, P, P]
+        lib.dflash2_quantize_blocks_e4m3.restype = i32
+        lib.dflash2_linear_fp8_blocks_workspace_size.argtypes = [i64, i32, i32]
+        lib.dflash2_linear_fp8_blocks_workspace_size.restype = sz
+        lib.dflash2_linear_fp8_blocks.argtypes = [P, i64, i32, P, P, P, P, i64, i32, i32, i32, P, P,
+                                                  sz, P, P]
+        lib.dflash2_linear_fp8_blocks.restype = i32
+        lib.dflash2_sublayer_norm.argtypes = [P, i64, i32, P, f32, f32, i64, i32, i32, P, P, P]
+        lib.dflash2_sublayer_norm.restype = i32
+        lib.dflash2_sublayer_join.argtypes = [P, i64, i32, P, i64, P, P, i32, i64, i32, f32, P, f32,
+                                              f32, i64, i32, i32, P, i64, P, P, P]
+        lib.dflash2_sublayer_join.restype = i32
+        lib.dflash2_rotary.argtypes = [P, i64, P, i64, P, i32, P, P, i32, i32, f32, i64, i32, i32,
+                                       i32, i32, P, i64, P, i64, P, P]
+        lib.dflash2_rotary.restype = i32
+        lib.dflash2_rotary_kv_write.argtypes = [P, i64, P, i64, P, i64, P, i32, P, P, i32, i32, f32,
+                                                P, i64, i32, i32, i32, i32, i64, i32, i32, P, i64,
+                                                P, i64, P, P, P, P, P, P]
+        lib.dflash2_rotary_kv_write.restype = i32
         lib.dflash2_unary_topk_launches.argtypes = [i64, i64, i32, f32, i32]
         lib.dflash2_unary_topk_launches.restype = i32
         if lib.dflash2_abi_version() != ABI_VERSION:
@@ -939,6 +963,287 @@ def prompt_attention(q, k, v, cu_q, scale: float, out=None, lse=None, with_lse: 
         float(scale), _dtype_code(q), _ptr(out), _ptr(lse), _ptr(workspace), workspace.nbytes,
         _ptr(err), _stream(stream)))
     return out, lse, err
+
+
+# ---- norms, FP8 linear layers and rotary positions -----------------------------------
+
+def _need_matrix(t: torch.Tensor, name: str, dtype=None, shape=None) -> int:
+    """A [rows, cols] tensor whose rows may be strided (a slice of a wider one); returns
+    the row stride."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2 or (shape is not None and t.shape != tuple(shape)):
+        raise ValueError(f"{name} must have shape {'[rows, cols]' if shape is None else tuple(shape)}"
+                         f", got {tuple(t.shape)}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if rows > 1 and t.stride(0) < cols:
+        raise ValueError(f"{name} must not repeat rows")
+    return t.stride(0) if rows > 1 else cols
+
+
+def _blocks_of(cols: int) -> int:
+    return -(-cols // 128)
+
+
+def quantize_blocks_e4m3(x, q=None, scale=None, stream=None):
+    """dflash2_quantize_blocks_e4m3: E4M3 codes (uint8) of x [rows, cols] (rows may be
+    strided) and one fp32 scale per 128 values of a row [rows, ceil(cols / 128)]."""
+    xs = _need_matrix(x, "x")
+    rows, cols = x.shape
+    if q is None:
+        q = _empty((rows, cols), torch.uint8, x.device, stream)
+    else:
+        _need(q, "q", torch.uint8, (rows, cols))
+    if scale is None:
+        scale = _empty((rows, _blocks_of(cols)), torch.float32, x.device, stream)
+    else:
+        _need(scale, "scale", torch.float32, (rows, _blocks_of(cols)))
+    _check("dflash2_quantize_blocks_e4m3", library().dflash2_quantize_blocks_e4m3(
+        _ptr(x), xs, rows, cols, _dtype_code(x), _ptr(q), _ptr(scale), _stream(stream)))
+    return q, scale
+
+
+def linear_fp8_blocks_workspace_size(rows: int, in_features: int, out_features: int) -> int:
+    return int(library().dflash2_linear_fp8_blocks_workspace_size(rows, in_features, out_features))
+
+
+def linear_fp8_blocks(x, w_q, w_scale, x_scale=None, out_dtype=None, out=None, workspace=None,
+                      err=None, stream=None):
+    """dflash2_linear_fp8_blocks: x [rows, in] times E4M3 weights w_q [out, in] (uint8)
+    with a scale per 128 x 128 of them.  x is fp32 or bf16 (rows may be strided) and
+    quantised on the way, or uint8 codes with their x_scale, as quantize_blocks_e4m3 or a
+    norm here returns them.  out_dtype: x's, or bfloat16 for codes, unless given or `out`
+    is.  Returns (out [rows, out], err)."""
+    n_out, n_in = w_q.shape
+    _need(w_q, "w_q", torch.uint8)
+    _need(w_scale, "w_scale", torch.float32, (_blocks_of(n_out), _blocks_of(n_in)))
+    rows = x.shape[0]
+    dev = x.device
+    codes = x.dtype == torch.uint8
+    if codes:
+        if x_scale is None:
+            raise ValueError("codes need x_scale")
+        _need(x, "x", torch.uint8, (rows, n_in))
+        _need(x_scale, "x_scale", torch.float32, (rows, _blocks_of(n_in)))
+    else:
+        if x_scale is not None:
+            raise ValueError("x_scale belongs to uint8 codes")
+        xs = _need_matrix(x, "x", None, (rows, n_in))
+        x_code = _dtype_code(x)
+    if out is None:
+        if out_dtype is None:
+            out_dtype = torch.bfloat16 if codes else x.dtype
+        out = _empty((rows, n_out), out_dtype, dev, stream)
+    else:
+        _need(out, "out", out_dtype, (rows, n_out))
+    if workspace is not None:
+        _need(workspace, "workspace")
+    elif not codes:
+        workspace = _workspace(linear_fp8_blocks_workspace_size(rows, n_in, n_out), dev, stream)
+    err = _need_error_word(err, dev, stream)
+    _check("dflash2_linear_fp8_blocks", library().dflash2_linear_fp8_blocks(
+        None if codes else _ptr(x), 0 if codes else xs, 0 if codes else x_code,
+        _ptr(x) if codes else None, _ptr(x_scale), _ptr(w_q), _ptr(w_scale), rows, n_in, n_out,
+        _dtype_code(out), _ptr(out), _ptr(workspace), 0 if workspace is None else workspace.nbytes,
+        _ptr(err), _stream(stream)))
+    return out, err
+
+
+def _norm_out(rows, hidden, dtype, e4m3, out, scale, device, stream):
+    if e4m3:
+        if scale is None:
+            scale = _empty((rows, _blocks_of(hidden)), torch.float32, device, stream)
+        else:
+            _need(scale, "scale", torch.float32, (rows, _blocks_of(hidden)))
+    elif scale is not None:
+        raise ValueError("scale belongs to e4m3=True")
+    held = torch.uint8 if e4m3 else dtype
+    if out is None:
+        out = _empty((rows, hidden), held, device, stream)
+    else:
+        _need(out, "out", held, (rows, hidden))
+    return out, scale
+
+
+def sublayer_norm(x, weight, eps: float = 1e-6, weight_offset: float = 0.0, e4m3: bool = False,
+                  out=None, scale=None, stream=None):
+    """dflash2_sublayer_norm: rms(x) * (weight + weight_offset) of x [rows, hidden] (rows
+    may be strided; fp32 or bf16, whatever weight is) in weight's dtype, or with e4m3 as
+    codes and scales of E4M3 blocks.  Returns (out, scale or None)."""
+    xs = _need_matrix(x, "x")
+    rows, hidden = x.shape
+    _need(weight, "weight", None, (hidden,))
+    out, scale = _norm_out(rows, hidden, weight.dtype, e4m3, out, scale, x.device, stream)
+    _check("dflash2_sublayer_norm", library().dflash2_sublayer_norm(
+        _ptr(x), xs, _dtype_code(x), _ptr(weight), float(weight_offset), float(eps), rows, hidden,
+        _dtype_code(weight), _ptr(out), _ptr(scale), _stream(stream)))
+    return out, scale
+
+
+def sublayer_join(residual, y, post_weight=None, gate=None, gate_act: str = "none",
+                  branch_scale: float = 1.0, next_weight=None, eps: float = 1e-6,
+                  weight_offset: float = 0.0, e4m3: bool = False, residual_out=None, out=None,
+                  scale=None, stream=None):
+    """dflash2_sublayer_join: a sublayer's output y [rows, hidden] normed (post_weight),
+    gated (gate [hidden], [rows, 1] or [rows, hidden]; gate_act none, sigmoid or tanh of
+    it), scaled and added to residual, and the next sublayer's norm of that (next_weight),
+    with e4m3 as E4M3 blocks.  The residual may have another dtype than y, the gate and
+    the weights; residual_out may be residual.  Returns (residual_out, out or None, scale
+    or None)."""
+    rs = _need_matrix(residual, "residual")
+    rows, hidden = residual.shape
+    ys = _need_matrix(y, "y", None, (rows, hidden))
+    dt, dev = y.dtype, y.device
+    for w, name in ((post_weight, "post_weight"), (next_weight, "next_weight")):
+        if w is not None:
+            _need(w, name, dt, (hidden,))
+    kind, gs = GATE_NONE, 0
+    if gate_act not in GATE_ACTS:
+        raise ValueError(f"gate_act must be one of {', '.join(GATE_ACTS)}, got {gate_act!r}")
+    if gate is not None:
+        if gate.dim() == 1:
+            _need(gate, "gate", dt, (hidden,))
+            kind = GATE_CHANNEL
+        elif gate.shape[-1] == 1 and hidden > 1:
+            gs = _need_matrix(gate, "gate", dt, (rows, 1))
+            kind = GATE_TOKEN
+        else:
+            gs = _need_matrix(gate, "gate", dt, (rows, hidden))
+            kind = GATE_FULL
+    if residual_out is None:
+        residual_out = _empty((rows, hidden), residual.dtype, dev, stream)
+    ros = _need_matrix(residual_out, "residual_out", residual.dtype, (rows, hidden))
+    if next_weight is not None:
+        out, scale = _norm_out(rows, hidden, dt, e4m3, out, scale, dev, stream)
+    elif out is not None or scale is not None or e4m3:
+        raise ValueError("out, scale and e4m3 belong to next_weight")
+    _check("dflash2_sublayer_join", library().dflash2_sublayer_join(
+        _ptr(residual), rs, _dtype_code(residual), _ptr(y), ys, _ptr(post_weight), _ptr(gate), kind,
+        gs, GATE_ACTS[gate_act], float(branch_scale), _ptr(next_weight), float(weight_offset),
+        float(eps), rows, hidden, _dtype_code(y), _ptr(residual_out), ros, _ptr(out), _ptr(scale),
+        _stream(stream)))
+    return residual_out, out, scale
+
+
+class RotaryTable(NamedTuple):
+    """Frequencies of rotary positions: freq int64 [rotary_dim / 2], the bits of a uint64
+    fraction of a turn per position, in units of 2^-64; axis uint8 [rotary_dim / 2], the
+    row of the positions that turns each pair; adjacent: pairs (2j, 2j + 1), not (j, j +
+    rotary_dim / 2); magnitude: a factor of sines and cosines.  rotary_table makes one."""
+    freq: torch.Tensor
+    axis: torch.Tensor
+    adjacent: bool = False
+    magnitude: float = 1.0
+
+
+def rotary_table(rotary_dim: int, base: float = 10000.0, sections=None, interleaved: bool = False,
+                 inv_freq=None, adjacent: bool = False, magnitude: float = 1.0,
+                 device="cuda") -> RotaryTable:
+    """The table of frequencies base^(-2j / rotary_dim), or of inv_freq (radians per
+    position, rotary_dim / 2 numbers).  sections: how many pairs each axis turns, adding
+    up to rotary_dim / 2, one axis after the other; interleaved: the axes take turns from
+    the first pair on, as far as each one's section goes, and the first axis takes the
+    rest."""
+    half = rotary_dim // 2
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even and positive")
+    if inv_freq is None:
+        inv_freq = [float(base) ** (-j / half) for j in range(half)]
+    inv_freq = [float(f) for f in inv_freq]
+    sections = [half] if sections is None else [int(n) for n in sections]
+    if len(inv_freq) != half or sum(sections) != half or min(sections) < 0 or len(sections) > 255:
+        raise ValueError(f"inv_freq and sections must cover rotary_dim / 2 = {half} pairs")
+    axis = [a for a, n in enumerate(sections) for _ in range(n)]
+    if interleaved:
+        axis = [0] * half
+        for a, n in enumerate(sections[1:], 1):
+            for i in range(n):
+                if a + i * len(sections) >= half:
+                    raise ValueError(f"section {a} does not fit between the others")
+                axis[a + i * len(sections)] = a
+    # the fraction of a turn, rounded to 2^-64; whole turns drop out
+    turns = [round(math.fmod(f / math.tau, 1.0) * 2.0 ** 64) % 2 ** 64 for f in inv_freq]
+    turns = [t - 2 ** 64 if t >= 2 ** 63 else t for t in turns]
+    return RotaryTable(torch.tensor(turns, dtype=torch.int64, device=device),
+                       torch.tensor(axis, dtype=torch.uint8, device=device), bool(adjacent),
+                       float(magnitude))
+
+
+def _need_rotary(positions, table: RotaryTable, n: int):
+    freq, axis, adjacent, magnitude = table
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    _need(positions, "positions", torch.int64, (n,) if positions.dim() == 1 else (axes, n))
+    _need(freq, "table.freq", torch.int64)
+    _need(axis, "table.axis", torch.uint8, freq.shape)
+    return (_ptr(positions), axes, _ptr(freq), _ptr(axis), 2 * freq.numel(), int(bool(adjacent)),
+            float(magnitude))
+
+
+def _rotated(x, name, out, stream):
+    """Strides of x and of where it goes, which is made unless given."""
+    xs = _need_rows(x, name, x.dtype, x.shape)
+    if out is None:
+        out = _empty(x.shape, x.dtype, x.device, stream)
+    return xs, out, _need_rows(out, name + "_out", x.dtype, x.shape)
+
+
+def rotary(q, k, positions, table: RotaryTable, q_out=None, k_out=None, err=None, stream=None):
+    """dflash2_rotary: queries q [n, q_heads, head_dim] and keys k [n, kv_heads, head_dim]
+    (slices of a packed projection are read in place; k may be None) turned by positions
+    int64 [n] or [axes, n].  q_out and k_out may be q and k.  Returns (q_out, k_out or
+    None, err)."""
+    n, heads, d = q.shape
+    place = _need_rotary(positions, table, n)
+    qs, q_out, qos = _rotated(q, "q", q_out, stream)
+    ks = kos = kv_heads = 0
+    if k is not None:
+        kv_heads = k.shape[1]
+        if k.shape != (n, kv_heads, d) or k.dtype != q.dtype:
+            raise ValueError(f"k must be {q.dtype} [{n}, kv_heads, {d}]")
+        ks, k_out, kos = _rotated(k, "k", k_out, stream)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    err = _need_error_word(err, q.device, stream)
+    _check("dflash2_rotary", library().dflash2_rotary(
+        _ptr(q), qs, _ptr(k), ks, *place, n, heads, kv_heads, d, _dtype_code(q), _ptr(q_out), qos,
+        _ptr(k_out), kos, _ptr(err), _stream(stream)))
+    return q_out, k_out, err
+
+
+def rotary_kv_write(cache: KVCache, q, k, v, positions, table: RotaryTable, slots, q_out=None,
+                    k_out=None, with_k: bool = False, err=None, stream=None):
+    """dflash2_rotary_kv_write: rotary's turn of q (or None) and k, and the turned keys and
+    the values v into the cache's slots (int64 [n], negative skips), an E4M3 cache's rows
+    quantised on the way.  with_k: the turned keys are returned too (a prompt's own
+    attention reads them).  Returns (q_out or None, k_out or None, err)."""
+    pages, kv_heads, ps, d, fmt = _need_cache(cache, k.dtype)
+    n = k.shape[0]
+    if k.shape != (n, kv_heads, d):
+        raise ValueError(f"k must have shape {(n, kv_heads, d)}, got {tuple(k.shape)}")
+    place = _need_rotary(positions, table, n)
+    ks = _need_rows(k, "k", k.dtype, (n, kv_heads, d))
+    vs = _need_rows(v, "v", k.dtype, (n, kv_heads, d))
+    _need(slots, "slots", torch.int64, (n,))
+    qs = qos = kos = heads = 0
+    if q is not None:
+        heads = q.shape[1]
+        if q.shape != (n, heads, d) or q.dtype != k.dtype:
+            raise ValueError(f"q must be {k.dtype} [{n}, q_heads, {d}]")
+        qs, q_out, qos = _rotated(q, "q", q_out, stream)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if with_k or k_out is not None:
+        ks, k_out, kos = _rotated(k, "k", k_out, stream)
+    err = _need_error_word(err, k.device, stream)
+    _check("dflash2_rotary_kv_write", library().dflash2_rotary_kv_write(
+        _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, *place, _ptr(slots), n, heads, kv_heads, d, ps,
+        pages, _dtype_code(k), fmt, _ptr(q_out), qos, _ptr(k_out), kos, _ptr(cache.k),
+        _ptr(cache.v), _ptr(cache.k_exp), _ptr(cache.v_exp), _ptr(err), _stream(stream)))
+    return q_out, k_out, err
 
 
 # ---- host <-> device helpers (plumbing) ----------------------------------------------

@@ -729,6 +729,177 @@ dflash2_status dflash2_prompt_attention(const void *q, const void *k, const void
                                         float *lse, void *workspace, size_t ws_bytes,
                                         int32_t *err_word, void *stream);
 
+/*
+ * Operators of a layer around its attention: norms, products with FP8 weights,
+ * rotary positions.  The pages leave them to the serving engine; the definitions
+ * here are the standard ones.
+ *
+ * E4M3 blocks: a row's values in blocks of 128 columns (the last may be short),
+ * uint8 codes [rows, cols] and scales float [rows, ceil(cols / 128)].  With amax
+ * the block's largest finite magnitude, not below 2^-100, in fp32:
+ *   scale = amax / 448,  code = E4M3(x * (448 / amax))   (to nearest even)
+ * A block without a finite value other than 0 has scale 1.  NaN and infinities
+ * become the NaN code.
+ *
+ * dflash2_quantize_blocks_e4m3: x device, rows of `cols` values at x + i *
+ *   x_row_stride elements -> q, scale.
+ *   Errors: dtype -> UNSUPPORTED_DTYPE; rows outside [0, 2^31), cols outside
+ *   [1, 2^30], a row stride below cols or above 2^32, more than 2^34 blocks, a null
+ *   pointer -> INVALID_ARG; x or scale not aligned to its element -> MISALIGNED.  rows == 0
+ *   queues nothing.
+ */
+dflash2_status dflash2_quantize_blocks_e4m3(const void *x, int64_t x_row_stride, int64_t rows,
+                                            int32_t cols, int32_t dtype, uint8_t *q, float *scale,
+                                            void *stream);
+
+/*
+ * Linear layer with E4M3 weights, a scale per 128 x 128 weights and one per 128
+ * activations of a row:
+ *
+ *   y[m, n] = sum_b xs[m, b] * ws[n / 128, b] * sum_{k in block b} x_q[m, k] * w_q[n, k]
+ *
+ * x          device, rows at x + m * x_row_stride elements (x_dtype f32 or bf16),
+ *            quantised to E4M3 blocks on the way; or NULL, with
+ * x_q        device uint8 [rows, in_features], 16-byte aligned, and x_scale
+ *            float [rows, ceil(in / 128)]: E4M3 blocks as the calls here write
+ *            them.  Exactly one of x and x_q is given.
+ * w_q        device uint8 [out_features, in_features] (nn.Linear weight layout),
+ *            16-byte aligned; w_scale device float [ceil(out / 128), ceil(in / 128)].
+ * out        device [rows, out_features], out_dtype f32 or bf16.
+ * workspace  device, 256-byte aligned, ws_bytes >=
+ *            dflash2_linear_fp8_blocks_workspace_size(...): the codes and scales
+ *            of x.  Not read with x_q (may be NULL).
+ * err_word   device int32 or NULL: DFLASH2_DEVERR_TIMEOUT.
+ * Arithmetic: a block's products summed in fp32, times xs * ws (fp32), the blocks
+ *            added in fp32; the result rounded once.  NaN codes give NaN.
+ *            Reduction orders are fixed, so results are deterministic.
+ * Errors:    rows outside [0, 2^20], in_features outside [1, 2^20], out_features
+ *            outside [1, 2^24], rows * in or out * in >= 2^40, both or none of x
+ *            and x_q, a null pointer, what dflash2_quantize_blocks_e4m3 refuses of
+ *            x -> INVALID_ARG; an unknown dtype -> UNSUPPORTED_DTYPE; in_features
+ *            % 16 != 0 or a pointer not aligned as above or to its element ->
+ *            MISALIGNED; a workspace (with x) that is NULL, too small or not
+ *            aligned -> WORKSPACE.  rows == 0 queues nothing.
+ */
+size_t dflash2_linear_fp8_blocks_workspace_size(int64_t rows, int32_t in_features,
+                                                int32_t out_features);
+dflash2_status dflash2_linear_fp8_blocks(const void *x, int64_t x_row_stride, int32_t x_dtype,
+                                         const uint8_t *x_q, const float *x_scale,
+                                         const uint8_t *w_q, const float *w_scale, int64_t rows,
+                                         int32_t in_features, int32_t out_features,
+                                         int32_t out_dtype, void *out, void *workspace,
+                                         size_t ws_bytes, int32_t *err_word, void *stream);
+
+/*
+ * The norm before a sublayer, and after it the norm, gate and residual with the
+ * next norm:
+ *
+ *   rms(x) = x / sqrt(mean(x^2) + eps)      over a row's `hidden` values
+ *   norm:  out = rms(x) * (weight + weight_offset)
+ *   join:  h   = post_weight ? rms(y) * (post_weight + weight_offset) : y
+ *          r'  = residual + branch_scale * act(gate) * h   (no gate: 1)
+ *          out = rms(r') * (next_weight + weight_offset)   (next_weight NULL: none)
+ *
+ * x, residual device, rows at + i * row stride elements, in x_dtype /
+ *            residual_dtype; y, gate and the weights [hidden] in dtype; each of the
+ *            two is f32 or bf16.
+ * gate       DFLASH2_GATE_NONE (NULL), _CHANNEL [hidden], _TOKEN one value per row
+ *            at gate + i * gate_row_stride, _FULL rows of hidden values at that
+ *            stride.  gate_act: identity, sigmoid or tanh of it.
+ * residual_out  r' in residual_dtype, rows at residual_out_row_stride; may be
+ *            `residual` itself (same stride), and must not overlap it otherwise.
+ * out        [rows, hidden]: in dtype where scale is NULL; else uint8 codes of E4M3
+ *            blocks, with scale float [rows, ceil(hidden / 128)].
+ * Arithmetic: fp32, sums of squares included; the next norm takes r' as computed,
+ *            not as rounded.  Reduction orders are fixed.  A row of zeros with eps
+ *            0 gives NaN (0 / 0).
+ * Errors:    rows outside [0, 2^31), hidden outside [1, 32768], eps negative or not
+ *            finite, weight_offset or branch_scale not finite, a row stride below
+ *            hidden (gate per token: below 1) or above 2^32, an unknown gate kind or
+ *            activation, a null pointer, out or scale without next_weight ->
+ *            INVALID_ARG; dtypes -> UNSUPPORTED_DTYPE; a pointer not aligned to its
+ *            element -> MISALIGNED.  rows == 0 queues nothing.
+ * The fast path wants hidden % 8 == 0 and every row 16-byte aligned.
+ */
+typedef enum {
+    DFLASH2_GATE_NONE = 0,
+    DFLASH2_GATE_CHANNEL = 1,
+    DFLASH2_GATE_TOKEN = 2,
+    DFLASH2_GATE_FULL = 3
+} dflash2_gate_kind;
+typedef enum {
+    DFLASH2_GATE_IDENTITY = 0,
+    DFLASH2_GATE_SIGMOID = 1,
+    DFLASH2_GATE_TANH = 2
+} dflash2_gate_act;
+dflash2_status dflash2_sublayer_norm(const void *x, int64_t x_row_stride, int32_t x_dtype,
+                                     const void *weight, float weight_offset, float eps,
+                                     int64_t rows, int32_t hidden, int32_t dtype, void *out,
+                                     float *scale, void *stream);
+dflash2_status dflash2_sublayer_join(const void *residual, int64_t residual_row_stride,
+                                     int32_t residual_dtype, const void *y, int64_t y_row_stride,
+                                     const void *post_weight, const void *gate, int32_t gate_kind,
+                                     int64_t gate_row_stride, int32_t gate_act, float branch_scale,
+                                     const void *next_weight, float weight_offset, float eps,
+                                     int64_t rows, int32_t hidden, int32_t dtype,
+                                     void *residual_out, int64_t residual_out_row_stride, void *out,
+                                     float *scale, void *stream);
+
+/*
+ * Rotary positions with several axes (text: one; images and video: time, height,
+ * width), of queries and keys:
+ *
+ *   angle(i, j) = positions[axis[j], i] * freq[j] / 2^64 turns,  j < rotary_dim / 2
+ *   (a, b) -> magnitude * (a cos - b sin, b cos + a sin)
+ *
+ * on the pairs (j, j + rotary_dim / 2) of every head, or adjacent (2j, 2j + 1); a
+ * head's values from rotary_dim on are copied.  The angle is exact modulo a turn
+ * for every 64-bit position.  Turned back (and a gradient): negated positions.
+ *
+ * q, k       device, rows [q_heads, head_dim] / [kv_heads, head_dim] of token i at
+ *            q + i * q_row_stride elements (k likewise); 0 heads: absent.
+ * positions  device int64 [axes, n_tokens];  freq device uint64 and axis device
+ *            uint8 [rotary_dim / 2].
+ * q_out, k_out  device, rows like q and k at their own strides; may be q and k
+ *            themselves (same stride), and must not overlap them otherwise.
+ * Arithmetic: fp32 (sines and cosines by CUDA's sincospif of the exact fraction of
+ *            a turn); one rounding per value.
+ * dflash2_rotary_kv_write also writes the rotated keys and the values (rows v, as
+ * k) into the cache as dflash2_kv_cache_write does (its slots, formats and device
+ * errors); an E4M3 row is quantised from the fp32 values.  k_out may be NULL.
+ * Errors:    head_dim outside [1, 256], rotary_dim odd or outside [2, head_dim],
+ *            axes outside [1, 255], magnitude not finite, n_tokens < 0, heads < 0,
+ *            no heads (of keys, with a cache), more than 2^16 rows a token,
+ *            n_tokens * rows >= 2^31, a row stride below its heads * head_dim or
+ *            above 2^32, page_size < 1, num_pages < 0, a null pointer ->
+ *            INVALID_ARG; unknown dtype or kv_format -> UNSUPPORTED_DTYPE; a
+ *            pointer not aligned to its element -> MISALIGNED.  n_tokens == 0 queues
+ *            nothing.
+ * Device:    an axis[j] >= axes sets DFLASH2_DEVERR_ID_RANGE, and its pairs take
+ *            angle 0; slots as for dflash2_kv_cache_write.
+ * The fast path wants head_dim % 8 == 0, rotary_dim % 16 == 0 (adjacent pairs: % 8)
+ * and every row 16-byte aligned (8-byte for E4M3 codes); other layouts take a
+ * scalar path.
+ */
+dflash2_status dflash2_rotary(const void *q, int64_t q_row_stride, const void *k,
+                              int64_t k_row_stride, const int64_t *positions, int32_t axes,
+                              const uint64_t *freq, const uint8_t *axis, int32_t rotary_dim,
+                              int32_t adjacent, float magnitude, int64_t n_tokens, int32_t q_heads,
+                              int32_t kv_heads, int32_t head_dim, int32_t dtype, void *q_out,
+                              int64_t q_out_row_stride, void *k_out, int64_t k_out_row_stride,
+                              int32_t *err_word, void *stream);
+dflash2_status dflash2_rotary_kv_write(const void *q, int64_t q_row_stride, const void *k,
+                                       int64_t k_row_stride, const void *v, int64_t v_row_stride,
+                                       const int64_t *positions, int32_t axes, const uint64_t *freq,
+                                       const uint8_t *axis, int32_t rotary_dim, int32_t adjacent,
+                                       float magnitude, const int64_t *slots, int64_t n_tokens,
+                                       int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                       int32_t page_size, int64_t num_pages, int32_t dtype,
+                                       int32_t kv_format, void *q_out, int64_t q_out_row_stride,
+                                       void *k_out, int64_t k_out_row_stride, void *k_cache,
+                                       void *v_cache, uint8_t *k_exp, uint8_t *v_exp,
+                                       int32_t *err_word, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
