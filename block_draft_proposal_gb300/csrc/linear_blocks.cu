@@ -2,64 +2,534 @@
 //
 //   y[m, n] = sum_b xs[m, b] * ws[n / 128, b] * sum_{k in b} dec(xq[m, k]) * dec(wq[n, k])
 //
-// the products of a block in fp32, scaled and added in fp32.
+// The tensor cores multiply and add one block of 128 at a time (four MMAs of K = 32 into a
+// fresh TMEM accumulator); the epilogue warps read it, scale it and add it to sums that
+// they keep in registers in fp32, while the MMAs of the next block fill the other
+// accumulator.  Every scale is an fp32 number, so the scaling cannot be left to block-scaled
+// MMAs, whose scales are powers of two.
+//
+// Two kernels, by the rows (launch_linear):
+//   linear_pair_kernel  many rows: CTA pairs (M = 256 rows of x, kCols outputs).
+//   linear_few_kernel   few rows: the weights are the MMA's M side, 128 a CTA, and the
+//                       rows of x its N side; the blocks are split over a cluster's CTAs,
+//                       which add their sums through distributed shared memory.
 #include "rows.cuh"
+#include "tcgen05.cuh"
 
 namespace dflash2 {
 namespace {
 
 struct LinearArgs {
-    const uint8_t *xq, *wq;
     const float *xs, *ws;
-    int32_t rows, n_in, n_out, blocks;  // blocks of 128 along n_in
+    int32_t rows, n_out, blocks;  // blocks of 128 along in_features
     void *y;
     int32_t *err;
+    int32_t m_tiles, n_tiles, stages;
+    bool vec;    // rows of y are 16-byte aligned
+    bool early;  // the weights may be read before the kernel before this one is done
 };
 
-constexpr int kTile = 64, kStep = 32;
+constexpr uint32_t kBoxBytes = 128 * 128;  // 128 rows of one block
+constexpr int kMaxStages = 8;
 
-// 64 x 64 outputs a CTA of 256 threads, 4 x 4 each, on CUDA cores.
-template <typename T>
-__global__ void __launch_bounds__(256) linear_simple_kernel(const LinearArgs a) {
-    __shared__ float xt[kStep][kTile + 1], wt[kStep][kTile + 1];
-    grid_dep_wait();
-    const int64_t m0 = (int64_t)blockIdx.y * kTile, n0 = (int64_t)blockIdx.x * kTile;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float y[4][4] = {}, part[4][4] = {};
-    for (int k0 = 0; k0 < a.n_in; k0 += kStep) {
-        for (int i = threadIdx.x; i < kTile * kStep; i += 256) {
-            const int r = i / kStep, k = i % kStep;
-            const bool in = k0 + k < a.n_in;
-            xt[k][r] = in && m0 + r < a.rows ? decode1(a.xq[(m0 + r) * a.n_in + k0 + k]) : 0.0f;
-            wt[k][r] = in && n0 + r < a.n_out ? decode1(a.wq[(n0 + r) * a.n_in + k0 + k]) : 0.0f;
-        }
-        __syncthreads();
-        for (int k = 0; k < kStep; ++k)
-            for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j) part[i][j] += xt[k][ty + 16 * i] * wt[k][tx + 16 * j];
-        __syncthreads();
-        if ((k0 + kStep) % 128 == 0 || k0 + kStep >= a.n_in) {
-            const int b = k0 / 128;
-            for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j) {
-                    const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-                    if (m < a.rows && n < a.n_out)
-                        y[i][j] += part[i][j] * (a.xs[m * a.blocks + b] * a.ws[n / 128 * a.blocks + b]);
-                    part[i][j] = 0.0f;
-                }
-        }
-    }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-            if (m < a.rows && n < a.n_out) from_f32((T *)a.y + m * a.n_out + n, y[i][j]);
-        }
+__device__ __forceinline__ bool wait_drain(uint64_t *bar, uint32_t parity) {
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity))
+        if (clock64() - t0 > kWaitLimitCycles) return false;
+    return true;
+}
+// No copy is still writing shared memory when the CTA leaves: waits (bounded) for the
+// last `stages` loads issued.
+__device__ __forceinline__ void drain_loads(uint64_t *full, uint32_t issued, uint32_t stages) {
+    for (uint32_t n = issued > stages ? issued - stages : 0; n < issued; ++n)
+        wait_drain(&full[n % stages], (n / stages) & 1u);
 }
 
-template <typename T> dflash2_status launch_linear(const LinearArgs &a, cudaStream_t st) {
-    launch_k(linear_simple_kernel<T>, dim3((a.n_out + kTile - 1) / kTile, (a.rows + kTile - 1) / kTile), dim3(256), 0,
-             st, a);
+// 32 results of one row from p on, n of them inside.
+template <typename T> __device__ __forceinline__ void store32(T *p, int n, bool vec, const uint64_t *v) {
+    float x[32];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) unf2(v[i], x[2 * i], x[2 * i + 1]);
+    if (vec && n >= 32) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = x[8 * i + j];
+            store8(p + 8 * i, y);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        if (i < n) from_f32(p + i, x[i]);
+}
+
+// ---- many rows -----------------------------------------------------------------
+// Roles (384 threads, one CTA per SM, persistent over tiles): warp 0 loads, warp 1 of the
+// leader issues the MMAs, warps 4 to 11 scale and add: four lane quarters, each with two
+// warps that take half of the tile's columns, kCols / 2 sums a thread.
+constexpr int kPairThreads = 384;
+constexpr int kPairEpiWarps = 8;
+
+template <int kCols> constexpr uint32_t kPairStage = kBoxBytes + kCols / 2 * 128;
+
+template <typename T, int kCols>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                       const LinearArgs a) {
+    constexpr int kHalf = kCols / 2, kChunks = kHalf / 32;
+    // weight blocks of 128 that a thread's columns lie in
+    constexpr int kScales = 128 % kHalf == 0 ? 1 : kChunks;
+    constexpr uint32_t kAccCols = kCols <= 32 ? 32 : kCols <= 64 ? 64 : kCols <= 128 ? 128 : 256;
+    constexpr uint32_t kStage = kPairStage<kCols>;
+    extern __shared__ uint8_t dsmem[];
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~(uintptr_t)1023);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < a.stages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_empty[i], 2 * kPairEpiWarps);
+        mbar_init(&drain, 1);
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc_pair(&tmem_slot, 2 * kAccCols);
+        tmem_relinquish_pair();
+    }
+    if (warp == 1 && lane == 0) prefetch_tmap(&tm_x), prefetch_tmap(&tm_w);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    grid_dep_wait();
+    const uint32_t tmem = tmem_slot;
+    const int total = a.m_tiles * a.n_tiles, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+    // Tiles in groups of kGroup row tiles, row tiles fastest: the tiles at work together
+    // share x and weight rows in L2.
+    constexpr int kGroup = 8;
+    const auto tile_of = [&](int w, int *m, int *n) {
+        const int g = w / (kGroup * a.n_tiles), r = w - g * kGroup * a.n_tiles;
+        const int rows = min(kGroup, a.m_tiles - g * kGroup);
+        *n = r / rows;
+        *m = g * kGroup + r - *n * rows;
+    };
+
+    if (warp < 4) {
+        regs_give<40>();
+        if (warp == 0 && lane == 0) {
+            uint32_t issued = 0, s = 0, ph = 1;  // the first pass finds every stage free
+            bool ok = true;
+            for (int w = pair; w < total && ok; w += pairs) {
+                int m, n;
+                tile_of(w, &m, &n);
+                for (int b = 0; b < a.blocks; ++b) {
+                    if (!bar_wait(&empty[s], ph, &abort_flag, a.err)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStage);
+                    uint8_t *st = smem + s * kStage;
+                    tma_load_2d_pair(st, &tm_x, bar, b * 128, m * 256 + (int)rank * 128);
+                    tma_load_2d_pair(st + kBoxBytes, &tm_w, bar, b * 128, n * kCols + (int)rank * kHalf);
+                    ++issued;
+                    if (++s == (uint32_t)a.stages) s = 0, ph ^= 1u;
+                }
+            }
+            if (rank == 0) drain_loads(full, issued, (uint32_t)a.stages);
+        } else if (warp == 1 && lane == 0 && rank == 0) {
+            const uint32_t idesc = idesc_e4m3(256, kCols);
+            const uint64_t xd = sw128_desc(smem_u32(smem)), wd = sw128_desc(smem_u32(smem + kBoxBytes));
+            uint32_t s = 0, ph = 0, it = 0;
+            bool ok = true;
+            for (int w = pair; w < total && ok; w += pairs) {
+                for (int b = 0; b < a.blocks; ++b, ++it) {
+                    const uint32_t i = it & 1u;
+                    if (!bar_wait(&acc_empty[i], ((it >> 1) & 1u) ^ 1u, &abort_flag, a.err) ||
+                        !bar_wait(&full[s], ph, &abort_flag, a.err)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t x0 = xd + s * (kStage >> 4), w0 = wd + s * (kStage >> 4);
+                    const uint32_t d = tmem + i * kAccCols;
+                    tc_mma_f8_pair(d, x0, w0, idesc, 0u);
+                    tc_mma_f8_pair(d, x0 + 2, w0 + 2, idesc, 1u);
+                    tc_mma_f8_pair(d, x0 + 4, w0 + 4, idesc, 1u);
+                    tc_mma_f8_pair(d, x0 + 6, w0 + 6, idesc, 1u);
+                    tc_commit_pair_mc(&empty[s], 0x3);
+                    tc_commit_pair_mc(&acc_full[i], 0x3);
+                    if (++s == (uint32_t)a.stages) s = 0, ph ^= 1u;
+                }
+            }
+            if (!ok) {  // the MMAs already issued finish before TMEM is released
+                tc_commit_pair(&drain);
+                wait_drain(&drain, 0);
+            }
+        }
+    } else {
+        regs_take<232>();
+        const int quarter = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t empty_leader[2] = {mapa_shared(smem_u32(&acc_empty[0]), 0),
+                                          mapa_shared(smem_u32(&acc_empty[1]), 0)};
+        const uint32_t tbase = tmem + (uint32_t)(half * kHalf) + ((uint32_t)(quarter * 32) << 16);
+        uint32_t it = 0;
+        bool ok = true;
+        for (int w = pair; w < total && ok; w += pairs) {
+            int mt, nt;
+            tile_of(w, &mt, &nt);
+            const int64_t m = (int64_t)mt * 256 + (int)rank * 128 + quarter * 32 + lane;
+            const int n0 = nt * kCols + half * kHalf;
+            const float *xs = a.xs + min(m, (int64_t)a.rows - 1) * a.blocks;
+            const float *ws[kScales];
+#pragma unroll
+            for (int c = 0; c < kScales; ++c)  // columns past the end take the last block's scales
+                ws[c] = a.ws + (int64_t)(min(n0 + 32 * c, a.n_out - 1) / 128) * a.blocks;
+            uint64_t sum[kHalf / 2];
+#pragma unroll
+            for (int i = 0; i < kHalf / 2; ++i) sum[i] = 0;
+            float x_next = __ldg(xs), w_next[kScales];
+#pragma unroll
+            for (int c = 0; c < kScales; ++c) w_next[c] = __ldg(ws[c]);
+            for (int b = 0; b < a.blocks; ++b, ++it) {
+                uint64_t f[kScales];
+#pragma unroll
+                for (int c = 0; c < kScales; ++c) {
+                    const float v = x_next * w_next[c];
+                    f[c] = f2(v, v);
+                }
+                if (b + 1 < a.blocks) {  // the next block's scales, ahead of the wait
+                    x_next = __ldg(xs + b + 1);
+#pragma unroll
+                    for (int c = 0; c < kScales; ++c) w_next[c] = __ldg(ws[c] + b + 1);
+                }
+                const uint32_t i = it & 1u;
+                if (!bar_wait(&acc_full[i], (it >> 1) & 1u, &abort_flag, a.err)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t t = tbase + i * kAccCols;
+                uint32_t r[2][32];
+                tmem_ld32(t, r[0]);
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    tmem_ld_wait();
+                    tmem_tie(r[c & 1]);
+                    if (c + 1 < kChunks) {
+                        tmem_ld32(t + 32 * (c + 1), r[(c + 1) & 1]);
+                    } else {  // all read: the accumulator goes back
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(empty_leader[i]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        sum[16 * c + j] = fma2(f[kScales == 1 ? 0 : c], f2(r[c & 1][2 * j], r[c & 1][2 * j + 1]),
+                                               sum[16 * c + j]);
+                }
+            }
+            if (ok && m < a.rows) {
+                T *y = (T *)a.y + m * a.n_out + n0;
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) store32(y + 32 * c, a.n_out - n0 - 32 * c, a.vec, sum + 16 * c);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // no CTA leaves while its peer may still touch its shared memory
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 2 * kAccCols);
+    }
+}
+
+// ---- few rows --------------------------------------------------------------------
+// Roles (192 threads): warp 0 loads, warp 1 issues the MMAs, warps 2 to 5 scale and add:
+// a thread owns one output column and kN rows of x.  A block's factors xs * ws lie in a
+// table of the warp's own, made from scales loaded two blocks ahead.
+constexpr int kFewThreads = 192;
+constexpr int kFewMaxSplit = 8;
+
+template <int kN> constexpr uint32_t kFewStage = kBoxBytes + kN * 128;
+
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+template <typename T, int kN>
+__global__ void __launch_bounds__(kFewThreads, kN <= 64 ? 2 : 1)
+    linear_few_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                      const LinearArgs a, const int split) {
+    constexpr int kChunk = kN < 32 ? kN : 32, kPer = (kN + 31) / 32;
+    constexpr uint32_t kAccCols = kN < 32 ? 32 : kN;
+    constexpr uint32_t kStage = kFewStage<kN>;
+    extern __shared__ uint8_t dsmem[];
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+    __shared__ __align__(16) float factor[4][2][kN];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~(uintptr_t)1023);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = blockIdx.x % split;  // the CTA's rank in its cluster
+    const int tile = blockIdx.x / split;
+    const int nt = tile % a.n_tiles, mt = tile / a.n_tiles;
+    const int b0 = (int)((int64_t)a.blocks * rank / split), b1 = (int)((int64_t)a.blocks * (rank + 1) / split);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < a.stages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_empty[i], 4);
+        mbar_init(&drain, 1);
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(&tmem_slot, 2 * kAccCols);
+        tmem_relinquish();
+    }
+    if (warp == 1 && lane == 0) prefetch_tmap(&tm_x), prefetch_tmap(&tm_w);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    // the rows' scales and codes wait for the kernel before; the weights need not where
+    // that one is this call's own quantisation
+    if (!(a.early && warp == 0)) grid_dep_wait();
+
+    float sum[kN];
+    if (warp == 0) {
+        if (lane == 0) {
+            const auto arm = [&](int b, uint32_t s) {
+                mbar_arrive_expect_tx(&full[s], kStage);
+                tma_load_2d(smem + s * kStage, &tm_w, &full[s], b * 128, nt * 128);
+            };
+            const auto load_x = [&](int b, uint32_t s) {
+                tma_load_2d(smem + s * kStage + kBoxBytes, &tm_x, &full[s], b * 128, mt * kN);
+            };
+            const int first = min(b1 - b0, a.stages);  // stages that nothing has used yet
+            for (int i = 0; i < first; ++i) arm(b0 + i, (uint32_t)i);
+            if (a.early) grid_dep_wait();
+            for (int i = 0; i < first; ++i) load_x(b0 + i, (uint32_t)i);
+            uint32_t issued = (uint32_t)first, s = 0, ph = 0;
+            for (int b = b0 + first; b < b1; ++b) {
+                if (!bar_wait(&empty[s], ph, &abort_flag, a.err)) break;
+                arm(b, s);
+                load_x(b, s);
+                ++issued;
+                if (++s == (uint32_t)a.stages) s = 0, ph ^= 1u;
+            }
+            drain_loads(full, issued, (uint32_t)a.stages);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = idesc_e4m3(128, kN);
+            const uint64_t wd = sw128_desc(smem_u32(smem)), xd = sw128_desc(smem_u32(smem + kBoxBytes));
+            uint32_t s = 0, ph = 0;
+            for (int b = b0; b < b1; ++b) {
+                const uint32_t it = (uint32_t)(b - b0), i = it & 1u;
+                if (!bar_wait(&acc_empty[i], ((it >> 1) & 1u) ^ 1u, &abort_flag, a.err) ||
+                    !bar_wait(&full[s], ph, &abort_flag, a.err)) {
+                    tc_commit(&drain);
+                    wait_drain(&drain, 0);
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t w0 = wd + s * (kStage >> 4), x0 = xd + s * (kStage >> 4);
+                const uint32_t d = tmem + i * kAccCols;
+                tc_mma_f8(d, w0, x0, idesc, 0u);
+                tc_mma_f8(d, w0 + 2, x0 + 2, idesc, 1u);
+                tc_mma_f8(d, w0 + 4, x0 + 4, idesc, 1u);
+                tc_mma_f8(d, w0 + 6, x0 + 6, idesc, 1u);
+                tc_commit(&empty[s]);
+                tc_commit(&acc_full[i]);
+                if (++s == (uint32_t)a.stages) s = 0, ph ^= 1u;
+            }
+        }
+    } else {
+        const int quarter = warp & 3;
+        float(*table)[kN] = factor[quarter];
+        const uint32_t tbase = tmem + ((uint32_t)(quarter * 32) << 16);
+        const float *ws = a.ws + (int64_t)nt * a.blocks;
+        const float *xs[kPer];
+        bool in[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int64_t m = (int64_t)mt * kN + i * 32 + lane;
+            in[i] = m < a.rows && i * 32 + lane < kN;
+            xs[i] = a.xs + (in[i] ? m : 0) * a.blocks;
+        }
+        const auto scales = [&](int b, float (&f)[kPer]) {
+            const float w = __ldg(ws + b);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) f[i] = in[i] ? __ldg(xs[i] + b) * w : 0.0f;
+        };
+        uint64_t acc[kN / 2];
+#pragma unroll
+        for (int i = 0; i < kN / 2; ++i) acc[i] = 0;
+        float f0[kPer], f1[kPer];  // of this block and the next
+        if (b0 < b1) scales(b0, f0);
+        if (b0 + 1 < b1) scales(b0 + 1, f1);
+        for (int b = b0; b < b1; ++b) {
+            const uint32_t it = (uint32_t)(b - b0), i = it & 1u;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                if (k * 32 + lane < kN) table[i][k * 32 + lane] = f0[k];
+                f0[k] = f1[k];
+            }
+            if (b + 2 < b1) scales(b + 2, f1);
+            __syncwarp();
+            if (!bar_wait(&acc_full[i], (it >> 1) & 1u, &abort_flag, a.err)) break;
+            tc_fence_after();
+            const uint32_t t = tbase + i * kAccCols;
+#pragma unroll
+            for (int c = 0; c < kN / kChunk; ++c) {
+                uint32_t r[kChunk];
+                if constexpr (kChunk == 32)
+                    tmem_ld32(t + 32 * c, r);
+                else
+                    tmem_ld16(t, r);
+                tmem_ld_wait();
+                if constexpr (kChunk == 32)
+                    tmem_tie(r);
+                else
+                    tmem_tie16(r);
+                if (c + 1 == kN / kChunk) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&acc_empty[i]);
+                }
+#pragma unroll
+                for (int j = 0; j < kChunk / 4; ++j) {
+                    const float4 f = *reinterpret_cast<const float4 *>(&table[i][kChunk * c + 4 * j]);
+                    uint64_t *s2 = acc + (kChunk * c) / 2 + 2 * j;
+                    s2[0] = fma2(f2(f.x, f.y), f2(r[4 * j], r[4 * j + 1]), s2[0]);
+                    s2[1] = fma2(f2(f.z, f.w), f2(r[4 * j + 2], r[4 * j + 3]), s2[1]);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kN / 2; ++i) unf2(acc[i], sum[2 * i], sum[2 * i + 1]);
+    }
+
+    // The sums of the cluster's CTAs, added in the order of the blocks: each CTA leaves its
+    // own in shared memory (its stages are done with) and takes a share of the rows.
+    const int row = ((warp & 3) * 32 + lane);  // epilogue warps: the output column in the tile
+    const int64_t n = (int64_t)nt * 128 + row;
+    const int m0 = mt * kN, live = min(kN, a.rows - m0);
+    T *y = (T *)a.y + (int64_t)m0 * a.n_out + n;
+    tc_fence_before();
+    if (split == 1) {
+        if (warp >= 2 && n < a.n_out) {
+#pragma unroll
+            for (int j = 0; j < kN; ++j)
+                if (j < live) from_f32(y + (int64_t)j * a.n_out, sum[j]);
+        }
+        __syncthreads();
+    } else {
+        float *part = reinterpret_cast<float *>(smem);
+        __syncthreads();  // the loads have landed and been read, on the failing path too
+        if (warp >= 2) {
+#pragma unroll
+            for (int j = 0; j < kN; ++j)
+                if (j < live) part[j * 128 + row] = sum[j];
+        }
+        cluster_sync();
+        if (warp >= 2 && n < a.n_out) {
+            const uint32_t mine = smem_u32(part) + (uint32_t)row * 4;
+            for (int j = live * rank / split; j < live * (rank + 1) / split; ++j) {
+                float v[kFewMaxSplit], s = 0.0f;
+#pragma unroll
+                for (int c = 0; c < kFewMaxSplit; ++c)
+                    v[c] = c < split ? ld_cluster(mapa_shared(mine + (uint32_t)j * 512, (uint32_t)c)) : 0.0f;
+#pragma unroll
+                for (int c = 0; c < kFewMaxSplit; ++c)
+                    if (c < split) s += v[c];
+                from_f32(y + (int64_t)j * a.n_out, s);
+            }
+        }
+        __syncwarp();
+        cluster_sync();  // no CTA leaves while another reads its sums
+    }
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 2 * kAccCols);
+    }
+}
+
+// ---- launches ----------------------------------------------------------------------
+constexpr int kSmemMost = 220 * 1024;
+
+template <typename T, int kCols>
+dflash2_status launch_pair(const DeviceInfo &di, const uint8_t *xq, const uint8_t *wq, int32_t n_in, LinearArgs a,
+                           cudaStream_t st) {
+    static std::atomic<uint64_t> allowed{0};
+    constexpr uint32_t stage = kPairStage<kCols>;
+    a.stages = min(kMaxStages, (int)((kSmemMost - 1024) / stage));
+    a.m_tiles = (a.rows + 255) / 256, a.n_tiles = (a.n_out + kCols - 1) / kCols;
+    CUtensorMap tm_x, tm_w;
+    dflash2_status s = encode_tmap_2d(&tm_x, xq, (uint64_t)a.rows, (uint64_t)n_in, 128, 1);
+    if (s == DFLASH2_OK) s = encode_tmap_2d(&tm_w, wq, (uint64_t)a.n_out, (uint64_t)n_in, kCols / 2, 1);
+    if (s == DFLASH2_OK) s = allow_smem(linear_pair_kernel<T, kCols>, kSmemMost, di.device, allowed);
+    if (s != DFLASH2_OK) return s;
+    const int64_t total = (int64_t)a.m_tiles * a.n_tiles;
+    if (total > INT32_MAX / 2) return DFLASH2_ERR_INVALID_ARG;
+    const int pairs = (int)min((int64_t)di.sm_count / 2, total);
+    launch_k(linear_pair_kernel<T, kCols>, dim3(2 * pairs), dim3(kPairThreads), a.stages * stage + 1024, st, tm_x, tm_w,
+             a);
     return launch_status();
+}
+
+template <typename T, int kN>
+dflash2_status launch_few(const DeviceInfo &di, const uint8_t *xq, const uint8_t *wq, int32_t n_in, LinearArgs a,
+                          cudaStream_t st) {
+    static std::atomic<uint64_t> allowed{0};
+    constexpr uint32_t stage = kFewStage<kN>;
+    constexpr int most = kN <= 64 ? 108 * 1024 : kSmemMost;  // two CTAs per SM, or one
+    a.stages = min(kMaxStages, (int)((most - 1024) / stage));
+    a.m_tiles = (a.rows + kN - 1) / kN, a.n_tiles = (a.n_out + 127) / 128;
+    const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles;
+    if (tiles > INT32_MAX / kFewMaxSplit) return DFLASH2_ERR_INVALID_ARG;
+    int split = 1;
+    while (split < kFewMaxSplit && tiles * split * 2 <= 2 * di.sm_count && a.blocks >= 4 * split) split *= 2;
+    CUtensorMap tm_x, tm_w;
+    dflash2_status s = encode_tmap_2d(&tm_x, xq, (uint64_t)a.rows, (uint64_t)n_in, kN, 1);
+    if (s == DFLASH2_OK) s = encode_tmap_2d(&tm_w, wq, (uint64_t)a.n_out, (uint64_t)n_in, 128, 1);
+    if (s == DFLASH2_OK) s = allow_smem(linear_few_kernel<T, kN>, most, di.device, allowed);
+    if (s != DFLASH2_OK) return s;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * split));
+    cfg.blockDim = dim3(kFewThreads);
+    cfg.dynamicSmemBytes = a.stages * stage + 1024;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)split, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    cudaLaunchKernelEx(&cfg, linear_few_kernel<T, kN>, tm_x, tm_w, a, split);
+    return launch_status();
+}
+
+template <typename T>
+dflash2_status launch_linear(const DeviceInfo &di, const uint8_t *xq, const uint8_t *wq, int32_t n_in,
+                             const LinearArgs &a, cudaStream_t st) {
+    if (a.rows <= 16) return launch_few<T, 16>(di, xq, wq, n_in, a, st);
+    if (a.rows <= 32) return launch_few<T, 32>(di, xq, wq, n_in, a, st);
+    if (a.rows <= 64) return launch_few<T, 64>(di, xq, wq, n_in, a, st);
+    if (a.rows <= 128) return launch_few<T, 128>(di, xq, wq, n_in, a, st);
+    return launch_pair<T, 256>(di, xq, wq, n_in, a, st);
 }
 
 bool shape_ok(int64_t rows, int32_t n_in, int32_t n_out) {
@@ -104,16 +574,19 @@ extern "C" dflash2_status dflash2_linear_fp8_blocks(const void *x, int64_t x_row
     st = current_device(&di);
     if (st != DFLASH2_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    LinearArgs a{};
     if (!x_q) {
         uint8_t *q = static_cast<uint8_t *>(workspace);
         float *scale = reinterpret_cast<float *>(q + codes_bytes(rows, in_features));
         st = launch_quant_blocks_e4m3(x, x_row_stride, x_dtype, rows, in_features, q, scale, s);
         if (st != DFLASH2_OK) return st;
         x_q = q, x_scale = scale;
+        a.early = true;
     }
-    LinearArgs a{};
-    a.xq = x_q, a.wq = w_q, a.xs = x_scale, a.ws = w_scale;
-    a.rows = (int32_t)rows, a.n_in = in_features, a.n_out = out_features, a.blocks = (in_features + 127) / 128;
+    a.xs = x_scale, a.ws = w_scale;
+    a.rows = (int32_t)rows, a.n_out = out_features, a.blocks = (in_features + 127) / 128;
     a.y = out, a.err = err_word;
-    return out_dtype == DFLASH2_F32 ? launch_linear<float>(a, s) : launch_linear<__nv_bfloat16>(a, s);
+    a.vec = aligned16(out) && (int64_t)out_features * (out_dtype == DFLASH2_F32 ? 4 : 2) % 16 == 0;
+    return out_dtype == DFLASH2_F32 ? launch_linear<float>(di, x_q, w_q, in_features, a, s)
+                                    : launch_linear<__nv_bfloat16>(di, x_q, w_q, in_features, a, s);
 }

@@ -236,6 +236,7 @@ __global__ void __launch_bounds__(kQuantThreads)
     quantise_rows_kernel(const T *x, int64_t stride, int64_t rows, int32_t cols, uint8_t *q, float *scale,
                          bool code_vec) {
     grid_dep_wait();
+    grid_dep_launch();  // a product that follows loads its weights meanwhile
     const int nb = (cols + kQuantBlock - 1) / kQuantBlock;
     const int64_t b = ((int64_t)blockIdx.x * kQuantThreads + threadIdx.x) / kQuantLanes;
     const bool live = b < rows * nb;
