@@ -228,7 +228,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     } else {  // all read: the accumulator goes back
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(empty_leader[i]);
+                        if (lane == 0) mbar_arrive_cluster_relaxed(empty_leader[i]);
                     }
 #pragma unroll
                     for (int j = 0; j < 16; ++j)

@@ -101,6 +101,13 @@ __device__ __forceinline__ void tmem_tie4(uint32_t (&r)[4]) {
 }
 __device__ __forceinline__ void tmem_tie8(uint32_t *r) { asm volatile("" : DF_OUT8(DF_TIE, r)); }
 
+// Arrive on an mbarrier of a CTA of the cluster that hands over TMEM alone, after
+// tc_fence_before: nothing in memory is published, and a release at cluster scope would
+// wait for the loads that the thread has in flight.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // Register split of a warpgroup, inside its branch (ptxas allots a branch what it sees there).
 template <int kN> __device__ __forceinline__ void regs_give() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kN));
