@@ -66,11 +66,12 @@ template <typename T> __device__ __forceinline__ void store32(T *p, int n, bool 
 }
 
 // ---- many rows -----------------------------------------------------------------
-// Roles (384 threads, one CTA per SM, persistent over tiles): warp 0 loads, warp 1 of the
-// leader issues the MMAs, warps 4 to 11 scale and add: four lane quarters, each with two
+// Roles (384 threads, one CTA per SM, persistent over tiles): warp 0 loads, warps 1 and 2
+// of the leader issue the MMAs, warps 4 to 11 scale and add: four lane quarters, each with two
 // warps that take half of the tile's columns, kCols / 2 sums a thread.
 constexpr int kPairThreads = 384;
 constexpr int kPairEpiWarps = 8;
+constexpr int kIssuers = 2;
 
 template <int kCols> constexpr uint32_t kPairStage = kBoxBytes + kCols / 2 * 128;
 
@@ -84,7 +85,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     constexpr uint32_t kAccCols = kCols <= 32 ? 32 : kCols <= 64 ? 64 : kCols <= 128 ? 128 : 256;
     constexpr uint32_t kStage = kPairStage<kCols>;
     extern __shared__ uint8_t dsmem[];
-    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain[kIssuers];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~(uintptr_t)1023);
@@ -94,7 +95,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
         for (int i = 0; i < 2; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_empty[i], 2 * kPairEpiWarps);
-        mbar_init(&drain, 1);
+        for (int i = 0; i < kIssuers; ++i) mbar_init(&drain[i], 1);
         abort_flag = 0;
         fence_mbar_init();
     }
@@ -144,34 +145,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 }
             }
             if (rank == 0) drain_loads(full, issued, (uint32_t)a.stages);
-        } else if (warp == 1 && lane == 0 && rank == 0) {
-            const uint32_t idesc = idesc_e4m3(256, kCols);
+        } else if (warp <= kIssuers && lane == 0 && rank == 0) {
+            const uint32_t idesc = idesc_e4m3(256, kCols), i = (uint32_t)warp - 1;
             const uint64_t xd = sw128_desc(smem_u32(smem)), wd = sw128_desc(smem_u32(smem + kBoxBytes));
-            uint32_t s = 0, ph = 0, it = 0;
+            const uint32_t d = tmem + i * kAccCols;
+            uint32_t s = i, ph = 0, turn = 0;
             bool ok = true;
-            for (int w = pair; w < total && ok; w += pairs) {
-                for (int b = 0; b < a.blocks; ++b, ++it) {
-                    const uint32_t i = it & 1u;
-                    if (!bar_wait(&acc_empty[i], ((it >> 1) & 1u) ^ 1u, &abort_flag, a.err) ||
-                        !bar_wait(&full[s], ph, &abort_flag, a.err)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint64_t x0 = xd + s * (kStage >> 4), w0 = wd + s * (kStage >> 4);
-                    const uint32_t d = tmem + i * kAccCols;
-                    tc_mma_f8_pair(d, x0, w0, idesc, 0u);
-                    tc_mma_f8_pair(d, x0 + 2, w0 + 2, idesc, 1u);
-                    tc_mma_f8_pair(d, x0 + 4, w0 + 4, idesc, 1u);
-                    tc_mma_f8_pair(d, x0 + 6, w0 + 6, idesc, 1u);
-                    tc_commit_pair_mc(&empty[s], 0x3);
-                    tc_commit_pair_mc(&acc_full[i], 0x3);
-                    if (++s == (uint32_t)a.stages) s = 0, ph ^= 1u;
+            const uint32_t mine = (uint32_t)(((int64_t)(total - pair + pairs - 1) / pairs * a.blocks + 1 - i) / 2);
+            for (; turn < mine; ++turn) {
+                if (!bar_wait(&acc_empty[i], (turn & 1u) ^ 1u, &abort_flag, a.err) ||
+                    !bar_wait(&full[s], ph, &abort_flag, a.err)) {
+                    ok = false;
+                    break;
                 }
+                tc_fence_after();
+                const uint64_t x0 = xd + s * (kStage >> 4), w0 = wd + s * (kStage >> 4);
+                tc_mma_f8_pair(d, x0, w0, idesc, 0u);
+                tc_mma_f8_pair(d, x0 + 2, w0 + 2, idesc, 1u);
+                tc_mma_f8_pair(d, x0 + 4, w0 + 4, idesc, 1u);
+                tc_mma_f8_pair(d, x0 + 6, w0 + 6, idesc, 1u);
+                tc_commit_pair_mc(&acc_full[i], 0x3);
+                tc_commit_pair_mc(&empty[s], 0x3);
+                s += 2;
+                if (s >= (uint32_t)a.stages) s -= (uint32_t)a.stages, ph ^= 1u;
             }
             if (!ok) {  // the MMAs already issued finish before TMEM is released
-                tc_commit_pair(&drain);
-                wait_drain(&drain, 0);
+                tc_commit_pair(&drain[i]);
+                wait_drain(&drain[i], 0);
             }
         }
     } else {
@@ -217,23 +217,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 }
                 tc_fence_after();
                 const uint32_t t = tbase + i * kAccCols;
+                // two loads of 32 columns in flight; the next two are issued between the
+                // sums, so that a block waits for TMEM twice
                 uint32_t r[2][32];
                 tmem_ld32(t, r[0]);
+                if (kChunks > 1) tmem_ld32(t + 32, r[1]);
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c) {
-                    tmem_ld_wait();
-                    tmem_tie(r[c & 1]);
-                    if (c + 1 < kChunks) {
-                        tmem_ld32(t + 32 * (c + 1), r[(c + 1) & 1]);
-                    } else {  // all read: the accumulator goes back
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster_relaxed(empty_leader[i]);
+                    if (c % 2 == 0) {
+                        tmem_ld_wait();
+                        tmem_tie(r[0]);
+                        if (c + 1 < kChunks) tmem_tie(r[1]);
+                        if (c + 2 >= kChunks) {  // all read: the accumulator goes back
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive_cluster_relaxed(empty_leader[i]);
+                        }
                     }
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
                         sum[16 * c + j] = fma2(f[kScales == 1 ? 0 : c], f2(r[c & 1][2 * j], r[c & 1][2 * j + 1]),
                                                sum[16 * c + j]);
+                    if (c + 2 < kChunks) tmem_ld32(t + 32 * (c + 2), r[c & 1]);
                 }
             }
             if (ok && m < a.rows) {
