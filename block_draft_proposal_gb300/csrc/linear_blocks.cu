@@ -25,7 +25,7 @@ struct LinearArgs {
     void *y;
     int32_t *err;
     int32_t m_tiles, n_tiles, stages;
-    bool vec;    // rows of y are 16-byte aligned
+    bool vec;    // results go out by TMA (rows of y are 16-byte aligned)
     bool early;  // the weights may be read before the kernel before this one is done
 };
 
@@ -45,44 +45,74 @@ __device__ __forceinline__ void drain_loads(uint64_t *full, uint32_t issued, uin
         wait_drain(&full[n % stages], (n / stages) & 1u);
 }
 
-// 32 results of one row from p on, n of them inside.
-template <typename T> __device__ __forceinline__ void store32(T *p, int n, bool vec, const uint64_t *v) {
-    float x[32];
+// 32 results of one row from p on, n of them inside, value by value.
+template <typename T> __device__ __forceinline__ void store32(T *p, int n, const uint64_t *v) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) unf2(v[i], x[2 * i], x[2 * i + 1]);
-    if (vec && n >= 32) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float y[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = x[8 * i + j];
-            store8(p + 8 * i, y);
-        }
-        return;
+    for (int i = 0; i < 16; ++i) {
+        float lo, hi;
+        unf2(v[i], lo, hi);
+        if (2 * i < n) from_f32(p + 2 * i, lo);
+        if (2 * i + 1 < n) from_f32(p + 2 * i + 1, hi);
     }
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-        if (i < n) from_f32(p + i, x[i]);
 }
 
 // ---- many rows -----------------------------------------------------------------
 // Roles (384 threads, one CTA per SM, persistent over tiles): warp 0 loads, warps 1 and 2
-// of the leader issue the MMAs, warps 4 to 11 scale and add: four lane quarters, each with two
-// warps that take half of the tile's columns, kCols / 2 sums a thread.
+// of the leader issue the MMAs, warps 4 to 11 scale and add: four lane quarters, each with
+// two warps that take half of the tile's columns, kCols / 2 sums a thread.
 constexpr int kPairThreads = 384;
 constexpr int kPairEpiWarps = 8;
-constexpr int kIssuers = 2;
+constexpr int kIssuers = 2;  // of the even and of the odd blocks
 
 template <int kCols> constexpr uint32_t kPairStage = kBoxBytes + kCols / 2 * 128;
+constexpr uint32_t kOutBytes = 4096;  // an epilogue warp's results on their way out
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, uint32_t src, int32_t c0, int32_t c1) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, 0}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(src), "r"(c0), "r"(c1)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int kLeft> __device__ __forceinline__ void bulk_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kLeft) : "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// 32 results of the lane's row, in 16-byte units of T; into row `lane` of a [32][32] tile
+// with the store's swizzle (rows of 64 bytes: unit ^ (row / 2) % 4; of 128: unit ^ row % 8).
+__device__ __forceinline__ void stage32(uint8_t *tile, int lane, const uint64_t *v, __nv_bfloat16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float lo, hi;
+            unf2(v[4 * i + j], lo, hi);
+            const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+            w[j] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+        *reinterpret_cast<uint4 *>(tile + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+__device__ __forceinline__ void stage32(uint8_t *tile, int lane, const uint64_t *v, float) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float4 f;
+        unf2(v[2 * i], f.x, f.y);
+        unf2(v[2 * i + 1], f.z, f.w);
+        *reinterpret_cast<float4 *>(tile + lane * 128 + ((i ^ (lane & 7)) << 4)) = f;
+    }
+}
 
 template <typename T, int kCols>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
-                       const LinearArgs a) {
+                       const __grid_constant__ CUtensorMap tm_y, const LinearArgs a) {
     constexpr int kHalf = kCols / 2, kChunks = kHalf / 32;
     // weight blocks of 128 that a thread's columns lie in
     constexpr int kScales = 128 % kHalf == 0 ? 1 : kChunks;
-    constexpr uint32_t kAccCols = kCols <= 32 ? 32 : kCols <= 64 ? 64 : kCols <= 128 ? 128 : 256;
+    constexpr uint32_t kAccCols = kCols <= 64 ? 64 : kCols <= 128 ? 128 : 256;
     constexpr uint32_t kStage = kPairStage<kCols>;
     extern __shared__ uint8_t dsmem[];
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain[kIssuers];
@@ -103,7 +133,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         tmem_alloc_pair(&tmem_slot, 2 * kAccCols);
         tmem_relinquish_pair();
     }
-    if (warp == 1 && lane == 0) prefetch_tmap(&tm_x), prefetch_tmap(&tm_w);
+    if (warp == 1 && lane == 0) prefetch_tmap(&tm_x), prefetch_tmap(&tm_w), prefetch_tmap(&tm_y);
     tc_fence_before();
     __syncthreads();
     cluster_sync();
@@ -145,16 +175,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 }
             }
             if (rank == 0) drain_loads(full, issued, (uint32_t)a.stages);
-        } else if (warp <= kIssuers && lane == 0 && rank == 0) {
+        } else if (warp >= 1 && warp <= kIssuers && lane == 0 && rank == 0) {
             const uint32_t idesc = idesc_e4m3(256, kCols), i = (uint32_t)warp - 1;
             const uint64_t xd = sw128_desc(smem_u32(smem)), wd = sw128_desc(smem_u32(smem + kBoxBytes));
             const uint32_t d = tmem + i * kAccCols;
-            uint32_t s = i, ph = 0, turn = 0;
+            // of the pair's blocks, tile after tile, every other one
+            const uint32_t all = (uint32_t)((int64_t)((total - pair + pairs - 1) / pairs) * a.blocks);
+            uint32_t s = i, ph = 0;
             bool ok = true;
-            const uint32_t mine = (uint32_t)(((int64_t)(total - pair + pairs - 1) / pairs * a.blocks + 1 - i) / 2);
-            for (; turn < mine; ++turn) {
-                if (!bar_wait(&acc_empty[i], (turn & 1u) ^ 1u, &abort_flag, a.err) ||
-                    !bar_wait(&full[s], ph, &abort_flag, a.err)) {
+            for (uint32_t it = i; it < all; it += 2) {
+                // the operands first: they are there long before the accumulator is free
+                if (!bar_wait(&full[s], ph, &abort_flag, a.err) ||
+                    !bar_wait(&acc_empty[i], ((it >> 1) & 1u) ^ 1u, &abort_flag, a.err)) {
                     ok = false;
                     break;
                 }
@@ -180,12 +212,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const uint32_t empty_leader[2] = {mapa_shared(smem_u32(&acc_empty[0]), 0),
                                           mapa_shared(smem_u32(&acc_empty[1]), 0)};
         const uint32_t tbase = tmem + (uint32_t)(half * kHalf) + ((uint32_t)(quarter * 32) << 16);
-        uint32_t it = 0;
+        uint8_t *out = smem + (uint32_t)a.stages * kStage + (uint32_t)(warp - 4) * kOutBytes;
+        uint32_t it = 0, stored = 0;
         bool ok = true;
         for (int w = pair; w < total && ok; w += pairs) {
             int mt, nt;
             tile_of(w, &mt, &nt);
-            const int64_t m = (int64_t)mt * 256 + (int)rank * 128 + quarter * 32 + lane;
+            const int64_t m0 = (int64_t)mt * 256 + (int)rank * 128 + quarter * 32, m = m0 + lane;
             const int n0 = nt * kCols + half * kHalf;
             const float *xs = a.xs + min(m, (int64_t)a.rows - 1) * a.blocks;
             const float *ws[kScales];
@@ -241,12 +274,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     if (c + 2 < kChunks) tmem_ld32(t + 32 * (c + 2), r[c & 1]);
                 }
             }
-            if (ok && m < a.rows) {
+            if (!ok) break;
+            if (a.vec) {
+                // 32 columns at a time through shared memory and out by TMA, which writes
+                // whole lines while the next tile begins (stores of 16 bytes a lane held the
+                // warps up: 349 us in place of 306) and leaves out what is past the end
+                constexpr int kBufs = (int)(kOutBytes / (1024 * sizeof(T)));
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    uint8_t *buf = out + (stored++ % kBufs) * (1024 * sizeof(T));
+                    if (lane == 0) bulk_wait_read<kBufs - 1>();
+                    __syncwarp();
+                    stage32(buf, lane, sum + 16 * c, T());
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (m0 < a.rows && n0 + 32 * c < a.n_out)
+                            tma_store_3d(&tm_y, smem_u32(buf), (n0 + 32 * c) * (int)sizeof(T), (int)m0);
+                        bulk_commit();
+                    }
+                }
+            } else if (m < a.rows) {
                 T *y = (T *)a.y + m * a.n_out + n0;
 #pragma unroll
-                for (int c = 0; c < kChunks; ++c) store32(y + 32 * c, a.n_out - n0 - 32 * c, a.vec, sum + 16 * c);
+                for (int c = 0; c < kChunks; ++c) store32(y + 32 * c, a.n_out - n0 - 32 * c, sum + 16 * c);
             }
         }
+        if (lane == 0) bulk_wait_all();
     }
     tc_fence_before();
     __syncthreads();
@@ -472,25 +526,33 @@ __global__ void __launch_bounds__(kFewThreads, kN <= 64 ? 2 : 1)
 }
 
 // ---- launches ----------------------------------------------------------------------
-constexpr int kSmemMost = 220 * 1024;
+constexpr int kSmemMost = 226 * 1024;  // with the barriers and the 1 KB the system takes: 227
 
 template <typename T, int kCols>
 dflash2_status launch_pair(const DeviceInfo &di, const uint8_t *xq, const uint8_t *wq, int32_t n_in, LinearArgs a,
                            cudaStream_t st) {
     static std::atomic<uint64_t> allowed{0};
     constexpr uint32_t stage = kPairStage<kCols>;
-    a.stages = min(kMaxStages, (int)((kSmemMost - 1024) / stage));
+    constexpr uint32_t outs = 8 * kOutBytes;
+    a.stages = min(kMaxStages, (int)((kSmemMost - 1024 - outs) / stage));
     a.m_tiles = (a.rows + 255) / 256, a.n_tiles = (a.n_out + kCols - 1) / kCols;
-    CUtensorMap tm_x, tm_w;
-    dflash2_status s = encode_tmap_2d(&tm_x, xq, (uint64_t)a.rows, (uint64_t)n_in, 128, 1);
-    if (s == DFLASH2_OK) s = encode_tmap_2d(&tm_w, wq, (uint64_t)a.n_out, (uint64_t)n_in, kCols / 2, 1);
-    if (s == DFLASH2_OK) s = allow_smem(linear_pair_kernel<T, kCols>, kSmemMost, di.device, allowed);
-    if (s != DFLASH2_OK) return s;
     const int64_t total = (int64_t)a.m_tiles * a.n_tiles;
     if (total > INT32_MAX / 2) return DFLASH2_ERR_INVALID_ARG;
+    CUtensorMap tm_x, tm_w, tm_y;
+    dflash2_status s = encode_tmap_2d(&tm_x, xq, (uint64_t)a.rows, (uint64_t)n_in, 128, 1);
+    if (s == DFLASH2_OK) s = encode_tmap_2d(&tm_w, wq, (uint64_t)a.n_out, (uint64_t)n_in, kCols / 2, 1);
+    // results as bytes, so that one box serves both types
+    const uint64_t bytes = (uint64_t)a.n_out * sizeof(T);
+    a.vec = aligned16(a.y) && bytes % 16 == 0 && bytes * a.rows < 1ull << 40;
+    tm_y = tm_x;
+    if (s == DFLASH2_OK && a.vec)
+        s = encode_tmap_3d(&tm_y, a.y, {bytes, (uint64_t)a.rows, 1}, {bytes, bytes * a.rows},
+                           {32 * (uint32_t)sizeof(T), 32, 1}, 1);
+    if (s == DFLASH2_OK) s = allow_smem(linear_pair_kernel<T, kCols>, kSmemMost, di.device, allowed);
+    if (s != DFLASH2_OK) return s;
     const int pairs = (int)min((int64_t)di.sm_count / 2, total);
-    launch_k(linear_pair_kernel<T, kCols>, dim3(2 * pairs), dim3(kPairThreads), a.stages * stage + 1024, st, tm_x, tm_w,
-             a);
+    launch_k(linear_pair_kernel<T, kCols>, dim3(2 * pairs), dim3(kPairThreads), a.stages * stage + outs + 1024, st,
+             tm_x, tm_w, tm_y, a);
     return launch_status();
 }
 
@@ -499,7 +561,7 @@ dflash2_status launch_few(const DeviceInfo &di, const uint8_t *xq, const uint8_t
                           cudaStream_t st) {
     static std::atomic<uint64_t> allowed{0};
     constexpr uint32_t stage = kFewStage<kN>;
-    constexpr int most = kN <= 64 ? 108 * 1024 : kSmemMost;  // two CTAs per SM, or one
+    constexpr int most = kN <= 64 ? 108 * 1024 : 220 * 1024;  // two CTAs per SM, or one
     a.stages = min(kMaxStages, (int)((most - 1024) / stage));
     a.m_tiles = (a.rows + kN - 1) / kN, a.n_tiles = (a.n_out + 127) / 128;
     const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles;
@@ -591,7 +653,6 @@ extern "C" dflash2_status dflash2_linear_fp8_blocks(const void *x, int64_t x_row
     a.xs = x_scale, a.ws = w_scale;
     a.rows = (int32_t)rows, a.n_out = out_features, a.blocks = (in_features + 127) / 128;
     a.y = out, a.err = err_word;
-    a.vec = aligned16(out) && (int64_t)out_features * (out_dtype == DFLASH2_F32 ? 4 : 2) % 16 == 0;
     return out_dtype == DFLASH2_F32 ? launch_linear<float>(di, x_q, w_q, in_features, a, s)
                                     : launch_linear<__nv_bfloat16>(di, x_q, w_q, in_features, a, s);
 }
