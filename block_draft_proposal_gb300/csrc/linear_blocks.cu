@@ -57,12 +57,13 @@ template <typename T> __device__ __forceinline__ void store32(T *p, int n, const
 }
 
 // ---- many rows -----------------------------------------------------------------
-// Roles (384 threads, one CTA per SM, persistent over tiles): warp 0 loads, warps 1 and 2
-// of the leader issue the MMAs, warps 4 to 11 scale and add: four lane quarters, each with
+// Roles (384 threads, one CTA per SM, persistent over tiles): warps 0 and 3 load, warps 1
+// and 2 of the leader issue the MMAs (a pair of each, for the even and the odd blocks: waits,
+// copies and commits take one thread longer than the MMAs of a block), warps 4 to 11 scale and add: four lane quarters, each with
 // two warps that take half of the tile's columns, kCols / 2 sums a thread.
 constexpr int kPairThreads = 384;
 constexpr int kPairEpiWarps = 8;
-constexpr int kIssuers = 2;  // of the even and of the odd blocks
+constexpr int kIssuers = 2;
 
 template <int kCols> constexpr uint32_t kPairStage = kBoxBytes + kCols / 2 * 128;
 constexpr uint32_t kOutBytes = 4096;  // an epilogue warp's results on their way out
@@ -112,10 +113,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     constexpr int kHalf = kCols / 2, kChunks = kHalf / 32;
     // weight blocks of 128 that a thread's columns lie in
     constexpr int kScales = 128 % kHalf == 0 ? 1 : kChunks;
-    constexpr uint32_t kAccCols = kCols <= 64 ? 64 : kCols <= 128 ? 128 : 256;
+    constexpr uint32_t kAccCols = kCols <= 64 ? 64 : kCols <= 128 ? 128 : 256, kBufs = 512 / kAccCols;
     constexpr uint32_t kStage = kPairStage<kCols>;
     extern __shared__ uint8_t dsmem[];
-    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain[kIssuers];
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[kBufs], acc_empty[kBufs], drain[kIssuers];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~(uintptr_t)1023);
@@ -124,13 +125,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const uint32_t rank = cluster_ctarank();
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_empty[i], 2 * kPairEpiWarps);
+        for (uint32_t i = 0; i < kBufs; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_empty[i], 2 * kPairEpiWarps);
         for (int i = 0; i < kIssuers; ++i) mbar_init(&drain[i], 1);
         abort_flag = 0;
         fence_mbar_init();
     }
     if (warp == 0) {
-        tmem_alloc_pair(&tmem_slot, 2 * kAccCols);
+        tmem_alloc_pair(&tmem_slot, 512);
         tmem_relinquish_pair();
     }
     if (warp == 1 && lane == 0) prefetch_tmap(&tm_x), prefetch_tmap(&tm_w), prefetch_tmap(&tm_y);
@@ -139,6 +140,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     cluster_sync();
     tc_fence_after();
     grid_dep_wait();
+    grid_dep_launch();
     const uint32_t tmem = tmem_slot;
     const int total = a.m_tiles * a.n_tiles, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
@@ -153,40 +155,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     };
 
     if (warp < 4) {
-        regs_give<40>();
-        if (warp == 0 && lane == 0) {
-            uint32_t issued = 0, s = 0, ph = 1;  // the first pass finds every stage free
-            bool ok = true;
-            for (int w = pair; w < total && ok; w += pairs) {
-                int m, n;
-                tile_of(w, &m, &n);
-                for (int b = 0; b < a.blocks; ++b) {
-                    if (!bar_wait(&empty[s], ph, &abort_flag, a.err)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
-                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStage);
-                    uint8_t *st = smem + s * kStage;
-                    tma_load_2d_pair(st, &tm_x, bar, b * 128, m * 256 + (int)rank * 128);
-                    tma_load_2d_pair(st + kBoxBytes, &tm_w, bar, b * 128, n * kCols + (int)rank * kHalf);
-                    ++issued;
-                    if (++s == (uint32_t)a.stages) s = 0, ph ^= 1u;
+        regs_give<56>();
+        // of the pair's blocks, tile after tile, every other one
+        const uint32_t all = (uint32_t)((int64_t)((total - pair + pairs - 1) / pairs) * a.blocks);
+        if ((warp == 0 || warp == 3) && lane == 0) {
+            const uint32_t first = warp == 0 ? 0 : 1;
+            uint32_t it = first, s = first, ph = 1;  // the first pass finds every stage free
+            int w = pair, b = (int)first, m, n;
+            tile_of(w, &m, &n);
+            for (; it < all; it += 2, b += 2) {
+                while (b >= a.blocks) {
+                    b -= a.blocks, w += pairs;
+                    tile_of(w, &m, &n);
                 }
+                if (!bar_wait(&empty[s], ph, &abort_flag, a.err)) break;
+                const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
+                if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStage);
+                uint8_t *st = smem + s * kStage;
+                tma_load_2d_pair(st, &tm_x, bar, b * 128, m * 256 + (int)rank * 128);
+                tma_load_2d_pair(st + kBoxBytes, &tm_w, bar, b * 128, n * kCols + (int)rank * kHalf);
+                s += 2;
+                if (s >= (uint32_t)a.stages) s -= (uint32_t)a.stages, ph ^= 1u;
             }
-            if (rank == 0) drain_loads(full, issued, (uint32_t)a.stages);
+            // no copy of either CTA is still on its way when the leader leaves: the last use
+            // of every stage has landed
+            if (rank == 0) {
+                const uint32_t stages = (uint32_t)a.stages, end = min(it, all), from = end > stages ? end - stages : 0;
+                for (uint32_t k = from + ((from ^ first) & 1u); k < end; k += 2)
+                    wait_drain(&full[k % stages], (k / stages) & 1u);
+            }
         } else if (warp >= 1 && warp <= kIssuers && lane == 0 && rank == 0) {
-            const uint32_t idesc = idesc_e4m3(256, kCols), i = (uint32_t)warp - 1;
+            const uint32_t idesc = idesc_e4m3(256, kCols), first = (uint32_t)warp - 1;
             const uint64_t xd = sw128_desc(smem_u32(smem)), wd = sw128_desc(smem_u32(smem + kBoxBytes));
-            const uint32_t d = tmem + i * kAccCols;
-            // of the pair's blocks, tile after tile, every other one
-            const uint32_t all = (uint32_t)((int64_t)((total - pair + pairs - 1) / pairs) * a.blocks);
-            uint32_t s = i, ph = 0;
+            uint32_t s = first, ph = 0;
             bool ok = true;
-            for (uint32_t it = i; it < all; it += 2) {
+            for (uint32_t it = first; it < all; it += 2) {
+                const uint32_t i = it % kBufs, d = tmem + i * kAccCols;
                 // the operands first: they are there long before the accumulator is free
                 if (!bar_wait(&full[s], ph, &abort_flag, a.err) ||
-                    !bar_wait(&acc_empty[i], ((it >> 1) & 1u) ^ 1u, &abort_flag, a.err)) {
+                    !bar_wait(&acc_empty[i], ((it / kBufs) & 1u) ^ 1u, &abort_flag, a.err)) {
                     ok = false;
                     break;
                 }
@@ -202,15 +209,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 if (s >= (uint32_t)a.stages) s -= (uint32_t)a.stages, ph ^= 1u;
             }
             if (!ok) {  // the MMAs already issued finish before TMEM is released
-                tc_commit_pair(&drain[i]);
-                wait_drain(&drain[i], 0);
+                tc_commit_pair(&drain[first]);
+                wait_drain(&drain[first], 0);
             }
         }
     } else {
-        regs_take<232>();
+        regs_take<224>();
         const int quarter = warp & 3, half = (warp - 4) >> 2;
-        const uint32_t empty_leader[2] = {mapa_shared(smem_u32(&acc_empty[0]), 0),
-                                          mapa_shared(smem_u32(&acc_empty[1]), 0)};
+        const uint32_t empty_leader = mapa_shared(smem_u32(acc_empty), 0);
         const uint32_t tbase = tmem + (uint32_t)(half * kHalf) + ((uint32_t)(quarter * 32) << 16);
         uint8_t *out = smem + (uint32_t)a.stages * kStage + (uint32_t)(warp - 4) * kOutBytes;
         uint32_t it = 0, stored = 0;
@@ -243,8 +249,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
                     for (int c = 0; c < kScales; ++c) w_next[c] = __ldg(ws[c] + b + 1);
                 }
-                const uint32_t i = it & 1u;
-                if (!bar_wait(&acc_full[i], (it >> 1) & 1u, &abort_flag, a.err)) {
+                const uint32_t i = it % kBufs;
+                if (!bar_wait(&acc_full[i], (it / kBufs) & 1u, &abort_flag, a.err)) {
                     ok = false;
                     break;
                 }
@@ -264,7 +270,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         if (c + 2 >= kChunks) {  // all read: the accumulator goes back
                             tc_fence_before();
                             __syncwarp();
-                            if (lane == 0) mbar_arrive_cluster_relaxed(empty_leader[i]);
+                            if (lane == 0) mbar_arrive_cluster_relaxed(empty_leader + 8 * i);
                         }
                     }
 #pragma unroll
@@ -307,7 +313,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     cluster_sync();  // no CTA leaves while its peer may still touch its shared memory
     if (warp == 0) {
         tc_fence_after();
-        tmem_dealloc_pair(tmem, 2 * kAccCols);
+        tmem_dealloc_pair(tmem, 512);
     }
 }
 
@@ -331,10 +337,10 @@ __global__ void __launch_bounds__(kFewThreads, kN <= 64 ? 2 : 1)
     linear_few_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                       const LinearArgs a, const int split) {
     constexpr int kChunk = kN < 32 ? kN : 32, kPer = (kN + 31) / 32;
-    constexpr uint32_t kAccCols = kN < 32 ? 32 : kN;
+    constexpr uint32_t kAccCols = kN < 32 ? 32 : kN, kBufs = 256 / kAccCols;
     constexpr uint32_t kStage = kFewStage<kN>;
     extern __shared__ uint8_t dsmem[];
-    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[kBufs], acc_empty[kBufs], drain;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     __shared__ __align__(16) float factor[4][2][kN];
@@ -347,13 +353,13 @@ __global__ void __launch_bounds__(kFewThreads, kN <= 64 ? 2 : 1)
     const int b0 = (int)((int64_t)a.blocks * rank / split), b1 = (int)((int64_t)a.blocks * (rank + 1) / split);
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_empty[i], 4);
+        for (uint32_t i = 0; i < kBufs; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_empty[i], 4);
         mbar_init(&drain, 1);
         abort_flag = 0;
         fence_mbar_init();
     }
     if (warp == 0) {
-        tmem_alloc(&tmem_slot, 2 * kAccCols);
+        tmem_alloc(&tmem_slot, 256);
         tmem_relinquish();
     }
     if (warp == 1 && lane == 0) prefetch_tmap(&tm_x), prefetch_tmap(&tm_w);
@@ -364,6 +370,7 @@ __global__ void __launch_bounds__(kFewThreads, kN <= 64 ? 2 : 1)
     // the rows' scales and codes wait for the kernel before; the weights need not where
     // that one is this call's own quantisation
     if (!(a.early && warp == 0)) grid_dep_wait();
+    if (warp != 0) grid_dep_launch();
 
     float sum[kN];
     if (warp == 0) {
@@ -395,8 +402,8 @@ __global__ void __launch_bounds__(kFewThreads, kN <= 64 ? 2 : 1)
             const uint64_t wd = sw128_desc(smem_u32(smem)), xd = sw128_desc(smem_u32(smem + kBoxBytes));
             uint32_t s = 0, ph = 0;
             for (int b = b0; b < b1; ++b) {
-                const uint32_t it = (uint32_t)(b - b0), i = it & 1u;
-                if (!bar_wait(&acc_empty[i], ((it >> 1) & 1u) ^ 1u, &abort_flag, a.err) ||
+                const uint32_t it = (uint32_t)(b - b0), i = it % kBufs;
+                if (!bar_wait(&acc_empty[i], ((it / kBufs) & 1u) ^ 1u, &abort_flag, a.err) ||
                     !bar_wait(&full[s], ph, &abort_flag, a.err)) {
                     tc_commit(&drain);
                     wait_drain(&drain, 0);
@@ -439,15 +446,15 @@ __global__ void __launch_bounds__(kFewThreads, kN <= 64 ? 2 : 1)
         if (b0 < b1) scales(b0, f0);
         if (b0 + 1 < b1) scales(b0 + 1, f1);
         for (int b = b0; b < b1; ++b) {
-            const uint32_t it = (uint32_t)(b - b0), i = it & 1u;
+            const uint32_t it = (uint32_t)(b - b0), i = it % kBufs;
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
-                if (k * 32 + lane < kN) table[i][k * 32 + lane] = f0[k];
+                if (k * 32 + lane < kN) table[it & 1u][k * 32 + lane] = f0[k];
                 f0[k] = f1[k];
             }
             if (b + 2 < b1) scales(b + 2, f1);
             __syncwarp();
-            if (!bar_wait(&acc_full[i], (it >> 1) & 1u, &abort_flag, a.err)) break;
+            if (!bar_wait(&acc_full[i], (it / kBufs) & 1u, &abort_flag, a.err)) break;
             tc_fence_after();
             const uint32_t t = tbase + i * kAccCols;
 #pragma unroll
@@ -469,7 +476,7 @@ __global__ void __launch_bounds__(kFewThreads, kN <= 64 ? 2 : 1)
                 }
 #pragma unroll
                 for (int j = 0; j < kChunk / 4; ++j) {
-                    const float4 f = *reinterpret_cast<const float4 *>(&table[i][kChunk * c + 4 * j]);
+                    const float4 f = *reinterpret_cast<const float4 *>(&table[it & 1u][kChunk * c + 4 * j]);
                     uint64_t *s2 = acc + (kChunk * c) / 2 + 2 * j;
                     s2[0] = fma2(f2(f.x, f.y), f2(r[4 * j], r[4 * j + 1]), s2[0]);
                     s2[1] = fma2(f2(f.z, f.w), f2(r[4 * j + 2], r[4 * j + 3]), s2[1]);
@@ -521,7 +528,7 @@ __global__ void __launch_bounds__(kFewThreads, kN <= 64 ? 2 : 1)
     }
     if (warp == 0) {
         tc_fence_after();
-        tmem_dealloc(tmem, 2 * kAccCols);
+        tmem_dealloc(tmem, 256);
     }
 }
 
