@@ -184,7 +184,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 for (uint32_t k = from + ((from ^ first) & 1u); k < end; k += 2)
                     wait_drain(&full[k % stages], (k / stages) & 1u);
             }
-        } else if (warp >= 1 && warp <= kIssuers && lane == 0 && rank == 0) {
+        } else if ((warp == 1 || warp == 2) && rank == 0) {
+            // the whole warp runs the loop, so that what an MMA takes stays in uniform
+            // registers, and one lane issues
             const uint32_t idesc = idesc_e4m3(256, kCols), first = (uint32_t)warp - 1;
             const uint64_t xd = sw128_desc(smem_u32(smem)), wd = sw128_desc(smem_u32(smem + kBoxBytes));
             uint32_t s = first, ph = 0;
@@ -198,17 +200,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                const uint64_t x0 = xd + s * (kStage >> 4), w0 = wd + s * (kStage >> 4);
-                tc_mma_f8_pair(d, x0, w0, idesc, 0u);
-                tc_mma_f8_pair(d, x0 + 2, w0 + 2, idesc, 1u);
-                tc_mma_f8_pair(d, x0 + 4, w0 + 4, idesc, 1u);
-                tc_mma_f8_pair(d, x0 + 6, w0 + 6, idesc, 1u);
-                tc_commit_pair_mc(&acc_full[i], 0x3);
-                tc_commit_pair_mc(&empty[s], 0x3);
+                if (elect_one()) {
+                    const uint64_t x0 = xd + s * (kStage >> 4), w0 = wd + s * (kStage >> 4);
+                    tc_mma_f8_pair(d, x0, w0, idesc, 0u);
+                    tc_mma_f8_pair(d, x0 + 2, w0 + 2, idesc, 1u);
+                    tc_mma_f8_pair(d, x0 + 4, w0 + 4, idesc, 1u);
+                    tc_mma_f8_pair(d, x0 + 6, w0 + 6, idesc, 1u);
+                    tc_commit_pair_mc(&acc_full[i], 0x3);
+                    tc_commit_pair_mc(&empty[s], 0x3);
+                }
+                __syncwarp();
                 s += 2;
                 if (s >= (uint32_t)a.stages) s -= (uint32_t)a.stages, ph ^= 1u;
             }
-            if (!ok) {  // the MMAs already issued finish before TMEM is released
+            if (!ok && elect_one()) {  // the MMAs already issued finish before TMEM is released
                 tc_commit_pair(&drain[first]);
                 wait_drain(&drain[first], 0);
             }
