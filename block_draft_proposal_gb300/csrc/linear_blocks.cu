@@ -158,7 +158,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         regs_give<56>();
         // of the pair's blocks, tile after tile, every other one
         const uint32_t all = (uint32_t)((int64_t)((total - pair + pairs - 1) / pairs) * a.blocks);
-        if ((warp == 0 || warp == 3) && lane == 0) {
+        // (whole warps run the loops, so that what a copy or an MMA takes stays in uniform
+        // registers, and one lane issues)
+        if (warp == 0 || warp == 3) {
             const uint32_t first = warp == 0 ? 0 : 1;
             uint32_t it = first, s = first, ph = 1;  // the first pass finds every stage free
             int w = pair, b = (int)first, m, n;
@@ -169,11 +171,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     tile_of(w, &m, &n);
                 }
                 if (!bar_wait(&empty[s], ph, &abort_flag, a.err)) break;
-                const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
-                if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStage);
-                uint8_t *st = smem + s * kStage;
-                tma_load_2d_pair(st, &tm_x, bar, b * 128, m * 256 + (int)rank * 128);
-                tma_load_2d_pair(st + kBoxBytes, &tm_w, bar, b * 128, n * kCols + (int)rank * kHalf);
+                if (elect_one()) {
+                    const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStage);
+                    uint8_t *st = smem + s * kStage;
+                    tma_load_2d_pair(st, &tm_x, bar, b * 128, m * 256 + (int)rank * 128);
+                    tma_load_2d_pair(st + kBoxBytes, &tm_w, bar, b * 128, n * kCols + (int)rank * kHalf);
+                }
+                __syncwarp();
                 s += 2;
                 if (s >= (uint32_t)a.stages) s -= (uint32_t)a.stages, ph ^= 1u;
             }
@@ -185,8 +190,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     wait_drain(&full[k % stages], (k / stages) & 1u);
             }
         } else if ((warp == 1 || warp == 2) && rank == 0) {
-            // the whole warp runs the loop, so that what an MMA takes stays in uniform
-            // registers, and one lane issues
             const uint32_t idesc = idesc_e4m3(256, kCols), first = (uint32_t)warp - 1;
             const uint64_t xd = sw128_desc(smem_u32(smem)), wd = sw128_desc(smem_u32(smem + kBoxBytes));
             uint32_t s = first, ph = 0;
@@ -331,14 +334,12 @@ constexpr int kFewMaxSplit = 8;
 
 template <int kN> constexpr uint32_t kFewStage = kBoxBytes + kN * 128;
 
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
+__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 template <typename T, int kN>
-__global__ void __launch_bounds__(kFewThreads, kN <= 64 ? 2 : 1)
+__global__ void __launch_bounds__(kFewThreads, 2)
     linear_few_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                       const LinearArgs a, const int split) {
     constexpr int kChunk = kN < 32 ? kN : 32, kPer = (kN + 31) / 32;
@@ -379,52 +380,60 @@ __global__ void __launch_bounds__(kFewThreads, kN <= 64 ? 2 : 1)
 
     float sum[kN];
     if (warp == 0) {
-        if (lane == 0) {
-            const auto arm = [&](int b, uint32_t s) {
-                mbar_arrive_expect_tx(&full[s], kStage);
-                tma_load_2d(smem + s * kStage, &tm_w, &full[s], b * 128, nt * 128);
-            };
-            const auto load_x = [&](int b, uint32_t s) {
-                tma_load_2d(smem + s * kStage + kBoxBytes, &tm_x, &full[s], b * 128, mt * kN);
-            };
-            const int first = min(b1 - b0, a.stages);  // stages that nothing has used yet
+        const auto arm = [&](int b, uint32_t s) {
+            mbar_arrive_expect_tx(&full[s], kStage);
+            tma_load_2d(smem + s * kStage, &tm_w, &full[s], b * 128, nt * 128);
+        };
+        const auto load_x = [&](int b, uint32_t s) {
+            tma_load_2d(smem + s * kStage + kBoxBytes, &tm_x, &full[s], b * 128, mt * kN);
+        };
+        const int first = min(b1 - b0, a.stages);  // stages that nothing has used yet
+        if (elect_one())
             for (int i = 0; i < first; ++i) arm(b0 + i, (uint32_t)i);
-            if (a.early) grid_dep_wait();
+        __syncwarp();
+        if (a.early) grid_dep_wait();
+        if (elect_one())
             for (int i = 0; i < first; ++i) load_x(b0 + i, (uint32_t)i);
-            uint32_t issued = (uint32_t)first, s = 0, ph = 0;
-            for (int b = b0 + first; b < b1; ++b) {
-                if (!bar_wait(&empty[s], ph, &abort_flag, a.err)) break;
+        __syncwarp();
+        uint32_t issued = (uint32_t)first, s = 0, ph = 0;
+        for (int b = b0 + first; b < b1; ++b) {
+            if (!bar_wait(&empty[s], ph, &abort_flag, a.err)) break;
+            if (elect_one()) {
                 arm(b, s);
                 load_x(b, s);
-                ++issued;
-                if (++s == (uint32_t)a.stages) s = 0, ph ^= 1u;
             }
-            drain_loads(full, issued, (uint32_t)a.stages);
+            __syncwarp();
+            ++issued;
+            if (++s == (uint32_t)a.stages) s = 0, ph ^= 1u;
         }
+        drain_loads(full, issued, (uint32_t)a.stages);
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = idesc_e4m3(128, kN);
-            const uint64_t wd = sw128_desc(smem_u32(smem)), xd = sw128_desc(smem_u32(smem + kBoxBytes));
-            uint32_t s = 0, ph = 0;
-            for (int b = b0; b < b1; ++b) {
-                const uint32_t it = (uint32_t)(b - b0), i = it % kBufs;
-                if (!bar_wait(&acc_empty[i], ((it / kBufs) & 1u) ^ 1u, &abort_flag, a.err) ||
-                    !bar_wait(&full[s], ph, &abort_flag, a.err)) {
+        const uint32_t idesc = idesc_e4m3(128, kN);
+        const uint64_t wd = sw128_desc(smem_u32(smem)), xd = sw128_desc(smem_u32(smem + kBoxBytes));
+        uint32_t s = 0, ph = 0;
+        for (int b = b0; b < b1; ++b) {
+            const uint32_t it = (uint32_t)(b - b0), i = it % kBufs;
+            if (!bar_wait(&full[s], ph, &abort_flag, a.err) ||
+                !bar_wait(&acc_empty[i], ((it / kBufs) & 1u) ^ 1u, &abort_flag, a.err)) {
+                if (elect_one()) {
                     tc_commit(&drain);
                     wait_drain(&drain, 0);
-                    break;
                 }
-                tc_fence_after();
+                break;
+            }
+            tc_fence_after();
+            if (elect_one()) {
                 const uint64_t w0 = wd + s * (kStage >> 4), x0 = xd + s * (kStage >> 4);
                 const uint32_t d = tmem + i * kAccCols;
                 tc_mma_f8(d, w0, x0, idesc, 0u);
                 tc_mma_f8(d, w0 + 2, x0 + 2, idesc, 1u);
                 tc_mma_f8(d, w0 + 4, x0 + 4, idesc, 1u);
                 tc_mma_f8(d, w0 + 6, x0 + 6, idesc, 1u);
-                tc_commit(&empty[s]);
                 tc_commit(&acc_full[i]);
-                if (++s == (uint32_t)a.stages) s = 0, ph ^= 1u;
+                tc_commit(&empty[s]);
             }
+            __syncwarp();
+            if (++s == (uint32_t)a.stages) s = 0, ph ^= 1u;
         }
     } else {
         const int quarter = warp & 3;
@@ -492,45 +501,48 @@ __global__ void __launch_bounds__(kFewThreads, kN <= 64 ? 2 : 1)
         for (int i = 0; i < kN / 2; ++i) unf2(acc[i], sum[2 * i], sum[2 * i + 1]);
     }
 
-    // The sums of the cluster's CTAs, added in the order of the blocks: each CTA leaves its
-    // own in shared memory (its stages are done with) and takes a share of the rows.
-    const int row = ((warp & 3) * 32 + lane);  // epilogue warps: the output column in the tile
+    // The sums of the cluster's CTAs, added in the order of the blocks: row j of x is CTA j %
+    // split's, and every CTA sends it its sums (the stages, done with everywhere, hold
+    // them).  Sent sums do not wait for one another; fetched ones did, 6 us for 64 rows.
+    const int row = (warp & 3) * 32 + lane;  // epilogue warps: the output column in the tile
     const int64_t n = (int64_t)nt * 128 + row;
     const int m0 = mt * kN, live = min(kN, a.rows - m0);
     T *y = (T *)a.y + (int64_t)m0 * a.n_out + n;
     tc_fence_before();
+    __syncthreads();  // the loads have landed and been read, on the failing path too
     if (split == 1) {
         if (warp >= 2 && n < a.n_out) {
 #pragma unroll
             for (int j = 0; j < kN; ++j)
                 if (j < live) from_f32(y + (int64_t)j * a.n_out, sum[j]);
         }
-        __syncthreads();
     } else {
-        float *part = reinterpret_cast<float *>(smem);
-        __syncthreads();  // the loads have landed and been read, on the failing path too
-        if (warp >= 2) {
-#pragma unroll
-            for (int j = 0; j < kN; ++j)
-                if (j < live) part[j * 128 + row] = sum[j];
-        }
+        float *part = reinterpret_cast<float *>(smem);  // [sender][slot][128]
+        const int slots = (kN + split - 1) / split;
         cluster_sync();
-        if (warp >= 2 && n < a.n_out) {
-            const uint32_t mine = smem_u32(part) + (uint32_t)row * 4;
-            for (int j = live * rank / split; j < live * (rank + 1) / split; ++j) {
-                float v[kFewMaxSplit], s = 0.0f;
+        if (warp >= 2) {
+            const uint32_t mine = smem_u32(part) + (uint32_t)((rank * slots * 128 + row) * 4);
+            int to = 0, slot = 0;
 #pragma unroll
-                for (int c = 0; c < kFewMaxSplit; ++c)
-                    v[c] = c < split ? ld_cluster(mapa_shared(mine + (uint32_t)j * 512, (uint32_t)c)) : 0.0f;
-#pragma unroll
-                for (int c = 0; c < kFewMaxSplit; ++c)
-                    if (c < split) s += v[c];
-                from_f32(y + (int64_t)j * a.n_out, s);
+            for (int j = 0; j < kN; ++j) {
+                if (j < live) st_cluster(mapa_shared(mine + (uint32_t)slot * 512, (uint32_t)to), sum[j]);
+                if (++to == split) to = 0, ++slot;
             }
         }
         __syncwarp();
-        cluster_sync();  // no CTA leaves while another reads its sums
+        cluster_sync();
+        if (warp >= 2 && n < a.n_out) {
+#pragma unroll 4
+            for (int s = 0; s < (live - rank + split - 1) / split; ++s) {
+                float v = 0.0f;
+#pragma unroll
+                for (int c = 0; c < kFewMaxSplit; ++c)
+                    if (c < split) v += part[(c * slots + s) * 128 + row];
+                from_f32(y + (int64_t)(s * split + rank) * a.n_out, v);
+            }
+        }
     }
+    __syncwarp();
     if (warp == 0) {
         tc_fence_after();
         tmem_dealloc(tmem, 256);
@@ -573,13 +585,20 @@ dflash2_status launch_few(const DeviceInfo &di, const uint8_t *xq, const uint8_t
                           cudaStream_t st) {
     static std::atomic<uint64_t> allowed{0};
     constexpr uint32_t stage = kFewStage<kN>;
-    constexpr int most = kN <= 64 ? 108 * 1024 : 220 * 1024;  // two CTAs per SM, or one
+    constexpr int most = 108 * 1024;  // two CTAs per SM
     a.stages = min(kMaxStages, (int)((most - 1024) / stage));
     a.m_tiles = (a.rows + kN - 1) / kN, a.n_tiles = (a.n_out + 127) / 128;
     const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles;
     if (tiles > INT32_MAX / kFewMaxSplit) return DFLASH2_ERR_INVALID_ARG;
+    // As many CTAs as run at once (two per SM), with two blocks each: one row x 4096 x 6144
+    // takes 11.4 us unsplit, 7.6 us split in four, 11.5 in eight (a second wave); x 4096 x
+    // 1024 10.7, 5.0 and 4.0 us.  Clusters of 6 leave SMs idle (12.0 us for the first).
     int split = 1;
-    while (split < kFewMaxSplit && tiles * split * 2 <= 2 * di.sm_count && a.blocks >= 4 * split) split *= 2;
+    for (const int s : {8, 5, 4, 2})
+        if (tiles * s <= 2 * di.sm_count && a.blocks >= 2 * s) {
+            split = s;
+            break;
+        }
     CUtensorMap tm_x, tm_w;
     dflash2_status s = encode_tmap_2d(&tm_x, xq, (uint64_t)a.rows, (uint64_t)n_in, kN, 1);
     if (s == DFLASH2_OK) s = encode_tmap_2d(&tm_w, wq, (uint64_t)a.n_out, (uint64_t)n_in, 128, 1);
@@ -607,7 +626,13 @@ dflash2_status launch_linear(const DeviceInfo &di, const uint8_t *xq, const uint
     if (a.rows <= 16) return launch_few<T, 16>(di, xq, wq, n_in, a, st);
     if (a.rows <= 32) return launch_few<T, 32>(di, xq, wq, n_in, a, st);
     if (a.rows <= 64) return launch_few<T, 64>(di, xq, wq, n_in, a, st);
-    if (a.rows <= 128) return launch_few<T, 128>(di, xq, wq, n_in, a, st);
+    // The tile's width by the time of its waves: a block takes a pair 0.48 and 0.6 times as
+    // long at 64 and 128 columns as at 256.
+    const int64_t m_tiles = (a.rows + 255) / 256, pairs = di.sm_count / 2;
+    const auto waves = [&](int cols) { return (m_tiles * ((a.n_out + cols - 1) / cols) + pairs - 1) / pairs; };
+    const double t64 = 0.48 * (double)waves(64), t128 = 0.6 * (double)waves(128), t256 = (double)waves(256);
+    if (t64 < t128 && t64 < t256) return launch_pair<T, 64>(di, xq, wq, n_in, a, st);
+    if (t128 < t256) return launch_pair<T, 128>(di, xq, wq, n_in, a, st);
     return launch_pair<T, 256>(di, xq, wq, n_in, a, st);
 }
 
