@@ -231,34 +231,41 @@ bool vec_rows(const void *p, int64_t stride, uintptr_t el) {
 // ---- block quantisation of rows ----------------------------------------------
 constexpr int kQuantThreads = 256;
 
+constexpr int kQuantUnroll = 4;  // neighbouring blocks of a row per 16 lanes, loaded together
+
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kQuantThreads)
     quantise_rows_kernel(const T *x, int64_t stride, int64_t rows, int32_t cols, uint8_t *q, float *scale,
                          bool code_vec) {
     grid_dep_wait();
     grid_dep_launch();  // a product that follows loads its weights meanwhile
-    const int nb = (cols + kQuantBlock - 1) / kQuantBlock;
-    const int64_t b = ((int64_t)blockIdx.x * kQuantThreads + threadIdx.x) / kQuantLanes;
-    const bool live = b < rows * nb;
-    const int64_t row = live ? b / nb : 0;
-    const int block = live ? (int)(b - row * nb) : 0, lane = threadIdx.x % kQuantLanes;
-    const int col = block * kQuantBlock + lane * 8, n = live ? cols - col : 0;
-    Held<T, kVec> h;
-    float v[8], s;
-    h.load(x + row * stride + col, n);
-    h.get(v);
-    const uint2 codes = quantise_block(v, &s);
-    if (n <= 0) return;
-    store_codes(q + row * cols + col, n, code_vec, codes);
-    if (lane == 0) scale[row * nb + block] = s;
+    const int nb = (cols + kQuantBlock - 1) / kQuantBlock, groups = (nb + kQuantUnroll - 1) / kQuantUnroll;
+    const int64_t g = ((int64_t)blockIdx.x * kQuantThreads + threadIdx.x) / kQuantLanes;
+    const int64_t row = g / groups;
+    const int block = (int)(g - row * groups) * kQuantUnroll, lane = threadIdx.x % kQuantLanes;
+    const int left = row < rows ? cols - block * kQuantBlock - lane * 8 : 0;  // values from the first on
+    Held<T, kVec> h[kQuantUnroll];
+#pragma unroll
+    for (int u = 0; u < kQuantUnroll; ++u)
+        h[u].load(x + row * stride + block * kQuantBlock + lane * 8 + u * kQuantBlock, left - u * kQuantBlock);
+#pragma unroll
+    for (int u = 0; u < kQuantUnroll; ++u) {
+        float v[8], s;
+        h[u].get(v);
+        const uint2 codes = quantise_block(v, &s);
+        const int n = left - u * kQuantBlock;
+        if (n <= 0) continue;
+        store_codes(q + row * cols + (block + u) * kQuantBlock + lane * 8, n, code_vec, codes);
+        if (lane == 0) scale[row * nb + block + u] = s;
+    }
 }
 
 }  // namespace
 
 dflash2_status launch_quant_blocks_e4m3(const void *x, int64_t stride, int32_t dtype, int64_t rows, int32_t cols,
                                         uint8_t *q, float *scale, cudaStream_t st) {
-    const int64_t blocks = rows * ((cols + kQuantBlock - 1) / kQuantBlock);
-    const int64_t grid = (blocks * kQuantLanes + kQuantThreads - 1) / kQuantThreads;
+    constexpr int kCols = kQuantBlock * kQuantUnroll;
+    const int64_t grid = (rows * ((cols + kCols - 1) / kCols) * kQuantLanes + kQuantThreads - 1) / kQuantThreads;
     const bool vec = cols % 8 == 0 && vec_rows(x, stride, size_of(dtype));
     const bool code_vec = cols % 8 == 0 && aligned_to(q, 8);
     const dim3 g((unsigned)grid), t(kQuantThreads);
