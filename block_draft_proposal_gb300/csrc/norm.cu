@@ -12,8 +12,7 @@
 // as computed in fp32, not as rounded for storage.
 //
 // HBM bounds them once the rows fill the GPU, a launch below that.  A thread holds
-// kChunks x 8 values; a row takes as many threads as it needs (a warp where kChunks x 256
-// values suffice), and the loads of y, r and the gate are all in flight at once.
+// 4 x 8 values; a row takes as many threads as it needs (a warp up to 1024 values), and the loads of y, r and the gate are all in flight at once.
 #include "rows.cuh"
 
 namespace dflash2 {
@@ -60,7 +59,7 @@ template <typename T, bool kVec> __device__ __forceinline__ void put8(T *p, int 
 }
 
 __device__ __forceinline__ float gate_value(float g, int act) {
-    if (act == DFLASH2_GATE_SIGMOID) return __fdiv_rn(1.0f, 1.0f + expf(-g));
+    if (act == DFLASH2_GATE_SIGMOID) return __fdividef(1.0f, 1.0f + expf(-g));  // 2 ulp each
     return act == DFLASH2_GATE_TANH ? tanhf(g) : g;
 }
 
@@ -78,9 +77,10 @@ template <bool kWarpRow> __device__ __forceinline__ float row_sum(float v, float
 }
 
 // kThreads: a row's threads at most; 32 stands for a warp per row, 8 rows a block.
-template <typename TX, typename T, int kChunks, bool kVec, bool kJoin, int kThreads>
+template <typename TX, typename T, bool kVec, bool kJoin, int kThreads>
 __global__ void __launch_bounds__(kThreads == 32 ? 256 : kThreads) sublayer_kernel(const NormArgs a) {
     constexpr bool kWarpRow = kThreads == 32;
+    constexpr int kChunks = kQuantUnroll;
     __shared__ float red[2][32];
     grid_dep_wait();
     const int t = kWarpRow ? threadIdx.x & 31 : threadIdx.x;
@@ -122,29 +122,31 @@ __global__ void __launch_bounds__(kThreads == 32 ? 256 : kThreads) sublayer_kern
             }
             y_rms = __frsqrt_rn(row_sum<kWarpRow>(s, red[0]) * inv_n + a.eps);
         }
+        // the branch's scale goes with the row's root or its gate
+        const float factor = y_rms * a.branch * token_gate;
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
             const int col = (c * per + t) * 8;
             float h[8], v[8];
             y[c].get(h);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[i] *= factor;
             if (a.w_post) {
                 Held<T, kVec> w;
                 w.load((const T *)a.w_post + col, hidden - col);
                 w.get(v);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) h[i] = h[i] * y_rms * (v[i] + a.w_off);
+                for (int i = 0; i < 8; ++i) h[i] *= v[i] + a.w_off;
             }
+            held[c].get(r[c]);
             if (a.gate_kind == kGateChannel || a.gate_kind == kGateFull) {
                 g[c].get(v);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) h[i] *= gate_value(v[i], a.gate_act);
-            } else if (a.gate_kind == kGateToken) {
+                for (int i = 0; i < 8; ++i) r[c][i] += h[i] * gate_value(v[i], a.gate_act);
+            } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) h[i] *= token_gate;
+                for (int i = 0; i < 8; ++i) r[c][i] += h[i];
             }
-            held[c].get(r[c]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) r[c][i] += a.branch * h[i];
             put8<TX, kVec>((TX *)a.r_out + row * a.r_stride + col, hidden - col, r[c]);
         }
         if (!a.w_next) return;
@@ -166,34 +168,40 @@ __global__ void __launch_bounds__(kThreads == 32 ? 256 : kThreads) sublayer_kern
         w.load((const T *)a.w_next + col, hidden - col);
         w.get(v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = r[c][i] * rms * (v[i] + a.w_off);
-        if (!a.scale) {
-            put8<T, kVec>((T *)a.out + row * hidden + col, hidden - col, v);
-            continue;
-        }
-        if (!kVec)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = col + i < hidden ? v[i] : 0.0f;
-        float s;
-        const uint2 codes = quantise_block(v, &s);
-        if (col >= hidden) continue;
-        store_codes((uint8_t *)a.out + row * hidden + col, hidden - col, a.code_vec, codes);
-        if (col % kQuantBlock == 0)
-            a.scale[row * ((hidden + kQuantBlock - 1) / kQuantBlock) + col / kQuantBlock] = s;
+        for (int i = 0; i < 8; ++i) r[c][i] *= rms * (v[i] + a.w_off);
+        if (!a.scale) put8<T, kVec>((T *)a.out + row * hidden + col, hidden - col, r[c]);
     }
+    if (!a.scale) return;
+    if (!kVec)
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if ((c * per + t) * 8 + i >= hidden) r[c][i] = 0.0f;
+    uint2 codes[kChunks];
+    float scale;
+    quantise_blocks(r, &scale, codes);
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+        const int col = (c * per + t) * 8;
+        if (col < hidden) store_codes((uint8_t *)a.out + row * hidden + col, hidden - col, a.code_vec, codes[c]);
+    }
+    const int block = (quant_lane() * per + t) / kQuantLanes;
+    if ((t & 3) == 0 && block * kQuantBlock < hidden)
+        a.scale[row * ((hidden + kQuantBlock - 1) / kQuantBlock) + block] = scale;
 }
 
 template <typename TX, typename T, bool kVec, bool kJoin>
 dflash2_status launch_vec(const NormArgs &a, cudaStream_t st) {
-    constexpr int kChunks = 4;
+    constexpr int kChunks = kQuantUnroll;
     const int threads = ((a.hidden + 8 * kChunks - 1) / (8 * kChunks) + 31) / 32 * 32;
     if (threads == 32)
-        launch_k(sublayer_kernel<TX, T, kChunks, kVec, kJoin, 32>, dim3((unsigned)((a.rows + 7) / 8)), dim3(256), 0,
+        launch_k(sublayer_kernel<TX, T, kVec, kJoin, 32>, dim3((unsigned)((a.rows + 7) / 8)), dim3(256), 0,
                  st, a);
     else if (threads <= 256)
-        launch_k(sublayer_kernel<TX, T, kChunks, kVec, kJoin, 256>, dim3((unsigned)a.rows), dim3(threads), 0, st, a);
+        launch_k(sublayer_kernel<TX, T, kVec, kJoin, 256>, dim3((unsigned)a.rows), dim3(threads), 0, st, a);
     else
-        launch_k(sublayer_kernel<TX, T, kChunks, kVec, kJoin, 1024>, dim3((unsigned)a.rows), dim3(threads), 0, st, a);
+        launch_k(sublayer_kernel<TX, T, kVec, kJoin, 1024>, dim3((unsigned)a.rows), dim3(threads), 0, st, a);
     return launch_status();
 }
 
@@ -231,8 +239,7 @@ bool vec_rows(const void *p, int64_t stride, uintptr_t el) {
 // ---- block quantisation of rows ----------------------------------------------
 constexpr int kQuantThreads = 256;
 
-constexpr int kQuantUnroll = 4;  // neighbouring blocks of a row per 16 lanes, loaded together
-
+// Sixteen lanes take four neighbouring blocks of a row.
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kQuantThreads)
     quantise_rows_kernel(const T *x, int64_t stride, int64_t rows, int32_t cols, uint8_t *q, float *scale,
@@ -248,16 +255,17 @@ __global__ void __launch_bounds__(kQuantThreads)
 #pragma unroll
     for (int u = 0; u < kQuantUnroll; ++u)
         h[u].load(x + row * stride + block * kQuantBlock + lane * 8 + u * kQuantBlock, left - u * kQuantBlock);
+    float v[kQuantUnroll][8], s;
+#pragma unroll
+    for (int u = 0; u < kQuantUnroll; ++u) h[u].get(v[u]);
+    uint2 codes[kQuantUnroll];
+    quantise_blocks(v, &s, codes);
 #pragma unroll
     for (int u = 0; u < kQuantUnroll; ++u) {
-        float v[8], s;
-        h[u].get(v);
-        const uint2 codes = quantise_block(v, &s);
         const int n = left - u * kQuantBlock;
-        if (n <= 0) continue;
-        store_codes(q + row * cols + (block + u) * kQuantBlock + lane * 8, n, code_vec, codes);
-        if (lane == 0) scale[row * nb + block + u] = s;
+        if (n > 0) store_codes(q + row * cols + (block + u) * kQuantBlock + lane * 8, n, code_vec, codes[u]);
     }
+    if ((lane & 3) == 0 && row < rows && block + quant_lane() < nb) scale[row * nb + block + quant_lane()] = s;
 }
 
 }  // namespace

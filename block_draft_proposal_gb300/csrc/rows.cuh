@@ -115,7 +115,13 @@ constexpr float kQuantFloor = 7.888609e-31f;  // 2^-100: below it 448 / amax wou
 // has scale 1.  Infinities, which E4M3 has no code for, become NaN codes like NaN: a
 // product with them stays visible.  The divisions are IEEE and nothing is contracted, so
 // the codes are fixed by the values.
-__device__ __forceinline__ uint2 quantise_block(float (&x)[8], float *scale) {
+__device__ __forceinline__ void block_scale(float amax, float *scale, float *inv) {
+    const bool some = amax > 0.0f;
+    amax = fmaxf(amax, kQuantFloor);
+    *scale = some ? __fdiv_rn(amax, 448.0f) : 1.0f;
+    *inv = some ? __fdiv_rn(448.0f, amax) : 0.0f;
+}
+__device__ __forceinline__ float finite_amax(float (&x)[8]) {
     float amax = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -125,12 +131,41 @@ __device__ __forceinline__ uint2 quantise_block(float (&x)[8], float *scale) {
         else
             x[i] = __uint_as_float(0x7FFFFFFFu);
     }
+    return amax;
+}
+// Four blocks of the same 16 lanes at a time: the lanes' maxima are folded so that a
+// quarter of the lanes ends with each block's (5 shuffles in place of 16), and the
+// divisions are made once for the four.  The lane's `scale` is that of block quant_lane().
+constexpr int kQuantUnroll = 4;
+__device__ __forceinline__ int quant_lane() { return (threadIdx.x >> 2) & 3; }
+__device__ __forceinline__ void quantise_blocks(float (&x)[kQuantUnroll][8], float *scale, uint2 (&codes)[kQuantUnroll]) {
+    float m[kQuantUnroll];
 #pragma unroll
-    for (int o = kQuantLanes / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-    const bool some = amax > 0.0f;
-    amax = fmaxf(amax, kQuantFloor);
-    *scale = some ? __fdiv_rn(amax, 448.0f) : 1.0f;
-    return encode8(x, some ? __fdiv_rn(448.0f, amax) : 0.0f);
+    for (int c = 0; c < kQuantUnroll; ++c) {
+        m[c] = 0.0f;  // fmaxf leaves NaN out
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m[c] = fmaxf(m[c], fabsf(x[c][i]));
+    }
+    const auto fold = [&]() {
+        const bool h8 = threadIdx.x & 8, h4 = threadIdx.x & 4;
+        const float s0 = __shfl_xor_sync(0xFFFFFFFFu, h8 ? m[0] : m[2], 8);
+        const float s1 = __shfl_xor_sync(0xFFFFFFFFu, h8 ? m[1] : m[3], 8);
+        const float a0 = fmaxf(h8 ? m[2] : m[0], s0), a1 = fmaxf(h8 ? m[3] : m[1], s1);
+        float k = fmaxf(h4 ? a1 : a0, __shfl_xor_sync(0xFFFFFFFFu, h4 ? a0 : a1, 4));
+        k = fmaxf(k, __shfl_xor_sync(0xFFFFFFFFu, k, 2));
+        return fmaxf(k, __shfl_xor_sync(0xFFFFFFFFu, k, 1));
+    };
+    float amax = fold();
+    if (__any_sync(0xFFFFFFFFu, amax > FLT_MAX)) {
+#pragma unroll
+        for (int c = 0; c < kQuantUnroll; ++c) m[c] = finite_amax(x[c]);
+        amax = fold();
+    }
+    float inv;
+    block_scale(amax, scale, &inv);
+#pragma unroll
+    for (int c = 0; c < kQuantUnroll; ++c)
+        codes[c] = encode8(x[c], __shfl_sync(0xFFFFFFFFu, inv, (threadIdx.x & 16) | (4 * c)));
 }
 // Stores 8 codes, n of them when the row ends (vec: 8-byte aligned and whole).
 __device__ __forceinline__ void store_codes(uint8_t *p, int n, bool vec, uint2 c) {

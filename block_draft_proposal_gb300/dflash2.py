@@ -203,7 +203,7 @@ def _ptr(t):  # the argument types make a void * of it
 
 def _stream(stream):
     if stream is None:  # torch.cuda.current_stream() without building a Stream object
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream
 
 
@@ -970,6 +970,14 @@ def prompt_attention(q, k, v, cu_q, scale: float, out=None, lse=None, with_lse: 
 def _need_matrix(t: torch.Tensor, name: str, dtype=None, shape=None) -> int:
     """A [rows, cols] tensor whose rows may be strided (a slice of a wider one); returns
     the row stride."""
+    if (t.is_cuda and (dtype is None or t.dtype == dtype) and t.dim() == 2
+            and (shape is None or t.shape == shape)):
+        rows, cols = t.shape
+        s0, s1 = t.stride()
+        if rows < 2 and (s1 == 1 or cols == 1):
+            return cols
+        if (s1 == 1 or cols == 1) and s0 >= cols:
+            return s0
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if dtype is not None and t.dtype != dtype:
@@ -977,12 +985,9 @@ def _need_matrix(t: torch.Tensor, name: str, dtype=None, shape=None) -> int:
     if t.dim() != 2 or (shape is not None and t.shape != tuple(shape)):
         raise ValueError(f"{name} must have shape {'[rows, cols]' if shape is None else tuple(shape)}"
                          f", got {tuple(t.shape)}")
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    if t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    if rows > 1 and t.stride(0) < cols:
-        raise ValueError(f"{name} must not repeat rows")
-    return t.stride(0) if rows > 1 else cols
+    raise ValueError(f"{name} must not repeat rows")
 
 
 def _blocks_of(cols: int) -> int:
@@ -1115,8 +1120,9 @@ def sublayer_join(residual, y, post_weight=None, gate=None, gate_act: str = "non
             gs = _need_matrix(gate, "gate", dt, (rows, hidden))
             kind = GATE_FULL
     if residual_out is None:
-        residual_out = _empty((rows, hidden), residual.dtype, dev, stream)
-    ros = _need_matrix(residual_out, "residual_out", residual.dtype, (rows, hidden))
+        residual_out, ros = _empty((rows, hidden), residual.dtype, dev, stream), hidden
+    else:
+        ros = _need_matrix(residual_out, "residual_out", residual.dtype, (rows, hidden))
     if next_weight is not None:
         out, scale = _norm_out(rows, hidden, dt, e4m3, out, scale, dev, stream)
     elif out is not None or scale is not None or e4m3:
@@ -1177,18 +1183,21 @@ def _need_rotary(positions, table: RotaryTable, n: int):
     freq, axis, adjacent, magnitude = table
     axes = 1 if positions.dim() == 1 else positions.shape[0]
     _need(positions, "positions", torch.int64, (n,) if positions.dim() == 1 else (axes, n))
-    _need(freq, "table.freq", torch.int64)
-    _need(axis, "table.axis", torch.uint8, freq.shape)
-    return (_ptr(positions), axes, _ptr(freq), _ptr(axis), 2 * freq.numel(), int(bool(adjacent)),
-            float(magnitude))
+    if not (freq.is_cuda and axis.is_cuda and freq.dtype == torch.int64 and axis.dtype == torch.uint8
+            and freq.shape == axis.shape and freq.is_contiguous() and axis.is_contiguous()):
+        _need(freq, "table.freq", torch.int64)
+        _need(axis, "table.axis", torch.uint8, freq.shape)
+    return (positions.data_ptr(), axes, freq.data_ptr(), axis.data_ptr(), 2 * freq.numel(),
+            1 if adjacent else 0, magnitude)
 
 
 def _rotated(x, name, out, stream):
-    """Strides of x and of where it goes, which is made unless given."""
-    xs = _need_rows(x, name, x.dtype, x.shape)
+    """The token strides of x and of where it goes, which is made unless given."""
+    shape = x.shape
+    xs = _need_rows(x, name, x.dtype, shape)
     if out is None:
-        out = _empty(x.shape, x.dtype, x.device, stream)
-    return xs, out, _need_rows(out, name + "_out", x.dtype, x.shape)
+        return xs, _empty(shape, x.dtype, x.device, stream), shape[1] * shape[2]
+    return xs, out, _need_rows(out, name + "_out", x.dtype, shape)
 
 
 def rotary(q, k, positions, table: RotaryTable, q_out=None, k_out=None, err=None, stream=None):
