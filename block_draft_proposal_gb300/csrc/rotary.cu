@@ -14,8 +14,9 @@
 // same two steps of 8 values of every row, chosen so that both halves of its pairs are
 // its own (for halves: step u and u + rotary_dim / 16), so sines and cosines are read from
 // shared memory once per token and the rows need no exchange between lanes but the E4M3
-// maximum.  A warp computes a token's sines and cosines for up to kUnroll rows per lane
-// group, all of whose loads are in flight together.
+// maximum.  A block computes its tokens' sines and cosines once and keeps several groups'
+// loads in flight per warp (computed by every warp of a token, at 18 instructions a value,
+// 20011 tokens x 56 rows took 172 us).
 #include "rows.cuh"
 
 namespace dflash2 {
@@ -42,25 +43,21 @@ struct RotaryArgs {
     int64_t n_slots;
     void *kc, *vc;
     uint8_t *ke, *ve;
-    int32_t parts;             // warps a token's rows are split over
+    int32_t parts;             // warps a token's rows are split over (a power of two; scalar: any)
     int32_t *err;
 };
 
-// Sines and cosines of a token's pairs into the warp's table.
-__device__ __forceinline__ void token_angles(const RotaryArgs &a, int64_t token, bool report, float2 *cs) {
-    const int lane = threadIdx.x & 31;
-    for (int j = lane; j < a.pairs; j += 32) {
-        const int axis = __ldg(a.axis + j);
-        uint64_t phase = 0;
-        if (axis < a.axes)
-            phase = (uint64_t)__ldg(a.positions + axis * a.n_tokens + token) * __ldg(a.freq + j);
-        else if (report && a.err)
-            atomicOr(a.err, DFLASH2_DEVERR_ID_RANGE);
-        float s, c;
-        sincospif(__ll2float_rn((int64_t)phase) * 0x1p-63f, &s, &c);
-        cs[j] = make_float2(c * a.magnitude, s * a.magnitude);
-    }
-    __syncwarp();
+// Sine and cosine (times the magnitude) of a token's pair.
+__device__ __forceinline__ float2 turn_of(const RotaryArgs &a, int64_t token, int pair) {
+    const int axis = __ldg(a.axis + pair);
+    uint64_t phase = 0;
+    if (axis < a.axes)
+        phase = (uint64_t)__ldg(a.positions + axis * a.n_tokens + token) * __ldg(a.freq + pair);
+    else if (a.err)
+        atomicOr(a.err, DFLASH2_DEVERR_ID_RANGE);
+    float s, c;
+    sincospif(__ll2float_rn((int64_t)phase) * 0x1p-63f, &s, &c);
+    return make_float2(c * a.magnitude, s * a.magnitude);
 }
 
 // Head 0's row of a token in the cache arrays, or -1.
@@ -76,19 +73,19 @@ __device__ __forceinline__ int64_t cache_row(const RotaryArgs &a, int64_t token,
     return page * a.kv_heads * a.page_size + (slot - page * a.page_size);
 }
 
-// kLanes lanes (a power of two) hold a row of up to 16 kLanes values.
-template <typename T, bool kE4M3, int kLanes, int kUnroll>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
+// kLanes lanes (a power of two) hold a row of up to 16 kLanes values, a warp kRows rows at
+// once: a group.
+template <typename T, bool kE4M3, int kLanes>
+__global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const RotaryArgs a) {
     constexpr int kRows = 32 / kLanes;
-    __shared__ float2 table[kWarps][kMaxPairs];
+    constexpr int kAhead = sizeof(T) == 2 ? 3 : 2;  // groups whose loads are in flight
+    __shared__ float2 table[kWarps * kMaxPairs];
     grid_dep_wait();
-    const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int64_t token = w / a.parts;
-    if (token >= a.n_tokens) return;
-    const int part = (int)(w - token * a.parts);
+    const int warp = threadIdx.x >> 5, tokens = kWarps / a.parts;
+    const int64_t token0 = (int64_t)blockIdx.x * tokens, token = token0 + warp / a.parts;
     const int lane = threadIdx.x % kLanes, sub = (threadIdx.x & 31) / kLanes;
     const int total = a.q_rows + a.k_rows + a.v_rows, d = a.head_dim;
-    const int first = part * kRows * kUnroll;
+    const int groups = token < a.n_tokens ? (total + kRows - 1) / kRows : 0;
 
     // this lane's two steps, and whether each is turned
     const int steps = d / 8, turned = a.pairs / 4;
@@ -99,27 +96,38 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
         s0 = lane, s1 = lane + turned / 2;
     }
     const bool on0 = s0 < steps, on1 = s1 < steps;
+    const T *q = (const T *)a.q + token * a.q_stride, *k = (const T *)a.k + token * a.k_stride;
+    const T *v = (const T *)a.v + token * a.v_stride;
 
-    Raw8<T> raw[kUnroll][2];
+    struct Pair {
+        Raw8<T> x, y;
+    } raw[kAhead];
+    const auto fetch = [&](int g, Pair &p) {
+        int r = g * kRows + sub;
+        p.x = p.y = Raw8<T>{};
+        if (g >= groups || r >= total) return;
+        const T *src = q;
+        if (r >= a.q_rows) {
+            r -= a.q_rows, src = k;
+            if (r >= a.k_rows) r -= a.k_rows, src = v;
+        }
+        src += r * d;
+        if (on0) p.x = load_raw8_written(src + s0 * 8);
+        if (on1) p.y = load_raw8_written(src + s1 * 8);
+    };
+    int g = warp % a.parts;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-        int r = first + u * kRows + sub;
-        raw[u][0] = raw[u][1] = Raw8<T>{};
-        if (r >= total) continue;
-        const T *p;
-        if (r < a.q_rows)
-            p = (const T *)a.q + token * a.q_stride + (int64_t)r * d;
-        else if ((r -= a.q_rows) < a.k_rows)
-            p = (const T *)a.k + token * a.k_stride + (int64_t)r * d;
-        else
-            p = (const T *)a.v + token * a.v_stride + (int64_t)(r - a.k_rows) * d;
-        if (on0) raw[u][0] = load_raw8_written(p + s0 * 8);
-        if (on1) raw[u][1] = load_raw8_written(p + s1 * 8);
+    for (int i = 0; i < kAhead; ++i) fetch(g + i * a.parts, raw[i]);
+
+    const int64_t at = groups && a.k_rows ? cache_row(a, token, (threadIdx.x & 31) == 0 && g == 0) : -1;
+    // the sines and cosines of the block's tokens, each once
+    for (int i = threadIdx.x; i < tokens * a.pairs; i += kThreads) {
+        const int t = i / a.pairs;
+        if (token0 + t < a.n_tokens) table[i] = turn_of(a, token0 + t, i - t * a.pairs);
     }
-    const bool reports = part == 0 && (threadIdx.x & 31) == 0;
-    const int64_t at = cache_row(a, token, reports);
-    float2 *cs = table[threadIdx.x >> 5];
-    token_angles(a, token, part == 0, cs);
+    __syncthreads();
+    if (groups == 0) return;
+    const float2 *cs = table + warp / a.parts * a.pairs;
     float co[8], si[8];  // halves: of the 8 pairs; adjacent: of the 4 of each step
     const bool turn0 = s0 < turned, turn1 = s1 < turned;
 #pragma unroll
@@ -128,47 +136,47 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
         const float2 x = j < a.pairs ? cs[j] : make_float2(1.0f, 0.0f);
         co[i] = x.x, si[i] = x.y;
     }
+    const auto turn = [&](float (&x)[8], float (&y)[8]) {
+        if (a.adjacent) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-        if (first + u * kRows >= total) break;  // the whole warp
-        const int r = first + u * kRows + sub;
-        const bool values = r >= a.q_rows + a.k_rows, key = !values && r >= a.q_rows;
-        float x[8], y[8];
-        as_floats(raw[u][0], x);
-        as_floats(raw[u][1], y);
-        if (!values) {
-            if (a.adjacent) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float p = x[2 * i], o = x[2 * i + 1], p1 = y[2 * i], o1 = y[2 * i + 1];
-                    if (turn0) {
-                        x[2 * i] = p * co[i] - o * si[i];
-                        x[2 * i + 1] = o * co[i] + p * si[i];
-                    }
-                    if (turn1) {
-                        y[2 * i] = p1 * co[4 + i] - o1 * si[4 + i];
-                        y[2 * i + 1] = o1 * co[4 + i] + p1 * si[4 + i];
-                    }
+            for (int i = 0; i < 4; ++i) {
+                const float p = x[2 * i], o = x[2 * i + 1], p1 = y[2 * i], o1 = y[2 * i + 1];
+                if (turn0) {
+                    x[2 * i] = p * co[i] - o * si[i];
+                    x[2 * i + 1] = o * co[i] + p * si[i];
                 }
-            } else if (turn0) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float p = x[i], o = y[i];
-                    x[i] = p * co[i] - o * si[i];
-                    y[i] = o * co[i] + p * si[i];
+                if (turn1) {
+                    y[2 * i] = p1 * co[4 + i] - o1 * si[4 + i];
+                    y[2 * i + 1] = o1 * co[4 + i] + p1 * si[4 + i];
                 }
             }
+        } else if (turn0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float p = x[i], o = y[i];
+                x[i] = p * co[i] - o * si[i];
+                y[i] = o * co[i] + p * si[i];
+            }
         }
-        const bool live = r < total;
+    };
+    T *q_out = (T *)a.qo + token * a.qo_stride, *k_out = (T *)a.ko + token * a.ko_stride;
+
+    const auto finish = [&](int g, const Pair &p) {
+        const int r = g * kRows + sub;
+        float x[8], y[8];
+        as_floats(p.x, x);
+        as_floats(p.y, y);
+        if ((g + 1) * kRows <= a.q_rows) {  // queries alone, the most
+            turn(x, y);
+            if (on0) store8(q_out + r * d + s0 * 8, x);
+            if (on1) store8(q_out + r * d + s1 * 8, y);
+            return;
+        }
+        const bool live = r < total, values = r >= a.q_rows + a.k_rows, key = !values && r >= a.q_rows;
+        if (!values) turn(x, y);
         const int head = values ? r - a.q_rows - a.k_rows : key ? r - a.q_rows : r;
-        T *dst = nullptr;
-        if (live && !values) {
-            if (!key)
-                dst = (T *)a.qo + token * a.qo_stride + (int64_t)head * d;
-            else if (a.ko)
-                dst = (T *)a.ko + token * a.ko_stride + (int64_t)head * d;
-        }
-        if (dst) {
+        if (live && !values && (!key || a.ko)) {
+            T *dst = (key ? k_out : q_out) + head * d;
             if (on0) store8(dst + s0 * 8, x);
             if (on1) store8(dst + s1 * 8, y);
         }
@@ -180,7 +188,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
             for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(x[i]), fabsf(y[i])));
 #pragma unroll
             for (int o = kLanes / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-            if (!held) continue;
+            if (!held) return;
             const int e = row_exponent(amax);
             uint8_t *c = (uint8_t *)(values ? a.vc : a.kc) + row * d;
             if (on0) *reinterpret_cast<uint2 *>(c + s0 * 8) = encode8(x, pow2i(-e));
@@ -189,12 +197,21 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
         } else if (held) {
             T *c = (T *)(values ? a.vc : a.kc) + row * d;
             if (values) {  // a value row keeps its bits
-                if (on0) store_raw8(c + s0 * 8, raw[u][0]);
-                if (on1) store_raw8(c + s1 * 8, raw[u][1]);
+                if (on0) store_raw8(c + s0 * 8, p.x);
+                if (on1) store_raw8(c + s1 * 8, p.y);
             } else {
                 if (on0) store8(c + s0 * 8, x);
                 if (on1) store8(c + s1 * 8, y);
             }
+        }
+    };
+    while (g < groups) {  // the same for the whole warp
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (g >= groups) break;
+            finish(g, raw[i]);
+            fetch(g + kAhead * a.parts, raw[i]);
+            g += a.parts;
         }
     }
 }
@@ -215,7 +232,8 @@ __global__ void __launch_bounds__(kThreads) rotary_scalar(const RotaryArgs a) {
     const int total = a.q_rows + a.k_rows + a.v_rows, d = a.head_dim;
     const int64_t at = cache_row(a, token, part == 0 && lane == 0);
     float2 *cs = table[threadIdx.x >> 5];
-    token_angles(a, token, part == 0, cs);
+    for (int j = lane; j < a.pairs; j += 32) cs[j] = turn_of(a, token, j);
+    __syncwarp();
     for (int r = part * kScalarRows; r < min(total, (part + 1) * kScalarRows); ++r) {
         const bool values = r >= a.q_rows + a.k_rows, key = !values && r >= a.q_rows;
         const int head = values ? r - a.q_rows - a.k_rows : key ? r - a.q_rows : r;
@@ -264,27 +282,33 @@ __global__ void __launch_bounds__(kThreads) rotary_scalar(const RotaryArgs a) {
     }
 }
 
-template <typename T, bool kE4M3, int kLanes, int kUnroll>
-void launch_unroll(RotaryArgs a, cudaStream_t st) {
-    constexpr int rows = 32 / kLanes * kUnroll;
-    a.parts = (a.q_rows + a.k_rows + a.v_rows + rows - 1) / rows;
-    const int64_t warps = a.n_tokens * a.parts;
-    launch_k(rotary_kernel<T, kE4M3, kLanes, kUnroll>, dim3((unsigned)((warps + kWarps - 1) / kWarps)), dim3(kThreads),
-             0, st, a);
+template <typename T, bool kE4M3, int kLanes>
+void launch_lanes(RotaryArgs a, int sms, cudaStream_t st) {
+    constexpr int rows = 32 / kLanes;
+    // As few warps per token as leave a block per SM (512 tokens x 48 rows: 4.2 us, with
+    // twice as many 6.3), one only where there are three per SM (20011 tokens x 56 rows 90
+    // us, with two warps 94; 1536 tokens 11.6 and 9.0); no more than a token has groups.
+    const int groups = (a.q_rows + a.k_rows + a.v_rows + rows - 1) / rows;
+    a.parts = kWarps;
+    while (a.parts > 1 &&
+           (a.parts > groups || a.n_tokens * a.parts / 2 >= (a.parts > 2 ? 1ll : 3ll) * kWarps * sms))
+        a.parts /= 2;
+    const int64_t grid = (a.n_tokens * a.parts + kWarps - 1) / kWarps;
+    launch_k(rotary_kernel<T, kE4M3, kLanes>, dim3((unsigned)grid), dim3(kThreads), 0, st, a);
 }
 
 template <typename T, bool kE4M3>
-dflash2_status launch_rotary(RotaryArgs a, bool vec, cudaStream_t st) {
+dflash2_status launch_rotary(RotaryArgs a, bool vec, int sms, cudaStream_t st) {
     if (!vec) {
         a.parts = (a.q_rows + a.k_rows + a.v_rows + kScalarRows - 1) / kScalarRows;
         const int64_t warps = a.n_tokens * a.parts;
         launch_k(rotary_scalar<T, kE4M3>, dim3((unsigned)((warps + kWarps - 1) / kWarps)), dim3(kThreads), 0, st, a);
     } else if (a.head_dim <= 64) {
-        launch_unroll<T, kE4M3, 4, 4>(a, st);
+        launch_lanes<T, kE4M3, 4>(a, sms, st);
     } else if (a.head_dim <= 128) {
-        launch_unroll<T, kE4M3, 8, 4>(a, st);
+        launch_lanes<T, kE4M3, 8>(a, sms, st);
     } else {
-        launch_unroll<T, kE4M3, 16, 4>(a, st);
+        launch_lanes<T, kE4M3, 16>(a, sms, st);
     }
     return launch_status();
 }
@@ -332,8 +356,8 @@ dflash2_status run_rotary(RotaryArgs a, int32_t dtype, int32_t kv_format, int32_
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     using B = __nv_bfloat16;
     if (cached && q8)
-        return dtype == DFLASH2_F32 ? launch_rotary<float, true>(a, vec, s) : launch_rotary<B, true>(a, vec, s);
-    return dtype == DFLASH2_F32 ? launch_rotary<float, false>(a, vec, s) : launch_rotary<B, false>(a, vec, s);
+        return dtype == DFLASH2_F32 ? launch_rotary<float, true>(a, vec, di.sm_count, s) : launch_rotary<B, true>(a, vec, di.sm_count, s);
+    return dtype == DFLASH2_F32 ? launch_rotary<float, false>(a, vec, di.sm_count, s) : launch_rotary<B, false>(a, vec, di.sm_count, s);
 }
 
 }  // namespace
