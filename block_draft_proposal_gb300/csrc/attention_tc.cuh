@@ -8,8 +8,9 @@ namespace dflash2 {
 namespace attn {
 namespace {
 
-constexpr int kTile = 128;  // keys per tile
+using dflash2::bar_wait;  // the wait of every role here
 
+constexpr int kTile = 128;  // keys per tile
 
 // ---- tensor-core helpers -----------------------------------------------------
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint64_t *bar,

@@ -990,6 +990,18 @@ def _need_matrix(t: torch.Tensor, name: str, dtype=None, shape=None) -> int:
     raise ValueError(f"{name} must not repeat rows")
 
 
+def _current_device() -> int:
+    return torch._C._cuda_getDevice()
+
+
+def _need_one_device(*tensors):
+    """Everything a call is given lies on the current device, where it is launched."""
+    dev = _current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors must be on the current device cuda:{dev}, got {t.device}")
+
+
 def _blocks_of(cols: int) -> int:
     return -(-cols // 128)
 
@@ -1007,6 +1019,7 @@ def quantize_blocks_e4m3(x, q=None, scale=None, stream=None):
         scale = _empty((rows, _blocks_of(cols)), torch.float32, x.device, stream)
     else:
         _need(scale, "scale", torch.float32, (rows, _blocks_of(cols)))
+    _need_one_device(x, q, scale)
     _check("dflash2_quantize_blocks_e4m3", library().dflash2_quantize_blocks_e4m3(
         _ptr(x), xs, rows, cols, _dtype_code(x), _ptr(q), _ptr(scale), _stream(stream)))
     return q, scale
@@ -1050,6 +1063,7 @@ def linear_fp8_blocks(x, w_q, w_scale, x_scale=None, out_dtype=None, out=None, w
     elif not codes:
         workspace = _workspace(linear_fp8_blocks_workspace_size(rows, n_in, n_out), dev, stream)
     err = _need_error_word(err, dev, stream)
+    _need_one_device(x, w_q, w_scale, x_scale, out, workspace, err)
     _check("dflash2_linear_fp8_blocks", library().dflash2_linear_fp8_blocks(
         None if codes else _ptr(x), 0 if codes else xs, 0 if codes else x_code,
         _ptr(x) if codes else None, _ptr(x_scale), _ptr(w_q), _ptr(w_scale), rows, n_in, n_out,
@@ -1083,6 +1097,7 @@ def sublayer_norm(x, weight, eps: float = 1e-6, weight_offset: float = 0.0, e4m3
     rows, hidden = x.shape
     _need(weight, "weight", None, (hidden,))
     out, scale = _norm_out(rows, hidden, weight.dtype, e4m3, out, scale, x.device, stream)
+    _need_one_device(x, weight, out, scale)
     _check("dflash2_sublayer_norm", library().dflash2_sublayer_norm(
         _ptr(x), xs, _dtype_code(x), _ptr(weight), float(weight_offset), float(eps), rows, hidden,
         _dtype_code(weight), _ptr(out), _ptr(scale), _stream(stream)))
@@ -1127,6 +1142,7 @@ def sublayer_join(residual, y, post_weight=None, gate=None, gate_act: str = "non
         out, scale = _norm_out(rows, hidden, dt, e4m3, out, scale, dev, stream)
     elif out is not None or scale is not None or e4m3:
         raise ValueError("out, scale and e4m3 belong to next_weight")
+    _need_one_device(residual, y, post_weight, gate, next_weight, residual_out, out, scale)
     _check("dflash2_sublayer_join", library().dflash2_sublayer_join(
         _ptr(residual), rs, _dtype_code(residual), _ptr(y), ys, _ptr(post_weight), _ptr(gate), kind,
         gs, GATE_ACTS[gate_act], float(branch_scale), _ptr(next_weight), float(weight_offset),
@@ -1187,7 +1203,7 @@ def _need_rotary(positions, table: RotaryTable, n: int):
             and freq.shape == axis.shape and freq.is_contiguous() and axis.is_contiguous()):
         _need(freq, "table.freq", torch.int64)
         _need(axis, "table.axis", torch.uint8, freq.shape)
-    return (positions.data_ptr(), axes, freq.data_ptr(), axis.data_ptr(), 2 * freq.numel(),
+    return (_ptr(positions), axes, _ptr(freq), _ptr(axis), 2 * freq.numel(),
             1 if adjacent else 0, magnitude)
 
 
@@ -1217,6 +1233,7 @@ def rotary(q, k, positions, table: RotaryTable, q_out=None, k_out=None, err=None
     elif k_out is not None:
         raise ValueError("k_out without k")
     err = _need_error_word(err, q.device, stream)
+    _need_one_device(q, k, positions, table.freq, table.axis, q_out, k_out, err)
     _check("dflash2_rotary", library().dflash2_rotary(
         _ptr(q), qs, _ptr(k), ks, *place, n, heads, kv_heads, d, _dtype_code(q), _ptr(q_out), qos,
         _ptr(k_out), kos, _ptr(err), _stream(stream)))
@@ -1248,6 +1265,7 @@ def rotary_kv_write(cache: KVCache, q, k, v, positions, table: RotaryTable, slot
     if with_k or k_out is not None:
         ks, k_out, kos = _rotated(k, "k", k_out, stream)
     err = _need_error_word(err, k.device, stream)
+    _need_one_device(k, v, q, positions, table.freq, table.axis, slots, q_out, k_out, cache.k, err)
     _check("dflash2_rotary_kv_write", library().dflash2_rotary_kv_write(
         _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, *place, _ptr(slots), n, heads, kv_heads, d, ps,
         pages, _dtype_code(k), fmt, _ptr(q_out), qos, _ptr(k_out), kos, _ptr(cache.k),

@@ -21,7 +21,9 @@ SHAPES = [  # rows, in, out
     (1, 16, 1), (1, 128, 128), (1, 4096, 384), (2, 144, 130), (7, 1936, 1001), (16, 256, 257), (17, 384, 96),
     (33, 512, 640), (48, 1040, 200), (64, 128, 300), (65, 640, 128), (100, 2048, 130), (128, 256, 512),
     (129, 1296, 511), (200, 400, 264), (256, 256, 256), (257, 144, 1030), (300, 1152, 384), (513, 272, 520),
-    (1000, 656, 776), (1500, 128, 144)]
+    (1000, 656, 776), (1500, 128, 144),
+    # tiles of 64, 128 and 256 columns; more tiles than pairs of CTAs; the last ones ragged
+    (70, 272, 6001), (256, 400, 6016), (300, 144, 5000), (300, 272, 5001), (1100, 272, 9003), (2500, 144, 2600)]
 
 
 @pytest.mark.parametrize("rows,n_in,n_out", SHAPES)
@@ -40,14 +42,15 @@ def test_product(cuda, rows, n_in, n_out, dtype):
     assert int(err) == 0 and torch.equal(y2, y)
 
 
-@pytest.mark.parametrize("rows", [1, 5, 40, 130, 700])
-def test_whole_numbers_are_exact(cuda, rows):
+@pytest.mark.parametrize("rows,n_out", [(1, 400), (5, 400), (40, 400), (130, 400), (700, 400), (90, 6008),
+                                        (2600, 2500)])
+def test_whole_numbers_are_exact(cuda, rows, n_out):
     g = torch.Generator().manual_seed(rows)
-    n_in, n_out = 656, 400
+    n_in = 656
     x = torch.randint(-8, 9, (rows, n_in), generator=g).float()
     w = torch.randint(-8, 9, (n_out, n_in), generator=g).float()
     x_s = 2.0 ** torch.randint(-3, 4, (rows, 6), generator=g).float()
-    w_s = 2.0 ** torch.randint(-3, 4, (4, 6), generator=g).float()
+    w_s = 2.0 ** torch.randint(-3, 4, (-(-n_out // 128), 6), generator=g).float()
     code = ref.encode(x.double()), ref.encode(w.double())
     y, _ = dflash2.linear_fp8_blocks(code[0].cuda(), code[1].cuda(), w_s.cuda(), x_scale=x_s.cuda(), out_dtype=F32)
     want, _ = ref.product(code[0], x_s, code[1], w_s)

@@ -40,6 +40,7 @@ def allocations(monkeypatch):
     monkeypatch.setattr(dflash2, "library", _Library)
     monkeypatch.setattr(dflash2, "_ptr", lambda t: None if t is None else 256)
     monkeypatch.setattr(dflash2, "_stream", lambda s: 0 if s is None else s.cuda_stream)
+    monkeypatch.setattr(dflash2, "_current_device", lambda: 0)
     with FakeTensorMode():
         yield log
 
@@ -175,3 +176,21 @@ def test_types(call):
 def test_tables(kw):
     with pytest.raises(ValueError):
         dflash2.rotary_table(**kw)
+
+
+@pytest.mark.parametrize("call", [_quantise, _norm, _join, _linear, _rotary, _write])
+def test_another_device_than_the_current_one(call, monkeypatch):
+    call()
+    monkeypatch.setattr(dflash2, "_current_device", lambda: 1)
+    with pytest.raises(ValueError, match="current device"):
+        call()
+
+
+def test_tensors_of_two_devices():
+    there = "cuda:1"
+    for call in (lambda: _norm(w=_t(256, device=there)), lambda: _join(gate=_t(256, device=there)),
+                 lambda: _linear(s=_t(2, 2, dtype=F32, device=there)), lambda: _rotary(pos=_i(3, device=there)),
+                 lambda: _write(slots=_i(3, device=there)),
+                 lambda: _rotary(table=dflash2.RotaryTable(_i(32, device=there), _i(32, dtype=U8, device=there)))):
+        with pytest.raises(ValueError, match="current device"):
+            call()
