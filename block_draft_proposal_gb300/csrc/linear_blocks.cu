@@ -13,6 +13,8 @@
 //   linear_few_kernel   few rows: the weights are the MMA's M side, 128 a CTA, and the
 //                       rows of x its N side; the blocks are split over a cluster's CTAs,
 //                       which add their sums through distributed shared memory.
+#include <type_traits>
+
 #include "rows.cuh"
 #include "tcgen05.cuh"
 
@@ -21,6 +23,9 @@ namespace {
 
 struct LinearArgs {
     const float *xs, *ws;
+    const void *x;  // rows that the kernel quantises itself (linear_few_kernel with a type X)
+    int64_t x_stride;
+    int32_t n_in;
     int32_t rows, n_out, blocks;  // blocks of 128 along in_features
     void *y;
     int32_t *err;
@@ -329,27 +334,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 // Roles (192 threads): warp 0 loads, warp 1 issues the MMAs, warps 2 to 5 scale and add:
 // a thread owns one output column and kN rows of x.  A block's factors xs * ws lie in a
 // table of the warp's own, made from scales loaded two blocks ahead.
-constexpr int kFewThreads = 192;
+//
+// With a type X (up to 16 rows, 320 threads) x is not codes yet: warps 6 to 9 take every
+// fourth block each, quantise its rows into the stage and leave their factors beside it.
+// Every CTA does this for its own blocks, which costs less than the launch of a
+// quantisation before (one row x 4096 x 6144: 8.0 us in place of 9.3).
+constexpr int kFewThreads = 192, kFewQuantThreads = 320;
 constexpr int kFewMaxSplit = 8;
 
 template <int kN> constexpr uint32_t kFewStage = kBoxBytes + kN * 128;
+template <typename X> constexpr bool kQuantises = !std::is_same<X, uint8_t>::value;  // uint8_t: codes
 
 __device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-template <typename T, int kN>
-__global__ void __launch_bounds__(kFewThreads, 2)
+template <typename T, int kN, typename X>
+__global__ void __launch_bounds__(kQuantises<X> ? kFewQuantThreads : kFewThreads, 2)
     linear_few_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                       const LinearArgs a, const int split) {
     constexpr int kChunk = kN < 32 ? kN : 32, kPer = (kN + 31) / 32;
     constexpr uint32_t kAccCols = kN < 32 ? 32 : kN, kBufs = 256 / kAccCols;
     constexpr uint32_t kStage = kFewStage<kN>;
     extern __shared__ uint8_t dsmem[];
+    constexpr bool kQuant = kQuantises<X>;
+    static_assert(!kQuant || kN == 16, "a quantising warp takes sixteen rows");
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[kBufs], acc_empty[kBufs], drain;
+    __shared__ uint64_t factor_full[kBufs];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
-    __shared__ __align__(16) float factor[4][2][kN];
+    // codes: [warp][block & 1]; quantised here: [accumulator], one for all warps
+    __shared__ __align__(16) float factor[8][kN];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~(uintptr_t)1023);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -358,8 +373,9 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     const int nt = tile % a.n_tiles, mt = tile / a.n_tiles;
     const int b0 = (int)((int64_t)a.blocks * rank / split), b1 = (int)((int64_t)a.blocks * (rank + 1) / split);
     if (threadIdx.x == 0) {
-        for (int s = 0; s < a.stages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
-        for (uint32_t i = 0; i < kBufs; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_empty[i], 4);
+        for (int s = 0; s < a.stages; ++s) mbar_init(&full[s], kQuant ? 2 : 1), mbar_init(&empty[s], 1);
+        for (uint32_t i = 0; i < kBufs; ++i)
+            mbar_init(&acc_full[i], 1), mbar_init(&acc_empty[i], 4), mbar_init(&factor_full[i], 1);
         mbar_init(&drain, 1);
         abort_flag = 0;
         fence_mbar_init();
@@ -368,7 +384,10 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         tmem_alloc(&tmem_slot, 256);
         tmem_relinquish();
     }
-    if (warp == 1 && lane == 0) prefetch_tmap(&tm_x), prefetch_tmap(&tm_w);
+    if (warp == 1 && lane == 0) {
+        if (!kQuant) prefetch_tmap(&tm_x);
+        prefetch_tmap(&tm_w);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -381,11 +400,11 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     float sum[kN];
     if (warp == 0) {
         const auto arm = [&](int b, uint32_t s) {
-            mbar_arrive_expect_tx(&full[s], kStage);
+            mbar_arrive_expect_tx(&full[s], kQuant ? kBoxBytes : kStage);
             tma_load_2d(smem + s * kStage, &tm_w, &full[s], b * 128, nt * 128);
         };
         const auto load_x = [&](int b, uint32_t s) {
-            tma_load_2d(smem + s * kStage + kBoxBytes, &tm_x, &full[s], b * 128, mt * kN);
+            if (!kQuant) tma_load_2d(smem + s * kStage + kBoxBytes, &tm_x, &full[s], b * 128, mt * kN);
         };
         const int first = min(b1 - b0, a.stages);  // stages that nothing has used yet
         if (elect_one())
@@ -435,9 +454,9 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             __syncwarp();
             if (++s == (uint32_t)a.stages) s = 0, ph ^= 1u;
         }
-    } else {
+    } else if (warp < 6) {
         const int quarter = warp & 3;
-        float(*table)[kN] = factor[quarter];
+        float(*table)[kN] = kQuant ? factor : factor + 2 * quarter;
         const uint32_t tbase = tmem + ((uint32_t)(quarter * 32) << 16);
         const float *ws = a.ws + (int64_t)nt * a.blocks;
         const float *xs[kPer];
@@ -456,18 +475,22 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         uint64_t acc[kN / 2];
 #pragma unroll
         for (int i = 0; i < kN / 2; ++i) acc[i] = 0;
-        float f0[kPer], f1[kPer];  // of this block and the next
-        if (b0 < b1) scales(b0, f0);
-        if (b0 + 1 < b1) scales(b0 + 1, f1);
+        float f0[kPer] = {}, f1[kPer] = {};  // of this block and the next
+        if (!kQuant && b0 < b1) scales(b0, f0);
+        if (!kQuant && b0 + 1 < b1) scales(b0 + 1, f1);
         for (int b = b0; b < b1; ++b) {
-            const uint32_t it = (uint32_t)(b - b0), i = it % kBufs;
+            const uint32_t it = (uint32_t)(b - b0), i = it % kBufs, at = kQuant ? i : it & 1u;
+            if constexpr (!kQuant) {
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-                if (k * 32 + lane < kN) table[it & 1u][k * 32 + lane] = f0[k];
-                f0[k] = f1[k];
+                for (int k = 0; k < kPer; ++k) {
+                    if (k * 32 + lane < kN) table[at][k * 32 + lane] = f0[k];
+                    f0[k] = f1[k];
+                }
+                if (b + 2 < b1) scales(b + 2, f1);
+                __syncwarp();
+            } else if (!bar_wait(&factor_full[i], (it / kBufs) & 1u, &abort_flag, a.err)) {
+                break;
             }
-            if (b + 2 < b1) scales(b + 2, f1);
-            __syncwarp();
             if (!bar_wait(&acc_full[i], (it / kBufs) & 1u, &abort_flag, a.err)) break;
             tc_fence_after();
             const uint32_t t = tbase + i * kAccCols;
@@ -483,6 +506,10 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                     tmem_tie(r);
                 else
                     tmem_tie16(r);
+                float4 fs[kChunk / 4];  // read before they go back with the accumulator
+#pragma unroll
+                for (int j = 0; j < kChunk / 4; ++j)
+                    fs[j] = *reinterpret_cast<const float4 *>(&table[at][kChunk * c + 4 * j]);
                 if (c + 1 == kN / kChunk) {
                     tc_fence_before();
                     __syncwarp();
@@ -490,7 +517,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 }
 #pragma unroll
                 for (int j = 0; j < kChunk / 4; ++j) {
-                    const float4 f = *reinterpret_cast<const float4 *>(&table[it & 1u][kChunk * c + 4 * j]);
+                    const float4 f = fs[j];
                     uint64_t *s2 = acc + (kChunk * c) / 2 + 2 * j;
                     s2[0] = fma2(f2(f.x, f.y), f2(r[4 * j], r[4 * j + 1]), s2[0]);
                     s2[1] = fma2(f2(f.z, f.w), f2(r[4 * j + 2], r[4 * j + 3]), s2[1]);
@@ -499,19 +526,69 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         }
 #pragma unroll
         for (int i = 0; i < kN / 2; ++i) unf2(acc[i], sum[2 * i], sum[2 * i + 1]);
+    } else if constexpr (kQuant) {
+        // Sixteen lanes a row, two rows at a time; the codes go where the copy's swizzle
+        // would have put them.  Rows past the last are not written: they are columns of the
+        // product that nothing reads.
+        const int q = warp - 6, l = lane & 15, live = min(kN, a.rows - mt * kN);
+        const X *x = (const X *)a.x + (int64_t)mt * kN * a.x_stride;
+        for (int b = b0 + q; b < b1; b += 4) {
+            const uint32_t it = (uint32_t)(b - b0), i = it % kBufs;
+            const uint32_t s = it % (uint32_t)a.stages, ph = (it / (uint32_t)a.stages) & 1u;
+            const int col = b * 128 + l * 8;
+            Raw8<X> raw[kN / 2];
+#pragma unroll
+            for (int u = 0; u < kN / 2; ++u) {
+                const int r = 2 * u + (lane >> 4);
+                raw[u] = Raw8<X>{};
+                if (r < live && col < a.n_in) raw[u] = load_raw8(x + r * a.x_stride + col);
+            }
+            const float w = __ldg(a.ws + (int64_t)nt * a.blocks + b);
+            if (!bar_wait(&empty[s], ph ^ 1u, &abort_flag, a.err) ||
+                !bar_wait(&acc_empty[i], ((it / kBufs) & 1u) ^ 1u, &abort_flag, a.err))
+                break;
+            uint8_t *codes = smem + s * kStage + kBoxBytes;
+            const auto put = [&](int r, uint2 c) {
+                if (r < live)
+                    *reinterpret_cast<uint2 *>(codes + r * 128 + (((l >> 1) ^ (r & 7)) << 4) + (l & 1) * 8) = c;
+            };
+            if (live <= 2) {
+                float v[8], scale;
+                as_floats(raw[0], v);
+                put(lane >> 4, quantise_block(v, &scale));
+                if (l == 0) factor[i][lane >> 4] = scale * w;
+            } else {
+#pragma unroll
+                for (int u = 0; u < kN / 2; u += kQuantUnroll) {
+                    if (2 * u >= live) break;  // the whole warp
+                    float v[kQuantUnroll][8], scale;
+                    uint2 c[kQuantUnroll];
+#pragma unroll
+                    for (int k = 0; k < kQuantUnroll; ++k) as_floats(raw[u + k], v[k]);
+                    quantise_blocks(v, &scale, c);
+#pragma unroll
+                    for (int k = 0; k < kQuantUnroll; ++k) put(2 * (u + k) + (lane >> 4), c[k]);
+                    if ((l & 3) == 0) factor[i][2 * (u + quant_lane()) + (lane >> 4)] = scale * w;
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[s]), mbar_arrive(&factor_full[i]);
+        }
     }
 
     // The sums of the cluster's CTAs, added in the order of the blocks: row j of x is CTA j %
     // split's, and every CTA sends it its sums (the stages, done with everywhere, hold
     // them).  Sent sums do not wait for one another; fetched ones did, 6 us for 64 rows.
-    const int row = (warp & 3) * 32 + lane;  // epilogue warps: the output column in the tile
+    const bool scales_and_adds = warp >= 2 && warp < 6;
+    const int row = (warp & 3) * 32 + lane;  // their output column in the tile
     const int64_t n = (int64_t)nt * 128 + row;
     const int m0 = mt * kN, live = min(kN, a.rows - m0);
     T *y = (T *)a.y + (int64_t)m0 * a.n_out + n;
     tc_fence_before();
     __syncthreads();  // the loads have landed and been read, on the failing path too
     if (split == 1) {
-        if (warp >= 2 && n < a.n_out) {
+        if (scales_and_adds && n < a.n_out) {
 #pragma unroll
             for (int j = 0; j < kN; ++j)
                 if (j < live) from_f32(y + (int64_t)j * a.n_out, sum[j]);
@@ -520,7 +597,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         float *part = reinterpret_cast<float *>(smem);  // [sender][slot][128]
         const int slots = (kN + split - 1) / split;
         cluster_sync();
-        if (warp >= 2) {
+        if (scales_and_adds) {
             const uint32_t mine = smem_u32(part) + (uint32_t)((rank * slots * 128 + row) * 4);
             int to = 0, slot = 0;
 #pragma unroll
@@ -531,7 +608,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         }
         __syncwarp();
         cluster_sync();
-        if (warp >= 2 && n < a.n_out) {
+        if (scales_and_adds && n < a.n_out) {
 #pragma unroll 4
             for (int s = 0; s < (live - rank + split - 1) / split; ++s) {
                 float v = 0.0f;
@@ -580,7 +657,7 @@ dflash2_status launch_pair(const DeviceInfo &di, const uint8_t *xq, const uint8_
     return launch_status();
 }
 
-template <typename T, int kN>
+template <typename T, int kN, typename X>
 dflash2_status launch_few(const DeviceInfo &di, const uint8_t *xq, const uint8_t *wq, int32_t n_in, LinearArgs a,
                           cudaStream_t st) {
     static std::atomic<uint64_t> allowed{0};
@@ -600,13 +677,14 @@ dflash2_status launch_few(const DeviceInfo &di, const uint8_t *xq, const uint8_t
             break;
         }
     CUtensorMap tm_x, tm_w;
-    dflash2_status s = encode_tmap_2d(&tm_x, xq, (uint64_t)a.rows, (uint64_t)n_in, kN, 1);
-    if (s == DFLASH2_OK) s = encode_tmap_2d(&tm_w, wq, (uint64_t)a.n_out, (uint64_t)n_in, 128, 1);
-    if (s == DFLASH2_OK) s = allow_smem(linear_few_kernel<T, kN>, most, di.device, allowed);
+    dflash2_status s = encode_tmap_2d(&tm_w, wq, (uint64_t)a.n_out, (uint64_t)n_in, 128, 1);
+    tm_x = tm_w;
+    if (s == DFLASH2_OK && !kQuantises<X>) s = encode_tmap_2d(&tm_x, xq, (uint64_t)a.rows, (uint64_t)n_in, kN, 1);
+    if (s == DFLASH2_OK) s = allow_smem(linear_few_kernel<T, kN, X>, most, di.device, allowed);
     if (s != DFLASH2_OK) return s;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * split));
-    cfg.blockDim = dim3(kFewThreads);
+    cfg.blockDim = dim3(kQuantises<X> ? kFewQuantThreads : kFewThreads);
     cfg.dynamicSmemBytes = a.stages * stage + 1024;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -616,16 +694,18 @@ dflash2_status launch_few(const DeviceInfo &di, const uint8_t *xq, const uint8_t
     attr[1].val.clusterDim.x = (unsigned)split, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    cudaLaunchKernelEx(&cfg, linear_few_kernel<T, kN>, tm_x, tm_w, a, split);
+    cudaLaunchKernelEx(&cfg, linear_few_kernel<T, kN, X>, tm_x, tm_w, a, split);
     return launch_status();
 }
 
 template <typename T>
 dflash2_status launch_linear(const DeviceInfo &di, const uint8_t *xq, const uint8_t *wq, int32_t n_in,
-                             const LinearArgs &a, cudaStream_t st) {
-    if (a.rows <= 16) return launch_few<T, 16>(di, xq, wq, n_in, a, st);
-    if (a.rows <= 32) return launch_few<T, 32>(di, xq, wq, n_in, a, st);
-    if (a.rows <= 64) return launch_few<T, 64>(di, xq, wq, n_in, a, st);
+                             const LinearArgs &a, int32_t x_dtype, cudaStream_t st) {
+    if (a.x && x_dtype == DFLASH2_F32) return launch_few<T, 16, float>(di, xq, wq, n_in, a, st);
+    if (a.x) return launch_few<T, 16, __nv_bfloat16>(di, xq, wq, n_in, a, st);
+    if (a.rows <= 16) return launch_few<T, 16, uint8_t>(di, xq, wq, n_in, a, st);
+    if (a.rows <= 32) return launch_few<T, 32, uint8_t>(di, xq, wq, n_in, a, st);
+    if (a.rows <= 64) return launch_few<T, 64, uint8_t>(di, xq, wq, n_in, a, st);
     // The tile's width by the time of its waves: a block takes a pair 0.48 and 0.6 times as
     // long at 64 and 128 columns as at 256.
     const int64_t m_tiles = (a.rows + 255) / 256, pairs = di.sm_count / 2;
@@ -679,7 +759,10 @@ extern "C" dflash2_status dflash2_linear_fp8_blocks(const void *x, int64_t x_row
     if (st != DFLASH2_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     LinearArgs a{};
-    if (!x_q) {
+    const int64_t el = x_dtype == DFLASH2_F32 ? 4 : 2;
+    if (!x_q && rows <= 16 && aligned16(x) && (rows == 1 || x_row_stride * el % 16 == 0)) {
+        a.x = x, a.x_stride = x_row_stride, a.n_in = in_features;  // quantised as it is multiplied
+    } else if (!x_q) {
         uint8_t *q = static_cast<uint8_t *>(workspace);
         float *scale = reinterpret_cast<float *>(q + codes_bytes(rows, in_features));
         st = launch_quant_blocks_e4m3(x, x_row_stride, x_dtype, rows, in_features, q, scale, s);
@@ -690,6 +773,6 @@ extern "C" dflash2_status dflash2_linear_fp8_blocks(const void *x, int64_t x_row
     a.xs = x_scale, a.ws = w_scale;
     a.rows = (int32_t)rows, a.n_out = out_features, a.blocks = (in_features + 127) / 128;
     a.y = out, a.err = err_word;
-    return out_dtype == DFLASH2_F32 ? launch_linear<float>(di, x_q, w_q, in_features, a, s)
-                                    : launch_linear<__nv_bfloat16>(di, x_q, w_q, in_features, a, s);
+    return out_dtype == DFLASH2_F32 ? launch_linear<float>(di, x_q, w_q, in_features, a, x_dtype, s)
+                                    : launch_linear<__nv_bfloat16>(di, x_q, w_q, in_features, a, x_dtype, s);
 }

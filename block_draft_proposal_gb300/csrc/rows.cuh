@@ -133,6 +133,24 @@ __device__ __forceinline__ float finite_amax(float (&x)[8]) {
     }
     return amax;
 }
+// One block of 16 lanes.
+__device__ __forceinline__ uint2 quantise_block(float (&x)[8], float *scale) {
+    float amax = 0.0f;  // fmaxf leaves NaN out
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
+    const auto fold = [&]() {
+#pragma unroll
+        for (int o = kQuantLanes / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+    };
+    fold();
+    if (__any_sync(0xFFFFFFFFu, amax > FLT_MAX)) {
+        amax = finite_amax(x);
+        fold();
+    }
+    float inv;
+    block_scale(amax, scale, &inv);
+    return encode8(x, inv);
+}
 // Four blocks of the same 16 lanes at a time: the lanes' maxima are folded so that a
 // quarter of the lanes ends with each block's (5 shuffles in place of 16), and the
 // divisions are made once for the four.  The lane's `scale` is that of block quant_lane().

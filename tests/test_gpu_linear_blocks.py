@@ -18,7 +18,7 @@ def _check(y, x_q, x_s, w_q, w_s, name):
 
 
 SHAPES = [  # rows, in, out
-    (1, 16, 1), (1, 128, 128), (1, 4096, 384), (2, 144, 130), (7, 1936, 1001), (16, 256, 257), (17, 384, 96),
+    (1, 16, 1), (1, 128, 128), (1, 4096, 384), (3, 2560, 20000), (16, 2576, 7000), (9, 1040, 260), (2, 144, 130), (7, 1936, 1001), (16, 256, 257), (17, 384, 96),
     (33, 512, 640), (48, 1040, 200), (64, 128, 300), (65, 640, 128), (100, 2048, 130), (128, 256, 512),
     (129, 1296, 511), (200, 400, 264), (256, 256, 256), (257, 144, 1030), (300, 1152, 384), (513, 272, 520),
     (1000, 656, 776), (1500, 128, 144),
@@ -73,17 +73,18 @@ def test_nan_stays_in_its_row_and_column(cuda, rows):
     assert torch.isnan(y[2]).all() and not torch.isnan(y[0, 8:]).any()
 
 
-def test_strided_rows_and_zero_rows(cuda):
-    wide = ref.rows(50, 700, BF, 3).cuda()
+@pytest.mark.parametrize("rows,dtype", [(50, BF), (11, BF), (16, F32), (1, BF)])
+def test_strided_rows_and_zero_rows(cuda, rows, dtype):
+    wide = ref.rows(rows, 700, dtype, 3).cuda()
     w_q, w_s = (t.cuda() for t in ref.weights(200, 320, 4))
     for at in (0, 8, 3):                                       # 3: off 16-byte alignment
         x = wide[:, at:at + 320]
         y, _ = dflash2.linear_fp8_blocks(x, w_q, w_s)
         want, _ = dflash2.linear_fp8_blocks(x.contiguous(), w_q, w_s)
         assert torch.equal(y, want)
-    wide[7, :320] = 0
+    wide[rows // 7, :320] = 0
     y, _ = dflash2.linear_fp8_blocks(wide[:, :320], w_q, w_s)
-    assert not y[7].any()
+    assert not y[rows // 7].any()
     y, _ = dflash2.linear_fp8_blocks(wide[:0, :320], w_q, w_s)
     assert y.shape == (0, 200)
 
