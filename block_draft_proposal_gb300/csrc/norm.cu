@@ -34,27 +34,45 @@ struct NormArgs {
     bool code_vec;  // rows of codes are 8-byte aligned
 };
 
-template <typename T, bool kVec> struct Held {  // 8 values of a thread
+// 8 values of a thread, at first, first + step, ... of a row of n: steps of 1 and whole
+// 16-byte pieces (kVec), or any.
+template <typename T, bool kVec> struct Held {
     Raw8<T> raw;
-    __device__ __forceinline__ void load(const T *p, int n) {
+    __device__ __forceinline__ void load(const T *row, int first, int, int n) {
         raw = Raw8<T>{};
-        if (n > 0) raw = load_raw8_written(p);
+        if (first < n) raw = load_raw8_written(row + first);
     }
     __device__ __forceinline__ void get(float (&x)[8]) const { as_floats(raw, x); }
 };
 template <typename T> struct Held<T, false> {
     float v[8];
-    __device__ __forceinline__ void load(const T *p, int n) { load8_any(p, n, v); }
+    __device__ __forceinline__ void load(const T *row, int first, int step, int n) {
+        const T *p = row + first;
+        if (first + 7 * step < n) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = to_f32(p[i * step]);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = first + i * step < n ? to_f32(p[i * step]) : 0.0f;
+    }
     __device__ __forceinline__ void get(float (&x)[8]) const {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = v[i];
     }
 };
-template <typename T, bool kVec> __device__ __forceinline__ void put8(T *p, int n, const float (&x)[8]) {
+template <typename T, bool kVec>
+__device__ __forceinline__ void put8(T *row, int first, int step, int n, const float (&x)[8]) {
     if constexpr (kVec) {
-        if (n > 0) store8(p, x);
+        if (first < n) store8(row + first, x);
+    } else if (first + 7 * step < n) {
+        T *p = row + first;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) from_f32(p + i * step, x[i]);
     } else {
-        store8_any(p, n, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (first + i * step < n) from_f32(row + first + i * step, x[i]);
     }
 }
 
@@ -89,23 +107,25 @@ __global__ void __launch_bounds__(kThreads == 32 ? 256 : kThreads) sublayer_kern
     if (row >= a.rows) return;  // a whole warp or block
     const int hidden = a.hidden;
     const float inv_n = 1.0f / (float)hidden;
+    // Eight neighbouring values of each of four pieces of the row; rows that are not whole
+    // 16-byte pieces go value by value, neighbours in neighbouring threads, unless E4M3
+    // blocks want them as above.
+    const bool apart = !kVec && !a.scale;
+    const int step = apart ? per : 1, origin = apart ? t : t * 8;
+    const auto first = [&](int c) { return c * 8 * per + origin; };
 
     Held<TX, kVec> held[kChunks];
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-        const int col = (c * per + t) * 8;
-        held[c].load((const TX *)a.x + row * a.x_stride + col, hidden - col);
-    }
+    for (int c = 0; c < kChunks; ++c) held[c].load((const TX *)a.x + row * a.x_stride, first(c), step, hidden);
     float r[kChunks][8];
     float sum = 0.0f;
     if constexpr (kJoin) {
         Held<T, kVec> y[kChunks], g[kChunks];
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-            const int col = (c * per + t) * 8;
-            y[c].load((const T *)a.y + row * a.y_stride + col, hidden - col);
+            y[c].load((const T *)a.y + row * a.y_stride, first(c), step, hidden);
             if (a.gate_kind == kGateChannel || a.gate_kind == kGateFull)
-                g[c].load((const T *)a.gate + (a.gate_kind == kGateFull ? row * a.gate_stride : 0) + col, hidden - col);
+                g[c].load((const T *)a.gate + (a.gate_kind == kGateFull ? row * a.gate_stride : 0), first(c), step, hidden);
         }
         const float token_gate =
             a.gate_kind == kGateToken
@@ -126,14 +146,13 @@ __global__ void __launch_bounds__(kThreads == 32 ? 256 : kThreads) sublayer_kern
         const float factor = y_rms * a.branch * token_gate;
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-            const int col = (c * per + t) * 8;
             float h[8], v[8];
             y[c].get(h);
 #pragma unroll
             for (int i = 0; i < 8; ++i) h[i] *= factor;
             if (a.w_post) {
                 Held<T, kVec> w;
-                w.load((const T *)a.w_post + col, hidden - col);
+                w.load((const T *)a.w_post, first(c), step, hidden);
                 w.get(v);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) h[i] *= v[i] + a.w_off;
@@ -147,7 +166,7 @@ __global__ void __launch_bounds__(kThreads == 32 ? 256 : kThreads) sublayer_kern
 #pragma unroll
                 for (int i = 0; i < 8; ++i) r[c][i] += h[i];
             }
-            put8<TX, kVec>((TX *)a.r_out + row * a.r_stride + col, hidden - col, r[c]);
+            put8<TX, kVec>((TX *)a.r_out + row * a.r_stride, first(c), step, hidden, r[c]);
         }
         if (!a.w_next) return;
     } else {
@@ -158,18 +177,17 @@ __global__ void __launch_bounds__(kThreads == 32 ? 256 : kThreads) sublayer_kern
     for (int c = 0; c < kChunks; ++c)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (kVec || !kJoin || (c * per + t) * 8 + i < hidden) sum += r[c][i] * r[c][i];
+            if (kVec || !kJoin || first(c) + i * step < hidden) sum += r[c][i] * r[c][i];
     const float rms = __frsqrt_rn(row_sum<kWarpRow>(sum, red[1]) * inv_n + a.eps);
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
-        const int col = (c * per + t) * 8;
         Held<T, kVec> w;
         float v[8];
-        w.load((const T *)a.w_next + col, hidden - col);
+        w.load((const T *)a.w_next, first(c), step, hidden);
         w.get(v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) r[c][i] *= rms * (v[i] + a.w_off);
-        if (!a.scale) put8<T, kVec>((T *)a.out + row * hidden + col, hidden - col, r[c]);
+        if (!a.scale) put8<T, kVec>((T *)a.out + row * hidden, first(c), step, hidden, r[c]);
     }
     if (!a.scale) return;
     if (!kVec)
@@ -177,15 +195,14 @@ __global__ void __launch_bounds__(kThreads == 32 ? 256 : kThreads) sublayer_kern
         for (int c = 0; c < kChunks; ++c)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if ((c * per + t) * 8 + i >= hidden) r[c][i] = 0.0f;
+                if (first(c) + i >= hidden) r[c][i] = 0.0f;
     uint2 codes[kChunks];
     float scale;
     quantise_blocks(r, &scale, codes);
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-        const int col = (c * per + t) * 8;
-        if (col < hidden) store_codes((uint8_t *)a.out + row * hidden + col, hidden - col, a.code_vec, codes[c]);
-    }
+    for (int c = 0; c < kChunks; ++c)
+        if (first(c) < hidden)
+            store_codes((uint8_t *)a.out + row * hidden + first(c), hidden - first(c), a.code_vec, codes[c]);
     const int block = (quant_lane() * per + t) / kQuantLanes;
     if ((t & 3) == 0 && block * kQuantBlock < hidden)
         a.scale[row * ((hidden + kQuantBlock - 1) / kQuantBlock) + block] = scale;
@@ -254,7 +271,7 @@ __global__ void __launch_bounds__(kQuantThreads)
     Held<T, kVec> h[kQuantUnroll];
 #pragma unroll
     for (int u = 0; u < kQuantUnroll; ++u)
-        h[u].load(x + row * stride + block * kQuantBlock + lane * 8 + u * kQuantBlock, left - u * kQuantBlock);
+        h[u].load(x + row * stride + block * kQuantBlock + lane * 8, u * kQuantBlock, 1, left);
     float v[kQuantUnroll][8], s;
 #pragma unroll
     for (int u = 0; u < kQuantUnroll; ++u) h[u].get(v[u]);

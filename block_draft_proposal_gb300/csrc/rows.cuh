@@ -63,18 +63,6 @@ __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162flo
 __device__ __forceinline__ void from_f32(float *p, float v) { *p = v; }
 __device__ __forceinline__ void from_f32(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
-// Up to 8 values from p on (n of them; the rest zeros), value by value: rows of any
-// alignment and length.
-template <typename T> __device__ __forceinline__ void load8_any(const T *p, int n, float (&x)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = i < n ? to_f32(p[i]) : 0.0f;
-}
-template <typename T> __device__ __forceinline__ void store8_any(T *p, int n, const float (&x)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < n) from_f32(p + i, x[i]);
-}
-
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
 // The exponent of an E4M3 cache's row: the smallest e in [kKvMinExp, kKvMaxExp] with
