@@ -9,10 +9,21 @@
 // MMAs, whose scales are powers of two.
 //
 // Two kernels, by the rows (launch_linear):
-//   linear_pair_kernel  many rows: CTA pairs (M = 256 rows of x, kCols outputs).
-//   linear_few_kernel   few rows: the weights are the MMA's M side, 128 a CTA, and the
-//                       rows of x its N side; the blocks are split over a cluster's CTAs,
-//                       which add their sums through distributed shared memory.
+//   linear_pair_kernel  65 rows and more: CTA pairs (M = 256 rows of x, kCols outputs).
+//   linear_few_kernel   fewer: the weights are the MMA's M side, 128 a CTA, and the rows of
+//                       x its N side; the blocks are split over a cluster's CTAs, which
+//                       send one another their sums through distributed shared memory.
+// (64 rows x 4096 x 6144: 11.4 us by the few-row kernel, 10.6 by pairs; x 7168 x 7168 14.0
+// and 15.9; x 4096 x 1024 5.7 and 8.1.)
+//
+// Few rows are bound by the weights' bytes and the latencies around them, many by the
+// accumulators' round trip: a block's MMAs take a pair 512 cycles at 256 columns, and from
+// their issue to the accumulator's return some 1500 pass for two accumulators (last MMA to
+// the waiting warps 200, two TMEM loads and half the sums 370 to 440, the slowest of
+// sixteen warps 250 more), so a block takes about 750.
+// Measured on codes (graph replays): one row x 4096 x 6144 7.7 us, 3.3 TB/s; x 4096 x 28672
+// 20 us, 5.8 TB/s; 256 rows x 4096 x 6144 11.7 us; 512 16.6; 1536 x 5120 x 7168 47 us, 2.4
+// PFLOP/s; 8192 x 7168 x 7168 255 to 282 us with the clock, 3.0 to 3.3 PFLOP/s.
 #include <type_traits>
 
 #include "rows.cuh"
@@ -63,9 +74,10 @@ template <typename T> __device__ __forceinline__ void store32(T *p, int n, const
 
 // ---- many rows -----------------------------------------------------------------
 // Roles (384 threads, one CTA per SM, persistent over tiles): warps 0 and 3 load, warps 1
-// and 2 of the leader issue the MMAs (a pair of each, for the even and the odd blocks: waits,
-// copies and commits take one thread longer than the MMAs of a block), warps 4 to 11 scale and add: four lane quarters, each with
-// two warps that take half of the tile's columns, kCols / 2 sums a thread.
+// and 2 of the leader issue the MMAs (two of each, for the even and the odd blocks: one
+// thread's waits, copies and commits take longer than a block's MMAs), warps 4 to 11 scale
+// and add: four lane quarters, each with two warps that take half of the tile's columns,
+// kCols / 2 sums a thread.  As many accumulators as TMEM holds, 2 at 256 columns.
 constexpr int kPairThreads = 384;
 constexpr int kPairEpiWarps = 8;
 constexpr int kIssuers = 2;
@@ -116,8 +128,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                        const __grid_constant__ CUtensorMap tm_y, const LinearArgs a) {
     constexpr int kHalf = kCols / 2, kChunks = kHalf / 32;
-    // weight blocks of 128 that a thread's columns lie in
-    constexpr int kScales = 128 % kHalf == 0 ? 1 : kChunks;
+    static_assert(128 % kHalf == 0, "a thread's columns lie in one block of the weights");
     constexpr uint32_t kAccCols = kCols <= 64 ? 64 : kCols <= 128 ? 128 : 256, kBufs = 512 / kAccCols;
     constexpr uint32_t kStage = kPairStage<kCols>;
     extern __shared__ uint8_t dsmem[];
@@ -240,27 +251,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const int64_t m0 = (int64_t)mt * 256 + (int)rank * 128 + quarter * 32, m = m0 + lane;
             const int n0 = nt * kCols + half * kHalf;
             const float *xs = a.xs + min(m, (int64_t)a.rows - 1) * a.blocks;
-            const float *ws[kScales];
-#pragma unroll
-            for (int c = 0; c < kScales; ++c)  // columns past the end take the last block's scales
-                ws[c] = a.ws + (int64_t)(min(n0 + 32 * c, a.n_out - 1) / 128) * a.blocks;
+            // columns past the end take the last block's scales
+            const float *ws = a.ws + (int64_t)(min(n0, a.n_out - 1) / 128) * a.blocks;
             uint64_t sum[kHalf / 2];
 #pragma unroll
             for (int i = 0; i < kHalf / 2; ++i) sum[i] = 0;
-            float x_next = __ldg(xs), w_next[kScales];
-#pragma unroll
-            for (int c = 0; c < kScales; ++c) w_next[c] = __ldg(ws[c]);
+            float x_next = __ldg(xs), w_next = __ldg(ws);
             for (int b = 0; b < a.blocks; ++b, ++it) {
-                uint64_t f[kScales];
-#pragma unroll
-                for (int c = 0; c < kScales; ++c) {
-                    const float v = x_next * w_next[c];
-                    f[c] = f2(v, v);
-                }
+                const float v = x_next * w_next;
+                const uint64_t f = f2(v, v);
                 if (b + 1 < a.blocks) {  // the next block's scales, ahead of the wait
                     x_next = __ldg(xs + b + 1);
-#pragma unroll
-                    for (int c = 0; c < kScales; ++c) w_next[c] = __ldg(ws[c] + b + 1);
+                    w_next = __ldg(ws + b + 1);
                 }
                 const uint32_t i = it % kBufs;
                 if (!bar_wait(&acc_full[i], (it / kBufs) & 1u, &abort_flag, a.err)) {
@@ -288,8 +290,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     }
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
-                        sum[16 * c + j] = fma2(f[kScales == 1 ? 0 : c], f2(r[c & 1][2 * j], r[c & 1][2 * j + 1]),
-                                               sum[16 * c + j]);
+                        sum[16 * c + j] = fma2(f, f2(r[c & 1][2 * j], r[c & 1][2 * j + 1]), sum[16 * c + j]);
                     if (c + 2 < kChunks) tmem_ld32(t + 32 * (c + 2), r[c & 1]);
                 }
             }

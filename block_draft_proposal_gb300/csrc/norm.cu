@@ -11,8 +11,15 @@
 // pass, but the next norm would lose what cancels in r + h).  r' goes into the next norm
 // as computed in fp32, not as rounded for storage.
 //
-// HBM bounds them once the rows fill the GPU, a launch below that.  A thread holds
-// 4 x 8 values; a row takes as many threads as it needs (a warp up to 1024 values), and the loads of y, r and the gate are all in flight at once.
+// HBM bounds them once the rows fill the GPU, a launch below that, and issue slots where
+// E4M3 blocks are made (70 % busy).  A thread holds 4 x 8 values; a row takes as many
+// threads as it needs (a warp up to 1024 values), and the loads of y, r and the gate are
+// all in flight at once.  The choice goes by the row's length alone, so a row's result does
+// not depend on how many there are.
+// Measured (graph replays, rotating inputs): norm of 20011 x 7168 bf16 85 us, 6.8 TB/s; join
+// with an fp32 stream, a full sigmoid gate and both norms 320 us, 6.3 TB/s; norm of 20011 x
+// 5120 to E4M3 blocks 68 us, 4.5 TB/s; quantisation of 8192 x 7168 bf16 30 us, 6.0 TB/s; one
+// row of 4096: norm 2.1 us, join 3.1 us.
 #include "rows.cuh"
 
 namespace dflash2 {

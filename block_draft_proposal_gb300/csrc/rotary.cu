@@ -12,11 +12,13 @@
 //
 // Every value moves once: HBM bounds it, a launch where tokens are few.  A lane holds the
 // same two steps of 8 values of every row, chosen so that both halves of its pairs are
-// its own (for halves: step u and u + rotary_dim / 16), so sines and cosines are read from
-// shared memory once per token and the rows need no exchange between lanes but the E4M3
-// maximum.  A block computes its tokens' sines and cosines once and keeps several groups'
-// loads in flight per warp (computed by every warp of a token, at 18 instructions a value,
-// 20011 tokens x 56 rows took 172 us).
+// its own (for halves: step u and u + rotary_dim / 16), so its sines and cosines are read
+// from shared memory once per token and the rows need no exchange between lanes but the
+// E4M3 maximum.  A block computes its tokens' sines and cosines once and keeps several
+// groups' loads in flight per warp (computed by every warp of a token, at 18 instructions a
+// value, 20011 tokens x 56 rows took 172 us).
+// Measured, heads of 128, bf16: 20011 tokens, 40 + 8 heads with the write into an E4M3 cache
+// 90 us, 5.9 TB/s; 32 + 8 heads into a bf16 cache 86 us; 512 tokens 4.2 us; one 2.9 us.
 #include "rows.cuh"
 
 namespace dflash2 {

@@ -768,11 +768,14 @@ dflash2_status dflash2_quantize_blocks_e4m3(const void *x, int64_t x_row_stride,
  * out        device [rows, out_features], out_dtype f32 or bf16.
  * workspace  device, 256-byte aligned, ws_bytes >=
  *            dflash2_linear_fp8_blocks_workspace_size(...): the codes and scales
- *            of x.  Not read with x_q (may be NULL).
+ *            of x.  Not read with x_q (may be NULL).  Contents need no clearing;
+ *            calls that overlap on the GPU need one each.  out must not overlap
+ *            it or an input.
  * err_word   device int32 or NULL: DFLASH2_DEVERR_TIMEOUT.
  * Arithmetic: a block's products summed in fp32, times xs * ws (fp32), the blocks
  *            added in fp32; the result rounded once.  NaN codes give NaN.
- *            Reduction orders are fixed, so results are deterministic.
+ *            Reduction orders are fixed, so results are deterministic; they differ in
+ *            their last bits between calls of more and of fewer than 64 rows.
  * Errors:    rows outside [0, 2^20], in_features outside [1, 2^20], out_features
  *            outside [1, 2^24], rows * in or out * in >= 2^40, both or none of x
  *            and x_q, a null pointer, what dflash2_quantize_blocks_e4m3 refuses of
@@ -807,12 +810,12 @@ dflash2_status dflash2_linear_fp8_blocks(const void *x, int64_t x_row_stride, in
  *            at gate + i * gate_row_stride, _FULL rows of hidden values at that
  *            stride.  gate_act: identity, sigmoid or tanh of it.
  * residual_out  r' in residual_dtype, rows at residual_out_row_stride; may be
- *            `residual` itself (same stride), and must not overlap it otherwise.
+ *            `residual` itself (same stride).  Outputs overlap nothing else.
  * out        [rows, hidden]: in dtype where scale is NULL; else uint8 codes of E4M3
  *            blocks, with scale float [rows, ceil(hidden / 128)].
  * Arithmetic: fp32, sums of squares included; the next norm takes r' as computed,
  *            not as rounded.  Reduction orders are fixed.  A row of zeros with eps
- *            0 gives NaN (0 / 0).
+ *            0 gives NaN (0 / 0).  A row's result does not depend on the others.
  * Errors:    rows outside [0, 2^31), hidden outside [1, 32768], eps negative or not
  *            finite, weight_offset or branch_scale not finite, a row stride below
  *            hidden (gate per token: below 1) or above 2^32, an unknown gate kind or
