@@ -370,8 +370,7 @@ __global__ void __launch_bounds__(kQuantises<X> ? kFewQuantThreads : kFewThreads
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = blockIdx.x % split;  // the CTA's rank in its cluster
-    const int tile = blockIdx.x / split;
-    const int nt = tile % a.n_tiles, mt = tile / a.n_tiles;
+    const int nt = blockIdx.x / split;    // its tile of 128 output columns
     const int b0 = (int)((int64_t)a.blocks * rank / split), b1 = (int)((int64_t)a.blocks * (rank + 1) / split);
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) mbar_init(&full[s], kQuant ? 2 : 1), mbar_init(&empty[s], 1);
@@ -405,7 +404,7 @@ __global__ void __launch_bounds__(kQuantises<X> ? kFewQuantThreads : kFewThreads
             tma_load_2d(smem + s * kStage, &tm_w, &full[s], b * 128, nt * 128);
         };
         const auto load_x = [&](int b, uint32_t s) {
-            if (!kQuant) tma_load_2d(smem + s * kStage + kBoxBytes, &tm_x, &full[s], b * 128, mt * kN);
+            if (!kQuant) tma_load_2d(smem + s * kStage + kBoxBytes, &tm_x, &full[s], b * 128, 0);
         };
         const int first = min(b1 - b0, a.stages);  // stages that nothing has used yet
         if (elect_one())
@@ -464,9 +463,9 @@ __global__ void __launch_bounds__(kQuantises<X> ? kFewQuantThreads : kFewThreads
         bool in[kPer];
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            const int64_t m = (int64_t)mt * kN + i * 32 + lane;
-            in[i] = m < a.rows && i * 32 + lane < kN;
-            xs[i] = a.xs + (in[i] ? m : 0) * a.blocks;
+            const int m = i * 32 + lane;
+            in[i] = m < a.rows;
+            xs[i] = a.xs + (int64_t)(in[i] ? m : 0) * a.blocks;
         }
         const auto scales = [&](int b, float (&f)[kPer]) {
             const float w = __ldg(ws + b);
@@ -531,8 +530,8 @@ __global__ void __launch_bounds__(kQuantises<X> ? kFewQuantThreads : kFewThreads
         // Sixteen lanes a row, two rows at a time; the codes go where the copy's swizzle
         // would have put them.  Rows past the last are not written: they are columns of the
         // product that nothing reads.
-        const int q = warp - 6, l = lane & 15, live = min(kN, a.rows - mt * kN);
-        const X *x = (const X *)a.x + (int64_t)mt * kN * a.x_stride;
+        const int q = warp - 6, l = lane & 15, live = a.rows;
+        const X *x = (const X *)a.x;
         for (int b = b0 + q; b < b1; b += 4) {
             const uint32_t it = (uint32_t)(b - b0), i = it % kBufs;
             const uint32_t s = it % (uint32_t)a.stages, ph = (it / (uint32_t)a.stages) & 1u;
@@ -584,8 +583,8 @@ __global__ void __launch_bounds__(kQuantises<X> ? kFewQuantThreads : kFewThreads
     const bool scales_and_adds = warp >= 2 && warp < 6;
     const int row = (warp & 3) * 32 + lane;  // their output column in the tile
     const int64_t n = (int64_t)nt * 128 + row;
-    const int m0 = mt * kN, live = min(kN, a.rows - m0);
-    T *y = (T *)a.y + (int64_t)m0 * a.n_out + n;
+    const int live = a.rows;
+    T *y = (T *)a.y + n;
     tc_fence_before();
     __syncthreads();  // the loads have landed and been read, on the failing path too
     if (split == 1) {
@@ -638,8 +637,7 @@ dflash2_status launch_pair(const DeviceInfo &di, const uint8_t *xq, const uint8_
     constexpr uint32_t outs = 8 * kOutBytes;
     a.stages = min(kMaxStages, (int)((kSmemMost - 1024 - outs) / stage));
     a.m_tiles = (a.rows + 255) / 256, a.n_tiles = (a.n_out + kCols - 1) / kCols;
-    const int64_t total = (int64_t)a.m_tiles * a.n_tiles;
-    if (total > INT32_MAX / 2) return DFLASH2_ERR_INVALID_ARG;
+    const int total = a.m_tiles * a.n_tiles;  // below 2^27 (shape_ok)
     CUtensorMap tm_x, tm_w, tm_y;
     dflash2_status s = encode_tmap_2d(&tm_x, xq, (uint64_t)a.rows, (uint64_t)n_in, 128, 1);
     if (s == DFLASH2_OK) s = encode_tmap_2d(&tm_w, wq, (uint64_t)a.n_out, (uint64_t)n_in, kCols / 2, 1);
@@ -652,7 +650,7 @@ dflash2_status launch_pair(const DeviceInfo &di, const uint8_t *xq, const uint8_
                            {32 * (uint32_t)sizeof(T), 32, 1}, 1);
     if (s == DFLASH2_OK) s = allow_smem(linear_pair_kernel<T, kCols>, kSmemMost, di.device, allowed);
     if (s != DFLASH2_OK) return s;
-    const int pairs = (int)min((int64_t)di.sm_count / 2, total);
+    const int pairs = min(di.sm_count / 2, total);
     launch_k(linear_pair_kernel<T, kCols>, dim3(2 * pairs), dim3(kPairThreads), a.stages * stage + outs + 1024, st,
              tm_x, tm_w, tm_y, a);
     return launch_status();
@@ -665,9 +663,7 @@ dflash2_status launch_few(const DeviceInfo &di, const uint8_t *xq, const uint8_t
     constexpr uint32_t stage = kFewStage<kN>;
     constexpr int most = 108 * 1024;  // two CTAs per SM
     a.stages = min(kMaxStages, (int)((most - 1024) / stage));
-    a.m_tiles = (a.rows + kN - 1) / kN, a.n_tiles = (a.n_out + 127) / 128;
-    const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles;
-    if (tiles > INT32_MAX / kFewMaxSplit) return DFLASH2_ERR_INVALID_ARG;
+    const int tiles = (a.n_out + 127) / 128;
     // As many CTAs as run at once (two per SM), with two blocks each: one row x 4096 x 6144
     // takes 11.4 us unsplit, 7.6 us split in four, 11.5 in eight (a second wave); x 4096 x
     // 1024 10.7, 5.0 and 4.0 us.  Clusters of 6 leave SMs idle (12.0 us for the first).
@@ -719,7 +715,7 @@ dflash2_status launch_linear(const DeviceInfo &di, const uint8_t *xq, const uint
 
 bool shape_ok(int64_t rows, int32_t n_in, int32_t n_out) {
     return rows >= 0 && rows <= 1 << 20 && n_in >= 1 && n_in <= 1 << 20 && n_out >= 1 && n_out <= 1 << 24 &&
-           rows * n_in < 1ll << 40 && (int64_t)n_out * n_in < 1ll << 40;
+           rows * n_in < 1ll << 40 && (int64_t)n_out * n_in < 1ll << 40 && rows * n_out < 1ll << 40;
 }
 size_t codes_bytes(int64_t rows, int32_t n_in) { return ((size_t)rows * n_in + 255) / 256 * 256; }
 

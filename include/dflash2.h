@@ -777,8 +777,8 @@ dflash2_status dflash2_quantize_blocks_e4m3(const void *x, int64_t x_row_stride,
  *            Reduction orders are fixed, so results are deterministic; they differ in
  *            their last bits between calls of more and of fewer than 64 rows.
  * Errors:    rows outside [0, 2^20], in_features outside [1, 2^20], out_features
- *            outside [1, 2^24], rows * in or out * in >= 2^40, both or none of x
- *            and x_q, a null pointer, what dflash2_quantize_blocks_e4m3 refuses of
+ *            outside [1, 2^24], rows * in, out * in or rows * out >= 2^40, both or
+ *            none of x and x_q, a null pointer, what dflash2_quantize_blocks_e4m3 refuses of
  *            x -> INVALID_ARG; an unknown dtype -> UNSUPPORTED_DTYPE; in_features
  *            % 16 != 0 or a pointer not aligned as above or to its element ->
  *            MISALIGNED; a workspace (with x) that is NULL, too small or not

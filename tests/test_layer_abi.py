@@ -47,7 +47,7 @@ def _linear(lib, **kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(xt=2), DTYPE), (dict(ot=-1), DTYPE), (dict(rows=-1), INVALID), (dict(rows=2 ** 20 + 1), INVALID),
     (dict(n_in=0, stride=0), INVALID), (dict(n_out=0), INVALID), (dict(n_out=2 ** 24, n_in=2 ** 17, stride=2 ** 17), INVALID),
-    (dict(stride=255), INVALID), (dict(n_in=248), MISALIGNED), (dict(x=None), INVALID), (dict(xq=P, xs=P), INVALID),
+    (dict(rows=2 ** 18, n_out=2 ** 22, n_in=16, stride=16), INVALID), (dict(stride=255), INVALID), (dict(n_in=248), MISALIGNED), (dict(x=None), INVALID), (dict(xq=P, xs=P), INVALID),
     (dict(x=None, xq=P), INVALID), (dict(w=None), INVALID), (dict(ws=None), INVALID), (dict(out=None), INVALID),
     (dict(x=ODD), MISALIGNED), (dict(w=ctypes.c_void_p(264)), MISALIGNED), (dict(out=ODD), MISALIGNED),
     (dict(ws=ctypes.c_void_p(258)), MISALIGNED), (dict(err=ODD), MISALIGNED),
