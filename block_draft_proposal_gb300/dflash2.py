@@ -990,12 +990,20 @@ def _need_matrix(t: torch.Tensor, name: str, dtype=None, shape=None) -> int:
     raise ValueError(f"{name} must not repeat rows")
 
 
+_one_device = None  # whether there is but one: then every CUDA tensor lies on it
+
+
 def _current_device() -> int:
     return torch._C._cuda_getDevice()
 
 
 def _need_one_device(*tensors):
     """Everything a call is given lies on the current device, where it is launched."""
+    global _one_device
+    if _one_device:
+        return
+    if _one_device is None:
+        _one_device = torch.cuda.device_count() == 1
     dev = _current_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:

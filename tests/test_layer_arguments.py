@@ -41,6 +41,7 @@ def allocations(monkeypatch):
     monkeypatch.setattr(dflash2, "_ptr", lambda t: None if t is None else 256)
     monkeypatch.setattr(dflash2, "_stream", lambda s: 0 if s is None else s.cuda_stream)
     monkeypatch.setattr(dflash2, "_current_device", lambda: 0)
+    monkeypatch.setattr(dflash2, "_one_device", False)
     with FakeTensorMode():
         yield log
 
