@@ -21,6 +21,7 @@
 // 5120 to E4M3 blocks 68 us, 4.5 TB/s; quantisation of 8192 x 7168 bf16 30 us, 6.0 TB/s; one
 // row of 4096: norm 2.1 us, join 3.1 us.
 #include "rows.cuh"
+#include "tcgen05.cuh"
 
 namespace dflash2 {
 namespace {
@@ -83,6 +84,29 @@ __device__ __forceinline__ void put8(T *row, int first, int step, int n, const f
     }
 }
 
+// Eight values two at a time (one issue slot each; the kernel is bound by them where it
+// makes E4M3 blocks).
+__device__ __forceinline__ uint64_t two(const float (&x)[8], int i) { return f2(x[2 * i], x[2 * i + 1]); }
+__device__ __forceinline__ void set_two(float (&x)[8], int i, uint64_t v) { unf2(v, x[2 * i], x[2 * i + 1]); }
+__device__ __forceinline__ void add_squares(const float (&x)[8], uint64_t &sum) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum = fma2(two(x, i), two(x, i), sum);
+}
+__device__ __forceinline__ float both(uint64_t v) {
+    float lo, hi;
+    unf2(v, lo, hi);
+    return lo + hi;
+}
+// x *= factor * (w + offset), or factor alone
+__device__ __forceinline__ void scale8(float (&x)[8], float factor) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) set_two(x, i, mul2(two(x, i), f2(factor, factor)));
+}
+__device__ __forceinline__ void weigh8(float (&x)[8], const float (&w)[8], float offset) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) set_two(x, i, mul2(two(x, i), add2(two(w, i), f2(offset, offset))));
+}
+
 __device__ __forceinline__ float gate_value(float g, int act) {
     if (act == DFLASH2_GATE_SIGMOID) return __fdividef(1.0f, 1.0f + expf(-g));  // 2 ulp each
     return act == DFLASH2_GATE_TANH ? tanhf(g) : g;
@@ -125,7 +149,7 @@ __global__ void __launch_bounds__(kThreads == 32 ? 256 : kThreads) sublayer_kern
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) held[c].load((const TX *)a.x + row * a.x_stride, first(c), step, hidden);
     float r[kChunks][8];
-    float sum = 0.0f;
+    uint64_t sum = 0;
     if constexpr (kJoin) {
         Held<T, kVec> y[kChunks], g[kChunks];
 #pragma unroll
@@ -139,15 +163,14 @@ __global__ void __launch_bounds__(kThreads == 32 ? 256 : kThreads) sublayer_kern
                 ? gate_value(to_f32(((const T *)a.gate)[row * a.gate_stride]), a.gate_act) : 1.0f;
         float y_rms = 1.0f;
         if (a.w_post) {
-            float s = 0.0f;
+            uint64_t s = 0;
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
                 float v[8];
                 y[c].get(v);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) s += v[i] * v[i];
+                add_squares(v, s);
             }
-            y_rms = __frsqrt_rn(row_sum<kWarpRow>(s, red[0]) * inv_n + a.eps);
+            y_rms = __frsqrt_rn(row_sum<kWarpRow>(both(s), red[0]) * inv_n + a.eps);
         }
         // the branch's scale goes with the row's root or its gate
         const float factor = y_rms * a.branch * token_gate;
@@ -155,23 +178,23 @@ __global__ void __launch_bounds__(kThreads == 32 ? 256 : kThreads) sublayer_kern
         for (int c = 0; c < kChunks; ++c) {
             float h[8], v[8];
             y[c].get(h);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) h[i] *= factor;
+            scale8(h, factor);
             if (a.w_post) {
                 Held<T, kVec> w;
                 w.load((const T *)a.w_post, first(c), step, hidden);
                 w.get(v);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) h[i] *= v[i] + a.w_off;
+                weigh8(h, v, a.w_off);
             }
             held[c].get(r[c]);
             if (a.gate_kind == kGateChannel || a.gate_kind == kGateFull) {
                 g[c].get(v);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) r[c][i] += h[i] * gate_value(v[i], a.gate_act);
+                for (int i = 0; i < 8; ++i) v[i] = gate_value(v[i], a.gate_act);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) set_two(r[c], i, fma2(two(h, i), two(v, i), two(r[c], i)));
             } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) r[c][i] += h[i];
+                for (int i = 0; i < 4; ++i) set_two(r[c], i, add2(two(r[c], i), two(h, i)));
             }
             put8<TX, kVec>((TX *)a.r_out + row * a.r_stride, first(c), step, hidden, r[c]);
         }
@@ -181,19 +204,16 @@ __global__ void __launch_bounds__(kThreads == 32 ? 256 : kThreads) sublayer_kern
         for (int c = 0; c < kChunks; ++c) held[c].get(r[c]);
     }
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (kVec || !kJoin || first(c) + i * step < hidden) sum += r[c][i] * r[c][i];
-    const float rms = __frsqrt_rn(row_sum<kWarpRow>(sum, red[1]) * inv_n + a.eps);
+    for (int c = 0; c < kChunks; ++c) add_squares(r[c], sum);  // past the end r is 0, or the row NaN
+    const float rms = __frsqrt_rn(row_sum<kWarpRow>(both(sum), red[1]) * inv_n + a.eps);
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
         Held<T, kVec> w;
         float v[8];
         w.load((const T *)a.w_next, first(c), step, hidden);
         w.get(v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r[c][i] *= rms * (v[i] + a.w_off);
+        scale8(r[c], rms);
+        weigh8(r[c], v, a.w_off);
         if (!a.scale) put8<T, kVec>((T *)a.out + row * hidden, first(c), step, hidden, r[c]);
     }
     if (!a.scale) return;
