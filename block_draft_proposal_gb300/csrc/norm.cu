@@ -11,15 +11,15 @@
 // pass, but the next norm would lose what cancels in r + h).  r' goes into the next norm
 // as computed in fp32, not as rounded for storage.
 //
-// HBM bounds them once the rows fill the GPU, a launch below that, and issue slots where
-// E4M3 blocks are made (70 % busy).  A thread holds 4 x 8 values; a row takes as many
+// HBM bounds them once the rows fill the GPU, a launch below that.  A thread holds 4 x 8 values; a row takes as many
 // threads as it needs (a warp up to 1024 values), and the loads of y, r and the gate are
 // all in flight at once.  The choice goes by the row's length alone, so a row's result does
 // not depend on how many there are.
-// Measured (graph replays, rotating inputs): norm of 20011 x 7168 bf16 85 us, 6.8 TB/s; join
-// with an fp32 stream, a full sigmoid gate and both norms 320 us, 6.3 TB/s; norm of 20011 x
-// 5120 to E4M3 blocks 68 us, 4.5 TB/s; quantisation of 8192 x 7168 bf16 30 us, 6.0 TB/s; one
-// row of 4096: norm 2.1 us, join 3.1 us.
+// Measured (graph replays, rotating inputs): norm of 20011 x 7168 bf16 86 us, 6.7 TB/s; join
+// with an fp32 stream, a full sigmoid gate and both norms 284 us, 7.1 TB/s; bf16 join without
+// a gate 165 us, 6.9 TB/s, to E4M3 blocks 167; norm of 20011 x 5120 to E4M3 blocks 61 us, 5.1
+// TB/s; quantisation of 8192 x 7168 bf16 30 us, 6.0 TB/s; one row of 4096: norm 2.3 us, join
+// 3.2 us.
 #include "rows.cuh"
 #include "tcgen05.cuh"
 
@@ -84,8 +84,7 @@ __device__ __forceinline__ void put8(T *row, int first, int step, int n, const f
     }
 }
 
-// Eight values two at a time (one issue slot each; the kernel is bound by them where it
-// makes E4M3 blocks).
+// Eight values two at a time, an issue slot for both.
 __device__ __forceinline__ uint64_t two(const float (&x)[8], int i) { return f2(x[2 * i], x[2 * i + 1]); }
 __device__ __forceinline__ void set_two(float (&x)[8], int i, uint64_t v) { unf2(v, x[2 * i], x[2 * i + 1]); }
 __device__ __forceinline__ void add_squares(const float (&x)[8], uint64_t &sum) {
@@ -125,9 +124,23 @@ template <bool kWarpRow> __device__ __forceinline__ float row_sum(float v, float
     return v;
 }
 
+// Blocks of 256 threads per SM that the registers leave room for, by the bytes a value takes:
+// rows in flight against what a thread holds of each.  20011 x 7168: join with an fp32 stream
+// and a full gate 2: 315 us, 3: 284, 4: 309; bf16 join 2: 176, 4: 165; fp32 join of 20011 x
+// 4096 2: 189, 3: 242; bf16 norm 4: 90, 5: 86.  (Value by value, a thread holds them in
+// fp32: one block fewer in bf16.)
+template <typename TX, typename T, bool kVec, bool kJoin>
+constexpr int kBlocks256 = kJoin ? (sizeof(TX) + sizeof(T) == 4   ? (kVec ? 4 : 3)
+                                    : sizeof(TX) + sizeof(T) == 6 ? 3 : 2)
+                           : kVec && sizeof(TX) + sizeof(T) == 4 ? 5 : 4;
+template <typename TX, typename T, bool kVec, bool kJoin, int kThreads>
+constexpr int kRowBlocks = kThreads <= 256 ? kBlocks256<TX, T, kVec, kJoin>
+                           : kThreads == 512 && kBlocks256<TX, T, kVec, kJoin> > 3 ? 2 : 1;
+
 // kThreads: a row's threads at most; 32 stands for a warp per row, 8 rows a block.
 template <typename TX, typename T, bool kVec, bool kJoin, int kThreads>
-__global__ void __launch_bounds__(kThreads == 32 ? 256 : kThreads) sublayer_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kThreads == 32 ? 256 : kThreads, kRowBlocks<TX, T, kVec, kJoin, kThreads>)
+    sublayer_kernel(const NormArgs a) {
     constexpr bool kWarpRow = kThreads == 32;
     constexpr int kChunks = kQuantUnroll;
     __shared__ float red[2][32];
@@ -244,6 +257,8 @@ dflash2_status launch_vec(const NormArgs &a, cudaStream_t st) {
                  st, a);
     else if (threads <= 256)
         launch_k(sublayer_kernel<TX, T, kVec, kJoin, 256>, dim3((unsigned)a.rows), dim3(threads), 0, st, a);
+    else if (threads <= 512)
+        launch_k(sublayer_kernel<TX, T, kVec, kJoin, 512>, dim3((unsigned)a.rows), dim3(threads), 0, st, a);
     else
         launch_k(sublayer_kernel<TX, T, kVec, kJoin, 1024>, dim3((unsigned)a.rows), dim3(threads), 0, st, a);
     return launch_status();

@@ -11,7 +11,7 @@ from block_draft_proposal_gb300 import dflash2
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
 SHAPES = [(1, 1), (3, 7), (5, 64), (2, 1000), (9, 1024), (4, 1032), (33, 4096), (2, 7168), (3, 8200),
-          (2, 9999), (1, 32768)]
+          (2, 9999), (3, 16384), (2, 20001), (1, 32768)]
 
 
 def _weight(n, dtype, seed):
@@ -34,7 +34,7 @@ def test_norm(cuda, n, hidden, xt, wt, e4m3):
             check(f"norm {n}x{hidden}", out, want, bound + ref.HALF_STEP[wt] * want.abs())
 
 
-@pytest.mark.parametrize("n,hidden", [(1, 5), (4, 256), (7, 1000), (3, 4096), (2, 8200)])
+@pytest.mark.parametrize("n,hidden", [(1, 5), (4, 256), (7, 1000), (3, 4096), (2, 8200), (2, 16392)])
 @pytest.mark.parametrize("rt,dt", [(BF, BF), (F32, BF), (F32, F32), (BF, F32)])
 @pytest.mark.parametrize("gate,act", [("none", "none"), ("channel", "tanh"), ("token", "sigmoid"),
                                       ("full", "sigmoid"), ("full", "none")])
