@@ -18,7 +18,7 @@
 // groups' loads in flight per warp (computed by every warp of a token, at 18 instructions a
 // value, 20011 tokens x 56 rows took 172 us).
 // Measured, heads of 128, bf16: 20011 tokens, 40 + 8 heads with the write into an E4M3 cache
-// 90 us, 5.9 TB/s; 32 + 8 heads into a bf16 cache 86 us; 512 tokens 4.2 us; one 2.9 us.
+// 90 us, 5.9 TB/s; 32 + 8 heads into a bf16 cache 84 us; 512 tokens 4.1 us; one 2.9 us.
 #include "rows.cuh"
 
 namespace dflash2 {
@@ -77,10 +77,15 @@ __device__ __forceinline__ int64_t cache_row(const RotaryArgs &a, int64_t token,
 
 // kLanes lanes (a power of two) hold a row of up to 16 kLanes values, a warp kRows rows at
 // once: a group.
+// Groups whose loads are in flight, and blocks per SM, which give their registers: 20011
+// tokens into an E4M3 cache 2 groups 94 us, 3: 90, 4: 108; into a bf16 cache 84, 86, 97; 8000
+// tokens in fp32 with 3 blocks 63 us, with 2 and 3 groups 58.
+template <typename T, bool kE4M3> constexpr int kInFlight = sizeof(T) == 4 || kE4M3 ? 3 : 2;
+template <typename T> constexpr int kBlocks = sizeof(T) == 4 ? 2 : 3;
+
 template <typename T, bool kE4M3, int kLanes>
-__global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const RotaryArgs a) {
-    constexpr int kRows = 32 / kLanes;
-    constexpr int kAhead = sizeof(T) == 2 ? 3 : 2;  // groups whose loads are in flight
+__global__ void __launch_bounds__(kThreads, kBlocks<T>) rotary_kernel(const RotaryArgs a) {
+    constexpr int kRows = 32 / kLanes, kAhead = kInFlight<T, kE4M3>;
     __shared__ float2 table[kWarps * kMaxPairs];
     grid_dep_wait();
     const int warp = threadIdx.x >> 5, tokens = kWarps / a.parts;
