@@ -12,13 +12,19 @@
 //
 // Every value moves once: HBM bounds it, a launch where tokens are few.  A lane holds the
 // same two steps of 8 values of every row, chosen so that both halves of its pairs are
-// its own (for halves: step u and u + rotary_dim / 16), so its sines and cosines are read
+// its own (for halves: step u and u + rotary_dim / 16; rows whose halves or addresses allow
+// no 8 go in steps of 4), so its sines and cosines are read
 // from shared memory once per token and the rows need no exchange between lanes but the
 // E4M3 maximum.  A block computes its tokens' sines and cosines once and keeps several
 // groups' loads in flight per warp (computed by every warp of a token, at 18 instructions a
 // value, 20011 tokens x 56 rows took 172 us).
 // Measured, heads of 128, bf16: 20011 tokens, 40 + 8 heads with the write into an E4M3 cache
 // 90 us, 5.9 TB/s; 32 + 8 heads into a bf16 cache 84 us; 512 tokens 4.1 us; one 2.9 us.
+// Steps of 4, 10000 tokens, 8 + 8 heads of 72 into a bf16 cache: 24 us, 2.9 TB/s (value by
+// value 108).
+#include <algorithm>
+#include <type_traits>
+
 #include "rows.cuh"
 
 namespace dflash2 {
@@ -75,17 +81,64 @@ __device__ __forceinline__ int64_t cache_row(const RotaryArgs &a, int64_t token,
     return page * a.kv_heads * a.page_size + (slot - page * a.page_size);
 }
 
-// kLanes lanes (a power of two) hold a row of up to 16 kLanes values, a warp kRows rows at
-// once: a group.
+// A step: 8 values, or 4.
+template <typename T> struct Raw4 {
+    uint2 w[sizeof(T) / 2];
+};
+template <typename T, int kStep> using Raw = std::conditional_t<kStep == 8, Raw8<T>, Raw4<T>>;
+__device__ __forceinline__ void load_step(const float *p, Raw4<float> &r) {
+    const uint4 w = *reinterpret_cast<const uint4 *>(p);
+    r.w[0] = make_uint2(w.x, w.y), r.w[1] = make_uint2(w.z, w.w);
+}
+__device__ __forceinline__ void load_step(const __nv_bfloat16 *p, Raw4<__nv_bfloat16> &r) {
+    r.w[0] = *reinterpret_cast<const uint2 *>(p);
+}
+template <typename T> __device__ __forceinline__ void load_step(const T *p, Raw8<T> &r) { r = load_raw8_written(p); }
+__device__ __forceinline__ void as_floats(const Raw4<float> &r, float (&x)[4]) {
+    x[0] = __uint_as_float(r.w[0].x), x[1] = __uint_as_float(r.w[0].y);
+    x[2] = __uint_as_float(r.w[1].x), x[3] = __uint_as_float(r.w[1].y);
+}
+__device__ __forceinline__ void as_floats(const Raw4<__nv_bfloat16> &r, float (&x)[4]) {
+    x[0] = __uint_as_float(r.w[0].x << 16), x[1] = __uint_as_float(r.w[0].x & 0xFFFF0000u);
+    x[2] = __uint_as_float(r.w[0].y << 16), x[3] = __uint_as_float(r.w[0].y & 0xFFFF0000u);
+}
+__device__ __forceinline__ void store_step(float *p, const Raw4<float> &r) {
+    *reinterpret_cast<uint4 *>(p) = make_uint4(r.w[0].x, r.w[0].y, r.w[1].x, r.w[1].y);
+}
+__device__ __forceinline__ void store_step(__nv_bfloat16 *p, const Raw4<__nv_bfloat16> &r) {
+    *reinterpret_cast<uint2 *>(p) = r.w[0];
+}
+template <typename T> __device__ __forceinline__ void store_step(T *p, const Raw8<T> &r) { store_raw8(p, r); }
+__device__ __forceinline__ void store_step(float *p, const float (&x)[4]) {
+    *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ void store_step(__nv_bfloat16 *p, const float (&x)[4]) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+    *reinterpret_cast<uint2 *>(p) =
+        make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+}
+template <typename T> __device__ __forceinline__ void store_step(T *p, const float (&x)[8]) { store8(p, x); }
+__device__ __forceinline__ void encode_step(uint8_t *c, const float (&x)[8], float s) {
+    *reinterpret_cast<uint2 *>(c) = encode8(x, s);
+}
+__device__ __forceinline__ void encode_step(uint8_t *c, const float (&x)[4], float s) {
+    *reinterpret_cast<uint32_t *>(c) = encode4(x, s);
+}
+
+// kLanes lanes (a power of two) hold a row of up to 2 kStep kLanes values, a warp kRows rows
+// at once: a group.
 // Groups whose loads are in flight, and blocks per SM, which give their registers: 20011
 // tokens into an E4M3 cache 2 groups 94 us, 3: 90, 4: 108; into a bf16 cache 84, 86, 97; 8000
-// tokens in fp32 with 3 blocks 63 us, with 2 and 3 groups 58.
-template <typename T, bool kE4M3> constexpr int kInFlight = sizeof(T) == 4 || kE4M3 ? 3 : 2;
+// tokens in fp32 with 3 blocks 63 us, with 2 and 3 groups 58.  Steps of 4, 10000 tokens of
+// 16 + 16 heads of 80: bf16 cache 2 groups 48 us, 3: 45, 4: 43, 6: 42 (500 tokens 5 % slower);
+// E4M3 55, 50, 53, 52.
+template <typename T, bool kE4M3, int kStep>
+constexpr int kInFlight = sizeof(T) == 4 || kE4M3 ? 3 : kStep == 4 ? 4 : 2;
 template <typename T> constexpr int kBlocks = sizeof(T) == 4 ? 2 : 3;
 
-template <typename T, bool kE4M3, int kLanes>
+template <typename T, bool kE4M3, int kStep, int kLanes>
 __global__ void __launch_bounds__(kThreads, kBlocks<T>) rotary_kernel(const RotaryArgs a) {
-    constexpr int kRows = 32 / kLanes, kAhead = kInFlight<T, kE4M3>;
+    constexpr int kRows = 32 / kLanes, kAhead = kInFlight<T, kE4M3, kStep>, kHalf = kStep / 2;
     __shared__ float2 table[kWarps * kMaxPairs];
     grid_dep_wait();
     const int warp = threadIdx.x >> 5, tokens = kWarps / a.parts;
@@ -95,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<T>) rotary_kernel(const Rota
     const int groups = token < a.n_tokens ? (total + kRows - 1) / kRows : 0;
 
     // this lane's two steps, and whether each is turned
-    const int steps = d / 8, turned = a.pairs / 4;
+    const int steps = d / kStep, turned = 2 * a.pairs / kStep;
     int s0, s1;
     if (a.adjacent || lane >= turned / 2) {
         s0 = 2 * lane, s1 = s0 + 1;
@@ -107,11 +160,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks<T>) rotary_kernel(const Rota
     const T *v = (const T *)a.v + token * a.v_stride;
 
     struct Pair {
-        Raw8<T> x, y;
+        Raw<T, kStep> x, y;
     } raw[kAhead];
     const auto fetch = [&](int g, Pair &p) {
         int r = g * kRows + sub;
-        p.x = p.y = Raw8<T>{};
+        p.x = p.y = Raw<T, kStep>{};
         if (g >= groups || r >= total) return;
         const T *src = q;
         if (r >= a.q_rows) {
@@ -119,8 +172,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks<T>) rotary_kernel(const Rota
             if (r >= a.k_rows) r -= a.k_rows, src = v;
         }
         src += r * d;
-        if (on0) p.x = load_raw8_written(src + s0 * 8);
-        if (on1) p.y = load_raw8_written(src + s1 * 8);
+        if (on0) load_step(src + s0 * kStep, p.x);
+        if (on1) load_step(src + s1 * kStep, p.y);
     };
     int g = warp % a.parts;
 #pragma unroll
@@ -135,31 +188,31 @@ __global__ void __launch_bounds__(kThreads, kBlocks<T>) rotary_kernel(const Rota
     __syncthreads();
     if (groups == 0) return;
     const float2 *cs = table + warp / a.parts * a.pairs;
-    float co[8], si[8];  // halves: of the 8 pairs; adjacent: of the 4 of each step
+    float co[kStep], si[kStep];  // halves: of the step's pairs; adjacent: of half as many of each step
     const bool turn0 = s0 < turned, turn1 = s1 < turned;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int j = a.adjacent ? (i < 4 ? 4 * s0 + i : 4 * s1 + i - 4) : 8 * s0 + i;
+    for (int i = 0; i < kStep; ++i) {
+        const int j = a.adjacent ? (i < kHalf ? kHalf * s0 + i : kHalf * s1 + i - kHalf) : kStep * s0 + i;
         const float2 x = j < a.pairs ? cs[j] : make_float2(1.0f, 0.0f);
         co[i] = x.x, si[i] = x.y;
     }
-    const auto turn = [&](float (&x)[8], float (&y)[8]) {
+    const auto turn = [&](float (&x)[kStep], float (&y)[kStep]) {
         if (a.adjacent) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kHalf; ++i) {
                 const float p = x[2 * i], o = x[2 * i + 1], p1 = y[2 * i], o1 = y[2 * i + 1];
                 if (turn0) {
                     x[2 * i] = p * co[i] - o * si[i];
                     x[2 * i + 1] = o * co[i] + p * si[i];
                 }
                 if (turn1) {
-                    y[2 * i] = p1 * co[4 + i] - o1 * si[4 + i];
-                    y[2 * i + 1] = o1 * co[4 + i] + p1 * si[4 + i];
+                    y[2 * i] = p1 * co[kHalf + i] - o1 * si[kHalf + i];
+                    y[2 * i + 1] = o1 * co[kHalf + i] + p1 * si[kHalf + i];
                 }
             }
         } else if (turn0) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < kStep; ++i) {
                 const float p = x[i], o = y[i];
                 x[i] = p * co[i] - o * si[i];
                 y[i] = o * co[i] + p * si[i];
@@ -170,13 +223,13 @@ __global__ void __launch_bounds__(kThreads, kBlocks<T>) rotary_kernel(const Rota
 
     const auto finish = [&](int g, const Pair &p) {
         const int r = g * kRows + sub;
-        float x[8], y[8];
+        float x[kStep], y[kStep];
         as_floats(p.x, x);
         as_floats(p.y, y);
         if ((g + 1) * kRows <= a.q_rows) {  // queries alone, the most
             turn(x, y);
-            if (on0) store8(q_out + r * d + s0 * 8, x);
-            if (on1) store8(q_out + r * d + s1 * 8, y);
+            if (on0) store_step(q_out + r * d + s0 * kStep, x);
+            if (on1) store_step(q_out + r * d + s1 * kStep, y);
             return;
         }
         const bool live = r < total, values = r >= a.q_rows + a.k_rows, key = !values && r >= a.q_rows;
@@ -184,31 +237,31 @@ __global__ void __launch_bounds__(kThreads, kBlocks<T>) rotary_kernel(const Rota
         const int head = values ? r - a.q_rows - a.k_rows : key ? r - a.q_rows : r;
         if (live && !values && (!key || a.ko)) {
             T *dst = (key ? k_out : q_out) + head * d;
-            if (on0) store8(dst + s0 * 8, x);
-            if (on1) store8(dst + s1 * 8, y);
+            if (on0) store_step(dst + s0 * kStep, x);
+            if (on1) store_step(dst + s1 * kStep, y);
         }
         const bool held = live && (key || values) && at >= 0;
         const int64_t row = at + (int64_t)head * a.page_size;
         if constexpr (kE4M3) {
             float amax = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(x[i]), fabsf(y[i])));
+            for (int i = 0; i < kStep; ++i) amax = fmaxf(amax, fmaxf(fabsf(x[i]), fabsf(y[i])));
 #pragma unroll
             for (int o = kLanes / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
             if (!held) return;
             const int e = row_exponent(amax);
             uint8_t *c = (uint8_t *)(values ? a.vc : a.kc) + row * d;
-            if (on0) *reinterpret_cast<uint2 *>(c + s0 * 8) = encode8(x, pow2i(-e));
-            if (on1) *reinterpret_cast<uint2 *>(c + s1 * 8) = encode8(y, pow2i(-e));
+            if (on0) encode_step(c + s0 * kStep, x, pow2i(-e));
+            if (on1) encode_step(c + s1 * kStep, y, pow2i(-e));
             if (lane == 0) (values ? a.ve : a.ke)[row] = (uint8_t)(e + 127);
         } else if (held) {
             T *c = (T *)(values ? a.vc : a.kc) + row * d;
             if (values) {  // a value row keeps its bits
-                if (on0) store_raw8(c + s0 * 8, p.x);
-                if (on1) store_raw8(c + s1 * 8, p.y);
+                if (on0) store_step(c + s0 * kStep, p.x);
+                if (on1) store_step(c + s1 * kStep, p.y);
             } else {
-                if (on0) store8(c + s0 * 8, x);
-                if (on1) store8(c + s1 * 8, y);
+                if (on0) store_step(c + s0 * kStep, x);
+                if (on1) store_step(c + s1 * kStep, y);
             }
         }
     };
@@ -223,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<T>) rotary_kernel(const Rota
     }
 }
 
-// Any head_dim up to 256, rotary_dim and alignment: a warp per kScalarRows rows of a token,
+// What no step of 4 fits, up to head_dim 256: a warp per kScalarRows rows of a token,
 // a value per lane and step.  All of a row is read before any of it is written, so calls
 // in place are safe here too.
 constexpr int kScalarRows = 4;
@@ -289,7 +342,7 @@ __global__ void __launch_bounds__(kThreads) rotary_scalar(const RotaryArgs a) {
     }
 }
 
-template <typename T, bool kE4M3, int kLanes>
+template <typename T, bool kE4M3, int kStep, int kLanes>
 void launch_lanes(RotaryArgs a, int sms, cudaStream_t st) {
     constexpr int rows = 32 / kLanes;
     // As few warps per token as leave a block per SM (512 tokens x 48 rows: 4.2 us, with
@@ -301,21 +354,30 @@ void launch_lanes(RotaryArgs a, int sms, cudaStream_t st) {
            (a.parts > groups || a.n_tokens * a.parts / 2 >= (a.parts > 2 ? 1ll : 3ll) * kWarps * sms))
         a.parts /= 2;
     const int64_t grid = (a.n_tokens * a.parts + kWarps - 1) / kWarps;
-    launch_k(rotary_kernel<T, kE4M3, kLanes>, dim3((unsigned)grid), dim3(kThreads), 0, st, a);
+    launch_k(rotary_kernel<T, kE4M3, kStep, kLanes>, dim3((unsigned)grid), dim3(kThreads), 0, st, a);
+}
+
+template <typename T, bool kE4M3, int kStep>
+void launch_steps(const RotaryArgs &a, int sms, cudaStream_t st) {
+    constexpr int kMost = 128 / kStep;  // lanes of a row of 256 values
+    if (a.head_dim <= 64)
+        launch_lanes<T, kE4M3, kStep, kMost / 4>(a, sms, st);
+    else if (a.head_dim <= 128)
+        launch_lanes<T, kE4M3, kStep, kMost / 2>(a, sms, st);
+    else
+        launch_lanes<T, kE4M3, kStep, kMost>(a, sms, st);
 }
 
 template <typename T, bool kE4M3>
-dflash2_status launch_rotary(RotaryArgs a, bool vec, int sms, cudaStream_t st) {
-    if (!vec) {
+dflash2_status launch_rotary(RotaryArgs a, int step, int sms, cudaStream_t st) {
+    if (step == 8) {
+        launch_steps<T, kE4M3, 8>(a, sms, st);
+    } else if (step == 4) {
+        launch_steps<T, kE4M3, 4>(a, sms, st);
+    } else {
         a.parts = (a.q_rows + a.k_rows + a.v_rows + kScalarRows - 1) / kScalarRows;
         const int64_t warps = a.n_tokens * a.parts;
         launch_k(rotary_scalar<T, kE4M3>, dim3((unsigned)((warps + kWarps - 1) / kWarps)), dim3(kThreads), 0, st, a);
-    } else if (a.head_dim <= 64) {
-        launch_lanes<T, kE4M3, 4>(a, sms, st);
-    } else if (a.head_dim <= 128) {
-        launch_lanes<T, kE4M3, 8>(a, sms, st);
-    } else {
-        launch_lanes<T, kE4M3, 16>(a, sms, st);
     }
     return launch_status();
 }
@@ -353,18 +415,24 @@ dflash2_status run_rotary(RotaryArgs a, int32_t dtype, int32_t kv_format, int32_
     const dflash2_status st = current_device(&di);
     if (st != DFLASH2_OK) return st;
     a.n_slots = cached ? num_pages * a.page_size : 0;
-    // steps of 8 values: aligned rows, and pairs whose halves both begin at a step
-    const auto rows_vec = [&](const void *p, int64_t stride) { return aligned_to(p, 16) && stride * (int64_t)el % 16 == 0; };
-    const uintptr_t kept = q8 ? 8 : 16;
-    bool vec = a.head_dim % 8 == 0 && rotary_dim % (a.adjacent ? 8 : 16) == 0;
-    if (a.q_rows) vec = vec && rows_vec(a.q, a.q_stride) && rows_vec(a.qo, a.qo_stride);
-    if (a.k_rows) vec = vec && rows_vec(a.k, a.k_stride) && (!a.ko || rows_vec(a.ko, a.ko_stride));
-    if (cached) vec = vec && rows_vec(a.v, a.v_stride) && aligned_to(a.kc, kept) && aligned_to(a.vc, kept);
+    // the widest step with aligned rows and pairs whose halves both begin at a step
+    const auto steps_of = [&](int step) {
+        const int64_t bytes = std::min<int64_t>(16, step * (int64_t)el);
+        const auto rows = [&](const void *p, int64_t stride) {
+            return aligned_to(p, (uintptr_t)bytes) && stride * (int64_t)el % bytes == 0;
+        };
+        const uintptr_t kept = q8 ? (uintptr_t)step : (uintptr_t)bytes;
+        return a.head_dim % step == 0 && rotary_dim % (a.adjacent ? step : 2 * step) == 0 &&
+               (!a.q_rows || (rows(a.q, a.q_stride) && rows(a.qo, a.qo_stride))) &&
+               (!a.k_rows || (rows(a.k, a.k_stride) && (!a.ko || rows(a.ko, a.ko_stride)))) &&
+               (!cached || (rows(a.v, a.v_stride) && aligned_to(a.kc, kept) && aligned_to(a.vc, kept)));
+    };
+    const int step = steps_of(8) ? 8 : steps_of(4) ? 4 : 1;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     using B = __nv_bfloat16;
     if (cached && q8)
-        return dtype == DFLASH2_F32 ? launch_rotary<float, true>(a, vec, di.sm_count, s) : launch_rotary<B, true>(a, vec, di.sm_count, s);
-    return dtype == DFLASH2_F32 ? launch_rotary<float, false>(a, vec, di.sm_count, s) : launch_rotary<B, false>(a, vec, di.sm_count, s);
+        return dtype == DFLASH2_F32 ? launch_rotary<float, true>(a, step, di.sm_count, s) : launch_rotary<B, true>(a, step, di.sm_count, s);
+    return dtype == DFLASH2_F32 ? launch_rotary<float, false>(a, step, di.sm_count, s) : launch_rotary<B, false>(a, step, di.sm_count, s);
 }
 
 }  // namespace

@@ -81,16 +81,13 @@ __device__ __forceinline__ float decode1(uint8_t c) {
     return __half2float(__half(h));
 }
 // The codes of x * s, nearest even, saturating at 448, NaN as NaN.
+__device__ __forceinline__ uint32_t encode4(const float *x, float s) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[0] * s, x[1] * s), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[2] * s, x[3] * s), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+}
 __device__ __forceinline__ uint2 encode8(const float (&x)[8], float s) {
-    uint32_t c[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float *y = x + 4 * i;
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0] * s, y[1] * s), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2] * s, y[3] * s), __NV_SATFINITE, __NV_E4M3);
-        c[i] = lo | (hi << 16);
-    }
-    return make_uint2(c[0], c[1]);
+    return make_uint2(encode4(x, s), encode4(x + 4, s));
 }
 
 // ---- E4M3 blocks: one fp32 scale per 128 values of a row ---------------------

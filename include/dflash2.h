@@ -881,8 +881,9 @@ dflash2_status dflash2_sublayer_join(const void *residual, int64_t residual_row_
  * Device:    an axis[j] >= axes sets DFLASH2_DEVERR_ID_RANGE, and its pairs take
  *            angle 0; slots as for dflash2_kv_cache_write.
  * The fast path wants head_dim % 8 == 0, rotary_dim % 16 == 0 (adjacent pairs: % 8)
- * and every row 16-byte aligned (8-byte for E4M3 codes); other layouts take a
- * scalar path.
+ * and every row 16-byte aligned (8-byte for E4M3 codes); with half of these numbers
+ * (fp32 rows 16-byte aligned all the same) rows go in narrower steps, and other
+ * layouts take a scalar path.
  */
 dflash2_status dflash2_rotary(const void *q, int64_t q_row_stride, const void *k,
                               int64_t k_row_stride, const int64_t *positions, int32_t axes,

@@ -39,7 +39,11 @@ SHAPES = [  # n, q heads, kv heads, head_dim, rotary_dim, axes, adjacent
     (3, 8, 8, 256, 256, 1, True), (7, 3, 1, 80, 40, 2, True), (7, 3, 1, 80, 80, 2, False),
     (4, 5, 5, 96, 96, 3, False), (6, 2, 1, 72, 24, 1, True), (2, 1, 1, 2, 2, 1, False),
     (9, 3, 3, 33, 10, 2, False), (9, 3, 3, 33, 10, 2, True), (2, 70, 1, 128, 128, 1, False),
-    (300, 4, 2, 16, 16, 1, False)]
+    (300, 4, 2, 16, 16, 1, False),
+    # halves that begin at a step of 4, not of 8, and rows of such steps
+    (19, 10, 2, 80, 40, 2, False), (7, 3, 1, 72, 72, 3, False), (33, 5, 1, 36, 24, 1, False),
+    (3, 4, 4, 252, 248, 1, False), (5, 2, 1, 20, 12, 1, True), (300, 2, 2, 256, 120, 3, False),
+    (1, 1, 1, 4, 4, 1, True), (65, 3, 3, 132, 8, 1, False), (2, 70, 1, 100, 72, 1, False)]
 
 
 @pytest.mark.parametrize("shape", SHAPES)
@@ -142,10 +146,11 @@ def test_into_the_cache(cuda, shape, dtype, e4m3):
     assert none is None and none2 is None and torch.equal(again.k, cache.k) and torch.equal(again.v, cache.v)
 
 
-def test_misaligned_rows_and_one_axis(cuda):
+@pytest.mark.parametrize("skip", [1, 2, 4, 8])
+def test_misaligned_rows_and_one_axis(cuda, skip):
     c = Case(11, 4, 2, 128, 128, dtype=BF)
-    flat = torch.zeros(1 + c.q.numel(), dtype=BF, device=cuda)
-    odd = flat[1:].view(11, 4, 128)
+    flat = torch.zeros(skip + c.q.numel(), dtype=BF, device=cuda)
+    odd = flat[skip:].view(11, 4, 128)
     odd.copy_(c.q)
     got, _, _ = dflash2.rotary(odd, None, c.positions[0].contiguous().cuda(), c.table)
     c.check("q", got, c.q)
