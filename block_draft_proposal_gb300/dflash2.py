@@ -1136,7 +1136,7 @@ def sublayer_join(residual, y, post_weight=None, gate=None, gate_act: str = "non
         if gate.dim() == 1:
             _need(gate, "gate", dt, (hidden,))
             kind = GATE_CHANNEL
-        elif gate.shape[-1] == 1 and hidden > 1:
+        elif gate.dim() == 2 and gate.shape[1] == 1 and hidden > 1:
             gs = _need_matrix(gate, "gate", dt, (rows, 1))
             kind = GATE_TOKEN
         else:
@@ -1273,7 +1273,7 @@ def rotary_kv_write(cache: KVCache, q, k, v, positions, table: RotaryTable, slot
     if with_k or k_out is not None:
         ks, k_out, kos = _rotated(k, "k", k_out, stream)
     err = _need_error_word(err, k.device, stream)
-    _need_one_device(k, v, q, positions, table.freq, table.axis, slots, q_out, k_out, cache.k, err)
+    _need_one_device(k, v, q, positions, table.freq, table.axis, slots, q_out, k_out, *cache, err)
     _check("dflash2_rotary_kv_write", library().dflash2_rotary_kv_write(
         _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, *place, _ptr(slots), n, heads, kv_heads, d, ps,
         pages, _dtype_code(k), fmt, _ptr(q_out), qos, _ptr(k_out), kos, _ptr(cache.k),

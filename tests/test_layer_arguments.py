@@ -136,7 +136,7 @@ def test_outputs_and_their_types():
     lambda: _norm(_t(1, 256).expand(3, 256)), lambda: _norm(w=_t(255)), lambda: _norm(out=_t(3, 255)),
     lambda: _norm(scale=_t(3, 2, dtype=F32)), lambda: _norm(e4m3=True, scale=_t(3, 3, dtype=F32)),
     lambda: _join(y=_t(3, 255)), lambda: _join(gate=_t(255)), lambda: _join(gate=_t(2, 256)),
-    lambda: _join(gate=_t(3, 2)), lambda: _join(gate_act="relu"), lambda: _join(post_weight=_t(128)),
+    lambda: _join(gate=_t(3, 2)), lambda: _join(gate=_t()), lambda: _join(gate_act="relu"), lambda: _join(post_weight=_t(128)),
     lambda: _join(next_weight=None, e4m3=True), lambda: _join(next_weight=None, out=_t(3, 256)),
     lambda: _join(residual_out=_t(2, 256)), lambda: _join(residual_out=_t(1, 256).expand(3, 256)),
     lambda: _linear(_t(3, 255)), lambda: _linear(s=_t(2, 3, dtype=F32)), lambda: _linear(_i(3, 256, dtype=U8)),
@@ -195,3 +195,14 @@ def test_tensors_of_two_devices():
                  lambda: _rotary(table=dflash2.RotaryTable(_i(32, device=there), _i(32, dtype=U8, device=there)))):
         with pytest.raises(ValueError, match="current device"):
             call()
+
+
+def test_a_cache_of_two_devices():
+    there = "cuda:1"
+    n, heads, d = 3, 2, 64
+    kv, exps = (4, heads, 16, d), (4, heads, 16)
+    for cache in (dflash2.KVCache(_t(*kv), _t(*kv, device=there)),
+                  dflash2.KVCache(_i(*kv, dtype=U8), _i(*kv, dtype=U8), _i(*exps, dtype=U8, device=there), _i(*exps, dtype=U8)),
+                  dflash2.KVCache(_i(*kv, dtype=U8), _i(*kv, dtype=U8), _i(*exps, dtype=U8), _i(*exps, dtype=U8, device=there))):
+        with pytest.raises(ValueError, match="current device"):
+            dflash2.rotary_kv_write(cache, None, _t(n, heads, d), _t(n, heads, d), _i(n), _table(), _i(n))
