@@ -11,15 +11,18 @@
 // pass, but the next norm would lose what cancels in r + h).  r' goes into the next norm
 // as computed in fp32, not as rounded for storage.
 //
-// HBM bounds them once the rows fill the GPU, a launch below that.  A thread holds 4 x 8 values; a row takes as many
-// threads as it needs (a warp up to 1024 values), and the loads of y, r and the gate are
+// HBM bounds them once the rows fill the GPU, a launch below that.  A thread holds 4 x 8 values
+// (2 x 8 of rows that go value by value); a row takes as many threads as it needs (a warp
+// up to 1024 values, 512 value by value), and the loads of y, r and the gate are
 // all in flight at once.  The choice goes by the row's length alone, so a row's result does
 // not depend on how many there are.
-// Measured (graph replays, rotating inputs): norm of 20011 x 7168 bf16 86 us, 6.7 TB/s; join
+// Measured (graph replays, rotating inputs): norm of 20011 x 7168 bf16 84 us, 6.9 TB/s; join
 // with an fp32 stream, a full sigmoid gate and both norms 284 us, 7.1 TB/s; bf16 join without
-// a gate 165 us, 6.9 TB/s, to E4M3 blocks 167; norm of 20011 x 5120 to E4M3 blocks 61 us, 5.1
-// TB/s; quantisation of 8192 x 7168 bf16 30 us, 6.0 TB/s; one row of 4096: norm 2.3 us, join
-// 3.2 us.
+// a gate 165 us, 6.9 TB/s, to E4M3 blocks 166; norm of 20011 x 5120 to E4M3 blocks 58 us, 5.3
+// TB/s; quantisation of 8192 x 7168 bf16 30 us, 6.0 TB/s; one row of 4096: norm 2.1 us, join
+// 3.1 us.
+#include <type_traits>
+
 #include "rows.cuh"
 #include "tcgen05.cuh"
 
@@ -52,21 +55,23 @@ template <typename T, bool kVec> struct Held {
     }
     __device__ __forceinline__ void get(float (&x)[8]) const { as_floats(raw, x); }
 };
+// (bits: a conversion beside its load waits for it, and the row's loads for one another)
 template <typename T> struct Held<T, false> {
-    float v[8];
+    using Bits = std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t>;
+    uint32_t v[8];
     __device__ __forceinline__ void load(const T *row, int first, int step, int n) {
-        const T *p = row + first;
+        const Bits *p = reinterpret_cast<const Bits *>(row) + first;
         if (first + 7 * step < n) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = to_f32(p[i * step]);
+            for (int i = 0; i < 8; ++i) v[i] = p[i * step];
             return;
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = first + i * step < n ? to_f32(p[i * step]) : 0.0f;
+        for (int i = 0; i < 8; ++i) v[i] = first + i * step < n ? p[i * step] : 0u;
     }
     __device__ __forceinline__ void get(float (&x)[8]) const {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = v[i];
+        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(sizeof(T) == 4 ? v[i] : v[i] << 16);
     }
 };
 template <typename T, bool kVec>
@@ -127,22 +132,27 @@ template <bool kWarpRow> __device__ __forceinline__ float row_sum(float v, float
 // Blocks of 256 threads per SM that the registers leave room for, by the bytes a value takes:
 // rows in flight against what a thread holds of each.  20011 x 7168: join with an fp32 stream
 // and a full gate 2: 315 us, 3: 284, 4: 309; bf16 join 2: 176, 4: 165; fp32 join of 20011 x
-// 4096 2: 189, 3: 242; bf16 norm 4: 90, 5: 86.  (Value by value, a thread holds them in
-// fp32: one block fewer in bf16.)
-template <typename TX, typename T, bool kVec, bool kJoin>
-constexpr int kBlocks256 = kJoin ? (sizeof(TX) + sizeof(T) == 4   ? (kVec ? 4 : 3)
-                                    : sizeof(TX) + sizeof(T) == 6 ? 3 : 2)
+// 4096 2: 189, 3: 242; bf16 norm 4: 90, 5: 84.
+// Value by value a thread holds 32 bits of each, so it takes two pieces in place of four, four
+// blocks: bf16 join of 10000 x 5001 127 us (four pieces 181, one 240), with an fp32 stream and
+// a full gate 165 (230), of 30000 x 1001 73 (71) and 91 (93).
+template <typename TX, typename T, bool kVec, bool kJoin, int kChunks>
+constexpr int kBlocks256 = kJoin ? (kChunks == 2                    ? 4
+                                    : sizeof(TX) + sizeof(T) == 4   ? (kVec ? 4 : 3)
+                                    : sizeof(TX) + sizeof(T) == 6 && kVec ? 3 : 2)
                            : kVec && sizeof(TX) + sizeof(T) == 4 ? 5 : 4;
-template <typename TX, typename T, bool kVec, bool kJoin, int kThreads>
-constexpr int kRowBlocks = kThreads <= 256 ? kBlocks256<TX, T, kVec, kJoin>
-                           : kThreads == 512 && kBlocks256<TX, T, kVec, kJoin> > 3 ? 2 : 1;
+template <typename TX, typename T, bool kVec, bool kJoin, int kChunks, int kThreads>
+constexpr int kRowBlocks = kThreads <= 256 ? kBlocks256<TX, T, kVec, kJoin, kChunks>
+                           : kThreads == 512 && kBlocks256<TX, T, kVec, kJoin, kChunks> > 3 ? 2 : 1;
 
-// kThreads: a row's threads at most; 32 stands for a warp per row, 8 rows a block.
-template <typename TX, typename T, bool kVec, bool kJoin, int kThreads>
-__global__ void __launch_bounds__(kThreads == 32 ? 256 : kThreads, kRowBlocks<TX, T, kVec, kJoin, kThreads>)
+// kThreads: a row's threads at most; 32 stands for a warp per row, 8 rows a block.  kChunks:
+// a thread's pieces of 8 values.
+// (kE4M3 in the type, not from a.scale: norms to E4M3 blocks 60 -> 58 us at 20011 x 5120.)
+template <typename TX, typename T, bool kVec, bool kJoin, bool kE4M3, int kChunks, int kThreads>
+__global__ void __launch_bounds__(kThreads == 32 ? 256 : kThreads, kRowBlocks<TX, T, kVec, kJoin, kChunks, kThreads>)
     sublayer_kernel(const NormArgs a) {
+    static_assert(!kE4M3 || kChunks == kQuantUnroll, "blocks are quantised four at a time");
     constexpr bool kWarpRow = kThreads == 32;
-    constexpr int kChunks = kQuantUnroll;
     __shared__ float red[2][32];
     grid_dep_wait();
     const int t = kWarpRow ? threadIdx.x & 31 : threadIdx.x;
@@ -151,10 +161,10 @@ __global__ void __launch_bounds__(kThreads == 32 ? 256 : kThreads, kRowBlocks<TX
     if (row >= a.rows) return;  // a whole warp or block
     const int hidden = a.hidden;
     const float inv_n = 1.0f / (float)hidden;
-    // Eight neighbouring values of each of four pieces of the row; rows that are not whole
+    // Eight neighbouring values of each of a thread's pieces of the row; rows that are not whole
     // 16-byte pieces go value by value, neighbours in neighbouring threads, unless E4M3
     // blocks want them as above.
-    const bool apart = !kVec && !a.scale;
+    constexpr bool apart = !kVec && !kE4M3;
     const int step = apart ? per : 1, origin = apart ? t : t * 8;
     const auto first = [&](int c) { return c * 8 * per + origin; };
 
@@ -227,46 +237,58 @@ __global__ void __launch_bounds__(kThreads == 32 ? 256 : kThreads, kRowBlocks<TX
         w.get(v);
         scale8(r[c], rms);
         weigh8(r[c], v, a.w_off);
-        if (!a.scale) put8<T, kVec>((T *)a.out + row * hidden, first(c), step, hidden, r[c]);
+        if constexpr (!kE4M3) put8<T, kVec>((T *)a.out + row * hidden, first(c), step, hidden, r[c]);
     }
-    if (!a.scale) return;
-    if (!kVec)
+    if constexpr (kE4M3) {
+        if (!kVec)
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (first(c) + i >= hidden) r[c][i] = 0.0f;
+        uint2 codes[kChunks];
+        float scale;
+        quantise_blocks(r, &scale, codes);
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (first(c) + i >= hidden) r[c][i] = 0.0f;
-    uint2 codes[kChunks];
-    float scale;
-    quantise_blocks(r, &scale, codes);
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c)
-        if (first(c) < hidden)
-            store_codes((uint8_t *)a.out + row * hidden + first(c), hidden - first(c), a.code_vec, codes[c]);
-    const int block = (quant_lane() * per + t) / kQuantLanes;
-    if ((t & 3) == 0 && block * kQuantBlock < hidden)
-        a.scale[row * ((hidden + kQuantBlock - 1) / kQuantBlock) + block] = scale;
+            if (first(c) < hidden)
+                store_codes((uint8_t *)a.out + row * hidden + first(c), hidden - first(c), a.code_vec, codes[c]);
+        const int block = (quant_lane() * per + t) / kQuantLanes;
+        if ((t & 3) == 0 && block * kQuantBlock < hidden)
+            a.scale[row * ((hidden + kQuantBlock - 1) / kQuantBlock) + block] = scale;
+    }
 }
 
-template <typename TX, typename T, bool kVec, bool kJoin>
-dflash2_status launch_vec(const NormArgs &a, cudaStream_t st) {
-    constexpr int kChunks = kQuantUnroll;
+template <typename TX, typename T, bool kVec, bool kJoin, bool kE4M3, int kChunks>
+void launch_chunks(const NormArgs &a, cudaStream_t st) {
     const int threads = ((a.hidden + 8 * kChunks - 1) / (8 * kChunks) + 31) / 32 * 32;
+    const dim3 grid((unsigned)a.rows);
     if (threads == 32)
-        launch_k(sublayer_kernel<TX, T, kVec, kJoin, 32>, dim3((unsigned)((a.rows + 7) / 8)), dim3(256), 0,
-                 st, a);
+        launch_k(sublayer_kernel<TX, T, kVec, kJoin, kE4M3, kChunks, 32>, dim3((unsigned)((a.rows + 7) / 8)), dim3(256),
+                 0, st, a);
     else if (threads <= 256)
-        launch_k(sublayer_kernel<TX, T, kVec, kJoin, 256>, dim3((unsigned)a.rows), dim3(threads), 0, st, a);
+        launch_k(sublayer_kernel<TX, T, kVec, kJoin, kE4M3, kChunks, 256>, grid, dim3(threads), 0, st, a);
     else if (threads <= 512)
-        launch_k(sublayer_kernel<TX, T, kVec, kJoin, 512>, dim3((unsigned)a.rows), dim3(threads), 0, st, a);
+        launch_k(sublayer_kernel<TX, T, kVec, kJoin, kE4M3, kChunks, 512>, grid, dim3(threads), 0, st, a);
     else
-        launch_k(sublayer_kernel<TX, T, kVec, kJoin, 1024>, dim3((unsigned)a.rows), dim3(threads), 0, st, a);
+        launch_k(sublayer_kernel<TX, T, kVec, kJoin, kE4M3, kChunks, 1024>, grid, dim3(threads), 0, st, a);
+}
+
+template <typename TX, typename T, bool kVec, bool kJoin, bool kE4M3>
+dflash2_status launch_vec(const NormArgs &a, cudaStream_t st) {
+    if constexpr (kVec || kE4M3)
+        launch_chunks<TX, T, kVec, kJoin, kE4M3, kQuantUnroll>(a, st);
+    else if (a.hidden <= 1024 * 16)  // what 1024 threads hold in two pieces
+        launch_chunks<TX, T, false, kJoin, false, 2>(a, st);
+    else
+        launch_k(sublayer_kernel<TX, T, false, kJoin, false, 4, 1024>, dim3((unsigned)a.rows), dim3(1024), 0, st, a);
     return launch_status();
 }
 
 template <typename TX, typename T, bool kJoin>
 dflash2_status launch_norm(const NormArgs &a, bool vec, cudaStream_t st) {
-    return vec ? launch_vec<TX, T, true, kJoin>(a, st) : launch_vec<TX, T, false, kJoin>(a, st);
+    if (a.scale) return vec ? launch_vec<TX, T, true, kJoin, true>(a, st) : launch_vec<TX, T, false, kJoin, true>(a, st);
+    return vec ? launch_vec<TX, T, true, kJoin, false>(a, st) : launch_vec<TX, T, false, kJoin, false>(a, st);
 }
 
 template <bool kJoin>

@@ -34,7 +34,8 @@ def test_norm(cuda, n, hidden, xt, wt, e4m3):
             check(f"norm {n}x{hidden}", out, want, bound + ref.HALF_STEP[wt] * want.abs())
 
 
-@pytest.mark.parametrize("n,hidden", [(1, 5), (4, 256), (7, 1000), (3, 4096), (2, 8200), (2, 16392)])
+@pytest.mark.parametrize("n,hidden", [(1, 5), (4, 256), (7, 1000), (3, 4096), (2, 8200), (2, 16392),
+                                      (19, 511), (9, 513), (3, 4097), (5, 5001), (2, 16383), (2, 16385)])
 @pytest.mark.parametrize("rt,dt", [(BF, BF), (F32, BF), (F32, F32), (BF, F32)])
 @pytest.mark.parametrize("gate,act", [("none", "none"), ("channel", "tanh"), ("token", "sigmoid"),
                                       ("full", "sigmoid"), ("full", "none")])
