@@ -43,7 +43,7 @@ def test_product(cuda, rows, n_in, n_out, dtype):
 
 
 @pytest.mark.parametrize("rows,n_out", [(1, 400), (5, 400), (40, 400), (130, 400), (700, 400), (90, 6008),
-                                        (2600, 2500)])
+                                        (2600, 2500), (130, 399), (700, 401), (90, 6007), (2601, 2501)])
 def test_whole_numbers_are_exact(cuda, rows, n_out):
     g = torch.Generator().manual_seed(rows)
     n_in = 656
