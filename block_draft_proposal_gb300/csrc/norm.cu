@@ -155,6 +155,8 @@ __global__ void __launch_bounds__(kThreads == 32 ? 256 : kThreads, kRowBlocks<TX
     constexpr bool kWarpRow = kThreads == 32;
     __shared__ float red[2][32];
     grid_dep_wait();
+    grid_dep_launch();  // a product that follows sets itself up meanwhile (1 x 4096 x 6144 after a
+                        // norm 8.3 us in place of 9.6, 512 rows 20.5 for 21.4)
     const int t = kWarpRow ? threadIdx.x & 31 : threadIdx.x;
     const int per = kWarpRow ? 32 : blockDim.x;
     const int64_t row = kWarpRow ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
