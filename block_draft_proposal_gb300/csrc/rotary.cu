@@ -7,8 +7,7 @@
 //
 // Frequencies are 64-bit fractions of a turn, so position * frequency modulo 2^64 is the
 // angle modulo a turn: exact for every 64-bit position, where an fp32 product has lost
-// 0.06 rad at position 10^6, and one integer multiplication.  The signed fraction goes to
-// sincospi in fp32.
+// 0.06 rad at position 10^6, and one integer multiplication.
 //
 // Every value moves once: HBM bounds it, a launch where tokens are few.  A lane holds the
 // same two steps of 8 values of every row, chosen so that both halves of its pairs are
@@ -55,7 +54,34 @@ struct RotaryArgs {
     int32_t *err;
 };
 
-// Sine and cosine (times the magnitude) of a token's pair.
+// Cosine and sine of phase / 2^64 turns, within 0.8 of a last place (0.5 of it the final
+// rounding).
+// The nearest quarter turn leaves exactly; the rest x, at most pi / 4, is held in two
+// floats (the fraction of a turn in one costs pi 2^-25 of angle, more than all other
+// roundings), and the Taylor series' small terms are added to x and to 1 last.
+__device__ __forceinline__ float2 turn_by(uint64_t phase) {
+    const int64_t quarter = (((int64_t)phase >> 61) + 1) >> 1;
+    const int64_t rest = (int64_t)(phase - ((uint64_t)quarter << 62));  // |rest| <= 2^61
+    const float hi = __ll2float_rn(rest), lo = __ll2float_rn(rest - __float2ll_rn(hi));
+    constexpr float kPi = 0x1.921fb6p-62f, kPiLow = -0x1.777a5cp-87f;  // pi / 2^63
+    const float x = __fmul_rn(hi, kPi);
+    const float x_low = __fmaf_rn(lo, kPi, __fmaf_rn(hi, kPiLow, __fmaf_rn(hi, kPi, -x)));
+    const float xx = __fmul_rn(x, x), xx_half = 0.5f * xx;
+    const float xx_low = __fmaf_rn(x + x, x_low, __fmaf_rn(x, x, -xx));
+    float s = __fmaf_rn(xx, 1.0f / 362880, -1.0f / 5040);
+    s = __fmaf_rn(xx, __fmaf_rn(xx, s, 1.0f / 120), -1.0f / 6);
+    s = __fadd_rn(x, __fmaf_rn(x, __fmul_rn(xx, s), __fmaf_rn(-xx_half, x_low, x_low)));
+    float c = __fmaf_rn(xx, -1.0f / 3628800, 1.0f / 40320);
+    c = __fmaf_rn(xx, __fmaf_rn(xx, c, -1.0f / 720), 1.0f / 24);
+    c = __fmaf_rn(__fmul_rn(xx, xx), c, -0.5f * xx_low);
+    const float one = __fsub_rn(1.0f, xx_half);  // and what its rounding lost
+    c = __fadd_rn(one, __fadd_rn(__fsub_rn(__fsub_rn(1.0f, one), xx_half), c));
+    const bool swap = quarter & 1;
+    const float cosine = swap ? s : c, sine = swap ? c : s;
+    return make_float2((quarter + 1) & 2 ? -cosine : cosine, quarter & 2 ? -sine : sine);
+}
+
+// Cosine and sine (times the magnitude) of a token's pair.
 __device__ __forceinline__ float2 turn_of(const RotaryArgs &a, int64_t token, int pair) {
     const int axis = __ldg(a.axis + pair);
     uint64_t phase = 0;
@@ -63,9 +89,8 @@ __device__ __forceinline__ float2 turn_of(const RotaryArgs &a, int64_t token, in
         phase = (uint64_t)__ldg(a.positions + axis * a.n_tokens + token) * __ldg(a.freq + pair);
     else if (a.err)
         atomicOr(a.err, DFLASH2_DEVERR_ID_RANGE);
-    float s, c;
-    sincospif(__ll2float_rn((int64_t)phase) * 0x1p-63f, &s, &c);
-    return make_float2(c * a.magnitude, s * a.magnitude);
+    const float2 x = turn_by(phase);
+    return make_float2(x.x * a.magnitude, x.y * a.magnitude);
 }
 
 // Head 0's row of a token in the cache arrays, or -1.

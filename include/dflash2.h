@@ -865,8 +865,8 @@ dflash2_status dflash2_sublayer_join(const void *residual, int64_t residual_row_
  *            uint8 [rotary_dim / 2].
  * q_out, k_out  device, rows like q and k at their own strides; may be q and k
  *            themselves (same stride), and must not overlap them otherwise.
- * Arithmetic: fp32 (sines and cosines by CUDA's sincospif of the exact fraction of
- *            a turn); one rounding per value.
+ * Arithmetic: fp32 (sines and cosines within 0.8 of a last place of those of the
+ *            exact angle); one rounding per value.
  * dflash2_rotary_kv_write also writes the rotated keys and the values (rows v, as
  * k) into the cache as dflash2_kv_cache_write does (its slots, formats and device
  * errors); an E4M3 row is quantised from the fp32 values.  k_out may be NULL.

@@ -74,6 +74,24 @@ def test_turned_back(cuda):
     check("back", back, x, 2 * math.sqrt(2) * ref.TURN * 1.01 * size + 2 * ref.U_F32 * size)
 
 
+@pytest.mark.parametrize("eighths", [False, True])
+def test_sines_and_cosines(cuda, eighths):
+    """Pairs (1, 0) become (cos, sin): the last rounding's half place, and 0.3 of one for the terms that
+    are added to the angle (a ninth of the sine, three roundings in it) and the series' end."""
+    c = Case(1000, 1, 1, 256, 256, dtype=F32, far=2 ** 62)
+    if eighths:                                                # of a turn, and steps of 2^-8 from there
+        c.table = c.table._replace(freq=torch.arange(128, device=cuda) << 56)
+        c.positions = torch.arange(-500, 500)[None]
+    x = torch.zeros((1000, 1, 256), device=cuda)
+    x[..., :128] = 1
+    q, _, _ = dflash2.rotary(x, None, c.positions.cuda(), c.table)
+    angle = ref.angles(c.positions, c.table.freq.cpu(), c.table.axis.cpu())
+    for got, want in ((q[:, 0, :128], torch.cos(angle)), (q[:, 0, 128:], torch.sin(angle))):
+        place = torch.ldexp(torch.ones_like(want), torch.frexp(want)[1] - 24)
+        # the reference's own angle is rounded: up to pi, to 2^-52
+        assert bool(((got.cpu().double() - want).abs() <= 0.8 * place + 2.0 ** -51).all())
+
+
 def test_far_positions(cuda):
     c = Case(8, 2, 1, 64, 64)
     c.positions = torch.tensor([[0, 1, -1, 2 ** 31, 2 ** 40 + 1, -2 ** 50 + 3, 2 ** 62, -2 ** 63]])
