@@ -62,10 +62,11 @@ struct RotaryArgs {
 __device__ __forceinline__ float2 turn_by(uint64_t phase) {
     const int64_t quarter = (((int64_t)phase >> 61) + 1) >> 1;
     const int64_t rest = (int64_t)(phase - ((uint64_t)quarter << 62));  // |rest| <= 2^61
-    const float hi = __ll2float_rn(rest), lo = __ll2float_rn(rest - __float2ll_rn(hi));
-    constexpr float kPi = 0x1.921fb6p-62f, kPiLow = -0x1.777a5cp-87f;  // pi / 2^63
-    const float x = __fmul_rn(hi, kPi);
-    const float x_low = __fmaf_rn(lo, kPi, __fmaf_rn(hi, kPiLow, __fmaf_rn(hi, kPi, -x)));
+    const int32_t high = (int32_t)((rest + (1ll << 37)) >> 38);          // 24 bits
+    const int32_t low = (int32_t)((rest - ((int64_t)high << 38)) >> 7);  // and the next 30
+    constexpr float kPi = 0x1.921fb6p-24f, kPiLow = -0x1.777a5cp-49f;    // pi / 2^25
+    const float hi = (float)high, x = __fmul_rn(hi, kPi);
+    const float x_low = __fmaf_rn((float)low, 0x1p-31f * kPi, __fmaf_rn(hi, kPiLow, __fmaf_rn(hi, kPi, -x)));
     const float xx = __fmul_rn(x, x), xx_half = 0.5f * xx;
     const float xx_low = __fmaf_rn(x + x, x_low, __fmaf_rn(x, x, -xx));
     float s = __fmaf_rn(xx, 1.0f / 362880, -1.0f / 5040);
