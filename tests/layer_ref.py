@@ -143,8 +143,8 @@ def angles(positions, freq, axis):
     return out
 
 
-# The fraction's rounding moves the angle (up to pi) by pi 2^-24, sincospif is within 2 ulp, then
-# the magnitude, the product and the sum: below ten roundings of |a| + |b| in all.
+# Sines and cosines are within 0.8 of a place, then come the magnitude, the products and the sum:
+# below ten roundings of |a| + |b| in all.
 TURN = 10 * U_F32
 
 
