@@ -27,6 +27,7 @@
 #include <type_traits>
 
 #include "rows.cuh"
+#include "stage_ring.h"
 #include "tcgen05.cuh"
 
 namespace dflash2 {
@@ -54,11 +55,18 @@ __device__ __forceinline__ bool wait_drain(uint64_t *bar, uint32_t parity) {
         if (clock64() - t0 > kWaitLimitCycles) return false;
     return true;
 }
-// No copy is still writing shared memory when the CTA leaves: waits (bounded) for the
-// last `stages` loads issued.
-__device__ __forceinline__ void drain_loads(uint64_t *full, uint32_t issued, uint32_t stages) {
-    for (uint32_t n = issued > stages ? issued - stages : 0; n < issued; ++n)
-        wait_drain(&full[n % stages], (n / stages) & 1u);
+// What a producer waits for before its CTA may leave: the last use of each stage, of its blocks
+// first, first + step, ... below `end`.  A commit arrives on `empty` in the shared memory of
+// every CTA that loads the stage whenever its MMAs are done, and only a producer that takes the
+// stage again has waited for it; a CTA that left before would have it arrive on whatever lies
+// there next.  Once it is there, the copies have landed and the MMAs have read them.  Where a role has
+// given up, the copies alone (`landed`: the CTA whose barriers count them).  All waits are bounded.
+__device__ __forceinline__ void drain_stages(uint64_t *full, uint64_t *empty, uint32_t first, uint32_t step,
+                                             uint32_t end, uint32_t stages, bool landed, volatile int *abort_flag,
+                                             int32_t *err) {
+    for (uint32_t k = ring_last_uses(first, step, end, stages); k < end; k += step)
+        if (!bar_wait(&empty[k % stages], ring_parity(k, stages), abort_flag, err) && landed)
+            wait_drain(&full[k % stages], ring_parity(k, stages));
 }
 
 // ---- many rows -----------------------------------------------------------------
@@ -187,13 +195,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 s += 2;
                 if (s >= (uint32_t)a.stages) s -= (uint32_t)a.stages, ph ^= 1u;
             }
-            // no copy of either CTA is still on its way when the leader leaves: the last use
-            // of every stage has landed
-            if (rank == 0) {
-                const uint32_t stages = (uint32_t)a.stages, end = min(it, all), from = end > stages ? end - stages : 0;
-                for (uint32_t k = from + ((from ^ first) & 1u); k < end; k += 2)
-                    wait_drain(&full[k % stages], (k / stages) & 1u);
-            }
+            // the leader's barriers count the copies of both CTAs
+            drain_stages(full, empty, first, 2, min(it, all), (uint32_t)a.stages, rank == 0, &abort_flag, a.err);
         } else if ((warp == 1 || warp == 2) && rank == 0) {
             const uint32_t idesc = idesc_e4m3(256, kCols), first = (uint32_t)warp - 1;
             const uint64_t xd = sw128_desc(smem_u32(smem)), wd = sw128_desc(smem_u32(smem + kBoxBytes));
@@ -433,7 +436,7 @@ __global__ void __launch_bounds__(kQuantises<X> ? kFewQuantThreads : kFewThreads
             ++issued;
             if (++s == (uint32_t)a.stages) s = 0, ph ^= 1u;
         }
-        drain_loads(full, issued, (uint32_t)a.stages);
+        drain_stages(full, empty, 0, 1, issued, (uint32_t)a.stages, true, &abort_flag, a.err);
     } else if (warp == 1) {
         const uint32_t idesc = idesc_e4m3(128, kN);
         const uint64_t wd = sw128_desc(smem_u32(smem)), xd = sw128_desc(smem_u32(smem + kBoxBytes));
