@@ -675,12 +675,17 @@ dflash2_status launch_few(const DeviceInfo &di, const uint8_t *xq, const uint8_t
     constexpr int most = 108 * 1024;  // two CTAs per SM
     a.stages = min(kMaxStages, (int)((most - 1024) / stage));
     const int tiles = (a.n_out + 127) / 128;
-    // As many CTAs as run at once (two per SM), with two blocks each: one row x 4096 x 6144
-    // takes 11.4 us unsplit, 7.6 us split in four, 11.5 in eight (a second wave); x 4096 x
-    // 1024 10.7, 5.0 and 4.0 us.  Clusters of 6 leave SMs idle (12.0 us for the first).
+    // As many CTAs per tile as run at once for all tiles, with two blocks each.  Two CTAs run per SM,
+    // but a cluster stays within a group of SMs, which leaves up to two clusters' worth of them idle.
+    // One row of 4096: 75 tiles of 4 (300 CTAs of 304) take a second wave, 13.4 us for 9.9 in clusters of 2, 74 do
+    // not (9.3 for 9.8); 59 of 5 12.4 for 8.3 in clusters of 4, 58 not; 37 of 8 10.3 for 7.2 in 5, 36 not (6.7).
+    // On codes by the CTAs per tile 1 to 8: 48 tiles (4096 x 6144), one row 11.4, 8.6, 8.1, 7.6, 7.7 us, then a
+    // second wave (11.6, 11.7, 11.4); 64 rows 15.5, 13.1, 13.4, 12.5, 11.5, then 17.7, 17.5, 16.3; 8 tiles
+    // (4096 x 1024) one row 10.6, 7.2, 5.8, 5.0, 4.7, 4.4, 4.2, 3.9.  3, 6 and 7 are left out: where the larger of
+    // these do not run at once and they do, one row is within 5 % of the next smaller's time.
     int split = 1;
     for (const int s : {8, 5, 4, 2})
-        if (tiles * s <= 2 * di.sm_count && a.blocks >= 2 * s) {
+        if (tiles * s <= 2 * di.sm_count - 2 * s && a.blocks >= 2 * s) {
             split = s;
             break;
         }

@@ -78,6 +78,7 @@ def test_blocks_are_those_of_the_values(cuda, hidden, xt):
 # splits that leave CTAs uneven runs of blocks, and 5 uneven shares of the rows
 @pytest.mark.parametrize("rows", [17, 32, 33, 50, 64])
 @pytest.mark.parametrize("n_in,n_out", [(2048, 260), (2416, 400), (4752, 129), (1296, 5000), (1664, 5001), (2672, 7600),
+                                        (1040, 9700),
                                         (1040, 300), (1536, 9000), (528, 300), (656, 19000)])
 def test_few_rows_split(cuda, rows, n_in, n_out):
     x = ref.rows(rows, n_in, BF, rows + n_in)
