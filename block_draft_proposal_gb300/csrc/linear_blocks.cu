@@ -13,8 +13,9 @@
 //   linear_few_kernel   fewer: the weights are the MMA's M side, 128 a CTA, and the rows of
 //                       x its N side; the blocks are split over a cluster's CTAs, which
 //                       send one another their sums through distributed shared memory.
-// (64 rows x 4096 x 6144: 11.4 us by the few-row kernel, 10.6 by pairs; x 7168 x 7168 14.0
-// and 15.9; x 4096 x 1024 5.7 and 8.1.)
+// (64 rows on codes, few-row kernel and pairs: x 4096 x 1024 5.7 and 7.9 us, x 5120 x 7168 11.7 and 12.3, x 7168 x
+// 7168 14.1 and 15.6, x 4096 x 28672 25.1 and 26.7; x 4096 x 6144, whose tiles fill the pairs to two
+// thirds, 11.4 and 10.6.  40 rows x 4096 x 6144 10.0 and 10.4.)
 //
 // Few rows are bound by the weights' bytes and the latencies around them, many by the
 // accumulators' round trip: a block's MMAs take a pair 512 cycles at 256 columns, and from
@@ -22,8 +23,9 @@
 // the waiting warps 200, two TMEM loads and half the sums 370 to 440, the slowest of
 // sixteen warps 250 more), so a block takes about 750.
 // Measured on codes (graph replays): one row x 4096 x 6144 7.7 us, 3.3 TB/s; x 4096 x 28672
-// 20 us, 5.8 TB/s; 256 rows x 4096 x 6144 11.7 us; 512 16.6; 1536 x 5120 x 7168 47 us, 2.4
-// PFLOP/s; 8192 x 7168 x 7168 255 to 282 us with the clock, 3.0 to 3.3 PFLOP/s.
+// 20 us, 5.8 TB/s; 256 rows x 4096 x 6144 11.5 us; 512 16.6; 1536 x 5120 x 7168 48 us, 2.4
+// PFLOP/s; 8192 x 7168 x 7168 259 to 270 us, 3.1 to 3.2 PFLOP/s, and 311, 2.7, once the power cap
+// holds the SMs at 1.5 GHz (some 0.2 s of such calls).
 #include <type_traits>
 
 #include "rows.cuh"
@@ -719,8 +721,11 @@ dflash2_status launch_linear(const DeviceInfo &di, const uint8_t *xq, const uint
     if (a.rows <= 16) return launch_few<T, 16, uint8_t>(di, xq, wq, n_in, a, st);
     if (a.rows <= 32) return launch_few<T, 32, uint8_t>(di, xq, wq, n_in, a, st);
     if (a.rows <= 64) return launch_few<T, 64, uint8_t>(di, xq, wq, n_in, a, st);
-    // The tile's width by the time of its waves: a block takes a pair 0.48 and 0.6 times as
-    // long at 64 and 128 columns as at 256.
+    // The tile's width by the time of its waves, one of 64 or 128 columns taken as 0.48 or 0.6 of one
+    // of 256.  Measured at 256, 128 and 64 columns (us, and waves): 512 x 4096 x 6144
+    // 17.1 (1), 19.2 (2), 22.6 (3); 768 x 7168 x 7168 44.2 (2), 40.2 (3), 49.9 (5); 1024 x 4096 x 6144 29.4 (2), 26.7
+    // (3), 41.5 (6); 2048 x 5120 x 7168 49.4 (3), 56.8 (6), 79.7 (12); 8192 x 7168 x 7168 262 (12), 319 (24), 433
+    // (48): 0.56 to 0.61 at 128 columns, 0.40 to 0.47 at 64, which are thus taken where they win clearly.
     const int64_t m_tiles = (a.rows + 255) / 256, pairs = di.sm_count / 2;
     const auto waves = [&](int cols) { return (m_tiles * ((a.n_out + cols - 1) / cols) + pairs - 1) / pairs; };
     const double t64 = 0.48 * (double)waves(64), t128 = 0.6 * (double)waves(128), t256 = (double)waves(256);

@@ -16,11 +16,11 @@
 // up to 1024 values, 512 value by value), and the loads of y, r and the gate are
 // all in flight at once.  The choice goes by the row's length alone, so a row's result does
 // not depend on how many there are.
-// Measured (graph replays, rotating inputs): norm of 20011 x 7168 bf16 84 us, 6.9 TB/s; join
+// Measured (graph replays, rotating inputs): norm of 20011 x 7168 bf16 83 us, 6.9 TB/s; join
 // with an fp32 stream, a full sigmoid gate and both norms 284 us, 7.1 TB/s; bf16 join without
-// a gate 165 us, 6.9 TB/s, to E4M3 blocks 166; norm of 20011 x 5120 to E4M3 blocks 58 us, 5.3
-// TB/s; quantisation of 8192 x 7168 bf16 30 us, 6.0 TB/s; one row of 4096: norm 2.1 us, join
-// 3.1 us.
+// a gate 164 us, 7.0 TB/s, to E4M3 blocks 165; norm of 20011 x 5120 to E4M3 blocks 57 us, 5.4
+// TB/s; quantisation of 8192 x 7168 bf16 30 us, 6.0 TB/s; one row of 4096: norm 2.3 us, join
+// 3.3 us.
 #include <type_traits>
 
 #include "rows.cuh"
@@ -136,6 +136,8 @@ template <bool kWarpRow> __device__ __forceinline__ float row_sum(float v, float
 // Value by value a thread holds 32 bits of each, so it takes two pieces in place of four, four
 // blocks: bf16 join of 10000 x 5001 127 us (four pieces 181, one 240), with an fp32 stream and
 // a full gate 165 (230), of 30000 x 1001 73 (71) and 91 (93).
+// What these leave some joins is less than they hold, and they spill: bf16 rows 56 to 68 bytes, a bf16 stream
+// with fp32 rows 164 to 200, E4M3 blocks of odd widths 274 to 288, rows of more than 16384 60 to 550.
 template <typename TX, typename T, bool kVec, bool kJoin, int kChunks>
 constexpr int kBlocks256 = kJoin ? (kChunks == 2                    ? 4
                                     : sizeof(TX) + sizeof(T) == 4   ? (kVec ? 4 : 3)

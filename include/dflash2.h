@@ -774,8 +774,8 @@ dflash2_status dflash2_quantize_blocks_e4m3(const void *x, int64_t x_row_stride,
  * err_word   device int32 or NULL: DFLASH2_DEVERR_TIMEOUT.
  * Arithmetic: a block's products summed in fp32, times xs * ws (fp32), the blocks
  *            added in fp32; the result rounded once.  NaN codes give NaN.
- *            Reduction orders are fixed, so results are deterministic; they differ in
- *            their last bits between calls of more and of fewer than 64 rows.
+ *            Reduction orders are fixed, so results are deterministic; a row's differ in
+ *            their last bits between calls of up to 64 rows and of more.
  * Errors:    rows outside [0, 2^20], in_features outside [1, 2^20], out_features
  *            outside [1, 2^24], rows * in, out * in or rows * out >= 2^40, both or
  *            none of x and x_q, a null pointer, what dflash2_quantize_blocks_e4m3 refuses of
@@ -866,7 +866,8 @@ dflash2_status dflash2_sublayer_join(const void *residual, int64_t residual_row_
  * q_out, k_out  device, rows like q and k at their own strides; may be q and k
  *            themselves (same stride), and must not overlap them otherwise.
  * Arithmetic: fp32 (sines and cosines within 0.8 of a last place of those of the
- *            exact angle); one rounding per value.
+ *            exact angle, small ones included, then times magnitude); a value is
+ *            rounded to its type once.
  * dflash2_rotary_kv_write also writes the rotated keys and the values (rows v, as
  * k) into the cache as dflash2_kv_cache_write does (its slots, formats and device
  * errors); an E4M3 row is quantised from the fp32 values.  k_out may be NULL.
